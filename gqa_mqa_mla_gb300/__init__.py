@@ -13,15 +13,27 @@ from .binding import (  # noqa: F401
     DecAttnError,
     FLAG_BAD_BLOCK,
     FLAG_BAD_SEQ_LEN,
+    FLAG_NO_ROOM,
     FLAG_TIMEOUT,
+    PagedPlan,
+    RopeTable,
     gqa_decode,
     gqa_decode_fp8kv,
+    gqa_decode_fp8kv_sinks,
     gqa_decode_fp8kv_window,
+    gqa_decode_sinks,
     gqa_decode_window,
     gqa_fp8_plan_splits,
     gqa_kv_append,
     gqa_kv_append_fp8kv,
     gqa_plan_splits,
+    gqa_prefill,
+    gqa_prefill_fp8kv,
+    gqa_prefill_plan_splits,
+    gqa_prefill_workspace_size,
+    gqa_rope_append,
+    gqa_rope_append_fp8kv,
+    gqa_sinks_plan_splits,
     gqa_window_plan_splits,
     gqa_workspace_size,
     kv_bytes_per_token,
@@ -34,6 +46,8 @@ from .binding import (  # noqa: F401
     mla_plan_splits,
     mla_unabsorb_out,
     mla_workspace_size,
+    paged_plan,
+    rope_table,
     status_string,
 )
 

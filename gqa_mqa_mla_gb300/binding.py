@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -25,6 +26,7 @@ DECATTN_BF16 = 1
 FLAG_BAD_BLOCK = 1
 FLAG_BAD_SEQ_LEN = 2
 FLAG_TIMEOUT = 4
+FLAG_NO_ROOM = 8
 MAX_SPLITS = 256
 
 MLA_HEADS, MLA_D_C, MLA_D_R = 128, 512, 64
@@ -52,6 +54,28 @@ class Launch(ctypes.Structure):
         ("err_flag", ctypes.c_void_p),
         ("stream", ctypes.c_void_p),
     ]
+
+
+class RopeTable(ctypes.Structure):
+    """decattn_rope: how a model's heads are rotated (made by rope_table)."""
+
+    _fields_ = [
+        ("rot_dim", ctypes.c_int),
+        ("n_axes", ctypes.c_int),
+        ("interleaved", ctypes.c_int),
+        ("axis", ctypes.c_uint8 * 64),
+        ("turns", ctypes.c_uint64 * 64),
+    ]
+
+
+class PagedPlan(NamedTuple):
+    """What paged_plan writes beside the block table and the free stack."""
+
+    seq_lens: torch.Tensor    # int32 [B]
+    q_start: torch.Tensor     # int32 [B + 1]
+    slots: torch.Tensor       # int32 [max_tokens]
+    positions: torch.Tensor   # int32 [max_tokens]
+    free_count: torch.Tensor  # int32 [1]
 
 
 _lock = threading.Lock()
@@ -85,6 +109,32 @@ def lib() -> ctypes.CDLL:
             L.gqa_decode_fp8kv_window.restype = I
             L.gqa_decode_window_plan_splits.argtypes = [I, I, I, I, I, I, I, I, I]
             L.gqa_decode_window_plan_splits.restype = I
+            L.gqa_decode_sinks.argtypes = [P, P, P, P, P, P, I, I, I, F, I, I, LP]
+            L.gqa_decode_sinks.restype = I
+            L.gqa_decode_fp8kv_sinks.argtypes = [P, P, P, P, P, P, P, P, I, I, I, F, I, I, LP]
+            L.gqa_decode_fp8kv_sinks.restype = I
+            L.gqa_decode_sinks_plan_splits.argtypes = [I, I, I, I, I, I, I, I, I, I]
+            L.gqa_decode_sinks_plan_splits.restype = I
+            L.paged_plan.argtypes = [P, P, P, P, P, P, P, P, P, P, I, LP]
+            L.paged_plan.restype = I
+            RP = ctypes.POINTER(RopeTable)
+            L.decattn_rope_fill.argtypes = [RP, ctypes.POINTER(ctypes.c_double), I,
+                                            ctypes.POINTER(I), I, I]
+            L.decattn_rope_fill.restype = I
+            L.gqa_rope_append.argtypes = [P, P, P, I64, I64, I64, P, RP, P, P, P, P, I, I, I, I,
+                                          LP]
+            L.gqa_rope_append.restype = I
+            L.gqa_rope_append_fp8kv.argtypes = [P, P, P, I64, I64, I64, P, P, P, RP, P, P, P, P, I,
+                                                I, I, I, LP]
+            L.gqa_rope_append_fp8kv.restype = I
+            L.gqa_prefill.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, F, I, I, LP]
+            L.gqa_prefill.restype = I
+            L.gqa_prefill_fp8kv.argtypes = [P, P, P, P, P, P, P, P, P, I, I, I, I, I, F, I, I, LP]
+            L.gqa_prefill_fp8kv.restype = I
+            L.gqa_prefill_plan_splits.argtypes = [I, I, I, I, I, I, I, I, I, I]
+            L.gqa_prefill_plan_splits.restype = I
+            L.gqa_prefill_workspace_size.argtypes = [I, I, I, I]
+            L.gqa_prefill_workspace_size.restype = S
             L.gqa_kv_append.argtypes = [P, P, P, P, P, P, I, I, LP]
             L.gqa_kv_append.restype = I
             L.gqa_kv_append_fp8kv.argtypes = [P, P, P, P, P, P, P, P, I, I, LP]
@@ -171,6 +221,30 @@ def gqa_window_plan_splits(batch: int, h_q: int, h_kv: int, max_seq_len: int, wi
     return r
 
 
+def gqa_sinks_plan_splits(batch: int, h_q: int, h_kv: int, max_seq_len: int, window: int,
+                          sinks: int, block_size: int, kv_bytes: int = 2, d_head: int = 128,
+                          num_sms: int = 0) -> int:
+    r = lib().gqa_decode_sinks_plan_splits(batch, h_q, h_kv, d_head, max_seq_len, window, sinks,
+                                           block_size, kv_bytes, num_sms)
+    if r < 0:
+        raise DecAttnError("gqa_decode_sinks_plan_splits", r)
+    return r
+
+
+def gqa_prefill_plan_splits(batch: int, tokens: int, max_q_len: int, h_q: int, h_kv: int,
+                            max_seq_len: int, window: int = 0, sinks: int = 0, d_head: int = 128,
+                            num_sms: int = 0) -> int:
+    r = lib().gqa_prefill_plan_splits(batch, tokens, max_q_len, h_q, h_kv, d_head, max_seq_len,
+                                      window, sinks, num_sms)
+    if r < 0:
+        raise DecAttnError("gqa_prefill_plan_splits", r)
+    return r
+
+
+def gqa_prefill_workspace_size(tokens: int, h_q: int, num_splits: int, d_head: int = 128) -> int:
+    return int(lib().gqa_prefill_workspace_size(tokens, h_q, d_head, num_splits))
+
+
 def mla_plan_splits(batch: int, max_seq_len: int, num_sms: int = 0) -> int:
     r = lib().mla_decode_plan_splits(batch, max_seq_len, num_sms)
     if r < 0:
@@ -201,6 +275,42 @@ def _check(t: torch.Tensor, name: str, dtype=None, ndim=None):
         raise ValueError(f"{name} must be contiguous")
 
 
+def _check_out(t: torch.Tensor, name: str, dtype, shape, device):
+    _check(t, name, dtype)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    _check_device(device, (name, t))
+
+
+def _check_device(device, *named):
+    for name, t in named:
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, the call's other tensors on {device}")
+
+
+def _check_flag(err_flag, device):
+    if err_flag is not None:
+        _check(err_flag, "err_flag", torch.int32)
+        if err_flag.numel() < 1:
+            raise ValueError("err_flag needs one element")
+        _check_device(device, ("err_flag", err_flag))
+
+
+def _check_sinks(window, sinks):
+    if sinks < 0:
+        raise ValueError("sinks must not be negative")
+    if sinks and window is None:
+        raise ValueError("sinks need a window (without one every token is visible)")
+
+
+def _on_device(device):
+    # The library launches on the current device; its calls run under the
+    # device that holds the tensors.
+    if device.type != "cuda":
+        raise ValueError("the tensors must be on a CUDA device")
+    return torch.cuda.device(device)
+
+
 def _stream_handle(stream) -> int:
     if stream is None:
         stream = torch.cuda.current_stream()
@@ -215,15 +325,17 @@ def make_launch(batch, num_blocks, block_size, max_blocks_per_seq, max_seq_len, 
 
 def gqa_decode(q, k_cache, v_cache, block_table, seq_lens, *, scale: float, max_seq_len: int,
                out=None, num_splits: int = 0, workspace=None, err_flag=None, stream=None,
-               window: int | None = None):
+               window: int | None = None, sinks: int = 0):
     """MHA/GQA/MQA decode through the C ABI; returns out [B, h_q, d].
 
     q [B, h_q, d]; k_cache/v_cache [num_blocks, block_size, h_kv, d];
     block_table int32 [B, max_blocks]; seq_lens int32 [B]; max_seq_len a host
     upper bound of seq_lens.  workspace: optional uint8 CUDA tensor (sized by
     gqa_workspace_size); allocated here when needed and not given.  window:
-    attend only to each sequence's last `window` tokens (gqa_decode_window).
+    attend only to each sequence's last `window` tokens (gqa_decode_window),
+    and with sinks > 0 to its first `sinks` tokens too (gqa_decode_sinks).
     """
+    _check_sinks(window, sinks)
     _check(q, "q", ndim=3)
     _check(k_cache, "k_cache", q.dtype, 4)
     _check(v_cache, "v_cache", q.dtype, 4)
@@ -244,7 +356,7 @@ def gqa_decode(q, k_cache, v_cache, block_table, seq_lens, *, scale: float, max_
     elif window is None:
         ns = gqa_plan_splits(B, h_q, h_kv, max_seq_len, d)
     else:
-        ns = gqa_window_plan_splits(B, h_q, h_kv, max_seq_len, window, bs, 2, d)
+        ns = gqa_sinks_plan_splits(B, h_q, h_kv, max_seq_len, window, sinks, bs, 2, d)
     need = gqa_workspace_size(B, h_q, ns, d)
     if need and workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
@@ -255,12 +367,20 @@ def gqa_decode(q, k_cache, v_cache, block_table, seq_lens, *, scale: float, max_
             seq_lens.data_ptr(), out.data_ptr(), h_q, h_kv, d, float(scale))
     if window is None:
         name, st = "gqa_decode", lib().gqa_decode(*args, ctypes.byref(L))
+    elif sinks:
+        name = "gqa_decode_sinks"
+        st = lib().gqa_decode_sinks(*args, int(window), int(sinks), ctypes.byref(L))
     else:
         name = "gqa_decode_window"
         st = lib().gqa_decode_window(*args, int(window), ctypes.byref(L))
     if st != DECATTN_OK:
         raise DecAttnError(name, st)
     return out
+
+
+def gqa_decode_sinks(q, k_cache, v_cache, block_table, seq_lens, *, window: int, sinks: int, **kw):
+    """gqa_decode restricted to each sequence's first `sinks` and last `window` tokens."""
+    return gqa_decode(q, k_cache, v_cache, block_table, seq_lens, window=window, sinks=sinks, **kw)
 
 
 def gqa_decode_window(q, k_cache, v_cache, block_table, seq_lens, *, window: int, **kw):
@@ -270,14 +390,16 @@ def gqa_decode_window(q, k_cache, v_cache, block_table, seq_lens, *, window: int
 
 def gqa_decode_fp8kv(q, k_codes, v_codes, k_scale, v_scale, block_table, seq_lens, *,
                      scale: float, max_seq_len: int, out=None, num_splits: int = 0,
-                     workspace=None, err_flag=None, stream=None, window: int | None = None):
+                     workspace=None, err_flag=None, stream=None, window: int | None = None,
+                     sinks: int = 0):
     """GQA decode over an 8-bit (e4m3) KV cache through the C ABI; returns out.
 
     q [B, h_q, d] fp16/bf16; k_codes/v_codes uint8 (or float8_e4m3fn)
     [num_blocks, block_size, h_kv, d]; k_scale/v_scale float32 [h_kv] (the
     value of KV head j is e4m3(code) * scale[j]); the rest as gqa_decode
-    (window: gqa_decode_fp8kv_window).
+    (window: gqa_decode_fp8kv_window; sinks: gqa_decode_fp8kv_sinks).
     """
+    _check_sinks(window, sinks)
     _check(q, "q", ndim=3)
     if q.dtype not in _DT:
         raise TypeError("q must be float16 or bfloat16")
@@ -306,7 +428,7 @@ def gqa_decode_fp8kv(q, k_codes, v_codes, k_scale, v_scale, block_table, seq_len
     elif window is None:
         ns = gqa_fp8_plan_splits(B, h_q, h_kv, max_seq_len, d)
     else:
-        ns = gqa_window_plan_splits(B, h_q, h_kv, max_seq_len, window, bs, 1, d)
+        ns = gqa_sinks_plan_splits(B, h_q, h_kv, max_seq_len, window, sinks, bs, 1, d)
     need = gqa_workspace_size(B, h_q, ns, d)
     if need and workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
@@ -318,6 +440,9 @@ def gqa_decode_fp8kv(q, k_codes, v_codes, k_scale, v_scale, block_table, seq_len
             h_q, h_kv, d, float(scale))
     if window is None:
         name, st = "gqa_decode_fp8kv", lib().gqa_decode_fp8kv(*args, ctypes.byref(L))
+    elif sinks:
+        name = "gqa_decode_fp8kv_sinks"
+        st = lib().gqa_decode_fp8kv_sinks(*args, int(window), int(sinks), ctypes.byref(L))
     else:
         name = "gqa_decode_fp8kv_window"
         st = lib().gqa_decode_fp8kv_window(*args, int(window), ctypes.byref(L))
@@ -331,6 +456,13 @@ def gqa_decode_fp8kv_window(q, k_codes, v_codes, k_scale, v_scale, block_table, 
     """gqa_decode_fp8kv restricted to each sequence's last `window` tokens."""
     return gqa_decode_fp8kv(q, k_codes, v_codes, k_scale, v_scale, block_table, seq_lens,
                             window=window, **kw)
+
+
+def gqa_decode_fp8kv_sinks(q, k_codes, v_codes, k_scale, v_scale, block_table, seq_lens, *,
+                           window: int, sinks: int, **kw):
+    """gqa_decode_fp8kv restricted to each sequence's first `sinks` and last `window` tokens."""
+    return gqa_decode_fp8kv(q, k_codes, v_codes, k_scale, v_scale, block_table, seq_lens,
+                            window=window, sinks=sinks, **kw)
 
 
 def _append_launch(new, cache, block_table, dtype, err_flag, stream) -> Launch:
@@ -393,6 +525,255 @@ def gqa_kv_append_fp8kv(k_new, v_new, k_scale, v_scale, positions, block_table, 
                                    h_kv, d, ctypes.byref(L))
     if st != DECATTN_OK:
         raise DecAttnError("gqa_kv_append_fp8kv", st)
+
+
+def paged_plan(cached_lens, new_lens, block_table, free_blocks, free_count, *, block_size: int,
+               max_tokens: int, seq_lens=None, q_start=None, slots=None, positions=None,
+               free_count_out=None, err_flag=None, stream=None) -> PagedPlan:
+    """A serving step's paged state from the requests' lengths, on the GPU.
+
+    cached_lens, new_lens int32 [B] (new < 0 gives tokens back); block_table
+    int32 [B, max_blocks] and free_blocks int32 [num_blocks] (a stack of
+    free_count[0] ids) are updated in place.  The outputs are allocated when
+    not given; free_count_out may be free_count and seq_lens may be
+    cached_lens (in place).  Rows past the step's last token get slot and
+    position -1.
+    """
+    for t, n in ((cached_lens, "cached_lens"), (new_lens, "new_lens"),
+                 (free_blocks, "free_blocks"), (free_count, "free_count")):
+        _check(t, n, torch.int32, 1)
+    _check(block_table, "block_table", torch.int32, 2)
+    B, dev = cached_lens.shape[0], cached_lens.device
+    if new_lens.shape != (B,) or block_table.shape[0] != B or free_count.numel() != 1:
+        raise ValueError("paged_plan: shape mismatch")
+    if max_tokens < 0:
+        raise ValueError("max_tokens must not be negative")
+    _check_device(dev, ("new_lens", new_lens), ("block_table", block_table),
+                  ("free_blocks", free_blocks), ("free_count", free_count))
+    _check_flag(err_flag, dev)
+
+    def given(t, name, n):
+        if t is None:
+            return torch.empty(n, dtype=torch.int32, device=dev)
+        _check_out(t, name, torch.int32, (n,), dev)
+        return t
+
+    plan = PagedPlan(given(seq_lens, "seq_lens", B), given(q_start, "q_start", B + 1),
+                     given(slots, "slots", max_tokens), given(positions, "positions", max_tokens),
+                     given(free_count_out, "free_count_out", 1))
+    with _on_device(dev):
+        L = make_launch(B, free_blocks.shape[0], block_size, block_table.shape[1], 0, 1,
+                        DECATTN_FP16, None, 0, _ptr(err_flag), _stream_handle(stream))
+        st = lib().paged_plan(cached_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(),
+                              free_blocks.data_ptr(), free_count.data_ptr(),
+                              plan.free_count.data_ptr(), plan.seq_lens.data_ptr(),
+                              plan.q_start.data_ptr(), plan.slots.data_ptr(),
+                              plan.positions.data_ptr(), max_tokens, ctypes.byref(L))
+    if st != DECATTN_OK:
+        raise DecAttnError("paged_plan", st)
+    return plan
+
+
+def rope_table(inv_freq, *, sections=None, interleaved: bool = False, device=None) -> RopeTable:
+    """How a model's heads are rotated, for gqa_rope_append.
+
+    inv_freq: rot_dim / 2 frequencies (radians per position), a sequence or a
+    tensor; sections: how many consecutive pairs follow each position axis
+    (default: one axis); interleaved: pairs (2 i, 2 i + 1) instead of
+    (i, i + rot_dim / 2).  Host data (`device` is accepted for symmetry with
+    tensor factories and ignored).
+    """
+    freq = [float(f) for f in (inv_freq.tolist() if isinstance(inv_freq, torch.Tensor)
+                               else inv_freq)]
+    cut = None if sections is None else [int(n) for n in sections]
+    rope = RopeTable()
+    st = lib().decattn_rope_fill(
+        ctypes.byref(rope), (ctypes.c_double * max(1, len(freq)))(*freq), 2 * len(freq),
+        None if cut is None else (ctypes.c_int * max(1, len(cut)))(*cut),
+        1 if cut is None else len(cut), int(bool(interleaved)))
+    if st != DECATTN_OK:
+        raise DecAttnError("decattn_rope_fill", st)
+    return rope
+
+
+def _packed_rows(t, name, dtype):
+    """A [tokens, heads, 128] tensor whose heads are contiguous within a token
+    (a part of a wider projection's output will do): its token stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 3:
+        raise ValueError(f"{name}: expected 3 dims, got shape {tuple(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    T, h, d = t.shape
+    if t.numel() and ((d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d)):
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    return t.stride(0) if T > 1 else h * d
+
+
+def _rope_append(fp8, q, k_new, v_new, scales, positions, rope, slots, k_cache, v_cache, q_out,
+                 err_flag, stream):
+    name = "gqa_rope_append_fp8kv" if fp8 else "gqa_rope_append"
+    qs = _packed_rows(q, "q", None)
+    if q.dtype not in _DT:
+        raise TypeError("q must be float16 or bfloat16")
+    ks, vs = _packed_rows(k_new, "k_new", q.dtype), _packed_rows(v_new, "v_new", q.dtype)
+    if not isinstance(rope, RopeTable):
+        raise TypeError("rope must come from rope_table")
+    _check(positions, "positions", torch.int32)
+    if positions.dim() == 1:
+        positions = positions[None]
+    _check(slots, "slots", torch.int32, 1)
+    cache_dtype = torch.uint8 if fp8 else q.dtype
+    _check(k_cache, "k_cache", cache_dtype, 4)
+    _check(v_cache, "v_cache", cache_dtype, 4)
+    T, h_q, d = q.shape
+    h_kv = k_new.shape[1]
+    if k_new.shape != (T, h_kv, d) or v_new.shape != k_new.shape or \
+            k_cache.shape[2:] != (h_kv, d) or v_cache.shape != k_cache.shape or \
+            slots.shape != (T,):
+        raise ValueError(f"{name}: shape mismatch")
+    if positions.shape != (rope.n_axes, T):
+        raise ValueError(f"positions must be [{rope.n_axes}, {T}]")
+    for n, s in (("k_scale", scales[0]), ("v_scale", scales[1])) if fp8 else ():
+        _check(s, n, torch.float32, 1)
+        if s.shape != (h_kv,):
+            raise ValueError(f"{n} must be [h_kv]")
+        _check_device(q.device, (n, s))
+    _check_device(q.device, ("k_new", k_new), ("v_new", v_new), ("positions", positions),
+                  ("slots", slots), ("k_cache", k_cache), ("v_cache", v_cache))
+    _check_flag(err_flag, q.device)
+    if q_out is None:
+        q_out = torch.empty((T, h_q, d), dtype=q.dtype, device=q.device)
+    else:
+        _check_out(q_out, "q_out", q.dtype, (T, h_q, d), q.device)
+    with _on_device(q.device):
+        L = make_launch(1, k_cache.shape[0], k_cache.shape[1], 1, 0, 1, _DT[q.dtype], None, 0,
+                        _ptr(err_flag), _stream_handle(stream))
+        st = getattr(lib(), name)(
+            q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), qs, ks, vs,
+            *([s.data_ptr() for s in scales] if fp8 else []), positions.data_ptr(),
+            ctypes.byref(rope), slots.data_ptr(), q_out.data_ptr(), k_cache.data_ptr(),
+            v_cache.data_ptr(), T, h_q, h_kv, d, ctypes.byref(L))
+    if st != DECATTN_OK:
+        raise DecAttnError(name, st)
+    return q_out
+
+
+def gqa_rope_append(q, k_new, v_new, positions, rope, slots, k_cache, v_cache, *, q_out=None,
+                    err_flag=None, stream=None):
+    """Rotate q and k by their positions, write k and v into the paged cache's
+    slots (in place) and return the rotated q [T, h_q, d].
+
+    q [T, h_q, d], k_new / v_new [T, h_kv, d]: each token's heads contiguous,
+    tokens any stride (parts of one projection's output); positions int32
+    [n_axes, T] (or [T]); rope: rope_table's; slots int32 [T] (negative: no
+    cache row); q_out: a contiguous [T, h_q, d], may be q.
+    """
+    return _rope_append(False, q, k_new, v_new, None, positions, rope, slots, k_cache, v_cache,
+                        q_out, err_flag, stream)
+
+
+def gqa_rope_append_fp8kv(q, k_new, v_new, k_scale, v_scale, positions, rope, slots, k_codes,
+                          v_codes, *, q_out=None, err_flag=None, stream=None):
+    """gqa_rope_append into an 8-bit e4m3 cache (uint8 or float8_e4m3fn) with
+    one scale per KV head."""
+    return _rope_append(True, q, k_new, v_new, (k_scale, v_scale), positions, rope, slots,
+                        _codes(k_codes), _codes(v_codes), q_out, err_flag, stream)
+
+
+def _codes(t):
+    return t.view(torch.uint8) if isinstance(t, torch.Tensor) and \
+        t.dtype == torch.float8_e4m3fn else t
+
+
+def _prefill(fp8, q, k_cache, v_cache, scales, block_table, q_start, seq_lens, scale, max_q_len,
+             max_seq_len, window, sinks, out, num_splits, workspace, err_flag, stream):
+    name = "gqa_prefill_fp8kv" if fp8 else "gqa_prefill"
+    _check(q, "q", ndim=3)
+    if q.dtype not in _DT:
+        raise TypeError("q must be float16 or bfloat16")
+    cache_dtype = torch.uint8 if fp8 else q.dtype
+    _check(k_cache, "k_cache", cache_dtype, 4)
+    _check(v_cache, "v_cache", cache_dtype, 4)
+    _check(block_table, "block_table", torch.int32, 2)
+    _check(q_start, "q_start", torch.int32, 1)
+    _check(seq_lens, "seq_lens", torch.int32, 1)
+    _check_sinks(window, sinks)
+    if window is not None and window < 1:
+        raise ValueError("window must be at least 1")
+    T, h_q, d = q.shape
+    nb, bs, h_kv, d2 = k_cache.shape
+    B = seq_lens.shape[0]
+    if d2 != d or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache / v_cache shape mismatch")
+    if block_table.shape[0] != B or q_start.shape != (B + 1,):
+        raise ValueError("block_table must be [B, max_blocks] and q_start [B + 1]")
+    if h_kv < 1 or h_q % h_kv != 0:
+        raise ValueError(f"h_q={h_q} is not a multiple of h_kv={h_kv}")
+    for n, s in (("k_scale", scales[0]), ("v_scale", scales[1])) if fp8 else ():
+        _check(s, n, torch.float32, 1)
+        if s.shape != (h_kv,):
+            raise ValueError(f"{n} must be [h_kv]")
+        _check_device(q.device, (n, s))
+    _check_device(q.device, ("k_cache", k_cache), ("v_cache", v_cache),
+                  ("block_table", block_table), ("q_start", q_start), ("seq_lens", seq_lens))
+    _check_flag(err_flag, q.device)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _check_out(out, "out", q.dtype, q.shape, q.device)
+    with _on_device(q.device):
+        ns = num_splits
+        if ns == 0:
+            ns = gqa_prefill_plan_splits(B, T, max_q_len, h_q, h_kv, max_seq_len, window or 0,
+                                         sinks, d)
+        need = gqa_prefill_workspace_size(T, h_q, ns, d) if T else 0
+        if workspace is not None:
+            _check(workspace, "workspace", torch.uint8)
+            _check_device(q.device, ("workspace", workspace))
+        elif need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        L = make_launch(B, nb, bs, block_table.shape[1], max_seq_len, ns, _DT[q.dtype],
+                        _ptr(workspace), 0 if workspace is None else workspace.numel(),
+                        _ptr(err_flag), _stream_handle(stream))
+        st = getattr(lib(), name)(
+            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            *([s.data_ptr() for s in scales] if fp8 else []), block_table.data_ptr(),
+            q_start.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), T, max_q_len, h_q, h_kv, d,
+            float(scale), window or 0, sinks, ctypes.byref(L))
+    if st != DECATTN_OK:
+        raise DecAttnError(name, st)
+    return out
+
+
+def gqa_prefill(q, k_cache, v_cache, block_table, q_start, seq_lens, *, scale: float,
+                max_q_len: int, max_seq_len: int, window: int | None = None, sinks: int = 0,
+                out=None, num_splits: int = 0, workspace=None, err_flag=None, stream=None):
+    """Attention of a chunk of new tokens per sequence over the paged cache;
+    returns out [T, h_q, d].
+
+    q [T, h_q, d] packed rows, sequence b's being q_start[b] .. q_start[b + 1]
+    - 1 (int32 [B + 1]); seq_lens int32 [B] counts the cached tokens, the
+    chunk included; row i of a chunk of n is position seq_lens[b] - n + i and
+    sees the positions up to its own, of them the last `window` and the first
+    `sinks` where a window is given.  max_q_len, max_seq_len: host upper
+    bounds.  Rows outside every sequence are not written.
+    """
+    return _prefill(False, q, k_cache, v_cache, None, block_table, q_start, seq_lens, scale,
+                    max_q_len, max_seq_len, window, sinks, out, num_splits, workspace, err_flag,
+                    stream)
+
+
+def gqa_prefill_fp8kv(q, k_codes, v_codes, k_scale, v_scale, block_table, q_start, seq_lens, *,
+                      scale: float, max_q_len: int, max_seq_len: int, window: int | None = None,
+                      sinks: int = 0, out=None, num_splits: int = 0, workspace=None,
+                      err_flag=None, stream=None):
+    """gqa_prefill over an 8-bit e4m3 cache (uint8 or float8_e4m3fn) with one
+    scale per KV head."""
+    return _prefill(True, q, _codes(k_codes), _codes(v_codes), (k_scale, v_scale), block_table,
+                    q_start, seq_lens, scale, max_q_len, max_seq_len, window, sinks, out,
+                    num_splits, workspace, err_flag, stream)
 
 
 def mla_kv_append(latent_new, positions, block_table, latent_cache, *, err_flag=None,

@@ -133,6 +133,16 @@ int window_span(int max_seq_len, int window, int block_size) {
   return span < max_seq_len ? static_cast<int>(span) : max_seq_len;
 }
 
+// A window with kept first tokens streams its window's range and the sinks'
+// own 64-token tiles; once both cover every length, the whole sequence.
+int sinks_span(int max_seq_len, int window, int sinks, int block_size) {
+  const int span = window_span(max_seq_len, window, block_size);
+  if (window <= 0 || sinks <= 0) return span;
+  if (static_cast<int64_t>(window) + sinks >= max_seq_len) return max_seq_len;
+  const int64_t both = (static_cast<int64_t>(sinks) + kTile - 1) / kTile * kTile + span;
+  return static_cast<int>(both < 0x7fffffc0 ? both : 0x7fffffc0);
+}
+
 namespace {
 
 // Split count for `units` independent (sequence[, KV head]) work units on
@@ -321,6 +331,19 @@ int gqa_decode_window_plan_splits(int batch, int h_q, int h_kv, int d_head, int 
                        : plan_gqa_splits(batch, h_q, h_kv, span, num_sms);
 }
 
+int gqa_decode_sinks_plan_splits(int batch, int h_q, int h_kv, int d_head, int max_seq_len,
+                                 int window, int sinks, int block_size, int kv_bytes,
+                                 int num_sms) {
+  if (batch < 1 || h_q < 1 || h_kv < 1 || h_q % h_kv != 0 || d_head < 1 || max_seq_len < 0 ||
+      window < 1 || sinks < 0 || !is_pow2(block_size) || (kv_bytes != 1 && kv_bytes != 2))
+    return DECATTN_ERR_INVALID_ARG;
+  if (num_sms <= 0) num_sms = device_sm_count();
+  if (num_sms <= 0) return DECATTN_ERR_CUDA;
+  const int span = sinks_span(max_seq_len, window, sinks, block_size);
+  return kv_bytes == 1 ? plan_gqa_fp8_splits(batch, h_q, h_kv, span, num_sms)
+                       : plan_gqa_splits(batch, h_q, h_kv, span, num_sms);
+}
+
 int mla_decode_plan_splits(int batch, int max_seq_len, int num_sms) {
   if (batch < 1 || max_seq_len < 0) return DECATTN_ERR_INVALID_ARG;
   if (num_sms <= 0) num_sms = device_sm_count();
@@ -380,12 +403,12 @@ extern "C" {
 static int gqa_decode_impl(const void* q, const void* k_cache, const void* v_cache,
                            const float* k_scale, const float* v_scale, bool fp8,
                            const int32_t* block_table, const int32_t* seq_lens, void* out,
-                           int h_q, int h_kv, int d_head, float scale, int window,
+                           int h_q, int h_kv, int d_head, float scale, int window, int sinks,
                            const decattn_launch* L) {
   const int st = gqa_check_args(q, k_cache, v_cache, k_scale, v_scale, fp8, block_table,
                                 seq_lens, out, h_q, h_kv, d_head, scale, window, L);
   if (st != DECATTN_OK) return st;
-  const int span = window_span(L->max_seq_len, window, L->block_size);
+  const int span = sinks_span(L->max_seq_len, window, sinks, L->block_size);
   int n_split = L->num_splits;
   if (n_split == 0) {
     const int sms = device_sm_count();
@@ -415,6 +438,7 @@ static int gqa_decode_impl(const void* q, const void* k_cache, const void* v_cac
   p.tokens_per_split = tps;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.window = window;
+  p.sinks = window > 0 ? sinks : 0;
   p.k_scale = k_scale;
   p.v_scale = v_scale;
   if (eff > 1) {
@@ -473,7 +497,7 @@ int gqa_decode(const void* q, const void* k_cache, const void* v_cache,
                const int32_t* block_table, const int32_t* seq_lens, void* out, int h_q, int h_kv,
                int d_head, float scale, const decattn_launch* L) {
   return gqa_decode_impl(q, k_cache, v_cache, nullptr, nullptr, false, block_table, seq_lens, out,
-                         h_q, h_kv, d_head, scale, 0, L);
+                         h_q, h_kv, d_head, scale, 0, 0, L);
 }
 
 int gqa_decode_fp8kv(const void* q, const void* k_cache, const void* v_cache,
@@ -481,7 +505,7 @@ int gqa_decode_fp8kv(const void* q, const void* k_cache, const void* v_cache,
                      const int32_t* seq_lens, void* out, int h_q, int h_kv, int d_head,
                      float scale, const decattn_launch* L) {
   return gqa_decode_impl(q, k_cache, v_cache, k_scale, v_scale, true, block_table, seq_lens, out,
-                         h_q, h_kv, d_head, scale, 0, L);
+                         h_q, h_kv, d_head, scale, 0, 0, L);
 }
 
 int gqa_decode_window(const void* q, const void* k_cache, const void* v_cache,
@@ -489,7 +513,7 @@ int gqa_decode_window(const void* q, const void* k_cache, const void* v_cache,
                       int h_kv, int d_head, float scale, int window, const decattn_launch* L) {
   if (window < 1) return DECATTN_ERR_INVALID_ARG;
   return gqa_decode_impl(q, k_cache, v_cache, nullptr, nullptr, false, block_table, seq_lens, out,
-                         h_q, h_kv, d_head, scale, window, L);
+                         h_q, h_kv, d_head, scale, window, 0, L);
 }
 
 int gqa_decode_fp8kv_window(const void* q, const void* k_cache, const void* v_cache,
@@ -499,7 +523,26 @@ int gqa_decode_fp8kv_window(const void* q, const void* k_cache, const void* v_ca
                             const decattn_launch* L) {
   if (window < 1) return DECATTN_ERR_INVALID_ARG;
   return gqa_decode_impl(q, k_cache, v_cache, k_scale, v_scale, true, block_table, seq_lens, out,
-                         h_q, h_kv, d_head, scale, window, L);
+                         h_q, h_kv, d_head, scale, window, 0, L);
+}
+
+int gqa_decode_sinks(const void* q, const void* k_cache, const void* v_cache,
+                     const int32_t* block_table, const int32_t* seq_lens, void* out, int h_q,
+                     int h_kv, int d_head, float scale, int window, int sinks,
+                     const decattn_launch* L) {
+  if (window < 1 || sinks < 0) return DECATTN_ERR_INVALID_ARG;
+  return gqa_decode_impl(q, k_cache, v_cache, nullptr, nullptr, false, block_table, seq_lens, out,
+                         h_q, h_kv, d_head, scale, window, sinks, L);
+}
+
+int gqa_decode_fp8kv_sinks(const void* q, const void* k_cache, const void* v_cache,
+                           const float* k_scale, const float* v_scale,
+                           const int32_t* block_table, const int32_t* seq_lens, void* out,
+                           int h_q, int h_kv, int d_head, float scale, int window, int sinks,
+                           const decattn_launch* L) {
+  if (window < 1 || sinks < 0) return DECATTN_ERR_INVALID_ARG;
+  return gqa_decode_impl(q, k_cache, v_cache, k_scale, v_scale, true, block_table, seq_lens, out,
+                         h_q, h_kv, d_head, scale, window, sinks, L);
 }
 
 int mla_decode(const void* q_absorbed, const void* q_rope, const void* latent_cache,
@@ -653,6 +696,308 @@ int mla_kv_append(const void* latent_new, const int32_t* positions, const int32_
                   void* latent_cache, const decattn_launch* L) {
   return kv_append_impl(latent_new, nullptr, nullptr, nullptr, false, positions, block_table,
                         latent_cache, nullptr, kMlaWidth, kMlaWidth, true, L);
+}
+
+int paged_plan(const int32_t* cached_lens, const int32_t* new_lens, int32_t* block_table,
+               int32_t* free_blocks, const int32_t* free_count, int32_t* free_count_out,
+               int32_t* seq_lens, int32_t* q_start, int32_t* slots, int32_t* positions,
+               int max_tokens, const decattn_launch* L) {
+  if (!L) return DECATTN_ERR_INVALID_ARG;
+  if (L->batch < 1 || L->num_blocks < 1 || L->max_blocks_per_seq < 1 || max_tokens < 0)
+    return DECATTN_ERR_INVALID_ARG;
+  if (!is_pow2(L->block_size)) return DECATTN_ERR_INVALID_ARG;
+  if (L->block_size < 8 || L->block_size > 256 || L->batch > kPlanMaxBatch)
+    return DECATTN_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(L->num_blocks) * L->block_size > 0x7fffffffLL ||
+      static_cast<int64_t>(L->max_blocks_per_seq) * L->block_size > 0x7fffffffLL - 256)
+    return DECATTN_ERR_UNSUPPORTED;
+  const void* all[] = {cached_lens, new_lens, block_table, free_blocks, free_count,
+                       free_count_out, seq_lens, q_start};
+  for (const void* a : all)
+    if (!a || !aligned(a, 4)) return DECATTN_ERR_INVALID_ARG;
+  if (max_tokens > 0 && (!slots || !positions)) return DECATTN_ERR_INVALID_ARG;
+  if (!aligned(slots, 4) || !aligned(positions, 4)) return DECATTN_ERR_INVALID_ARG;
+  if (L->err_flag && !aligned(L->err_flag, 4)) return DECATTN_ERR_INVALID_ARG;
+  PlanParams p{};
+  p.cached_lens = cached_lens;
+  p.new_lens = new_lens;
+  p.block_table = block_table;
+  p.free_blocks = free_blocks;
+  p.free_count = free_count;
+  p.free_count_out = free_count_out;
+  p.seq_lens = seq_lens;
+  p.q_start = q_start;
+  p.slots = slots;
+  p.positions = positions;
+  p.err_flag = L->err_flag;
+  p.batch = L->batch;
+  p.max_tokens = max_tokens;
+  p.block_size = L->block_size;
+  p.log2_block_size = ilog2(L->block_size);
+  p.num_blocks = L->num_blocks;
+  p.max_blocks_per_seq = L->max_blocks_per_seq;
+  const cudaError_t e = launch_paged_plan(p, static_cast<cudaStream_t>(L->stream));
+  return e == cudaSuccess ? DECATTN_OK : DECATTN_ERR_CUDA;
+}
+
+int decattn_rope_fill(decattn_rope* rope, const double* inv_freq, int rot_dim,
+                      const int* sections, int n_axes, int interleaved) {
+  if (!rope || !inv_freq || n_axes < 1 || n_axes > 8 || (interleaved != 0 && interleaved != 1))
+    return DECATTN_ERR_INVALID_ARG;
+  if (rot_dim < 16 || rot_dim > kHeadDim || rot_dim % 16 != 0) return DECATTN_ERR_UNSUPPORTED;
+  if (!sections && n_axes != 1) return DECATTN_ERR_INVALID_ARG;
+  const int pairs = rot_dim / 2;
+  int64_t sum = 0;
+  for (int a = 0; sections && a < n_axes; ++a) {
+    if (sections[a] < 0) return DECATTN_ERR_INVALID_ARG;
+    sum += sections[a];
+  }
+  if (sections && sum != pairs) return DECATTN_ERR_INVALID_ARG;
+  for (int i = 0; i < pairs; ++i)
+    if (!std::isfinite(inv_freq[i])) return DECATTN_ERR_INVALID_ARG;
+  *rope = decattn_rope{};
+  rope->rot_dim = rot_dim;
+  rope->n_axes = n_axes;
+  rope->interleaved = interleaved;
+  int axis = 0, left = sections ? sections[0] : pairs;
+  for (int i = 0; i < pairs; ++i) {
+    while (left == 0) left = sections[++axis];
+    --left;
+    rope->axis[i] = static_cast<uint8_t>(axis);
+    // Turns per position modulo one turn, as a 64-bit fraction.  The double
+    // product's relative error of 2^-53 is the frequency's own precision.
+    double turns = inv_freq[i] / 6.283185307179586476925286766559;
+    turns -= std::floor(turns);
+    const double scaled = std::ldexp(turns, 64);  // <= 2^64; exact
+    rope->turns[i] = scaled >= 18446744073709551616.0 ? 0 : static_cast<uint64_t>(scaled);
+  }
+  return DECATTN_OK;
+}
+
+static int rope_append_impl(const void* q, const void* k_new, const void* v_new, int64_t q_stride,
+                            int64_t k_stride, int64_t v_stride, const float* k_scale,
+                            const float* v_scale, bool e4m3, const int32_t* positions,
+                            const decattn_rope* rope, const int32_t* slots, void* q_out,
+                            void* k_cache, void* v_cache, int tokens, int h_q, int h_kv,
+                            int d_head, const decattn_launch* L) {
+  if (!L || !rope) return DECATTN_ERR_INVALID_ARG;
+  if (L->num_blocks < 1 || tokens < 0) return DECATTN_ERR_INVALID_ARG;
+  if (L->dtype != DECATTN_FP16 && L->dtype != DECATTN_BF16) return DECATTN_ERR_INVALID_ARG;
+  if (!is_pow2(L->block_size)) return DECATTN_ERR_INVALID_ARG;
+  if (L->block_size < 8 || L->block_size > 256) return DECATTN_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(L->num_blocks) * L->block_size > 0x7fffffffLL)
+    return DECATTN_ERR_UNSUPPORTED;
+  if (h_q < 1 || h_kv < 1 || h_q > (1 << 20) || h_kv > 1024) return DECATTN_ERR_INVALID_ARG;
+  if (d_head != kHeadDim) return DECATTN_ERR_UNSUPPORTED;
+  if (rope->rot_dim < 16 || rope->rot_dim > kHeadDim || rope->rot_dim % 16 != 0)
+    return DECATTN_ERR_UNSUPPORTED;
+  if (rope->n_axes < 1 || rope->n_axes > 8 || (rope->interleaved != 0 && rope->interleaved != 1))
+    return DECATTN_ERR_INVALID_ARG;
+  for (int i = 0; i < rope->rot_dim / 2; ++i)
+    if (rope->axis[i] >= rope->n_axes) return DECATTN_ERR_INVALID_ARG;
+  if (L->err_flag && !aligned(L->err_flag, 4)) return DECATTN_ERR_INVALID_ARG;
+  if (tokens == 0) return DECATTN_OK;
+  if (!q || !k_new || !v_new || !positions || !slots || !q_out || !k_cache || !v_cache)
+    return DECATTN_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(q_out, 16) ||
+      !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(positions, 4) ||
+      !aligned(slots, 4))
+    return DECATTN_ERR_INVALID_ARG;
+  if (q_stride % 8 != 0 || k_stride % 8 != 0 || v_stride % 8 != 0 ||
+      q_stride < static_cast<int64_t>(h_q) * kHeadDim ||
+      k_stride < static_cast<int64_t>(h_kv) * kHeadDim ||
+      v_stride < static_cast<int64_t>(h_kv) * kHeadDim)
+    return DECATTN_ERR_INVALID_ARG;
+  // In place only where every row stays where it is.
+  if (q_out == q && q_stride != static_cast<int64_t>(h_q) * kHeadDim)
+    return DECATTN_ERR_INVALID_ARG;
+  if (e4m3 && (!k_scale || !v_scale || !aligned(k_scale, 4) || !aligned(v_scale, 4)))
+    return DECATTN_ERR_INVALID_ARG;
+  RopeParams p{};
+  p.q = q;
+  p.k = k_new;
+  p.v = v_new;
+  p.q_out = q_out;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.positions = positions;
+  p.slots = slots;
+  p.err_flag = L->err_flag;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.tokens = tokens;
+  p.h_q = h_q;
+  p.h_kv = h_kv;
+  p.num_slots = L->num_blocks * L->block_size;
+  p.rope = *rope;
+  const cudaError_t e = launch_rope_append(p, e4m3, L->dtype == DECATTN_BF16,
+                                           static_cast<cudaStream_t>(L->stream));
+  return e == cudaSuccess ? DECATTN_OK : DECATTN_ERR_CUDA;
+}
+
+int gqa_rope_append(const void* q, const void* k_new, const void* v_new, int64_t q_stride,
+                    int64_t k_stride, int64_t v_stride, const int32_t* positions,
+                    const decattn_rope* rope, const int32_t* slots, void* q_out, void* k_cache,
+                    void* v_cache, int tokens, int h_q, int h_kv, int d_head,
+                    const decattn_launch* L) {
+  return rope_append_impl(q, k_new, v_new, q_stride, k_stride, v_stride, nullptr, nullptr, false,
+                          positions, rope, slots, q_out, k_cache, v_cache, tokens, h_q, h_kv,
+                          d_head, L);
+}
+
+int gqa_rope_append_fp8kv(const void* q, const void* k_new, const void* v_new, int64_t q_stride,
+                          int64_t k_stride, int64_t v_stride, const float* k_scale,
+                          const float* v_scale, const int32_t* positions,
+                          const decattn_rope* rope, const int32_t* slots, void* q_out,
+                          void* k_cache, void* v_cache, int tokens, int h_q, int h_kv,
+                          int d_head, const decattn_launch* L) {
+  return rope_append_impl(q, k_new, v_new, q_stride, k_stride, v_stride, k_scale, v_scale, true,
+                          positions, rope, slots, q_out, k_cache, v_cache, tokens, h_q, h_kv,
+                          d_head, L);
+}
+
+// Pieces (of two Q tiles) that a step's rows can at most be cut into.
+static int64_t prefill_items(int batch, int tokens, int max_q_len, int group) {
+  const int tpi = 2 * (128 / group);
+  const int64_t by_rows = static_cast<int64_t>(tokens) / tpi + batch;
+  const int64_t by_seq = static_cast<int64_t>(batch) *
+                         ((static_cast<int64_t>(max_q_len) + tpi - 1) / tpi);
+  return by_rows < by_seq ? by_rows : by_seq;
+}
+
+static int plan_prefill_splits(int batch, int tokens, int max_q_len, int h_q, int h_kv,
+                               int max_seq_len, int window, int sinks, int sms) {
+  const int64_t units = prefill_items(batch, tokens, max_q_len, h_q / h_kv) * h_kv;
+  int64_t span = max_seq_len;
+  if (window > 0) {
+    const int64_t seen = static_cast<int64_t>(window) + max_q_len + sinks + 256;
+    if (seen < span) span = seen;
+  }
+  const int64_t tiles = (span + 127) / 128;
+  int64_t ns = units > 0 ? sms / units : 1;  // one wave of one CTA per SM
+  if (ns > tiles / 2) ns = tiles / 2;
+  if (ns > DECATTN_MAX_SPLITS) ns = DECATTN_MAX_SPLITS;
+  return ns < 1 ? 1 : static_cast<int>(ns);
+}
+
+size_t gqa_prefill_workspace_size(int tokens, int h_q, int d_head, int num_splits) {
+  return gqa_decode_workspace_size(tokens, h_q, d_head, num_splits);
+}
+
+int gqa_prefill_plan_splits(int batch, int tokens, int max_q_len, int h_q, int h_kv, int d_head,
+                            int max_seq_len, int window, int sinks, int num_sms) {
+  if (batch < 1 || tokens < 0 || max_q_len < 1 || h_q < 1 || h_kv < 1 || h_q % h_kv != 0 ||
+      h_q / h_kv > 64 || d_head < 1 || max_seq_len < 0 || window < 0 || sinks < 0)
+    return DECATTN_ERR_INVALID_ARG;
+  if (num_sms <= 0) num_sms = device_sm_count();
+  if (num_sms <= 0) return DECATTN_ERR_CUDA;
+  return plan_prefill_splits(batch, tokens, max_q_len, h_q, h_kv, max_seq_len, window, sinks,
+                             num_sms);
+}
+
+static int gqa_prefill_impl(const void* q, const void* k_cache, const void* v_cache,
+                            const float* k_scale, const float* v_scale, bool fp8,
+                            const int32_t* block_table, const int32_t* q_start,
+                            const int32_t* seq_lens, void* out, int tokens, int max_q_len,
+                            int h_q, int h_kv, int d_head, float scale, int window, int sinks,
+                            const decattn_launch* L) {
+  if (tokens < 0 || max_q_len < 1 || sinks < 0) return DECATTN_ERR_INVALID_ARG;
+  if (tokens == 0) {
+    // No row to compute: q and out may be null, the rest is still checked.
+    static const uint4 nothing{};
+    q = q ? q : &nothing;
+    out = out ? out : const_cast<uint4*>(&nothing);
+  }
+  const int st = gqa_check_args(q, k_cache, v_cache, k_scale, v_scale, fp8, block_table,
+                                seq_lens, out, h_q, h_kv, d_head, scale, window, L);
+  if (st != DECATTN_OK) return st;
+  if (!q_start || !aligned(q_start, 4)) return DECATTN_ERR_INVALID_ARG;
+  if (tokens == 0) return DECATTN_OK;
+  const int group = h_q / h_kv;
+  int ns = L->num_splits;
+  if (ns == 0) {
+    const int sms = device_sm_count();
+    if (sms <= 0) return DECATTN_ERR_CUDA;
+    ns = plan_prefill_splits(L->batch, tokens, max_q_len, h_q, h_kv, L->max_seq_len, window,
+                             sinks, sms);
+  }
+  const int64_t items = prefill_items(L->batch, tokens, max_q_len, group);
+  if (items * h_kv * ns > 0x7fffffffLL || static_cast<int64_t>(tokens) * h_q > 0x7fffffffLL)
+    return DECATTN_ERR_UNSUPPORTED;
+  PrefillParams p{};
+  p.block_table = block_table;
+  p.q_start = q_start;
+  p.seq_lens = seq_lens;
+  p.out = out;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.err_flag = L->err_flag;
+  p.batch = L->batch;
+  p.tokens = tokens;
+  p.max_q_len = max_q_len;
+  p.h_q = h_q;
+  p.h_kv = h_kv;
+  p.group = group;
+  p.block_size = L->block_size;
+  p.log2_block_size = ilog2(L->block_size);
+  p.num_blocks = L->num_blocks;
+  p.max_blocks_per_seq = L->max_blocks_per_seq;
+  p.max_seq_len = L->max_seq_len;
+  p.window = window;
+  p.sinks = window > 0 ? sinks : 0;
+  p.tokens_per_tile = 128 / group;
+  p.n_items = static_cast<int>(items);
+  p.n_split = ns;
+  p.negate = scale < 0.f ? 1 : 0;
+  // A zero scale (equal weights) is a scale that no score can feel: the
+  // kernel's masked scores are -inf, and -inf times 0 would be NaN.
+  const float mag = std::fabs(scale) * 1.4426950408889634f;
+  p.scale_log2 = mag > 1e-37f ? mag : 1e-37f;
+  if (ns > 1) {
+    const size_t need = gqa_prefill_workspace_size(tokens, h_q, d_head, ns);
+    if (!L->workspace || L->workspace_bytes < need) return DECATTN_ERR_WORKSPACE;
+    p.part_o = static_cast<float*>(L->workspace);
+    p.part_lse = reinterpret_cast<float*>(
+        static_cast<char*>(L->workspace) +
+        align_up(static_cast<size_t>(tokens) * h_q * ns * d_head * sizeof(float)));
+  }
+  if (fp8) return DECATTN_ERR_UNSUPPORTED;
+  const bool bf16 = L->dtype == DECATTN_BF16;
+  const uint64_t rows_total = static_cast<uint64_t>(L->num_blocks) * L->block_size;
+  const uint32_t box_rows = static_cast<uint32_t>(L->block_size < 128 ? L->block_size : 128);
+  const uint64_t width = static_cast<uint64_t>(h_kv) * kHeadDim;
+  CUtensorMap tq, tk, tv;
+  if (!make_map_3d(&tq, q, bf16, kHeadDim, static_cast<uint64_t>(h_q),
+                   static_cast<uint64_t>(tokens), 64, static_cast<uint32_t>(group),
+                   static_cast<uint32_t>(p.tokens_per_tile)) ||
+      !make_map_2d(&tk, k_cache, bf16, width, rows_total, width * 2, 64, box_rows) ||
+      !make_map_2d(&tv, v_cache, bf16, width, rows_total, width * 2, 64, box_rows))
+    return DECATTN_ERR_CUDA;
+  const cudaError_t e =
+      launch_gqa_prefill(p, tq, tk, tv, bf16, static_cast<cudaStream_t>(L->stream));
+  return e == cudaSuccess ? DECATTN_OK : DECATTN_ERR_CUDA;
+}
+
+int gqa_prefill(const void* q, const void* k_cache, const void* v_cache,
+                const int32_t* block_table, const int32_t* q_start, const int32_t* seq_lens,
+                void* out, int tokens, int max_q_len, int h_q, int h_kv, int d_head, float scale,
+                int window, int sinks, const decattn_launch* L) {
+  return gqa_prefill_impl(q, k_cache, v_cache, nullptr, nullptr, false, block_table, q_start,
+                          seq_lens, out, tokens, max_q_len, h_q, h_kv, d_head, scale, window,
+                          sinks, L);
+}
+
+int gqa_prefill_fp8kv(const void* q, const void* k_cache, const void* v_cache,
+                      const float* k_scale, const float* v_scale, const int32_t* block_table,
+                      const int32_t* q_start, const int32_t* seq_lens, void* out, int tokens,
+                      int max_q_len, int h_q, int h_kv, int d_head, float scale, int window,
+                      int sinks, const decattn_launch* L) {
+  return gqa_prefill_impl(q, k_cache, v_cache, k_scale, v_scale, true, block_table, q_start,
+                          seq_lens, out, tokens, max_q_len, h_q, h_kv, d_head, scale, window,
+                          sinks, L);
 }
 
 // MLA's absorption GEMMs: Y[b, i, :] = X[b, i, :] W_i^T for every head i.

@@ -13,12 +13,63 @@ namespace decattn {
 // Tiles start at the block (or 64-token) boundary holding w0; blocks wholly
 // before the window are never read.  `bad` is this thread's verdict only: the
 // caller ORs it over the CTA (block ids are checked strided by threadIdx.x).
-struct GqaSpan {
-  int w0, t_begin, t_end, bad;
+//
+// kSinks: the sequence's first s_end = min(sinks, w0) tokens stay visible
+// too.  Its tiles are then those of [0, s_end) followed by those from the
+// window's boundary on, numbered through and dealt out to the splits in that
+// order; a tile holds tokens of one of the two ranges only, so no token is
+// counted twice where both ranges meet in one block.  With sinks >= w0 the
+// ranges join: plain attention over the whole sequence.
+struct GqaTile {
+  int t0;    // first token
+  int skip;  // rows [skip, nval) of the tile's 64 are attended
+  int nval;
 };
 
-DECATTN_DEV GqaSpan gqa_span(const GqaParams& p, int split, int j, int b) {
-  GqaSpan r;
+template <bool kSinks>
+struct GqaSpan {
+  int w0, t_begin, t_end, bad;
+  int n_tiles;
+  int tile0, sink_tiles, s_end, base, seq_len;  // kSinks only
+
+  DECATTN_DEV GqaTile tile(int it) const {
+    GqaTile r;
+    if constexpr (kSinks) {
+      const int vt = tile0 + it;
+      const bool sink = vt < sink_tiles;
+      r.t0 = sink ? vt * kTile : base + (vt - sink_tiles) * kTile;
+      r.skip = sink ? 0 : max(0, w0 - r.t0);
+      r.nval = min(kTile, (sink ? s_end : seq_len) - r.t0);
+    } else {
+      r.t0 = t_begin + it * kTile;
+      r.skip = max(0, w0 - r.t0);
+      r.nval = min(kTile, t_end - r.t0);
+    }
+    return r;
+  }
+  DECATTN_DEV bool empty() const { return kSinks ? n_tiles <= 0 : t_end <= t_begin; }
+  // One past the last token whose block may be read.
+  DECATTN_DEV int end() const { return kSinks ? seq_len : t_end; }
+};
+
+// 1 (and the flag) if a block id of tokens [t0, t1) is out of range.
+DECATTN_DEV int gqa_bad_blocks(const GqaParams& p, int b, int t0, int t1) {
+  int bad = 0;
+  const int32_t* bt = p.block_table + static_cast<size_t>(b) * p.max_blocks_per_seq;
+  const int k1 = (t1 - 1) >> p.log2_block_size;
+  for (int k = (t0 >> p.log2_block_size) + threadIdx.x; k <= k1; k += blockDim.x) {
+    const int id = bt[k];
+    if (id < 0 || id >= p.num_blocks) {
+      bad = 1;
+      flag_error(p.err_flag, kFlagBadBlock);
+    }
+  }
+  return bad;
+}
+
+template <bool kSinks = false>
+DECATTN_DEV GqaSpan<kSinks> gqa_span(const GqaParams& p, int split, int j, int b) {
+  GqaSpan<kSinks> r;
   const int seq_len = p.seq_lens[b];
   r.bad = 0;
   if (seq_len < 0 || seq_len > p.max_seq_len) {
@@ -26,19 +77,32 @@ DECATTN_DEV GqaSpan gqa_span(const GqaParams& p, int split, int j, int b) {
     if (threadIdx.x == 0 && split == 0 && j == 0) flag_error(p.err_flag, kFlagBadSeqLen);
   }
   r.w0 = (p.window > 0 && seq_len > p.window) ? seq_len - p.window : 0;
+  if (kSinks && p.sinks >= r.w0) r.w0 = 0;
   const int base = r.w0 & ~((p.block_size < kTile ? p.block_size : kTile) - 1);
-  r.t_begin = base + split * p.tokens_per_split;
-  r.t_end = r.bad ? r.t_begin : min(seq_len, r.t_begin + p.tokens_per_split);
-  if (!r.bad && r.t_end > r.t_begin) {
-    const int32_t* bt = p.block_table + static_cast<size_t>(b) * p.max_blocks_per_seq;
-    const int k1 = (r.t_end - 1) >> p.log2_block_size;
-    for (int k = (r.t_begin >> p.log2_block_size) + threadIdx.x; k <= k1; k += blockDim.x) {
-      const int id = bt[k];
-      if (id < 0 || id >= p.num_blocks) {
-        r.bad = 1;
-        flag_error(p.err_flag, kFlagBadBlock);
-      }
-    }
+  if constexpr (kSinks) {
+    r.seq_len = seq_len;
+    r.base = base;
+    r.s_end = min(p.sinks, r.w0);
+    r.sink_tiles = (r.s_end + kTile - 1) / kTile;
+    r.t_begin = r.t_end = 0;
+    r.n_tiles = 0;
+    if (r.bad) return r;
+    const int total = r.sink_tiles + (seq_len - base + kTile - 1) / kTile;
+    const int per = p.tokens_per_split / kTile;
+    r.tile0 = min(split * per, total);
+    r.n_tiles = min(per, total - r.tile0);
+    if (r.n_tiles <= 0) return r;
+    const int end = r.tile0 + r.n_tiles;
+    if (r.tile0 < r.sink_tiles)
+      r.bad |= gqa_bad_blocks(p, b, r.tile0 * kTile, min(r.s_end, end * kTile));
+    if (end > r.sink_tiles)
+      r.bad |= gqa_bad_blocks(p, b, base + max(0, r.tile0 - r.sink_tiles) * kTile,
+                              min(seq_len, base + (end - r.sink_tiles) * kTile));
+  } else {
+    r.t_begin = base + split * p.tokens_per_split;
+    r.t_end = r.bad ? r.t_begin : min(seq_len, r.t_begin + p.tokens_per_split);
+    if (!r.bad && r.t_end > r.t_begin) r.bad = gqa_bad_blocks(p, b, r.t_begin, r.t_end);
+    r.n_tiles = (r.t_end - r.t_begin + kTile - 1) / kTile;
   }
   return r;
 }

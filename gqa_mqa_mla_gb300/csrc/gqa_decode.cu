@@ -715,7 +715,7 @@ __host__ __device__ constexpr int smem_bytes() {
   return 1024 /*alignment slack*/ + kStages * stage_bytes<Consumer>() + 256 /*barriers*/;
 }
 
-template <class Consumer, bool kBF16, int kStages>
+template <class Consumer, bool kBF16, int kStages, bool kSinks>
 __global__ void __launch_bounds__(32 * (1 + Consumer::kWarps), Consumer::kMinBlocks)
     gqa_partial_kernel(const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const GqaParams p) {
@@ -735,8 +735,7 @@ __global__ void __launch_bounds__(32 * (1 + Consumer::kWarps), Consumer::kMinBlo
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = p.group;
 
-  const GqaSpan span = gqa_span(p, split, j, b);
-  const int w0 = span.w0, t_begin = span.t_begin, t_end = span.t_end;
+  const GqaSpan<kSinks> span = gqa_span<kSinks>(p, split, j, b);
   int bad = span.bad;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -750,12 +749,12 @@ __global__ void __launch_bounds__(32 * (1 + Consumer::kWarps), Consumer::kMinBlo
   bad = __syncthreads_or(bad);
 
   const size_t row0 = static_cast<size_t>(b) * p.h_q + static_cast<size_t>(j) * G;
-  if (bad || t_end <= t_begin) {
+  if (bad || span.empty()) {
     gqa_write_empty(p, row0, G, split, bad);
     return;
   }
 
-  const int n_tiles = (t_end - t_begin + kTile - 1) / kTile;
+  const int n_tiles = span.n_tiles;
   const int bs = p.block_size;
 
   if (warp == 0) {
@@ -770,8 +769,8 @@ __global__ void __launch_bounds__(32 * (1 + Consumer::kWarps), Consumer::kMinBlo
       for (int it = 0; it < n_tiles; ++it) {
         const int s = it % kStages;
         if (!mbar_wait(empty0 + 8 * s, ((it / kStages) & 1) ^ 1, p.err_flag)) break;
-        const int t0 = t_begin + it * kTile;
-        const int nval = min(kTile, t_end - t0);
+        const GqaTile tl = span.tile(it);
+        const int t0 = tl.t0, nval = tl.nval;
         const uint32_t st = smem_u32(smem + s * kStage);
         const uint32_t fb = full0 + 8 * s;
         if constexpr (Consumer::kCacheBytes == 1) {
@@ -835,9 +834,8 @@ __global__ void __launch_bounds__(32 * (1 + Consumer::kWarps), Consumer::kMinBlo
       ok = false;
       break;
     }
-    const int t0 = t_begin + it * kTile;
-    const int nval = min(kTile, t_end - t0);
-    c.tile(smem + s * kStage, max(0, w0 - t0), nval, scale_log2);
+    const GqaTile tl = span.tile(it);
+    c.tile(smem + s * kStage, tl.skip, tl.nval, scale_log2);
     fence_proxy_async_smem();  // order any generic smem writes before the next TMA fill
     __syncwarp();
     if (lane == 0) mbar_arrive(empty0 + 8 * s);
@@ -884,10 +882,10 @@ __global__ void __launch_bounds__(32 * (1 + Consumer::kWarps), Consumer::kMinBlo
   }
 }
 
-template <class Consumer, bool kBF16, int kStages>
-cudaError_t launch_one(const GqaParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
-                       cudaStream_t stream, unsigned max_cluster) {
-  auto kern = gqa_partial_kernel<Consumer, kBF16, kStages>;
+template <class Consumer, bool kBF16, int kStages, bool kSinks>
+cudaError_t launch_with(const GqaParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
+                        cudaStream_t stream, unsigned max_cluster) {
+  auto kern = gqa_partial_kernel<Consumer, kBF16, kStages, kSinks>;
   constexpr int smem = smem_bytes<Consumer, kStages>();
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -920,6 +918,14 @@ cudaError_t launch_one(const GqaParams& p, const CUtensorMap& tk, const CUtensor
   return cudaGetLastError();
 }
 
+// A window with kept first tokens has its own instantiations, so that the
+// plain and windowed calls' code stays as it was.
+template <class Consumer, bool kBF16, int kStages>
+cudaError_t launch_one(const GqaParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
+                       cudaStream_t stream, unsigned max_cluster) {
+  return p.sinks > 0 ? launch_with<Consumer, kBF16, kStages, true>(p, tk, tv, stream, max_cluster)
+                     : launch_with<Consumer, kBF16, kStages, false>(p, tk, tv, stream, max_cluster);
+}
 
 template <bool kBF16>
 cudaError_t dispatch(const GqaParams& p, const CUtensorMap& tk, const CUtensorMap& tv,

@@ -1,0 +1,666 @@
+// gqa_prefill.cu -- attention of a chunk of new tokens per sequence over a
+// paged KV cache (MHA / GQA / MQA), on tcgen05 / TMEM, sm_103a.
+//
+// Row (i, h) of sequence b, position p = L - n + i, sees cache positions
+// t <= p (with a window W and S kept first tokens: t > p - W or t < S):
+//     out = sum_t e^{s_t} v_t / sum_t e^{s_t},   s_t = scale q . k_t.
+// The G = h_q / h_kv query heads of a KV head read the same cache rows, so a
+// Q tile packs floor(128 / G) tokens x G heads into the 128 rows of an MMA,
+// and a CTA works on two such tiles (A: the first tokens, B: the next ones)
+// of one KV head, against the same 128-token K and V tiles:
+//     S_X = Q_X K^T   128 x 128 x 128        X = A, B
+//     O_X += P_X V    128 x 128 x 128
+// Bound by the tensor cores once a chunk has a few hundred rows per KV head
+// (each 64 KB pair of K and V tiles then serves 2 x 2 MMAs of 2^21 products),
+// by HBM below that; few rows over a long cache are cut along the cache
+// (n_split) and joined by a log-sum-exp combine.
+//
+// Operand placement:
+//   Q_A, Q_B   shared memory [2 halves][128 rows][128 B], 128-byte swizzle,
+//              by TMA (a 3-D box: 64 columns x G heads x tokens)   A of S
+//   K, V       one TMA ring of five 32 KB slots, K(0) V(0) K(1) V(1) ...,
+//              [2 halves][128 tokens][128 B], 128-byte swizzle, one box per
+//              half and cache block         K: B of S;  V: B of P V (MN-major)
+//   S_X, P_X   TMEM, 128 fp32 columns; P_X (16-bit, 64 columns) over S_X  A of P V
+//   O_X        TMEM, 128 fp32 columns
+// (2 x (128 + 128) columns: all of TMEM, one CTA per SM.)
+//
+// Warps (384 threads):
+//   0-3, 4-7  softmax of tile A, of tile B: a thread owns a row (TMEM lane),
+//             so no value of a row is ever exchanged: running maximum, lazy
+//             rescale of O, P, running sum; epilogue;
+//   8         TMA producer (walks the block table, checks the block ids);
+//   9         MMA issuer: P_A V, S_A of the next tile, P_B V, S_B of the next
+//             tile: while one tile's softmax runs, the tensor cores work on
+//             the other's products.  MMAs of one thread run in order, so
+//             S_A(j + 1) may overwrite P_A(j) right behind its last reader;
+//   10        TMEM allocation (11 only fills its warpgroup).
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace decattn {
+namespace {
+
+constexpr int kM = 128;                        // rows of a Q tile
+constexpr int kKv = 128;                       // tokens of a K / V tile
+constexpr int kHalf = 128 * 128;               // 64 columns x 128 rows, 16 KB
+constexpr int kTileBytes = 2 * kHalf;          // 32 KB
+constexpr int kRing = 5;
+constexpr int kOffRing = 2 * kTileBytes;       // behind Q_A, Q_B
+constexpr int kOffBars = kOffRing + kRing * kTileBytes;
+constexpr int kSmemBytes = 1024 + kOffBars + 512;
+static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
+
+constexpr int kThreads = 384;
+constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpTmem = 10;
+constexpr int kTmemS = 0;                      // S_X: 128 X
+constexpr int kTmemO = 256;                    // O_X: 256 + 128 X
+constexpr float kNegInf = -__builtin_huge_valf();
+constexpr float kRescaleThreshold = 8.0f;      // log2 units: P stays <= 2^8
+
+enum : int {
+  kBarQ = 0,
+  kBarFull = 1,                 // ring slot landed
+  kBarEmpty = kBarFull + kRing, // ring slot free
+  kBarS = kBarEmpty + kRing,    // 2: S_X computed
+  kBarP = kBarS + 2,            // 2: P_X written (128 arrivals)
+  kBarO = kBarP + 2,            // 2: O_X complete
+  kBarDrain = kBarO + 2,
+  kNumBars = kBarDrain + 1
+};
+
+// One CTA's work: rows of one sequence and KV head against a range of tiles.
+struct Item {
+  int b, j, split;
+  int n, len;       // chunk length, cache length
+  int q0;           // first packed row of the sequence
+  int i0;           // first token of the chunk in tile A
+  int tok[2];       // tokens in tile A, B
+  int lo, s_end, base, sink_tiles;
+  int hi;           // one past the last position any row sees
+  int tile0;        // first tile of this split
+  int n_tiles[2];   // tiles that tile A, B need, from tile0 on
+  int bad;
+};
+
+struct Tile {
+  int t0, skip, nval;  // rows [skip, nval) hold tokens that may be seen
+};
+
+__device__ __forceinline__ Tile tile_of(const Item& w, int it) {
+  const int vt = w.tile0 + it;
+  const bool sink = vt < w.sink_tiles;
+  Tile r;
+  r.t0 = sink ? vt * kKv : w.base + (vt - w.sink_tiles) * kKv;
+  r.skip = sink ? 0 : max(0, w.lo - r.t0);
+  r.nval = min(kKv, (sink ? w.s_end : w.hi) - r.t0);
+  return r;
+}
+
+// Number of tiles up to and including the one that holds position `last`.
+__device__ __forceinline__ int tiles_to(const Item& w, int last) {
+  return last < w.base ? 0 : w.sink_tiles + (last - w.base) / kKv + 1;
+}
+
+// Finds the item of this CTA: the rows of all sequences are cut into pieces
+// of 2 tpt tokens, numbered through; false if there is no such piece.
+__device__ __forceinline__ bool find_item(const PrefillParams& p, int index, Item& w) {
+  __shared__ int warp_sum[kThreads / 32];
+  __shared__ int found[3];  // b, piece within b, 1
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int tpi = 2 * p.tokens_per_tile;
+  int carry = 0;
+  if (threadIdx.x == 0) found[2] = 0;
+  for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
+    const int b = b0 + threadIdx.x;
+    int cnt = 0;
+    if (b < p.batch) {
+      const int a = p.q_start[b], e = p.q_start[b + 1];
+      if (a < 0 || e < a || e > p.tokens || e - a > p.max_q_len) {
+        if (blockIdx.x == 0) flag_error(p.err_flag, kFlagBadSeqLen);
+      } else {
+        cnt = (e - a + tpi - 1) / tpi;
+      }
+    }
+    int inc = cnt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += up;
+    }
+    __syncthreads();
+    if (lane == 31) warp_sum[warp] = inc;
+    __syncthreads();
+    int before = carry, total = 0;
+#pragma unroll
+    for (int k = 0; k < kThreads / 32; ++k) {
+      if (k < warp) before += warp_sum[k];
+      total += warp_sum[k];
+    }
+    const int first = before + inc - cnt;
+    if (index >= first && index < first + cnt) {
+      found[0] = b;
+      found[1] = index - first;
+      found[2] = 1;
+    }
+    carry += total;
+    if (carry > index) break;  // uniform
+  }
+  __syncthreads();
+  if (!found[2]) return false;
+  w.b = found[0];
+  w.q0 = p.q_start[w.b];
+  w.n = p.q_start[w.b + 1] - w.q0;
+  w.i0 = found[1] * tpi;
+  w.tok[0] = min(p.tokens_per_tile, w.n - w.i0);
+  w.tok[1] = max(0, min(p.tokens_per_tile, w.n - w.i0 - p.tokens_per_tile));
+  w.len = p.seq_lens[w.b];
+  w.bad = w.len < 0 || w.len > p.max_seq_len;
+  if (w.bad) {
+    if (threadIdx.x == 0) flag_error(p.err_flag, kFlagBadSeqLen);
+    w.len = 0;
+  }
+  // Positions of the first and last rows, and the tiles that they see: with
+  // a window those of [0, s_end) (kept first tokens before the window of the
+  // first row), then those from the window's block boundary on.  Kept tokens
+  // that reach the window join it.
+  const int p_first = w.len - w.n + w.i0;
+  const int p_last = p_first + w.tok[0] + w.tok[1] - 1;
+  w.hi = max(0, min(w.len, p_last + 1));
+  w.lo = p.window > 0 ? max(0, p_first + 1 - p.window) : 0;
+  if (p.sinks >= w.lo) w.lo = 0;
+  w.lo = min(w.lo, w.hi);
+  w.s_end = min(p.sinks, w.lo);
+  w.base = w.lo & ~(min(p.block_size, kKv) - 1);
+  w.sink_tiles = (w.s_end + kKv - 1) / kKv;
+  const int total = w.bad ? 0 : tiles_to(w, w.hi - 1);
+  const int total_a = w.bad ? 0 : max(0, min(total, tiles_to(w, p_first + w.tok[0] - 1)));
+  const int per = (total + p.n_split - 1) / p.n_split;
+  w.tile0 = min(total, w.split * per);
+  w.n_tiles[0] = max(0, min(per, total_a - w.tile0));
+  w.n_tiles[1] = w.tok[1] > 0 ? min(per, total - w.tile0) : 0;
+  return true;
+}
+
+template <bool kBF16>
+__device__ __forceinline__ void store_row(const PrefillParams& p, int64_t row, int split, int c0,
+                                          const float (&o)[32], float inv) {
+  if (p.n_split == 1) {
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * kHeadDim + c0);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      dst[k] = make_uint4(pack2<kBF16>(o[8 * k] * inv, o[8 * k + 1] * inv),
+                          pack2<kBF16>(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
+                          pack2<kBF16>(o[8 * k + 4] * inv, o[8 * k + 5] * inv),
+                          pack2<kBF16>(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
+  } else {
+    float4* dst = reinterpret_cast<float4*>(p.part_o + (row * p.n_split + split) * kHeadDim + c0);
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      dst[k] = make_float4(o[4 * k] * inv, o[4 * k + 1] * inv, o[4 * k + 2] * inv,
+                           o[4 * k + 3] * inv);
+  }
+}
+
+template <bool kBF16>
+__global__ void __launch_bounds__(kThreads, 1)
+    gqa_prefill_kernel(const __grid_constant__ CUtensorMap tm_q,
+                       const __grid_constant__ CUtensorMap tm_k,
+                       const __grid_constant__ CUtensorMap tm_v, const PrefillParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bar0 = sbase + kOffBars;
+  auto bar = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
+  volatile int* abort_word = reinterpret_cast<volatile int*>(smem + kOffBars + kNumBars * 8);
+  volatile int* bad_word = abort_word + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffBars + kNumBars * 8 + 8);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // Longest work first: the last pieces of a chunk see the most positions.
+  Item w;
+  w.j = static_cast<int>(blockIdx.x) % p.h_kv;
+  const int rest = static_cast<int>(blockIdx.x) / p.h_kv;
+  w.split = rest % p.n_split;
+  if (!find_item(p, p.n_items - 1 - rest / p.n_split, w)) return;
+  const int n = max(w.n_tiles[0], w.n_tiles[1]);
+
+  const int G = p.group;
+  if (n == 0) {
+    // Nothing to see (or bad lengths): zero rows, or an empty partial.
+    const int rows = (w.tok[0] + w.tok[1]) * G;
+    for (int e = threadIdx.x; e < rows * 16; e += kThreads) {
+      const int r = e >> 4;
+      const int64_t row = static_cast<int64_t>(w.q0 + w.i0 + r / G) * p.h_q + w.j * G + r % G;
+      if (p.n_split == 1)
+        reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * kHeadDim)[e & 15] =
+            make_uint4(0, 0, 0, 0);
+      else if ((e & 15) == 0)
+        p.part_lse[row * p.n_split + w.split] = w.bad ? DECATTN_POISON_LSE : kNegInf;
+    }
+    return;
+  }
+
+  if (threadIdx.x == 0) {
+    mbar_init(bar(kBarQ), 1);
+    for (int s = 0; s < kRing; ++s) {
+      mbar_init(bar(kBarFull + s), 1);
+      mbar_init(bar(kBarEmpty + s), 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(bar(kBarS + x), 1);
+      mbar_init(bar(kBarP + x), kM);
+      mbar_init(bar(kBarO + x), 1);
+    }
+    mbar_init(bar(kBarDrain), 1);
+    *abort_word = 0;
+    *bad_word = 0;
+    fence_barrier_init();
+  }
+  if (warp == kWarpTmem) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  // Ring slot and phase parity of the e-th copy (e = 2 it: K, 2 it + 1: V).
+  auto slot_of = [](int e) { return e % kRing; };
+  auto phase_of = [](int e) { return static_cast<uint32_t>((e / kRing) & 1); };
+
+  if (warp >= 8) {
+    if (warp == kWarpLoad) {
+      // ---------------- TMA producer
+      const uint64_t keep = policy_evict_last();
+      if (lane == 0) {
+        tma_prefetch_desc(&tm_q);
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
+        const int tiles = w.tok[1] > 0 ? 2 : 1;
+        const uint32_t bytes = static_cast<uint32_t>(tiles * 2 * p.tokens_per_tile * G * 128);
+        mbar_arrive_expect_tx(bar(kBarQ), bytes);
+        for (int x = 0; x < tiles; ++x)
+          for (int h = 0; h < 2; ++h)
+            tma_load_3d(sbase + x * kTileBytes + h * kHalf, &tm_q, 64 * h, w.j * G,
+                        w.q0 + w.i0 + x * p.tokens_per_tile, bar(kBarQ));
+      }
+      const int32_t* bt = p.block_table + static_cast<size_t>(w.b) * p.max_blocks_per_seq;
+      const int bs = p.block_size, lg = p.log2_block_size;
+      const int x0 = w.j * kHeadDim;
+      const int kb_end = ((w.hi - 1) >> lg) + 1;
+      int cache0 = -(1 << 30), my_id = 0;
+      int issued = 0;
+      bool ok = true;
+      for (int it = 0; ok && it < n; ++it) {
+        const Tile t = tile_of(w, it);
+        const int kb0 = t.t0 >> lg;
+        const int nblk = bs >= kKv ? 1 : (t.nval + bs - 1) >> lg;
+        // The lanes hold the ids of the next 32 blocks (read ahead of use).
+        if (kb0 + nblk > cache0 + 32) {
+          cache0 = kb0;
+          my_id = kb0 + lane < kb_end ? bt[kb0 + lane] : 0;
+        }
+        int id = __shfl_sync(0xffffffffu, my_id, kb0 - cache0 + min(lane, nblk - 1));
+        if (id < 0 || id >= p.num_blocks) {
+          // Copy block 0 instead; the rows become zeros.
+          id = 0;
+          *bad_word = 1;
+          flag_error(p.err_flag, kFlagBadBlock);
+        }
+        const int row = id * bs + (bs >= kKv ? (t.t0 & (bs - 1)) : 0);
+        const uint32_t bytes = static_cast<uint32_t>(bs >= kKv ? kTileBytes : nblk * bs * 256);
+        for (int kv = 0; kv < 2; ++kv) {
+          const int e = 2 * it + kv, s = slot_of(e);
+          bool got = true;
+          if (lane == 0) {
+            got = mbar_wait_or_abort(bar(kBarEmpty + s), phase_of(e) ^ 1u, p.err_flag, abort_word);
+            if (got) mbar_arrive_expect_tx(bar(kBarFull + s), bytes);
+          }
+          if (__shfl_sync(0xffffffffu, got ? 1 : 0, 0) == 0) {
+            ok = false;
+            break;
+          }
+          issued = e + 1;
+          if (lane < nblk) {
+            const CUtensorMap* tm = kv ? &tm_v : &tm_k;
+            const uint32_t dst = sbase + kOffRing + s * kTileBytes + static_cast<uint32_t>(lane * bs * 128);
+            tma_load_2d_hint(dst, tm, x0, row, bar(kBarFull + s), keep);
+            tma_load_2d_hint(dst + kHalf, tm, x0 + 64, row, bar(kBarFull + s), keep);
+          }
+        }
+      }
+      // Never leave the CTA with copies in flight.
+      if (lane == 0) {
+        mbar_wait(bar(kBarQ), 0, p.err_flag);
+        for (int e = max(0, issued - kRing); e < issued; ++e)
+          if (!mbar_wait(bar(kBarFull + slot_of(e)), phase_of(e), p.err_flag)) break;
+      }
+      __syncwarp();
+    } else if (warp == kWarpMma) {
+      // ---------------- MMA issuer: the whole warp runs the loop, lane 0
+      // waits, one elected lane issues.
+      const uint64_t dq = smem_desc_sw128(sbase, 16, 1024);
+      const uint64_t dk = smem_desc_sw128(sbase + kOffRing, 16, 1024);
+      const uint64_t dv = smem_desc_sw128(sbase + kOffRing, kHalf, 1024);
+      constexpr uint32_t idesc_s = idesc_f16(kBF16, kM, kKv, false, false);
+      constexpr uint32_t idesc_o = idesc_f16(kBF16, kM, kHeadDim, false, true);
+      auto wait = [&](int bi, uint32_t parity) -> bool {
+        bool g = true;
+        if (lane == 0) g = mbar_wait_or_abort(bar(bi), parity, p.err_flag, abort_word);
+        g = __shfl_sync(0xffffffffu, g ? 1 : 0, 0) != 0;
+        tc_fence_after();
+        return g;
+      };
+      // S_X = Q_X K^T: eight k-steps of 16 dims, four per 64-column half.
+      auto issue_s = [&](int x, int s) {
+        const uint64_t a = dq + static_cast<uint64_t>((x * kTileBytes) >> 4);
+        const uint64_t b = dk + static_cast<uint64_t>((s * kTileBytes) >> 4);
+        const uint32_t done = bar(kBarS + x);
+        if (elect_one()) {
+  #pragma unroll
+          for (int ks = 0; ks < 8; ++ks) {
+            const uint64_t off = static_cast<uint64_t>(((ks >> 2) * kHalf + (ks & 3) * 32) >> 4);
+            tc_mma_f16(tmem + kTmemS + kKv * x, a + off, b + off, idesc_s, ks > 0 ? 1u : 0u);
+          }
+          tc_commit(done);
+        }
+        __syncwarp();
+      };
+      // O_X += P_X V: eight k-steps of 16 tokens, P from TMEM.
+      auto issue_pv = [&](int x, int s, bool first) {
+        const uint64_t b = dv + static_cast<uint64_t>((s * kTileBytes) >> 4);
+        const uint32_t acc0 = first ? 0u : 1u;
+        if (elect_one()) {
+  #pragma unroll
+          for (int ks = 0; ks < 8; ++ks)
+            tc_mma_f16_ts(tmem + kTmemO + kHeadDim * x, tmem + kTmemS + kKv * x + ks * 8,
+                          b + static_cast<uint64_t>((ks * 2048) >> 4), idesc_o, ks > 0 ? 1u : acc0);
+        }
+        __syncwarp();
+      };
+      auto commit = [&](int bi) {
+        const uint32_t at = bar(bi);
+        if (elect_one()) tc_commit(at);
+        __syncwarp();
+      };
+      bool ok = wait(kBarQ, 0) && wait(kBarFull + slot_of(0), phase_of(0));
+      if (ok) {
+        for (int x = 0; x < 2; ++x)
+          if (w.n_tiles[x] > 0) issue_s(x, slot_of(0));
+        commit(kBarEmpty + slot_of(0));
+      }
+      for (int it = 0; ok && it < n; ++it) {
+        const int ev = 2 * it + 1, ek = 2 * it + 2;
+        const Tile t = tile_of(w, it);
+        ok = wait(kBarFull + slot_of(ev), phase_of(ev));
+        if (ok && (t.nval < kKv || t.skip > 0)) {
+          // V rows outside [skip, nval) become zeros (P is 0 there, but the
+          // slots may hold NaN), while the softmax works on this tile.  (All
+          // 128 bytes of a row: the swizzle does not matter.)
+          uint8_t* v = smem + kOffRing + slot_of(ev) * kTileBytes;
+          for (int i = lane; i < (t.skip + kKv - t.nval) * 16; i += 32) {
+            const int k = i >> 4, c = i & 15;
+            const int r = k < t.skip ? k : t.nval + (k - t.skip);
+            *reinterpret_cast<uint4*>(v + (c >> 3) * kHalf + r * 128 + ((c & 7) << 4)) =
+                make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        bool have_k = false;
+        for (int x = 0; ok && x < 2; ++x) {
+          if (it >= w.n_tiles[x]) continue;
+          ok = wait(kBarP + x, it & 1);
+          if (!ok) break;
+          issue_pv(x, slot_of(ev), it == 0);
+          if (it + 1 < w.n_tiles[x]) {
+            if (!have_k) ok = wait(kBarFull + slot_of(ek), phase_of(ek));
+            have_k = true;
+            if (!ok) break;
+            issue_s(x, slot_of(ek));
+          } else {
+            commit(kBarO + x);
+          }
+        }
+        if (ok) {
+          commit(kBarEmpty + slot_of(ev));
+          if (it + 1 < n) commit(kBarEmpty + slot_of(ek));
+        }
+      }
+      // Wait (bounded) until every MMA this warp issued has completed.
+      if (elect_one()) {
+        tc_commit(bar(kBarDrain));
+        mbar_wait(bar(kBarDrain), 0, p.err_flag);
+      }
+      __syncwarp();
+    }
+  } else {
+    // ---------------- softmax: thread = row r of tile x
+    const int x = warp >> 2;
+    const int r = 32 * (warp & 3) + lane;
+    const int nt = w.n_tiles[x];
+    const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const uint32_t ts = tmem + lanes + kTmemS + kKv * x;
+    const uint32_t to = tmem + lanes + kTmemO + kHeadDim * x;
+    const int i = w.i0 + x * p.tokens_per_tile + min(r / G, max(0, w.tok[x] - 1));
+    const bool mine = r < w.tok[x] * G;
+    const int pos = w.len - w.n + i;
+    // Positions of the tile's first and last rows: tiles at or before the
+    // first (and inside the last one's window) need no mask.
+    const int pos0 = w.len - w.n + w.i0 + x * p.tokens_per_tile;
+    const int pos1 = pos0 + w.tok[x] - 1;
+    const float scale = p.scale_log2;
+    float m = kNegInf, l = 0.f;
+    bool ok = true;
+    for (int it = 0; it < nt; ++it) {
+      const Tile t = tile_of(w, it);
+      if (!mbar_wait_or_abort(bar(kBarS + x), it & 1, p.err_flag, abort_word)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const bool plain = !p.negate && t.skip == 0 && t.nval == kKv && t.t0 + kKv - 1 <= pos0 &&
+                         (p.window <= 0 || t.t0 > pos1 - p.window);
+      // Seen: [skip, nval), at or before the row's position, inside its
+      // window or among the kept first tokens.
+      const int c_hi = min(t.nval, pos + 1 - t.t0);
+      const int c_lo = p.window > 0 ? pos + 1 - p.window - t.t0 : 0;
+      const int c_sink = p.sinks - t.t0;
+      auto mask = [&](float (&v)[32], int c0) {
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          const int c = c0 + k;
+          const bool seen = c < c_hi && c >= t.skip && (c >= c_lo || c < c_sink);
+          v[k] = seen ? (p.negate ? -v[k] : v[k]) : kNegInf;
+        }
+      };
+      float va[32], vb[32], mx[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+      auto peak = [&](float (&v)[32], int c0) {
+        if (!plain) mask(v, c0);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) mx[k & 3] = fmaxf(mx[k & 3], v[k]);
+      };
+      tmem_ld32(ts, va);
+      tc_wait_ld_for(va);
+      tmem_ld32(ts + 32, vb);
+      peak(va, 0);
+      tc_wait_ld_for(vb);
+      tmem_ld32(ts + 64, va);
+      peak(vb, 32);
+      tc_wait_ld_for(va);
+      tmem_ld32(ts + 96, vb);
+      peak(va, 64);
+      tc_wait_ld_for(vb);
+      tmem_ld32(ts, va);
+      peak(vb, 96);
+      const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+      // Lazy rescale: the maximum used for the exponentials moves only when
+      // a score exceeds it by more than 2^8 (P and l stay far from fp32's
+      // limits, and the final division uses the same maximum).  S(it) is
+      // complete, so O += P(it - 1) V before it is too.
+      const bool need = mt > m + kRescaleThreshold;
+      if (__any_sync(0xffffffffu, need)) {
+        const float m_new = need ? mt : m;
+        const float f = need ? ex2(m - m_new) : 1.f;  // 0 from -inf
+        if (it > 0) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            float o[32];
+            tmem_ld32(to + 32 * c, o);
+            tc_wait_ld_for(o);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] *= f;
+            tmem_st32(to + 32 * c, o);
+          }
+        }
+        l *= f;
+        m = m_new;
+      }
+      const float neg_m = m == kNegInf ? 0.f : -m;
+      float ls[4] = {0.f, 0.f, 0.f, 0.f};
+      auto probs = [&](float (&v)[32], int c0) {
+        if (!plain) mask(v, c0);
+        uint32_t pk[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const float p0 = ex2(fmaf(v[2 * k], scale, neg_m));
+          const float p1 = ex2(fmaf(v[2 * k + 1], scale, neg_m));
+          ls[k & 3] += p0 + p1;
+          pk[k] = pack2<kBF16>(p0, p1);
+        }
+        // (Scores up to column c0 + 63 are in registers: P may overwrite
+        // columns up to c0 / 2 + 15.)
+        tmem_st16(ts + c0 / 2, pk);
+      };
+      tc_wait_ld_for(va);
+      tmem_ld32(ts + 32, vb);
+      probs(va, 0);
+      tc_wait_ld_for(vb);
+      tmem_ld32(ts + 64, va);
+      probs(vb, 32);
+      tc_wait_ld_for(va);
+      tmem_ld32(ts + 96, vb);
+      probs(va, 64);
+      tc_wait_ld_for(vb);
+      probs(vb, 96);
+      l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+      tc_wait_st();
+      tc_fence_before();
+      mbar_arrive(bar(kBarP + x));
+    }
+    // ---------------- epilogue
+    if (ok && nt > 0) ok = mbar_wait_or_abort(bar(kBarO + x), 0, p.err_flag, abort_word);
+    if (ok && w.tok[x] > 0) {
+      tc_fence_after();
+      const bool bad = *bad_word != 0;
+      const bool live = l > 0.f && !bad;
+      const float inv = live ? 1.f / l : 0.f;
+      const int64_t row = static_cast<int64_t>(w.q0 + i) * p.h_q + w.j * G + r % G;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        float o[32];
+        tmem_ld32(to + 32 * c, o);
+        tc_wait_ld_for(o);
+        if (!live) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = 0.f;
+        }
+        if (mine) store_row<kBF16>(p, row, w.split, 32 * c, o, inv);
+      }
+      if (mine && p.n_split > 1)
+        p.part_lse[row * p.n_split + w.split] =
+            bad ? DECATTN_POISON_LSE : l > 0.f ? m + lg2(l) : kNegInf;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kWarpTmem) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the splits of a row: out = sum_s w_s o_s / sum_s w_s, w_s = 2^(lse_s -
+// max).  One warp per (token, head); tokens outside every sequence stay as
+// they are, splits with nothing to see (lse = -inf) have no partial to read,
+// and a bad sequence (+inf) gives zeros.
+template <bool kBF16>
+__global__ void __launch_bounds__(256) gqa_prefill_combine_kernel(const PrefillParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x & 31;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (row >= static_cast<int64_t>(p.tokens) * p.h_q) return;
+  const int tok = static_cast<int>(row / p.h_q);
+  int lo = 0, hi = p.batch;  // the sequence whose rows hold tok
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (p.q_start[mid] <= tok) lo = mid; else hi = mid;
+  }
+  const int a = p.q_start[lo], e = p.q_start[lo + 1];
+  if (tok < a || tok >= e || a < 0 || e > p.tokens || e - a > p.max_q_len) return;
+  const float* lse = p.part_lse + row * p.n_split;
+  float mx = kNegInf;
+  for (int s = lane; s < p.n_split; s += 32) mx = fmaxf(mx, lse[s]);
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  uint2* dst = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + row * kHeadDim);
+  if (mx == kNegInf || mx == DECATTN_POISON_LSE) {
+    dst[lane] = make_uint2(0, 0);
+    return;
+  }
+  const float4* po = reinterpret_cast<const float4*>(p.part_o + row * p.n_split * kHeadDim);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float sum = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < p.n_split; ++s) {
+    const float wt = ex2(lse[s] - mx);
+    if (wt == 0.f) continue;
+    const float4 x = po[s * (kHeadDim / 4) + lane];
+    sum += wt;
+    acc.x = fmaf(wt, x.x, acc.x);
+    acc.y = fmaf(wt, x.y, acc.y);
+    acc.z = fmaf(wt, x.z, acc.z);
+    acc.w = fmaf(wt, x.w, acc.w);
+  }
+  const float inv = 1.f / sum;
+  dst[lane] = make_uint2(pack2<kBF16>(acc.x * inv, acc.y * inv),
+                         pack2<kBF16>(acc.z * inv, acc.w * inv));
+}
+
+template <bool kBF16>
+cudaError_t launch_t(const PrefillParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
+                     const CUtensorMap& tv, cudaStream_t stream) {
+  auto kern = gqa_prefill_kernel<kBF16>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       kSmemBytes);
+  if (e != cudaSuccess) return e;
+  const unsigned grid = static_cast<unsigned>(p.n_items) * p.n_split * p.h_kv;
+  kern<<<grid, kThreads, kSmemBytes, stream>>>(tq, tk, tv, p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || p.n_split == 1) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((static_cast<int64_t>(p.tokens) * p.h_q + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, gqa_prefill_combine_kernel<kBF16>, p);
+}
+
+}  // namespace
+
+cudaError_t launch_gqa_prefill(const PrefillParams& p, const CUtensorMap& tm_q,
+                               const CUtensorMap& tm_k, const CUtensorMap& tm_v, bool bf16,
+                               cudaStream_t stream) {
+  return bf16 ? launch_t<true>(p, tm_q, tm_k, tm_v, stream)
+              : launch_t<false>(p, tm_q, tm_k, tm_v, stream);
+}
+
+}  // namespace decattn

@@ -219,7 +219,7 @@ __device__ __forceinline__ uint32_t e4m3_round2(float x, float y, float& rx, flo
 // score scale, V's into the output).  S = Q K^T then runs as kind::f8f6f4 on
 // the landed K codes, with Q split into e4m3 terms, and O += P V on f16
 // operands (V converted by the softmax threads).
-template <bool kBF16, bool kF8>
+template <bool kBF16, bool kF8, bool kSinks>
 // (A minimum-blocks bound of 1 here made ptxas cap the registers at 168 and
 // spill; without it the kernel takes under 100.)
 __global__ void __launch_bounds__(kThreads)
@@ -242,8 +242,7 @@ __global__ void __launch_bounds__(kThreads)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = p.group;
 
-  const GqaSpan span = gqa_span(p, split, j, b);
-  const int w0 = span.w0, t_begin = span.t_begin, t_end = span.t_end;
+  const GqaSpan<kSinks> span = gqa_span<kSinks>(p, split, j, b);
   if (threadIdx.x == 0) {
     mbar_init(bar(kBarQ), kSoftmaxThreads);
     for (int s = 0; s < kRing; ++s) {
@@ -266,7 +265,7 @@ __global__ void __launch_bounds__(kThreads)
   }
   const int bad = __syncthreads_or(span.bad);
   const size_t row0 = static_cast<size_t>(b) * p.h_q + static_cast<size_t>(j) * G;
-  if (bad || t_end <= t_begin) {
+  if (bad || span.empty()) {
     gqa_write_empty(p, row0, G, split, bad);
     return;
   }
@@ -279,7 +278,7 @@ __global__ void __launch_bounds__(kThreads)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int n = (t_end - t_begin + kTile - 1) / kTile;
+  const int n = span.n_tiles;
 
   if (warp == kWarpProducerK || warp == kWarpProducerV) {
     // ---------------- TMA producers, one warp for K and one for V (two
@@ -294,7 +293,7 @@ __global__ void __launch_bounds__(kThreads)
     const int32_t* bt = p.block_table + static_cast<size_t>(b) * p.max_blocks_per_seq;
     const int x0 = j * kHeadDim;  // element (= byte, for an 8-bit cache) column of head j
     const int bs = p.block_size, lg = p.log2_block_size;
-    const int kb_end = ((t_end - 1) >> lg) + 1;  // one past the range's last block
+    const int kb_end = ((span.end() - 1) >> lg) + 1;  // one past the range's last block
     const int bar_full = is_v ? kBarFullV : kBarFullK, bar_empty = is_v ? kBarEmptyV : kBarEmptyK;
     const uint32_t ring = sbase + (is_v ? L::kOffV : L::kOffK);
     constexpr int kStageBytes = L::kStageBytes;
@@ -304,8 +303,8 @@ __global__ void __launch_bounds__(kThreads)
     auto request = [&](int it) -> bool {
       const int s = it % kRing;
       const uint32_t ph = static_cast<uint32_t>((it / kRing) & 1) ^ 1u;
-      const int t0 = t_begin + it * kTile;
-      const int nval = min(kTile, t_end - t0);
+      const GqaTile tl = span.tile(it);
+      const int t0 = tl.t0, nval = tl.nval;
       const int kb0 = t0 >> lg;
       const int nblk = bs >= kTile ? 1 : (nval + bs - 1) >> lg;
       if (kb0 + nblk > cache0 + 32) {
@@ -548,9 +547,8 @@ __global__ void __launch_bounds__(kThreads)
     const int c_own = 32 * hl + 16 * cg, c_oth = 32 * hl + 16 * (cg ^ 1);
     for (int it = 0; ok && it < n; ++it) {
       const int s = it % kStages;
-      const int t0 = t_begin + it * kTile;
-      const int nval = min(kTile, t_end - t0);
-      const int nskip = max(0, w0 - t0);
+      const GqaTile tl = span.tile(it);
+      const int nval = tl.nval, nskip = tl.skip;
       const bool ragged = nval < kTile || nskip > 0;
       if (!mbar_wait_or_abort(bar(kBarSFull + (it & 1)), (it >> 1) & 1, p.err_flag, abort_word)) {
         ok = false;
@@ -741,7 +739,7 @@ __global__ void __launch_bounds__(kThreads)
 template <bool kBF16, bool kF8>
 cudaError_t launch_t(const GqaParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
                      cudaStream_t stream) {
-  auto kern = gqa_wide_kernel<kBF16, kF8>;
+  auto kern = p.sinks > 0 ? gqa_wide_kernel<kBF16, kF8, true> : gqa_wide_kernel<kBF16, kF8, false>;
   constexpr int smem = WLayout<kBF16, kF8>::kSmemBytes;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;

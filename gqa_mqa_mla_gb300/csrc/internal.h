@@ -35,6 +35,7 @@ struct GqaParams {
   int n_split, tokens_per_split;  // tokens_per_split is a multiple of kTile
   float scale_log2;               // scale * log2(e)
   int window;                     // > 0: attend only to the last `window` tokens
+  int sinks;                      // > 0 (with a window): and to the first `sinks` tokens
   const float* k_scale;           // [h_kv], 8-bit caches only: K value = e4m3 * k_scale[j]
   const float* v_scale;           // [h_kv], 8-bit caches only
 };
@@ -83,6 +84,64 @@ struct AppendParams {
   int* err_flag;
   int batch, row_elems, head_elems;
   int block_size, log2_block_size, num_blocks, max_blocks_per_seq;
+};
+
+// A serving step's paged state from the requests' lengths.
+struct PlanParams {
+  const int32_t* cached_lens; // [B] tokens in the cache
+  const int32_t* new_lens;    // [B] tokens to add (> 0) or to take back (< 0)
+  int32_t* block_table;       // [B, max_blocks_per_seq]
+  int32_t* free_blocks;       // [num_blocks] stack of free block ids
+  const int32_t* free_count;  // [1]
+  int32_t* free_count_out;    // [1], may alias free_count
+  int32_t* seq_lens;          // [B], may alias cached_lens
+  int32_t* q_start;           // [B + 1]
+  int32_t* slots;             // [max_tokens]
+  int32_t* positions;         // [max_tokens]
+  int* err_flag;
+  int batch, max_tokens;
+  int block_size, log2_block_size, num_blocks, max_blocks_per_seq;
+};
+
+constexpr int kPlanMaxBatch = 8192;  // the scan's arrays stay in shared memory
+
+// Rotary positions on a step's queries and keys, and its cache write.
+struct RopeParams {
+  const void* q;              // rows of h_q * 128, q_stride elements apart
+  const void* k;
+  const void* v;
+  void* q_out;                // [tokens, h_q, 128]
+  void* k_cache;              // [num_slots, h_kv, 128]
+  void* v_cache;
+  const float* k_scale;       // [h_kv], 8-bit caches only
+  const float* v_scale;
+  const int32_t* positions;   // [n_axes, tokens]
+  const int32_t* slots;       // [tokens]; < 0: no cache row
+  int* err_flag;
+  int64_t q_stride, k_stride, v_stride;
+  int tokens, h_q, h_kv, num_slots;
+  decattn_rope rope;
+};
+
+// Attention of a chunk of new tokens per sequence.
+struct PrefillParams {
+  const int32_t* block_table; // [B, max_blocks_per_seq]
+  const int32_t* q_start;     // [B + 1]
+  const int32_t* seq_lens;    // [B]
+  void* out;                  // [tokens, h_q, 128]
+  float* part_o;              // [tokens, h_q, n_split, 128]   (n_split > 1)
+  float* part_lse;            // [tokens, h_q, n_split]        log2 domain
+  const float* k_scale;       // [h_kv], 8-bit caches only
+  const float* v_scale;
+  int* err_flag;
+  int batch, tokens, max_q_len, h_q, h_kv, group;
+  int block_size, log2_block_size, num_blocks, max_blocks_per_seq, max_seq_len;
+  int window, sinks;          // window 0: none; sinks only with a window
+  int tokens_per_tile;        // floor(128 / group)
+  int n_items;                // upper bound of the pieces of 2 tokens_per_tile tokens
+  int n_split;
+  int negate;                 // the scale is negative: scores change sign
+  float scale_log2;           // |scale| * log2(e), > 0
 };
 
 // Per-head batched GEMM Y[b, i, :] = X[b, i, :] W_i^T (MLA absorption).
@@ -143,6 +202,14 @@ cudaError_t launch_head_gemm(const HeadGemmParams& p, const CUtensorMap& tm_w,
 int head_gemm_smem_bytes(const HeadGemmParams& p);
 // e4m3: quantise with k_scale / v_scale (bf16 or fp16 input); else a copy.
 cudaError_t launch_append(const AppendParams& p, bool e4m3, bool bf16, cudaStream_t stream);
+// tm_q: 3-D [tokens, h_q, 128] 16-bit, boxes of 64 x group x tokens_per_tile;
+// tm_k, tm_v: 2-D [rows, h_kv * 128], boxes of 64 x min(block_size, 128); all
+// with 128-byte swizzle.
+cudaError_t launch_gqa_prefill(const PrefillParams& p, const CUtensorMap& tm_q,
+                               const CUtensorMap& tm_k, const CUtensorMap& tm_v, bool bf16,
+                               cudaStream_t stream);
+cudaError_t launch_paged_plan(const PlanParams& p, cudaStream_t stream);
+cudaError_t launch_rope_append(const RopeParams& p, bool e4m3, bool bf16, cudaStream_t stream);
 cudaError_t launch_mla_combine(const MlaCombineParams& p, bool bf16, cudaStream_t stream);
 
 // Bounded-wait self test (csrc/selftest.cu).

@@ -14,6 +14,7 @@ namespace decattn {
 constexpr int kFlagBadBlock = 1;
 constexpr int kFlagBadSeqLen = 2;
 constexpr int kFlagTimeout = 4;
+constexpr int kFlagNoRoom = 8;
 
 // A pipeline wait gives up after this long (ns of %globaltimer).
 constexpr uint64_t kWaitTimeoutNs = 2000000000ull;
@@ -278,6 +279,19 @@ DECATTN_DEV uint64_t policy_evict_last() {
 
 DECATTN_DEV void named_bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// ------------------------------------------------------------------ registers
+
+// Move a warpgroup's register limit (all four warps).  The limits of a block's
+// warpgroups together must not exceed what the block was launched with.
+template <int kRegs>
+DECATTN_DEV void reg_grow() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+DECATTN_DEV void reg_shrink() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
 // ------------------------------------------------------------------ math
@@ -549,6 +563,23 @@ DECATTN_DEV void tc_commit(uint32_t bar) {
 
 DECATTN_DEV void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 DECATTN_DEV void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Wait for every tcgen05.ld of this thread; v (loaded by one of them) may be
+// used only behind this statement, even where other arithmetic stands between
+// the load and the wait.
+DECATTN_DEV void tc_wait_ld_for(float (&v)[32]) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]),
+                 "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]),
+                 "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]),
+                 "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]),
+                 "+r"(r[31])
+               :
+               : "memory");
+}
 
 // 32 lanes x 32 columns of 32-bit from TMEM: thread t of the warp gets lane
 // (base lane + t), columns [col, col + 32).

@@ -70,6 +70,7 @@ typedef enum { DECATTN_FP16 = 0, DECATTN_BF16 = 1 } decattn_dtype;
 #define DECATTN_FLAG_BAD_BLOCK 1   /* a block id outside [0, num_blocks)          */
 #define DECATTN_FLAG_BAD_SEQ_LEN 2 /* seq_lens[b] < 0 or > max_seq_len            */
 #define DECATTN_FLAG_TIMEOUT 4     /* a pipeline wait gave up (internal error)    */
+#define DECATTN_FLAG_NO_ROOM 8     /* paged_plan: too few free blocks, token rows */
 
 /* Largest split count accepted (num_splits) and chosen by the planner. */
 #define DECATTN_MAX_SPLITS 256
@@ -208,6 +209,32 @@ int gqa_decode_fp8kv_window(const void* q, const void* k_cache, const void* v_ca
                             const decattn_launch* launch);
 
 /*
+ * gqa_decode_sinks, gqa_decode_fp8kv_sinks -- the windowed decode with the
+ * sequence's first `sinks` tokens kept visible beside its last `window`: a
+ * query of a sequence of length L attends to positions
+ *     [0, min(L, sinks))  and  [max(0, L - window), L),
+ * each position once; sinks + window >= L is full attention.  (Models run
+ * with a window put much of their attention on the first tokens; without
+ * them the output degrades once the window has passed.)
+ *   window       >= 1, sinks >= 0 (else DECATTN_ERR_INVALID_ARG); sinks = 0
+ *                is gqa_decode_window
+ * Every other argument, layout, status and the workspace rule as
+ * gqa_decode_window (resp. gqa_decode_fp8kv_window).  Blocks that hold
+ * neither a kept first token nor a token of the window are never read and
+ * their block_table entries never checked.  The planner counts the window's
+ * token range (as for gqa_decode_window) plus sinks rounded up to 64.
+ */
+int gqa_decode_sinks(const void* q, const void* k_cache, const void* v_cache,
+                     const int32_t* block_table, const int32_t* seq_lens, void* out, int h_q,
+                     int h_kv, int d_head, float scale, int window, int sinks,
+                     const decattn_launch* launch);
+int gqa_decode_fp8kv_sinks(const void* q, const void* k_cache, const void* v_cache,
+                           const float* k_scale, const float* v_scale,
+                           const int32_t* block_table, const int32_t* seq_lens, void* out,
+                           int h_q, int h_kv, int d_head, float scale, int window, int sinks,
+                           const decattn_launch* launch);
+
+/*
  * mla_decode -- absorbed multi-head latent attention decode ("MQA, GQA, and
  * MLA", section 5; "Why GQA's KV Cache Savings Don't Fully Reduce TPOT",
  * "What Makes MLA Different").  128 heads, d_c = 512, d_rope = 64.
@@ -271,6 +298,151 @@ int mla_kv_append(const void* latent_new, const int32_t* positions, const int32_
                   void* latent_cache, const decattn_launch* launch);
 
 /*
+ * paged_plan -- a serving step's paged state, built on the GPU from the
+ * requests' lengths: block tables, slot map, positions, row offsets.
+ *   cached_lens  [batch] int32: tokens each request has in the cache
+ *   new_lens     [batch] int32: tokens it gains in this step (> 0), none (0),
+ *                or gives back (< 0: rejected drafts; -cached_lens[b] ends it)
+ *   block_table  [batch, max_blocks_per_seq] int32 (updated): entries of the
+ *                blocks that a request gains; no other entry is written
+ *   free_blocks  [num_blocks] int32 (updated): a stack of free block ids, its
+ *                first free_count[0] entries valid
+ *   free_count, free_count_out  [1] int32: the stack's height before / after
+ *   seq_lens     [batch] int32 (written): cached_lens + new_lens
+ *   q_start      [batch + 1] int32 (written): first row of each request's new
+ *                tokens in the step's packed rows; q_start[batch] is their number
+ *   slots        [max_tokens] int32 (written): cache slot (block id times
+ *                block_size plus offset) of each packed row; -1 past the last
+ *   positions    [max_tokens] int32 (written): the row's position in its
+ *                sequence; -1 past the last
+ * Blocks given back are pushed in request order, each request's in ascending
+ * order; then the k-th block needed (same order) takes the k-th entry from the
+ * top.  free_count_out may be free_count and seq_lens may be cached_lens; no
+ * other arrays may overlap.  With separate ones the call can be repeated on
+ * the same inputs with the same result.
+ * A request whose lengths are negative or do not fit its table row sets
+ * DECATTN_FLAG_BAD_SEQ_LEN and stays as it is (seq_lens: its cached length, 0
+ * if that itself is bad).  If the free blocks or max_tokens do not suffice,
+ * DECATTN_FLAG_NO_ROOM is set, tokens are still given back, and no request
+ * grows (no row is used).  A free count outside [0, num_blocks], or more
+ * blocks given back than the stack has place for, sets
+ * DECATTN_FLAG_BAD_BLOCK and nothing moves; a block id outside
+ * [0, num_blocks) sets it too, and the rows that would lie in that block get
+ * slot -1.
+ * Of the launch block batch (<= 8192), num_blocks, block_size (8..256, power
+ * of two), max_blocks_per_seq, err_flag and stream are used.
+ */
+int paged_plan(const int32_t* cached_lens, const int32_t* new_lens, int32_t* block_table,
+               int32_t* free_blocks, const int32_t* free_count, int32_t* free_count_out,
+               int32_t* seq_lens, int32_t* q_start, int32_t* slots, int32_t* positions,
+               int max_tokens, const decattn_launch* launch);
+
+/* Rotary positions of a model: how the first rot_dim dimensions of a head are
+ * turned, pair by pair (rot_dim a multiple of 16, at most 128; filled on the
+ * host, by decattn_rope_fill or by hand, and passed by address; the call
+ * copies it).
+ *   interleaved  0: pair i is dimensions (i, i + rot_dim / 2);
+ *                1: pair i is dimensions (2 i, 2 i + 1)
+ *   n_axes       position axes (1..8); pair i follows axis[i]
+ *   turns[i]     turns per position of pair i in units of 2^-64, modulo 2^64 */
+typedef struct {
+  int rot_dim;
+  int n_axes;
+  int interleaved;
+  uint8_t axis[64];
+  uint64_t turns[64];
+} decattn_rope;
+
+/* Fill a decattn_rope from inv_freq[rot_dim / 2] (angle of pair i =
+ * position * inv_freq[i], radians, finite) and the number of consecutive
+ * pairs that follow each axis, sections[n_axes] (their sum rot_dim / 2; NULL
+ * with n_axes = 1).  Host arithmetic, no CUDA call; returns a status. */
+int decattn_rope_fill(decattn_rope* rope, const double* inv_freq, int rot_dim,
+                      const int* sections, int n_axes, int interleaved);
+
+/*
+ * gqa_rope_append, gqa_rope_append_fp8kv -- a step's rotation and cache write
+ * for any number of packed tokens: q and k are turned by their positions
+ * (time, height and width axes for images and video, one axis for text), q
+ * goes to q_out, k and v go to the cache slots of the slot map.
+ *   q            [tokens, h_q, 128], k_new, v_new [tokens, h_kv, 128] in
+ *                launch->dtype; the 128 values of a head and a token's heads
+ *                are contiguous, tokens are q_stride, k_stride, v_stride
+ *                elements apart (multiples of 8, at least the row), so the
+ *                three may be parts of one projection's output
+ *   positions    [n_axes, tokens] int32, any value
+ *   slots        [tokens] int32 (paged_plan's); a negative slot turns q only
+ *   q_out        [tokens, h_q, 128], contiguous; may be q itself when
+ *                q_stride is h_q * 128; no other overlap is allowed
+ *   k_cache, v_cache, k_scale, v_scale  as gqa_kv_append (_fp8kv)
+ * Pair (x, y) becomes (x cos a - y sin a, x sin a + y cos a), a = position of
+ * the pair's axis times its frequency, reduced exactly at any position;
+ * products in fp32, each result rounded once (k of an 8-bit cache: divided by
+ * its scale in fp32 and rounded once to e4m3, saturating at 448).  Dimensions
+ * past rot_dim and v are only moved (or quantised).  A slot past the cache
+ * sets DECATTN_FLAG_BAD_BLOCK and that token's k and v are skipped.  Tokens
+ * must name distinct slots.  tokens = 0 does nothing.
+ * Of the launch block num_blocks, block_size (8..256, power of two), dtype,
+ * err_flag and stream are used.
+ */
+int gqa_rope_append(const void* q, const void* k_new, const void* v_new, int64_t q_stride,
+                    int64_t k_stride, int64_t v_stride, const int32_t* positions,
+                    const decattn_rope* rope, const int32_t* slots, void* q_out, void* k_cache,
+                    void* v_cache, int tokens, int h_q, int h_kv, int d_head,
+                    const decattn_launch* launch);
+int gqa_rope_append_fp8kv(const void* q, const void* k_new, const void* v_new, int64_t q_stride,
+                          int64_t k_stride, int64_t v_stride, const float* k_scale,
+                          const float* v_scale, const int32_t* positions,
+                          const decattn_rope* rope, const int32_t* slots, void* q_out,
+                          void* k_cache, void* v_cache, int tokens, int h_q, int h_kv,
+                          int d_head, const decattn_launch* launch);
+
+/*
+ * gqa_prefill, gqa_prefill_fp8kv -- attention of a chunk of new tokens per
+ * sequence over the paged cache (whole prompts, chunks of prompts behind a
+ * cached prefix, drafted tokens to check, single tokens, and any mix): the
+ * chunk's own keys and values are already in the cache.
+ *   q            [tokens, h_q, 128] packed rows
+ *   q_start      [batch + 1] int32: sequence b's rows are q_start[b] ..
+ *                q_start[b + 1] - 1 (paged_plan's)
+ *   seq_lens     [batch] int32: tokens in the cache, the chunk included
+ *   out          [tokens, h_q, 128]; rows outside every sequence (before
+ *                q_start[0], from q_start[batch] on) are left as they were
+ *   max_q_len    host upper bound of the chunk lengths (>= 1)
+ *   window       0: none; > 0: each row sees only its last `window` positions
+ *   sinks        with a window: and the sequence's first `sinks` positions
+ * Row i of a chunk of n tokens is position p = seq_lens[b] - n + i and sees
+ * positions t <= p with (window = 0 or t > p - window or t < sinks); rows
+ * with p < 0 (a chunk longer than its sequence) see nothing and are zeros.
+ * Block sizes 8..256, h_q / h_kv <= 64, d_head 128; scores, softmax and sums
+ * in fp32, the probabilities rounded to the 16-bit type for the second
+ * product.  Values that only some rows of a chunk see must be finite: a
+ * NaN or infinity in v at position t may reach the rows before t that share
+ * its tile (slots past seq_lens and slots that no row of the tile's sequence
+ * may see can hold anything).
+ * A seq_len outside [0, max_seq_len], a chunk longer than max_q_len or a bad
+ * block id (flags as for gqa_decode) gives zero rows for that sequence's
+ * affected rows; row offsets that decrease or leave [0, tokens] set
+ * DECATTN_FLAG_BAD_SEQ_LEN and that sequence's rows are not written.
+ * num_splits: parts that each sequence's cache is cut into (0 = automatic);
+ * workspace sized by gqa_prefill_workspace_size.  tokens = 0 does nothing.
+ */
+int gqa_prefill(const void* q, const void* k_cache, const void* v_cache,
+                const int32_t* block_table, const int32_t* q_start, const int32_t* seq_lens,
+                void* out, int tokens, int max_q_len, int h_q, int h_kv, int d_head, float scale,
+                int window, int sinks, const decattn_launch* launch);
+int gqa_prefill_fp8kv(const void* q, const void* k_cache, const void* v_cache,
+                      const float* k_scale, const float* v_scale, const int32_t* block_table,
+                      const int32_t* q_start, const int32_t* seq_lens, void* out, int tokens,
+                      int max_q_len, int h_q, int h_kv, int d_head, float scale, int window,
+                      int sinks, const decattn_launch* launch);
+/* Splits that num_splits = 0 picks (num_sms <= 0 queries the device; >= 1 or
+ * a negative status), and the workspace bytes for a split count (0 for one). */
+int gqa_prefill_plan_splits(int batch, int tokens, int max_q_len, int h_q, int h_kv, int d_head,
+                            int max_seq_len, int window, int sinks, int num_sms);
+size_t gqa_prefill_workspace_size(int tokens, int h_q, int d_head, int num_splits);
+
+/*
  * mla_absorb_q, mla_unabsorb_out -- the two GEMMs either side of mla_decode
  * ("MQA, GQA, and MLA", section 5: q_i . k_i = x (W_q^(i) W_uk^(i)^T) c^T, so
  * the query is multiplied by W_uk^(i)^T once and the scores are taken
@@ -308,6 +480,10 @@ int mla_decode_plan_splits(int batch, int max_seq_len, int num_sms);
  * gqa_decode_fp8kv_window; block_size a power of two. */
 int gqa_decode_window_plan_splits(int batch, int h_q, int h_kv, int d_head, int max_seq_len,
                                   int window, int block_size, int kv_bytes, int num_sms);
+/* The same with `sinks` (>= 0) first tokens kept. */
+int gqa_decode_sinks_plan_splits(int batch, int h_q, int h_kv, int d_head, int max_seq_len,
+                                 int window, int sinks, int block_size, int kv_bytes,
+                                 int num_sms);
 
 /* Helpers of the interface with no defining passage on the pages (workspace
  * sizes, status text, version): conveniences of this C ABI.
