@@ -75,11 +75,11 @@ struct Item {
   int n, len;       // chunk length, cache length
   int q0;           // first packed row of the sequence
   int i0;           // first token of the chunk in tile A
-  int tok[2];       // tokens in tile A, B
+  int tok_a, tok_b; // tokens in tile A, B
   int lo, s_end, base, sink_tiles;
   int hi;           // one past the last position any row sees
   int tile0;        // first tile of this split
-  int n_tiles[2];   // tiles that tile A, B need, from tile0 on
+  int n_a, n_b;     // tiles that tile A, B need, from tile0 on
   int bad;
 };
 
@@ -152,8 +152,8 @@ __device__ __forceinline__ bool find_item(const PrefillParams& p, int index, Ite
   w.q0 = p.q_start[w.b];
   w.n = p.q_start[w.b + 1] - w.q0;
   w.i0 = found[1] * tpi;
-  w.tok[0] = min(p.tokens_per_tile, w.n - w.i0);
-  w.tok[1] = max(0, min(p.tokens_per_tile, w.n - w.i0 - p.tokens_per_tile));
+  w.tok_a = min(p.tokens_per_tile, w.n - w.i0);
+  w.tok_b = max(0, min(p.tokens_per_tile, w.n - w.i0 - p.tokens_per_tile));
   w.len = p.seq_lens[w.b];
   w.bad = w.len < 0 || w.len > p.max_seq_len;
   if (w.bad) {
@@ -165,7 +165,7 @@ __device__ __forceinline__ bool find_item(const PrefillParams& p, int index, Ite
   // first row), then those from the window's block boundary on.  Kept tokens
   // that reach the window join it.
   const int p_first = w.len - w.n + w.i0;
-  const int p_last = p_first + w.tok[0] + w.tok[1] - 1;
+  const int p_last = p_first + w.tok_a + w.tok_b - 1;
   w.hi = max(0, min(w.len, p_last + 1));
   w.lo = p.window > 0 ? max(0, p_first + 1 - p.window) : 0;
   if (p.sinks >= w.lo) w.lo = 0;
@@ -174,12 +174,19 @@ __device__ __forceinline__ bool find_item(const PrefillParams& p, int index, Ite
   w.base = w.lo & ~(min(p.block_size, kKv) - 1);
   w.sink_tiles = (w.s_end + kKv - 1) / kKv;
   const int total = w.bad ? 0 : tiles_to(w, w.hi - 1);
-  const int total_a = w.bad ? 0 : max(0, min(total, tiles_to(w, p_first + w.tok[0] - 1)));
+  const int total_a = w.bad ? 0 : max(0, min(total, tiles_to(w, p_first + w.tok_a - 1)));
   const int per = (total + p.n_split - 1) / p.n_split;
   w.tile0 = min(total, w.split * per);
-  w.n_tiles[0] = max(0, min(per, total_a - w.tile0));
-  w.n_tiles[1] = w.tok[1] > 0 ? min(per, total - w.tile0) : 0;
+  w.n_a = max(0, min(per, total_a - w.tile0));
+  w.n_b = w.tok_b > 0 ? min(per, total - w.tile0) : 0;
   return true;
+}
+
+// The lowest n bits set (none for n <= 0, all for n >= 32).
+__device__ __forceinline__ uint32_t below(int n) {
+  uint32_t r;
+  asm("shl.b32 %0, %1, %2;" : "=r"(r) : "r"(0xffffffffu), "r"(max(n, 0)));  // clamps at 32
+  return ~r;
 }
 
 template <bool kBF16>
@@ -224,12 +231,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int rest = static_cast<int>(blockIdx.x) / p.h_kv;
   w.split = rest % p.n_split;
   if (!find_item(p, p.n_items - 1 - rest / p.n_split, w)) return;
-  const int n = max(w.n_tiles[0], w.n_tiles[1]);
+  const int n = max(w.n_a, w.n_b);
 
   const int G = p.group;
   if (n == 0) {
     // Nothing to see (or bad lengths): zero rows, or an empty partial.
-    const int rows = (w.tok[0] + w.tok[1]) * G;
+    const int rows = (w.tok_a + w.tok_b) * G;
     for (int e = threadIdx.x; e < rows * 16; e += kThreads) {
       const int r = e >> 4;
       const int64_t row = static_cast<int64_t>(w.q0 + w.i0 + r / G) * p.h_q + w.j * G + r % G;
@@ -267,10 +274,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  // Ring slot and phase parity of the e-th copy (e = 2 it: K, 2 it + 1: V).
-  auto slot_of = [](int e) { return e % kRing; };
-  auto phase_of = [](int e) { return static_cast<uint32_t>((e / kRing) & 1); };
-
   if (warp >= 8) {
     if (warp == kWarpLoad) {
       // ---------------- TMA producer
@@ -279,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(&tm_q);
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
-        const int tiles = w.tok[1] > 0 ? 2 : 1;
+        const int tiles = w.tok_b > 0 ? 2 : 1;
         const uint32_t bytes = static_cast<uint32_t>(tiles * 2 * p.tokens_per_tile * G * 128);
         mbar_arrive_expect_tx(bar(kBarQ), bytes);
         for (int x = 0; x < tiles; ++x)
@@ -292,7 +295,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int x0 = w.j * kHeadDim;
       const int kb_end = ((w.hi - 1) >> lg) + 1;
       int cache0 = -(1 << 30), my_id = 0;
-      int issued = 0;
+      // Copies go round the ring: slot and phase parity of the next one, and
+      // the number made.
+      int slot = 0, made = 0;
+      uint32_t phase = 0;
       bool ok = true;
       for (int it = 0; ok && it < n; ++it) {
         const Tile t = tile_of(w, it);
@@ -312,31 +318,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const int row = id * bs + (bs >= kKv ? (t.t0 & (bs - 1)) : 0);
         const uint32_t bytes = static_cast<uint32_t>(bs >= kKv ? kTileBytes : nblk * bs * 256);
+#pragma unroll 1
         for (int kv = 0; kv < 2; ++kv) {
-          const int e = 2 * it + kv, s = slot_of(e);
           bool got = true;
           if (lane == 0) {
-            got = mbar_wait_or_abort(bar(kBarEmpty + s), phase_of(e) ^ 1u, p.err_flag, abort_word);
-            if (got) mbar_arrive_expect_tx(bar(kBarFull + s), bytes);
+            got = mbar_wait_or_abort(bar(kBarEmpty + slot), phase ^ 1u, p.err_flag, abort_word);
+            if (got) mbar_arrive_expect_tx(bar(kBarFull + slot), bytes);
           }
           if (__shfl_sync(0xffffffffu, got ? 1 : 0, 0) == 0) {
             ok = false;
             break;
           }
-          issued = e + 1;
           if (lane < nblk) {
             const CUtensorMap* tm = kv ? &tm_v : &tm_k;
-            const uint32_t dst = sbase + kOffRing + s * kTileBytes + static_cast<uint32_t>(lane * bs * 128);
-            tma_load_2d_hint(dst, tm, x0, row, bar(kBarFull + s), keep);
-            tma_load_2d_hint(dst + kHalf, tm, x0 + 64, row, bar(kBarFull + s), keep);
+            const uint32_t dst =
+                sbase + kOffRing + slot * kTileBytes + static_cast<uint32_t>(lane * bs * 128);
+            tma_load_2d_hint(dst, tm, x0, row, bar(kBarFull + slot), keep);
+            tma_load_2d_hint(dst + kHalf, tm, x0 + 64, row, bar(kBarFull + slot), keep);
+          }
+          ++made;
+          if (++slot == kRing) {
+            slot = 0;
+            phase ^= 1u;
           }
         }
       }
-      // Never leave the CTA with copies in flight.
+      // Never leave the CTA with copies in flight: the last round's are waited
+      // for, each slot's by its own phase.
       if (lane == 0) {
         mbar_wait(bar(kBarQ), 0, p.err_flag);
-        for (int e = max(0, issued - kRing); e < issued; ++e)
-          if (!mbar_wait(bar(kBarFull + slot_of(e)), phase_of(e), p.err_flag)) break;
+        for (int e = max(0, made - kRing); e < made; ++e)
+          if (!mbar_wait(bar(kBarFull + e % kRing), (e / kRing) & 1, p.err_flag)) break;
       }
       __syncwarp();
     } else if (warp == kWarpMma) {
@@ -347,60 +359,77 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t dv = smem_desc_sw128(sbase + kOffRing, kHalf, 1024);
       constexpr uint32_t idesc_s = idesc_f16(kBF16, kM, kKv, false, false);
       constexpr uint32_t idesc_o = idesc_f16(kBF16, kM, kHeadDim, false, true);
+      // All lanes probe; lane 0 waits where that does not succeed at once.
       auto wait = [&](int bi, uint32_t parity) -> bool {
-        bool g = true;
-        if (lane == 0) g = mbar_wait_or_abort(bar(bi), parity, p.err_flag, abort_word);
-        g = __shfl_sync(0xffffffffu, g ? 1 : 0, 0) != 0;
+        bool g = mbar_try_wait(bar(bi), parity);
+        if (!__all_sync(0xffffffffu, g)) {
+          if (lane == 0) g = mbar_wait_or_abort(bar(bi), parity, p.err_flag, abort_word);
+          g = __shfl_sync(0xffffffffu, g ? 1 : 0, 0) != 0;
+        }
         tc_fence_after();
         return g;
       };
       // S_X = Q_X K^T: eight k-steps of 16 dims, four per 64-column half.
-      auto issue_s = [&](int x, int s) {
+      // `last`: no other tile reads this K slot after this one.
+      auto issue_s = [&](int x, int s, bool last) {
         const uint64_t a = dq + static_cast<uint64_t>((x * kTileBytes) >> 4);
         const uint64_t b = dk + static_cast<uint64_t>((s * kTileBytes) >> 4);
-        const uint32_t done = bar(kBarS + x);
+        const uint32_t done = bar(kBarS + x), empty = bar(kBarEmpty + s);
+        const uint32_t d = tmem + kTmemS + kKv * x;
         if (elect_one()) {
-  #pragma unroll
+#pragma unroll
           for (int ks = 0; ks < 8; ++ks) {
             const uint64_t off = static_cast<uint64_t>(((ks >> 2) * kHalf + (ks & 3) * 32) >> 4);
-            tc_mma_f16(tmem + kTmemS + kKv * x, a + off, b + off, idesc_s, ks > 0 ? 1u : 0u);
+            tc_mma_f16(d, a + off, b + off, idesc_s, ks > 0 ? 1u : 0u);
           }
           tc_commit(done);
+          if (last) tc_commit(empty);
         }
         __syncwarp();
       };
-      // O_X += P_X V: eight k-steps of 16 tokens, P from TMEM.
-      auto issue_pv = [&](int x, int s, bool first) {
+      // O_X += P_X V: eight k-steps of 16 tokens, P from TMEM.  `done`: O_X is
+      // complete behind this one; `last` as above, for the V slot.
+      auto issue_pv = [&](int x, int s, bool first, bool done, bool last) {
         const uint64_t b = dv + static_cast<uint64_t>((s * kTileBytes) >> 4);
         const uint32_t acc0 = first ? 0u : 1u;
+        const uint32_t d = tmem + kTmemO + kHeadDim * x, a = tmem + kTmemS + kKv * x;
+        const uint32_t full = bar(kBarO + x), empty = bar(kBarEmpty + s);
         if (elect_one()) {
-  #pragma unroll
+#pragma unroll
           for (int ks = 0; ks < 8; ++ks)
-            tc_mma_f16_ts(tmem + kTmemO + kHeadDim * x, tmem + kTmemS + kKv * x + ks * 8,
-                          b + static_cast<uint64_t>((ks * 2048) >> 4), idesc_o, ks > 0 ? 1u : acc0);
+            tc_mma_f16_ts(d, a + ks * 8, b + static_cast<uint64_t>((ks * 2048) >> 4), idesc_o,
+                          ks > 0 ? 1u : acc0);
+          if (done) tc_commit(full);
+          if (last) tc_commit(empty);
         }
         __syncwarp();
       };
-      auto commit = [&](int bi) {
-        const uint32_t at = bar(bi);
-        if (elect_one()) tc_commit(at);
-        __syncwarp();
+      // Tile B needs at least the tiles that A needs, or there is no tile B.
+      int slot = 0;
+      uint32_t phase = 0;
+      auto next = [&]() {
+        if (++slot == kRing) {
+          slot = 0;
+          phase ^= 1u;
+        }
       };
-      bool ok = wait(kBarQ, 0) && wait(kBarFull + slot_of(0), phase_of(0));
+      bool ok = wait(kBarQ, 0) && wait(kBarFull + slot, phase);
       if (ok) {
-        for (int x = 0; x < 2; ++x)
-          if (w.n_tiles[x] > 0) issue_s(x, slot_of(0));
-        commit(kBarEmpty + slot_of(0));
+        if (w.n_a > 0) issue_s(0, slot, w.n_b == 0);
+        if (w.n_b > 0) issue_s(1, slot, true);
       }
       for (int it = 0; ok && it < n; ++it) {
-        const int ev = 2 * it + 1, ek = 2 * it + 2;
+        next();
+        const int sv = slot;
+        ok = wait(kBarFull + sv, phase);
+        if (!ok) break;
         const Tile t = tile_of(w, it);
-        ok = wait(kBarFull + slot_of(ev), phase_of(ev));
-        if (ok && (t.nval < kKv || t.skip > 0)) {
+        if (t.nval < kKv || t.skip > 0) {
           // V rows outside [skip, nval) become zeros (P is 0 there, but the
           // slots may hold NaN), while the softmax works on this tile.  (All
           // 128 bytes of a row: the swizzle does not matter.)
-          uint8_t* v = smem + kOffRing + slot_of(ev) * kTileBytes;
+          uint8_t* v = smem + kOffRing + sv * kTileBytes;
+#pragma unroll 1
           for (int i = lane; i < (t.skip + kKv - t.nval) * 16; i += 32) {
             const int k = i >> 4, c = i & 15;
             const int r = k < t.skip ? k : t.nval + (k - t.skip);
@@ -410,24 +439,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_proxy_async_smem();
           __syncwarp();
         }
-        bool have_k = false;
-        for (int x = 0; ok && x < 2; ++x) {
-          if (it >= w.n_tiles[x]) continue;
-          ok = wait(kBarP + x, it & 1);
+        // The next K tile is waited for first, so that O += P V and the next S
+        // follow each other without a pause.
+        if (it + 1 < n) {
+          next();
+          ok = wait(kBarFull + slot, phase);
           if (!ok) break;
-          issue_pv(x, slot_of(ev), it == 0);
-          if (it + 1 < w.n_tiles[x]) {
-            if (!have_k) ok = wait(kBarFull + slot_of(ek), phase_of(ek));
-            have_k = true;
-            if (!ok) break;
-            issue_s(x, slot_of(ek));
-          } else {
-            commit(kBarO + x);
-          }
         }
-        if (ok) {
-          commit(kBarEmpty + slot_of(ev));
-          if (it + 1 < n) commit(kBarEmpty + slot_of(ek));
+        if (it < w.n_a) {
+          ok = wait(kBarP, it & 1);
+          if (!ok) break;
+          issue_pv(0, sv, it == 0, it + 1 == w.n_a, it >= w.n_b);
+          if (it + 1 < w.n_a) issue_s(0, slot, it + 1 >= w.n_b);
+        }
+        if (it < w.n_b) {
+          ok = wait(kBarP + 1, it & 1);
+          if (!ok) break;
+          issue_pv(1, sv, it == 0, it + 1 == w.n_b, true);
+          if (it + 1 < w.n_b) issue_s(1, slot, true);
         }
       }
       // Wait (bounded) until every MMA this warp issued has completed.
@@ -441,62 +470,68 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------- softmax: thread = row r of tile x
     const int x = warp >> 2;
     const int r = 32 * (warp & 3) + lane;
-    const int nt = w.n_tiles[x];
+    const int nt = x ? w.n_b : w.n_a, tok = x ? w.tok_b : w.tok_a;
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t ts = tmem + lanes + kTmemS + kKv * x;
     const uint32_t to = tmem + lanes + kTmemO + kHeadDim * x;
-    const int i = w.i0 + x * p.tokens_per_tile + min(r / G, max(0, w.tok[x] - 1));
-    const bool mine = r < w.tok[x] * G;
+    const int i0 = w.i0 + x * p.tokens_per_tile;
+    const int i = i0 + min(r / G, max(0, tok - 1));
     const int pos = w.len - w.n + i;
     // Positions of the tile's first and last rows: tiles at or before the
     // first (and inside the last one's window) need no mask.
-    const int pos0 = w.len - w.n + w.i0 + x * p.tokens_per_tile;
-    const int pos1 = pos0 + w.tok[x] - 1;
-    const float scale = p.scale_log2;
+    const int pos0 = w.len - w.n + i0, pos1 = pos0 + tok - 1;
+    const float scale = p.scale_log2, sign = p.negate ? -1.f : 1.f;
     float m = kNegInf, l = 0.f;
     bool ok = true;
     for (int it = 0; it < nt; ++it) {
       const Tile t = tile_of(w, it);
+      const bool plain = !p.negate && t.skip == 0 && t.nval == kKv && t.t0 + kKv - 1 <= pos0 &&
+                         (p.window <= 0 || t.t0 > pos1 - p.window);
+      // Seen columns: [skip, hi), of them those from lo on or below sink (at
+      // or before the row's position; in its window or kept first tokens).
+      const int c_hi = min(t.nval, pos + 1 - t.t0);
+      const int c_lo = p.window > 0 ? pos + 1 - p.window - t.t0 : 0;
+      const int c_sink = p.sinks - t.t0;
+      auto mask = [&](float (&v)[32], int c0) {
+        const uint32_t seen = (below(c_hi - c0) & ~below(t.skip - c0)) &
+                              (~below(c_lo - c0) | below(c_sink - c0));
+#pragma unroll
+        for (int k = 0; k < 32; ++k) v[k] = (seen >> k) & 1u ? v[k] * sign : kNegInf;
+      };
       if (!mbar_wait_or_abort(bar(kBarS + x), it & 1, p.err_flag, abort_word)) {
         ok = false;
         break;
       }
       tc_fence_after();
-      const bool plain = !p.negate && t.skip == 0 && t.nval == kKv && t.t0 + kKv - 1 <= pos0 &&
-                         (p.window <= 0 || t.t0 > pos1 - p.window);
-      // Seen: [skip, nval), at or before the row's position, inside its
-      // window or among the kept first tokens.
-      const int c_hi = min(t.nval, pos + 1 - t.t0);
-      const int c_lo = p.window > 0 ? pos + 1 - p.window - t.t0 : 0;
-      const int c_sink = p.sinks - t.t0;
-      auto mask = [&](float (&v)[32], int c0) {
+      // The row's 128 scores, in registers from here on.
+      float va[32], vb[32], vc[32], vd[32];
+      tmem_ld32(ts, va);
+      tmem_ld32(ts + 32, vb);
+      tmem_ld32(ts + 64, vc);
+      tmem_ld32(ts + 96, vd);
+      tc_wait_ld_for(va);
+      tc_wait_ld_for(vb);
+      tc_wait_ld_for(vc);
+      tc_wait_ld_for(vd);
+      if (!plain) {
+        mask(va, 0);
+        mask(vb, 32);
+        mask(vc, 64);
+        mask(vd, 96);
+      }
+      float mx0 = kNegInf, mx1 = kNegInf;
+      auto peak = [&](float (&v)[32]) {
 #pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          const int c = c0 + k;
-          const bool seen = c < c_hi && c >= t.skip && (c >= c_lo || c < c_sink);
-          v[k] = seen ? (p.negate ? -v[k] : v[k]) : kNegInf;
+        for (int k = 0; k < 32; k += 4) {
+          mx0 = fmaxf(mx0, fmaxf(v[k], v[k + 1]));
+          mx1 = fmaxf(mx1, fmaxf(v[k + 2], v[k + 3]));
         }
       };
-      float va[32], vb[32], mx[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
-      auto peak = [&](float (&v)[32], int c0) {
-        if (!plain) mask(v, c0);
-#pragma unroll
-        for (int k = 0; k < 32; ++k) mx[k & 3] = fmaxf(mx[k & 3], v[k]);
-      };
-      tmem_ld32(ts, va);
-      tc_wait_ld_for(va);
-      tmem_ld32(ts + 32, vb);
-      peak(va, 0);
-      tc_wait_ld_for(vb);
-      tmem_ld32(ts + 64, va);
-      peak(vb, 32);
-      tc_wait_ld_for(va);
-      tmem_ld32(ts + 96, vb);
-      peak(va, 64);
-      tc_wait_ld_for(vb);
-      tmem_ld32(ts, va);
-      peak(vb, 96);
-      const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+      peak(va);
+      peak(vb);
+      peak(vc);
+      peak(vd);
+      const float mt = fmaxf(mx0, mx1) * scale;
       // Lazy rescale: the maximum used for the exponentials moves only when
       // a score exceeds it by more than 2^8 (P and l stay far from fp32's
       // limits, and the final division uses the same maximum).  S(it) is
@@ -506,69 +541,60 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float m_new = need ? mt : m;
         const float f = need ? ex2(m - m_new) : 1.f;  // 0 from -inf
         if (it > 0) {
+#pragma unroll 1
+          for (int c = 0; c < kHeadDim; c += 8) {
+            float o[8];
+            tmem_ld8(to + c, o);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            float o[32];
-            tmem_ld32(to + 32 * c, o);
-            tc_wait_ld_for(o);
-#pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] *= f;
-            tmem_st32(to + 32 * c, o);
+            for (int k = 0; k < 8; ++k) o[k] *= f;
+            tmem_st8(to + c, o);
           }
         }
         l *= f;
         m = m_new;
       }
       const float neg_m = m == kNegInf ? 0.f : -m;
-      float ls[4] = {0.f, 0.f, 0.f, 0.f};
+      float l0 = 0.f, l1 = 0.f;
       auto probs = [&](float (&v)[32], int c0) {
-        if (!plain) mask(v, c0);
         uint32_t pk[16];
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
           const float p0 = ex2(fmaf(v[2 * k], scale, neg_m));
           const float p1 = ex2(fmaf(v[2 * k + 1], scale, neg_m));
-          ls[k & 3] += p0 + p1;
+          l0 += p0;
+          l1 += p1;
           pk[k] = pack2<kBF16>(p0, p1);
         }
-        // (Scores up to column c0 + 63 are in registers: P may overwrite
-        // columns up to c0 / 2 + 15.)
         tmem_st16(ts + c0 / 2, pk);
       };
-      tc_wait_ld_for(va);
-      tmem_ld32(ts + 32, vb);
       probs(va, 0);
-      tc_wait_ld_for(vb);
-      tmem_ld32(ts + 64, va);
       probs(vb, 32);
-      tc_wait_ld_for(va);
-      tmem_ld32(ts + 96, vb);
-      probs(va, 64);
-      tc_wait_ld_for(vb);
-      probs(vb, 96);
-      l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+      probs(vc, 64);
+      probs(vd, 96);
+      l += l0 + l1;
       tc_wait_st();
       tc_fence_before();
       mbar_arrive(bar(kBarP + x));
     }
     // ---------------- epilogue
     if (ok && nt > 0) ok = mbar_wait_or_abort(bar(kBarO + x), 0, p.err_flag, abort_word);
-    if (ok && w.tok[x] > 0) {
+    if (ok && tok > 0) {
       tc_fence_after();
       const bool bad = *bad_word != 0;
       const bool live = l > 0.f && !bad;
+      const bool mine = r < tok * G;
       const float inv = live ? 1.f / l : 0.f;
       const int64_t row = static_cast<int64_t>(w.q0 + i) * p.h_q + w.j * G + r % G;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
+#pragma unroll 1
+      for (int c = 0; c < kHeadDim; c += 32) {
         float o[32];
-        tmem_ld32(to + 32 * c, o);
+        tmem_ld32(to + c, o);
         tc_wait_ld_for(o);
         if (!live) {
 #pragma unroll
           for (int k = 0; k < 32; ++k) o[k] = 0.f;
         }
-        if (mine) store_row<kBF16>(p, row, w.split, 32 * c, o, inv);
+        if (mine) store_row<kBF16>(p, row, w.split, c, o, inv);
       }
       if (mine && p.n_split > 1)
         p.part_lse[row * p.n_split + w.split] =
