@@ -29,12 +29,13 @@
 //   0-3, 4-7  softmax of tile A, of tile B: a thread owns a row (TMEM lane),
 //             so no value of a row is ever exchanged: running maximum, lazy
 //             rescale of O, P, running sum; epilogue;
-//   8         TMA producer (walks the block table, checks the block ids);
+//   8, 10     TMA producers of Q and K, of V (they walk the block table and
+//             check the block ids);
 //   9         MMA issuer: P_A V, S_A of the next tile, P_B V, S_B of the next
 //             tile: while one tile's softmax runs, the tensor cores work on
 //             the other's products.  MMAs of one thread run in order, so
 //             S_A(j + 1) may overwrite P_A(j) right behind its last reader;
-//   10        TMEM allocation (11 only fills its warpgroup).
+//   11        TMEM allocation.
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -52,7 +53,7 @@ constexpr int kSmemBytes = 1024 + kOffBars + 512;
 static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
 
 constexpr int kThreads = 384;
-constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpTmem = 10;
+constexpr int kWarpLoadK = 8, kWarpMma = 9, kWarpLoadV = 10, kWarpTmem = 11;
 constexpr int kTmemS = 0;                      // S_X: 128 X
 constexpr int kTmemO = 256;                    // O_X: 256 + 128 X
 constexpr float kNegInf = -__builtin_huge_valf();
@@ -222,7 +223,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto bar = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
   volatile int* abort_word = reinterpret_cast<volatile int*>(smem + kOffBars + kNumBars * 8);
   volatile int* bad_word = abort_word + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffBars + kNumBars * 8 + 8);
+  volatile int* made_by = abort_word + 2;  // copies that the K and the V producer made
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffBars + kNumBars * 8 + 16);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   // Longest work first: the last pieces of a chunk see the most positions.
@@ -275,13 +277,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
 
   if (warp >= 8) {
-    if (warp == kWarpLoad) {
-      // ---------------- TMA producer
+    if (warp == kWarpLoadK || warp == kWarpLoadV) {
+      // ---------------- TMA producers: one warp for Q and K, one for V (two
+      // streams of boxes; a warp gets a small box accepted about every 100 cycles)
+      const bool is_v = warp == kWarpLoadV;
+      const CUtensorMap* tm = is_v ? &tm_v : &tm_k;
       const uint64_t keep = policy_evict_last();
-      if (lane == 0) {
+      if (lane == 0) tma_prefetch_desc(tm);
+      if (lane == 0 && !is_v) {
         tma_prefetch_desc(&tm_q);
-        tma_prefetch_desc(&tm_k);
-        tma_prefetch_desc(&tm_v);
         const int tiles = w.tok_b > 0 ? 2 : 1;
         const uint32_t bytes = static_cast<uint32_t>(tiles * 2 * p.tokens_per_tile * G * 128);
         mbar_arrive_expect_tx(bar(kBarQ), bytes);
@@ -295,9 +299,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int x0 = w.j * kHeadDim;
       const int kb_end = ((w.hi - 1) >> lg) + 1;
       int cache0 = -(1 << 30), my_id = 0;
-      // Copies go round the ring: slot and phase parity of the next one, and
-      // the number made.
-      int slot = 0, made = 0;
+      // K(it) is the ring's copy 2 it, V(it) the copy 2 it + 1: slot and phase
+      // parity of this warp's next one, and the number it made.
+      int slot = is_v ? 1 : 0, made = 0;
       uint32_t phase = 0;
       bool ok = true;
       for (int it = 0; ok && it < n; ++it) {
@@ -318,38 +322,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const int row = id * bs + (bs >= kKv ? (t.t0 & (bs - 1)) : 0);
         const uint32_t bytes = static_cast<uint32_t>(bs >= kKv ? kTileBytes : nblk * bs * 256);
-#pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv) {
-          bool got = true;
-          if (lane == 0) {
-            got = mbar_wait_or_abort(bar(kBarEmpty + slot), phase ^ 1u, p.err_flag, abort_word);
-            if (got) mbar_arrive_expect_tx(bar(kBarFull + slot), bytes);
-          }
-          if (__shfl_sync(0xffffffffu, got ? 1 : 0, 0) == 0) {
-            ok = false;
-            break;
-          }
-          if (lane < nblk) {
-            const CUtensorMap* tm = kv ? &tm_v : &tm_k;
-            const uint32_t dst =
-                sbase + kOffRing + slot * kTileBytes + static_cast<uint32_t>(lane * bs * 128);
-            tma_load_2d_hint(dst, tm, x0, row, bar(kBarFull + slot), keep);
-            tma_load_2d_hint(dst + kHalf, tm, x0 + 64, row, bar(kBarFull + slot), keep);
-          }
-          ++made;
-          if (++slot == kRing) {
-            slot = 0;
-            phase ^= 1u;
-          }
+        bool got = true;
+        if (lane == 0) {
+          got = mbar_wait_or_abort(bar(kBarEmpty + slot), phase ^ 1u, p.err_flag, abort_word);
+          if (got) mbar_arrive_expect_tx(bar(kBarFull + slot), bytes);
+        }
+        if (__shfl_sync(0xffffffffu, got ? 1 : 0, 0) == 0) {
+          ok = false;
+          break;
+        }
+        if (lane < nblk) {
+          const uint32_t dst =
+              sbase + kOffRing + slot * kTileBytes + static_cast<uint32_t>(lane * bs * 128);
+          tma_load_2d_hint(dst, tm, x0, row, bar(kBarFull + slot), keep);
+          tma_load_2d_hint(dst + kHalf, tm, x0 + 64, row, bar(kBarFull + slot), keep);
+        }
+        ++made;
+        slot += 2;
+        if (slot >= kRing) {
+          slot -= kRing;
+          phase ^= 1u;
         }
       }
-      // Never leave the CTA with copies in flight: the last round's are waited
-      // for, each slot's by its own phase.
-      if (lane == 0) {
-        mbar_wait(bar(kBarQ), 0, p.err_flag);
-        for (int e = max(0, made - kRing); e < made; ++e)
-          if (!mbar_wait(bar(kBarFull + e % kRing), (e / kRing) & 1, p.err_flag)) break;
-      }
+      if (lane == 0) made_by[is_v ? 1 : 0] = made;
       __syncwarp();
     } else if (warp == kWarpMma) {
       // ---------------- MMA issuer: the whole warp runs the loop, lane 0
@@ -607,6 +602,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kWarpTmem) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
+  }
+  if (threadIdx.x == 0) {
+    // Never leave the CTA with copies in flight (after an abort there may be
+    // some): the last copy into each ring slot is waited for.
+    mbar_wait(bar(kBarQ), 0, p.err_flag);
+    const int made_k = made_by[0], made_v = made_by[1];
+    auto was_made = [&](int e) { return (e >> 1) < ((e & 1) ? made_v : made_k); };
+    const int end = 2 * max(made_k, made_v);
+    for (int e = max(0, end - 2 * kRing); e < end; ++e)
+      if (was_made(e) && !was_made(e + kRing) &&
+          !mbar_wait(bar(kBarFull + e % kRing), (e / kRing) & 1, p.err_flag))
+        break;
   }
 }
 
