@@ -917,10 +917,10 @@ static int gqa_prefill_impl(const void* q, const void* k_cache, const void* v_ca
   if (!q_start || !aligned(q_start, 4)) return DECATTN_ERR_INVALID_ARG;
   if (tokens == 0) return DECATTN_OK;
   const int group = h_q / h_kv;
+  const int sms = device_sm_count();
+  if (sms <= 0) return DECATTN_ERR_CUDA;
   int ns = L->num_splits;
   if (ns == 0) {
-    const int sms = device_sm_count();
-    if (sms <= 0) return DECATTN_ERR_CUDA;
     ns = plan_prefill_splits(L->batch, tokens, max_q_len, h_q, h_kv, L->max_seq_len, window,
                              sinks, sms);
   }
@@ -951,6 +951,7 @@ static int gqa_prefill_impl(const void* q, const void* k_cache, const void* v_ca
   p.tokens_per_tile = 128 / group;
   p.n_items = static_cast<int>(items);
   p.n_split = ns;
+  p.steal = items * h_kv * ns > sms ? 1 : 0;
   p.negate = scale < 0.f ? 1 : 0;
   // A zero scale (equal weights) is a scale that no score can feel: the
   // kernel's masked scores are -inf, and -inf times 0 would be NaN.

@@ -18,9 +18,10 @@
 // Operand placement:
 //   Q_A, Q_B   shared memory [2 halves][128 rows][128 B], 128-byte swizzle,
 //              by TMA (a 3-D box: 64 columns x G heads x tokens)   A of S
-//   K, V       one TMA ring of five 32 KB slots, K(0) V(0) K(1) V(1) ...,
+//   K, V       one TMA ring of four 32 KB slots, K(0) V(0) K(1) V(1) ...,
 //              [2 halves][128 tokens][128 B], 128-byte swizzle, one box per
 //              half and cache block         K: B of S;  V: B of P V (MN-major)
+//   out        32 KB in which a warp turns its rows' lanes into whole lines
 //   S_X, P_X   TMEM, 128 fp32 columns; P_X (16-bit, 64 columns) over S_X  A of P V
 //   O_X        TMEM, 128 fp32 columns
 // (2 x (128 + 128) columns: all of TMEM, one CTA per SM.)
@@ -35,7 +36,13 @@
 //             tile: while one tile's softmax runs, the tensor cores work on
 //             the other's products.  MMAs of one thread run in order, so
 //             S_A(j + 1) may overwrite P_A(j) right behind its last reader;
-//   11        TMEM allocation.
+//   11        scheduler: which rows next (below); TMEM allocation.
+//
+// A CTA stays on its SM and goes from piece to piece (two Q tiles of one
+// sequence and KV head): the scheduler takes over CTAs of the grid that have
+// not started (cluster launch control) while the present piece is worked on,
+// so the next one's Q, K and V are on their way, and its first S is computed,
+// during the softmax warps' epilogue.  Pieces come longest first.
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -46,35 +53,50 @@ constexpr int kM = 128;                        // rows of a Q tile
 constexpr int kKv = 128;                       // tokens of a K / V tile
 constexpr int kHalf = 128 * 128;               // 64 columns x 128 rows, 16 KB
 constexpr int kTileBytes = 2 * kHalf;          // 32 KB
-constexpr int kRing = 5;
+constexpr int kRing = 4;
 constexpr int kOffRing = 2 * kTileBytes;       // behind Q_A, Q_B
-constexpr int kOffBars = kOffRing + kRing * kTileBytes;
-constexpr int kSmemBytes = 1024 + kOffBars + 512;
+constexpr int kOffStage = kOffRing + kRing * kTileBytes;
+constexpr int kStageBytes = 32 * 128;          // one softmax warp's: 32 rows x 128 B
+constexpr int kOffBars = kOffStage + 8 * kStageBytes;
+constexpr int kSmemBytes = 1024 + kOffBars + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
 
 constexpr int kThreads = 384;
-constexpr int kWarpLoadK = 8, kWarpMma = 9, kWarpLoadV = 10, kWarpTmem = 11;
+constexpr int kWarpLoadK = 8, kWarpMma = 9, kWarpLoadV = 10, kWarpNext = 11;
 constexpr int kTmemS = 0;                      // S_X: 128 X
 constexpr int kTmemO = 256;                    // O_X: 256 + 128 X
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kRescaleThreshold = 8.0f;      // log2 units: P stays <= 2^8
 
 enum : int {
-  kBarQ = 0,
-  kBarFull = 1,                 // ring slot landed
+  kBarQ = 0,                    // Q tiles landed
+  kBarQFree = 1,                // every S of the piece computed
+  kBarFull = 2,                 // ring slot landed
   kBarEmpty = kBarFull + kRing, // ring slot free
   kBarS = kBarEmpty + kRing,    // 2: S_X computed
   kBarP = kBarS + 2,            // 2: P_X written (128 arrivals)
   kBarO = kBarP + 2,            // 2: O_X complete
-  kBarDrain = kBarO + 2,
+  kBarItem = kBarO + 2,         // 2: piece published
+  kBarItemFree = kBarItem + 2,  // 2: piece done by every role (11 warps)
+  kBarNext = kBarItemFree + 2,  // the launch control's answer
+  kBarAsk = kBarNext + 1,       // the piece's last K copy is on its way
+  kBarDrain = kBarAsk + 1,
   kNumBars = kBarDrain + 1
 };
+constexpr int kRoleWarps = 11;  // producers, MMA, softmax
 
-// One CTA's work: rows of one sequence and KV head against a range of tiles.
+// Behind the barriers, in the same kilobyte.
+constexpr int kOffWords = kOffBars + 256;   // abort, bad, copies made by the producers, TMEM
+constexpr int kOffAnswer = kOffBars + 320;  // the launch control's answer, 16 bytes
+constexpr int kOffItems = kOffBars + 384;   // two pieces
+static_assert(kNumBars * 8 <= 256, "barriers");
+
+// A piece of work: rows of one sequence and KV head against a range of tiles.
 struct Item {
-  int b, j, split;
+  int valid;        // 0: no more pieces
+  int j, split;
   int n, len;       // chunk length, cache length
-  int q0;           // first packed row of the sequence
+  int b, q0;        // sequence, its first packed row
   int i0;           // first token of the chunk in tile A
   int tok_a, tok_b; // tokens in tile A, B
   int lo, s_end, base, sink_tiles;
@@ -83,6 +105,7 @@ struct Item {
   int n_a, n_b;     // tiles that tile A, B need, from tile0 on
   int bad;
 };
+static_assert(2 * sizeof(Item) <= 1024 - 384, "items");
 
 struct Tile {
   int t0, skip, nval;  // rows [skip, nval) hold tokens that may be seen
@@ -103,62 +126,70 @@ __device__ __forceinline__ int tiles_to(const Item& w, int last) {
   return last < w.base ? 0 : w.sink_tiles + (last - w.base) / kKv + 1;
 }
 
-// Finds the item of this CTA: the rows of all sequences are cut into pieces
-// of 2 tpt tokens, numbered through; false if there is no such piece.
-__device__ __forceinline__ bool find_item(const PrefillParams& p, int index, Item& w) {
-  __shared__ int warp_sum[kThreads / 32];
-  __shared__ int found[3];  // b, piece within b, 1
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int tpi = 2 * p.tokens_per_tile;
-  int carry = 0;
-  if (threadIdx.x == 0) found[2] = 0;
-  for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
-    const int b = b0 + threadIdx.x;
-    int cnt = 0;
-    if (b < p.batch) {
-      const int a = p.q_start[b], e = p.q_start[b + 1];
-      if (a < 0 || e < a || e > p.tokens || e - a > p.max_q_len) {
-        if (blockIdx.x == 0) flag_error(p.err_flag, kFlagBadSeqLen);
-      } else {
-        cnt = (e - a + tpi - 1) / tpi;
-      }
+// Walks the pieces from the last sequence's last one back (within a chunk the
+// last rows see most): 32 sequences at a time, one per lane.
+struct Cursor {
+  int b0;      // the lanes hold sequences b0 .. b0 + 31
+  int before;  // pieces behind those sequences
+  int start, n, len, cnt, pre;  // this lane's sequence; pre: pieces of the lanes above it
+};
+
+__device__ __forceinline__ void load_cursor(const PrefillParams& p, Cursor& c, int lane) {
+  const int b = c.b0 + lane, tpi = 2 * p.tokens_per_tile;
+  c.cnt = c.n = c.start = c.len = 0;
+  if (b >= 0 && b < p.batch) {
+    const int a = p.q_start[b], e = p.q_start[b + 1];
+    c.len = p.seq_lens[b];
+    if (a < 0 || e < a || e > p.tokens || e - a > p.max_q_len) {
+      if (blockIdx.x == 0) flag_error(p.err_flag, kFlagBadSeqLen);
+    } else {
+      c.start = a;
+      c.n = e - a;
+      c.cnt = (e - a + tpi - 1) / tpi;
     }
-    int inc = cnt;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int up = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += up;
-    }
-    __syncthreads();
-    if (lane == 31) warp_sum[warp] = inc;
-    __syncthreads();
-    int before = carry, total = 0;
-#pragma unroll
-    for (int k = 0; k < kThreads / 32; ++k) {
-      if (k < warp) before += warp_sum[k];
-      total += warp_sum[k];
-    }
-    const int first = before + inc - cnt;
-    if (index >= first && index < first + cnt) {
-      found[0] = b;
-      found[1] = index - first;
-      found[2] = 1;
-    }
-    carry += total;
-    if (carry > index) break;  // uniform
   }
-  __syncthreads();
-  if (!found[2]) return false;
-  w.b = found[0];
-  w.q0 = p.q_start[w.b];
-  w.n = p.q_start[w.b + 1] - w.q0;
-  w.i0 = found[1] * tpi;
+  int sum = c.cnt;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int up = __shfl_down_sync(0xffffffffu, sum, o);
+    if (lane + o < 32) sum += up;
+  }
+  c.pre = sum - c.cnt;
+}
+
+// The index-th piece (all lanes; index counts from the end); false if there
+// are not that many.
+__device__ __forceinline__ bool find_item(const PrefillParams& p, Cursor& c, int index, Item& w) {
+  const int lane = threadIdx.x & 31;
+  if (index < c.before) {  // (launch control hands out later pieces; be safe)
+    c.b0 = p.batch - 32;
+    c.before = 0;
+    load_cursor(p, c, lane);
+  }
+  for (;;) {
+    const int all = __shfl_sync(0xffffffffu, c.pre + c.cnt, 0);
+    if (index < c.before + all) break;
+    if (c.b0 <= 0) return false;
+    c.before += all;
+    c.b0 -= 32;
+    load_cursor(p, c, lane);
+  }
+  const int at = index - c.before;
+  const bool mine = at >= c.pre && at < c.pre + c.cnt;
+  const int src = __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
+  const int tpi = 2 * p.tokens_per_tile;
+  w.valid = 1;
+  w.b = c.b0 + src;
+  w.q0 = __shfl_sync(0xffffffffu, c.start, src);
+  w.n = __shfl_sync(0xffffffffu, c.n, src);
+  w.len = __shfl_sync(0xffffffffu, c.len, src);
+  const int cnt = __shfl_sync(0xffffffffu, c.cnt, src), pre = __shfl_sync(0xffffffffu, c.pre, src);
+  w.i0 = (cnt - 1 - (at - pre)) * tpi;
   w.tok_a = min(p.tokens_per_tile, w.n - w.i0);
   w.tok_b = max(0, min(p.tokens_per_tile, w.n - w.i0 - p.tokens_per_tile));
-  w.len = p.seq_lens[w.b];
   w.bad = w.len < 0 || w.len > p.max_seq_len;
   if (w.bad) {
-    if (threadIdx.x == 0) flag_error(p.err_flag, kFlagBadSeqLen);
+    if (lane == 0) flag_error(p.err_flag, kFlagBadSeqLen);
     w.len = 0;
   }
   // Positions of the first and last rows, and the tiles that they see: with
@@ -190,24 +221,17 @@ __device__ __forceinline__ uint32_t below(int n) {
   return ~r;
 }
 
-template <bool kBF16>
-__device__ __forceinline__ void store_row(const PrefillParams& p, int64_t row, int split, int c0,
-                                          const float (&o)[32], float inv) {
-  if (p.n_split == 1) {
-    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * kHeadDim + c0);
+// A warp's 32 rows of 128 bytes (eight 16-byte pieces, one row per thread)
+// go through its own 4 KB of shared memory, so that eight lanes store a row's
+// whole line: piece c of row r lies at place c ^ (r % 8) of its row.
+__device__ __forceinline__ void stage_rows(uint8_t* stage, const uint4 (&v)[8], int lane) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      dst[k] = make_uint4(pack2<kBF16>(o[8 * k] * inv, o[8 * k + 1] * inv),
-                          pack2<kBF16>(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
-                          pack2<kBF16>(o[8 * k + 4] * inv, o[8 * k + 5] * inv),
-                          pack2<kBF16>(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
-  } else {
-    float4* dst = reinterpret_cast<float4*>(p.part_o + (row * p.n_split + split) * kHeadDim + c0);
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      dst[k] = make_float4(o[4 * k] * inv, o[4 * k + 1] * inv, o[4 * k + 2] * inv,
-                           o[4 * k + 3] * inv);
-  }
+  for (int c = 0; c < 8; ++c)
+    *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) = v[c];
+  __syncwarp();
+}
+__device__ __forceinline__ uint4 staged(const uint8_t* stage, int row, int c) {
+  return *reinterpret_cast<const uint4*>(stage + row * 128 + ((c ^ (row & 7)) << 4));
 }
 
 template <bool kBF16>
@@ -221,38 +245,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sbase = smem_u32(smem);
   const uint32_t bar0 = sbase + kOffBars;
   auto bar = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
-  volatile int* abort_word = reinterpret_cast<volatile int*>(smem + kOffBars + kNumBars * 8);
-  volatile int* bad_word = abort_word + 1;
-  volatile int* made_by = abort_word + 2;  // copies that the K and the V producer made
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffBars + kNumBars * 8 + 16);
+  volatile int* abort_word = reinterpret_cast<volatile int*>(smem + kOffWords);
+  volatile int* bad_word = abort_word + 1;  // 2: a piece met a bad block id
+  volatile int* made_by = abort_word + 3;   // copies made by the K and V producers, Q loads
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffWords + 32);
+  Item* items = reinterpret_cast<Item*>(smem + kOffItems);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-
-  // Longest work first: the last pieces of a chunk see the most positions.
-  Item w;
-  w.j = static_cast<int>(blockIdx.x) % p.h_kv;
-  const int rest = static_cast<int>(blockIdx.x) / p.h_kv;
-  w.split = rest % p.n_split;
-  if (!find_item(p, p.n_items - 1 - rest / p.n_split, w)) return;
-  const int n = max(w.n_a, w.n_b);
-
   const int G = p.group;
-  if (n == 0) {
-    // Nothing to see (or bad lengths): zero rows, or an empty partial.
-    const int rows = (w.tok_a + w.tok_b) * G;
-    for (int e = threadIdx.x; e < rows * 16; e += kThreads) {
-      const int r = e >> 4;
-      const int64_t row = static_cast<int64_t>(w.q0 + w.i0 + r / G) * p.h_q + w.j * G + r % G;
-      if (p.n_split == 1)
-        reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * kHeadDim)[e & 15] =
-            make_uint4(0, 0, 0, 0);
-      else if ((e & 15) == 0)
-        p.part_lse[row * p.n_split + w.split] = w.bad ? DECATTN_POISON_LSE : kNegInf;
-    }
-    return;
-  }
 
   if (threadIdx.x == 0) {
     mbar_init(bar(kBarQ), 1);
+    mbar_init(bar(kBarQFree), 1);
     for (int s = 0; s < kRing; ++s) {
       mbar_init(bar(kBarFull + s), 1);
       mbar_init(bar(kBarEmpty + s), 1);
@@ -261,13 +264,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(kBarS + x), 1);
       mbar_init(bar(kBarP + x), kM);
       mbar_init(bar(kBarO + x), 1);
+      mbar_init(bar(kBarItem + x), 1);
+      mbar_init(bar(kBarItemFree + x), kRoleWarps);
     }
+    mbar_init(bar(kBarNext), 1);
+    mbar_init(bar(kBarAsk), 1);
     mbar_init(bar(kBarDrain), 1);
-    *abort_word = 0;
-    *bad_word = 0;
+    for (int k = 0; k < 6; ++k) abort_word[k] = 0;
     fence_barrier_init();
   }
-  if (warp == kWarpTmem) {
+  if (warp == kWarpNext) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
@@ -275,6 +281,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+
+  // The k-th piece, as every role sees it (all lanes of its warp); released
+  // once the role is done with it.
+  auto get_item = [&](int k, Item& w) -> bool {
+    const bool there =
+        mbar_wait_or_abort(bar(kBarItem + (k & 1)), (k >> 1) & 1, p.err_flag, abort_word);
+    if (!__all_sync(0xffffffffu, there)) return false;
+    w = items[k & 1];
+    return w.valid != 0;
+  };
+  auto release_item = [&](int k) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(kBarItemFree + (k & 1)));
+  };
 
   if (warp >= 8) {
     if (warp == kWarpLoadK || warp == kWarpLoadV) {
@@ -284,65 +304,76 @@ __global__ void __launch_bounds__(kThreads, 1)
       const CUtensorMap* tm = is_v ? &tm_v : &tm_k;
       const uint64_t keep = policy_evict_last();
       if (lane == 0) tma_prefetch_desc(tm);
-      if (lane == 0 && !is_v) {
-        tma_prefetch_desc(&tm_q);
-        const int tiles = w.tok_b > 0 ? 2 : 1;
-        const uint32_t bytes = static_cast<uint32_t>(tiles * 2 * p.tokens_per_tile * G * 128);
-        mbar_arrive_expect_tx(bar(kBarQ), bytes);
-        for (int x = 0; x < tiles; ++x)
-          for (int h = 0; h < 2; ++h)
-            tma_load_3d(sbase + x * kTileBytes + h * kHalf, &tm_q, 64 * h, w.j * G,
-                        w.q0 + w.i0 + x * p.tokens_per_tile, bar(kBarQ));
-      }
-      const int32_t* bt = p.block_table + static_cast<size_t>(w.b) * p.max_blocks_per_seq;
+      if (lane == 0 && !is_v) tma_prefetch_desc(&tm_q);
       const int bs = p.block_size, lg = p.log2_block_size;
-      const int x0 = w.j * kHeadDim;
-      const int kb_end = ((w.hi - 1) >> lg) + 1;
-      int cache0 = -(1 << 30), my_id = 0;
-      // K(it) is the ring's copy 2 it, V(it) the copy 2 it + 1: slot and phase
-      // parity of this warp's next one, and the number it made.
-      int slot = is_v ? 1 : 0, made = 0;
+      // K(it) is the ring's copy 2 it, V(it) the copy 2 it + 1, counted over
+      // all pieces: slot and phase parity of this warp's next one, and the
+      // number it made.
+      int slot = is_v ? 1 : 0, made = 0, q_loads = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int it = 0; ok && it < n; ++it) {
-        const Tile t = tile_of(w, it);
-        const int kb0 = t.t0 >> lg;
-        const int nblk = bs >= kKv ? 1 : (t.nval + bs - 1) >> lg;
-        // The lanes hold the ids of the next 32 blocks (read ahead of use).
-        if (kb0 + nblk > cache0 + 32) {
-          cache0 = kb0;
-          my_id = kb0 + lane < kb_end ? bt[kb0 + lane] : 0;
+      Item w;
+      for (int k = 0; ok && get_item(k, w); ++k) {
+        const int n = max(w.n_a, w.n_b);
+        if (n > 0 && !is_v) {
+          if (lane == 0) {
+            ok = mbar_wait_or_abort(bar(kBarQFree), (q_loads & 1) ^ 1, p.err_flag, abort_word);
+            if (ok) {
+              const int tiles = w.tok_b > 0 ? 2 : 1;
+              mbar_arrive_expect_tx(
+                  bar(kBarQ), static_cast<uint32_t>(tiles * 2 * p.tokens_per_tile * G * 128));
+              for (int x = 0; x < tiles; ++x)
+                for (int h = 0; h < 2; ++h)
+                  tma_load_3d(sbase + x * kTileBytes + h * kHalf, &tm_q, 64 * h, w.j * G,
+                              w.q0 + w.i0 + x * p.tokens_per_tile, bar(kBarQ));
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+          if (ok) made_by[2] = ++q_loads;
         }
-        int id = __shfl_sync(0xffffffffu, my_id, kb0 - cache0 + min(lane, nblk - 1));
-        if (id < 0 || id >= p.num_blocks) {
-          // Copy block 0 instead; the rows become zeros.
-          id = 0;
-          *bad_word = 1;
-          flag_error(p.err_flag, kFlagBadBlock);
+        const int32_t* bt = p.block_table + static_cast<size_t>(w.b) * p.max_blocks_per_seq;
+        const int x0 = w.j * kHeadDim;
+        const int kb_end = ((w.hi - 1) >> lg) + 1;
+        int cache0 = -(1 << 30), my_id = 0;
+        for (int it = 0; ok && it < n; ++it) {
+          const Tile t = tile_of(w, it);
+          const int kb0 = t.t0 >> lg;
+          const int nblk = bs >= kKv ? 1 : (t.nval + bs - 1) >> lg;
+          // The lanes hold the ids of the next 32 blocks (read ahead of use).
+          if (kb0 + nblk > cache0 + 32) {
+            cache0 = kb0;
+            my_id = kb0 + lane < kb_end ? bt[kb0 + lane] : 0;
+          }
+          int id = __shfl_sync(0xffffffffu, my_id, kb0 - cache0 + min(lane, nblk - 1));
+          if (id < 0 || id >= p.num_blocks) {
+            // Copy block 0 instead; the rows become zeros.
+            id = 0;
+            bad_word[k & 1] = 1;
+            flag_error(p.err_flag, kFlagBadBlock);
+          }
+          const int row = id * bs + (bs >= kKv ? (t.t0 & (bs - 1)) : 0);
+          const uint32_t bytes = static_cast<uint32_t>(bs >= kKv ? kTileBytes : nblk * bs * 256);
+          if (lane == 0) {
+            ok = mbar_wait_or_abort(bar(kBarEmpty + slot), phase ^ 1u, p.err_flag, abort_word);
+            if (ok) mbar_arrive_expect_tx(bar(kBarFull + slot), bytes);
+          }
+          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+          if (!ok) break;
+          if (lane < nblk) {
+            const uint32_t dst =
+                sbase + kOffRing + slot * kTileBytes + static_cast<uint32_t>(lane * bs * 128);
+            tma_load_2d_hint(dst, tm, x0, row, bar(kBarFull + slot), keep);
+            tma_load_2d_hint(dst + kHalf, tm, x0 + 64, row, bar(kBarFull + slot), keep);
+          }
+          ++made;
+          slot += 2;
+          if (slot >= kRing) {
+            slot -= kRing;
+            phase ^= 1u;
+          }
         }
-        const int row = id * bs + (bs >= kKv ? (t.t0 & (bs - 1)) : 0);
-        const uint32_t bytes = static_cast<uint32_t>(bs >= kKv ? kTileBytes : nblk * bs * 256);
-        bool got = true;
-        if (lane == 0) {
-          got = mbar_wait_or_abort(bar(kBarEmpty + slot), phase ^ 1u, p.err_flag, abort_word);
-          if (got) mbar_arrive_expect_tx(bar(kBarFull + slot), bytes);
-        }
-        if (__shfl_sync(0xffffffffu, got ? 1 : 0, 0) == 0) {
-          ok = false;
-          break;
-        }
-        if (lane < nblk) {
-          const uint32_t dst =
-              sbase + kOffRing + slot * kTileBytes + static_cast<uint32_t>(lane * bs * 128);
-          tma_load_2d_hint(dst, tm, x0, row, bar(kBarFull + slot), keep);
-          tma_load_2d_hint(dst + kHalf, tm, x0 + 64, row, bar(kBarFull + slot), keep);
-        }
-        ++made;
-        slot += 2;
-        if (slot >= kRing) {
-          slot -= kRing;
-          phase ^= 1u;
-        }
+        if (lane == 0 && !is_v) mbar_arrive(bar(kBarAsk));
+        release_item(k);
       }
       if (lane == 0) made_by[is_v ? 1 : 0] = made;
       __syncwarp();
@@ -365,11 +396,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         return g;
       };
       // S_X = Q_X K^T: eight k-steps of 16 dims, four per 64-column half.
-      // `last`: no other tile reads this K slot after this one.
-      auto issue_s = [&](int x, int s, bool last) {
+      // `last`: no other tile reads this K slot after this one; `end`: this is
+      // the piece's last S.
+      auto issue_s = [&](int x, int s, bool last, bool end) {
         const uint64_t a = dq + static_cast<uint64_t>((x * kTileBytes) >> 4);
         const uint64_t b = dk + static_cast<uint64_t>((s * kTileBytes) >> 4);
-        const uint32_t done = bar(kBarS + x), empty = bar(kBarEmpty + s);
+        const uint32_t done = bar(kBarS + x), empty = bar(kBarEmpty + s), q_free = bar(kBarQFree);
         const uint32_t d = tmem + kTmemS + kKv * x;
         if (elect_one()) {
 #pragma unroll
@@ -379,6 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc_commit(done);
           if (last) tc_commit(empty);
+          if (end) tc_commit(q_free);
         }
         __syncwarp();
       };
@@ -400,59 +433,71 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       };
       // Tile B needs at least the tiles that A needs, or there is no tile B.
-      int slot = 0;
-      uint32_t phase = 0;
+      // Counters run over all pieces: the ring's slot and phase, Q loads, P.
+      int slot = kRing - 1, q_loads = 0;
+      uint32_t phase = 1, phase_a = 0, phase_b = 0;
       auto next = [&]() {
         if (++slot == kRing) {
           slot = 0;
           phase ^= 1u;
         }
       };
-      bool ok = wait(kBarQ, 0) && wait(kBarFull + slot, phase);
-      if (ok) {
-        if (w.n_a > 0) issue_s(0, slot, w.n_b == 0);
-        if (w.n_b > 0) issue_s(1, slot, true);
-      }
-      for (int it = 0; ok && it < n; ++it) {
-        next();
-        const int sv = slot;
-        ok = wait(kBarFull + sv, phase);
-        if (!ok) break;
-        const Tile t = tile_of(w, it);
-        if (t.nval < kKv || t.skip > 0) {
-          // V rows outside [skip, nval) become zeros (P is 0 there, but the
-          // slots may hold NaN), while the softmax works on this tile.  (All
-          // 128 bytes of a row: the swizzle does not matter.)
-          uint8_t* v = smem + kOffRing + sv * kTileBytes;
-#pragma unroll 1
-          for (int i = lane; i < (t.skip + kKv - t.nval) * 16; i += 32) {
-            const int k = i >> 4, c = i & 15;
-            const int r = k < t.skip ? k : t.nval + (k - t.skip);
-            *reinterpret_cast<uint4*>(v + (c >> 3) * kHalf + r * 128 + ((c & 7) << 4)) =
-                make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
-        // The next K tile is waited for first, so that O += P V and the next S
-        // follow each other without a pause.
-        if (it + 1 < n) {
+      bool ok = true;
+      Item w;
+      for (int k = 0; ok && get_item(k, w); ++k) {
+        const int n = max(w.n_a, w.n_b);
+        if (n > 0) {
           next();
-          ok = wait(kBarFull + slot, phase);
+          ok = wait(kBarQ, q_loads++ & 1) && wait(kBarFull + slot, phase);
           if (!ok) break;
+          if (w.n_a > 0) issue_s(0, slot, w.n_b == 0, n == 1 && w.n_b == 0);
+          if (w.n_b > 0) issue_s(1, slot, true, n == 1);
         }
-        if (it < w.n_a) {
-          ok = wait(kBarP, it & 1);
+        for (int it = 0; it < n; ++it) {
+          next();
+          const int sv = slot;
+          ok = wait(kBarFull + sv, phase);
           if (!ok) break;
-          issue_pv(0, sv, it == 0, it + 1 == w.n_a, it >= w.n_b);
-          if (it + 1 < w.n_a) issue_s(0, slot, it + 1 >= w.n_b);
+          const Tile t = tile_of(w, it);
+          if (t.nval < kKv || t.skip > 0) {
+            // V rows outside [skip, nval) become zeros (P is 0 there, but the
+            // slots may hold NaN), while the softmax works on this tile.  (All
+            // 128 bytes of a row: the swizzle does not matter.)
+            uint8_t* v = smem + kOffRing + sv * kTileBytes;
+#pragma unroll 1
+            for (int i = lane; i < (t.skip + kKv - t.nval) * 16; i += 32) {
+              const int kk = i >> 4, c = i & 15;
+              const int r = kk < t.skip ? kk : t.nval + (kk - t.skip);
+              *reinterpret_cast<uint4*>(v + (c >> 3) * kHalf + r * 128 + ((c & 7) << 4)) =
+                  make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          // The next K tile is waited for first, so that O += P V and the next
+          // S follow each other without a pause.
+          if (it + 1 < n) {
+            next();
+            ok = wait(kBarFull + slot, phase);
+            if (!ok) break;
+          }
+          if (it < w.n_a) {
+            ok = wait(kBarP, phase_a);
+            if (!ok) break;
+            phase_a ^= 1u;
+            issue_pv(0, sv, it == 0, it + 1 == w.n_a, it >= w.n_b);
+            if (it + 1 < w.n_a)
+              issue_s(0, slot, it + 1 >= w.n_b, it + 2 == n && w.n_b == 0);
+          }
+          if (it < w.n_b) {
+            ok = wait(kBarP + 1, phase_b);
+            if (!ok) break;
+            phase_b ^= 1u;
+            issue_pv(1, sv, it == 0, it + 1 == w.n_b, true);
+            if (it + 1 < w.n_b) issue_s(1, slot, true, it + 2 == n);
+          }
         }
-        if (it < w.n_b) {
-          ok = wait(kBarP + 1, it & 1);
-          if (!ok) break;
-          issue_pv(1, sv, it == 0, it + 1 == w.n_b, true);
-          if (it + 1 < w.n_b) issue_s(1, slot, true);
-        }
+        if (ok) release_item(k);
       }
       // Wait (bounded) until every MMA this warp issued has completed.
       if (elect_one()) {
@@ -460,153 +505,275 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait(bar(kBarDrain), 0, p.err_flag);
       }
       __syncwarp();
+    } else if (warp == kWarpNext) {
+      // ---------------- scheduler: publishes the pieces, one ahead of the
+      // one being worked on
+      Cursor c;
+      c.b0 = p.batch - 32;
+      c.before = 0;
+      load_cursor(p, c, lane);
+      int x = blockIdx.x, k = 0, asks = 0;
+      bool ok = true;
+      while (ok) {
+        const bool last = x < 0;
+        Item w;
+        bool some = false;
+        if (!last) {
+          // grid index: KV heads of a piece, then its splits, then pieces
+          w.j = x % p.h_kv;
+          const int rest = x / p.h_kv;
+          w.split = rest % p.n_split;
+          some = find_item(p, c, rest / p.n_split, w);
+        } else {
+          w = Item{};
+        }
+        if (some || last) {
+          if (lane == 0) {
+            ok = mbar_wait_or_abort(bar(kBarItemFree + (k & 1)), ((k >> 1) & 1) ^ 1, p.err_flag,
+                                    abort_word);
+            if (ok) {
+              bad_word[k & 1] = 0;
+              items[k & 1] = w;
+              mbar_arrive(bar(kBarItem + (k & 1)));
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+          ++k;
+        }
+        if (last || !ok) break;
+        // The next piece is claimed once the last copies of this one are on
+        // their way (about two tiles ahead: claimed at its start, it would be
+        // kept from CTAs that run out sooner; 256 pieces of 1 to 64 tiles took
+        // 146 us that way).  A grid of one wave has none to hand over.
+        x = -1;
+        if (p.steal) {
+          if (some) {
+            if (!mbar_wait_or_abort(bar(kBarAsk), (k - 1) & 1, p.err_flag, abort_word)) ok = false;
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+          }
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bar(kBarNext), 16);
+            clc_try_cancel(sbase + kOffAnswer, bar(kBarNext));
+          }
+          __syncwarp();
+          if (!mbar_wait_or_abort(bar(kBarNext), asks & 1, p.err_flag, abort_word)) ok = false;
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          ++asks;
+          x = clc_answer(sbase + kOffAnswer);
+          fence_proxy_async_smem();  // the answer is read before the next one is asked for
+        }
+      }
     }
   } else {
     // ---------------- softmax: thread = row r of tile x
     const int x = warp >> 2;
     const int r = 32 * (warp & 3) + lane;
-    const int nt = x ? w.n_b : w.n_a, tok = x ? w.tok_b : w.tok_a;
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t ts = tmem + lanes + kTmemS + kKv * x;
     const uint32_t to = tmem + lanes + kTmemO + kHeadDim * x;
-    const int i0 = w.i0 + x * p.tokens_per_tile;
-    const int i = i0 + min(r / G, max(0, tok - 1));
-    const int pos = w.len - w.n + i;
-    // Positions of the tile's first and last rows: tiles at or before the
-    // first (and inside the last one's window) need no mask.
-    const int pos0 = w.len - w.n + i0, pos1 = pos0 + tok - 1;
+    uint8_t* stage = smem + kOffStage + warp * kStageBytes;
+    // Row r is head r % G of token r / G: the division for r < 128, G <= 64.
+    const uint32_t inv_g = 65536u / static_cast<uint32_t>(G) + 1u;
+    const int r_tok = static_cast<int>((static_cast<uint32_t>(r) * inv_g) >> 16);
     const float scale = p.scale_log2, sign = p.negate ? -1.f : 1.f;
-    float m = kNegInf, l = 0.f;
+    uint32_t phase_s = 0, phase_o = 0;
     bool ok = true;
-    for (int it = 0; it < nt; ++it) {
-      const Tile t = tile_of(w, it);
-      const bool plain = !p.negate && t.skip == 0 && t.nval == kKv && t.t0 + kKv - 1 <= pos0 &&
-                         (p.window <= 0 || t.t0 > pos1 - p.window);
-      // Seen columns: [skip, hi), of them those from lo on or below sink (at
-      // or before the row's position; in its window or kept first tokens).
-      const int c_hi = min(t.nval, pos + 1 - t.t0);
-      const int c_lo = p.window > 0 ? pos + 1 - p.window - t.t0 : 0;
-      const int c_sink = p.sinks - t.t0;
-      auto mask = [&](float (&v)[32], int c0) {
-        const uint32_t seen = (below(c_hi - c0) & ~below(t.skip - c0)) &
-                              (~below(c_lo - c0) | below(c_sink - c0));
+    Item w;
+    for (int k = 0; ok && get_item(k, w); ++k) {
+      const int nt = x ? w.n_b : w.n_a, tok = x ? w.tok_b : w.tok_a;
+      const int i0 = w.i0 + x * p.tokens_per_tile;
+      const int pos = w.len - w.n + i0 + min(r_tok, max(0, tok - 1));
+      // Positions of the tile's first and last rows: tiles at or before the
+      // first (and inside the last one's window) need no mask.
+      const int pos0 = w.len - w.n + i0, pos1 = pos0 + tok - 1;
+      float m = kNegInf, l = 0.f;
+      for (int it = 0; it < nt; ++it) {
+        const Tile t = tile_of(w, it);
+        const bool plain = !p.negate && t.skip == 0 && t.nval == kKv && t.t0 + kKv - 1 <= pos0 &&
+                           (p.window <= 0 || t.t0 > pos1 - p.window);
+        // Seen columns: [skip, hi), of them those from lo on or below sink (at
+        // or before the row's position; in its window or kept first tokens).
+        const int c_hi = min(t.nval, pos + 1 - t.t0);
+        const int c_lo = p.window > 0 ? pos + 1 - p.window - t.t0 : 0;
+        const int c_sink = p.sinks - t.t0;
+        auto mask = [&](float (&v)[32], int c0) {
+          const uint32_t seen = (below(c_hi - c0) & ~below(t.skip - c0)) &
+                                (~below(c_lo - c0) | below(c_sink - c0));
 #pragma unroll
-        for (int k = 0; k < 32; ++k) v[k] = (seen >> k) & 1u ? v[k] * sign : kNegInf;
-      };
-      if (!mbar_wait_or_abort(bar(kBarS + x), it & 1, p.err_flag, abort_word)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      // The row's 128 scores, in registers from here on.
-      float va[32], vb[32], vc[32], vd[32];
-      tmem_ld32(ts, va);
-      tmem_ld32(ts + 32, vb);
-      tmem_ld32(ts + 64, vc);
-      tmem_ld32(ts + 96, vd);
-      tc_wait_ld_for(va);
-      tc_wait_ld_for(vb);
-      tc_wait_ld_for(vc);
-      tc_wait_ld_for(vd);
-      if (!plain) {
-        mask(va, 0);
-        mask(vb, 32);
-        mask(vc, 64);
-        mask(vd, 96);
-      }
-      float mx0 = kNegInf, mx1 = kNegInf;
-      auto peak = [&](float (&v)[32]) {
-#pragma unroll
-        for (int k = 0; k < 32; k += 4) {
-          mx0 = fmaxf(mx0, fmaxf(v[k], v[k + 1]));
-          mx1 = fmaxf(mx1, fmaxf(v[k + 2], v[k + 3]));
+          for (int k = 0; k < 32; ++k) v[k] = (seen >> k) & 1u ? v[k] * sign : kNegInf;
+        };
+        if (!mbar_wait_or_abort(bar(kBarS + x), phase_s, p.err_flag, abort_word)) {
+          ok = false;
+          break;
         }
-      };
-      peak(va);
-      peak(vb);
-      peak(vc);
-      peak(vd);
-      const float mt = fmaxf(mx0, mx1) * scale;
-      // Lazy rescale: the maximum used for the exponentials moves only when
-      // a score exceeds it by more than 2^8 (P and l stay far from fp32's
-      // limits, and the final division uses the same maximum).  S(it) is
-      // complete, so O += P(it - 1) V before it is too.
-      const bool need = mt > m + kRescaleThreshold;
-      if (__any_sync(0xffffffffu, need)) {
-        const float m_new = need ? mt : m;
-        const float f = need ? ex2(m - m_new) : 1.f;  // 0 from -inf
-        if (it > 0) {
-#pragma unroll 1
-          for (int c = 0; c < kHeadDim; c += 8) {
-            float o[8];
-            tmem_ld8(to + c, o);
+        phase_s ^= 1u;
+        tc_fence_after();
+        // The row's 128 scores, in registers from here on.
+        float va[32], vb[32], vc[32], vd[32];
+        tmem_ld32(ts, va);
+        tmem_ld32(ts + 32, vb);
+        tmem_ld32(ts + 64, vc);
+        tmem_ld32(ts + 96, vd);
+        tc_wait_ld_for(va);
+        tc_wait_ld_for(vb);
+        tc_wait_ld_for(vc);
+        tc_wait_ld_for(vd);
+        if (!plain) {
+          mask(va, 0);
+          mask(vb, 32);
+          mask(vc, 64);
+          mask(vd, 96);
+        }
+        float mx0 = kNegInf, mx1 = kNegInf;
+        auto peak = [&](float (&v)[32]) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) o[k] *= f;
-            tmem_st8(to + c, o);
+          for (int k = 0; k < 32; k += 4) {
+            mx0 = fmaxf(mx0, fmaxf(v[k], v[k + 1]));
+            mx1 = fmaxf(mx1, fmaxf(v[k + 2], v[k + 3]));
           }
-        }
-        l *= f;
-        m = m_new;
-      }
-      const float neg_m = m == kNegInf ? 0.f : -m;
-      float l0 = 0.f, l1 = 0.f;
-      auto probs = [&](float (&v)[32], int c0) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const float p0 = ex2(fmaf(v[2 * k], scale, neg_m));
-          const float p1 = ex2(fmaf(v[2 * k + 1], scale, neg_m));
-          l0 += p0;
-          l1 += p1;
-          pk[k] = pack2<kBF16>(p0, p1);
-        }
-        tmem_st16(ts + c0 / 2, pk);
-      };
-      probs(va, 0);
-      probs(vb, 32);
-      probs(vc, 64);
-      probs(vd, 96);
-      l += l0 + l1;
-      tc_wait_st();
-      tc_fence_before();
-      mbar_arrive(bar(kBarP + x));
-    }
-    // ---------------- epilogue
-    if (ok && nt > 0) ok = mbar_wait_or_abort(bar(kBarO + x), 0, p.err_flag, abort_word);
-    if (ok && tok > 0) {
-      tc_fence_after();
-      const bool bad = *bad_word != 0;
-      const bool live = l > 0.f && !bad;
-      const bool mine = r < tok * G;
-      const float inv = live ? 1.f / l : 0.f;
-      const int64_t row = static_cast<int64_t>(w.q0 + i) * p.h_q + w.j * G + r % G;
+        };
+        peak(va);
+        peak(vb);
+        peak(vc);
+        peak(vd);
+        const float mt = fmaxf(mx0, mx1) * scale;
+        // Lazy rescale: the maximum used for the exponentials moves only when
+        // a score exceeds it by more than 2^8 (P and l stay far from fp32's
+        // limits, and the final division uses the same maximum).  S(it) is
+        // complete, so O += P(it - 1) V before it is too.
+        const bool need = mt > m + kRescaleThreshold;
+        if (__any_sync(0xffffffffu, need)) {
+          const float m_new = need ? mt : m;
+          const float f = need ? ex2(m - m_new) : 1.f;  // 0 from -inf
+          if (it > 0) {
 #pragma unroll 1
-      for (int c = 0; c < kHeadDim; c += 32) {
-        float o[32];
-        tmem_ld32(to + c, o);
-        tc_wait_ld_for(o);
-        if (!live) {
+            for (int c = 0; c < kHeadDim; c += 8) {
+              float o[8];
+              tmem_ld8(to + c, o);
 #pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = 0.f;
+              for (int k = 0; k < 8; ++k) o[k] *= f;
+              tmem_st8(to + c, o);
+            }
+          }
+          l *= f;
+          m = m_new;
         }
-        if (mine) store_row<kBF16>(p, row, w.split, c, o, inv);
+        const float neg_m = m == kNegInf ? 0.f : -m;
+        float l0 = 0.f, l1 = 0.f;
+        auto probs = [&](float (&v)[32], int c0) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float p0 = ex2(fmaf(v[2 * k], scale, neg_m));
+            const float p1 = ex2(fmaf(v[2 * k + 1], scale, neg_m));
+            l0 += p0;
+            l1 += p1;
+            pk[k] = pack2<kBF16>(p0, p1);
+          }
+          tmem_st16(ts + c0 / 2, pk);
+        };
+        probs(va, 0);
+        probs(vb, 32);
+        probs(vc, 64);
+        probs(vd, 96);
+        l += l0 + l1;
+        tc_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(kBarP + x));
       }
-      if (mine && p.n_split > 1)
-        p.part_lse[row * p.n_split + w.split] =
-            bad ? DECATTN_POISON_LSE : l > 0.f ? m + lg2(l) : kNegInf;
+      // ---------------- epilogue
+      if (ok && nt > 0) {
+        ok = mbar_wait_or_abort(bar(kBarO + x), phase_o, p.err_flag, abort_word);
+        phase_o ^= 1u;
+      }
+      if (ok && tok > 0) {
+        tc_fence_after();
+        const bool bad = w.bad || bad_word[k & 1] != 0;
+        const bool live = l > 0.f && !bad;
+        const float inv = live ? 1.f / l : 0.f;
+        // Packed row of the chunk's first row of this tile; this lane stores
+        // piece lane % 8 of the warp's rows lane / 8, + 4, ... + 28.
+        const int64_t row0 = static_cast<int64_t>(w.q0 + i0) * p.h_q + w.j * G;
+        const int rows = tok * G;
+        auto store = [&](auto&& put) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int q = 32 * (warp & 3) + (lane >> 3) + 4 * e;
+            const int tk = static_cast<int>((static_cast<uint32_t>(q) * inv_g) >> 16);
+            if (q < rows)
+              put(row0 + static_cast<int64_t>(tk) * p.h_q + (q - tk * G),
+                  staged(stage, (lane >> 3) + 4 * e, lane & 7));
+          }
+          __syncwarp();
+        };
+        uint4 v[8];
+        if (p.n_split == 1) {
+#pragma unroll 1
+          for (int c = 0; c < kHeadDim; c += 64) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float o[32];
+              tmem_ld32(to + c + 32 * h, o);
+              tc_wait_ld_for(o);
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                v[4 * h + e] = make_uint4(pack2<kBF16>(o[8 * e] * inv, o[8 * e + 1] * inv),
+                                          pack2<kBF16>(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+                                          pack2<kBF16>(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
+                                          pack2<kBF16>(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+            }
+            if (!live) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) v[e] = make_uint4(0, 0, 0, 0);
+            }
+            stage_rows(stage, v, lane);
+            store([&](int64_t row, const uint4& y) {
+              reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * kHeadDim + c)[lane & 7] =
+                  y;
+            });
+          }
+        } else {
+          if (nt > 0) {
+#pragma unroll 1
+            for (int c = 0; c < kHeadDim; c += 32) {
+              float o[32];
+              tmem_ld32(to + c, o);
+              tc_wait_ld_for(o);
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                v[e] = live ? make_uint4(__float_as_uint(o[4 * e] * inv),
+                                         __float_as_uint(o[4 * e + 1] * inv),
+                                         __float_as_uint(o[4 * e + 2] * inv),
+                                         __float_as_uint(o[4 * e + 3] * inv))
+                            : make_uint4(0, 0, 0, 0);
+              stage_rows(stage, v, lane);
+              store([&](int64_t row, const uint4& y) {
+                reinterpret_cast<uint4*>(p.part_o + (row * p.n_split + w.split) * kHeadDim +
+                                         c)[lane & 7] = y;
+              });
+            }
+          }
+          if (r < rows)
+            p.part_lse[(row0 + static_cast<int64_t>(r_tok) * p.h_q + (r - r_tok * G)) * p.n_split +
+                       w.split] = bad ? DECATTN_POISON_LSE : l > 0.f ? m + lg2(l) : kNegInf;
+        }
+      }
+      if (ok) release_item(k);
     }
   }
 
   tc_fence_before();
   __syncthreads();
-  if (warp == kWarpTmem) {
+  if (warp == kWarpNext) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
   if (threadIdx.x == 0) {
     // Never leave the CTA with copies in flight (after an abort there may be
     // some): the last copy into each ring slot is waited for.
-    mbar_wait(bar(kBarQ), 0, p.err_flag);
+    if (made_by[2] > 0) mbar_wait(bar(kBarQ), (made_by[2] - 1) & 1, p.err_flag);
     const int made_k = made_by[0], made_v = made_by[1];
     auto was_made = [&](int e) { return (e >> 1) < ((e & 1) ? made_v : made_k); };
     const int end = 2 * max(made_k, made_v);

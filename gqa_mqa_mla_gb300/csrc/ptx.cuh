@@ -275,6 +275,34 @@ DECATTN_DEV uint64_t policy_evict_last() {
   return p;
 }
 
+// ------------------------------------------------------------------ cluster launch control
+
+// Ask for a CTA of this grid that has not started: the 16-byte answer lands at
+// dst (16-byte aligned shared memory) and completes 16 bytes on bar.
+DECATTN_DEV void clc_try_cancel(uint32_t dst, uint32_t bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], "
+      "[%1];" ::"r"(dst),
+      "r"(bar)
+      : "memory");
+}
+
+// The x index of the CTA that an answer handed over (it will not start: its
+// work is this CTA's), or -1 if there was none left.
+DECATTN_DEV int clc_answer(uint32_t src) {
+  int x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 h;\n\t.reg .b32 c, d, e;\n\t"
+      "ld.shared.b128 h, [%1];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+      "mov.b32 %0, -1;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, c, d, e}, h;\n\t}"
+      : "=r"(x)
+      : "r"(src)
+      : "memory");
+  return x;
+}
+
 // ------------------------------------------------------------------ named barriers
 
 DECATTN_DEV void named_bar_sync(int id, int threads) {
