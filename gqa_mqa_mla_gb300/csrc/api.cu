@@ -965,7 +965,6 @@ static int gqa_prefill_impl(const void* q, const void* k_cache, const void* v_ca
         static_cast<char*>(L->workspace) +
         align_up(static_cast<size_t>(tokens) * h_q * ns * d_head * sizeof(float)));
   }
-  if (fp8) return DECATTN_ERR_UNSUPPORTED;
   const bool bf16 = L->dtype == DECATTN_BF16;
   const uint64_t rows_total = static_cast<uint64_t>(L->num_blocks) * L->block_size;
   const uint32_t box_rows = static_cast<uint32_t>(L->block_size < 128 ? L->block_size : 128);
@@ -974,11 +973,15 @@ static int gqa_prefill_impl(const void* q, const void* k_cache, const void* v_ca
   if (!make_map_3d(&tq, q, bf16, kHeadDim, static_cast<uint64_t>(h_q),
                    static_cast<uint64_t>(tokens), 64, static_cast<uint32_t>(group),
                    static_cast<uint32_t>(p.tokens_per_tile)) ||
-      !make_map_2d(&tk, k_cache, bf16, width, rows_total, width * 2, 64, box_rows) ||
-      !make_map_2d(&tv, v_cache, bf16, width, rows_total, width * 2, 64, box_rows))
+      !(fp8 ? make_map_2d_t(&tk, k_cache, CU_TENSOR_MAP_DATA_TYPE_UINT8, width, rows_total, width,
+                            kHeadDim, box_rows) &&
+                  make_map_2d_t(&tv, v_cache, CU_TENSOR_MAP_DATA_TYPE_UINT8, width, rows_total,
+                                width, kHeadDim, box_rows)
+            : make_map_2d(&tk, k_cache, bf16, width, rows_total, width * 2, 64, box_rows) &&
+                  make_map_2d(&tv, v_cache, bf16, width, rows_total, width * 2, 64, box_rows)))
     return DECATTN_ERR_CUDA;
   const cudaError_t e =
-      launch_gqa_prefill(p, tq, tk, tv, bf16, static_cast<cudaStream_t>(L->stream));
+      launch_gqa_prefill(p, tq, tk, tv, bf16, fp8, static_cast<cudaStream_t>(L->stream));
   return e == cudaSuccess ? DECATTN_OK : DECATTN_ERR_CUDA;
 }
 

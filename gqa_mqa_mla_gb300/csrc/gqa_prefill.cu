@@ -31,18 +31,24 @@
 //             so no value of a row is ever exchanged: running maximum, lazy
 //             rescale of O, P, running sum; epilogue;
 //   8, 10     TMA producers of Q and K, of V (they walk the block table and
-//             check the block ids);
+//             check the block ids); 8 is the scheduler too (below);
 //   9         MMA issuer: P_A V, S_A of the next tile, P_B V, S_B of the next
 //             tile: while one tile's softmax runs, the tensor cores work on
 //             the other's products.  MMAs of one thread run in order, so
 //             S_A(j + 1) may overwrite P_A(j) right behind its last reader;
-//   11        scheduler: which rows next (below); TMEM allocation.
+//   11        TMEM allocation.
 //
 // A CTA stays on its SM and goes from piece to piece (two Q tiles of one
 // sequence and KV head): the scheduler takes over CTAs of the grid that have
 // not started (cluster launch control) while the present piece is worked on,
 // so the next one's Q, K and V are on their way, and its first S is computed,
 // during the softmax warps' epilogue.  Pieces come longest first.
+//
+// An 8-bit (e4m3) cache takes the same pipeline on fp16 operands: the ring
+// holds four 16 KB tiles of codes, and warps 10 and 11 convert each K and V
+// tile (exactly) into one of two 16-bit tiles; a bf16 Q is rewritten as fp16 in
+// place (exact within fp16's range).  K's scale joins the score scale, V's the
+// final division.
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -62,7 +68,8 @@ constexpr int kSmemBytes = 1024 + kOffBars + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
 
 constexpr int kThreads = 384;
-constexpr int kWarpLoadK = 8, kWarpMma = 9, kWarpLoadV = 10, kWarpNext = 11;
+// (8-bit cache: warp 8 loads K and V, 10 and 11 convert them.)
+constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpV = 10, kWarpTmem = 11;
 constexpr int kTmemS = 0;                      // S_X: 128 X
 constexpr int kTmemO = 256;                    // O_X: 256 + 128 X
 constexpr float kNegInf = -__builtin_huge_valf();
@@ -77,13 +84,14 @@ enum : int {
   kBarP = kBarS + 2,            // 2: P_X written (128 arrivals)
   kBarO = kBarP + 2,            // 2: O_X complete
   kBarItem = kBarO + 2,         // 2: piece published
-  kBarItemFree = kBarItem + 2,  // 2: piece done by every role (11 warps)
+  kBarItemFree = kBarItem + 2,  // 2: piece done by every other role
   kBarNext = kBarItemFree + 2,  // the launch control's answer
-  kBarAsk = kBarNext + 1,       // the piece's last K copy is on its way
-  kBarDrain = kBarAsk + 1,
+  kBarQ16 = kBarNext + 1,       // 8-bit cache: bf16 Q rewritten as fp16 (64 arrivals)
+  kBarFull16 = kBarQ16 + 1,     // 8-bit cache, K and V: converted (32 arrivals)
+  kBarEmpty16 = kBarFull16 + 2, // 8-bit cache, K and V: 16-bit tile free
+  kBarDrain = kBarEmpty16 + 2,
   kNumBars = kBarDrain + 1
 };
-constexpr int kRoleWarps = 11;  // producers, MMA, softmax
 
 // Behind the barriers, in the same kilobyte.
 constexpr int kOffWords = kOffBars + 256;   // abort, bad, copies made by the producers, TMEM
@@ -234,11 +242,13 @@ __device__ __forceinline__ uint4 staged(const uint8_t* stage, int row, int c) {
   return *reinterpret_cast<const uint4*>(stage + row * 128 + ((c ^ (row & 7)) << 4));
 }
 
-template <bool kBF16>
+// kF8: the cache holds e4m3 codes with per-KV-head scales.
+template <bool kBF16, bool kF8>
 __global__ void __launch_bounds__(kThreads, 1)
     gqa_prefill_kernel(const __grid_constant__ CUtensorMap tm_q,
                        const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const PrefillParams p) {
+  constexpr bool kMmaBF16 = kBF16 && !kF8;  // operand type of both products
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -265,15 +275,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(kBarP + x), kM);
       mbar_init(bar(kBarO + x), 1);
       mbar_init(bar(kBarItem + x), 1);
-      mbar_init(bar(kBarItemFree + x), kRoleWarps);
+      // V producer or the two converters, MMA, softmax
+      mbar_init(bar(kBarItemFree + x), kF8 ? 11 : 10);
+      mbar_init(bar(kBarFull16 + x), 32);
+      mbar_init(bar(kBarEmpty16 + x), 1);
     }
     mbar_init(bar(kBarNext), 1);
-    mbar_init(bar(kBarAsk), 1);
+    mbar_init(bar(kBarQ16), 64);
     mbar_init(bar(kBarDrain), 1);
     for (int k = 0; k < 6; ++k) abort_word[k] = 0;
     fence_barrier_init();
   }
-  if (warp == kWarpNext) {
+  if (warp == kWarpTmem) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
@@ -297,42 +310,96 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp >= 8) {
-    if (warp == kWarpLoadK || warp == kWarpLoadV) {
+    if (warp == kWarpLoad || (!kF8 && warp == kWarpV)) {
       // ---------------- TMA producers: one warp for Q and K, one for V (two
-      // streams of boxes; a warp gets a small box accepted about every 100 cycles)
-      const bool is_v = warp == kWarpLoadV;
-      const CUtensorMap* tm = is_v ? &tm_v : &tm_k;
+      // streams of boxes; a warp gets a small box accepted about every 100
+      // cycles); over an 8-bit cache, with half the boxes, one warp for all.
+      // Warp 8 also is the scheduler: it publishes each piece when it begins
+      // to load it.
+      const bool lead = warp == kWarpLoad;
       const uint64_t keep = policy_evict_last();
-      if (lane == 0) tma_prefetch_desc(tm);
-      if (lane == 0 && !is_v) tma_prefetch_desc(&tm_q);
+      if (lane == 0) {
+        if (lead) tma_prefetch_desc(&tm_q);
+        tma_prefetch_desc(lead ? &tm_k : &tm_v);
+      }
       const int bs = p.block_size, lg = p.log2_block_size;
+      constexpr int kBytes = kF8 ? kTileBytes / 2 : kTileBytes;  // of a tile
       // K(it) is the ring's copy 2 it, V(it) the copy 2 it + 1, counted over
       // all pieces: slot and phase parity of this warp's next one, and the
-      // number it made.
-      int slot = is_v ? 1 : 0, made = 0, q_loads = 0;
+      // numbers it made.
+      int slot = lead ? 0 : 1, made_k = 0, made_v = 0, q_loads = 0;
       uint32_t phase = 0;
+      Cursor c;
+      c.b0 = p.batch - 32;
+      c.before = 0;
+      if (lead) load_cursor(p, c, lane);
+      int x = blockIdx.x, asks = 0;
+      // Takes over a CTA that has not started: its index in x, or -1.  Asked
+      // for once the last copies of a piece are on their way, about two tiles
+      // ahead (at the piece's start it would be kept from CTAs that run out
+      // sooner: 256 pieces of 1 to 64 tiles took 146 us that way, 112 so).  A
+      // grid of one wave has none to hand over.
+      auto claim = [&]() -> bool {
+        x = -1;
+        if (!p.steal) return true;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar(kBarNext), 16);
+          clc_try_cancel(sbase + kOffAnswer, bar(kBarNext));
+        }
+        __syncwarp();
+        const bool there = mbar_wait_or_abort(bar(kBarNext), asks++ & 1, p.err_flag, abort_word);
+        if (!__all_sync(0xffffffffu, there)) return false;
+        x = clc_answer(sbase + kOffAnswer);
+        fence_proxy_async_smem();  // the answer is read before the next one is asked for
+        return true;
+      };
       bool ok = true;
       Item w;
-      for (int k = 0; ok && get_item(k, w); ++k) {
+      for (int k = 0; ok; ++k) {
+        if (lead) {
+          bool some = false;
+          while (ok && x >= 0 && !some) {
+            // grid index: KV heads of a piece, then its splits, then pieces
+            w.j = x % p.h_kv;
+            const int rest = x / p.h_kv;
+            w.split = rest % p.n_split;
+            some = find_item(p, c, rest / p.n_split, w);
+            if (!some) ok = claim();
+          }
+          w.valid = some;
+          if (lane == 0 && ok) {
+            ok = mbar_wait_or_abort(bar(kBarItemFree + (k & 1)), ((k >> 1) & 1) ^ 1, p.err_flag,
+                                    abort_word);
+            if (ok) {
+              bad_word[k & 1] = 0;
+              items[k & 1] = w;
+              mbar_arrive(bar(kBarItem + (k & 1)));
+            }
+          }
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok || !some) break;
+        } else if (!get_item(k, w)) {
+          break;
+        }
         const int n = max(w.n_a, w.n_b);
-        if (n > 0 && !is_v) {
+        if (n > 0 && lead) {
           if (lane == 0) {
             ok = mbar_wait_or_abort(bar(kBarQFree), (q_loads & 1) ^ 1, p.err_flag, abort_word);
             if (ok) {
               const int tiles = w.tok_b > 0 ? 2 : 1;
               mbar_arrive_expect_tx(
                   bar(kBarQ), static_cast<uint32_t>(tiles * 2 * p.tokens_per_tile * G * 128));
-              for (int x = 0; x < tiles; ++x)
+              for (int q = 0; q < tiles; ++q)
                 for (int h = 0; h < 2; ++h)
-                  tma_load_3d(sbase + x * kTileBytes + h * kHalf, &tm_q, 64 * h, w.j * G,
-                              w.q0 + w.i0 + x * p.tokens_per_tile, bar(kBarQ));
+                  tma_load_3d(sbase + q * kTileBytes + h * kHalf, &tm_q, 64 * h, w.j * G,
+                              w.q0 + w.i0 + q * p.tokens_per_tile, bar(kBarQ));
             }
           }
-          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+          ok = __all_sync(0xffffffffu, ok);
           if (ok) made_by[2] = ++q_loads;
         }
         const int32_t* bt = p.block_table + static_cast<size_t>(w.b) * p.max_blocks_per_seq;
-        const int x0 = w.j * kHeadDim;
+        const int x0 = w.j * kHeadDim;  // element (= byte, of an 8-bit cache) column of head j
         const int kb_end = ((w.hi - 1) >> lg) + 1;
         int cache0 = -(1 << 30), my_id = 0;
         for (int it = 0; ok && it < n; ++it) {
@@ -352,30 +419,133 @@ __global__ void __launch_bounds__(kThreads, 1)
             flag_error(p.err_flag, kFlagBadBlock);
           }
           const int row = id * bs + (bs >= kKv ? (t.t0 & (bs - 1)) : 0);
-          const uint32_t bytes = static_cast<uint32_t>(bs >= kKv ? kTileBytes : nblk * bs * 256);
-          if (lane == 0) {
-            ok = mbar_wait_or_abort(bar(kBarEmpty + slot), phase ^ 1u, p.err_flag, abort_word);
-            if (ok) mbar_arrive_expect_tx(bar(kBarFull + slot), bytes);
+          const uint32_t bytes =
+              static_cast<uint32_t>(bs >= kKv ? kBytes : nblk * bs * (kF8 ? 128 : 256));
+#pragma unroll 1
+          for (int kv = lead ? 0 : 1; ok && kv < (kF8 || !lead ? 2 : 1); ++kv) {
+            if (lane == 0) {
+              ok = mbar_wait_or_abort(bar(kBarEmpty + slot), phase ^ 1u, p.err_flag, abort_word);
+              if (ok) mbar_arrive_expect_tx(bar(kBarFull + slot), bytes);
+            }
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            if (lane < nblk) {
+              const CUtensorMap* tm = kv ? &tm_v : &tm_k;
+              const uint32_t dst =
+                  sbase + kOffRing + slot * kBytes + static_cast<uint32_t>(lane * bs * 128);
+              tma_load_2d_hint(dst, tm, x0, row, bar(kBarFull + slot), keep);
+              if (!kF8) tma_load_2d_hint(dst + kHalf, tm, x0 + 64, row, bar(kBarFull + slot), keep);
+            }
+            if (kv)
+              ++made_v;
+            else
+              ++made_k;
+            slot += kF8 ? 1 : 2;
+            if (slot >= kRing) {
+              slot -= kRing;
+              phase ^= 1u;
+            }
           }
-          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        }
+        if (ok && lead) ok = claim();
+        if (ok && !lead) release_item(k);
+      }
+      if (lane == 0) {
+        if (kF8 || lead) made_by[0] = made_k;
+        if (kF8 || !lead) made_by[1] = made_v;
+      }
+      __syncwarp();
+    } else if (kF8 && (warp == kWarpV || warp == kWarpTmem)) {
+      // ---------------- converters (8-bit cache): warp 10 the K tiles, 11 the
+      // V tiles, [128 tokens][128 codes] to [2 halves][128 tokens][128 B], both
+      // with 128-byte swizzle; e4m3 -> fp16 is exact.  V rows outside
+      // [skip, nval) become zeros (their slots may hold NaN codes).  A bf16 Q is
+      // rewritten as fp16 in place, one tile by each.
+      const int kv = warp == kWarpV ? 0 : 1;
+      uint8_t* dst = smem + kOffRing + (2 + kv) * kTileBytes;
+      int slot = kv, q_loads = 0;
+      uint32_t phase = 0, phase16 = 0;
+      bool ok = true;
+      Item w;
+      for (int k = 0; ok && get_item(k, w); ++k) {
+        const int n = max(w.n_a, w.n_b);
+        if (kBF16 && n > 0) {
+          ok = mbar_wait_or_abort(bar(kBarQ), q_loads++ & 1, p.err_flag, abort_word);
+          ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          if (lane < nblk) {
-            const uint32_t dst =
-                sbase + kOffRing + slot * kTileBytes + static_cast<uint32_t>(lane * bs * 128);
-            tma_load_2d_hint(dst, tm, x0, row, bar(kBarFull + slot), keep);
-            tma_load_2d_hint(dst + kHalf, tm, x0 + 64, row, bar(kBarFull + slot), keep);
+          if (kv == 0 || w.tok_b > 0) {
+            uint4* q = reinterpret_cast<uint4*>(smem + kv * kTileBytes);
+#pragma unroll 1
+            for (int e = lane; e < kTileBytes / 16; e += 8 * 32) {
+              uint4 y[8];
+#pragma unroll
+              for (int u = 0; u < 8; ++u) y[u] = q[e + 32 * u];
+#pragma unroll
+              for (int u = 0; u < 8; ++u) {
+                const float2 a = unpack2<true>(y[u].x), b = unpack2<true>(y[u].y),
+                             d = unpack2<true>(y[u].z), f = unpack2<true>(y[u].w);
+                q[e + 32 * u] = make_uint4(pack2<false>(a.x, a.y), pack2<false>(b.x, b.y),
+                                           pack2<false>(d.x, d.y), pack2<false>(f.x, f.y));
+              }
+            }
           }
-          ++made;
+          fence_proxy_async_smem();
+          mbar_arrive(bar(kBarQ16));
+        }
+        for (int it = 0; it < n; ++it) {
+          ok = mbar_wait_or_abort(bar(kBarFull + slot), phase, p.err_flag, abort_word) &&
+               mbar_wait_or_abort(bar(kBarEmpty16 + kv), phase16 ^ 1u, p.err_flag, abort_word);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const Tile t = tile_of(w, it);
+          const uint8_t* src = smem + kOffRing + slot * (kTileBytes / 2);
+          const int lo = kv ? t.skip : 0, hi = kv ? t.nval : kKv;
+          // Lane: 16 codes c = lane % 8 of rows lane / 8, + 4, ...; its two
+          // output pieces are 2 (c % 4) and the next one of half c / 4, the
+          // odd one first for c >= 4 (no bank is hit twice).
+          const int c = lane & 7, odd = c >> 2;
+          const int c0 = 2 * (c & 3);
+          // (Eight rows are read before any is written: a load does not pass a
+          // store to shared memory by itself.)
+#pragma unroll 1
+          for (int r0 = lane >> 3; r0 < kKv; r0 += 32) {
+            uint4 y[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              const int r = r0 + 4 * u;
+              y[u] = *reinterpret_cast<const uint4*>(src + r * 128 + ((c ^ (r & 7)) << 4));
+            }
+            if (lo > 0 || hi < kKv) {
+#pragma unroll
+              for (int u = 0; u < 8; ++u)
+                if (r0 + 4 * u < lo || r0 + 4 * u >= hi) y[u] = make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              const int r = r0 + 4 * u;
+              uint4 a, b;
+              e4m3x4_to_f16x2(y[u].x, a.x, a.y);
+              e4m3x4_to_f16x2(y[u].y, a.z, a.w);
+              e4m3x4_to_f16x2(y[u].z, b.x, b.y);
+              e4m3x4_to_f16x2(y[u].w, b.z, b.w);
+              uint8_t* o = dst + odd * kHalf + r * 128;
+              *reinterpret_cast<uint4*>(o + (((c0 + odd) ^ (r & 7)) << 4)) = odd ? b : a;
+              *reinterpret_cast<uint4*>(o + (((c0 + 1 - odd) ^ (r & 7)) << 4)) = odd ? a : b;
+            }
+          }
+          fence_proxy_async_smem();
+          mbar_arrive(bar(kBarFull16 + kv));
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBarEmpty + slot));
+          phase16 ^= 1u;
           slot += 2;
           if (slot >= kRing) {
             slot -= kRing;
             phase ^= 1u;
           }
         }
-        if (lane == 0 && !is_v) mbar_arrive(bar(kBarAsk));
-        release_item(k);
+        if (ok) release_item(k);
       }
-      if (lane == 0) made_by[is_v ? 1 : 0] = made;
       __syncwarp();
     } else if (warp == kWarpMma) {
       // ---------------- MMA issuer: the whole warp runs the loop, lane 0
@@ -383,8 +553,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t dq = smem_desc_sw128(sbase, 16, 1024);
       const uint64_t dk = smem_desc_sw128(sbase + kOffRing, 16, 1024);
       const uint64_t dv = smem_desc_sw128(sbase + kOffRing, kHalf, 1024);
-      constexpr uint32_t idesc_s = idesc_f16(kBF16, kM, kKv, false, false);
-      constexpr uint32_t idesc_o = idesc_f16(kBF16, kM, kHeadDim, false, true);
+      constexpr uint32_t idesc_s = idesc_f16(kMmaBF16, kM, kKv, false, false);
+      constexpr uint32_t idesc_o = idesc_f16(kMmaBF16, kM, kHeadDim, false, true);
       // All lanes probe; lane 0 waits where that does not succeed at once.
       auto wait = [&](int bi, uint32_t parity) -> bool {
         bool g = mbar_try_wait(bar(bi), parity);
@@ -395,13 +565,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         return g;
       };
+      auto free_bar = [](int s) { return kF8 ? kBarEmpty16 + s - 2 : kBarEmpty + s; };
       // S_X = Q_X K^T: eight k-steps of 16 dims, four per 64-column half.
       // `last`: no other tile reads this K slot after this one; `end`: this is
       // the piece's last S.
       auto issue_s = [&](int x, int s, bool last, bool end) {
         const uint64_t a = dq + static_cast<uint64_t>((x * kTileBytes) >> 4);
         const uint64_t b = dk + static_cast<uint64_t>((s * kTileBytes) >> 4);
-        const uint32_t done = bar(kBarS + x), empty = bar(kBarEmpty + s), q_free = bar(kBarQFree);
+        const uint32_t done = bar(kBarS + x), empty = bar(free_bar(s)), q_free = bar(kBarQFree);
         const uint32_t d = tmem + kTmemS + kKv * x;
         if (elect_one()) {
 #pragma unroll
@@ -421,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t b = dv + static_cast<uint64_t>((s * kTileBytes) >> 4);
         const uint32_t acc0 = first ? 0u : 1u;
         const uint32_t d = tmem + kTmemO + kHeadDim * x, a = tmem + kTmemS + kKv * x;
-        const uint32_t full = bar(kBarO + x), empty = bar(kBarEmpty + s);
+        const uint32_t full = bar(kBarO + x), empty = bar(free_bar(s));
         if (elect_one()) {
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks)
@@ -434,21 +605,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       // Tile B needs at least the tiles that A needs, or there is no tile B.
       // Counters run over all pieces: the ring's slot and phase, Q loads, P.
-      int slot = kRing - 1, q_loads = 0;
+      // 16-bit cache: K and V tiles go round the ring's four slots; 8-bit: the
+      // converted K and V tiles are slots 2 and 3.
+      int slot = kF8 ? 3 : kRing - 1, q_loads = 0;
       uint32_t phase = 1, phase_a = 0, phase_b = 0;
       auto next = [&]() {
         if (++slot == kRing) {
-          slot = 0;
+          slot = kF8 ? 2 : 0;
           phase ^= 1u;
         }
       };
+      auto full = [&](int s) { return kF8 ? kBarFull16 + s - 2 : kBarFull + s; };
       bool ok = true;
       Item w;
       for (int k = 0; ok && get_item(k, w); ++k) {
         const int n = max(w.n_a, w.n_b);
         if (n > 0) {
           next();
-          ok = wait(kBarQ, q_loads++ & 1) && wait(kBarFull + slot, phase);
+          ok = wait(kF8 && kBF16 ? kBarQ16 : kBarQ, q_loads++ & 1) && wait(full(slot), phase);
           if (!ok) break;
           if (w.n_a > 0) issue_s(0, slot, w.n_b == 0, n == 1 && w.n_b == 0);
           if (w.n_b > 0) issue_s(1, slot, true, n == 1);
@@ -456,10 +630,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int it = 0; it < n; ++it) {
           next();
           const int sv = slot;
-          ok = wait(kBarFull + sv, phase);
+          ok = wait(full(sv), phase);
           if (!ok) break;
           const Tile t = tile_of(w, it);
-          if (t.nval < kKv || t.skip > 0) {
+          if (!kF8 && (t.nval < kKv || t.skip > 0)) {
             // V rows outside [skip, nval) become zeros (P is 0 there, but the
             // slots may hold NaN), while the softmax works on this tile.  (All
             // 128 bytes of a row: the swizzle does not matter.)
@@ -478,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // S follow each other without a pause.
           if (it + 1 < n) {
             next();
-            ok = wait(kBarFull + slot, phase);
+            ok = wait(full(slot), phase);
             if (!ok) break;
           }
           if (it < w.n_a) {
@@ -505,66 +679,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait(bar(kBarDrain), 0, p.err_flag);
       }
       __syncwarp();
-    } else if (warp == kWarpNext) {
-      // ---------------- scheduler: publishes the pieces, one ahead of the
-      // one being worked on
-      Cursor c;
-      c.b0 = p.batch - 32;
-      c.before = 0;
-      load_cursor(p, c, lane);
-      int x = blockIdx.x, k = 0, asks = 0;
-      bool ok = true;
-      while (ok) {
-        const bool last = x < 0;
-        Item w;
-        bool some = false;
-        if (!last) {
-          // grid index: KV heads of a piece, then its splits, then pieces
-          w.j = x % p.h_kv;
-          const int rest = x / p.h_kv;
-          w.split = rest % p.n_split;
-          some = find_item(p, c, rest / p.n_split, w);
-        } else {
-          w = Item{};
-        }
-        if (some || last) {
-          if (lane == 0) {
-            ok = mbar_wait_or_abort(bar(kBarItemFree + (k & 1)), ((k >> 1) & 1) ^ 1, p.err_flag,
-                                    abort_word);
-            if (ok) {
-              bad_word[k & 1] = 0;
-              items[k & 1] = w;
-              mbar_arrive(bar(kBarItem + (k & 1)));
-            }
-          }
-          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-          ++k;
-        }
-        if (last || !ok) break;
-        // The next piece is claimed once the last copies of this one are on
-        // their way (about two tiles ahead: claimed at its start, it would be
-        // kept from CTAs that run out sooner; 256 pieces of 1 to 64 tiles took
-        // 146 us that way).  A grid of one wave has none to hand over.
-        x = -1;
-        if (p.steal) {
-          if (some) {
-            if (!mbar_wait_or_abort(bar(kBarAsk), (k - 1) & 1, p.err_flag, abort_word)) ok = false;
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-          }
-          if (lane == 0) {
-            mbar_arrive_expect_tx(bar(kBarNext), 16);
-            clc_try_cancel(sbase + kOffAnswer, bar(kBarNext));
-          }
-          __syncwarp();
-          if (!mbar_wait_or_abort(bar(kBarNext), asks & 1, p.err_flag, abort_word)) ok = false;
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          ++asks;
-          x = clc_answer(sbase + kOffAnswer);
-          fence_proxy_async_smem();  // the answer is read before the next one is asked for
-        }
-      }
     }
   } else {
     // ---------------- softmax: thread = row r of tile x
@@ -577,7 +691,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Row r is head r % G of token r / G: the division for r < 128, G <= 64.
     const uint32_t inv_g = 65536u / static_cast<uint32_t>(G) + 1u;
     const int r_tok = static_cast<int>((static_cast<uint32_t>(r) * inv_g) >> 16);
-    const float scale = p.scale_log2, sign = p.negate ? -1.f : 1.f;
     uint32_t phase_s = 0, phase_o = 0;
     bool ok = true;
     Item w;
@@ -588,10 +701,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Positions of the tile's first and last rows: tiles at or before the
       // first (and inside the last one's window) need no mask.
       const int pos0 = w.len - w.n + i0, pos1 = pos0 + tok - 1;
+      // An 8-bit cache's K scale multiplies every score of KV head j.
+      float scale = p.scale_log2;
+      bool negate = p.negate != 0;
+      if constexpr (kF8) {
+        const float ks = p.k_scale[w.j];
+        negate ^= ks < 0.f;
+        scale = fmaxf(scale * fabsf(ks), 1e-37f);
+      }
+      const float sign = negate ? -1.f : 1.f;
       float m = kNegInf, l = 0.f;
       for (int it = 0; it < nt; ++it) {
         const Tile t = tile_of(w, it);
-        const bool plain = !p.negate && t.skip == 0 && t.nval == kKv && t.t0 + kKv - 1 <= pos0 &&
+        const bool plain = !negate && t.skip == 0 && t.nval == kKv && t.t0 + kKv - 1 <= pos0 &&
                            (p.window <= 0 || t.t0 > pos1 - p.window);
         // Seen columns: [skip, hi), of them those from lo on or below sink (at
         // or before the row's position; in its window or kept first tokens).
@@ -670,7 +792,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float p1 = ex2(fmaf(v[2 * k + 1], scale, neg_m));
             l0 += p0;
             l1 += p1;
-            pk[k] = pack2<kBF16>(p0, p1);
+            pk[k] = pack2<kMmaBF16>(p0, p1);
           }
           tmem_st16(ts + c0 / 2, pk);
         };
@@ -692,7 +814,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const bool bad = w.bad || bad_word[k & 1] != 0;
         const bool live = l > 0.f && !bad;
-        const float inv = live ? 1.f / l : 0.f;
+        // (An 8-bit cache's V scale multiplies the whole row.)
+        const float inv = live ? (kF8 ? p.v_scale[w.j] : 1.f) / l : 0.f;
         // Packed row of the chunk's first row of this tile; this lane stores
         // piece lane % 8 of the warp's rows lane / 8, + 4, ... + 28.
         const int64_t row0 = static_cast<int64_t>(w.q0 + i0) * p.h_q + w.j * G;
@@ -766,7 +889,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (warp == kWarpNext) {
+  if (warp == kWarpTmem) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -831,10 +954,10 @@ __global__ void __launch_bounds__(256) gqa_prefill_combine_kernel(const PrefillP
                          pack2<kBF16>(acc.z * inv, acc.w * inv));
 }
 
-template <bool kBF16>
+template <bool kBF16, bool kF8>
 cudaError_t launch_t(const PrefillParams& p, const CUtensorMap& tq, const CUtensorMap& tk,
                      const CUtensorMap& tv, cudaStream_t stream) {
-  auto kern = gqa_prefill_kernel<kBF16>;
+  auto kern = gqa_prefill_kernel<kBF16, kF8>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        kSmemBytes);
   if (e != cudaSuccess) return e;
@@ -858,9 +981,12 @@ cudaError_t launch_t(const PrefillParams& p, const CUtensorMap& tq, const CUtens
 
 cudaError_t launch_gqa_prefill(const PrefillParams& p, const CUtensorMap& tm_q,
                                const CUtensorMap& tm_k, const CUtensorMap& tm_v, bool bf16,
-                               cudaStream_t stream) {
-  return bf16 ? launch_t<true>(p, tm_q, tm_k, tm_v, stream)
-              : launch_t<false>(p, tm_q, tm_k, tm_v, stream);
+                               bool fp8, cudaStream_t stream) {
+  if (fp8)
+    return bf16 ? launch_t<true, true>(p, tm_q, tm_k, tm_v, stream)
+                : launch_t<false, true>(p, tm_q, tm_k, tm_v, stream);
+  return bf16 ? launch_t<true, false>(p, tm_q, tm_k, tm_v, stream)
+              : launch_t<false, false>(p, tm_q, tm_k, tm_v, stream);
 }
 
 }  // namespace decattn

@@ -204,11 +204,11 @@ int head_gemm_smem_bytes(const HeadGemmParams& p);
 // e4m3: quantise with k_scale / v_scale (bf16 or fp16 input); else a copy.
 cudaError_t launch_append(const AppendParams& p, bool e4m3, bool bf16, cudaStream_t stream);
 // tm_q: 3-D [tokens, h_q, 128] 16-bit, boxes of 64 x group x tokens_per_tile;
-// tm_k, tm_v: 2-D [rows, h_kv * 128], boxes of 64 x min(block_size, 128); all
-// with 128-byte swizzle.
+// tm_k, tm_v: 2-D [rows, h_kv * 128], boxes of 64 x min(block_size, 128), or of
+// 128 codes (fp8); all with 128-byte swizzle.
 cudaError_t launch_gqa_prefill(const PrefillParams& p, const CUtensorMap& tm_q,
                                const CUtensorMap& tm_k, const CUtensorMap& tm_v, bool bf16,
-                               cudaStream_t stream);
+                               bool fp8, cudaStream_t stream);
 cudaError_t launch_paged_plan(const PlanParams& p, cudaStream_t stream);
 cudaError_t launch_rope_append(const RopeParams& p, bool e4m3, bool bf16, cudaStream_t stream);
 cudaError_t launch_mla_combine(const MlaCombineParams& p, bool bf16, cudaStream_t stream);

@@ -352,6 +352,64 @@ def test_prefill_matches_the_plain_form(case, splits):
     _close(out, _plain_prefill(x, window=window, sinks=sinks), dtype)
 
 
+def _fp16_probs(ref, dtype):
+    """An 8-bit cache's probabilities are fp16 for either output type: fewer
+    bits are lost than bf16's bound allows, but their lost small values count."""
+    return ref if dtype == "fp16" else (ref[0], ref[1] + 2.0**-25 * ref[2] / HALF[dtype], *ref[2:])
+
+
+@pytest.mark.parametrize("splits", [1, 0, 3])
+@pytest.mark.parametrize("case", range(len(CHUNKS)))
+def test_prefill_over_an_8_bit_cache(case, splits):
+    q_lens, lens, h_q, h_kv, dtype, bs, window, sinks = CHUNKS[case]
+    for kind in ("bf16", "fp16") if splits == 1 else (dtype,):
+        x = _attn_case(q_lens, lens, h_q, h_kv, kind, bs, 200 + case, fp8=True)
+        out, flag = _run_prefill(x, window=window or None, sinks=sinks, num_splits=splits)
+        assert flag == 0
+        _close(out, _fp16_probs(_plain_prefill(x, window=window, sinks=sinks), kind), kind)
+
+
+def test_prefill_over_an_8_bit_cache_with_odd_scales():
+    """Negative and zero head scales, a negative scale, bad blocks."""
+    x = _attn_case([30, 140], [200, 140], 6, 3, "bf16", 16, 250, fp8=True)
+    x["scales"][0].mul_(torch.tensor([-1.0, 0.0, 1.0], device=DEV))
+    x["scales"][1].mul_(torch.tensor([1.0, -1.0, 0.0], device=DEV))
+    for scale in (0.09, -0.09):
+        for splits in (1, 2):
+            out, flag = _run_prefill(x, scale=scale, num_splits=splits)
+            assert flag == 0
+            _close(out, _fp16_probs(_plain_prefill(x, scale=scale), "bf16"), "bf16")
+    ref = _plain_prefill(x)
+    x["table"][0, 5] = -1
+    out, flag = _run_prefill(x)
+    assert flag == da.FLAG_BAD_BLOCK and bool((out[:30] == 0).all())
+    for a in ref:
+        a[:30] = np.nan
+    _close(out, _fp16_probs(ref, "bf16"), "bf16")
+
+
+def test_prefill_more_pieces_than_sms():
+    """CTAs take over waiting pieces: a ragged batch of many pieces, twice, bit
+    for bit the same (a piece's result does not depend on who computes it)."""
+    rng = np.random.default_rng(9)
+    q_lens = rng.integers(0, 70, 60).tolist()
+    lens = [n + int(rng.integers(0, 200)) for n in q_lens]
+    for fp8 in (False, True):
+        x = _attn_case(q_lens, lens, 16, 4, "fp16", 16, 300, fp8=fp8)
+        a, flag = _run_prefill(x, num_splits=1)
+        b, _ = _run_prefill(x, num_splits=1)
+        assert flag == 0 and torch.equal(a, b)
+        rows = np.sort(rng.choice(int(sum(q_lens)), 40, replace=False))
+        start = np.concatenate([[0], np.cumsum(q_lens)])
+        for i in rows:  # each sampled row on its own, as a chunk of one token
+            s = int(np.searchsorted(start, i, side="right") - 1)
+            n = lens[s] - q_lens[s] + int(i - start[s]) + 1
+            y = dict(x, q=x["q"][i: i + 1], table=x["table"][s: s + 1], start=_i32([0, 1]),
+                     lens=_i32([n]))
+            ref = _plain_prefill(y)
+            _close(a[i: i + 1], ref, "fp16")
+
+
 @pytest.mark.parametrize("scale", [-0.07, 0.0, 1.5])
 def test_prefill_scales(scale):
     """A negative scale, equal weights, and a sharp softmax (rescaling)."""
@@ -548,7 +606,7 @@ def test_sinks_decode_flags_and_no_sinks():
 # ------------------------------------------------------------------ together
 
 
-@pytest.mark.parametrize("fp8", [False])
+@pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("window,sinks", [(0, 0), (40, 4)])
 def test_a_run_of_steps(fp8, window, sinks):
     """Prompts in chunks, drafted tokens taken back, single tokens, a request
