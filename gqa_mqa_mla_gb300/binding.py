@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 from typing import NamedTuple
 
@@ -89,6 +90,8 @@ def library_path() -> str:
 def lib() -> ctypes.CDLL:
     """Load libdecattn.so (built by gqa_mqa_mla_gb300.build.build())."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = _build.LIB
@@ -98,7 +101,7 @@ def lib() -> ctypes.CDLL:
             L = ctypes.CDLL(path)
             P, I, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_float
             S, I64 = ctypes.c_size_t, ctypes.c_int64
-            LP = ctypes.POINTER(Launch)
+            LP = P  # a Launch by reference, or its bytes (_launch_bytes)
             L.gqa_decode.argtypes = [P, P, P, P, P, P, I, I, I, F, LP]
             L.gqa_decode.restype = I
             L.gqa_decode_fp8kv.argtypes = [P, P, P, P, P, P, P, P, I, I, I, F, LP]
@@ -265,6 +268,9 @@ def _ptr(t: torch.Tensor | None) -> int | None:
 
 
 def _check(t: torch.Tensor, name: str, dtype=None, ndim=None):
+    if type(t) is torch.Tensor and (dtype is None or t.dtype is dtype) and \
+            (ndim is None or t.dim() == ndim) and t.is_contiguous():
+        return  # the usual case, in few steps
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if dtype is not None and t.dtype != dtype:
@@ -275,25 +281,31 @@ def _check(t: torch.Tensor, name: str, dtype=None, ndim=None):
         raise ValueError(f"{name} must be contiguous")
 
 
-def _check_out(t: torch.Tensor, name: str, dtype, shape, device):
+def _check_codes(t: torch.Tensor, name: str):
+    """An 8-bit cache: uint8 or float8_e4m3fn (the same bytes)."""
+    _check(t, name, torch.float8_e4m3fn if isinstance(t, torch.Tensor) and
+           t.dtype is torch.float8_e4m3fn else torch.uint8, 4)
+
+
+def _check_out(t: torch.Tensor, name: str, dtype, shape, index):
     _check(t, name, dtype)
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    _check_device(device, (name, t))
+    _check_device(index, (name, t))
 
 
-def _check_device(device, *named):
+def _check_device(index, *named):
     for name, t in named:
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, the call's other tensors on {device}")
+        if t.get_device() != index:
+            raise ValueError(f"{name} is on {t.device}, the call's other tensors on cuda:{index}")
 
 
-def _check_flag(err_flag, device):
+def _check_flag(err_flag, index):
     if err_flag is not None:
         _check(err_flag, "err_flag", torch.int32)
         if err_flag.numel() < 1:
             raise ValueError("err_flag needs one element")
-        _check_device(device, ("err_flag", err_flag))
+        _check_device(index, ("err_flag", err_flag))
 
 
 def _check_sinks(window, sinks):
@@ -303,18 +315,39 @@ def _check_sinks(window, sinks):
         raise ValueError("sinks need a window (without one every token is visible)")
 
 
-def _on_device(device):
-    # The library launches on the current device; its calls run under the
-    # device that holds the tensors.
-    if device.type != "cuda":
+def _device_index(t: torch.Tensor) -> int:
+    index = t.get_device()
+    if index < 0:
         raise ValueError("the tensors must be on a CUDA device")
-    return torch.cuda.device(device)
+    return index
 
 
-def _stream_handle(stream) -> int:
+def _call(fn, index, *args):
+    """fn(*args) with the tensors' device current (the library launches there)."""
+    if torch.cuda.current_device() == index:
+        return fn(*args)
+    with torch.cuda.device(index):
+        return fn(*args)
+
+
+def _stream_handle(stream, index=None) -> int:
     if stream is None:
+        if index is not None:  # the current stream's handle, without a Stream object
+            return torch._C._cuda_getCurrentRawStream(index)
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+# decattn_launch, field by field as Launch has them.
+_LAUNCH = struct.Struct("7i4xPQPP")
+
+
+def _launch_bytes(batch, num_blocks, block_size, max_blocks_per_seq, max_seq_len, num_splits,
+                  dtype, workspace, err_flag, stream) -> bytes:
+    return _LAUNCH.pack(batch, num_blocks, block_size, max_blocks_per_seq, max_seq_len, num_splits,
+                        dtype, 0 if workspace is None else workspace.data_ptr(),
+                        0 if workspace is None else workspace.numel(),
+                        0 if err_flag is None else err_flag.data_ptr(), stream)
 
 
 def make_launch(batch, num_blocks, block_size, max_blocks_per_seq, max_seq_len, num_splits,
@@ -357,22 +390,21 @@ def gqa_decode(q, k_cache, v_cache, block_table, seq_lens, *, scale: float, max_
         ns = gqa_plan_splits(B, h_q, h_kv, max_seq_len, d)
     else:
         ns = gqa_sinks_plan_splits(B, h_q, h_kv, max_seq_len, window, sinks, bs, 2, d)
-    need = gqa_workspace_size(B, h_q, ns, d)
+    need = gqa_workspace_size(B, h_q, ns, d) if ns > 1 else 0
     if need and workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    L = make_launch(B, nb, bs, block_table.shape[1], max_seq_len, ns, _DT[q.dtype],
-                    _ptr(workspace), 0 if workspace is None else workspace.numel(),
-                    _ptr(err_flag), _stream_handle(stream))
+    L = _launch_bytes(B, nb, bs, block_table.shape[1], max_seq_len, ns, _DT[q.dtype], workspace,
+                      err_flag, _stream_handle(stream, torch.cuda.current_device()))
     args = (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
             seq_lens.data_ptr(), out.data_ptr(), h_q, h_kv, d, float(scale))
     if window is None:
-        name, st = "gqa_decode", lib().gqa_decode(*args, ctypes.byref(L))
+        name, st = "gqa_decode", lib().gqa_decode(*args, L)
     elif sinks:
         name = "gqa_decode_sinks"
-        st = lib().gqa_decode_sinks(*args, int(window), int(sinks), ctypes.byref(L))
+        st = lib().gqa_decode_sinks(*args, int(window), int(sinks), L)
     else:
         name = "gqa_decode_window"
-        st = lib().gqa_decode_window(*args, int(window), ctypes.byref(L))
+        st = lib().gqa_decode_window(*args, int(window), L)
     if st != DECATTN_OK:
         raise DecAttnError(name, st)
     return out
@@ -403,12 +435,8 @@ def gqa_decode_fp8kv(q, k_codes, v_codes, k_scale, v_scale, block_table, seq_len
     _check(q, "q", ndim=3)
     if q.dtype not in _DT:
         raise TypeError("q must be float16 or bfloat16")
-    if k_codes.dtype == torch.float8_e4m3fn:
-        k_codes = k_codes.view(torch.uint8)
-    if v_codes.dtype == torch.float8_e4m3fn:
-        v_codes = v_codes.view(torch.uint8)
-    _check(k_codes, "k_codes", torch.uint8, 4)
-    _check(v_codes, "v_codes", torch.uint8, 4)
+    _check_codes(k_codes, "k_codes")
+    _check_codes(v_codes, "v_codes")
     _check(k_scale, "k_scale", torch.float32, 1)
     _check(v_scale, "v_scale", torch.float32, 1)
     _check(block_table, "block_table", torch.int32, 2)
@@ -429,23 +457,22 @@ def gqa_decode_fp8kv(q, k_codes, v_codes, k_scale, v_scale, block_table, seq_len
         ns = gqa_fp8_plan_splits(B, h_q, h_kv, max_seq_len, d)
     else:
         ns = gqa_sinks_plan_splits(B, h_q, h_kv, max_seq_len, window, sinks, bs, 1, d)
-    need = gqa_workspace_size(B, h_q, ns, d)
+    need = gqa_workspace_size(B, h_q, ns, d) if ns > 1 else 0
     if need and workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    L = make_launch(B, nb, bs, block_table.shape[1], max_seq_len, ns, _DT[q.dtype],
-                    _ptr(workspace), 0 if workspace is None else workspace.numel(),
-                    _ptr(err_flag), _stream_handle(stream))
+    L = _launch_bytes(B, nb, bs, block_table.shape[1], max_seq_len, ns, _DT[q.dtype], workspace,
+                      err_flag, _stream_handle(stream, torch.cuda.current_device()))
     args = (q.data_ptr(), k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(),
             v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(),
             h_q, h_kv, d, float(scale))
     if window is None:
-        name, st = "gqa_decode_fp8kv", lib().gqa_decode_fp8kv(*args, ctypes.byref(L))
+        name, st = "gqa_decode_fp8kv", lib().gqa_decode_fp8kv(*args, L)
     elif sinks:
         name = "gqa_decode_fp8kv_sinks"
-        st = lib().gqa_decode_fp8kv_sinks(*args, int(window), int(sinks), ctypes.byref(L))
+        st = lib().gqa_decode_fp8kv_sinks(*args, int(window), int(sinks), L)
     else:
         name = "gqa_decode_fp8kv_window"
-        st = lib().gqa_decode_fp8kv_window(*args, int(window), ctypes.byref(L))
+        st = lib().gqa_decode_fp8kv_window(*args, int(window), L)
     if st != DECATTN_OK:
         raise DecAttnError(name, st)
     return out
@@ -539,39 +566,44 @@ def paged_plan(cached_lens, new_lens, block_table, free_blocks, free_count, *, b
     cached_lens (in place).  Rows past the step's last token get slot and
     position -1.
     """
-    for t, n in ((cached_lens, "cached_lens"), (new_lens, "new_lens"),
-                 (free_blocks, "free_blocks"), (free_count, "free_count")):
-        _check(t, n, torch.int32, 1)
+    _check(cached_lens, "cached_lens", torch.int32, 1)
+    _check(new_lens, "new_lens", torch.int32, 1)
     _check(block_table, "block_table", torch.int32, 2)
-    B, dev = cached_lens.shape[0], cached_lens.device
-    if new_lens.shape != (B,) or block_table.shape[0] != B or free_count.numel() != 1:
+    _check(free_blocks, "free_blocks", torch.int32, 1)
+    _check(free_count, "free_count", torch.int32, 1)
+    B, index = cached_lens.shape[0], _device_index(cached_lens)
+    if new_lens.shape[0] != B or block_table.shape[0] != B or free_count.shape[0] != 1:
         raise ValueError("paged_plan: shape mismatch")
     if max_tokens < 0:
         raise ValueError("max_tokens must not be negative")
-    _check_device(dev, ("new_lens", new_lens), ("block_table", block_table),
+    _check_device(index, ("new_lens", new_lens), ("block_table", block_table),
                   ("free_blocks", free_blocks), ("free_count", free_count))
-    _check_flag(err_flag, dev)
-
-    def given(t, name, n):
+    _check_flag(err_flag, index)
+    outs = []
+    buf, at = None, 0  # what is not given is cut from one allocation
+    for t, name, n in ((seq_lens, "seq_lens", B), (q_start, "q_start", B + 1),
+                       (slots, "slots", max_tokens), (positions, "positions", max_tokens),
+                       (free_count_out, "free_count_out", 1)):
         if t is None:
-            return torch.empty(n, dtype=torch.int32, device=dev)
-        _check_out(t, name, torch.int32, (n,), dev)
-        return t
-
-    plan = PagedPlan(given(seq_lens, "seq_lens", B), given(q_start, "q_start", B + 1),
-                     given(slots, "slots", max_tokens), given(positions, "positions", max_tokens),
-                     given(free_count_out, "free_count_out", 1))
-    with _on_device(dev):
-        L = make_launch(B, free_blocks.shape[0], block_size, block_table.shape[1], 0, 1,
-                        DECATTN_FP16, None, 0, _ptr(err_flag), _stream_handle(stream))
-        st = lib().paged_plan(cached_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(),
-                              free_blocks.data_ptr(), free_count.data_ptr(),
-                              plan.free_count.data_ptr(), plan.seq_lens.data_ptr(),
-                              plan.q_start.data_ptr(), plan.slots.data_ptr(),
-                              plan.positions.data_ptr(), max_tokens, ctypes.byref(L))
+            if buf is None:
+                buf = torch.empty(2 * (B + max_tokens + 1), dtype=torch.int32,
+                                  device=cached_lens.device)
+            t = buf[at: at + n]
+            at += n
+        else:
+            _check(t, name, torch.int32, 1)
+            if t.shape[0] != n or t.get_device() != index:
+                raise ValueError(f"{name}: expected [{n}] on cuda:{index}")
+        outs.append(t)
+    L = _launch_bytes(B, free_blocks.shape[0], block_size, block_table.shape[1], 0, 1,
+                      DECATTN_FP16, None, err_flag, _stream_handle(stream, index))
+    st = _call(lib().paged_plan, index, cached_lens.data_ptr(), new_lens.data_ptr(),
+               block_table.data_ptr(), free_blocks.data_ptr(), free_count.data_ptr(),
+               outs[4].data_ptr(), outs[0].data_ptr(), outs[1].data_ptr(), outs[2].data_ptr(),
+               outs[3].data_ptr(), max_tokens, L)
     if st != DECATTN_OK:
         raise DecAttnError("paged_plan", st)
-    return plan
+    return PagedPlan(*outs)
 
 
 def rope_table(inv_freq, *, sections=None, interleaved: bool = False, device=None) -> RopeTable:
@@ -598,63 +630,67 @@ def rope_table(inv_freq, *, sections=None, interleaved: bool = False, device=Non
 
 def _packed_rows(t, name, dtype):
     """A [tokens, heads, 128] tensor whose heads are contiguous within a token
-    (a part of a wider projection's output will do): its token stride."""
+    (a part of a wider projection's output will do): its shape and token stride."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dim() != 3:
         raise ValueError(f"{name}: expected 3 dims, got shape {tuple(t.shape)}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    T, h, d = t.shape
-    if t.numel() and ((d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d)):
+    (T, h, d), (st, sh, sd) = t.shape, t.stride()
+    if T * h * d and ((d > 1 and sd != 1) or (h > 1 and sh != d)):
         raise ValueError(f"{name}: a token's heads must be contiguous")
-    return t.stride(0) if T > 1 else h * d
+    return T, h, d, st if T > 1 else h * d
 
 
 def _rope_append(fp8, q, k_new, v_new, scales, positions, rope, slots, k_cache, v_cache, q_out,
                  err_flag, stream):
     name = "gqa_rope_append_fp8kv" if fp8 else "gqa_rope_append"
-    qs = _packed_rows(q, "q", None)
-    if q.dtype not in _DT:
+    T, h_q, d, qs = _packed_rows(q, "q", None)
+    dtype = q.dtype
+    if dtype not in _DT:
         raise TypeError("q must be float16 or bfloat16")
-    ks, vs = _packed_rows(k_new, "k_new", q.dtype), _packed_rows(v_new, "v_new", q.dtype)
+    Tk, h_kv, dk, ks = _packed_rows(k_new, "k_new", dtype)
+    Tv, hv, dv, vs = _packed_rows(v_new, "v_new", dtype)
     if not isinstance(rope, RopeTable):
         raise TypeError("rope must come from rope_table")
     _check(positions, "positions", torch.int32)
-    if positions.dim() == 1:
-        positions = positions[None]
     _check(slots, "slots", torch.int32, 1)
-    cache_dtype = torch.uint8 if fp8 else q.dtype
-    _check(k_cache, "k_cache", cache_dtype, 4)
-    _check(v_cache, "v_cache", cache_dtype, 4)
-    T, h_q, d = q.shape
-    h_kv = k_new.shape[1]
-    if k_new.shape != (T, h_kv, d) or v_new.shape != k_new.shape or \
-            k_cache.shape[2:] != (h_kv, d) or v_cache.shape != k_cache.shape or \
-            slots.shape != (T,):
+    if fp8:
+        _check_codes(k_cache, "k_codes")
+        _check_codes(v_cache, "v_codes")
+    else:
+        _check(k_cache, "k_cache", dtype, 4)
+        _check(v_cache, "v_cache", dtype, 4)
+    nb, bs, hc, dc = k_cache.shape
+    if Tk != T or dk != d or Tv != T or hv != h_kv or dv != d or hc != h_kv or dc != d or \
+            v_cache.shape != k_cache.shape or slots.shape[0] != T:
         raise ValueError(f"{name}: shape mismatch")
-    if positions.shape != (rope.n_axes, T):
+    if positions.shape != (rope.n_axes, T) and not (rope.n_axes == 1 and positions.shape == (T,)):
         raise ValueError(f"positions must be [{rope.n_axes}, {T}]")
+    index = _device_index(q)
     for n, s in (("k_scale", scales[0]), ("v_scale", scales[1])) if fp8 else ():
         _check(s, n, torch.float32, 1)
-        if s.shape != (h_kv,):
+        if s.shape[0] != h_kv:
             raise ValueError(f"{n} must be [h_kv]")
-        _check_device(q.device, (n, s))
-    _check_device(q.device, ("k_new", k_new), ("v_new", v_new), ("positions", positions),
+        _check_device(index, (n, s))
+    _check_device(index, ("k_new", k_new), ("v_new", v_new), ("positions", positions),
                   ("slots", slots), ("k_cache", k_cache), ("v_cache", v_cache))
-    _check_flag(err_flag, q.device)
+    _check_flag(err_flag, index)
     if q_out is None:
-        q_out = torch.empty((T, h_q, d), dtype=q.dtype, device=q.device)
+        q_out = torch.empty((T, h_q, d), dtype=dtype, device=q.device)
     else:
-        _check_out(q_out, "q_out", q.dtype, (T, h_q, d), q.device)
-    with _on_device(q.device):
-        L = make_launch(1, k_cache.shape[0], k_cache.shape[1], 1, 0, 1, _DT[q.dtype], None, 0,
-                        _ptr(err_flag), _stream_handle(stream))
-        st = getattr(lib(), name)(
-            q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), qs, ks, vs,
-            *([s.data_ptr() for s in scales] if fp8 else []), positions.data_ptr(),
-            ctypes.byref(rope), slots.data_ptr(), q_out.data_ptr(), k_cache.data_ptr(),
-            v_cache.data_ptr(), T, h_q, h_kv, d, ctypes.byref(L))
+        _check_out(q_out, "q_out", dtype, (T, h_q, d), index)
+    L = _launch_bytes(1, nb, bs, 1, 0, 1, _DT[dtype], None, err_flag,
+                      _stream_handle(stream, index))
+    tail = (positions.data_ptr(), ctypes.byref(rope), slots.data_ptr(), q_out.data_ptr(),
+            k_cache.data_ptr(), v_cache.data_ptr(), T, h_q, h_kv, d, L)
+    head = (q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), qs, ks, vs)
+    if fp8:
+        st = _call(lib().gqa_rope_append_fp8kv, index, *head, scales[0].data_ptr(),
+                   scales[1].data_ptr(), *tail)
+    else:
+        st = _call(lib().gqa_rope_append, index, *head, *tail)
     if st != DECATTN_OK:
         raise DecAttnError(name, st)
     return q_out
@@ -679,12 +715,7 @@ def gqa_rope_append_fp8kv(q, k_new, v_new, k_scale, v_scale, positions, rope, sl
     """gqa_rope_append into an 8-bit e4m3 cache (uint8 or float8_e4m3fn) with
     one scale per KV head."""
     return _rope_append(True, q, k_new, v_new, (k_scale, v_scale), positions, rope, slots,
-                        _codes(k_codes), _codes(v_codes), q_out, err_flag, stream)
-
-
-def _codes(t):
-    return t.view(torch.uint8) if isinstance(t, torch.Tensor) and \
-        t.dtype == torch.float8_e4m3fn else t
+                        k_codes, v_codes, q_out, err_flag, stream)
 
 
 def _prefill(fp8, q, k_cache, v_cache, scales, block_table, q_start, seq_lens, scale, max_q_len,
@@ -693,9 +724,12 @@ def _prefill(fp8, q, k_cache, v_cache, scales, block_table, q_start, seq_lens, s
     _check(q, "q", ndim=3)
     if q.dtype not in _DT:
         raise TypeError("q must be float16 or bfloat16")
-    cache_dtype = torch.uint8 if fp8 else q.dtype
-    _check(k_cache, "k_cache", cache_dtype, 4)
-    _check(v_cache, "v_cache", cache_dtype, 4)
+    if fp8:
+        _check_codes(k_cache, "k_codes")
+        _check_codes(v_cache, "v_codes")
+    else:
+        _check(k_cache, "k_cache", q.dtype, 4)
+        _check(v_cache, "v_cache", q.dtype, 4)
     _check(block_table, "block_table", torch.int32, 2)
     _check(q_start, "q_start", torch.int32, 1)
     _check(seq_lens, "seq_lens", torch.int32, 1)
@@ -711,37 +745,39 @@ def _prefill(fp8, q, k_cache, v_cache, scales, block_table, q_start, seq_lens, s
         raise ValueError("block_table must be [B, max_blocks] and q_start [B + 1]")
     if h_kv < 1 or h_q % h_kv != 0:
         raise ValueError(f"h_q={h_q} is not a multiple of h_kv={h_kv}")
+    index = _device_index(q)
     for n, s in (("k_scale", scales[0]), ("v_scale", scales[1])) if fp8 else ():
         _check(s, n, torch.float32, 1)
-        if s.shape != (h_kv,):
+        if s.shape[0] != h_kv:
             raise ValueError(f"{n} must be [h_kv]")
-        _check_device(q.device, (n, s))
-    _check_device(q.device, ("k_cache", k_cache), ("v_cache", v_cache),
+        _check_device(index, (n, s))
+    _check_device(index, ("k_cache", k_cache), ("v_cache", v_cache),
                   ("block_table", block_table), ("q_start", q_start), ("seq_lens", seq_lens))
-    _check_flag(err_flag, q.device)
+    _check_flag(err_flag, index)
     if out is None:
         out = torch.empty_like(q)
     else:
-        _check_out(out, "out", q.dtype, q.shape, q.device)
-    with _on_device(q.device):
-        ns = num_splits
-        if ns == 0:
-            ns = gqa_prefill_plan_splits(B, T, max_q_len, h_q, h_kv, max_seq_len, window or 0,
-                                         sinks, d)
-        need = gqa_prefill_workspace_size(T, h_q, ns, d) if T else 0
-        if workspace is not None:
-            _check(workspace, "workspace", torch.uint8)
-            _check_device(q.device, ("workspace", workspace))
-        elif need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        L = make_launch(B, nb, bs, block_table.shape[1], max_seq_len, ns, _DT[q.dtype],
-                        _ptr(workspace), 0 if workspace is None else workspace.numel(),
-                        _ptr(err_flag), _stream_handle(stream))
-        st = getattr(lib(), name)(
-            q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-            *([s.data_ptr() for s in scales] if fp8 else []), block_table.data_ptr(),
-            q_start.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), T, max_q_len, h_q, h_kv, d,
-            float(scale), window or 0, sinks, ctypes.byref(L))
+        _check_out(out, "out", q.dtype, q.shape, index)
+    ns = num_splits
+    if ns == 0:
+        ns = _call(gqa_prefill_plan_splits, index, B, T, max_q_len, h_q, h_kv, max_seq_len,
+                   window or 0, sinks, d)
+    need = gqa_prefill_workspace_size(T, h_q, ns, d) if T and ns > 1 else 0
+    if workspace is not None:
+        _check(workspace, "workspace", torch.uint8)
+        _check_device(index, ("workspace", workspace))
+    elif need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    L = _launch_bytes(B, nb, bs, block_table.shape[1], max_seq_len, ns, _DT[q.dtype], workspace,
+                      err_flag, _stream_handle(stream, index))
+    head = (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr())
+    tail = (block_table.data_ptr(), q_start.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), T,
+            max_q_len, h_q, h_kv, d, float(scale), window or 0, sinks, L)
+    if fp8:
+        st = _call(lib().gqa_prefill_fp8kv, index, *head, scales[0].data_ptr(),
+                   scales[1].data_ptr(), *tail)
+    else:
+        st = _call(lib().gqa_prefill, index, *head, *tail)
     if st != DECATTN_OK:
         raise DecAttnError(name, st)
     return out
@@ -771,7 +807,7 @@ def gqa_prefill_fp8kv(q, k_codes, v_codes, k_scale, v_scale, block_table, q_star
                       err_flag=None, stream=None):
     """gqa_prefill over an 8-bit e4m3 cache (uint8 or float8_e4m3fn) with one
     scale per KV head."""
-    return _prefill(True, q, _codes(k_codes), _codes(v_codes), (k_scale, v_scale), block_table,
+    return _prefill(True, q, k_codes, v_codes, (k_scale, v_scale), block_table,
                     q_start, seq_lens, scale, max_q_len, max_seq_len, window, sinks, out,
                     num_splits, workspace, err_flag, stream)
 

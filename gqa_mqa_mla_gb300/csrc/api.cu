@@ -732,6 +732,7 @@ int paged_plan(const int32_t* cached_lens, const int32_t* new_lens, int32_t* blo
   p.err_flag = L->err_flag;
   p.batch = L->batch;
   p.max_tokens = max_tokens;
+  p.in_place = seq_lens == cached_lens || free_count_out == free_count;
   p.block_size = L->block_size;
   p.log2_block_size = ilog2(L->block_size);
   p.num_blocks = L->num_blocks;
@@ -917,10 +918,10 @@ static int gqa_prefill_impl(const void* q, const void* k_cache, const void* v_ca
   if (!q_start || !aligned(q_start, 4)) return DECATTN_ERR_INVALID_ARG;
   if (tokens == 0) return DECATTN_OK;
   const int group = h_q / h_kv;
-  const int sms = device_sm_count();
-  if (sms <= 0) return DECATTN_ERR_CUDA;
-  int ns = L->num_splits;
+  int sms = 0, ns = L->num_splits;
   if (ns == 0) {
+    sms = device_sm_count();
+    if (sms <= 0) return DECATTN_ERR_CUDA;
     ns = plan_prefill_splits(L->batch, tokens, max_q_len, h_q, h_kv, L->max_seq_len, window,
                              sinks, sms);
   }
@@ -951,7 +952,6 @@ static int gqa_prefill_impl(const void* q, const void* k_cache, const void* v_ca
   p.tokens_per_tile = 128 / group;
   p.n_items = static_cast<int>(items);
   p.n_split = ns;
-  p.steal = items * h_kv * ns > sms ? 1 : 0;
   p.negate = scale < 0.f ? 1 : 0;
   // A zero scale (equal weights) is a scale that no score can feel: the
   // kernel's masked scores are -inf, and -inf times 0 would be NaN.
@@ -965,6 +965,9 @@ static int gqa_prefill_impl(const void* q, const void* k_cache, const void* v_ca
         static_cast<char*>(L->workspace) +
         align_up(static_cast<size_t>(tokens) * h_q * ns * d_head * sizeof(float)));
   }
+  if (sms == 0) sms = device_sm_count();
+  if (sms <= 0) return DECATTN_ERR_CUDA;
+  p.steal = items * h_kv * ns > sms ? 1 : 0;
   const bool bf16 = L->dtype == DECATTN_BF16;
   const uint64_t rows_total = static_cast<uint64_t>(L->num_blocks) * L->block_size;
   const uint32_t box_rows = static_cast<uint32_t>(L->block_size < 128 ? L->block_size : 128);

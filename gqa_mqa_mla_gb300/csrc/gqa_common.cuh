@@ -30,16 +30,21 @@ template <bool kSinks>
 struct GqaSpan {
   int w0, t_begin, t_end, bad;
   int n_tiles;
-  int tile0, sink_tiles, s_end, base, seq_len;  // kSinks only
+  // kSinks only, in tokens counted from this split's first tile: one past the
+  // last sink, the window's start and end; and the first token of the split's
+  // tiles if they are sinks' (sink0) or the window's (win0).  (Few values: at
+  // 175 registers instead of 168 the 16-bit kernel ran one CTA per SM, not
+  // two, 211 us instead of 165 at 64 x 4100 tokens of 8 KV heads.)
+  int s_rel, w_rel, e_rel, sink0, win0;
 
   DECATTN_DEV GqaTile tile(int it) const {
     GqaTile r;
     if constexpr (kSinks) {
-      const int vt = tile0 + it;
-      const bool sink = vt < sink_tiles;
-      r.t0 = sink ? vt * kTile : base + (vt - sink_tiles) * kTile;
-      r.skip = sink ? 0 : max(0, w0 - r.t0);
-      r.nval = min(kTile, (sink ? s_end : seq_len) - r.t0);
+      const int o = it * kTile;
+      const bool sink = o < s_rel;
+      r.t0 = (sink ? sink0 : win0) + o;
+      r.skip = sink ? 0 : max(0, w_rel - o);
+      r.nval = min(kTile, (sink ? s_rel : e_rel) - o);
     } else {
       r.t0 = t_begin + it * kTile;
       r.skip = max(0, w0 - r.t0);
@@ -49,7 +54,7 @@ struct GqaSpan {
   }
   DECATTN_DEV bool empty() const { return kSinks ? n_tiles <= 0 : t_end <= t_begin; }
   // One past the last token whose block may be read.
-  DECATTN_DEV int end() const { return kSinks ? seq_len : t_end; }
+  DECATTN_DEV int end() const { return kSinks ? win0 + e_rel : t_end; }
 };
 
 // 1 (and the flag) if a block id of tokens [t0, t1) is out of range.
@@ -80,24 +85,26 @@ DECATTN_DEV GqaSpan<kSinks> gqa_span(const GqaParams& p, int split, int j, int b
   if (kSinks && p.sinks >= r.w0) r.w0 = 0;
   const int base = r.w0 & ~((p.block_size < kTile ? p.block_size : kTile) - 1);
   if constexpr (kSinks) {
-    r.seq_len = seq_len;
-    r.base = base;
-    r.s_end = min(p.sinks, r.w0);
-    r.sink_tiles = (r.s_end + kTile - 1) / kTile;
     r.t_begin = r.t_end = 0;
     r.n_tiles = 0;
     if (r.bad) return r;
-    const int total = r.sink_tiles + (seq_len - base + kTile - 1) / kTile;
+    const int s_end = min(p.sinks, r.w0);
+    const int sink_tiles = (s_end + kTile - 1) / kTile;
+    const int total = sink_tiles + (seq_len - base + kTile - 1) / kTile;
     const int per = p.tokens_per_split / kTile;
-    r.tile0 = min(split * per, total);
-    r.n_tiles = min(per, total - r.tile0);
+    const int tile0 = min(split * per, total);
+    r.n_tiles = min(per, total - tile0);
     if (r.n_tiles <= 0) return r;
-    const int end = r.tile0 + r.n_tiles;
-    if (r.tile0 < r.sink_tiles)
-      r.bad |= gqa_bad_blocks(p, b, r.tile0 * kTile, min(r.s_end, end * kTile));
-    if (end > r.sink_tiles)
-      r.bad |= gqa_bad_blocks(p, b, base + max(0, r.tile0 - r.sink_tiles) * kTile,
-                              min(seq_len, base + (end - r.sink_tiles) * kTile));
+    r.sink0 = tile0 * kTile;
+    r.win0 = base + (tile0 - sink_tiles) * kTile;
+    r.s_rel = s_end - r.sink0;
+    r.w_rel = r.w0 - r.win0;
+    r.e_rel = seq_len - r.win0;
+    const int end = tile0 + r.n_tiles;
+    if (tile0 < sink_tiles) r.bad |= gqa_bad_blocks(p, b, r.sink0, min(s_end, end * kTile));
+    if (end > sink_tiles)
+      r.bad |= gqa_bad_blocks(p, b, base + max(0, tile0 - sink_tiles) * kTile,
+                              min(seq_len, base + (end - sink_tiles) * kTile));
   } else {
     r.t_begin = base + split * p.tokens_per_split;
     r.t_end = r.bad ? r.t_begin : min(seq_len, r.t_begin + p.tokens_per_split);

@@ -100,6 +100,7 @@ struct PlanParams {
   int32_t* positions;         // [max_tokens]
   int* err_flag;
   int batch, max_tokens;
+  int in_place;               // seq_lens is cached_lens, or free_count_out free_count
   int block_size, log2_block_size, num_blocks, max_blocks_per_seq;
 };
 

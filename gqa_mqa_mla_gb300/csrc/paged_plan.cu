@@ -11,11 +11,15 @@
 //
 // Bound by latency: a step moves a few KB to a few hundred KB, so the cost
 // is the launch and the chain load lengths -> scan -> load ids -> store.  One
-// cluster does it all in one launch, with no workspace: every CTA repeats the
-// scan over all requests (a few KB, read from L2), returned blocks are pushed,
-// one cluster barrier orders them (and every read of the lengths and of the
-// free count, which the outputs may alias) before the writes, and the rest is
-// shared out by thread.
+// launch does it all, with no workspace: every CTA repeats the scan over all
+// requests (a few KB, read from L2) and the rest is shared out by thread.
+// A block that is given back and taken again in the same step is looked up in
+// the row that gives it back, not on the stack, so no write is read again and
+// the CTAs need not wait for one another -- except where the lengths or the
+// free count are updated in place: then one CTA does a small step, and a
+// cluster of eight, behind a barrier, a larger one.
+#include <algorithm>
+
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -133,21 +137,28 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const PlanParams p
   if (gtid == 0 && no_room) flag_error(p.err_flag, kFlagNoRoom);
 
   // Returned blocks go onto the stack in request order, each request's in
-  // ascending order.
+  // ascending order: the i-th of them.
   auto row_of = [&](int b) { return p.block_table + static_cast<int64_t>(b) * p.max_blocks_per_seq; };
+  auto returned = [&](int i) {
+    const int b = owner(lost, B, i);
+    const int now = (cached[b] + moved[b] + S - 1) >> lg;
+    return row_of(b)[now + i - lost[b]];
+  };
   if (trims) {
     for (int i = gtid; i < R; i += gsize) {
-      const int b = owner(lost, B, i);
-      const int now = (cached[b] + moved[b] + S - 1) >> lg;
-      const int id = row_of(b)[now + i - lost[b]];
+      const int id = returned(i);
       if (id < 0 || id >= p.num_blocks) flag_error(p.err_flag, kFlagBadBlock);
       p.free_blocks[F + i] = id;
     }
   }
-  cluster_sync();
+  // In place: every CTA has read the lengths and the free count behind this.
+  if (p.in_place) cluster_sync();
 
   // The k-th needed block is the k-th from the top of the stack.
-  auto fresh = [&](int k) { return __ldcg(p.free_blocks + (top - 1 - k)); };
+  auto fresh = [&](int k) {
+    const int at = top - 1 - k;
+    return at >= F ? returned(at - F) : p.free_blocks[at];
+  };
   if (grows) {
     for (int k = gtid; k < A; k += gsize) {
       const int b = owner(need, B, k);
@@ -188,20 +199,22 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const PlanParams p
 
 cudaError_t launch_paged_plan(const PlanParams& p, cudaStream_t stream) {
   const int smem = (5 * p.batch + 3) * static_cast<int>(sizeof(int));
-  cudaError_t e = cudaFuncSetAttribute(paged_plan_kernel,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = cudaSuccess;
+  if (smem > 48 * 1024)
+    e = cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
+  // A token a thread, up to a CTA on every other SM (more only repeat the
+  // scan); a cluster's CTAs where the step is updated in place.
+  const int by_rows = (p.max_tokens + kThreads - 1) / kThreads;
+  const int ctas = p.in_place ? (p.max_tokens <= 2048 ? 1 : 8) : std::max(1, std::min(by_rows, 64));
   cudaLaunchConfig_t cfg = {};
-  // A step of single tokens is one CTA's work; more rows are shared by a
-  // cluster of eight (the largest portable one).
-  const unsigned ctas = p.max_tokens <= 2048 ? 1 : 8;
-  cfg.gridDim = dim3(ctas);
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.x = p.in_place ? static_cast<unsigned>(ctas) : 1;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;

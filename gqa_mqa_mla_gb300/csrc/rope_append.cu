@@ -12,10 +12,11 @@
 // 2^-25 of a half turn.  Products are in fp32, each result rounded once.
 //
 // Bound by HBM: q, k and v are read once, q_out and the cache rows written
-// once.  One CTA takes one token: 64 threads make the token's sines and
-// cosines, shared by all heads through shared memory; a head's 128 values
-// are eight threads' work, two 16-byte pieces each, so that a thread holds
-// both halves of its eight pairs.
+// once.  A CTA takes one token (few tokens: latency) up to four: its
+// threads make the tokens' sines and cosines, which the heads share through
+// shared memory; a head's 128 values are eight threads' work, two 16-byte
+// pieces each, so that a thread holds both halves of its eight pairs, and the
+// next head's pieces are on their way while one is turned.
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -24,7 +25,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kLanes = 8;                       // threads per head
-constexpr int kHeads = kThreads / kLanes;       // heads per pass of a CTA
+constexpr int kHeads = kThreads / kLanes;       // heads at a time
 
 template <bool kBF16>
 __device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
@@ -53,80 +54,100 @@ __device__ __forceinline__ uint2 quant8(const float (&x)[8], float s) {
 }
 
 // kNext: pairs of neighbours (2i, 2i + 1); else pairs half the rotated width apart.
-template <bool kBF16, bool kF8, bool kNext>
+template <bool kBF16, bool kF8, bool kNext, int kTok>
 __global__ void __launch_bounds__(kThreads) rope_append_kernel(const __grid_constant__ RopeParams p) {
-  __shared__ float2 cs[64];
-  const int64_t t = blockIdx.x;
+  __shared__ float4 cs[kTok][32];  // (cos, sin) of pairs 2 i and 2 i + 1
+  __shared__ int slots[kTok];
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTok;
+  const int n_tok = min(kTok, static_cast<int>(p.tokens - t0));
   const int pairs = p.rope.rot_dim >> 1;
-  if (threadIdx.x < pairs) {
-    const int i = threadIdx.x;
-    const int pos = p.positions[p.rope.axis[i] * static_cast<int64_t>(p.tokens) + t];
-    const uint64_t phase = static_cast<uint64_t>(static_cast<int64_t>(pos)) * p.rope.turns[i];
-    const int half_turns = static_cast<int>(static_cast<uint32_t>((phase + 0x80000000ull) >> 32));
-    float s, c;
-    sincospif(static_cast<float>(half_turns) * 4.656612873077393e-10f, &s, &c);  // 2^-31
-    cs[i] = make_float2(c, s);
-  }
-  const int slot = p.slots[t];
-  const bool in_cache = slot >= 0 && slot < p.num_slots;
-  if (threadIdx.x == 0 && slot >= p.num_slots) flag_error(p.err_flag, kFlagBadBlock);
-  __syncthreads();
-
   const int u = threadIdx.x % kLanes;
   const bool turned = 8 * u < pairs;  // this thread's eight pairs (8 u .. 8 u + 7) are rotated
   // The thread's two 8-element pieces of a head: neighbours, or half the
   // rotated width apart; past the rotated part, neighbours again.
   const int e0 = kNext ? 16 * u : turned ? 8 * u : 16 * u;
   const int e1 = kNext ? e0 + 8 : turned ? e0 + pairs : e0 + 8;
-  float c[8], s[8];
-  if (turned) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float2 f = cs[8 * u + k];
-      c[k] = f.x;
-      s[k] = f.y;
+  const int heads = p.h_q + 2 * p.h_kv;
+
+  auto source = [&](int tl, int h) -> const uint16_t* {
+    const int64_t t = t0 + tl;
+    if (h < p.h_q) return static_cast<const uint16_t*>(p.q) + t * p.q_stride + h * kHeadDim;
+    h -= p.h_q;
+    if (h < p.h_kv) return static_cast<const uint16_t*>(p.k) + t * p.k_stride + h * kHeadDim;
+    return static_cast<const uint16_t*>(p.v) + t * p.v_stride + (h - p.h_kv) * kHeadDim;
+  };
+  // Units of work: the heads (q, k, v) of the CTA's tokens, one after another.
+  int tl = 0, h = threadIdx.x / kLanes;
+  auto wrap = [&](int& at, int& head) {
+    while (head >= heads) {
+      head -= heads;
+      ++at;
+    }
+  };
+  wrap(tl, h);
+  uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;
+  if (tl < n_tok) {
+    const uint16_t* src = source(tl, h);
+    w0 = *reinterpret_cast<const uint4*>(src + e0);
+    w1 = *reinterpret_cast<const uint4*>(src + e1);
+  }
+  for (int i = threadIdx.x; i < kTok * 64; i += kThreads) {
+    const int at = i >> 6, pair = i & 63;
+    if (at < n_tok && pair < pairs) {
+      const int pos = p.positions[p.rope.axis[pair] * static_cast<int64_t>(p.tokens) + t0 + at];
+      const uint64_t phase = static_cast<uint64_t>(static_cast<int64_t>(pos)) * p.rope.turns[pair];
+      const int half_turns = static_cast<int>(static_cast<uint32_t>((phase + 0x80000000ull) >> 32));
+      float sn, cn;
+      sincospif(static_cast<float>(half_turns) * 4.656612873077393e-10f, &sn, &cn);  // 2^-31
+      reinterpret_cast<float2*>(&cs[at][0])[pair] = make_float2(cn, sn);
     }
   }
-  const int n_heads = p.h_q + (in_cache ? 2 * p.h_kv : 0);
-#pragma unroll 2
-  for (int h = threadIdx.x / kLanes; h < n_heads; h += kHeads) {
+  if (threadIdx.x < n_tok) {
+    const int slot = p.slots[t0 + threadIdx.x];
+    if (slot >= p.num_slots) flag_error(p.err_flag, kFlagBadBlock);
+    slots[threadIdx.x] = slot < p.num_slots ? slot : -1;
+  }
+  __syncthreads();
+
+#pragma unroll 1
+  while (tl < n_tok) {
+    int tn = tl, hn = h + kHeads;
+    wrap(tn, hn);
+    uint4 n0 = make_uint4(0, 0, 0, 0), n1 = n0;
+    if (tn < n_tok) {
+      const uint16_t* src = source(tn, hn);
+      n0 = *reinterpret_cast<const uint4*>(src + e0);
+      n1 = *reinterpret_cast<const uint4*>(src + e1);
+    }
     const bool is_q = h < p.h_q, is_v = h >= p.h_q + p.h_kv;
-    const int hh = is_q ? h : is_v ? h - p.h_q - p.h_kv : h - p.h_q;
-    const uint16_t* src = static_cast<const uint16_t*>(is_q ? p.q : is_v ? p.v : p.k) +
-                          t * (is_q ? p.q_stride : is_v ? p.v_stride : p.k_stride) +
-                          hh * kHeadDim;
-    const uint4 w0 = *reinterpret_cast<const uint4*>(src + e0);
-    const uint4 w1 = *reinterpret_cast<const uint4*>(src + e1);
     float a[8], b[8];
     unpack8<kBF16>(w0, a);
     unpack8<kBF16>(w1, b);
     if (turned && !is_v) {
-      if constexpr (kNext) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float x = a[2 * k], y = a[2 * k + 1];
-          a[2 * k] = x * c[k] - y * s[k];
-          a[2 * k + 1] = x * s[k] + y * c[k];
-          const float z = b[2 * k], w = b[2 * k + 1];
-          b[2 * k] = z * c[4 + k] - w * s[4 + k];
-          b[2 * k + 1] = z * s[4 + k] + w * c[4 + k];
-        }
-      } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float x = a[k], y = b[k];
-          a[k] = x * c[k] - y * s[k];
-          b[k] = x * s[k] + y * c[k];
-        }
+      for (int j = 0; j < 4; ++j) {
+        const float4 f = cs[tl][4 * u + j];  // pairs 8 u + 2 j and the next
+        // Their places: neighbours in one piece, or place 2 j (2 j + 1) of both.
+        float& x0 = kNext ? (j < 2 ? a : b)[4 * (j & 1)] : a[2 * j];
+        float& y0 = kNext ? (j < 2 ? a : b)[4 * (j & 1) + 1] : b[2 * j];
+        float& x1 = kNext ? (j < 2 ? a : b)[4 * (j & 1) + 2] : a[2 * j + 1];
+        float& y1 = kNext ? (j < 2 ? a : b)[4 * (j & 1) + 3] : b[2 * j + 1];
+        const float p0 = x0 * f.x - y0 * f.y, q0 = x0 * f.y + y0 * f.x;
+        const float p1 = x1 * f.z - y1 * f.w, q1 = x1 * f.w + y1 * f.z;
+        x0 = p0;
+        y0 = q0;
+        x1 = p1;
+        y1 = q1;
       }
     }
     if (is_q) {
       uint16_t* dst = static_cast<uint16_t*>(p.q_out) +
-                      (t * p.h_q + hh) * static_cast<int64_t>(kHeadDim);
+                      ((t0 + tl) * p.h_q + h) * static_cast<int64_t>(kHeadDim);
       *reinterpret_cast<uint4*>(dst + e0) = pack8<kBF16>(a);
       *reinterpret_cast<uint4*>(dst + e1) = pack8<kBF16>(b);
-    } else {
-      const int64_t row = (static_cast<int64_t>(slot) * p.h_kv + hh) * kHeadDim;
+    } else if (slots[tl] >= 0) {
+      const int hh = is_v ? h - p.h_q - p.h_kv : h - p.h_q;
+      const int64_t row = (static_cast<int64_t>(slots[tl]) * p.h_kv + hh) * kHeadDim;
       if constexpr (kF8) {
         const float sc = (is_v ? p.v_scale : p.k_scale)[hh];
         uint8_t* dst = static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) + row;
@@ -138,16 +159,35 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const __grid_cons
         *reinterpret_cast<uint4*>(dst + e1) = pack8<kBF16>(b);
       }
     }
+    tl = tn;
+    h = hn;
+    w0 = n0;
+    w1 = n1;
   }
+}
+
+template <bool kBF16, bool kF8, bool kNext>
+void launch_n(const RopeParams& p, cudaStream_t stream) {
+  // A CTA's tokens: as few as put all CTAs on the GPU at once (four per SM
+  // of 152), at most four.  64 + 8 + 8 heads in bf16, by 1 / 2 / 4 tokens a
+  // CTA: 300 tokens 3.9 / 4.2 / 6.1 us, 1111 12.4 / 10.4 / 12.3, 2048 18.6 /
+  // 18.1 / 17.5, 8192 60.7 / 54.9 / 55.4 (6.1 TB/s); 8 tokens 62.7 there.
+  constexpr int kSlots = 4 * 152;
+  auto go = [&](auto kern, int tok) {
+    kern<<<static_cast<unsigned>((p.tokens + tok - 1) / tok), kThreads, 0, stream>>>(p);
+  };
+  if (p.tokens <= kSlots)
+    go(rope_append_kernel<kBF16, kF8, kNext, 1>, 1);
+  else if (p.tokens <= 2 * kSlots)
+    go(rope_append_kernel<kBF16, kF8, kNext, 2>, 2);
+  else
+    go(rope_append_kernel<kBF16, kF8, kNext, 4>, 4);
 }
 
 template <bool kBF16, bool kF8>
 void launch_t(const RopeParams& p, cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(p.tokens));
-  if (p.rope.interleaved)
-    rope_append_kernel<kBF16, kF8, true><<<grid, kThreads, 0, stream>>>(p);
-  else
-    rope_append_kernel<kBF16, kF8, false><<<grid, kThreads, 0, stream>>>(p);
+  p.rope.interleaved ? launch_n<kBF16, kF8, true>(p, stream)
+                     : launch_n<kBF16, kF8, false>(p, stream);
 }
 
 }  // namespace
