@@ -967,6 +967,7 @@ static int gqa_prefill_impl(const void* q, const void* k_cache, const void* v_ca
   }
   if (sms == 0) sms = device_sm_count();
   if (sms <= 0) return DECATTN_ERR_CUDA;
+  p.once = max_q_len <= 2 * p.tokens_per_tile ? 1 : 0;
   p.steal = items * h_kv * ns > sms ? 1 : 0;
   const bool bf16 = L->dtype == DECATTN_BF16;
   const uint64_t rows_total = static_cast<uint64_t>(L->num_blocks) * L->block_size;

@@ -44,6 +44,13 @@
 // so the next one's Q, K and V are on their way, and its first S is computed,
 // during the softmax warps' epilogue.  Pieces come longest first.
 //
+// A piece with one Q tile (few rows: drafted tokens, single tokens, a chunk's
+// rest) would leave the second set of softmax warps idle and every tile's chain
+// of product, softmax and product uncovered.  There (`solo`) both sets work on
+// the same rows, A on the even K / V tiles, B on the odd ones, with S, P and O
+// of their own, joined at the end through shared memory: 32 chunks of up to 8
+// tokens over 8k caches (64 heads, 8 KV heads) MEASURED.
+//
 // An 8-bit (e4m3) cache takes the same pipeline on fp16 operands: the ring
 // holds four 16 KB tiles of codes, and warps 10 and 11 convert each K and V
 // tile (exactly) into one of two 16-bit tiles; a bf16 Q is rewritten as fp16 in
@@ -64,7 +71,8 @@ constexpr int kOffRing = 2 * kTileBytes;       // behind Q_A, Q_B
 constexpr int kOffStage = kOffRing + kRing * kTileBytes;
 constexpr int kStageBytes = 32 * 128;          // one softmax warp's: 32 rows x 128 B
 constexpr int kOffBars = kOffStage + 8 * kStageBytes;
-constexpr int kSmemBytes = 1024 + kOffBars + 1024;
+constexpr int kOffMerge = kOffBars + 1024;     // 128 rows' (maximum, sum), see `solo`
+constexpr int kSmemBytes = 1024 + kOffMerge + 128 * 8;
 static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
 
 constexpr int kThreads = 384;
@@ -81,23 +89,24 @@ enum : int {
   kBarFull = 2,                 // ring slot landed
   kBarEmpty = kBarFull + kRing, // ring slot free
   kBarS = kBarEmpty + kRing,    // 2: S_X computed
-  kBarP = kBarS + 2,            // 2: P_X written (128 arrivals)
-  kBarO = kBarP + 2,            // 2: O_X complete
+  kBarP = kBarS + 2,            // 2 x 2: P_X, tokens 0-63 and 64-127, written (128 arrivals)
+  kBarO = kBarP + 4,            // 2: O_X complete
   kBarItem = kBarO + 2,         // 2: piece published
   kBarItemFree = kBarItem + 2,  // 2: piece done by every other role
   kBarNext = kBarItemFree + 2,  // the launch control's answer
   kBarQ16 = kBarNext + 1,       // 8-bit cache: bf16 Q rewritten as fp16 (64 arrivals)
   kBarFull16 = kBarQ16 + 1,     // 8-bit cache, K and V: converted (32 arrivals)
   kBarEmpty16 = kBarFull16 + 2, // 8-bit cache, K and V: 16-bit tile free
-  kBarDrain = kBarEmpty16 + 2,
+  kBarPair = kBarEmpty16 + 2,   // 4: the two softmax warps of the same rows (solo)
+  kBarDrain = kBarPair + 4,
   kNumBars = kBarDrain + 1
 };
 
 // Behind the barriers, in the same kilobyte.
-constexpr int kOffWords = kOffBars + 256;   // abort, bad, copies made by the producers, TMEM
-constexpr int kOffAnswer = kOffBars + 320;  // the launch control's answer, 16 bytes
-constexpr int kOffItems = kOffBars + 384;   // two pieces
-static_assert(kNumBars * 8 <= 256, "barriers");
+constexpr int kOffWords = kOffBars + 288;   // abort, bad, copies made by the producers, TMEM
+constexpr int kOffAnswer = kOffBars + 352;  // the launch control's answer, 16 bytes
+constexpr int kOffItems = kOffBars + 416;   // two pieces
+static_assert(kNumBars * 8 <= 288, "barriers");
 
 // A piece of work: rows of one sequence and KV head against a range of tiles.
 struct Item {
@@ -111,9 +120,10 @@ struct Item {
   int hi;           // one past the last position any row sees
   int tile0;        // first tile of this split
   int n_a, n_b;     // tiles that tile A, B need, from tile0 on
+  int solo;         // one Q tile: the warps of tile B take every other K / V tile
   int bad;
 };
-static_assert(2 * sizeof(Item) <= 1024 - 384, "items");
+static_assert(2 * sizeof(Item) <= 1024 - 416, "items");
 
 struct Tile {
   int t0, skip, nval;  // rows [skip, nval) hold tokens that may be seen
@@ -128,6 +138,17 @@ __device__ __forceinline__ Tile tile_of(const Item& w, int it) {
   r.nval = min(kKv, (sink ? w.s_end : w.hi) - r.t0);
   return r;
 }
+
+// Offsets (in tokens, from this split's first tile) of the window's first
+// token and of the sequence's end as tile_of counts them: the tiles at
+// [full_lo, full_hi) have no row outside [skip, nval) (sinks' tiles left out).
+__device__ __forceinline__ int win0_of(const Item& w) {
+  return w.base + (w.tile0 - w.sink_tiles) * kKv;
+}
+__device__ __forceinline__ int full_lo(const Item& w) {
+  return max(w.lo - win0_of(w), w.s_end - w.tile0 * kKv);
+}
+__device__ __forceinline__ int full_hi(const Item& w) { return w.hi - win0_of(w); }
 
 // Number of tiles up to and including the one that holds position `last`.
 __device__ __forceinline__ int tiles_to(const Item& w, int last) {
@@ -219,6 +240,7 @@ __device__ __forceinline__ bool find_item(const PrefillParams& p, Cursor& c, int
   w.tile0 = min(total, w.split * per);
   w.n_a = max(0, min(per, total_a - w.tile0));
   w.n_b = w.tok_b > 0 ? min(per, total - w.tile0) : 0;
+  w.solo = w.tok_b == 0 && w.n_a >= 2;
   return true;
 }
 
@@ -232,14 +254,8 @@ __device__ __forceinline__ uint32_t below(int n) {
 // A warp's 32 rows of 128 bytes (eight 16-byte pieces, one row per thread)
 // go through its own 4 KB of shared memory, so that eight lanes store a row's
 // whole line: piece c of row r lies at place c ^ (r % 8) of its row.
-__device__ __forceinline__ void stage_rows(uint8_t* stage, const uint4 (&v)[8], int lane) {
-#pragma unroll
-  for (int c = 0; c < 8; ++c)
-    *reinterpret_cast<uint4*>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) = v[c];
-  __syncwarp();
-}
-__device__ __forceinline__ uint4 staged(const uint8_t* stage, int row, int c) {
-  return *reinterpret_cast<const uint4*>(stage + row * 128 + ((c ^ (row & 7)) << 4));
+__device__ __forceinline__ uint4* staged(uint8_t* stage, int row, int c) {
+  return reinterpret_cast<uint4*>(stage + row * 128 + ((c ^ (row & 7)) << 4));
 }
 
 // kF8: the cache holds e4m3 codes with per-KV-head scales.
@@ -273,6 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int x = 0; x < 2; ++x) {
       mbar_init(bar(kBarS + x), 1);
       mbar_init(bar(kBarP + x), kM);
+      mbar_init(bar(kBarP + 2 + x), kM);
       mbar_init(bar(kBarO + x), 1);
       mbar_init(bar(kBarItem + x), 1);
       // V producer or the two converters, MMA, softmax
@@ -282,6 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(bar(kBarNext), 1);
     mbar_init(bar(kBarQ16), 64);
+    for (int x = 0; x < 4; ++x) mbar_init(bar(kBarPair + x), 64);
     mbar_init(bar(kBarDrain), 1);
     for (int k = 0; k < 6; ++k) abort_word[k] = 0;
     fence_barrier_init();
@@ -317,7 +335,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Warp 8 also is the scheduler: it publishes each piece when it begins
       // to load it.
       const bool lead = warp == kWarpLoad;
-      const uint64_t keep = policy_evict_last();
+      // A cache that only one piece of each sequence and KV head reads (few rows)
+      // streams through L2; otherwise its tiles are kept for the next piece.
+      // (32 chunks of 8 tokens over 8k caches: 180 us, 187 with tiles kept.)
+      const uint64_t keep = p.once ? policy_evict_first() : policy_evict_last();
       if (lane == 0) {
         if (lead) tma_prefetch_desc(&tm_q);
         tma_prefetch_desc(lead ? &tm_k : &tm_v);
@@ -566,11 +587,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         return g;
       };
       auto free_bar = [](int s) { return kF8 ? kBarEmpty16 + s - 2 : kBarEmpty + s; };
-      // S_X = Q_X K^T: eight k-steps of 16 dims, four per 64-column half.
+      // S_X = Q_X K^T (Q tile q): eight k-steps of 16 dims, four per 64-column half.
       // `last`: no other tile reads this K slot after this one; `end`: this is
       // the piece's last S.
-      auto issue_s = [&](int x, int s, bool last, bool end) {
-        const uint64_t a = dq + static_cast<uint64_t>((x * kTileBytes) >> 4);
+      auto issue_s = [&](int x, int q, int s, bool last, bool end) {
+        const uint64_t a = dq + static_cast<uint64_t>((q * kTileBytes) >> 4);
         const uint64_t b = dk + static_cast<uint64_t>((s * kTileBytes) >> 4);
         const uint32_t done = bar(kBarS + x), empty = bar(free_bar(s)), q_free = bar(kBarQFree);
         const uint32_t d = tmem + kTmemS + kKv * x;
@@ -588,87 +609,111 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       // O_X += P_X V: eight k-steps of 16 tokens, P from TMEM.  `done`: O_X is
       // complete behind this one; `last` as above, for the V slot.
-      auto issue_pv = [&](int x, int s, bool first, bool done, bool last) {
+      // In two halves, so that the first starts while the softmax is at the second
+      // (8192-token prompt, 64 / 8 heads: 719 us, 724 in one).
+      auto issue_pv_half = [&](int h, int x, int s, bool first, bool done, bool last) {
         const uint64_t b = dv + static_cast<uint64_t>((s * kTileBytes) >> 4);
         const uint32_t acc0 = first ? 0u : 1u;
         const uint32_t d = tmem + kTmemO + kHeadDim * x, a = tmem + kTmemS + kKv * x;
         const uint32_t full = bar(kBarO + x), empty = bar(free_bar(s));
         if (elect_one()) {
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
+          for (int k4 = 0; k4 < 4; ++k4) {
+            const int ks = 4 * h + k4;
             tc_mma_f16_ts(d, a + ks * 8, b + static_cast<uint64_t>((ks * 2048) >> 4), idesc_o,
                           ks > 0 ? 1u : acc0);
-          if (done) tc_commit(full);
-          if (last) tc_commit(empty);
+          }
+          if (h == 1) {
+            if (done) tc_commit(full);
+            if (last) tc_commit(empty);
+          }
         }
         __syncwarp();
       };
-      // Tile B needs at least the tiles that A needs, or there is no tile B.
-      // Counters run over all pieces: the ring's slot and phase, Q loads, P.
-      // 16-bit cache: K and V tiles go round the ring's four slots; 8-bit: the
-      // converted K and V tiles are slots 2 and 3.
-      int slot = kF8 ? 3 : kRing - 1, q_loads = 0;
-      uint32_t phase = 1, phase_a = 0, phase_b = 0;
-      auto next = [&]() {
-        if (++slot == kRing) {
-          slot = kF8 ? 2 : 0;
-          phase ^= 1u;
-        }
-      };
+      // The c-th tile of all pieces: 16-bit cache, K and V go round the ring's
+      // four slots; 8-bit, the converted K and V tiles are slots 2 and 3.
+      auto k_slot = [](int c) { return kF8 ? 2 : (2 * c) % kRing; };
+      auto v_slot = [](int c) { return kF8 ? 3 : (2 * c + 1) % kRing; };
+      auto phase_of = [](int c) { return static_cast<uint32_t>((kF8 ? c : 2 * c / kRing) & 1); };
       auto full = [&](int s) { return kF8 ? kBarFull16 + s - 2 : kBarFull + s; };
+      auto wait_k = [&](int c) { return wait(full(k_slot(c)), phase_of(c)); };
+      // V rows outside [skip, nval) become zeros (P is 0 there, but the slots
+      // may hold NaN), while the softmax works on the tile.  (All 128 bytes of
+      // a row: the swizzle does not matter.)
+      auto wait_v = [&](int c, const Item& w, int it, int lo, int hi) {
+        if (!wait(full(v_slot(c)), phase_of(c))) return false;
+        if (!kF8 && (it * kKv < lo || it * kKv + kKv > hi)) {
+          const Tile t = tile_of(w, it);
+          uint8_t* v = smem + kOffRing + v_slot(c) * kTileBytes;
+#pragma unroll 1
+          for (int i = lane; i < (t.skip + kKv - t.nval) * 16; i += 32) {
+            const int k = i >> 4, col = i & 15;
+            const int r = k < t.skip ? k : t.nval + (k - t.skip);
+            *reinterpret_cast<uint4*>(v + (col >> 3) * kHalf + r * 128 + ((col & 7) << 4)) =
+                make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        return true;
+      };
+      int c = 0, q_loads = 0;  // over all pieces: tiles, Q loads, P's phases
+      uint32_t phase_p[2] = {0, 0};
+      auto do_pv = [&](int x, int s, bool first, bool done, bool last) {
+        const uint32_t ph = x ? phase_p[1] : phase_p[0];
+        if (x)
+          phase_p[1] ^= 1u;
+        else
+          phase_p[0] ^= 1u;
+        if (!wait(kBarP + x, ph)) return false;
+        issue_pv_half(0, x, s, first, done, last);
+        if (!wait(kBarP + 2 + x, ph)) return false;
+        issue_pv_half(1, x, s, first, done, last);
+        return true;
+      };
       bool ok = true;
       Item w;
       for (int k = 0; ok && get_item(k, w); ++k) {
-        const int n = max(w.n_a, w.n_b);
+        const int n = max(w.n_a, w.n_b), lo = full_lo(w), hi = full_hi(w);
         if (n > 0) {
-          next();
-          ok = wait(kF8 && kBF16 ? kBarQ16 : kBarQ, q_loads++ & 1) && wait(full(slot), phase);
+          ok = wait(kF8 && kBF16 ? kBarQ16 : kBarQ, q_loads++ & 1) && wait_k(c);
           if (!ok) break;
-          if (w.n_a > 0) issue_s(0, slot, w.n_b == 0, n == 1 && w.n_b == 0);
-          if (w.n_b > 0) issue_s(1, slot, true, n == 1);
         }
-        for (int it = 0; it < n; ++it) {
-          next();
-          const int sv = slot;
-          ok = wait(full(sv), phase);
+        if (w.solo) {
+          issue_s(0, 0, k_slot(c), true, false);
+          ok = wait_k(c + 1);
           if (!ok) break;
-          const Tile t = tile_of(w, it);
-          if (!kF8 && (t.nval < kKv || t.skip > 0)) {
-            // V rows outside [skip, nval) become zeros (P is 0 there, but the
-            // slots may hold NaN), while the softmax works on this tile.  (All
-            // 128 bytes of a row: the swizzle does not matter.)
-            uint8_t* v = smem + kOffRing + sv * kTileBytes;
-#pragma unroll 1
-            for (int i = lane; i < (t.skip + kKv - t.nval) * 16; i += 32) {
-              const int kk = i >> 4, c = i & 15;
-              const int r = kk < t.skip ? kk : t.nval + (kk - t.skip);
-              *reinterpret_cast<uint4*>(v + (c >> 3) * kHalf + r * 128 + ((c & 7) << 4)) =
-                  make_uint4(0, 0, 0, 0);
+          issue_s(1, 0, k_slot(c + 1), true, n == 2);
+          for (int it = 0; it < n; ++it, ++c) {
+            const int x = it & 1;
+            ok = wait_v(c, w, it, lo, hi) && do_pv(x, v_slot(c), it < 2, it + 2 >= n, true);
+            if (!ok) break;
+            if (it + 2 < n) {
+              ok = wait_k(c + 2);
+              if (!ok) break;
+              issue_s(x, 0, k_slot(c + 2), true, it + 3 == n);
             }
-            fence_proxy_async_smem();
-            __syncwarp();
           }
-          // The next K tile is waited for first, so that O += P V and the next
-          // S follow each other without a pause.
-          if (it + 1 < n) {
-            next();
-            ok = wait(full(slot), phase);
+        } else {
+          // Tile B needs at least the tiles that A needs, or there is no tile B.
+          if (w.n_a > 0) issue_s(0, 0, k_slot(c), w.n_b == 0, n == 1 && w.n_b == 0);
+          if (w.n_b > 0) issue_s(1, 1, k_slot(c), true, n == 1);
+          for (int it = 0; it < n; ++it, ++c) {
+            // The next K tile is waited for first, so that O += P V and the
+            // next S follow each other without a pause.
+            ok = wait_v(c, w, it, lo, hi) && (it + 1 == n || wait_k(c + 1));
             if (!ok) break;
-          }
-          if (it < w.n_a) {
-            ok = wait(kBarP, phase_a);
-            if (!ok) break;
-            phase_a ^= 1u;
-            issue_pv(0, sv, it == 0, it + 1 == w.n_a, it >= w.n_b);
-            if (it + 1 < w.n_a)
-              issue_s(0, slot, it + 1 >= w.n_b, it + 2 == n && w.n_b == 0);
-          }
-          if (it < w.n_b) {
-            ok = wait(kBarP + 1, phase_b);
-            if (!ok) break;
-            phase_b ^= 1u;
-            issue_pv(1, sv, it == 0, it + 1 == w.n_b, true);
-            if (it + 1 < w.n_b) issue_s(1, slot, true, it + 2 == n);
+            if (it < w.n_a) {
+              ok = do_pv(0, v_slot(c), it == 0, it + 1 == w.n_a, it >= w.n_b);
+              if (!ok) break;
+              if (it + 1 < w.n_a)
+                issue_s(0, 0, k_slot(c + 1), it + 1 >= w.n_b, it + 2 == n && w.n_b == 0);
+            }
+            if (it < w.n_b) {
+              ok = do_pv(1, v_slot(c), it == 0, it + 1 == w.n_b, true);
+              if (!ok) break;
+              if (it + 1 < w.n_b) issue_s(1, 1, k_slot(c + 1), true, it + 2 == n);
+            }
           }
         }
         if (ok) release_item(k);
@@ -691,41 +736,55 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Row r is head r % G of token r / G: the division for r < 128, G <= 64.
     const uint32_t inv_g = 65536u / static_cast<uint32_t>(G) + 1u;
     const int r_tok = static_cast<int>((static_cast<uint32_t>(r) * inv_g) >> 16);
-    uint32_t phase_s = 0, phase_o = 0;
+    uint32_t phase_s = 0, phase_o = 0, phase_pair = 0;
     bool ok = true;
-    Item w;
-    for (int k = 0; ok && get_item(k, w); ++k) {
-      const int nt = x ? w.n_b : w.n_a, tok = x ? w.tok_b : w.tok_a;
-      const int i0 = w.i0 + x * p.tokens_per_tile;
-      const int pos = w.len - w.n + i0 + min(r_tok, max(0, tok - 1));
-      // Positions of the tile's first and last rows: tiles at or before the
-      // first (and inside the last one's window) need no mask.
-      const int pos0 = w.len - w.n + i0, pos1 = pos0 + tok - 1;
-      // An 8-bit cache's K scale multiplies every score of KV head j.
+    for (int k = 0; ok; ++k) {
+      // What the tiles' loop needs of the piece (a row's 128 scores leave few
+      // registers: the rest is read again where it is used).
+      int nt, step, pos, plain_lo, plain_hi;
+      bool idle;
       float scale = p.scale_log2;
       bool negate = p.negate != 0;
-      if constexpr (kF8) {
-        const float ks = p.k_scale[w.j];
-        negate ^= ks < 0.f;
-        scale = fmaxf(scale * fabsf(ks), 1e-37f);
+      {
+        Item w;
+        if (!get_item(k, w)) break;
+        // (Solo: tiles x, x + 2, ... for the rows of tile A.)
+        const int half = w.solo ? 0 : x;
+        const int tok = half ? w.tok_b : w.tok_a;
+        nt = w.solo ? (w.n_a + 1 - x) >> 1 : x ? w.n_b : w.n_a;
+        step = w.solo ? 2 * kKv : kKv;
+        idle = 32 * (warp & 3) >= tok * G;
+        // Positions, counted as the tiles: of this row, and of the tile's first
+        // and last rows.  Tiles at or before the first (and inside the last
+        // one's window) need no mask.
+        const int pos0 = w.len - w.n + w.i0 + half * p.tokens_per_tile - win0_of(w);
+        pos = pos0 + min(r_tok, max(0, tok - 1));
+        plain_lo = full_lo(w);
+        if (p.window > 0) plain_lo = max(plain_lo, pos0 + tok - p.window);
+        plain_hi = min(full_hi(w), pos0 + 1);
+        if constexpr (kF8) {
+          // An 8-bit cache's K scale multiplies every score of KV head j.
+          const float ks = p.k_scale[w.j];
+          negate ^= ks < 0.f;
+          scale = fmaxf(scale * fabsf(ks), 1e-37f);
+        }
+        if (negate) plain_hi = plain_lo;  // (every tile changes its scores' sign)
       }
-      const float sign = negate ? -1.f : 1.f;
       float m = kNegInf, l = 0.f;
-      for (int it = 0; it < nt; ++it) {
-        const Tile t = tile_of(w, it);
-        const bool plain = !negate && t.skip == 0 && t.nval == kKv && t.t0 + kKv - 1 <= pos0 &&
-                           (p.window <= 0 || t.t0 > pos1 - p.window);
-        // Seen columns: [skip, hi), of them those from lo on or below sink (at
-        // or before the row's position; in its window or kept first tokens).
-        const int c_hi = min(t.nval, pos + 1 - t.t0);
-        const int c_lo = p.window > 0 ? pos + 1 - p.window - t.t0 : 0;
-        const int c_sink = p.sinks - t.t0;
-        auto mask = [&](float (&v)[32], int c0) {
-          const uint32_t seen = (below(c_hi - c0) & ~below(t.skip - c0)) &
-                                (~below(c_lo - c0) | below(c_sink - c0));
-#pragma unroll
-          for (int k = 0; k < 32; ++k) v[k] = (seen >> k) & 1u ? v[k] * sign : kNegInf;
-        };
+      int o = step > kKv ? x * kKv : 0;  // this tile's first token
+      const int end = o + nt * step;
+      if (idle) {
+        // No row of this warp is real: its P may be anything.
+        for (; ok && o < end; o += step) {
+          ok = mbar_wait_or_abort(bar(kBarS + x), phase_s, p.err_flag, abort_word);
+          phase_s ^= 1u;
+          if (ok) {
+            mbar_arrive(bar(kBarP + x));
+            mbar_arrive(bar(kBarP + 2 + x));
+          }
+        }
+      }
+      for (const int o0 = o; o < end; o += step) {
         if (!mbar_wait_or_abort(bar(kBarS + x), phase_s, p.err_flag, abort_word)) {
           ok = false;
           break;
@@ -742,7 +801,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_wait_ld_for(vb);
         tc_wait_ld_for(vc);
         tc_wait_ld_for(vd);
-        if (!plain) {
+        if (o < plain_lo || o + kKv > plain_hi) {
+          // Seen columns: [skip, hi), of them those from lo on or below sink (at
+          // or before the row's position; in its window or kept first tokens).
+          const volatile Item& w = items[k & 1];
+          const int s_rel = w.s_end - w.tile0 * kKv;
+          const int win0 = w.base + (w.tile0 - w.sink_tiles) * kKv;
+          const bool sink = o < s_rel;
+          const int skip = sink ? 0 : w.lo - win0 - o;
+          const int row = sink ? kKv : pos - o;  // (a sink's tile is before every row)
+          const int c_hi = min(sink ? s_rel - o : w.hi - win0 - o, row + 1);
+          const int c_lo = p.window > 0 && !sink ? row + 1 - p.window : 0;
+          const int c_sink = p.sinks - win0 - o;
+          const float sign = negate ? -1.f : 1.f;
+          auto mask = [&](float (&v)[32], int c0) {
+            const uint32_t seen = (below(c_hi - c0) & ~below(skip - c0)) &
+                                  (~below(c_lo - c0) | below(c_sink - c0));
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = (seen >> j) & 1u ? v[j] * sign : kNegInf;
+          };
           mask(va, 0);
           mask(vb, 32);
           mask(vc, 64);
@@ -769,7 +846,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (__any_sync(0xffffffffu, need)) {
           const float m_new = need ? mt : m;
           const float f = need ? ex2(m - m_new) : 1.f;  // 0 from -inf
-          if (it > 0) {
+          if (o > o0) {
 #pragma unroll 1
             for (int c = 0; c < kHeadDim; c += 8) {
               float o[8];
@@ -783,101 +860,150 @@ __global__ void __launch_bounds__(kThreads, 1)
           m = m_new;
         }
         const float neg_m = m == kNegInf ? 0.f : -m;
-        float l0 = 0.f, l1 = 0.f;
+        const uint64_t scale2 = pair2(scale, scale), neg2 = pair2(neg_m, neg_m);
+        uint64_t sum2 = 0;
         auto probs = [&](float (&v)[32], int c0) {
           uint32_t pk[16];
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
-            const float p0 = ex2(fmaf(v[2 * k], scale, neg_m));
-            const float p1 = ex2(fmaf(v[2 * k + 1], scale, neg_m));
-            l0 += p0;
-            l1 += p1;
+            const float2 e = unpair2(fma2(pair2(v[2 * k], v[2 * k + 1]), scale2, neg2));
+            const float p0 = ex2(e.x), p1 = ex2(e.y);
+            sum2 = add2(sum2, pair2(p0, p1));
             pk[k] = pack2<kMmaBF16>(p0, p1);
           }
           tmem_st16(ts + c0 / 2, pk);
         };
         probs(va, 0);
         probs(vb, 32);
-        probs(vc, 64);
-        probs(vd, 96);
-        l += l0 + l1;
         tc_wait_st();
         tc_fence_before();
         mbar_arrive(bar(kBarP + x));
+        probs(vc, 64);
+        probs(vd, 96);
+        {
+          const float2 e = unpair2(sum2);
+          l += e.x + e.y;
+        }
+        tc_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar(kBarP + 2 + x));
       }
       // ---------------- epilogue
       if (ok && nt > 0) {
         ok = mbar_wait_or_abort(bar(kBarO + x), phase_o, p.err_flag, abort_word);
         phase_o ^= 1u;
       }
+      const Item w = items[k & 1];
+      const int half = w.solo ? 0 : x;
+      const int tok = half ? w.tok_b : w.tok_a;
+      const int i0 = w.i0 + half * p.tokens_per_tile;
       if (ok && tok > 0) {
         tc_fence_after();
         const bool bad = w.bad || bad_word[k & 1] != 0;
-        const bool live = l > 0.f && !bad;
-        // (An 8-bit cache's V scale multiplies the whole row.)
-        const float inv = live ? (kF8 ? p.v_scale[w.j] : 1.f) / l : 0.f;
+        // Weight of this warp's O (and, solo, of the other's): 1 / l, times an
+        // 8-bit cache's V scale; 0 for a row that sees nothing or is bad.
+        auto norm = [&]() { return l > 0.f && !bad ? (kF8 ? p.v_scale[w.j] : 1.f) / l : 0.f; };
+        float wa = norm(), wb = 0.f;
         // Packed row of the chunk's first row of this tile; this lane stores
         // piece lane % 8 of the warp's rows lane / 8, + 4, ... + 28.
         const int64_t row0 = static_cast<int64_t>(w.q0 + i0) * p.h_q + w.j * G;
         const int rows = tok * G;
-        auto store = [&](auto&& put) {
-#pragma unroll
+        // A row of the tile as (row, its place among the packed rows): 128
+        // bytes at `base` + row * `pitch` bytes.
+        auto store = [&](uint8_t* base, int64_t pitch) {
+          __syncwarp();
+#pragma unroll 2
           for (int e = 0; e < 8; ++e) {
-            const int q = 32 * (warp & 3) + (lane >> 3) + 4 * e;
+            const int local = (lane >> 3) + 4 * e, q = 32 * (warp & 3) + local;
             const int tk = static_cast<int>((static_cast<uint32_t>(q) * inv_g) >> 16);
             if (q < rows)
-              put(row0 + static_cast<int64_t>(tk) * p.h_q + (q - tk * G),
-                  staged(stage, (lane >> 3) + 4 * e, lane & 7));
+              reinterpret_cast<uint4*>(
+                  base + (row0 + static_cast<int64_t>(tk) * p.h_q + (q - tk * G)) * pitch)[lane & 7] =
+                  *staged(stage, local, lane & 7);
           }
           __syncwarp();
         };
-        uint4 v[8];
-        if (p.n_split == 1) {
+        // Solo: the two halves of a row join.  The B warp hands over its maximum,
+        // sum and O through its staging (32 columns at a time), the A warp weighs,
+        // adds and stores.  (The pair meets at a bounded barrier: a warp that
+        // gave up elsewhere does not leave the other waiting.)
+        float2* ml = reinterpret_cast<float2*>(smem + kOffMerge) + r;
+        uint8_t* hand = smem + kOffStage + (4 + (warp & 3)) * kStageBytes;
+        auto meet = [&]() {
+          const uint32_t at = bar(kBarPair + (warp & 3));
+          mbar_arrive(at);
+          ok = __all_sync(0xffffffffu, mbar_wait_or_abort(at, phase_pair, p.err_flag, abort_word));
+          phase_pair ^= 1u;
+        };
+        if (w.solo && x == 1) *ml = make_float2(m, l);
 #pragma unroll 1
-          for (int c = 0; c < kHeadDim; c += 64) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              float o[32];
-              tmem_ld32(to + c + 32 * h, o);
-              tc_wait_ld_for(o);
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                v[4 * h + e] = make_uint4(pack2<kBF16>(o[8 * e] * inv, o[8 * e + 1] * inv),
-                                          pack2<kBF16>(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
-                                          pack2<kBF16>(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
-                                          pack2<kBF16>(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
-            }
-            if (!live) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) v[e] = make_uint4(0, 0, 0, 0);
-            }
-            stage_rows(stage, v, lane);
-            store([&](int64_t row, const uint4& y) {
-              reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * kHeadDim + c)[lane & 7] =
-                  y;
-            });
-          }
-        } else {
-          if (nt > 0) {
-#pragma unroll 1
-            for (int c = 0; c < kHeadDim; c += 32) {
-              float o[32];
-              tmem_ld32(to + c, o);
-              tc_wait_ld_for(o);
+        for (int c = 0; ok && c < kHeadDim && (nt > 0 || p.n_split == 1); c += 32) {
+          float o[32];
+          tmem_ld32(to + c, o);
+          tc_wait_ld_for(o);
+          if (w.solo) {
+            if (x == 1) {
 #pragma unroll
               for (int e = 0; e < 8; ++e)
-                v[e] = live ? make_uint4(__float_as_uint(o[4 * e] * inv),
-                                         __float_as_uint(o[4 * e + 1] * inv),
-                                         __float_as_uint(o[4 * e + 2] * inv),
-                                         __float_as_uint(o[4 * e + 3] * inv))
-                            : make_uint4(0, 0, 0, 0);
-              stage_rows(stage, v, lane);
-              store([&](int64_t row, const uint4& y) {
-                reinterpret_cast<uint4*>(p.part_o + (row * p.n_split + w.split) * kHeadDim +
-                                         c)[lane & 7] = y;
-              });
+                *staged(hand, lane, e) = make_uint4(
+                    __float_as_uint(o[4 * e]), __float_as_uint(o[4 * e + 1]),
+                    __float_as_uint(o[4 * e + 2]), __float_as_uint(o[4 * e + 3]));
             }
+            meet();
+            if (!ok) break;
+            if (x == 0) {
+              if (c == 0) {
+                const float2 other = *ml;
+                const float top = fmaxf(m, other.x);
+                wa = m == kNegInf ? 0.f : ex2(m - top);
+                wb = other.x == kNegInf ? 0.f : ex2(other.x - top);
+                l = wa * l + wb * other.y;
+                m = top;
+                const float f = norm();
+                wa *= f;
+                wb *= f;
+              }
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const uint4 y = *staged(hand, lane, e);
+                o[4 * e] = wa * o[4 * e] + wb * __uint_as_float(y.x);
+                o[4 * e + 1] = wa * o[4 * e + 1] + wb * __uint_as_float(y.y);
+                o[4 * e + 2] = wa * o[4 * e + 2] + wb * __uint_as_float(y.z);
+                o[4 * e + 3] = wa * o[4 * e + 3] + wb * __uint_as_float(y.w);
+              }
+            }
+            meet();
+            if (!ok) break;
+            if (x == 1) continue;
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] *= wa;
           }
+          if (wa == 0.f && wb == 0.f) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0.f;  // (O may hold anything)
+          }
+          if (p.n_split == 1) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              *staged(stage, lane, ((c >> 3) & 4) + e) =
+                  make_uint4(pack2<kBF16>(o[8 * e], o[8 * e + 1]),
+                             pack2<kBF16>(o[8 * e + 2], o[8 * e + 3]),
+                             pack2<kBF16>(o[8 * e + 4], o[8 * e + 5]),
+                             pack2<kBF16>(o[8 * e + 6], o[8 * e + 7]));
+            if (c & 32)
+              store(static_cast<uint8_t*>(p.out) + 2 * (c - 32), 2 * kHeadDim);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              *staged(stage, lane, e) =
+                  make_uint4(__float_as_uint(o[4 * e]), __float_as_uint(o[4 * e + 1]),
+                             __float_as_uint(o[4 * e + 2]), __float_as_uint(o[4 * e + 3]));
+            store(reinterpret_cast<uint8_t*>(p.part_o) + 4 * (w.split * kHeadDim + c),
+                  static_cast<int64_t>(4 * kHeadDim) * p.n_split);
+          }
+        }
+        if (p.n_split > 1 && !(w.solo && x == 1)) {
           if (r < rows)
             p.part_lse[(row0 + static_cast<int64_t>(r_tok) * p.h_q + (r - r_tok * G)) * p.n_split +
                        w.split] = bad ? DECATTN_POISON_LSE : l > 0.f ? m + lg2(l) : kNegInf;

@@ -141,6 +141,7 @@ struct PrefillParams {
   int tokens_per_tile;        // floor(128 / group)
   int n_items;                // upper bound of the pieces of 2 tokens_per_tile tokens
   int n_split;
+  int once;                   // at most one piece per sequence and KV head
   int steal;                  // more pieces than SMs: CTAs take over pieces that wait
   int negate;                 // the scale is negative: scores change sign
   float scale_log2;           // |scale| * log2(e), > 0
