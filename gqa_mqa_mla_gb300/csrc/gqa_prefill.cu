@@ -120,6 +120,7 @@ struct Item {
   int hi;           // one past the last position any row sees
   int tile0;        // first tile of this split
   int n_a, n_b;     // tiles that tile A, B need, from tile0 on
+  int gap0, gap1;   // tiles [gap0, gap1) lie before tile B's window (A's only)
   int solo;         // one Q tile: the warps of tile B take every other K / V tile
   int bad;
 };
@@ -241,6 +242,15 @@ __device__ __forceinline__ bool find_item(const PrefillParams& p, Cursor& c, int
   w.n_a = max(0, min(per, total_a - w.tile0));
   w.n_b = w.tok_b > 0 ? min(per, total - w.tile0) : 0;
   w.solo = w.tok_b == 0 && w.n_a >= 2;
+  // With a window, the first window tiles may lie before every row of tile B.
+  const int lo_b = p.window > 0 ? p_first + w.tok_a + 1 - p.window : 0;
+  const int before_b = w.lo > 0 ? (lo_b - w.base) / kKv : 0;
+  w.gap0 = max(0, min(w.n_b, w.sink_tiles - w.tile0));
+  w.gap1 = max(w.gap0, min(w.n_b, w.sink_tiles + before_b - w.tile0));
+  if (w.gap1 == w.n_b) {  // nothing behind the gap (in this split)
+    w.n_b = w.gap0;
+    w.gap0 = w.gap1 = 0;
+  }
   return true;
 }
 
@@ -695,25 +705,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         } else {
-          // Tile B needs at least the tiles that A needs, or there is no tile B.
-          if (w.n_a > 0) issue_s(0, 0, k_slot(c), w.n_b == 0, n == 1 && w.n_b == 0);
-          if (w.n_b > 0) issue_s(1, 1, k_slot(c), true, n == 1);
+          // Each tile is needed by A, by B or by both (B leaves out the gap;
+          // either may end first).  A K or V slot is free behind its last
+          // reader: B's product, or A's where B has none.
+          auto has_b = [&](int it) { return it < w.n_b && (it < w.gap0 || it >= w.gap1); };
+          const int first_b = w.gap0 > 0 ? 0 : w.gap1;
+          if (w.n_a > 0) issue_s(0, 0, k_slot(c), !has_b(0), n == 1 && !has_b(0));
+          if (has_b(0)) issue_s(1, 1, k_slot(c), true, n == 1);
           for (int it = 0; it < n; ++it, ++c) {
             // The next K tile is waited for first, so that O += P V and the
             // next S follow each other without a pause.
             ok = wait_v(c, w, it, lo, hi) && (it + 1 == n || wait_k(c + 1));
             if (!ok) break;
+            const bool b0 = has_b(it), b1 = has_b(it + 1);
             if (it < w.n_a) {
-              ok = do_pv(0, v_slot(c), it == 0, it + 1 == w.n_a, it >= w.n_b);
+              ok = do_pv(0, v_slot(c), it == 0, it + 1 == w.n_a, !b0);
               if (!ok) break;
-              if (it + 1 < w.n_a)
-                issue_s(0, 0, k_slot(c + 1), it + 1 >= w.n_b, it + 2 == n && w.n_b == 0);
+              if (it + 1 < w.n_a) issue_s(0, 0, k_slot(c + 1), !b1, it + 2 == n && !b1);
             }
-            if (it < w.n_b) {
-              ok = do_pv(1, v_slot(c), it == 0, it + 1 == w.n_b, true);
+            if (b0) {
+              ok = do_pv(1, v_slot(c), it == first_b, it + 1 == w.n_b, true);
               if (!ok) break;
-              if (it + 1 < w.n_b) issue_s(1, 1, k_slot(c + 1), true, it + 2 == n);
             }
+            if (b1) issue_s(1, 1, k_slot(c + 1), true, it + 2 == n);
           }
         }
         if (ok) release_item(k);
@@ -741,7 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int k = 0; ok; ++k) {
       // What the tiles' loop needs of the piece (a row's 128 scores leave few
       // registers: the rest is read again where it is used).
-      int nt, step, pos, plain_lo, plain_hi;
+      int nt, step, pos, plain_lo, plain_hi, gap0, gap1;
       bool idle;
       float scale = p.scale_log2;
       bool negate = p.negate != 0;
@@ -753,6 +767,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int tok = half ? w.tok_b : w.tok_a;
         nt = w.solo ? (w.n_a + 1 - x) >> 1 : x ? w.n_b : w.n_a;
         step = w.solo ? 2 * kKv : kKv;
+        // (B's tiles leave out the gap; nt counts those in it too.)
+        gap0 = x && !w.solo ? w.gap0 * kKv : 0;
+        gap1 = x && !w.solo ? w.gap1 * kKv : 0;
         idle = 32 * (warp & 3) >= tok * G;
         // Positions, counted as the tiles: of this row, and of the tile's first
         // and last rows.  Tiles at or before the first (and inside the last
@@ -773,9 +790,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m = kNegInf, l = 0.f;
       int o = step > kKv ? x * kKv : 0;  // this tile's first token
       const int end = o + nt * step;
+      if (o == gap0) o += gap1 - gap0;
       if (idle) {
         // No row of this warp is real: its P may be anything.
-        for (; ok && o < end; o += step) {
+        for (; ok && o < end; o += o + step == gap0 ? step + gap1 - gap0 : step) {
           ok = mbar_wait_or_abort(bar(kBarS + x), phase_s, p.err_flag, abort_word);
           phase_s ^= 1u;
           if (ok) {
@@ -784,7 +802,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      for (const int o0 = o; o < end; o += step) {
+      for (const int o0 = o; o < end; o += o + step == gap0 ? step + gap1 - gap0 : step) {
         if (!mbar_wait_or_abort(bar(kBarS + x), phase_s, p.err_flag, abort_word)) {
           ok = false;
           break;
@@ -813,12 +831,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int c_hi = min(sink ? s_rel - o : w.hi - win0 - o, row + 1);
           const int c_lo = p.window > 0 && !sink ? row + 1 - p.window : 0;
           const int c_sink = p.sinks - win0 - o;
-          const float sign = negate ? -1.f : 1.f;
+          if (negate) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              va[j] = -va[j];
+              vb[j] = -vb[j];
+              vc[j] = -vc[j];
+              vd[j] = -vd[j];
+            }
+          }
           auto mask = [&](float (&v)[32], int c0) {
             const uint32_t seen = (below(c_hi - c0) & ~below(skip - c0)) &
                                   (~below(c_lo - c0) | below(c_sink - c0));
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = (seen >> j) & 1u ? v[j] * sign : kNegInf;
+            for (int j = 0; j < 32; ++j) v[j] = (seen >> j) & 1u ? v[j] : kNegInf;
           };
           mask(va, 0);
           mask(vb, 32);
@@ -904,23 +930,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         // 8-bit cache's V scale; 0 for a row that sees nothing or is bad.
         auto norm = [&]() { return l > 0.f && !bad ? (kF8 ? p.v_scale[w.j] : 1.f) / l : 0.f; };
         float wa = norm(), wb = 0.f;
-        // Packed row of the chunk's first row of this tile; this lane stores
-        // piece lane % 8 of the warp's rows lane / 8, + 4, ... + 28.
+        // This lane stores piece lane % 8 of the warp's rows lane / 8, + 4, ...
+        // + 28: their places among the packed rows, from the tile's first one on.
         const int64_t row0 = static_cast<int64_t>(w.q0 + i0) * p.h_q + w.j * G;
         const int rows = tok * G;
-        // A row of the tile as (row, its place among the packed rows): 128
-        // bytes at `base` + row * `pitch` bytes.
-        auto store = [&](uint8_t* base, int64_t pitch) {
+        int place[8];
+        bool real[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int q = 32 * (warp & 3) + (lane >> 3) + 4 * e;
+          const int tk = static_cast<int>((static_cast<uint32_t>(q) * inv_g) >> 16);
+          place[e] = tk * (p.h_q - G) + q;
+          real[e] = q < rows;
+        }
+        // 128 staged bytes of each row go to base + row * pitch bytes.
+        auto store = [&](uint8_t* base, int pitch) {
+          base += row0 * pitch + 16 * (lane & 7);
           __syncwarp();
-#pragma unroll 2
-          for (int e = 0; e < 8; ++e) {
-            const int local = (lane >> 3) + 4 * e, q = 32 * (warp & 3) + local;
-            const int tk = static_cast<int>((static_cast<uint32_t>(q) * inv_g) >> 16);
-            if (q < rows)
-              reinterpret_cast<uint4*>(
-                  base + (row0 + static_cast<int64_t>(tk) * p.h_q + (q - tk * G)) * pitch)[lane & 7] =
-                  *staged(stage, local, lane & 7);
-          }
+          uint4 y[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] = *staged(stage, (lane >> 3) + 4 * e, lane & 7);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (real[e])
+              *reinterpret_cast<uint4*>(base + static_cast<int64_t>(place[e]) * pitch) = y[e];
           __syncwarp();
         };
         // Solo: the two halves of a row join.  The B warp hands over its maximum,
@@ -936,7 +969,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           phase_pair ^= 1u;
         };
         if (w.solo && x == 1) *ml = make_float2(m, l);
-#pragma unroll 1
+#pragma unroll 2
         for (int c = 0; ok && c < kHeadDim && (nt > 0 || p.n_split == 1); c += 32) {
           float o[32];
           tmem_ld32(to + c, o);
@@ -976,12 +1009,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             if (x == 1) continue;
           } else {
+            const uint64_t wa2 = pair2(wa, wa);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] *= wa;
+            for (int e = 0; e < 32; e += 2) {
+              const float2 f = unpair2(mul2(pair2(o[e], o[e + 1]), wa2));
+              o[e] = f.x;
+              o[e + 1] = f.y;
+            }
           }
-          if (wa == 0.f && wb == 0.f) {
+          if (__any_sync(0xffffffffu, wa == 0.f && wb == 0.f)) {
+            // Rows that see nothing (their O may hold anything).
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = 0.f;  // (O may hold anything)
+            for (int e = 0; e < 32; ++e) o[e] = wa == 0.f && wb == 0.f ? 0.f : o[e];
           }
           if (p.n_split == 1) {
 #pragma unroll
@@ -1000,7 +1039,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   make_uint4(__float_as_uint(o[4 * e]), __float_as_uint(o[4 * e + 1]),
                              __float_as_uint(o[4 * e + 2]), __float_as_uint(o[4 * e + 3]));
             store(reinterpret_cast<uint8_t*>(p.part_o) + 4 * (w.split * kHeadDim + c),
-                  static_cast<int64_t>(4 * kHeadDim) * p.n_split);
+                  4 * kHeadDim * p.n_split);
           }
         }
         if (p.n_split > 1 && !(w.solo && x == 1)) {
