@@ -1,15 +1,17 @@
-"""ctypes binding of libdecattn (include/decattn.h).
+"""Python binding of libdecattn (include/decattn.h).
 
 Argument marshalling only: every step of the computation runs in the CUDA
 kernels behind the C ABI.  PyTorch supplies device memory and the current
-stream.  If the shared library is missing the calls raise; there is no
-fallback implementation.
+stream.  The GQA decode calls and the serving step's operators are marshalled
+natively (csrc/torch_calls.cpp: checks, allocations, stream and call in one
+step, for the latency of small calls); the others through ctypes.  If a shared
+library is missing the calls raise; there is no fallback implementation.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
-import struct
 import threading
 from typing import NamedTuple
 
@@ -81,6 +83,7 @@ class PagedPlan(NamedTuple):
 
 _lock = threading.Lock()
 _lib = None
+_calls = None
 
 
 def library_path() -> str:
@@ -101,7 +104,7 @@ def lib() -> ctypes.CDLL:
             L = ctypes.CDLL(path)
             P, I, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_float
             S, I64 = ctypes.c_size_t, ctypes.c_int64
-            LP = P  # a Launch by reference, or its bytes (_launch_bytes)
+            LP = ctypes.POINTER(Launch)
             L.gqa_decode.argtypes = [P, P, P, P, P, P, I, I, I, F, LP]
             L.gqa_decode.restype = I
             L.gqa_decode_fp8kv.argtypes = [P, P, P, P, P, P, P, P, I, I, I, F, LP]
@@ -172,6 +175,29 @@ def lib() -> ctypes.CDLL:
             L.decattn_version.restype = I
             _lib = L
     return _lib
+
+
+def calls():
+    """The native half of the binding (lib/_calls.so), opened on libdecattn.so."""
+    global _calls
+    if _calls is not None:
+        return _calls
+    lib()
+    with _lock:
+        if _calls is None:
+            if not os.path.exists(_build.CALLS):
+                raise RuntimeError(f"{_build.CALLS} is missing: build it with "
+                                   "`python -m gqa_mqa_mla_gb300.build` (no fallback exists)")
+            spec = importlib.util.spec_from_file_location("_calls", _build.CALLS)
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+            module.open(_build.LIB)
+            _calls = module
+    return _calls
+
+
+def _decode_name(name: str, window, sinks: int) -> str:
+    return name if window is None else name + ("_sinks" if sinks else "_window")
 
 
 def selftest_wait_timeout(limit_us: int = 1000, device="cuda"):
@@ -268,9 +294,6 @@ def _ptr(t: torch.Tensor | None) -> int | None:
 
 
 def _check(t: torch.Tensor, name: str, dtype=None, ndim=None):
-    if type(t) is torch.Tensor and (dtype is None or t.dtype is dtype) and \
-            (ndim is None or t.dim() == ndim) and t.is_contiguous():
-        return  # the usual case, in few steps
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if dtype is not None and t.dtype != dtype:
@@ -281,33 +304,6 @@ def _check(t: torch.Tensor, name: str, dtype=None, ndim=None):
         raise ValueError(f"{name} must be contiguous")
 
 
-def _check_codes(t: torch.Tensor, name: str):
-    """An 8-bit cache: uint8 or float8_e4m3fn (the same bytes)."""
-    _check(t, name, torch.float8_e4m3fn if isinstance(t, torch.Tensor) and
-           t.dtype is torch.float8_e4m3fn else torch.uint8, 4)
-
-
-def _check_out(t: torch.Tensor, name: str, dtype, shape, index):
-    _check(t, name, dtype)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    _check_device(index, (name, t))
-
-
-def _check_device(index, *named):
-    for name, t in named:
-        if t.get_device() != index:
-            raise ValueError(f"{name} is on {t.device}, the call's other tensors on cuda:{index}")
-
-
-def _check_flag(err_flag, index):
-    if err_flag is not None:
-        _check(err_flag, "err_flag", torch.int32)
-        if err_flag.numel() < 1:
-            raise ValueError("err_flag needs one element")
-        _check_device(index, ("err_flag", err_flag))
-
-
 def _check_sinks(window, sinks):
     if sinks < 0:
         raise ValueError("sinks must not be negative")
@@ -315,39 +311,16 @@ def _check_sinks(window, sinks):
         raise ValueError("sinks need a window (without one every token is visible)")
 
 
-def _device_index(t: torch.Tensor) -> int:
-    index = t.get_device()
-    if index < 0:
-        raise ValueError("the tensors must be on a CUDA device")
-    return index
-
-
-def _call(fn, index, *args):
-    """fn(*args) with the tensors' device current (the library launches there)."""
-    if torch.cuda.current_device() == index:
-        return fn(*args)
-    with torch.cuda.device(index):
-        return fn(*args)
-
-
-def _stream_handle(stream, index=None) -> int:
+def _stream_handle(stream) -> int:
     if stream is None:
-        if index is not None:  # the current stream's handle, without a Stream object
-            return torch._C._cuda_getCurrentRawStream(index)
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-# decattn_launch, field by field as Launch has them.
-_LAUNCH = struct.Struct("7i4xPQPP")
-
-
-def _launch_bytes(batch, num_blocks, block_size, max_blocks_per_seq, max_seq_len, num_splits,
-                  dtype, workspace, err_flag, stream) -> bytes:
-    return _LAUNCH.pack(batch, num_blocks, block_size, max_blocks_per_seq, max_seq_len, num_splits,
-                        dtype, 0 if workspace is None else workspace.data_ptr(),
-                        0 if workspace is None else workspace.numel(),
-                        0 if err_flag is None else err_flag.data_ptr(), stream)
+def _handle(stream) -> int | None:
+    """A given stream's handle; None stays: the native calls take the current
+    stream of the tensors' device."""
+    return None if stream is None else _stream_handle(stream)
 
 
 def make_launch(batch, num_blocks, block_size, max_blocks_per_seq, max_seq_len, num_splits,
@@ -369,45 +342,11 @@ def gqa_decode(q, k_cache, v_cache, block_table, seq_lens, *, scale: float, max_
     and with sinks > 0 to its first `sinks` tokens too (gqa_decode_sinks).
     """
     _check_sinks(window, sinks)
-    _check(q, "q", ndim=3)
-    _check(k_cache, "k_cache", q.dtype, 4)
-    _check(v_cache, "v_cache", q.dtype, 4)
-    _check(block_table, "block_table", torch.int32, 2)
-    _check(seq_lens, "seq_lens", torch.int32, 1)
-    if q.dtype not in _DT:
-        raise TypeError("q must be float16 or bfloat16")
-    B, h_q, d = q.shape
-    nb, bs, h_kv, d2 = k_cache.shape
-    if d2 != d or v_cache.shape != k_cache.shape:
-        raise ValueError("k_cache / v_cache shape mismatch")
-    if h_kv < 1 or h_q % h_kv != 0:
-        raise ValueError(f"h_q={h_q} is not a multiple of h_kv={h_kv}")
-    if out is None:
-        out = torch.empty_like(q)
-    if num_splits:
-        ns = num_splits
-    elif window is None:
-        ns = gqa_plan_splits(B, h_q, h_kv, max_seq_len, d)
-    else:
-        ns = gqa_sinks_plan_splits(B, h_q, h_kv, max_seq_len, window, sinks, bs, 2, d)
-    need = gqa_workspace_size(B, h_q, ns, d) if ns > 1 else 0
-    if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    L = _launch_bytes(B, nb, bs, block_table.shape[1], max_seq_len, ns, _DT[q.dtype], workspace,
-                      err_flag, _stream_handle(stream, torch.cuda.current_device()))
-    args = (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
-            seq_lens.data_ptr(), out.data_ptr(), h_q, h_kv, d, float(scale))
-    if window is None:
-        name, st = "gqa_decode", lib().gqa_decode(*args, L)
-    elif sinks:
-        name = "gqa_decode_sinks"
-        st = lib().gqa_decode_sinks(*args, int(window), int(sinks), L)
-    else:
-        name = "gqa_decode_window"
-        st = lib().gqa_decode_window(*args, int(window), L)
-    if st != DECATTN_OK:
-        raise DecAttnError(name, st)
-    return out
+    r = calls().decode(q, k_cache, v_cache, None, None, block_table, seq_lens, scale, max_seq_len,
+                       window, sinks, num_splits, out, workspace, err_flag, _handle(stream))
+    if type(r) is int:
+        raise DecAttnError(_decode_name("gqa_decode", window, sinks), r)
+    return r
 
 
 def gqa_decode_sinks(q, k_cache, v_cache, block_table, seq_lens, *, window: int, sinks: int, **kw):
@@ -432,50 +371,14 @@ def gqa_decode_fp8kv(q, k_codes, v_codes, k_scale, v_scale, block_table, seq_len
     (window: gqa_decode_fp8kv_window; sinks: gqa_decode_fp8kv_sinks).
     """
     _check_sinks(window, sinks)
-    _check(q, "q", ndim=3)
-    if q.dtype not in _DT:
-        raise TypeError("q must be float16 or bfloat16")
-    _check_codes(k_codes, "k_codes")
-    _check_codes(v_codes, "v_codes")
-    _check(k_scale, "k_scale", torch.float32, 1)
-    _check(v_scale, "v_scale", torch.float32, 1)
-    _check(block_table, "block_table", torch.int32, 2)
-    _check(seq_lens, "seq_lens", torch.int32, 1)
-    B, h_q, d = q.shape
-    nb, bs, h_kv, d2 = k_codes.shape
-    if d2 != d or v_codes.shape != k_codes.shape:
-        raise ValueError("k_codes / v_codes shape mismatch")
-    if k_scale.shape != (h_kv,) or v_scale.shape != (h_kv,):
-        raise ValueError("k_scale / v_scale must be [h_kv]")
-    if h_kv < 1 or h_q % h_kv != 0:
-        raise ValueError(f"h_q={h_q} is not a multiple of h_kv={h_kv}")
-    if out is None:
-        out = torch.empty_like(q)
-    if num_splits:
-        ns = num_splits
-    elif window is None:
-        ns = gqa_fp8_plan_splits(B, h_q, h_kv, max_seq_len, d)
-    else:
-        ns = gqa_sinks_plan_splits(B, h_q, h_kv, max_seq_len, window, sinks, bs, 1, d)
-    need = gqa_workspace_size(B, h_q, ns, d) if ns > 1 else 0
-    if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    L = _launch_bytes(B, nb, bs, block_table.shape[1], max_seq_len, ns, _DT[q.dtype], workspace,
-                      err_flag, _stream_handle(stream, torch.cuda.current_device()))
-    args = (q.data_ptr(), k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(),
-            v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(),
-            h_q, h_kv, d, float(scale))
-    if window is None:
-        name, st = "gqa_decode_fp8kv", lib().gqa_decode_fp8kv(*args, L)
-    elif sinks:
-        name = "gqa_decode_fp8kv_sinks"
-        st = lib().gqa_decode_fp8kv_sinks(*args, int(window), int(sinks), L)
-    else:
-        name = "gqa_decode_fp8kv_window"
-        st = lib().gqa_decode_fp8kv_window(*args, int(window), L)
-    if st != DECATTN_OK:
-        raise DecAttnError(name, st)
-    return out
+    if k_scale is None or v_scale is None:
+        raise TypeError("k_scale and v_scale must be torch.Tensors")
+    r = calls().decode(q, k_codes, v_codes, k_scale, v_scale, block_table, seq_lens, scale,
+                       max_seq_len, window, sinks, num_splits, out, workspace, err_flag,
+                       _handle(stream))
+    if type(r) is int:
+        raise DecAttnError(_decode_name("gqa_decode_fp8kv", window, sinks), r)
+    return r
 
 
 def gqa_decode_fp8kv_window(q, k_codes, v_codes, k_scale, v_scale, block_table, seq_lens, *,
@@ -566,44 +469,12 @@ def paged_plan(cached_lens, new_lens, block_table, free_blocks, free_count, *, b
     cached_lens (in place).  Rows past the step's last token get slot and
     position -1.
     """
-    _check(cached_lens, "cached_lens", torch.int32, 1)
-    _check(new_lens, "new_lens", torch.int32, 1)
-    _check(block_table, "block_table", torch.int32, 2)
-    _check(free_blocks, "free_blocks", torch.int32, 1)
-    _check(free_count, "free_count", torch.int32, 1)
-    B, index = cached_lens.shape[0], _device_index(cached_lens)
-    if new_lens.shape[0] != B or block_table.shape[0] != B or free_count.shape[0] != 1:
-        raise ValueError("paged_plan: shape mismatch")
-    if max_tokens < 0:
-        raise ValueError("max_tokens must not be negative")
-    _check_device(index, ("new_lens", new_lens), ("block_table", block_table),
-                  ("free_blocks", free_blocks), ("free_count", free_count))
-    _check_flag(err_flag, index)
-    outs = []
-    buf, at = None, 0  # what is not given is cut from one allocation
-    for t, name, n in ((seq_lens, "seq_lens", B), (q_start, "q_start", B + 1),
-                       (slots, "slots", max_tokens), (positions, "positions", max_tokens),
-                       (free_count_out, "free_count_out", 1)):
-        if t is None:
-            if buf is None:
-                buf = torch.empty(2 * (B + max_tokens + 1), dtype=torch.int32,
-                                  device=cached_lens.device)
-            t = buf[at: at + n]
-            at += n
-        else:
-            _check(t, name, torch.int32, 1)
-            if t.shape[0] != n or t.get_device() != index:
-                raise ValueError(f"{name}: expected [{n}] on cuda:{index}")
-        outs.append(t)
-    L = _launch_bytes(B, free_blocks.shape[0], block_size, block_table.shape[1], 0, 1,
-                      DECATTN_FP16, None, err_flag, _stream_handle(stream, index))
-    st = _call(lib().paged_plan, index, cached_lens.data_ptr(), new_lens.data_ptr(),
-               block_table.data_ptr(), free_blocks.data_ptr(), free_count.data_ptr(),
-               outs[4].data_ptr(), outs[0].data_ptr(), outs[1].data_ptr(), outs[2].data_ptr(),
-               outs[3].data_ptr(), max_tokens, L)
-    if st != DECATTN_OK:
-        raise DecAttnError("paged_plan", st)
-    return PagedPlan(*outs)
+    r = calls().paged_plan(cached_lens, new_lens, block_table, free_blocks, free_count, block_size,
+                           max_tokens, seq_lens, q_start, slots, positions, free_count_out,
+                           err_flag, _handle(stream))
+    if type(r) is int:
+        raise DecAttnError("paged_plan", r)
+    return PagedPlan(*r)
 
 
 def rope_table(inv_freq, *, sections=None, interleaved: bool = False, device=None) -> RopeTable:
@@ -628,72 +499,15 @@ def rope_table(inv_freq, *, sections=None, interleaved: bool = False, device=Non
     return rope
 
 
-def _packed_rows(t, name, dtype):
-    """A [tokens, heads, 128] tensor whose heads are contiguous within a token
-    (a part of a wider projection's output will do): its shape and token stride."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dim() != 3:
-        raise ValueError(f"{name}: expected 3 dims, got shape {tuple(t.shape)}")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    (T, h, d), (st, sh, sd) = t.shape, t.stride()
-    if T * h * d and ((d > 1 and sd != 1) or (h > 1 and sh != d)):
-        raise ValueError(f"{name}: a token's heads must be contiguous")
-    return T, h, d, st if T > 1 else h * d
-
-
-def _rope_append(fp8, q, k_new, v_new, scales, positions, rope, slots, k_cache, v_cache, q_out,
-                 err_flag, stream):
-    name = "gqa_rope_append_fp8kv" if fp8 else "gqa_rope_append"
-    T, h_q, d, qs = _packed_rows(q, "q", None)
-    dtype = q.dtype
-    if dtype not in _DT:
-        raise TypeError("q must be float16 or bfloat16")
-    Tk, h_kv, dk, ks = _packed_rows(k_new, "k_new", dtype)
-    Tv, hv, dv, vs = _packed_rows(v_new, "v_new", dtype)
+def _rope_append(name, q, k_new, v_new, k_scale, v_scale, positions, rope, slots, k_cache, v_cache,
+                 q_out, err_flag, stream):
     if not isinstance(rope, RopeTable):
         raise TypeError("rope must come from rope_table")
-    _check(positions, "positions", torch.int32)
-    _check(slots, "slots", torch.int32, 1)
-    if fp8:
-        _check_codes(k_cache, "k_codes")
-        _check_codes(v_cache, "v_codes")
-    else:
-        _check(k_cache, "k_cache", dtype, 4)
-        _check(v_cache, "v_cache", dtype, 4)
-    nb, bs, hc, dc = k_cache.shape
-    if Tk != T or dk != d or Tv != T or hv != h_kv or dv != d or hc != h_kv or dc != d or \
-            v_cache.shape != k_cache.shape or slots.shape[0] != T:
-        raise ValueError(f"{name}: shape mismatch")
-    if positions.shape != (rope.n_axes, T) and not (rope.n_axes == 1 and positions.shape == (T,)):
-        raise ValueError(f"positions must be [{rope.n_axes}, {T}]")
-    index = _device_index(q)
-    for n, s in (("k_scale", scales[0]), ("v_scale", scales[1])) if fp8 else ():
-        _check(s, n, torch.float32, 1)
-        if s.shape[0] != h_kv:
-            raise ValueError(f"{n} must be [h_kv]")
-        _check_device(index, (n, s))
-    _check_device(index, ("k_new", k_new), ("v_new", v_new), ("positions", positions),
-                  ("slots", slots), ("k_cache", k_cache), ("v_cache", v_cache))
-    _check_flag(err_flag, index)
-    if q_out is None:
-        q_out = torch.empty((T, h_q, d), dtype=dtype, device=q.device)
-    else:
-        _check_out(q_out, "q_out", dtype, (T, h_q, d), index)
-    L = _launch_bytes(1, nb, bs, 1, 0, 1, _DT[dtype], None, err_flag,
-                      _stream_handle(stream, index))
-    tail = (positions.data_ptr(), ctypes.byref(rope), slots.data_ptr(), q_out.data_ptr(),
-            k_cache.data_ptr(), v_cache.data_ptr(), T, h_q, h_kv, d, L)
-    head = (q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), qs, ks, vs)
-    if fp8:
-        st = _call(lib().gqa_rope_append_fp8kv, index, *head, scales[0].data_ptr(),
-                   scales[1].data_ptr(), *tail)
-    else:
-        st = _call(lib().gqa_rope_append, index, *head, *tail)
-    if st != DECATTN_OK:
-        raise DecAttnError(name, st)
-    return q_out
+    r = calls().rope_append(q, k_new, v_new, k_scale, v_scale, positions, ctypes.addressof(rope),
+                            rope.n_axes, slots, k_cache, v_cache, q_out, err_flag, _handle(stream))
+    if type(r) is int:
+        raise DecAttnError(name, r)
+    return r
 
 
 def gqa_rope_append(q, k_new, v_new, positions, rope, slots, k_cache, v_cache, *, q_out=None,
@@ -706,81 +520,31 @@ def gqa_rope_append(q, k_new, v_new, positions, rope, slots, k_cache, v_cache, *
     [n_axes, T] (or [T]); rope: rope_table's; slots int32 [T] (negative: no
     cache row); q_out: a contiguous [T, h_q, d], may be q.
     """
-    return _rope_append(False, q, k_new, v_new, None, positions, rope, slots, k_cache, v_cache,
-                        q_out, err_flag, stream)
+    return _rope_append("gqa_rope_append", q, k_new, v_new, None, None, positions, rope, slots,
+                        k_cache, v_cache, q_out, err_flag, stream)
 
 
 def gqa_rope_append_fp8kv(q, k_new, v_new, k_scale, v_scale, positions, rope, slots, k_codes,
                           v_codes, *, q_out=None, err_flag=None, stream=None):
     """gqa_rope_append into an 8-bit e4m3 cache (uint8 or float8_e4m3fn) with
     one scale per KV head."""
-    return _rope_append(True, q, k_new, v_new, (k_scale, v_scale), positions, rope, slots,
-                        k_codes, v_codes, q_out, err_flag, stream)
+    if k_scale is None or v_scale is None:
+        raise TypeError("k_scale and v_scale must be torch.Tensors")
+    return _rope_append("gqa_rope_append_fp8kv", q, k_new, v_new, k_scale, v_scale, positions, rope,
+                        slots, k_codes, v_codes, q_out, err_flag, stream)
 
 
-def _prefill(fp8, q, k_cache, v_cache, scales, block_table, q_start, seq_lens, scale, max_q_len,
-             max_seq_len, window, sinks, out, num_splits, workspace, err_flag, stream):
-    name = "gqa_prefill_fp8kv" if fp8 else "gqa_prefill"
-    _check(q, "q", ndim=3)
-    if q.dtype not in _DT:
-        raise TypeError("q must be float16 or bfloat16")
-    if fp8:
-        _check_codes(k_cache, "k_codes")
-        _check_codes(v_cache, "v_codes")
-    else:
-        _check(k_cache, "k_cache", q.dtype, 4)
-        _check(v_cache, "v_cache", q.dtype, 4)
-    _check(block_table, "block_table", torch.int32, 2)
-    _check(q_start, "q_start", torch.int32, 1)
-    _check(seq_lens, "seq_lens", torch.int32, 1)
+def _prefill(name, q, k_cache, v_cache, k_scale, v_scale, block_table, q_start, seq_lens, scale,
+             max_q_len, max_seq_len, window, sinks, out, num_splits, workspace, err_flag, stream):
     _check_sinks(window, sinks)
     if window is not None and window < 1:
         raise ValueError("window must be at least 1")
-    T, h_q, d = q.shape
-    nb, bs, h_kv, d2 = k_cache.shape
-    B = seq_lens.shape[0]
-    if d2 != d or v_cache.shape != k_cache.shape:
-        raise ValueError("k_cache / v_cache shape mismatch")
-    if block_table.shape[0] != B or q_start.shape != (B + 1,):
-        raise ValueError("block_table must be [B, max_blocks] and q_start [B + 1]")
-    if h_kv < 1 or h_q % h_kv != 0:
-        raise ValueError(f"h_q={h_q} is not a multiple of h_kv={h_kv}")
-    index = _device_index(q)
-    for n, s in (("k_scale", scales[0]), ("v_scale", scales[1])) if fp8 else ():
-        _check(s, n, torch.float32, 1)
-        if s.shape[0] != h_kv:
-            raise ValueError(f"{n} must be [h_kv]")
-        _check_device(index, (n, s))
-    _check_device(index, ("k_cache", k_cache), ("v_cache", v_cache),
-                  ("block_table", block_table), ("q_start", q_start), ("seq_lens", seq_lens))
-    _check_flag(err_flag, index)
-    if out is None:
-        out = torch.empty_like(q)
-    else:
-        _check_out(out, "out", q.dtype, q.shape, index)
-    ns = num_splits
-    if ns == 0:
-        ns = _call(gqa_prefill_plan_splits, index, B, T, max_q_len, h_q, h_kv, max_seq_len,
-                   window or 0, sinks, d)
-    need = gqa_prefill_workspace_size(T, h_q, ns, d) if T and ns > 1 else 0
-    if workspace is not None:
-        _check(workspace, "workspace", torch.uint8)
-        _check_device(index, ("workspace", workspace))
-    elif need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    L = _launch_bytes(B, nb, bs, block_table.shape[1], max_seq_len, ns, _DT[q.dtype], workspace,
-                      err_flag, _stream_handle(stream, index))
-    head = (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr())
-    tail = (block_table.data_ptr(), q_start.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), T,
-            max_q_len, h_q, h_kv, d, float(scale), window or 0, sinks, L)
-    if fp8:
-        st = _call(lib().gqa_prefill_fp8kv, index, *head, scales[0].data_ptr(),
-                   scales[1].data_ptr(), *tail)
-    else:
-        st = _call(lib().gqa_prefill, index, *head, *tail)
-    if st != DECATTN_OK:
-        raise DecAttnError(name, st)
-    return out
+    r = calls().prefill(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, q_start,
+                        scale, max_q_len, max_seq_len, window or 0, sinks, num_splits, out,
+                        workspace, err_flag, _handle(stream))
+    if type(r) is int:
+        raise DecAttnError(name, r)
+    return r
 
 
 def gqa_prefill(q, k_cache, v_cache, block_table, q_start, seq_lens, *, scale: float,
@@ -796,9 +560,9 @@ def gqa_prefill(q, k_cache, v_cache, block_table, q_start, seq_lens, *, scale: f
     `sinks` where a window is given.  max_q_len, max_seq_len: host upper
     bounds.  Rows outside every sequence are not written.
     """
-    return _prefill(False, q, k_cache, v_cache, None, block_table, q_start, seq_lens, scale,
-                    max_q_len, max_seq_len, window, sinks, out, num_splits, workspace, err_flag,
-                    stream)
+    return _prefill("gqa_prefill", q, k_cache, v_cache, None, None, block_table, q_start, seq_lens,
+                    scale, max_q_len, max_seq_len, window, sinks, out, num_splits, workspace,
+                    err_flag, stream)
 
 
 def gqa_prefill_fp8kv(q, k_codes, v_codes, k_scale, v_scale, block_table, q_start, seq_lens, *,
@@ -807,9 +571,11 @@ def gqa_prefill_fp8kv(q, k_codes, v_codes, k_scale, v_scale, block_table, q_star
                       err_flag=None, stream=None):
     """gqa_prefill over an 8-bit e4m3 cache (uint8 or float8_e4m3fn) with one
     scale per KV head."""
-    return _prefill(True, q, k_codes, v_codes, (k_scale, v_scale), block_table,
-                    q_start, seq_lens, scale, max_q_len, max_seq_len, window, sinks, out,
-                    num_splits, workspace, err_flag, stream)
+    if k_scale is None or v_scale is None:
+        raise TypeError("k_scale and v_scale must be torch.Tensors")
+    return _prefill("gqa_prefill_fp8kv", q, k_codes, v_codes, k_scale, v_scale, block_table, q_start,
+                    seq_lens, scale, max_q_len, max_seq_len, window, sinks, out, num_splits,
+                    workspace, err_flag, stream)
 
 
 def mla_kv_append(latent_new, positions, block_table, latent_cache, *, err_flag=None,
