@@ -929,6 +929,7 @@ static int gqa_prefill_impl(const void* q, const void* k_cache, const void* v_ca
   if (items * h_kv * ns > 0x7fffffffLL || static_cast<int64_t>(tokens) * h_q > 0x7fffffffLL)
     return DECATTN_ERR_UNSUPPORTED;
   PrefillParams p{};
+  p.q = q;
   p.block_table = block_table;
   p.q_start = q_start;
   p.seq_lens = seq_lens;

@@ -51,11 +51,13 @@
 // of their own, joined at the end through shared memory: 32 chunks of up to 8
 // tokens over 8k caches (64 heads, 8 KV heads) MEASURED.
 //
-// An 8-bit (e4m3) cache takes the same pipeline on fp16 operands: the ring
-// holds four 16 KB tiles of codes, and warps 10 and 11 convert each K and V
-// tile (exactly) into one of two 16-bit tiles; a bf16 Q is rewritten as fp16 in
-// place (exact within fp16's range).  K's scale joins the score scale, V's the
-// final division.
+// An 8-bit (e4m3) cache takes the same pipeline with four changes: the K tile's
+// codes, as they land, are the B operand of S on kind::f8f6f4, whose A operand is
+// Q as two (bf16) or three (fp16) e4m3 terms that the softmax warps make of their
+// rows; warps 10 and 11 convert each V tile to fp16; P is fp16; K's scale and
+// Q's row exponents join the score scale, V's scale the final division.  (With K
+// converted too, a tile took 4800 cycles, bound by the conversion; shared memory
+// is what a converter waits for: the MMAs' operands take most of its bandwidth.)
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -69,6 +71,7 @@ constexpr int kTileBytes = 2 * kHalf;          // 32 KB
 constexpr int kRing = 4;
 constexpr int kOffRing = 2 * kTileBytes;       // behind Q_A, Q_B
 constexpr int kOffStage = kOffRing + kRing * kTileBytes;
+constexpr int kCodeBytes = kTileBytes / 2;     // a tile, or a term of Q, in e4m3 codes
 constexpr int kStageBytes = 32 * 128;          // one softmax warp's: 32 rows x 128 B
 constexpr int kOffBars = kOffStage + 8 * kStageBytes;
 constexpr int kOffMerge = kOffBars + 1024;     // 128 rows' (maximum, sum), see `solo`
@@ -94,9 +97,8 @@ enum : int {
   kBarItem = kBarO + 2,         // 2: piece published
   kBarItemFree = kBarItem + 2,  // 2: piece done by every other role
   kBarNext = kBarItemFree + 2,  // the launch control's answer
-  kBarQ16 = kBarNext + 1,       // 8-bit cache: bf16 Q rewritten as fp16 (64 arrivals)
-  kBarFull16 = kBarQ16 + 1,     // 8-bit cache, K and V: converted (32 arrivals)
-  kBarEmpty16 = kBarFull16 + 2, // 8-bit cache, K and V: 16-bit tile free
+  kBarFull16 = kBarNext + 1,    // 8-bit cache, 2: fp16 V tile converted (64 arrivals)
+  kBarEmpty16 = kBarFull16 + 2, // 8-bit cache, 2: fp16 V tile free
   kBarPair = kBarEmpty16 + 2,   // 4: the two softmax warps of the same rows (solo)
   kBarDrain = kBarPair + 4,
   kNumBars = kBarDrain + 1
@@ -106,6 +108,7 @@ enum : int {
 constexpr int kOffWords = kOffBars + 288;   // abort, bad, copies made by the producers, TMEM
 constexpr int kOffAnswer = kOffBars + 352;  // the launch control's answer, 16 bytes
 constexpr int kOffItems = kOffBars + 416;   // two pieces
+constexpr int kOffQExp = kOffBars + 640;    // 8-bit cache: Q's row exponents, 2 x 128 bytes
 static_assert(kNumBars * 8 <= 288, "barriers");
 
 // A piece of work: rows of one sequence and KV head against a range of tiles.
@@ -124,7 +127,7 @@ struct Item {
   int solo;         // one Q tile: the warps of tile B take every other K / V tile
   int bad;
 };
-static_assert(2 * sizeof(Item) <= 1024 - 416, "items");
+static_assert(2 * sizeof(Item) <= 640 - 416, "items");
 
 struct Tile {
   int t0, skip, nval;  // rows [skip, nval) hold tokens that may be seen
@@ -268,13 +271,96 @@ __device__ __forceinline__ uint4* staged(uint8_t* stage, int row, int c) {
   return reinterpret_cast<uint4*>(stage + row * 128 + ((c ^ (row & 7)) << 4));
 }
 
+// 32 rows of a Q tile as sums of kTerms e4m3 values of row r times alpha_r = 2^k
+// (the largest power of two with max |q_r| alpha_r <= 448): t1 = e4m3(x), t2 =
+// e4m3(x - t1), ...  Each remainder is a multiple of the query's own last bit
+// no larger than half of the term's step, so two terms hold a bf16 query and
+// three an fp16 one exactly, but for parts below 2^-10 (e4m3's smallest step) of
+// the scaled row.  Term t of the tile: [128 rows][128 codes], 128-byte swizzle;
+// k goes to qexp[r].  16 lanes take a row, 8 values each.
+template <bool kBF16, int kTerms>
+__device__ __forceinline__ void split_q(const PrefillParams& p, const Item& w, int x, int part,
+                                        uint32_t inv_g, uint8_t* dst, int8_t* qexp) {
+  const int lane = threadIdx.x & 31, c = lane & 15;
+  const int rows = (x ? w.tok_b : w.tok_a) * p.group;
+  const uint16_t* src =
+      static_cast<const uint16_t*>(p.q) +
+      (static_cast<int64_t>(w.q0 + w.i0 + x * p.tokens_per_tile) * p.h_q + w.j * p.group) * kHeadDim +
+      8 * c;
+  // The group's next four rows are on their way while four are split.
+  auto load = [&](int b, uint4 (&y)[4]) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int r = 32 * part + 2 * (b + u) + (lane >> 4);
+      const int tk = static_cast<int>((static_cast<uint32_t>(r) * inv_g) >> 16);
+      y[u] = b < 16 && r < rows
+                 ? *reinterpret_cast<const uint4*>(
+                       src + static_cast<int64_t>(tk * (p.h_q - p.group) + r) * kHeadDim)
+                 : make_uint4(0, 0, 0, 0);
+    }
+  };
+  uint4 y[4], ahead[4];
+  load(0, y);
+#pragma unroll 1
+  for (int b = 0; b < 16; b += 4) {
+    load(b + 4, ahead);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int r = 32 * part + 2 * (b + u) + (lane >> 4);
+      float v[8];
+      const uint32_t in[4] = {y[u].x, y[u].y, y[u].z, y[u].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = unpack2<kBF16>(in[k]);
+        v[2 * k] = f.x;
+        v[2 * k + 1] = f.y;
+      }
+      float m = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) m = fmaxf(m, fabsf(v[k]));
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      const uint32_t bits = __float_as_uint(m);
+      const int ex = static_cast<int>((bits >> 23) & 0xffu) - 127;
+      const int k2 = min(max(((bits & 0x7fffffu) <= 0x600000u ? 8 : 7) - ex, -126), 126);
+      const float alpha = __uint_as_float(static_cast<uint32_t>(k2 + 127) << 23);
+      if (c == 0) qexp[r] = static_cast<int8_t>(k2);
+      uint32_t code[kTerms][2] = {};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float a0 = v[2 * k] * alpha, a1 = v[2 * k + 1] * alpha;
+#pragma unroll
+        for (int t = 0; t < kTerms; ++t) {
+          float r0, r1;
+          code[t][k >> 1] |= e4m3_round2(a0, a1, r0, r1) << (16 * (k & 1));
+          a0 -= r0;
+          a1 -= r1;
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < kTerms; ++t)
+        *reinterpret_cast<uint2*>(dst + t * kCodeBytes + r * 128 + (((c >> 1) ^ (r & 7)) << 4) +
+                                  (c & 1) * 8) = make_uint2(code[t][0], code[t][1]);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) y[u] = ahead[u];
+  }
+}
+
 // kF8: the cache holds e4m3 codes with per-KV-head scales.
 template <bool kBF16, bool kF8>
 __global__ void __launch_bounds__(kThreads, 1)
     gqa_prefill_kernel(const __grid_constant__ CUtensorMap tm_q,
                        const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const PrefillParams p) {
-  constexpr bool kMmaBF16 = kBF16 && !kF8;  // operand type of both products
+  constexpr bool kMmaBF16 = kBF16 && !kF8;  // operand type of the 16-bit products
+  // 8-bit cache: a bf16 query is two e4m3 terms, an fp16 one three; behind Q
+  // the ring of codes, then what is left below the staging for fp16 V tiles.
+  constexpr int kTerms = kBF16 ? 2 : 3;
+  constexpr int kRingAt = kF8 ? 2 * kTerms * kCodeBytes : kOffRing;
+  constexpr int kV16At = kRingAt + kRing * kCodeBytes;
+  constexpr int kV16 = (kOffStage - kV16At) / kTileBytes;
+  static_assert(!kF8 || (kV16 >= 1 && kV16 <= 2), "fp16 V tiles");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -290,11 +376,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int G = p.group;
 
   if (threadIdx.x == 0) {
-    mbar_init(bar(kBarQ), 1);
+    mbar_init(bar(kBarQ), kF8 ? 256 : 1);  // the copies, or every softmax thread
     mbar_init(bar(kBarQFree), 1);
     for (int s = 0; s < kRing; ++s) {
       mbar_init(bar(kBarFull + s), 1);
-      mbar_init(bar(kBarEmpty + s), 1);
+      mbar_init(bar(kBarEmpty + s), kF8 && (s & 1) ? 2 : 1);  // (V codes: two converters)
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(bar(kBarS + x), 1);
@@ -304,11 +390,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(kBarItem + x), 1);
       // V producer or the two converters, MMA, softmax
       mbar_init(bar(kBarItemFree + x), kF8 ? 11 : 10);
-      mbar_init(bar(kBarFull16 + x), 32);
+      mbar_init(bar(kBarFull16 + x), 64);
       mbar_init(bar(kBarEmpty16 + x), 1);
     }
     mbar_init(bar(kBarNext), 1);
-    mbar_init(bar(kBarQ16), 64);
     for (int x = 0; x < 4; ++x) mbar_init(bar(kBarPair + x), 64);
     mbar_init(bar(kBarDrain), 1);
     for (int k = 0; k < 6; ++k) abort_word[k] = 0;
@@ -354,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(lead ? &tm_k : &tm_v);
       }
       const int bs = p.block_size, lg = p.log2_block_size;
-      constexpr int kBytes = kF8 ? kTileBytes / 2 : kTileBytes;  // of a tile
+      constexpr int kBytes = kF8 ? kCodeBytes : kTileBytes;  // of a tile
       // K(it) is the ring's copy 2 it, V(it) the copy 2 it + 1, counted over
       // all pieces: slot and phase parity of this warp's next one, and the
       // numbers it made.
@@ -413,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         const int n = max(w.n_a, w.n_b);
-        if (n > 0 && lead) {
+        if (!kF8 && n > 0 && lead) {
           if (lane == 0) {
             ok = mbar_wait_or_abort(bar(kBarQFree), (q_loads & 1) ^ 1, p.err_flag, abort_word);
             if (ok) {
@@ -463,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane < nblk) {
               const CUtensorMap* tm = kv ? &tm_v : &tm_k;
               const uint32_t dst =
-                  sbase + kOffRing + slot * kBytes + static_cast<uint32_t>(lane * bs * 128);
+                  sbase + kRingAt + slot * kBytes + static_cast<uint32_t>(lane * bs * 128);
               tma_load_2d_hint(dst, tm, x0, row, bar(kBarFull + slot), keep);
               if (!kF8) tma_load_2d_hint(dst + kHalf, tm, x0 + 64, row, bar(kBarFull + slot), keep);
             }
@@ -487,64 +572,44 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     } else if (kF8 && (warp == kWarpV || warp == kWarpTmem)) {
-      // ---------------- converters (8-bit cache): warp 10 the K tiles, 11 the
-      // V tiles, [128 tokens][128 codes] to [2 halves][128 tokens][128 B], both
-      // with 128-byte swizzle; e4m3 -> fp16 is exact.  V rows outside
-      // [skip, nval) become zeros (their slots may hold NaN codes).  A bf16 Q is
-      // rewritten as fp16 in place, one tile by each.
-      const int kv = warp == kWarpV ? 0 : 1;
-      uint8_t* dst = smem + kOffRing + (2 + kv) * kTileBytes;
-      int slot = kv, q_loads = 0;
-      uint32_t phase = 0, phase16 = 0;
+      // ---------------- converters (8-bit cache): each V tile's [128 tokens][128
+      // codes] to fp16 [2 halves][128 tokens][128 B], both with 128-byte swizzle,
+      // warp 10 the first 64 tokens, 11 the others; e4m3 -> fp16 is exact.  Rows
+      // outside [skip, nval) become zeros (their slots may hold NaN codes).
+      const int part = warp == kWarpV ? 0 : 1;
+      int c = 0;  // tiles, over all pieces
       bool ok = true;
       Item w;
       for (int k = 0; ok && get_item(k, w); ++k) {
-        const int n = max(w.n_a, w.n_b);
-        if (kBF16 && n > 0) {
-          ok = mbar_wait_or_abort(bar(kBarQ), q_loads++ & 1, p.err_flag, abort_word);
+        const int n = max(w.n_a, w.n_b), full_from = full_lo(w), full_to = full_hi(w);
+        for (int it = 0; it < n; ++it, ++c) {
+          const int from = (2 * c + 1) % kRing, to = c % kV16;
+          ok = mbar_wait_or_abort(bar(kBarFull + from), (2 * c / kRing) & 1, p.err_flag,
+                                  abort_word) &&
+               mbar_wait_or_abort(bar(kBarEmpty16 + to), (c / kV16 & 1) ^ 1, p.err_flag, abort_word);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          if (kv == 0 || w.tok_b > 0) {
-            uint4* q = reinterpret_cast<uint4*>(smem + kv * kTileBytes);
-#pragma unroll 1
-            for (int e = lane; e < kTileBytes / 16; e += 8 * 32) {
-              uint4 y[8];
-#pragma unroll
-              for (int u = 0; u < 8; ++u) y[u] = q[e + 32 * u];
-#pragma unroll
-              for (int u = 0; u < 8; ++u) {
-                const float2 a = unpack2<true>(y[u].x), b = unpack2<true>(y[u].y),
-                             d = unpack2<true>(y[u].z), f = unpack2<true>(y[u].w);
-                q[e + 32 * u] = make_uint4(pack2<false>(a.x, a.y), pack2<false>(b.x, b.y),
-                                           pack2<false>(d.x, d.y), pack2<false>(f.x, f.y));
-              }
-            }
+          int lo = 0, hi = kKv;
+          if (it * kKv < full_from || it * kKv + kKv > full_to) {
+            const Tile t = tile_of(w, it);
+            lo = t.skip;
+            hi = t.nval;
           }
-          fence_proxy_async_smem();
-          mbar_arrive(bar(kBarQ16));
-        }
-        for (int it = 0; it < n; ++it) {
-          ok = mbar_wait_or_abort(bar(kBarFull + slot), phase, p.err_flag, abort_word) &&
-               mbar_wait_or_abort(bar(kBarEmpty16 + kv), phase16 ^ 1u, p.err_flag, abort_word);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          const Tile t = tile_of(w, it);
-          const uint8_t* src = smem + kOffRing + slot * (kTileBytes / 2);
-          const int lo = kv ? t.skip : 0, hi = kv ? t.nval : kKv;
-          // Lane: 16 codes c = lane % 8 of rows lane / 8, + 4, ...; its two
-          // output pieces are 2 (c % 4) and the next one of half c / 4, the
-          // odd one first for c >= 4 (no bank is hit twice).
-          const int c = lane & 7, odd = c >> 2;
-          const int c0 = 2 * (c & 3);
+          const uint8_t* src = smem + kRingAt + from * kCodeBytes;
+          // Lane: 16 codes e = lane % 8 of rows lane / 8, + 4, ...; its two
+          // output pieces are 2 (e % 4) and the next one of half e / 4, the
+          // odd one first for e >= 4 (no bank is hit twice).
+          const int e = lane & 7, odd = e >> 2, e0 = 2 * (e & 3);
+          uint8_t* dst = smem + kV16At + to * kTileBytes + odd * kHalf;
           // (Eight rows are read before any is written: a load does not pass a
           // store to shared memory by itself.)
 #pragma unroll 1
-          for (int r0 = lane >> 3; r0 < kKv; r0 += 32) {
+          for (int r0 = 64 * part + (lane >> 3); r0 < 64 * part + 64; r0 += 32) {
             uint4 y[8];
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
               const int r = r0 + 4 * u;
-              y[u] = *reinterpret_cast<const uint4*>(src + r * 128 + ((c ^ (r & 7)) << 4));
+              y[u] = *reinterpret_cast<const uint4*>(src + r * 128 + ((e ^ (r & 7)) << 4));
             }
             if (lo > 0 || hi < kKv) {
 #pragma unroll
@@ -559,21 +624,15 @@ __global__ void __launch_bounds__(kThreads, 1)
               e4m3x4_to_f16x2(y[u].y, a.z, a.w);
               e4m3x4_to_f16x2(y[u].z, b.x, b.y);
               e4m3x4_to_f16x2(y[u].w, b.z, b.w);
-              uint8_t* o = dst + odd * kHalf + r * 128;
-              *reinterpret_cast<uint4*>(o + (((c0 + odd) ^ (r & 7)) << 4)) = odd ? b : a;
-              *reinterpret_cast<uint4*>(o + (((c0 + 1 - odd) ^ (r & 7)) << 4)) = odd ? a : b;
+              uint8_t* o = dst + r * 128;
+              *reinterpret_cast<uint4*>(o + (((e0 + odd) ^ (r & 7)) << 4)) = odd ? b : a;
+              *reinterpret_cast<uint4*>(o + (((e0 + 1 - odd) ^ (r & 7)) << 4)) = odd ? a : b;
             }
           }
           fence_proxy_async_smem();
-          mbar_arrive(bar(kBarFull16 + kv));
+          mbar_arrive(bar(kBarFull16 + to));
           __syncwarp();
-          if (lane == 0) mbar_arrive(bar(kBarEmpty + slot));
-          phase16 ^= 1u;
-          slot += 2;
-          if (slot >= kRing) {
-            slot -= kRing;
-            phase ^= 1u;
-          }
+          if (lane == 0) mbar_arrive(bar(kBarEmpty + from));
         }
         if (ok) release_item(k);
       }
@@ -582,9 +641,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------- MMA issuer: the whole warp runs the loop, lane 0
       // waits, one elected lane issues.
       const uint64_t dq = smem_desc_sw128(sbase, 16, 1024);
-      const uint64_t dk = smem_desc_sw128(sbase + kOffRing, 16, 1024);
-      const uint64_t dv = smem_desc_sw128(sbase + kOffRing, kHalf, 1024);
-      constexpr uint32_t idesc_s = idesc_f16(kMmaBF16, kM, kKv, false, false);
+      const uint64_t dk = smem_desc_sw128(sbase + kRingAt, 16, 1024);
+      const uint64_t dv = smem_desc_sw128(sbase + (kF8 ? kV16At : kOffRing), kHalf, 1024);
+      constexpr uint32_t idesc_s =
+          kF8 ? idesc_e4m3(kM, kKv) : idesc_f16(kMmaBF16, kM, kKv, false, false);
       constexpr uint32_t idesc_o = idesc_f16(kMmaBF16, kM, kHeadDim, false, true);
       // All lanes probe; lane 0 waits where that does not succeed at once.
       auto wait = [&](int bi, uint32_t parity) -> bool {
@@ -596,20 +656,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         return g;
       };
-      auto free_bar = [](int s) { return kF8 ? kBarEmpty16 + s - 2 : kBarEmpty + s; };
-      // S_X = Q_X K^T (Q tile q): eight k-steps of 16 dims, four per 64-column half.
+      // S_X = Q_X K^T (Q tile q): eight k-steps of 16 dims, four per 64-column
+      // half; 8-bit: for each term of Q four k-steps of 32 dims on the codes.
       // `last`: no other tile reads this K slot after this one; `end`: this is
       // the piece's last S.
       auto issue_s = [&](int x, int q, int s, bool last, bool end) {
-        const uint64_t a = dq + static_cast<uint64_t>((q * kTileBytes) >> 4);
-        const uint64_t b = dk + static_cast<uint64_t>((s * kTileBytes) >> 4);
-        const uint32_t done = bar(kBarS + x), empty = bar(free_bar(s)), q_free = bar(kBarQFree);
+        constexpr int kQTile = kF8 ? kTerms * kCodeBytes : kTileBytes;
+        const uint64_t a = dq + static_cast<uint64_t>((q * kQTile) >> 4);
+        const uint64_t b = dk + static_cast<uint64_t>((s * (kF8 ? kCodeBytes : kTileBytes)) >> 4);
+        const uint32_t done = bar(kBarS + x), empty = bar(kBarEmpty + s), q_free = bar(kBarQFree);
         const uint32_t d = tmem + kTmemS + kKv * x;
         if (elect_one()) {
+          if constexpr (kF8) {
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks) {
-            const uint64_t off = static_cast<uint64_t>(((ks >> 2) * kHalf + (ks & 3) * 32) >> 4);
-            tc_mma_f16(d, a + off, b + off, idesc_s, ks > 0 ? 1u : 0u);
+            for (int t = 0; t < kTerms; ++t)
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks)
+                tc_mma_f8(d, a + static_cast<uint64_t>((t * kCodeBytes + ks * 32) >> 4),
+                          b + static_cast<uint64_t>((ks * 32) >> 4), idesc_s,
+                          (t | ks) > 0 ? 1u : 0u);
+          } else {
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks) {
+              const uint64_t off = static_cast<uint64_t>(((ks >> 2) * kHalf + (ks & 3) * 32) >> 4);
+              tc_mma_f16(d, a + off, b + off, idesc_s, ks > 0 ? 1u : 0u);
+            }
           }
           tc_commit(done);
           if (last) tc_commit(empty);
@@ -625,7 +696,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t b = dv + static_cast<uint64_t>((s * kTileBytes) >> 4);
         const uint32_t acc0 = first ? 0u : 1u;
         const uint32_t d = tmem + kTmemO + kHeadDim * x, a = tmem + kTmemS + kKv * x;
-        const uint32_t full = bar(kBarO + x), empty = bar(free_bar(s));
+        const uint32_t full = bar(kBarO + x), empty = bar(kF8 ? kBarEmpty16 + s : kBarEmpty + s);
         if (elect_one()) {
 #pragma unroll
           for (int k4 = 0; k4 < 4; ++k4) {
@@ -640,18 +711,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       };
-      // The c-th tile of all pieces: 16-bit cache, K and V go round the ring's
-      // four slots; 8-bit, the converted K and V tiles are slots 2 and 3.
-      auto k_slot = [](int c) { return kF8 ? 2 : (2 * c) % kRing; };
-      auto v_slot = [](int c) { return kF8 ? 3 : (2 * c + 1) % kRing; };
-      auto phase_of = [](int c) { return static_cast<uint32_t>((kF8 ? c : 2 * c / kRing) & 1); };
-      auto full = [&](int s) { return kF8 ? kBarFull16 + s - 2 : kBarFull + s; };
-      auto wait_k = [&](int c) { return wait(full(k_slot(c)), phase_of(c)); };
+      // The c-th tile of all pieces: K and V go round the ring's four slots (an
+      // 8-bit cache's V then into one of the fp16 tiles).
+      auto k_slot = [](int c) { return (2 * c) % kRing; };
+      auto v_slot = [](int c) { return kF8 ? c % kV16 : (2 * c + 1) % kRing; };
+      auto phase_of = [](int c) { return static_cast<uint32_t>((2 * c / kRing) & 1); };
+      auto wait_k = [&](int c) { return wait(kBarFull + k_slot(c), phase_of(c)); };
       // V rows outside [skip, nval) become zeros (P is 0 there, but the slots
       // may hold NaN), while the softmax works on the tile.  (All 128 bytes of
       // a row: the swizzle does not matter.)
       auto wait_v = [&](int c, const Item& w, int it, int lo, int hi) {
-        if (!wait(full(v_slot(c)), phase_of(c))) return false;
+        if (!(kF8 ? wait(kBarFull16 + v_slot(c), c / kV16 & 1)
+                  : wait(kBarFull + v_slot(c), phase_of(c))))
+          return false;
         if (!kF8 && (it * kKv < lo || it * kKv + kKv > hi)) {
           const Tile t = tile_of(w, it);
           uint8_t* v = smem + kOffRing + v_slot(c) * kTileBytes;
@@ -686,7 +758,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; ok && get_item(k, w); ++k) {
         const int n = max(w.n_a, w.n_b), lo = full_lo(w), hi = full_hi(w);
         if (n > 0) {
-          ok = wait(kF8 && kBF16 ? kBarQ16 : kBarQ, q_loads++ & 1) && wait_k(c);
+          ok = wait(kBarQ, q_loads++ & 1) && wait_k(c);
           if (!ok) break;
         }
         if (w.solo) {
@@ -751,6 +823,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t inv_g = 65536u / static_cast<uint32_t>(G) + 1u;
     const int r_tok = static_cast<int>((static_cast<uint32_t>(r) * inv_g) >> 16);
     uint32_t phase_s = 0, phase_o = 0, phase_pair = 0;
+    int q_made = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
       // What the tiles' loop needs of the piece (a row's 128 scores leave few
@@ -780,10 +853,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (p.window > 0) plain_lo = max(plain_lo, pos0 + tok - p.window);
         plain_hi = min(full_hi(w), pos0 + 1);
         if constexpr (kF8) {
-          // An 8-bit cache's K scale multiplies every score of KV head j.
-          const float ks = p.k_scale[w.j];
-          negate ^= ks < 0.f;
-          scale = fmaxf(scale * fabsf(ks), 1e-37f);
+          if (max(w.n_a, w.n_b) > 0) {
+            // Q as e4m3 terms, once the last S of the piece before has read it.
+            int8_t* qexp = reinterpret_cast<int8_t*>(smem + kOffQExp);
+            ok = mbar_wait_or_abort(bar(kBarQFree), (q_made & 1) ^ 1, p.err_flag, abort_word);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            if (x == 0 || w.tok_b > 0)
+              split_q<kBF16, kTerms>(p, w, x, warp & 3, inv_g, smem + x * kTerms * kCodeBytes,
+                                     qexp + x * kM);
+            fence_proxy_async_smem();
+            mbar_arrive(bar(kBarQ));
+            // (Solo: the B warps' row exponents come from the A warps.)
+            if (w.solo && x == 1) {
+              ok = mbar_wait_or_abort(bar(kBarQ), q_made & 1, p.err_flag, abort_word);
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
+            }
+            __syncwarp();
+            ++q_made;
+            // K's scale multiplies every score of KV head j, and the row carries
+            // 2^(its exponent).
+            const float ks = p.k_scale[w.j];
+            negate ^= ks < 0.f;
+            scale *= fabsf(ks);
+            scale = fmaxf(scale * __uint_as_float((127 - qexp[half * kM + r]) << 23), 1e-37f);
+          }
         }
         if (negate) plain_hi = plain_lo;  // (every tile changes its scores' sign)
       }

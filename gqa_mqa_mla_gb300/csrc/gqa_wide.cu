@@ -203,18 +203,6 @@ __device__ __forceinline__ void convert_v8(const uint8_t* src, uint8_t* dst, int
   }
 }
 
-// Two floats rounded to e4m3 (nearest even; |x| <= 448 here): the two codes
-// (x in the lower byte) and the rounded values.
-__device__ __forceinline__ uint32_t e4m3_round2(float x, float y, float& rx, float& ry) {
-  const uint32_t c = f32x2_to_e4m3x2(x, y);
-  uint32_t h, unused;
-  e4m3x4_to_f16x2(c, h, unused);
-  const float2 v = unpack2<false>(h);
-  rx = v.x;
-  ry = v.y;
-  return c;
-}
-
 // kF8: the cache holds e4m3 codes with per-KV-head scales (K's folds into the
 // score scale, V's into the output).  S = Q K^T then runs as kind::f8f6f4 on
 // the landed K codes, with Q split into e4m3 terms, and O += P V on f16

@@ -126,6 +126,7 @@ struct RopeParams {
 
 // Attention of a chunk of new tokens per sequence.
 struct PrefillParams {
+  const void* q;              // [tokens, h_q, 128]
   const int32_t* block_table; // [B, max_blocks_per_seq]
   const int32_t* q_start;     // [B + 1]
   const int32_t* seq_lens;    // [B]

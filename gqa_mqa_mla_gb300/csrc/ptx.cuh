@@ -425,6 +425,18 @@ DECATTN_DEV uint32_t f32x2_to_e4m3x2(float x, float y) {
   return h;
 }
 
+// Two floats rounded to e4m3 (nearest even; |x| <= 448 here): the two codes
+// (x in the lower byte) and the rounded values.
+DECATTN_DEV uint32_t e4m3_round2(float x, float y, float& rx, float& ry) {
+  const uint32_t c = f32x2_to_e4m3x2(x, y);
+  uint32_t h, unused;
+  e4m3x4_to_f16x2(c, h, unused);
+  const float2 v = unpack2<false>(h);
+  rx = v.x;
+  ry = v.y;
+  return c;
+}
+
 DECATTN_DEV uint32_t lds32(uint32_t addr) {
   uint32_t r;
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r) : "r"(addr));
