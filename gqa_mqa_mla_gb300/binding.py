@@ -311,6 +311,10 @@ def _check_sinks(window, sinks):
         raise ValueError("sinks need a window (without one every token is visible)")
 
 
+def _window(window) -> int | None:
+    return None if window is None else int(window)
+
+
 def _stream_handle(stream) -> int:
     if stream is None:
         stream = torch.cuda.current_stream()
@@ -343,7 +347,7 @@ def gqa_decode(q, k_cache, v_cache, block_table, seq_lens, *, scale: float, max_
     """
     _check_sinks(window, sinks)
     r = calls().decode(q, k_cache, v_cache, None, None, block_table, seq_lens, scale, max_seq_len,
-                       window, sinks, num_splits, out, workspace, err_flag, _handle(stream))
+                       _window(window), sinks, num_splits, out, workspace, err_flag, _handle(stream))
     if type(r) is int:
         raise DecAttnError(_decode_name("gqa_decode", window, sinks), r)
     return r
@@ -374,7 +378,7 @@ def gqa_decode_fp8kv(q, k_codes, v_codes, k_scale, v_scale, block_table, seq_len
     if k_scale is None or v_scale is None:
         raise TypeError("k_scale and v_scale must be torch.Tensors")
     r = calls().decode(q, k_codes, v_codes, k_scale, v_scale, block_table, seq_lens, scale,
-                       max_seq_len, window, sinks, num_splits, out, workspace, err_flag,
+                       max_seq_len, _window(window), sinks, num_splits, out, workspace, err_flag,
                        _handle(stream))
     if type(r) is int:
         raise DecAttnError(_decode_name("gqa_decode_fp8kv", window, sinks), r)

@@ -124,6 +124,9 @@ int resolve_splits(int max_seq_len, int n_split, int* tokens_per_split) {
   return (tiles + tiles_per - 1) / tiles_per;
 }
 
+// A window of every token there can be hides nothing: the kernels' plain case.
+int useful_window(int window, int max_seq_len) { return window < max_seq_len ? window : 0; }
+
 // A sliding window of W tokens starts at a block (or 64-token) boundary at
 // most min(block_size, 64) - 1 tokens before the window: the longest token
 // range any sequence streams.
@@ -408,6 +411,7 @@ static int gqa_decode_impl(const void* q, const void* k_cache, const void* v_cac
   const int st = gqa_check_args(q, k_cache, v_cache, k_scale, v_scale, fp8, block_table,
                                 seq_lens, out, h_q, h_kv, d_head, scale, window, L);
   if (st != DECATTN_OK) return st;
+  if (sinks > 0) window = useful_window(window, L->max_seq_len);
   const int span = sinks_span(L->max_seq_len, window, sinks, L->block_size);
   int n_split = L->num_splits;
   if (n_split == 0) {
@@ -878,8 +882,17 @@ static int plan_prefill_splits(int batch, int tokens, int max_q_len, int h_q, in
     if (seen < span) span = seen;
   }
   const int64_t tiles = (span + 127) / 128;
-  int64_t ns = units > 0 ? sms / units : 1;  // one wave of one CTA per SM
-  if (ns > tiles / 2) ns = tiles / 2;
+  // One wave of one CTA per SM, at least two tiles a split and, from eight
+  // splits on, five (each split adds to what the combine reads).  64 query
+  // heads on 8 KV heads: 4 tokens over a 1k cache with 1 / 2 / 4 / 8 splits
+  // 20.7 / 18.9 / 18.7 / 16.9 us, over 4k with 2 / 4 / 6 / 12 29.3 / 22.8 /
+  // 20.8 / 20.8, over 8k with 8 / 12 / 19 25.0 / 23.1 / 25.0; 8 over 131k with
+  // 8 / 12 / 19 / 24 136 / 103 / 96 / 125 (24: a second wave); 2 x 64 over 8k
+  // with 2 / 3 / 4 / 6 66 / 52 / 44 / 60; 16 x 8 (128 pieces) 1 / 2: 90 / 101.
+  int64_t cap = tiles / 2 < 8 ? tiles / 2 : 8;
+  if (cap < tiles / 5) cap = tiles / 5;
+  int64_t ns = units > 0 ? sms / units : 1;
+  if (ns > cap) ns = cap;
   if (ns > DECATTN_MAX_SPLITS) ns = DECATTN_MAX_SPLITS;
   return ns < 1 ? 1 : static_cast<int>(ns);
 }
@@ -915,6 +928,7 @@ static int gqa_prefill_impl(const void* q, const void* k_cache, const void* v_ca
   const int st = gqa_check_args(q, k_cache, v_cache, k_scale, v_scale, fp8, block_table,
                                 seq_lens, out, h_q, h_kv, d_head, scale, window, L);
   if (st != DECATTN_OK) return st;
+  window = useful_window(window, L->max_seq_len);
   if (!q_start || !aligned(q_start, 4)) return DECATTN_ERR_INVALID_ARG;
   if (tokens == 0) return DECATTN_OK;
   const int group = h_q / h_kv;

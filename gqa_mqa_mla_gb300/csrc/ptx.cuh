@@ -309,19 +309,6 @@ DECATTN_DEV void named_bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// ------------------------------------------------------------------ registers
-
-// Move a warpgroup's register limit (all four warps).  The limits of a block's
-// warpgroups together must not exceed what the block was launched with.
-template <int kRegs>
-DECATTN_DEV void reg_grow() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
-template <int kRegs>
-DECATTN_DEV void reg_shrink() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
-}
-
 // ------------------------------------------------------------------ math
 
 DECATTN_DEV float ex2(float x) {

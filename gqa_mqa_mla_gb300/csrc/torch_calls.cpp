@@ -104,8 +104,9 @@ int cuda_index(const Tensor& t) {
   return t.get_device();
 }
 
+// On the call's device, or in pinned host memory (which the device reads).
 void same_device(int index, const Tensor& t, const char* name) {
-  if (!t.is_cuda() || t.get_device() != index)
+  if (t.is_cuda() ? t.get_device() != index : !t.is_pinned())
     value_error(std::string(name) + " is on " + t.device().str() +
                 ", the call's other tensors on cuda:" + std::to_string(index));
 }
@@ -141,10 +142,10 @@ int size32(const Tensor& t, int64_t dim) {
 // The launch block's flag and stream.
 int* flag_of(PyObject* o, int index) {
   if (none(o)) return nullptr;
-  const Tensor& t = check(o, "err_flag", ScalarType::Int, -1);
-  if (t.numel() < 1) value_error("err_flag needs one element");
+  const Tensor& t = tensor(o, "err_flag");
+  if (t.nbytes() < sizeof(int)) value_error("err_flag needs one int32 element");
   same_device(index, t, "err_flag");
-  return t.data_ptr<int>();
+  return static_cast<int*>(t.data_ptr());
 }
 
 void* stream_of(PyObject* o, int index) {
@@ -157,9 +158,16 @@ void* stream_of(PyObject* o, int index) {
   return p;
 }
 
-Tensor scratch(int64_t bytes, const Tensor& like) {
-  return at::empty({bytes}, like.options().dtype(ScalarType::Byte));
-}
+// The allocations and the library's call run without the interpreter's lock (a
+// launch waits when the device's queue is full); it is held again on the way out.
+class Unlocked {
+  PyThreadState* state_ = PyEval_SaveThread();
+
+ public:
+  Unlocked() = default;
+  Unlocked(const Unlocked&) = delete;
+  ~Unlocked() { PyEval_RestoreThread(state_); }
+};
 
 PyObject* status(int st) { return PyLong_FromLong(st); }
 
@@ -216,12 +224,9 @@ PyObject* paged_plan(PyObject* const* a, Py_ssize_t n) {
   L.stream = stream_of(a[13], index);
   const char* names[] = {"seq_lens", "q_start", "slots", "positions", "free_count_out"};
   const int64_t sizes[] = {B, static_cast<int64_t>(B) + 1, tokens, tokens, 1};
-  const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(index));
   Tensor out[5];
   for (int k = 0; k < 5; ++k) {
-    if (none(a[7 + k])) {
-      out[k] = at::empty({sizes[k]}, cached.options());
-    } else {
+    if (!none(a[7 + k])) {
       out[k] = check(a[7 + k], names[k], ScalarType::Int, 1);
       if (out[k].size(0) != sizes[k])
         value_error(std::string(names[k]) + ": expected [" + std::to_string(sizes[k]) +
@@ -230,9 +235,14 @@ PyObject* paged_plan(PyObject* const* a, Py_ssize_t n) {
     }
   }
   auto at_ = [](const Tensor& t) { return t.data_ptr<int>(); };
-  const int st = lib.paged_plan(at_(cached), at_(moved), at_(table), at_(free), at_(top),
-                                at_(out[4]), at_(out[0]), at_(out[1]), at_(out[2]), at_(out[3]),
-                                tokens, &L);
+  const int st = [&] {
+    const Unlocked unlocked;
+    const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(index));
+    for (int k = 0; k < 5; ++k)
+      if (!out[k].defined()) out[k] = at::empty({sizes[k]}, cached.options());
+    return lib.paged_plan(at_(cached), at_(moved), at_(table), at_(free), at_(top), at_(out[4]),
+                          at_(out[0]), at_(out[1]), at_(out[2]), at_(out[3]), tokens, &L);
+  }();
   if (st != DECATTN_OK) return status(st);
   PyObject* r = PyTuple_New(5);
   for (int k = 0; r && k < 5; ++k) PyTuple_SET_ITEM(r, k, THPVariable_Wrap(out[k]));
@@ -305,24 +315,25 @@ PyObject* rope_append(PyObject* const* a, Py_ssize_t n) {
   L.err_flag = flag_of(a[12], index);
   L.stream = stream_of(a[13], index);
   const auto* rope = static_cast<const decattn_rope*>(PyLong_AsVoidPtr(a[6]));
-  const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(index));
   Tensor out;
-  if (none(a[11])) {
-    out = at::empty({T, h_q, d}, q.options());
-  } else {
+  if (!none(a[11])) {
     out = check(a[11], "q_out", q.scalar_type(), 3);
     if (out.sizes() != q.sizes())
       value_error("q_out: expected shape " + shape_of(q) + ", got " + shape_of(out));
     same_device(index, out, "q_out");
   }
-  const int st =
-      fp8 ? lib.gqa_rope_append_fp8kv(q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, sk, sv,
-                                      pos.data_ptr<int>(), rope, slots.data_ptr<int>(),
-                                      out.data_ptr(), kc.data_ptr(), vc.data_ptr(), T, h_q, h_kv,
-                                      d, &L)
-          : lib.gqa_rope_append(q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs,
-                                pos.data_ptr<int>(), rope, slots.data_ptr<int>(), out.data_ptr(),
-                                kc.data_ptr(), vc.data_ptr(), T, h_q, h_kv, d, &L);
+  const void *qp = q.data_ptr(), *kp = k.data_ptr(), *vp = v.data_ptr();
+  void *kcp = kc.data_ptr(), *vcp = vc.data_ptr();
+  const int *pp = pos.data_ptr<int>(), *sp = slots.data_ptr<int>();
+  const int st = [&] {
+    const Unlocked unlocked;
+    const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(index));
+    if (!out.defined()) out = at::empty({T, h_q, d}, q.options());
+    return fp8 ? lib.gqa_rope_append_fp8kv(qp, kp, vp, qs, ks, vs, sk, sv, pp, rope, sp,
+                                           out.data_ptr(), kcp, vcp, T, h_q, h_kv, d, &L)
+               : lib.gqa_rope_append(qp, kp, vp, qs, ks, vs, pp, rope, sp, out.data_ptr(), kcp,
+                                     vcp, T, h_q, h_kv, d, &L);
+  }();
   return st != DECATTN_OK ? status(st) : THPVariable_Wrap(out);
 }
 
@@ -371,28 +382,34 @@ struct Attention {
     L.stream = stream_of(stream, index);
     return L;
   }
-  Tensor output(PyObject* o) const {
-    if (none(o)) return at::empty(q->sizes(), q->options());
-    const Tensor& t = check(o, "out", q->scalar_type(), 3);
-    if (t.sizes() != q->sizes())
+  // The given output (undefined: none).  `exact`: [tokens, h_q, d]; else any
+  // contiguous tensor with room for it.
+  Tensor output(PyObject* o, bool exact) const {
+    if (none(o)) return Tensor();
+    const Tensor& t = check(o, "out", q->scalar_type(), exact ? 3 : -1);
+    if (exact ? t.sizes() != q->sizes() : t.numel() < q->numel())
       value_error("out: expected shape " + shape_of(*q) + ", got " + shape_of(t));
     same_device(index, t, "out");
     return t;
   }
-  // The given workspace, or one of `need` bytes, into L.
-  Tensor workspace(PyObject* o, size_t need, decattn_launch& L) const {
-    Tensor t;
-    if (!none(o)) {
-      t = check(o, "workspace", ScalarType::Byte, -1);
-      same_device(index, t, "workspace");
-    } else if (need) {
-      t = scratch(static_cast<int64_t>(need), *q);
-    }
-    if (t.defined()) {
-      L.workspace = t.data_ptr();
-      L.workspace_bytes = static_cast<size_t>(t.numel());
-    }
+  // The given workspace (undefined: none).
+  Tensor workspace(PyObject* o) const {
+    if (none(o)) return Tensor();
+    const Tensor& t = tensor(o, "workspace");
+    if (!t.is_contiguous()) value_error("workspace must be contiguous");
+    same_device(index, t, "workspace");
     return t;
+  }
+  // What was not given is allocated: the output, `need` bytes of workspace.
+  void* allocate(Tensor& out, Tensor& ws, size_t need, decattn_launch& L) const {
+    if (!out.defined()) out = at::empty(q->sizes(), q->options());
+    if (!ws.defined() && need)
+      ws = at::empty({static_cast<int64_t>(need)}, q->options().dtype(ScalarType::Byte));
+    if (ws.defined()) {
+      L.workspace = ws.data_ptr();
+      L.workspace_bytes = ws.nbytes();
+    }
+    return out.data_ptr();
   }
 };
 
@@ -408,35 +425,39 @@ PyObject* decode(PyObject* const* a, Py_ssize_t n) {
   const int window = windowed ? as_int(a[9], "window") : 0;
   const int B = size32(*x.q, 0);
   decattn_launch L = x.launch(B, max_len, a[14], a[15]);
-  const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(x.index));
-  int ns = as_int(a[11], "num_splits");
-  if (ns == 0) {
-    ns = windowed ? lib.gqa_decode_sinks_plan_splits(B, x.h_q, x.h_kv, x.d, max_len, window, sinks,
-                                                     L.block_size, x.fp8 ? 1 : 2, 0)
-         : x.fp8  ? lib.gqa_decode_fp8kv_plan_splits(B, x.h_q, x.h_kv, x.d, max_len, 0)
-                  : lib.gqa_decode_plan_splits(B, x.h_q, x.h_kv, x.d, max_len, 0);
-    if (ns < 0) return status(ns);
-  }
-  L.num_splits = ns;
-  const Tensor out = x.output(a[12]);
-  const Tensor ws =
-      x.workspace(a[13], ns > 1 ? lib.gqa_decode_workspace_size(B, x.h_q, x.d, ns) : 0, L);
+  L.num_splits = as_int(a[11], "num_splits");
+  Tensor out = x.output(a[12], false), ws = x.workspace(a[13]);
   const void *q = x.q->data_ptr(), *kc = x.kc->data_ptr(), *vc = x.vc->data_ptr();
   const int *bt = x.table->data_ptr<int>(), *sl = x.lens->data_ptr<int>();
-  void* o = out.data_ptr();
-  int st;
-  if (!windowed)
-    st = x.fp8 ? lib.gqa_decode_fp8kv(q, kc, vc, x.sk, x.sv, bt, sl, o, x.h_q, x.h_kv, x.d, scale, &L)
-               : lib.gqa_decode(q, kc, vc, bt, sl, o, x.h_q, x.h_kv, x.d, scale, &L);
-  else if (sinks == 0)
-    st = x.fp8 ? lib.gqa_decode_fp8kv_window(q, kc, vc, x.sk, x.sv, bt, sl, o, x.h_q, x.h_kv, x.d,
-                                             scale, window, &L)
-               : lib.gqa_decode_window(q, kc, vc, bt, sl, o, x.h_q, x.h_kv, x.d, scale, window, &L);
-  else
-    st = x.fp8 ? lib.gqa_decode_fp8kv_sinks(q, kc, vc, x.sk, x.sv, bt, sl, o, x.h_q, x.h_kv, x.d,
-                                            scale, window, sinks, &L)
-               : lib.gqa_decode_sinks(q, kc, vc, bt, sl, o, x.h_q, x.h_kv, x.d, scale, window,
-                                      sinks, &L);
+  const int st = [&] {
+    const Unlocked unlocked;
+    const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(x.index));
+    if (L.num_splits == 0) {
+      const int ns =
+          windowed ? lib.gqa_decode_sinks_plan_splits(B, x.h_q, x.h_kv, x.d, max_len, window,
+                                                      sinks, L.block_size, x.fp8 ? 1 : 2, 0)
+          : x.fp8  ? lib.gqa_decode_fp8kv_plan_splits(B, x.h_q, x.h_kv, x.d, max_len, 0)
+                   : lib.gqa_decode_plan_splits(B, x.h_q, x.h_kv, x.d, max_len, 0);
+      if (ns < 0) return ns;
+      L.num_splits = ns;
+    }
+    const int ns = L.num_splits;
+    void* o = x.allocate(out, ws,
+                         ns > 1 ? lib.gqa_decode_workspace_size(B, x.h_q, x.d, ns) : 0, L);
+    if (!windowed)
+      return x.fp8 ? lib.gqa_decode_fp8kv(q, kc, vc, x.sk, x.sv, bt, sl, o, x.h_q, x.h_kv, x.d,
+                                          scale, &L)
+                   : lib.gqa_decode(q, kc, vc, bt, sl, o, x.h_q, x.h_kv, x.d, scale, &L);
+    if (sinks == 0)
+      return x.fp8 ? lib.gqa_decode_fp8kv_window(q, kc, vc, x.sk, x.sv, bt, sl, o, x.h_q, x.h_kv,
+                                                 x.d, scale, window, &L)
+                   : lib.gqa_decode_window(q, kc, vc, bt, sl, o, x.h_q, x.h_kv, x.d, scale,
+                                           window, &L);
+    return x.fp8 ? lib.gqa_decode_fp8kv_sinks(q, kc, vc, x.sk, x.sv, bt, sl, o, x.h_q, x.h_kv, x.d,
+                                              scale, window, sinks, &L)
+                 : lib.gqa_decode_sinks(q, kc, vc, bt, sl, o, x.h_q, x.h_kv, x.d, scale, window,
+                                        sinks, &L);
+  }();
   return st != DECATTN_OK ? status(st) : THPVariable_Wrap(out);
 }
 
@@ -455,23 +476,28 @@ PyObject* prefill(PyObject* const* a, Py_ssize_t n) {
   const int max_q = as_int(a[9], "max_q_len"), max_len = as_int(a[10], "max_seq_len");
   const int window = as_int(a[11], "window"), sinks = as_int(a[12], "sinks");
   decattn_launch L = x.launch(B, max_len, a[16], a[17]);
-  const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(x.index));
-  int ns = as_int(a[13], "num_splits");
-  if (ns == 0) {
-    ns = lib.gqa_prefill_plan_splits(B, T, max_q, x.h_q, x.h_kv, x.d, max_len, window, sinks, 0);
-    if (ns < 0) return status(ns);
-  }
-  L.num_splits = ns;
-  const Tensor out = x.output(a[14]);
-  const Tensor ws =
-      x.workspace(a[15], T && ns > 1 ? lib.gqa_prefill_workspace_size(T, x.h_q, x.d, ns) : 0, L);
+  L.num_splits = as_int(a[13], "num_splits");
+  Tensor out = x.output(a[14], true), ws = x.workspace(a[15]);
   const void *q = x.q->data_ptr(), *kc = x.kc->data_ptr(), *vc = x.vc->data_ptr();
   const int *bt = x.table->data_ptr<int>(), *sl = x.lens->data_ptr<int>();
   const int* qs = start.data_ptr<int>();
-  const int st = x.fp8 ? lib.gqa_prefill_fp8kv(q, kc, vc, x.sk, x.sv, bt, qs, sl, out.data_ptr(), T,
-                                               max_q, x.h_q, x.h_kv, x.d, scale, window, sinks, &L)
-                       : lib.gqa_prefill(q, kc, vc, bt, qs, sl, out.data_ptr(), T, max_q, x.h_q,
-                                         x.h_kv, x.d, scale, window, sinks, &L);
+  const int st = [&] {
+    const Unlocked unlocked;
+    const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(x.index));
+    if (L.num_splits == 0) {
+      const int ns = lib.gqa_prefill_plan_splits(B, T, max_q, x.h_q, x.h_kv, x.d, max_len, window,
+                                                 sinks, 0);
+      if (ns < 0) return ns;
+      L.num_splits = ns;
+    }
+    const int ns = L.num_splits;
+    void* o = x.allocate(
+        out, ws, T && ns > 1 ? lib.gqa_prefill_workspace_size(T, x.h_q, x.d, ns) : 0, L);
+    return x.fp8 ? lib.gqa_prefill_fp8kv(q, kc, vc, x.sk, x.sv, bt, qs, sl, o, T, max_q, x.h_q,
+                                         x.h_kv, x.d, scale, window, sinks, &L)
+                 : lib.gqa_prefill(q, kc, vc, bt, qs, sl, o, T, max_q, x.h_q, x.h_kv, x.d, scale,
+                                   window, sinks, &L);
+  }();
   return st != DECATTN_OK ? status(st) : THPVariable_Wrap(out);
 }
 

@@ -687,3 +687,223 @@ def test_a_run_of_steps(fp8, window, sinks):
         _close(out, ref, dtype)
         if single and window:
             _close(dec, tuple(r[:B] for r in ref), dtype)
+
+
+# ------------------------------------------------------------------ drawn cases
+
+
+def _draw(seed):
+    """Chunk lengths, cached lengths, heads, type, block, window and sinks."""
+    rng = np.random.default_rng(1000 + seed)
+    pick = lambda *x: x[int(rng.integers(len(x)))]  # noqa: E731
+    B, most = pick(1, 2, 3, 5), pick(1, 3, 20, 150, 300)
+    q_lens = rng.integers(0, most + 1, B).tolist()
+    q_lens[0] = max(1, q_lens[0])
+    lens = [n + int(rng.integers(0, pick(2, 130, 900))) for n in q_lens]
+    h_kv = pick(1, 2, 3)
+    h_q = h_kv * pick(1, 2, 3, 4, 7, 8, 12, 16)
+    window = pick(0, 1, 2, int(rng.integers(1, 40)), int(rng.integers(40, 400)), 128, 2**31 - 1)
+    sinks = pick(0, 1, 4, int(rng.integers(0, 300)), 128, 2**31 - 1) if window else 0
+    return q_lens, lens, h_q, h_kv, pick("bf16", "fp16"), pick(8, 16, 32, 64, 128, 256), \
+        window, sinks, pick(0, 1, 2, 3, 5, 8, 17)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("seed", range(48))
+def test_prefill_drawn(seed, fp8):
+    q_lens, lens, h_q, h_kv, dtype, bs, window, sinks, splits = _draw(seed)
+    x = _attn_case(q_lens, lens, h_q, h_kv, dtype, bs, 400 + seed, fp8=fp8)
+    # The host's bounds need not be reached (the table must hold max_seq_len).
+    x["max_len"] = min(x["max_len"] + seed % 3 * 100, x["table"].shape[1] * bs)
+    x["max_q"] += seed % 4 * 5
+    out, flag = _run_prefill(x, window=window or None, sinks=sinks, num_splits=splits)
+    assert flag == 0
+    ref = _plain_prefill(x, window=window, sinks=sinks)
+    _close(out, _fp16_probs(ref, dtype) if fp8 else ref, dtype)
+    again, _ = _run_prefill(x, window=window or None, sinks=sinks, num_splits=splits)
+    assert torch.equal(again, out)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("seed", range(24))
+def test_sinks_decode_drawn(seed, fp8):
+    _, lens, h_q, h_kv, dtype, bs, window, sinks, splits = _draw(100 + seed)
+    window, sinks = window or 77, sinks or 1
+    x = _attn_case([1] * len(lens), lens, h_q, h_kv, dtype, bs, 500 + seed, fp8=fp8)
+    fn = da.gqa_decode_fp8kv_sinks if fp8 else da.gqa_decode_sinks
+    flag = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out = fn(x["q"], *x["caches"], *(x["scales"] or []), x["table"], x["lens"], scale=0.09,
+             max_seq_len=x["table"].shape[1] * bs, window=window, sinks=sinks,
+             num_splits=splits, err_flag=flag)
+    assert int(flag) == 0
+    ref = _plain_prefill(x, scale=0.09, window=window, sinks=sinks)
+    _close(out, _fp16_probs(ref, dtype) if fp8 else ref, dtype)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_prefill_of_an_empty_batch_and_of_empty_sequences(fp8):
+    x = _attn_case([3, 2], [40, 50], 8, 2, "bf16", 16, 600, fp8=fp8)
+    none = dict(x, start=_i32([0, 0, 0]))
+    for splits in (1, 0, 3):
+        out = torch.full_like(x["q"], 7.0)
+        _, flag = _run_prefill(none, out=out, num_splits=splits)
+        assert flag == 0 and bool((out == 7).all())
+        # no rows at all
+        got, flag = _run_prefill(dict(none, q=x["q"][:0]), num_splits=splits)
+        assert flag == 0 and got.shape == (0, 8, 128)
+        # rows of sequences that hold no token: zeros
+        got, flag = _run_prefill(dict(x, lens=_i32([0, 0])), num_splits=splits)
+        assert flag == 0 and bool((got == 0).all())
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_attention_and_cache_write_past_32_bits(fp8):
+    """A cache of more than 2^32 elements, used at its far end."""
+    h_kv, bs, dtype = 4, 16, "bf16"
+    nb = 2**32 // (bs * h_kv * 128) + 64
+    kind = torch.uint8 if fp8 else TYPES[dtype]
+    caches = [torch.empty((nb, bs, h_kv, 128), dtype=kind, device=DEV) for _ in range(2)]
+    scales = [torch.full((h_kv,), 0.25, device=DEV) for _ in range(2)] if fp8 else None
+    L = 40
+    table = _i32([[nb - 1, nb - 40, nb - 7]])
+    t = torch.arange(L, device=DEV)
+    slots = (table[0].long()[t // bs] * bs + t % bs).int()
+    assert int(slots.max()) * h_kv * 128 > 2**32
+    g = _gen(601)
+    q, k, v = (torch.randn((L, n, 128), generator=g, device=DEV).to(TYPES[dtype])
+               for n in (8, h_kv, h_kv))
+    rope = da.rope_table([0.0] * 64)  # no turn: the rows themselves
+    fn = da.gqa_rope_append_fp8kv if fp8 else da.gqa_rope_append
+    q = fn(q, k, v, *(scales or []), _i32(np.zeros((1, L))), rope, slots, *caches)
+    for c, rows in zip(caches, (k, v)):
+        got = c.view(-1, h_kv, 128)[slots.long()]
+        want = (rows.float() / 0.25).to(torch.float8_e4m3fn).view(torch.uint8) if fp8 else rows
+        assert torch.equal(got, want)
+    small = [c[[nb - 1, nb - 40, nb - 7]].contiguous() for c in caches]
+    x = dict(q=q, caches=caches, scales=scales, table=table, start=_i32([0, L]), lens=_i32([L]),
+             max_q=L, max_len=L, dtype=dtype)
+    y = dict(x, caches=small, table=_i32([[0, 1, 2]]))
+    a, fa = _run_prefill(x)
+    b, fb = _run_prefill(y)
+    assert fa == fb == 0 and torch.equal(a, b)
+    dec = da.gqa_decode_fp8kv_sinks if fp8 else da.gqa_decode_sinks
+    da_, db = (dec(z["q"][-1:].contiguous(), *z["caches"], *(scales or []), z["table"], z["lens"],
+                   scale=0.09, max_seq_len=L, window=9, sinks=3) for z in (x, y))
+    assert torch.equal(da_, db)
+
+
+def test_calls_on_two_streams_at_once():
+    """Prefill, rotation, plan and decode calls in flight together give what they
+    give alone."""
+    cases = [_attn_case([200, 90, 1], [900, 90, 700], 16, 4, "bf16", 16, 610 + i, fp8=i % 2 == 1)
+             for i in range(4)]
+    alone = [_run_prefill(x, num_splits=2)[0] for x in cases]
+    parts, rc, _, slots = _rope_case(700, 8, 2, "bf16", 16, False, 611)
+    rope = da.rope_table([1e4 ** (-i / 64) for i in range(64)])
+    pos = torch.arange(700, device=DEV, dtype=torch.int32)[None]
+    rq = da.gqa_rope_append(*parts, pos, rope, slots, *rc)
+    c0 = cases[0]
+    decode = lambda: da.gqa_decode_sinks(  # noqa: E731
+        c0["q"][:3], *c0["caches"], c0["table"], c0["lens"], scale=0.09, max_seq_len=900,
+        window=64, sinks=4)
+    dec = decode()
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    torch.cuda.synchronize()
+    outs = []
+    for rep in range(5):
+        for i, (x, s) in enumerate(zip(cases, streams)):
+            with torch.cuda.stream(s):
+                fn = da.gqa_prefill if x["scales"] is None else da.gqa_prefill_fp8kv
+                outs.append((alone[i], fn(x["q"], *x["caches"], *(x["scales"] or []), x["table"],
+                                          x["start"], x["lens"], scale=128 ** -0.5,
+                                          max_q_len=x["max_q"], max_seq_len=x["max_len"],
+                                          num_splits=2)))
+                outs.append((rq, da.gqa_rope_append(*parts, pos, rope, slots,
+                                                    *[c.clone() for c in rc])))
+                outs.append((dec, decode()))
+    torch.cuda.synchronize()
+    for want, got in outs:
+        assert torch.equal(want, got)
+
+
+def test_a_whole_step_in_one_graph():
+    """Plan, rotation with cache write, and 8-bit prefill captured together and
+    replayed for several steps equal the same calls made one by one."""
+    B, bs, M, T, h_q, h_kv = 3, 16, 30, 64, 8, 2
+    rng = np.random.default_rng(12)
+    rope = da.rope_table([1e4 ** (-i / 64) for i in range(64)])
+    scales = [torch.full((h_kv,), 0.02, device=DEV) for _ in range(2)]
+
+    def state():
+        return dict(lens=_i32(np.zeros(B)), new=_i32(np.zeros(B)),
+                    table=_i32(np.full((B, M), -1)), free=_i32(np.arange(B * M)),
+                    count=_i32([B * M]),
+                    caches=[torch.zeros((B * M, bs, h_kv, 128), dtype=torch.uint8, device=DEV)
+                            for _ in range(2)],
+                    qkv=torch.zeros((T, h_q + 2 * h_kv, 128), dtype=torch.bfloat16, device=DEV),
+                    flag=torch.zeros(1, dtype=torch.int32, device=DEV))
+
+    def run(s):
+        p = da.paged_plan(s["lens"], s["new"], s["table"], s["free"], s["count"], block_size=bs,
+                          max_tokens=T, seq_lens=s["lens"], free_count_out=s["count"],
+                          err_flag=s["flag"])
+        q, k, v = s["qkv"].split([h_q, h_kv, h_kv], 1)
+        q = da.gqa_rope_append_fp8kv(q, k, v, *scales, p.positions[None], rope, p.slots,
+                                     *s["caches"], err_flag=s["flag"])
+        return da.gqa_prefill_fp8kv(q, *s["caches"], *scales, s["table"], p.q_start, s["lens"],
+                                    scale=0.09, max_q_len=T, max_seq_len=M * bs,
+                                    err_flag=s["flag"])
+
+    a, b = state(), state()
+    run(a)  # (a step of no token)
+    graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=stream):
+        out = run(a)
+    for seed in range(6):
+        new = _i32(rng.integers(1, 21, B))
+        for s in (a, b):
+            s["new"].copy_(new)
+            s["qkv"].copy_(torch.randn(s["qkv"].shape, generator=_gen(seed), device=DEV))
+        graph.replay()
+        want = run(b)
+        torch.cuda.synchronize()
+        n = int(new.sum())
+        assert int(a["flag"]) == int(b["flag"]) == 0
+        assert torch.equal(out[:n], want[:n]) and bool((want[:n] != 0).any())
+        for x, y in zip(a["caches"], b["caches"]):
+            assert torch.equal(x, y)
+        assert torch.equal(a["lens"], b["lens"]) and torch.equal(a["table"], b["table"])
+
+
+def test_binding_refusals_and_what_it_takes():
+    x = _attn_case([1, 1, 1], [30, 50, 64], 8, 2, "bf16", 16, 620)
+    args = (x["q"], *x["caches"], x["table"], x["lens"])
+    kw = dict(scale=0.09, max_seq_len=64)
+    ref = da.gqa_decode(*args, **kw)
+    # outputs of another shape with room, a workspace of any type, a flag and
+    # lengths in pinned memory
+    flat = torch.zeros(4, 8 * 128, dtype=torch.bfloat16, device=DEV)
+    got = da.gqa_decode(*args, out=flat, **kw)
+    assert got is flat and torch.equal(flat[:3].view_as(ref), ref) and bool((flat[3] == 0).all())
+    ws = torch.empty(2**18, device=DEV)
+    flag = torch.zeros(1, dtype=torch.int32).pin_memory()
+    lens = torch.tensor([30, 50, 65], dtype=torch.int32).pin_memory()
+    da.gqa_decode(*args[:4], lens, num_splits=1, workspace=ws, err_flag=flag, **kw)
+    torch.cuda.synchronize()
+    assert int(flag) == da.FLAG_BAD_SEQ_LEN
+    bad = [dict(out=flat[:2]), dict(out=ref.float()), dict(out=ref.cpu()),
+           dict(out=torch.zeros(3, 8, 256, dtype=torch.bfloat16, device=DEV)[..., ::2]),
+           dict(workspace=ws.cpu()), dict(workspace=3), dict(err_flag=torch.zeros(0, device=DEV)),
+           dict(err_flag=torch.zeros(1, dtype=torch.int32)), dict(num_splits=2**40),
+           dict(max_seq_len=2**31), dict(scale="x"), dict(stream="x"), dict(num_splits=1.5)]
+    for b in bad:
+        with pytest.raises((TypeError, ValueError)):
+            da.gqa_decode(*args, **{**kw, **b})
+        with pytest.raises((TypeError, ValueError)):
+            da.gqa_prefill(*args[:4], x["start"], x["lens"], max_q_len=1, **{**kw, **b})
+    with pytest.raises(da.DecAttnError):
+        da.gqa_prefill(*args[:4], x["start"], x["lens"], max_q_len=1, num_splits=4,
+                       workspace=ws[:16], **kw)
+    with pytest.raises(ValueError):  # prefill writes rows of its own shape only
+        da.gqa_prefill(*args[:4], x["start"], x["lens"], max_q_len=1, out=flat, **kw)
