@@ -159,6 +159,11 @@ __device__ __forceinline__ int full_lo(const Item& w) {
 }
 __device__ __forceinline__ int full_hi(const Item& w) { return w.hi - win0_of(w); }
 
+template <bool kValue>
+struct Const {
+  __device__ constexpr operator bool() const { return kValue; }
+};
+
 // Number of tiles up to and including the one that holds position `last`.
 __device__ __forceinline__ int tiles_to(const Item& w, int last) {
   return last < w.base ? 0 : w.sink_tiles + (last - w.base) / kKv + 1;
@@ -693,8 +698,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       };
-      // O_X += P_X V: eight k-steps of 16 tokens, P from TMEM.  `done`: O_X is
-      // complete behind this one; `last` as above, for the V slot.
+      // O_X += P_X V: k-steps of 16 tokens, P from TMEM.  `done`: O_X is complete
+      // behind this one; `last` as above, for the V slot.
       // In two halves, so that the first starts while the softmax is at the second
       // (8192-token prompt, 64 / 8 heads: 719 us, 724 in one).
       auto issue_pv_half = [&](int h, int x, int s, bool first, bool done, bool last) {
@@ -716,26 +721,49 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       };
+      // The same for a tile of which only the k-steps live & 15 to live >> 4 (not
+      // included) hold tokens, after both halves of P.  (4 chunks of 1500 to 2048
+      // tokens in a window of 1024 behind 4 kept ones, 32 heads: 160 us, 174 with
+      // all eight steps taken.)
+      constexpr int kAll = 8 << 4;
+      auto issue_pv_some = [&](int live, int x, int s, bool first, bool done, bool last) {
+        const uint64_t b = dv + static_cast<uint64_t>((s * kTileBytes) >> 4);
+        const uint32_t d = tmem + kTmemO + kHeadDim * x, a = tmem + kTmemS + kKv * x;
+        const int from = live & 15, to = live >> 4;
+        if (elect_one()) {
+#pragma unroll 1
+          for (int ks = from; ks < to; ++ks)
+            tc_mma_f16_ts(d, a + ks * 8, b + static_cast<uint64_t>((ks * 2048) >> 4), idesc_o,
+                          ks > from || !first ? 1u : 0u);
+          if (done) tc_commit(bar(kBarO + x));
+          if (last) tc_commit(bar(kF8 ? kBarEmpty16 + s : kBarEmpty + s));
+        }
+        __syncwarp();
+      };
       // The c-th tile of all pieces: K and V go round the ring's four slots (an
       // 8-bit cache's V then into one of the fp16 tiles).
       auto k_slot = [](int c) { return (2 * c) % kRing; };
       auto v_slot = [](int c) { return kF8 ? c % kV16 : (2 * c + 1) % kRing; };
       auto phase_of = [](int c) { return static_cast<uint32_t>((2 * c / kRing) & 1); };
       auto wait_k = [&](int c) { return wait(kBarFull + k_slot(c), phase_of(c)); };
-      // V rows outside [skip, nval) become zeros (P is 0 there, but the slots
-      // may hold NaN), while the softmax works on the tile.  (All 128 bytes of
-      // a row: the swizzle does not matter.)
-      auto wait_v = [&](int c, const Item& w, int it, int lo, int hi) {
+      // The k-steps with rows of [skip, nval) go to `live`; rows of theirs outside
+      // become zeros (P is 0 there, but the slots may hold NaN), while the softmax
+      // works on the tile.  (All 128 bytes of a row: the swizzle does not matter.)
+      // An 8-bit cache's converters wrote every row: there all steps are taken.
+      // `inner`: the tile is whole.
+      auto wait_v = [&](int c, const Item& w, int it, auto inner, int& live) {
         if (!(kF8 ? wait(kBarFull16 + v_slot(c), c / kV16 & 1)
                   : wait(kBarFull + v_slot(c), phase_of(c))))
           return false;
-        if (!kF8 && (it * kKv < lo || it * kKv + kKv > hi)) {
+        live = kAll;
+        if (!kF8 && !inner) {
           const Tile t = tile_of(w, it);
+          live = t.skip >> 4 | (t.nval + 15) >> 4 << 4;
           uint8_t* v = smem + kOffRing + v_slot(c) * kTileBytes;
 #pragma unroll 1
-          for (int i = lane; i < (t.skip + kKv - t.nval) * 16; i += 32) {
-            const int k = i >> 4, col = i & 15;
-            const int r = k < t.skip ? k : t.nval + (k - t.skip);
+          for (int i = lane; i < ((t.skip & 15) + (-t.nval & 15)) * 16; i += 32) {
+            const int k = i >> 4, col = i & 15, before = t.skip & 15;
+            const int r = k < before ? (t.skip & ~15) + k : t.nval + k - before;
             *reinterpret_cast<uint4*>(v + (col >> 3) * kHalf + r * 128 + ((col & 7) << 4)) =
                 make_uint4(0, 0, 0, 0);
           }
@@ -746,13 +774,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       int c = 0, q_loads = 0;  // over all pieces: tiles, Q loads, P's phases
       uint32_t phase_p[2] = {0, 0};
-      auto do_pv = [&](int x, int s, bool first, bool done, bool last) {
+      auto do_pv = [&](int live, int x, int s, bool first, bool done, bool last) {
         const uint32_t ph = x ? phase_p[1] : phase_p[0];
         if (x)
           phase_p[1] ^= 1u;
         else
           phase_p[0] ^= 1u;
         if (!wait(kBarP + x, ph)) return false;
+        if (live != kAll) {
+          if (!wait(kBarP + 2 + x, ph)) return false;
+          issue_pv_some(live, x, s, first, done, last);
+          return true;
+        }
         issue_pv_half(0, x, s, first, done, last);
         if (!wait(kBarP + 2 + x, ph)) return false;
         issue_pv_half(1, x, s, first, done, last);
@@ -766,21 +799,37 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = wait(kBarQ, q_loads++ & 1) && wait_k(c);
           if (!ok) break;
         }
+        // The tiles at [lo, hi) are whole and need none of wait_v's care: the issue
+        // lies on the path from P to the next S, and a loop with that care in it is
+        // 2 to 3 % slower.
+        auto tiles = [&](auto step) {
+          for (int it = 0; ok && it < n;) {
+            if (kF8 || (it * kKv >= lo && it * kKv + kKv <= hi)) {
+              const int to = kF8 ? n : min(n, hi / kKv);
+              for (; ok && it < to; ++it, ++c) ok = step(it, Const<true>{});
+            } else {
+              ok = step(it, Const<false>{});
+              ++it, ++c;
+            }
+          }
+        };
         if (w.solo) {
           issue_s(0, 0, k_slot(c), true, false);
           ok = wait_k(c + 1);
           if (!ok) break;
           issue_s(1, 0, k_slot(c + 1), true, n == 2);
-          for (int it = 0; it < n; ++it, ++c) {
+          tiles([&](int it, auto inner) -> bool {
             const int x = it & 1;
-            ok = wait_v(c, w, it, lo, hi) && do_pv(x, v_slot(c), it < 2, it + 2 >= n, true);
-            if (!ok) break;
+            int live;
+            if (!wait_v(c, w, it, inner, live) ||
+                !do_pv(live, x, v_slot(c), it < 2, it + 2 >= n, true))
+              return false;
             if (it + 2 < n) {
-              ok = wait_k(c + 2);
-              if (!ok) break;
+              if (!wait_k(c + 2)) return false;
               issue_s(x, 0, k_slot(c + 2), true, it + 3 == n);
             }
-          }
+            return true;
+          });
         } else {
           // Each tile is needed by A, by B or by both (B leaves out the gap;
           // either may end first).  A K or V slot is free behind its last
@@ -789,23 +838,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int first_b = w.gap0 > 0 ? 0 : w.gap1;
           if (w.n_a > 0) issue_s(0, 0, k_slot(c), !has_b(0), n == 1 && !has_b(0));
           if (has_b(0)) issue_s(1, 1, k_slot(c), true, n == 1);
-          for (int it = 0; it < n; ++it, ++c) {
+          tiles([&](int it, auto inner) -> bool {
             // The next K tile is waited for first, so that O += P V and the
             // next S follow each other without a pause.
-            ok = wait_v(c, w, it, lo, hi) && (it + 1 == n || wait_k(c + 1));
-            if (!ok) break;
+            int live;
+            if (!wait_v(c, w, it, inner, live) || !(it + 1 == n || wait_k(c + 1))) return false;
             const bool b0 = has_b(it), b1 = has_b(it + 1);
             if (it < w.n_a) {
-              ok = do_pv(0, v_slot(c), it == 0, it + 1 == w.n_a, !b0);
-              if (!ok) break;
+              if (!do_pv(live, 0, v_slot(c), it == 0, it + 1 == w.n_a, !b0)) return false;
               if (it + 1 < w.n_a) issue_s(0, 0, k_slot(c + 1), !b1, it + 2 == n && !b1);
             }
-            if (b0) {
-              ok = do_pv(1, v_slot(c), it == first_b, it + 1 == w.n_b, true);
-              if (!ok) break;
-            }
+            if (b0 && !do_pv(live, 1, v_slot(c), it == first_b, it + 1 == w.n_b, true))
+              return false;
             if (b1) issue_s(1, 1, k_slot(c + 1), true, it + 2 == n);
-          }
+            return true;
+          });
         }
         if (ok) release_item(k);
       }
@@ -919,6 +966,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_wait_ld_for(vb);
         tc_wait_ld_for(vc);
         tc_wait_ld_for(vd);
+        bool narrow = false;  // no more than 32 tokens (a few kept first ones; a rest)
         if (o < plain_lo || o + kKv > plain_hi) {
           // Seen columns: [skip, hi), of them those from lo on or below sink (at
           // or before the row's position; in its window or kept first tokens).
@@ -931,6 +979,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int c_hi = min(sink ? s_rel - o : w.hi - win0 - o, row + 1);
           const int c_lo = p.window > 0 && !sink ? row + 1 - p.window : 0;
           const int c_sink = p.sinks - win0 - o;
+          narrow = (sink ? s_rel : w.hi - win0) - o <= 32;
           if (negate) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
@@ -943,6 +992,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           auto mask = [&](float (&v)[32], int c0) {
             const uint32_t seen = (below(c_hi - c0) & ~below(skip - c0)) &
                                   (~below(c_lo - c0) | below(c_sink - c0));
+            if (__all_sync(0xffffffffu, seen == 0xffffffffu)) return;
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = (seen >> j) & 1u ? v[j] : kNegInf;
           };
@@ -969,7 +1019,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // limits, and the final division uses the same maximum).  S(it) is
         // complete, so O += P(it - 1) V before it is too.
         const bool need = mt > m + kRescaleThreshold;
-        if (__any_sync(0xffffffffu, need)) {
+        if (__builtin_expect(__any_sync(0xffffffffu, need), 0)) {
           const float m_new = need ? mt : m;
           const float f = need ? ex2(m - m_new) : 1.f;  // 0 from -inf
           if (o > o0) {
@@ -999,13 +1049,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tmem_st16(ts + c0 / 2, pk);
         };
+        auto zeros = [&](int c0) {  // (8-bit: every step of P V is taken)
+          uint32_t pk[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) pk[k] = 0;
+          tmem_st16(ts + c0 / 2, pk);
+        };
         probs(va, 0);
-        probs(vb, 32);
+        if (!narrow) {
+          probs(vb, 32);
+        } else if (kF8) {
+          zeros(32);
+          zeros(64);
+          zeros(96);
+        }
         tc_wait_st();
         tc_fence_before();
         mbar_arrive(bar(kBarP + x));
-        probs(vc, 64);
-        probs(vd, 96);
+        if (!narrow) {
+          probs(vc, 64);
+          probs(vd, 96);
+        }
         {
           const float2 e = unpair2(sum2);
           l += e.x + e.y;
