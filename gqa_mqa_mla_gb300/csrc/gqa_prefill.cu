@@ -169,6 +169,20 @@ __device__ __forceinline__ int tiles_to(const Item& w, int last) {
   return last < w.base ? 0 : w.sink_tiles + (last - w.base) / kKv + 1;
 }
 
+// By how many tokens a chunk's first piece is shorter than the others (which
+// follow it without a gap).  A piece's tiles start at the block boundary before its
+// first row's window, and rounded down so 128 rows of a window of 1024 need ten
+// tiles instead of nine; pieces whose windows start at a boundary do not.  Not
+// where a tile is no whole number of blocks, or where it would take one more piece.
+// (4 chunks of 1500 to 2048 tokens, window 1024, 32 heads: 136 us, 144 with equal
+// pieces.)
+__device__ __forceinline__ int shorter_by(const PrefillParams& p, int n, int len) {
+  const int tpi = 2 * p.tokens_per_tile, step = min(p.block_size, kKv);
+  if (p.window <= 0 || p.tokens_per_tile % step != 0) return 0;
+  const int s = static_cast<int>((static_cast<uint32_t>(len) - n + 1u - p.window) & (step - 1));
+  return (n + s + tpi - 1) / tpi > (n + tpi - 1) / tpi ? 0 : s;
+}
+
 // Walks the pieces from the last sequence's last one back (within a chunk the
 // last rows see most): 32 sequences at a time, one per lane.
 struct Cursor {
@@ -227,9 +241,11 @@ __device__ __forceinline__ bool find_item(const PrefillParams& p, Cursor& c, int
   w.n = __shfl_sync(0xffffffffu, c.n, src);
   w.len = __shfl_sync(0xffffffffu, c.len, src);
   const int cnt = __shfl_sync(0xffffffffu, c.cnt, src), pre = __shfl_sync(0xffffffffu, c.pre, src);
-  w.i0 = (cnt - 1 - (at - pre)) * tpi;
-  w.tok_a = min(p.tokens_per_tile, w.n - w.i0);
-  w.tok_b = max(0, min(p.tokens_per_tile, w.n - w.i0 - p.tokens_per_tile));
+  const int end = (cnt - (at - pre)) * tpi - shorter_by(p, w.n, w.len);
+  w.i0 = max(0, end - tpi);
+  const int tok = min(w.n, end) - w.i0;
+  w.tok_a = min(p.tokens_per_tile, tok);
+  w.tok_b = tok - w.tok_a;
   w.bad = w.len < 0 || w.len > p.max_seq_len;
   if (w.bad) {
     if (lane == 0) flag_error(p.err_flag, kFlagBadSeqLen);
