@@ -882,19 +882,27 @@ static int plan_prefill_splits(int batch, int tokens, int max_q_len, int h_q, in
     if (seen < span) span = seen;
   }
   const int64_t tiles = (span + 127) / 128;
-  // One wave of one CTA per SM, at least two tiles a split and, from eight
-  // splits on, five (each split adds to what the combine reads).  64 query
-  // heads on 8 KV heads: 4 tokens over a 1k cache with 1 / 2 / 4 / 8 splits
-  // 20.7 / 18.9 / 18.7 / 16.9 us, over 4k with 2 / 4 / 6 / 12 29.3 / 22.8 /
-  // 20.8 / 20.8, over 8k with 8 / 12 / 19 25.0 / 23.1 / 25.0; 8 over 131k with
-  // 8 / 12 / 19 / 24 136 / 103 / 96 / 125 (24: a second wave); 2 x 64 over 8k
-  // with 2 / 3 / 4 / 6 66 / 52 / 44 / 60; 16 x 8 (128 pieces) 1 / 2: 90 / 101.
-  int64_t cap = tiles / 2 < 8 ? tiles / 2 : 8;
-  if (cap < tiles / 5) cap = tiles / 5;
-  int64_t ns = units > 0 ? sms / units : 1;
-  if (ns > cap) ns = cap;
-  if (ns > DECATTN_MAX_SPLITS) ns = DECATTN_MAX_SPLITS;
-  return ns < 1 ? 1 : static_cast<int>(ns);
+  // One wave of one CTA per SM at most, and the number that takes least by this
+  // count, in ns: a CTA's tiles (one Q tile's, two Q tiles'), and from two splits on
+  // the combine, its chain over the splits and its traffic.  Measured, 8 KV heads:
+  // 64 heads, 4 tokens over an 8k cache with 4 / 8 / 12 / 19 splits 31.0 / 25.0 /
+  // 23.1 / 25.0 us, over 2k with 1 / 2 / 4 / 8 24.1 / 20.0 / 16.7 / 15.2, 8 over
+  // 131k with 8 / 12 / 19 / 24 136 / 103 / 96 / 125 (24: a second wave), 2 x 64
+  // over 8k with 2 / 3 / 4 / 6 66 / 52 / 44 / 60; 32 heads, 2 x 128 over 1k with
+  // 1 / 2 / 4 24.9 / 23.0 / 21.0, 8 x 64 over 500 with 1 / 2 16.4 / 20.4.
+  const int64_t tile_ns = max_q_len <= 128 / (h_q / h_kv) ? 950 : 1700;
+  int64_t most = units > 0 ? sms / units : 1, ns = 1, best = tiles * tile_ns;
+  if (most > tiles) most = tiles;
+  if (most > DECATTN_MAX_SPLITS) most = DECATTN_MAX_SPLITS;
+  for (int64_t n = 2; n <= most; ++n) {
+    const int64_t cost = (tiles + n - 1) / n * tile_ns + 2000 + 300 * n +
+                         static_cast<int64_t>(tokens) * h_q * n / 12;
+    if (cost < best) {
+      best = cost;
+      ns = n;
+    }
+  }
+  return static_cast<int>(ns);
 }
 
 size_t gqa_prefill_workspace_size(int tokens, int h_q, int d_head, int num_splits) {

@@ -53,7 +53,7 @@
 // rest) would leave the second set of softmax warps idle and every tile's chain
 // of product, softmax and product uncovered.  There (`solo`) both sets work on
 // the same rows, A on the even K / V tiles, B on the odd ones, with S, P and O
-// of their own, joined at the end through shared memory (32 chunks of 8 tokens
+// of their own, joined at the end (32 chunks of 8 tokens
 // over 8k caches, 64 heads on 8: 187 us instead of 203).
 //
 // An 8-bit (e4m3) cache takes the same pipeline with four changes: the K tile's
@@ -429,6 +429,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
+  // The scheduler looks for its first piece meanwhile.
+  Cursor cursor;
+  Item first;
+  // Grid index: KV heads of a piece, then its splits, then pieces.
+  auto find = [&](int x, Item& w) -> bool {
+    const int rest = x / p.h_kv, item = rest / p.n_split;
+    w.j = x - rest * p.h_kv;
+    w.split = rest - item * p.n_split;
+    return find_item(p, cursor, item, w);
+  };
+  if (warp == kWarpLoad) {
+    if (lane == 0) {
+      tma_prefetch_desc(&tm_q);
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+    }
+    cursor.b0 = p.batch - 32;
+    cursor.before = 0;
+    load_cursor(p, cursor, lane);
+    first.valid = find(static_cast<int>(blockIdx.x), first);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -460,10 +481,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       // streams through L2; otherwise its tiles are kept for the next piece.
       // (32 chunks of 8 tokens over 8k caches: 180 us, 187 with tiles kept.)
       const uint64_t keep = p.once ? policy_evict_first() : policy_evict_last();
-      if (lane == 0) {
-        if (lead) tma_prefetch_desc(&tm_q);
-        tma_prefetch_desc(lead ? &tm_k : &tm_v);
-      }
       const int bs = p.block_size, lg = p.log2_block_size;
       constexpr int kBytes = kF8 ? kCodeBytes : kTileBytes;  // of a tile
       // K(it) is the ring's copy 2 it, V(it) the copy 2 it + 1, counted over
@@ -471,10 +488,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       // numbers it made.
       int slot = lead ? 0 : 1, made_k = 0, made_v = 0, q_loads = 0;
       uint32_t phase = 0;
-      Cursor c;
-      c.b0 = p.batch - 32;
-      c.before = 0;
-      if (lead) load_cursor(p, c, lane);
       int x = blockIdx.x, asks = 0;
       // Takes over a CTA that has not started: its index in x, or -1.  Asked
       // for once the last copies of a piece are on their way, about two tiles
@@ -499,14 +512,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       Item w;
       for (int k = 0; ok; ++k) {
         if (lead) {
-          bool some = false;
-          while (ok && x >= 0 && !some) {
-            // grid index: KV heads of a piece, then its splits, then pieces
-            w.j = x % p.h_kv;
-            const int rest = x / p.h_kv;
-            w.split = rest % p.n_split;
-            some = find_item(p, c, rest / p.n_split, w);
-            if (!some) ok = claim();
+          bool some = k == 0 && first.valid;
+          if (some) {
+            w = first;
+          } else {
+            if (k == 0) ok = claim();
+            while (ok && x >= 0 && !some) {
+              some = find(x, w);
+              if (!some) ok = claim();
+            }
           }
           w.valid = some;
           if (lane == 0 && ok) {
@@ -1103,7 +1117,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int half = w.solo ? 0 : x;
       const int tok = half ? w.tok_b : w.tok_a;
       const int i0 = w.i0 + half * p.tokens_per_tile;
-      if (ok && tok > 0) {
+      if (ok && 32 * (warp & 3) < tok * G) {
         tc_fence_after();
         const bool bad = w.bad || bad_word[k & 1] != 0;
         // Weight of this warp's O (and, solo, of the other's): 1 / l, times an
@@ -1136,59 +1150,60 @@ __global__ void __launch_bounds__(kThreads, 1)
               *reinterpret_cast<uint4*>(base + static_cast<int64_t>(place[e]) * pitch) = y[e];
           __syncwarp();
         };
-        // Solo: the two halves of a row join.  The B warp hands over its maximum,
-        // sum and O through its staging (32 columns at a time), the A warp weighs,
-        // adds and stores.  (The pair meets at a bounded barrier: a warp that
-        // gave up elsewhere does not leave the other waiting.)
+        // Solo: the two halves of a row join.  Both warps of a row reach all of its
+        // TMEM lane, so each weighs and stores 64 columns of the sum.  They meet
+        // when both O are complete, when the A warp has the weights (from its
+        // maxima and sums and the B warp's), and when both O are read.  (Bounded
+        // barriers: a warp that gave up elsewhere does not leave the other waiting.
+        // 3 chunks of 5 tokens over 300, 8 heads: 10.3 us; through shared memory, by
+        // the A warp alone, 11.4.)
         float2* ml = reinterpret_cast<float2*>(smem + kOffMerge) + r;
-        uint8_t* hand = smem + kOffStage + (4 + (warp & 3)) * kStageBytes;
         auto meet = [&]() {
           const uint32_t at = bar(kBarPair + (warp & 3));
+          tc_fence_before();
           mbar_arrive(at);
           ok = __all_sync(0xffffffffu, mbar_wait_or_abort(at, phase_pair, p.err_flag, abort_word));
           phase_pair ^= 1u;
+          tc_fence_after();
         };
-        if (w.solo && x == 1) *ml = make_float2(m, l);
-#pragma unroll 2
-        for (int c = 0; ok && c < kHeadDim && (nt > 0 || p.n_split == 1); c += 32) {
+        if (w.solo) {
+          if (x == 1) *ml = make_float2(m, l);
+          meet();
+          if (x == 0) {
+            const float2 other = *ml;
+            const float top = fmaxf(m, other.x);
+            wa = m == kNegInf ? 0.f : ex2(m - top);
+            wb = other.x == kNegInf ? 0.f : ex2(other.x - top);
+            l = wa * l + wb * other.y;
+            m = top;
+            const float f = norm();
+            wa *= f;
+            wb *= f;
+            *ml = make_float2(wa, wb);
+          }
+          if (ok) meet();
+          if (x == 1) {
+            const float2 both = *ml;
+            wa = both.x;
+            wb = both.y;
+          }
+        }
+        const uint32_t to_a = tmem + lanes + kTmemO, to_b = to_a + kHeadDim;
+        const int c0 = w.solo ? 64 * x : 0, c1 = w.solo ? c0 + 64 : kHeadDim;
+#pragma unroll 1
+        for (int c = c0; ok && c < c1 && (nt > 0 || p.n_split == 1); c += 32) {
           float o[32];
-          tmem_ld32(to + c, o);
-          tc_wait_ld_for(o);
           if (w.solo) {
-            if (x == 1) {
+            float y[32];
+            tmem_ld32(to_a + c, o);
+            tmem_ld32(to_b + c, y);
+            tc_wait_ld_for(o);
+            tc_wait_ld_for(y);
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                *staged(hand, lane, e) = make_uint4(
-                    __float_as_uint(o[4 * e]), __float_as_uint(o[4 * e + 1]),
-                    __float_as_uint(o[4 * e + 2]), __float_as_uint(o[4 * e + 3]));
-            }
-            meet();
-            if (!ok) break;
-            if (x == 0) {
-              if (c == 0) {
-                const float2 other = *ml;
-                const float top = fmaxf(m, other.x);
-                wa = m == kNegInf ? 0.f : ex2(m - top);
-                wb = other.x == kNegInf ? 0.f : ex2(other.x - top);
-                l = wa * l + wb * other.y;
-                m = top;
-                const float f = norm();
-                wa *= f;
-                wb *= f;
-              }
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const uint4 y = *staged(hand, lane, e);
-                o[4 * e] = wa * o[4 * e] + wb * __uint_as_float(y.x);
-                o[4 * e + 1] = wa * o[4 * e + 1] + wb * __uint_as_float(y.y);
-                o[4 * e + 2] = wa * o[4 * e + 2] + wb * __uint_as_float(y.z);
-                o[4 * e + 3] = wa * o[4 * e + 3] + wb * __uint_as_float(y.w);
-              }
-            }
-            meet();
-            if (!ok) break;
-            if (x == 1) continue;
+            for (int e = 0; e < 32; ++e) o[e] = wa * o[e] + wb * y[e];
           } else {
+            tmem_ld32(to + c, o);
+            tc_wait_ld_for(o);
             const uint64_t wa2 = pair2(wa, wa);
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
@@ -1222,6 +1237,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   4 * kHeadDim * p.n_split);
           }
         }
+        if (ok && w.solo) meet();
         if (p.n_split > 1 && !(w.solo && x == 1)) {
           if (r < rows)
             p.part_lse[(row0 + static_cast<int64_t>(r_tok) * p.h_q + (r - r_tok * G)) * p.n_split +
@@ -1283,16 +1299,23 @@ __global__ void __launch_bounds__(256) gqa_prefill_combine_kernel(const PrefillP
   const float4* po = reinterpret_cast<const float4*>(p.part_o + row * p.n_split * kHeadDim);
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float sum = 0.f;
-#pragma unroll 4
-  for (int s = 0; s < p.n_split; ++s) {
-    const float wt = ex2(lse[s] - mx);
-    if (wt == 0.f) continue;
-    const float4 x = po[s * (kHeadDim / 4) + lane];
-    sum += wt;
-    acc.x = fmaf(wt, x.x, acc.x);
-    acc.y = fmaf(wt, x.y, acc.y);
-    acc.z = fmaf(wt, x.z, acc.z);
-    acc.w = fmaf(wt, x.w, acc.w);
+  for (int s0 = 0; s0 < p.n_split; s0 += 4) {
+    float wt[4];
+    float4 x[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int s = s0 + u;
+      wt[u] = s < p.n_split ? ex2(lse[s] - mx) : 0.f;
+      x[u] = wt[u] != 0.f ? po[s * (kHeadDim / 4) + lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      sum += wt[u];
+      acc.x = fmaf(wt[u], x[u].x, acc.x);
+      acc.y = fmaf(wt[u], x[u].y, acc.y);
+      acc.z = fmaf(wt[u], x[u].z, acc.z);
+      acc.w = fmaf(wt[u], x[u].w, acc.w);
+    }
   }
   const float inv = 1.f / sum;
   dst[lane] = make_uint2(pack2<kBF16>(acc.x * inv, acc.y * inv),
