@@ -1,13 +1,19 @@
-"""libdecattn: GB300-native single-token decode attention over a paged KV cache.
+"""libdecattn: GB300-native attention over a paged KV cache, for decoding and for
+the serving step around it.
 
-MHA / GQA / MQA (``gqa_decode``, ``gqa_decode_fp8kv`` over an 8-bit e4m3 KV
-cache, and their sliding-window forms ``gqa_decode_window`` /
-``gqa_decode_fp8kv_window``) and absorbed MLA (``mla_decode``), plus the decode
-step's cache write (``gqa_kv_append``, ``gqa_kv_append_fp8kv``,
-``mla_kv_append``) and MLA's absorption GEMMs (``mla_absorb_q``,
-``mla_unabsorb_out``): hand-written CUDA kernels for sm_103a behind a C ABI
-(include/decattn.h).  This package is the thin Python binding; ``synth``
-draws seeded synthetic inputs.
+MHA / GQA / MQA decode (``gqa_decode``, ``gqa_decode_fp8kv`` over an 8-bit e4m3 KV
+cache, their sliding-window forms ``gqa_decode_window`` /
+``gqa_decode_fp8kv_window``, and those with the first tokens kept,
+``gqa_decode_sinks`` / ``gqa_decode_fp8kv_sinks``) and absorbed MLA
+(``mla_decode``), the decode step's cache write (``gqa_kv_append``,
+``gqa_kv_append_fp8kv``, ``mla_kv_append``) and MLA's absorption GEMMs
+(``mla_absorb_q``, ``mla_unabsorb_out``).  For steps with any number of new tokens
+per request: ``paged_plan`` (block tables, slots and positions from lengths),
+``gqa_rope_append`` / ``gqa_rope_append_fp8kv`` (rotary positions and the cache
+write by slot) and ``gqa_prefill`` / ``gqa_prefill_fp8kv`` (attention of chunks over
+the cache).  Hand-written CUDA kernels for sm_103a behind a C ABI
+(include/decattn.h); this package is the thin Python binding, ``synth`` draws
+seeded synthetic inputs.
 """
 from .binding import (  # noqa: F401
     DecAttnError,

@@ -938,6 +938,8 @@ static int gqa_prefill_impl(const void* q, const void* k_cache, const void* v_ca
   if (st != DECATTN_OK) return st;
   window = useful_window(window, L->max_seq_len);
   if (!q_start || !aligned(q_start, 4)) return DECATTN_ERR_INVALID_ARG;
+  // (Tile offsets and the step behind the last tile stay within 31 bits.)
+  if (L->max_seq_len > 0x7fffffff - 4096) return DECATTN_ERR_UNSUPPORTED;
   if (tokens == 0) return DECATTN_OK;
   const int group = h_q / h_kv;
   int sms = 0, ns = L->num_splits;

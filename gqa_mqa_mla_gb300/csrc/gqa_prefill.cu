@@ -258,7 +258,7 @@ __device__ __forceinline__ bool find_item(const PrefillParams& p, Cursor& c, int
   const int p_first = w.len - w.n + w.i0;
   const int p_last = p_first + w.tok_a + w.tok_b - 1;
   w.hi = max(0, min(w.len, p_last + 1));
-  w.lo = p.window > 0 ? max(0, p_first + 1 - p.window) : 0;
+  w.lo = p.window > 0 && p_first >= p.window ? p_first + 1 - p.window : 0;
   if (p.sinks >= w.lo) w.lo = 0;
   w.lo = min(w.lo, w.hi);
   w.s_end = min(p.sinks, w.lo);
@@ -272,8 +272,7 @@ __device__ __forceinline__ bool find_item(const PrefillParams& p, Cursor& c, int
   w.n_b = w.tok_b > 0 ? min(per, total - w.tile0) : 0;
   w.solo = w.tok_b == 0 && w.n_a >= 2;
   // With a window, the first window tiles may lie before every row of tile B.
-  const int lo_b = p.window > 0 ? p_first + w.tok_a + 1 - p.window : 0;
-  const int before_b = w.lo > 0 ? (lo_b - w.base) / kKv : 0;
+  const int before_b = w.lo > 0 ? (p_first + w.tok_a + 1 - p.window - w.base) / kKv : 0;
   w.gap0 = max(0, min(w.n_b, w.sink_tiles - w.tile0));
   w.gap1 = max(w.gap0, min(w.n_b, w.sink_tiles + before_b - w.tile0));
   if (w.gap1 == w.n_b) {  // nothing behind the gap (in this split)

@@ -169,7 +169,9 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const PlanParams p
     }
   }
   const int live = grows ? T : 0;
-  for (int i = gtid; i < p.max_tokens; i += gsize) {
+  // (Unsigned: i may pass 2^31 behind the last row.)
+  for (unsigned row = gtid; row < static_cast<unsigned>(p.max_tokens); row += gsize) {
+    const int i = static_cast<int>(row);
     int slot = -1, pos = -1;
     if (i < live) {
       const int b = owner(tok, B, i);
@@ -205,7 +207,7 @@ cudaError_t launch_paged_plan(const PlanParams& p, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   // A token a thread, up to a CTA on every other SM (more only repeat the
   // scan); a cluster's CTAs where the step is updated in place.
-  const int by_rows = (p.max_tokens + kThreads - 1) / kThreads;
+  const int by_rows = p.max_tokens / kThreads + 1;
   const int ctas = p.in_place ? (p.max_tokens <= 2048 ? 1 : 8) : std::max(1, std::min(by_rows, 64));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));

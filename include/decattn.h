@@ -416,14 +416,19 @@ int gqa_rope_append_fp8kv(const void* q, const void* k_new, const void* v_new, i
  * with p < 0 (a chunk longer than its sequence) see nothing and are zeros.
  * Block sizes 8..256, h_q / h_kv <= 64, d_head 128; scores, softmax and sums
  * in fp32, the probabilities rounded to the 16-bit type for the second
- * product.  Values that only some rows of a chunk see must be finite: a
+ * product (fp16 over an 8-bit cache).  An 8-bit cache's codes are multiplied as
+ * they are: each query row is split into e4m3 terms, two for bf16 and three for
+ * fp16, whose sum is the row but for parts below 2^-18 of its largest value.
+ * Values that only some rows of a chunk see must be finite: a
  * NaN or infinity in v at position t may reach the rows before t that share
  * its tile (slots past seq_lens and slots that no row of the tile's sequence
  * may see can hold anything).
- * A seq_len outside [0, max_seq_len], a chunk longer than max_q_len or a bad
- * block id (flags as for gqa_decode) gives zero rows for that sequence's
- * affected rows; row offsets that decrease or leave [0, tokens] set
- * DECATTN_FLAG_BAD_SEQ_LEN and that sequence's rows are not written.
+ * A seq_len outside [0, max_seq_len] or a bad block id (flags as for
+ * gqa_decode) gives zero rows for that sequence's affected rows.  A chunk longer
+ * than max_q_len, or row offsets that decrease or leave [0, tokens], set
+ * DECATTN_FLAG_BAD_SEQ_LEN, and that sequence's rows are not computed (what its
+ * rows of out hold is unspecified where the offsets of two sequences overlap,
+ * else they are left as they were).  out must not overlap an input.
  * num_splits: parts that each sequence's cache is cut into (0 = automatic);
  * workspace sized by gqa_prefill_workspace_size.  tokens = 0 does nothing.
  */

@@ -330,3 +330,23 @@ def test_plain_rotation_preserves_lengths_and_relative_positions():
         assert abs(np.linalg.norm(turn(x, 77)) - np.linalg.norm(x)) < 1e-12
         assert abs(turn(x, 105) @ turn(y, 100) - turn(x, 5) @ turn(y, 0)) < 1e-10
         assert np.array_equal(turn(x, 9)[16:], x[0, 0, 16:])
+
+
+def test_prefill_refuses_lengths_whose_tiles_pass_31_bits(lib):
+    for n, expect in [(2**31 - 1, UNSUPPORTED), (2**31 - 4096, UNSUPPORTED)]:
+        assert _prefill(lib, False, L=dict(max_seq_len=n, max_blocks_per_seq=2**28)) == expect
+
+
+def test_prefill_planner_is_the_same_for_windows_that_hide_nothing():
+    """The library drops such a window before it plans: a workspace sized by the
+    planner's answer fits either way."""
+    for B, n, S, h_q, h_kv in [(1, 4, 8192, 64, 8), (3, 200, 1000, 32, 8), (2, 1, 64, 8, 8)]:
+        plain = da.gqa_prefill_plan_splits(B, B * n, n, h_q, h_kv, S, num_sms=152)
+        for window, sinks in [(S, 0), (S + 5, 7), (2**31 - 1, 2**31 - 1)]:
+            assert da.gqa_prefill_plan_splits(B, B * n, n, h_q, h_kv, S, window, sinks,
+                                              num_sms=152) == plain
+            for kv in (1, 2):
+                sink_plan = da.gqa_sinks_plan_splits(B, h_q, h_kv, S, window, sinks, 16, kv,
+                                                     num_sms=152)
+                plan = binding.gqa_plan_splits if kv == 2 else binding.gqa_fp8_plan_splits
+                assert sink_plan == plan(B, h_q, h_kv, S, num_sms=152)
