@@ -183,12 +183,16 @@ __device__ __forceinline__ int shorter_by(const PrefillParams& p, int n, int len
   return (n + s + tpi - 1) / tpi > (n + tpi - 1) / tpi ? 0 : s;
 }
 
-// Walks the pieces from the last sequence's last one back (within a chunk the
-// last rows see most): 32 sequences at a time, one per lane.
+// Walks the pieces, 32 sequences at a time (one per lane), from the last sequences
+// back.  Among the 32 the longest come first (a piece of two Q tiles counts
+// double), and within a chunk the last rows, which see most: what is left for the
+// end is short.  (32 chunks of 1 to 8 tokens over 4 to 8k, 64 heads on 8: 131 us,
+// 142 in the batch's order.)
 struct Cursor {
   int b0;      // the lanes hold sequences b0 .. b0 + 31
   int before;  // pieces behind those sequences
-  int start, n, len, cnt, pre;  // this lane's sequence; pre: pieces of the lanes above it
+  int start, n, len, cnt, pre;  // this lane's sequence; pre: pieces of those before it
+  int all;                      // pieces of the 32
 };
 
 __device__ __forceinline__ void load_cursor(const PrefillParams& p, Cursor& c, int lane) {
@@ -205,13 +209,15 @@ __device__ __forceinline__ void load_cursor(const PrefillParams& p, Cursor& c, i
       c.cnt = (e - a + tpi - 1) / tpi;
     }
   }
-  int sum = c.cnt;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int up = __shfl_down_sync(0xffffffffu, sum, o);
-    if (lane + o < 32) sum += up;
+  c.all = __reduce_add_sync(0xffffffffu, c.cnt);
+  c.pre = 0;
+  // (A grid of one wave starts all of its pieces at once: any order will do.)
+  const uint32_t key = p.steal ? static_cast<uint32_t>(c.len) << (c.n > p.tokens_per_tile) : 0u;
+  for (int j = max(0, -c.b0); j < 32; ++j) {
+    const uint32_t other = __shfl_sync(0xffffffffu, key, j);
+    const int pieces = __shfl_sync(0xffffffffu, c.cnt, j);
+    if (other > key || (other == key && j > lane)) c.pre += pieces;
   }
-  c.pre = sum - c.cnt;
 }
 
 // The index-th piece (all lanes; index counts from the end); false if there
@@ -224,10 +230,9 @@ __device__ __forceinline__ bool find_item(const PrefillParams& p, Cursor& c, int
     load_cursor(p, c, lane);
   }
   for (;;) {
-    const int all = __shfl_sync(0xffffffffu, c.pre + c.cnt, 0);
-    if (index < c.before + all) break;
+    if (index < c.before + c.all) break;
     if (c.b0 <= 0) return false;
-    c.before += all;
+    c.before += c.all;
     c.b0 -= 32;
     load_cursor(p, c, lane);
   }

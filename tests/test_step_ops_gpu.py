@@ -757,6 +757,31 @@ def test_prefill_of_an_empty_batch_and_of_empty_sequences(fp8):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+def test_prefill_uneven_batch_with_bad_sequences(fp8):
+    """More pieces than SMs, taken in order of length: empty chunks, equal lengths,
+    bad lengths and a chunk beyond the bound among them."""
+    rng = np.random.default_rng(14)
+    q_lens = rng.choice([0, 1, 1, 3, 40, 70], 90).tolist()
+    q_lens[5], q_lens[40], q_lens[41], q_lens[89] = 40, 90, 1, 3
+    lens = [n + int(rng.choice([0, 0, 130, rng.integers(0, 300)])) for n in q_lens]
+    x = _attn_case(q_lens, lens, 8, 4, "bf16", 16, 615, fp8=fp8)
+    ref = _plain_prefill(x, window=100, sinks=3)
+    x["max_q"] = 70
+    x["lens"][5], x["lens"][41] = -1, 2**31 - 1
+    start = np.concatenate([[0], np.cumsum(q_lens)])
+    out = torch.full_like(x["q"], 7.0)
+    _, flag = _run_prefill(x, out=out, num_splits=1, window=100, sinks=3)
+    assert flag == da.FLAG_BAD_SEQ_LEN
+    for s in (5, 41):  # bad lengths: zeros
+        assert bool((out[start[s]:start[s + 1]] == 0).all())
+    assert bool((out[start[40]:start[41]] == 7).all())  # a longer chunk than said: left alone
+    for s in (5, 40, 41):
+        for a in ref:
+            a[start[s]:start[s + 1]] = np.nan
+    _close(out, _fp16_probs(ref, "bf16") if fp8 else ref, "bf16")
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 def test_attention_and_cache_write_past_32_bits(fp8):
     """A cache of more than 2^32 elements, used at its far end."""
     h_kv, bs, dtype = 4, 16, "bf16"
