@@ -11,14 +11,15 @@
 //     S_X = Q_X K^T   128 x 128 x 128        X = A, B
 //     O_X += P_X V    128 x 128 x 128
 // Bound by the tensor cores and their operands' path once a chunk has a few
-// hundred rows per KV head: each 64 KB pair of K and V tiles serves 2 x 2 MMAs
-// of 2^21 products, 2048 cycles at the tensor cores' rate, and the MMAs of S take
-// both operands from shared memory at close to its full bandwidth; measured
-// 3200 cycles a pair (an 8192-token prompt of 64 heads on 8: 720 us, 1.53
-// PFLOP/s, 0.78 of cuBLAS's burst rate; 8-bit cache 777 us).  Bound by HBM below
-// that: 32 chunks of 8 tokens over 8k caches take 177 us, 6.1 TB/s.  Few rows
-// over a long cache are cut along the cache (n_split) and joined by a
-// log-sum-exp combine: one chunk of 8 tokens over 131k tokens 94 us, 5.7 TB/s.
+// hundred rows per KV head: each 64 KB pair of K and V tiles serves 2 x 2 groups
+// of eight MMAs (2^21 products), each 512 cycles at the nominal rate, 629 at
+// cuBLAS's best, and the MMAs of S take both operands from shared memory at its
+// full bandwidth; measured 3100 cycles a pair, a group being issued in 650 to 700,
+// with the softmax warps waiting half of the time (an 8192-token prompt of 64 heads
+// on 8: 720 us, 1.53 PFLOP/s, 0.78 of cuBLAS's burst).  Bound by HBM below that: 32
+// chunks of 8 tokens over 8k caches take 169 us, 6.4 TB/s.  Few rows over a long
+// cache are cut along the cache (n_split) and joined by a log-sum-exp combine: one
+// chunk of 8 tokens over 131k tokens 94 us, 5.7 TB/s.
 //
 // Operand placement:
 //   Q_A, Q_B   shared memory [2 halves][128 rows][128 B], 128-byte swizzle,
@@ -54,7 +55,7 @@
 // of product, softmax and product uncovered.  There (`solo`) both sets work on
 // the same rows, A on the even K / V tiles, B on the odd ones, with S, P and O
 // of their own, joined at the end (32 chunks of 8 tokens
-// over 8k caches, 64 heads on 8: 187 us instead of 203).
+// over 8k caches, 64 heads on 8, when this was added: 187 us instead of 203).
 //
 // An 8-bit (e4m3) cache takes the same pipeline with four changes: the K tile's
 // codes, as they land, are the B operand of S on kind::f8f6f4, whose A operand is
@@ -483,7 +484,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool lead = warp == kWarpLoad;
       // A cache that only one piece of each sequence and KV head reads (few rows)
       // streams through L2; otherwise its tiles are kept for the next piece.
-      // (32 chunks of 8 tokens over 8k caches: 180 us, 187 with tiles kept.)
+      // (32 chunks of 8 tokens over 8k caches, when this was added: 180 us, 187 with
+      // tiles kept.)
       const uint64_t keep = p.once ? policy_evict_first() : policy_evict_last();
       const int bs = p.block_size, lg = p.log2_block_size;
       constexpr int kBytes = kF8 ? kCodeBytes : kTileBytes;  // of a tile
