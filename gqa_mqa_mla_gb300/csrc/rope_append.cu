@@ -109,8 +109,20 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const __grid_cons
   }
   __syncthreads();
 
+  // With one or two tokens a CTA a thread keeps its pairs' sines and cosines from
+  // head to head (64 tokens 3.2 -> 2.95 us, 1111 into an 8-bit cache 6.9 -> 6.5);
+  // with four it has them for two or three heads only, and the registers cost
+  // more CTAs than the reads (8192 tokens 55.1 -> 57.7).
+  constexpr bool kHold = kTok <= 2;
+  float4 held[4] = {};
+  int held_of = -1;
 #pragma unroll 1
   while (tl < n_tok) {
+    if (kHold && turned && tl != held_of) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) held[j] = cs[tl][4 * u + j];
+      held_of = tl;
+    }
     int tn = tl, hn = h + kHeads;
     wrap(tn, hn);
     uint4 n0 = make_uint4(0, 0, 0, 0), n1 = n0;
@@ -126,7 +138,7 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const __grid_cons
     if (turned && !is_v) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float4 f = cs[tl][4 * u + j];  // pairs 8 u + 2 j and the next
+        const float4 f = kHold ? held[j] : cs[tl][4 * u + j];  // pairs 8 u + 2 j and the next
         // Their places: neighbours in one piece, or place 2 j (2 j + 1) of both.
         float& x0 = kNext ? (j < 2 ? a : b)[4 * (j & 1)] : a[2 * j];
         float& y0 = kNext ? (j < 2 ? a : b)[4 * (j & 1) + 1] : b[2 * j];
@@ -170,8 +182,8 @@ template <bool kBF16, bool kF8, bool kNext>
 void launch_n(const RopeParams& p, cudaStream_t stream) {
   // A CTA's tokens: as few as put all CTAs on the GPU at once (four per SM
   // of 152), at most four.  64 + 8 + 8 heads in bf16, by 1 / 2 / 4 tokens a
-  // CTA: 300 tokens 3.9 / 4.2 / 6.1 us, 1111 12.4 / 10.4 / 12.3, 2048 18.6 /
-  // 18.1 / 17.5, 8192 60.7 / 54.9 / 55.4 (6.1 TB/s); 8 tokens 62.7 there.
+  // CTA (before `held`): 300 tokens 3.9 / 4.2 / 6.1 us, 1111 12.4 / 10.4 / 12.3,
+  // 2048 18.6 / 18.1 / 17.5, 8192 60.7 / 54.9 / 55.4 (6.1 TB/s); 8 tokens 62.7.
   constexpr int kSlots = 4 * 152;
   auto go = [&](auto kern, int tok) {
     kern<<<static_cast<unsigned>((p.tokens + tok - 1) / tok), kThreads, 0, stream>>>(p);
