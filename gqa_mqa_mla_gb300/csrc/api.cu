@@ -443,6 +443,8 @@ static int gqa_decode_impl(const void* q, const void* k_cache, const void* v_cac
   p.scale_log2 = scale * 1.4426950408889634f;
   p.window = window;
   p.sinks = window > 0 ? sinks : 0;
+  // (A cluster has at most eight CTAs; wide groups have a kernel of their own.)
+  p.joint = p.sinks > 0 && eff > 1 && eff <= 8 && p.group <= kWideGroup;
   p.k_scale = k_scale;
   p.v_scale = v_scale;
   if (eff > 1) {
@@ -490,7 +492,7 @@ static int gqa_decode_impl(const void* q, const void* k_cache, const void* v_cac
   const cudaError_t e = fp8 ? launch_gqa_partial_fp8(p, tk, tv, bf16, stream)
                             : launch_gqa_partial(p, tk, tv, bf16, 0, stream);
   if (e != cudaSuccess) return DECATTN_ERR_CUDA;
-  if (eff > 1) {
+  if (eff > 1 && !p.joint) {
     CombineParams c{p.part_o, p.part_lse, out, L->batch * h_q, eff};
     if (launch_combine(c, kHeadDim, bf16, stream) != cudaSuccess) return DECATTN_ERR_CUDA;
   }

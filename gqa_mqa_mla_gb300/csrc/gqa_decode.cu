@@ -716,9 +716,8 @@ __host__ __device__ constexpr int smem_bytes() {
 }
 
 template <class Consumer, bool kBF16, int kStages, bool kSinks>
-__global__ void __launch_bounds__(32 * (1 + Consumer::kWarps), Consumer::kMinBlocks)
-    gqa_partial_kernel(const __grid_constant__ CUtensorMap tm_k,
-                       const __grid_constant__ CUtensorMap tm_v, const GqaParams p) {
+DECATTN_DEV void gqa_partial(const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                             const GqaParams& p) {
   constexpr int kStage = stage_bytes<Consumer>();
   static_assert(merge_bytes<Consumer>() <= kStages * kStage, "merge area must fit the ring");
   constexpr int kW = Consumer::kWarps;
@@ -882,10 +881,69 @@ __global__ void __launch_bounds__(32 * (1 + Consumer::kWarps), Consumer::kMinBlo
   }
 }
 
-template <class Consumer, bool kBF16, int kStages, bool kSinks>
+// Few sequences in a window: the splits of a sequence and KV head are one cluster,
+// which merges its partials behind a cluster barrier instead of in a second launch
+// (8 sequences, window 2048 behind 64 kept tokens, 32 heads on 8, e4m3: 11.3 us,
+// 12.7 in two launches; 16 with a window of 4096, 64 heads on 8: 46.2 and 47.4).
+// The partials go through the workspace (L2); a warp merges a row as
+// lse_combine_kernel does, the cluster's CTAs taking the rows in turn.  (A call of
+// its own: inlined, the 16-bit kernel takes 175 registers, and above 168 one CTA
+// fits an SM instead of two.)
+template <bool kBF16, int kWarps>
+__device__ __noinline__ void merge_splits(const GqaParams& p) {
+  constexpr int kMost = 8;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, ns = p.n_split;
+  const size_t row0 = static_cast<size_t>(blockIdx.z) * p.h_q + blockIdx.y * p.group;
+  for (int r = blockIdx.x + ns * warp; r < p.group; r += ns * kWarps) {
+    const size_t at = (row0 + r) * ns;
+    const float lse = lane < ns ? __ldcg(p.part_lse + at + lane) : kNegInf;
+    const float4* po = reinterpret_cast<const float4*>(p.part_o + at * kHeadDim) + lane;
+    float4 x[kMost];
+#pragma unroll
+    for (int s = 0; s < kMost; ++s)
+      x[s] = s < ns ? __ldcg(po + s * (kHeadDim / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    float mx = lse;
+#pragma unroll
+    for (int o = kMost / 2; o >= 1; o >>= 1)
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    mx = __shfl_sync(0xffffffffu, mx, 0);
+    uint2 y = make_uint2(0, 0);
+    if (mx != kNegInf && mx != DECATTN_POISON_LSE) {
+      const float w = ex2(lse - mx);
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      float sum = 0.f;
+#pragma unroll
+      for (int s = 0; s < kMost; ++s) {
+        const float ws = __shfl_sync(0xffffffffu, w, s);
+        sum += ws;
+        acc.x = fmaf(ws, x[s].x, acc.x);
+        acc.y = fmaf(ws, x[s].y, acc.y);
+        acc.z = fmaf(ws, x[s].z, acc.z);
+        acc.w = fmaf(ws, x[s].w, acc.w);
+      }
+      const float inv = 1.f / sum;
+      y = make_uint2(pack2<kBF16>(acc.x * inv, acc.y * inv), pack2<kBF16>(acc.z * inv, acc.w * inv));
+    }
+    reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + (row0 + r) * kHeadDim)[lane] = y;
+  }
+}
+
+template <class Consumer, bool kBF16, int kStages, bool kSinks, bool kJoint>
+__global__ void __launch_bounds__(32 * (1 + Consumer::kWarps), Consumer::kMinBlocks)
+    gqa_partial_kernel(const __grid_constant__ CUtensorMap tm_k,
+                       const __grid_constant__ CUtensorMap tm_v, const GqaParams p) {
+  gqa_partial<Consumer, kBF16, kStages, kSinks>(tm_k, tm_v, p);
+  if constexpr (kJoint) {
+    __syncwarp();
+    cluster_sync();
+    merge_splits<kBF16, 1 + Consumer::kWarps>(p);
+  }
+}
+
+template <class Consumer, bool kBF16, int kStages, bool kSinks, bool kJoint>
 cudaError_t launch_with(const GqaParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
                         cudaStream_t stream, unsigned max_cluster) {
-  auto kern = gqa_partial_kernel<Consumer, kBF16, kStages, kSinks>;
+  auto kern = gqa_partial_kernel<Consumer, kBF16, kStages, kSinks, kJoint>;
   constexpr int smem = smem_bytes<Consumer, kStages>();
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -908,8 +966,8 @@ cudaError_t launch_with(const GqaParams& p, const CUtensorMap& tk, const CUtenso
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 1;
-  attr[0].val.clusterDim.y = cluster;
+  attr[0].val.clusterDim.x = kJoint ? static_cast<unsigned>(p.n_split) : 1;
+  attr[0].val.clusterDim.y = kJoint ? 1 : cluster;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
@@ -923,8 +981,11 @@ cudaError_t launch_with(const GqaParams& p, const CUtensorMap& tk, const CUtenso
 template <class Consumer, bool kBF16, int kStages>
 cudaError_t launch_one(const GqaParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
                        cudaStream_t stream, unsigned max_cluster) {
-  return p.sinks > 0 ? launch_with<Consumer, kBF16, kStages, true>(p, tk, tv, stream, max_cluster)
-                     : launch_with<Consumer, kBF16, kStages, false>(p, tk, tv, stream, max_cluster);
+  if (p.sinks > 0)
+    return p.joint
+               ? launch_with<Consumer, kBF16, kStages, true, true>(p, tk, tv, stream, max_cluster)
+               : launch_with<Consumer, kBF16, kStages, true, false>(p, tk, tv, stream, max_cluster);
+  return launch_with<Consumer, kBF16, kStages, false, false>(p, tk, tv, stream, max_cluster);
 }
 
 template <bool kBF16>

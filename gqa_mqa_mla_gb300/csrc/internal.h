@@ -36,6 +36,7 @@ struct GqaParams {
   float scale_log2;               // scale * log2(e)
   int window;                     // > 0: attend only to the last `window` tokens
   int sinks;                      // > 0 (with a window): and to the first `sinks` tokens
+  int joint;                      // sinks, n_split 2..8: the splits' CTAs merge their partials
   const float* k_scale;           // [h_kv], 8-bit caches only: K value = e4m3 * k_scale[j]
   const float* v_scale;           // [h_kv], 8-bit caches only
 };
