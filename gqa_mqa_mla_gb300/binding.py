@@ -188,6 +188,9 @@ def calls():
             if not os.path.exists(_build.CALLS):
                 raise RuntimeError(f"{_build.CALLS} is missing: build it with "
                                    "`python -m gqa_mqa_mla_gb300.build` (no fallback exists)")
+            if not _build.calls_match():
+                raise RuntimeError(f"{_build.CALLS} was built for another PyTorch: rebuild it with "
+                                   "`python -m gqa_mqa_mla_gb300.build`")
             spec = importlib.util.spec_from_file_location("_calls", _build.CALLS)
             module = importlib.util.module_from_spec(spec)
             spec.loader.exec_module(module)

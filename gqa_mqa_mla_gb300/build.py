@@ -25,6 +25,7 @@ LIB_DIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIB_DIR, "libdecattn.so")
 CALLS = os.path.join(LIB_DIR, "_calls.so")
 CALLS_SRC = os.path.join(CSRC, "torch_calls.cpp")
+CALLS_FOR = CALLS + ".for"  # the PyTorch that _calls.so was compiled against
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -47,8 +48,19 @@ def _inputs() -> list[str]:
         os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h")) + [__file__]
 
 
+def calls_match() -> bool:
+    """Was _calls.so compiled against the PyTorch that is installed?"""
+    import torch
+
+    try:
+        with open(CALLS_FOR) as f:
+            return f.read() == torch.__version__
+    except OSError:
+        return False
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(CALLS):
+    if not os.path.exists(LIB) or not os.path.exists(CALLS) or not calls_match():
         return False
     t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
     return all(os.path.getmtime(f) <= t for f in _inputs())
@@ -73,6 +85,8 @@ def _build_calls() -> None:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {CALLS_SRC}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, CALLS)
+    with open(CALLS_FOR, "w") as f:
+        f.write(torch.__version__)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:

@@ -10,6 +10,7 @@
 
 #include <dlfcn.h>
 
+#include <optional>
 #include <string>
 
 #include <ATen/ops/empty.h>
@@ -158,6 +159,20 @@ void* stream_of(PyObject* o, int index) {
   return p;
 }
 
+// A call on a given stream allocates on it, as one made under that stream would:
+// what it frees on its return (a workspace) is not handed to work on another.
+class OnStream {
+  c10::cuda::CUDAGuard device_;
+  std::optional<c10::cuda::CUDAStreamGuard> stream_;
+
+ public:
+  OnStream(int index, bool given, void* stream) : device_(static_cast<c10::DeviceIndex>(index)) {
+    if (given)
+      stream_.emplace(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(stream),
+                                                       static_cast<c10::DeviceIndex>(index)));
+  }
+};
+
 // The allocations and the library's call run without the interpreter's lock (a
 // launch waits when the device's queue is full); it is held again on the way out.
 class Unlocked {
@@ -235,9 +250,10 @@ PyObject* paged_plan(PyObject* const* a, Py_ssize_t n) {
     }
   }
   auto at_ = [](const Tensor& t) { return t.data_ptr<int>(); };
+  const bool given = !none(a[13]);
   const int st = [&] {
     const Unlocked unlocked;
-    const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(index));
+    const OnStream guard(index, given, L.stream);
     // One allocation for the outputs that were not given (a call of at::empty
     // takes 0.6 us, the smallest step's kernel 4).
     int64_t total = 0;
@@ -340,9 +356,10 @@ PyObject* rope_append(PyObject* const* a, Py_ssize_t n) {
   const void *qp = q.data_ptr(), *kp = k.data_ptr(), *vp = v.data_ptr();
   void *kcp = kc.data_ptr(), *vcp = vc.data_ptr();
   const int *pp = pos.data_ptr<int>(), *sp = slots.data_ptr<int>();
+  const bool given = !none(a[13]);
   const int st = [&] {
     const Unlocked unlocked;
-    const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(index));
+    const OnStream guard(index, given, L.stream);
     if (!out.defined()) out = at::empty({T, h_q, d}, q.options());
     return fp8 ? lib.gqa_rope_append_fp8kv(qp, kp, vp, qs, ks, vs, sk, sv, pp, rope, sp,
                                            out.data_ptr(), kcp, vcp, T, h_q, h_kv, d, &L)
@@ -444,9 +461,10 @@ PyObject* decode(PyObject* const* a, Py_ssize_t n) {
   Tensor out = x.output(a[12], false), ws = x.workspace(a[13]);
   const void *q = x.q->data_ptr(), *kc = x.kc->data_ptr(), *vc = x.vc->data_ptr();
   const int *bt = x.table->data_ptr<int>(), *sl = x.lens->data_ptr<int>();
+  const bool given = !none(a[15]);
   const int st = [&] {
     const Unlocked unlocked;
-    const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(x.index));
+    const OnStream guard(x.index, given, L.stream);
     if (L.num_splits == 0) {
       const int ns =
           windowed ? lib.gqa_decode_sinks_plan_splits(B, x.h_q, x.h_kv, x.d, max_len, window,
@@ -496,9 +514,10 @@ PyObject* prefill(PyObject* const* a, Py_ssize_t n) {
   const void *q = x.q->data_ptr(), *kc = x.kc->data_ptr(), *vc = x.vc->data_ptr();
   const int *bt = x.table->data_ptr<int>(), *sl = x.lens->data_ptr<int>();
   const int* qs = start.data_ptr<int>();
+  const bool given = !none(a[17]);
   const int st = [&] {
     const Unlocked unlocked;
-    const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(x.index));
+    const OnStream guard(x.index, given, L.stream);
     if (L.num_splits == 0) {
       const int ns = lib.gqa_prefill_plan_splits(B, T, max_q, x.h_q, x.h_kv, x.d, max_len, window,
                                                  sinks, 0);

@@ -851,6 +851,32 @@ def test_calls_on_two_streams_at_once():
         assert torch.equal(want, got)
 
 
+@pytest.mark.parametrize("decode", [False, True])
+def test_workspaces_of_calls_on_a_given_stream_stay_theirs(decode):
+    """A call on another stream frees its workspace when it returns, long before it
+    runs: work on the current stream must not get that memory."""
+    x = _attn_case([1, 1, 1], [900, 90, 700], 16, 4, "bf16", 16, 612)
+
+    def call(**kw):
+        if decode:
+            return da.gqa_decode_sinks(x["q"], *x["caches"], x["table"], x["lens"], scale=0.1,
+                                       max_seq_len=900, window=800, sinks=4, num_splits=10, **kw)
+        return da.gqa_prefill(x["q"], *x["caches"], x["table"], x["start"], x["lens"], scale=0.1,
+                              max_q_len=1, max_seq_len=900, num_splits=7, **kw)
+
+    want = call()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)  # the call runs in some ms
+    got = call(stream=s)
+    size = max(da.gqa_prefill_workspace_size(3, 16, 7), da.gqa_workspace_size(3, 16, 10))
+    spoil = [torch.full((size // 4,), float("nan"), device=DEV) for _ in range(4)]
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and len(spoil) == 4
+
+
 def test_a_whole_step_in_one_graph():
     """Plan, rotation with cache write, and 8-bit prefill captured together and
     replayed for several steps equal the same calls made one by one."""
