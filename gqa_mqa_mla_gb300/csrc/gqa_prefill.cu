@@ -13,10 +13,11 @@
 // Bound by the tensor cores and their operands' path once a chunk has a few
 // hundred rows per KV head: each 64 KB pair of K and V tiles serves 2 x 2 groups
 // of eight MMAs (2^21 products), each 512 cycles at the nominal rate, 629 at
-// cuBLAS's best, and the MMAs of S take both operands from shared memory at its
-// full bandwidth; measured 3100 cycles a pair, a group being issued in 650 to 700,
-// with the softmax warps waiting half of the time (an 8192-token prompt of 64 heads
-// on 8: 720 us, 1.53 PFLOP/s, 0.78 of cuBLAS's burst).  Bound by HBM below that: 32
+// cuBLAS's best, and moves 256 KB through shared memory (S takes both operands
+// from there); measured 3100 cycles a pair, a group being issued in 650 to 700, with
+// the softmax warps waiting half of the time (an 8192-token prompt of 64 heads on 8:
+// 720 us, 1.53 PFLOP/s, 0.78 of cuBLAS's burst).  S in halves of 64 tokens ahead of
+// the softmax moves 320 KB and takes a fifth longer: the bytes are the bound.  Bound by HBM below that: 32
 // chunks of 8 tokens over 8k caches take 169 us, 6.4 TB/s.  Few rows over a long
 // cache are cut along the cache (n_split) and joined by a log-sum-exp combine: one
 // chunk of 8 tokens over 131k tokens 94 us, 5.7 TB/s.
