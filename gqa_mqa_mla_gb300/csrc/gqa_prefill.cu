@@ -17,10 +17,10 @@
 // from there); measured 3100 cycles a pair, a group being issued in 650 to 700, with
 // the softmax warps waiting half of the time (an 8192-token prompt of 64 heads on 8:
 // 720 us, 1.53 PFLOP/s, 0.78 of cuBLAS's burst).  S in halves of 64 tokens ahead of
-// the softmax moves 320 KB and takes a fifth longer: the bytes are the bound.  Bound by HBM below that: 32
-// chunks of 8 tokens over 8k caches take 169 us, 6.4 TB/s.  Few rows over a long
-// cache are cut along the cache (n_split) and joined by a log-sum-exp combine: one
-// chunk of 8 tokens over 131k tokens 94 us, 5.7 TB/s.
+// the softmax moves 320 KB and takes a fifth longer: the bytes are the bound.
+// Bound by HBM below that: 32 chunks of 8 tokens over 8k caches take 169 us, 6.4
+// TB/s.  Few rows over a long cache are cut along the cache (n_split) and joined by
+// a log-sum-exp combine: one chunk of 8 tokens over 131k tokens 94 us, 5.7 TB/s.
 //
 // Operand placement:
 //   Q_A, Q_B   shared memory [2 halves][128 rows][128 B], 128-byte swizzle,
