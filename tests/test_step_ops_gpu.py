@@ -262,6 +262,37 @@ def test_rope_append_of_position_zero_moves_bytes():
         assert torch.equal(c.view(-1, 4, 128)[slots.long()], x)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_rope_append_quantises_as_the_single_token_write(dtype):
+    """Without a turn the e4m3 codes are gqa_kv_append_fp8kv's bit for bit: every
+    16-bit pattern (ties, signed zeros, subnormals, infinities, NaN) under scales
+    that make ties, odd ones, tiny, huge, negative, zero and infinite ones."""
+    h_kv, T = 16, 512
+    scale = [1.0, 0.5, 1 / 448, 0.0123, 3.0, 7.7e-3, -0.3, 1e-19, 1e19, 2.0**-70, 2.0**70,
+             1.9999999, 0.33333334, 1e-40, 0.0, float("inf")]
+    scales = [torch.tensor(scale, device=DEV), torch.tensor(scale[::-1], device=DEV)]
+    bits = torch.arange(2**16, device=DEV, dtype=torch.int32).to(torch.int16)
+    rows = bits.view(TYPES[dtype]).view(T, 1, 128).repeat(1, h_kv, 1).contiguous()
+    back = rows.flip(0).contiguous()
+    nb = T // 16
+    got = [torch.zeros((nb, 16, h_kv, 128), dtype=torch.uint8, device=DEV) for _ in range(2)]
+    want = [torch.zeros_like(c) for c in got]
+    rope = da.rope_table([0.0] * 64)
+    slots = torch.arange(T, device=DEV, dtype=torch.int32)
+    # (v is never turned; k only by zero angles: x * 1 - y * 0 is x where y is finite.)
+    da.gqa_rope_append_fp8kv(rows, back, rows, *scales, _i32(np.zeros((1, T))), rope, slots, *got)
+    table = torch.arange(nb, device=DEV, dtype=torch.int32)
+    da.gqa_kv_append_fp8kv(back, rows, *scales, slots % 16, (table[slots.long() // 16])[:, None],
+                           *want)
+    torch.cuda.synchronize()
+    assert torch.equal(got[1], want[1])
+    flat = lambda c: c.view(T, h_kv, 128)  # noqa: E731
+    x = back.float()
+    partner = torch.cat([x[..., 64:], x[..., :64]], -1)
+    plain = torch.isfinite(partner) & (x != 0)  # (a zero may gain the other sign: -0 + 0)
+    assert bool(plain.any()) and torch.equal(flat(got[0])[plain], flat(want[0])[plain])
+
+
 # ------------------------------------------------------------------ chunk attention
 
 
