@@ -309,10 +309,11 @@ __device__ __forceinline__ uint4* staged(uint8_t* stage, int row, int c) {
 // no larger than half of the term's step, so two terms hold a bf16 query and
 // three an fp16 one exactly, but for parts below 2^-10 (e4m3's smallest step) of
 // the scaled row.  Term t of the tile: [128 rows][128 codes], 128-byte swizzle;
-// k goes to qexp[r].  16 lanes take a row, 8 values each.
+// k goes to qexp[r].  16 lanes take a row, 8 values each; of the 32 rows the pairs
+// [b0, b1) are this warp's, as far as they are real (the others may hold anything).
 template <bool kBF16, int kTerms>
 __device__ __forceinline__ void split_q(const PrefillParams& p, const Item& w, int x, int part,
-                                        uint32_t inv_g, uint8_t* dst, int8_t* qexp) {
+                                        int b0, int b1, uint32_t inv_g, uint8_t* dst, int8_t* qexp) {
   const int lane = threadIdx.x & 31, c = lane & 15;
   const int rows = (x ? w.tok_b : w.tok_a) * p.group;
   const uint16_t* src =
@@ -325,16 +326,17 @@ __device__ __forceinline__ void split_q(const PrefillParams& p, const Item& w, i
     for (int u = 0; u < 4; ++u) {
       const int r = 32 * part + 2 * (b + u) + (lane >> 4);
       const int tk = static_cast<int>((static_cast<uint32_t>(r) * inv_g) >> 16);
-      y[u] = b < 16 && r < rows
+      y[u] = b < b1 && r < rows
                  ? *reinterpret_cast<const uint4*>(
                        src + static_cast<int64_t>(tk * (p.h_q - p.group) + r) * kHeadDim)
                  : make_uint4(0, 0, 0, 0);
     }
   };
   uint4 y[4], ahead[4];
-  load(0, y);
+  b1 = min(b1, (rows - 32 * part + 1) >> 1);
+  load(b0, y);
 #pragma unroll 1
-  for (int b = 0; b < 16; b += 4) {
+  for (int b = b0; b < b1; b += 4) {
     load(b + 4, ahead);
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -948,13 +950,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = mbar_wait_or_abort(bar(kBarQFree), (q_made & 1) ^ 1, p.err_flag, abort_word);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            if (x == 0 || w.tok_b > 0)
-              split_q<kBF16, kTerms>(p, w, x, warp & 3, inv_g, smem + x * kTerms * kCodeBytes,
-                                     qexp + x * kM);
+            // (Solo: tile A's rows, half of them each.)
+            if (w.solo || x == 0 || w.tok_b > 0)
+              split_q<kBF16, kTerms>(p, w, half, warp & 3, w.solo ? 8 * x : 0,
+                                     w.solo ? 8 * x + 8 : 16, inv_g,
+                                     smem + half * kTerms * kCodeBytes, qexp + half * kM);
             fence_proxy_async_smem();
             mbar_arrive(bar(kBarQ));
-            // (Solo: the B warps' row exponents come from the A warps.)
-            if (w.solo && x == 1) {
+            // (Solo: some of a warp's row exponents come from another warp.)
+            if (w.solo) {
               ok = mbar_wait_or_abort(bar(kBarQ), q_made & 1, p.err_flag, abort_word);
               ok = __all_sync(0xffffffffu, ok);
               if (!ok) break;
@@ -966,7 +970,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float ks = p.k_scale[w.j];
             negate ^= ks < 0.f;
             scale *= fabsf(ks);
-            scale = fmaxf(scale * __uint_as_float((127 - qexp[half * kM + r]) << 23), 1e-37f);
+            scale = fmaxf(
+                scale * __uint_as_float((127 - (r < tok * G ? qexp[half * kM + r] : 0)) << 23), 1e-37f);
           }
         }
         if (negate) plain_hi = plain_lo;  // (every tile changes its scores' sign)
