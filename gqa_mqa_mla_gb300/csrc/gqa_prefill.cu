@@ -1133,8 +1133,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const bool bad = w.bad || bad_word[k & 1] != 0;
         // Weight of this warp's O (and, solo, of the other's): 1 / l, times an
-        // 8-bit cache's V scale; 0 for a row that sees nothing or is bad.
-        auto norm = [&]() { return l > 0.f && !bad ? (kF8 ? p.v_scale[w.j] : 1.f) / l : 0.f; };
+        // 8-bit cache's V scale; 0 for a row that sees nothing (l = 0, exactly) or
+        // is bad.  NaN scores make l NaN, and the row with it.
+        auto norm = [&]() { return l == 0.f || bad ? 0.f : (kF8 ? p.v_scale[w.j] : 1.f) / l; };
         float wa = norm(), wb = 0.f;
         // This lane stores piece lane % 8 of the warp's rows lane / 8, + 4, ...
         // + 28: their places among the packed rows, from the tile's first one on.
@@ -1253,7 +1254,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (p.n_split > 1 && !(w.solo && x == 1)) {
           if (r < rows)
             p.part_lse[(row0 + static_cast<int64_t>(r_tok) * p.h_q + (r - r_tok * G)) * p.n_split +
-                       w.split] = bad ? DECATTN_POISON_LSE : l > 0.f ? m + lg2(l) : kNegInf;
+                       w.split] = bad ? DECATTN_POISON_LSE : l == 0.f ? kNegInf : m + lg2(l);
         }
       }
       if (ok) release_item(k);
@@ -1283,7 +1284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Joins the splits of a row: out = sum_s w_s o_s / sum_s w_s, w_s = 2^(lse_s -
 // max).  One warp per (token, head); tokens outside every sequence stay as
 // they are, splits with nothing to see (lse = -inf) have no partial to read,
-// and a bad sequence (+inf) gives zeros.
+// a bad sequence (+inf) gives zeros, and a split with NaN scores (lse NaN) NaN.
 template <bool kBF16>
 __global__ void __launch_bounds__(256) gqa_prefill_combine_kernel(const PrefillParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1299,12 +1300,16 @@ __global__ void __launch_bounds__(256) gqa_prefill_combine_kernel(const PrefillP
   const int a = p.q_start[lo], e = p.q_start[lo + 1];
   if (tok < a || tok >= e || a < 0 || e > p.tokens || e - a > p.max_q_len) return;
   const float* lse = p.part_lse + row * p.n_split;
-  float mx = kNegInf;
-  for (int s = lane; s < p.n_split; s += 32) mx = fmaxf(mx, lse[s]);
+  float mx = kNegInf;  // (the maximum of the numbers: NaN does not count)
+  bool some = false;
+  for (int s = lane; s < p.n_split; s += 32) {
+    mx = fmaxf(mx, lse[s]);
+    some |= lse[s] != kNegInf;
+  }
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   uint2* dst = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + row * kHeadDim);
-  if (mx == kNegInf || mx == DECATTN_POISON_LSE) {
+  if (!__any_sync(0xffffffffu, some) || mx == DECATTN_POISON_LSE) {
     dst[lane] = make_uint2(0, 0);
     return;
   }
@@ -1317,8 +1322,9 @@ __global__ void __launch_bounds__(256) gqa_prefill_combine_kernel(const PrefillP
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int s = s0 + u;
-      wt[u] = s < p.n_split ? ex2(lse[s] - mx) : 0.f;
-      x[u] = wt[u] != 0.f ? po[s * (kHeadDim / 4) + lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+      const float at = s < p.n_split ? lse[s] : kNegInf;
+      wt[u] = at != kNegInf ? ex2(at - mx) : 0.f;
+      x[u] = at != kNegInf ? po[s * (kHeadDim / 4) + lane] : make_float4(0.f, 0.f, 0.f, 0.f);
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {

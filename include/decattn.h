@@ -423,6 +423,8 @@ int gqa_rope_append_fp8kv(const void* q, const void* k_new, const void* v_new, i
  * NaN or infinity in v at position t may reach the rows before t that share
  * its tile (slots past seq_lens and slots that no row of the tile's sequence
  * may see can hold anything).
+ * A NaN in a query or in a key that it sees, or a score of +inf, makes a row
+ * NaN; a score of -inf has weight 0, and a row with no other is zeros.
  * A seq_len outside [0, max_seq_len] or a bad block id (flags as for
  * gqa_decode) gives zero rows for that sequence's affected rows.  A chunk longer
  * than max_q_len, or row offsets that decrease or leave [0, tokens], set

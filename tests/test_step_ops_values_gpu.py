@@ -1,0 +1,99 @@
+"""What the attention kernels make of NaN and infinity that a row sees, on the
+GPU against the definition in 64 bits: a NaN in a query or in a key of its, or an
+infinite score, makes the whole row NaN, and one in a value the value's dimension;
+a score of -inf has weight 0.  (What no row sees may hold anything: the other
+tests.)  Tolerances of the finite rows as in test_step_ops_gpu.py."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import step
+
+from test_step_ops_gpu import _attn_case, _close, _fp16_probs, _run_prefill
+
+pytestmark = pytest.mark.gpu
+
+NAN = float("nan")
+
+
+def _values(x):
+    """The caches' values in 64 bits, NaN and infinities as they are."""
+    if x["scales"] is None:
+        return [c.double().cpu().numpy() for c in x["caches"]]
+    return [(c.view(torch.float8_e4m3fn).double() * s.double()[:, None]).cpu().numpy()
+            for c, s in zip(x["caches"], x["scales"])]
+
+
+def _defined(x, **kw):
+    with np.errstate(all="ignore"):
+        return step.attend(x["q"].double().cpu().numpy(), *_values(x), x["table"].cpu().numpy(),
+                           x["start"].cpu().numpy(), x["lens"].cpu().numpy(), **kw)
+
+
+def _slot(x, b, t):
+    bs = x["caches"][0].shape[1]
+    return int(x["table"][b, t // bs]), t % bs
+
+
+def _spoil(x, what):
+    """Puts one value that is not finite where rows see it."""
+    fp8 = x["scales"] is not None
+    last = int(x["start"][1]) - 1  # the first sequence's last row
+    if what in ("q nan", "q inf", "q -inf"):
+        x["q"][last, 1, 77] = float(what[2:])
+        x["q"][0, 0, 3] = NAN  # and the first row's first head
+        return
+    kind, value, t = what.split()
+    t = int(x["lens"][0]) - 2 if t == "late" else int(t)
+    blk, at = _slot(x, 0, t)
+    x["caches"][0 if kind == "k" else 1][blk, at, 0, 5] = 0x7F if fp8 else float(value)
+
+
+def _agrees(got, ref, clean, dtype, what):
+    """NaN and infinities where the definition has them; the rest within the
+    tolerance (whose score error is the clean data's: an infinite key has no
+    error of its own)."""
+    out = ref[0]
+    g = got.double().cpu().numpy()
+    assert np.array_equal(np.isnan(g), np.isnan(out)), (what, int(np.isnan(g).sum()),
+                                                       int(np.isnan(out).sum()))
+    assert np.isnan(out).any() or np.isinf(out).any() or "inf" in what
+    big = np.isinf(out)
+    assert np.array_equal(g[big], out[big]), what
+    keep = np.isfinite(out)
+    r = [np.where(keep, a, np.nan) for a in ref[:3]]
+    # (0 times an infinite value: nothing is left of it.)
+    r[1], r[2] = (np.where(np.isfinite(a), a, c) for a, c in zip(r[1:], clean[1:3]))
+    _close(torch.from_numpy(np.where(keep, g, 0.0)), (r[0], r[1], r[2], clean[3]), dtype, what)
+
+
+# (An 8-bit cache holds no infinity.)
+WHAT = [(w, fp8) for w in ("q nan", "q inf", "q -inf", "k nan 0", "k nan late", "k inf 2",
+                           "k -inf 2", "v nan 0", "v inf 0")
+        for fp8 in (False, True) if not (fp8 and "inf" in w)]
+
+CHUNKS = [
+    # q_lens, lens, h_q, h_kv, dtype, block, window, sinks
+    ([40, 3, 130], [400, 300, 130], 8, 2, "bf16", 16, 0, 0),
+    ([3, 5], [700, 90], 64, 1, "fp16", 64, 0, 0),
+    ([50, 3, 200], [400, 900, 333], 8, 2, "fp16", 16, 60, 4),
+    ([260], [300], 4, 4, "bf16", 8, 0, 0),
+]
+
+
+@pytest.mark.parametrize("what,fp8", WHAT)
+@pytest.mark.parametrize("case", range(len(CHUNKS)))
+def test_prefill_passes_on_what_is_not_finite(case, what, fp8):
+    q_lens, lens, h_q, h_kv, dtype, bs, window, sinks = CHUNKS[case]
+    x = _attn_case(q_lens, lens, h_q, h_kv, dtype, bs, 700 + case, fp8=fp8)
+    kw = dict(scale=0.09, window=window, sinks=sinks)
+    clean = _defined(x, **kw)
+    _spoil(x, what)
+    ref = _defined(x, **kw)
+    if fp8:
+        ref, clean = (_fp16_probs(r, dtype) for r in (ref, clean))
+    for splits in (1, 3):
+        out, flag = _run_prefill(x, scale=0.09, window=window or None, sinks=sinks,
+                                 num_splits=splits)
+        assert flag == 0
+        _agrees(out, ref, clean, dtype, f"{what}, {splits} splits")
