@@ -5,7 +5,8 @@
 // denominator (log2 domain, scores already scaled by log2 e).  The merged
 // output is  sum_j w_j o_j / sum_j w_j  with  w_j = 2^(lse_j - max_k lse_k);
 // an empty range (lse = -inf) has weight 0.  A +inf lse marks a range that
-// met bad data: the whole row is written as zeros.
+// met bad data: the whole row is written as zeros.  A NaN lse (NaN scores)
+// makes the row NaN.
 //
 // One warp per row, kRowsPerCta rows per CTA.  Lane l owns the float4
 // columns l, l + 32, ...; the weights are computed one per lane and
@@ -28,18 +29,20 @@ template <int D, bool kBF16, typename RowOf>
 __device__ __forceinline__ void merge_row(const float* lse, const float* po, RowOf row, int ns,
                                           uint16_t* out, int lane) {
   constexpr int kVec = D / 128;  // float4 per lane
-  float mx = kNegInf;
-  bool poison = false;
+  float mx = kNegInf;  // the maximum of the numbers: NaN does not count
+  bool poison = false, some = false;
   for (int s = lane; s < ns; s += 32) {
     const float v = lse[row(s)];
     poison |= (v == kPosInf);
+    some |= (v != kNegInf);
     mx = fmaxf(mx, v);
   }
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, off));
   poison = __any_sync(kFull, poison);
+  some = __any_sync(kFull, some);
   uint2* dst = reinterpret_cast<uint2*>(out);
-  if (poison || mx == kNegInf) {
+  if (poison || !some) {
 #pragma unroll
     for (int v = 0; v < kVec; ++v) dst[v * 32 + lane] = make_uint2(0, 0);
     return;

@@ -57,6 +57,10 @@ constexpr int kHalfBytes = kTile * 128;         // one 64-column half of a K or 
 constexpr int kKvTileBytes = 2 * kHalfBytes;    // 16 KB
 constexpr int kStageBytes = 2 * kKvTileBytes;   // K + V: 32 KB
 constexpr float kNegInf = -__builtin_huge_valf();
+// The running maxima begin at the lowest finite value, not at -inf: 2^(s - m) is
+// then 0 for a score of -inf even where nothing else was seen, and only a NaN or
+// +inf score makes the sum NaN.
+constexpr float kLowest = -3.402823466e38f;
 
 // Byte offset of 16-byte chunk c (0..15) of token row r (0..63) in a 16-bit
 // K or V tile.  The tile lands in groups of R = min(block size, 64) rows
@@ -96,7 +100,7 @@ struct CcConsumer {
                    d = unpack2<kBF16>(w.w);
       q[g][0] = a.x; q[g][1] = a.y; q[g][2] = bb.x; q[g][3] = bb.y;
       q[g][4] = c.x; q[g][5] = c.y; q[g][6] = d.x; q[g][7] = d.y;
-      m[g] = kNegInf;
+      m[g] = kLowest;
       l[g] = 0.f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) o[g][e] = 0.f;
@@ -147,7 +151,7 @@ struct CcConsumer {
       for (int i = 1; i < 8; ++i) mt = fmaxf(mt, s[i][g]);
       mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));
       const float m_new = fmaxf(m[g], mt);
-      const float corr = (m_new == kNegInf) ? 1.f : ex2(m[g] - m_new);
+      const float corr = ex2(m[g] - m_new);
       m[g] = m_new;
       l[g] *= corr;
 #pragma unroll
@@ -241,7 +245,7 @@ struct MmaConsumer {
     }
 #pragma unroll
     for (int n = 0; n < 16; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
-    m[0] = m[1] = kNegInf;
+    m[0] = m[1] = kLowest;
     l[0] = l[1] = 0.f;
   }
 
@@ -298,7 +302,6 @@ struct MmaConsumer {
       mx_lo = fmaxf(mx_lo, __shfl_xor_sync(0xffffffffu, mx_lo, 2));
       mx_hi = fmaxf(mx_hi, __shfl_xor_sync(0xffffffffu, mx_hi, 1));
       mx_hi = fmaxf(mx_hi, __shfl_xor_sync(0xffffffffu, mx_hi, 2));
-      // Every chunk holds at least one valid token, so the new maxima are finite.
       const float mn_lo = fmaxf(m[0], mx_lo), mn_hi = fmaxf(m[1], mx_hi);
       const float c_lo = ex2(m[0] - mn_lo), c_hi = ex2(m[1] - mn_hi);
       m[0] = mn_lo;
@@ -396,7 +399,7 @@ struct CcConsumerF8 {
                    d = unpack2<kBF16>(w.w);
       q[g][0] = a.x; q[g][1] = a.y; q[g][2] = bb.x; q[g][3] = bb.y;
       q[g][4] = c.x; q[g][5] = c.y; q[g][6] = d.x; q[g][7] = d.y;
-      m[g] = kNegInf;
+      m[g] = kLowest;
       l[g] = 0.f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) o[g][e] = 0.f;
@@ -453,7 +456,7 @@ struct CcConsumerF8 {
       for (int i = 1; i < 8; ++i) mt = fmaxf(mt, s[i][g]);
       mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 16));
       const float m_new = fmaxf(m[g], mt);
-      const float corr = (m_new == kNegInf) ? 1.f : ex2(m[g] - m_new);
+      const float corr = ex2(m[g] - m_new);
       m[g] = m_new;
       l[g] *= corr;
 #pragma unroll
@@ -554,7 +557,7 @@ struct MmaConsumerF8T {
         qb[ks][nt][0] = pack2<false>(f0.x, f0.y);
         qb[ks][nt][1] = pack2<false>(f1.x, f1.y);
       }
-      m[nt][0] = m[nt][1] = kNegInf;
+      m[nt][0] = m[nt][1] = kLowest;
       l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
       for (int bb = 0; bb < 8; ++bb) o[bb][nt][0] = o[bb][nt][1] = o[bb][nt][2] = o[bb][nt][3] = 0.f;
@@ -621,7 +624,6 @@ struct MmaConsumerF8T {
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-        // Every chunk holds at least one valid token, so the new maximum is finite.
         const float mn = fmaxf(m[nt][e], mx);
         cr[nt][e] = ex2(m[nt][e] - mn);
         moved |= cr[nt][e] != 1.f;
@@ -856,7 +858,7 @@ DECATTN_DEV void gqa_partial(const CUtensorMap& tm_k, const CUtensorMap& tm_v,
   const int tid = threadIdx.x - 32;
   for (int e = tid; e < G * kHeadDim; e += kW * 32) {
     const int r = e / kHeadDim, d = e % kHeadDim;
-    float M = kNegInf;
+    float M = kLowest;
 #pragma unroll
     for (int w = 0; w < kW; ++w)
       if (Consumer::covers(w, r)) M = fmaxf(M, mm[Consumer::slot(w, r)]);
@@ -865,18 +867,17 @@ DECATTN_DEV void gqa_partial(const CUtensorMap& tm_k, const CUtensorMap& tm_v,
     for (int w = 0; w < kW; ++w) {
       if (!Consumer::covers(w, r)) continue;
       const int sl = Consumer::slot(w, r);
-      const float mw = mm[sl];
-      if (mw == kNegInf) continue;
-      const float f = ex2(mw - M);
+      const float f = ex2(mm[sl] - M);
       L = fmaf(ml[sl], f, L);
       O = fmaf(mo[sl * kHeadDim + d], f, O);
     }
-    const float res = L > 0.f ? O / L : 0.f;
+    // L is 0, exactly, where no score but -inf was seen; NaN scores make it NaN.
+    const float res = L == 0.f ? 0.f : O / L;
     if (p.n_split == 1) {
       static_cast<uint16_t*>(p.out)[(row0 + r) * kHeadDim + d] = round1<kBF16>(res);
     } else {
       p.part_o[((row0 + r) * p.n_split + split) * kHeadDim + d] = res;
-      if (d == 0) p.part_lse[(row0 + r) * p.n_split + split] = L > 0.f ? M + lg2(L) : kNegInf;
+      if (d == 0) p.part_lse[(row0 + r) * p.n_split + split] = L == 0.f ? kNegInf : M + lg2(L);
     }
   }
 }
@@ -902,13 +903,13 @@ __device__ __noinline__ void merge_splits(const GqaParams& p) {
 #pragma unroll
     for (int s = 0; s < kMost; ++s)
       x[s] = s < ns ? __ldcg(po + s * (kHeadDim / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
-    float mx = lse;
+    float mx = lse;  // (the maximum of the numbers: NaN does not count)
 #pragma unroll
     for (int o = kMost / 2; o >= 1; o >>= 1)
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     mx = __shfl_sync(0xffffffffu, mx, 0);
     uint2 y = make_uint2(0, 0);
-    if (mx != kNegInf && mx != DECATTN_POISON_LSE) {
+    if (__any_sync(0xffffffffu, lse != kNegInf) && mx != DECATTN_POISON_LSE) {
       const float w = ex2(lse - mx);
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
       float sum = 0.f;

@@ -95,6 +95,7 @@ constexpr int kTmemCols = 256;
 constexpr int kTmemO = 0;                         // 128 columns
 constexpr int kTmemS = 128;                       // S(j): 128 + 64 (j & 1)
 constexpr float kNegInf = -__builtin_huge_valf();
+constexpr float kLowest = -3.402823466e38f;  // where the running maxima begin (see gqa_decode.cu)
 constexpr float kRescaleThreshold = 8.0f;         // log2 units: p stays <= 2^8
 
 // Shared-memory layout.  16-bit cache: K and V rings of 16-bit tiles (the
@@ -530,7 +531,7 @@ __global__ void __launch_bounds__(kThreads)
     bool ok = true;
     // m_used: the row's running max (the same in all four threads of the
     // row); l: this thread's partial row sum over its columns.
-    float m_used = kNegInf, l = 0.f;
+    float m_used = kLowest, l = 0.f;
     const float lowest = scale >= 0.f ? kNegInf : -kNegInf;
     const int c_own = 32 * hl + 16 * cg, c_oth = 32 * hl + 16 * (cg ^ 1);
     for (int it = 0; ok && it < n; ++it) {
@@ -576,7 +577,7 @@ __global__ void __launch_bounds__(kThreads)
       const bool need = mt > m_used + kRescaleThreshold;
       if (__any_sync(0xffffffffu, need)) {
         const float m_new = need ? mt : m_used;
-        const float factor = need ? ex2(m_used - m_new) : 1.f;  // 0 when m_used = -inf
+        const float factor = need ? ex2(m_used - m_new) : 1.f;  // 0 from the lowest value
         if (it > 0) {
           // O += P(it - 1) V(it - 1) must have completed before O is rescaled.
           if (!mbar_wait_or_abort(bar(kBarPvDone + ((it - 1) & 1)), ((it - 1) >> 1) & 1,
@@ -687,10 +688,16 @@ __global__ void __launch_bounds__(kThreads)
       tc_fence_after();
       const float lsum = red[r] + red[kM + r];
       // An 8-bit cache's V scale multiplies the whole output row.
-      const float inv = lsum > 0.f ? (kF8 ? p.v_scale[j] : 1.f) / lsum : 0.f;
+      // (The sum is 0, exactly, where no score but -inf was seen: O may then be 0
+      // times an infinite value.  NaN scores make the sum NaN.)
+      const float inv = lsum == 0.f ? 0.f : (kF8 ? p.v_scale[j] : 1.f) / lsum;
       float o[32];
       tmem_ld16x2_x32<64>(tmem + lane_base + kTmemO + 32 * cg, o);
       tc_wait_ld();
+      if (__any_sync(0xffffffffu, lsum == 0.f)) {
+#pragma unroll
+        for (int kk = 0; kk < 32; ++kk) o[kk] = lsum == 0.f ? 0.f : o[kk];
+      }
       if (mine) {
         const size_t row = row0 + r;
         const int col = 64 * hl + 32 * cg;
@@ -710,7 +717,7 @@ __global__ void __launch_bounds__(kThreads)
             dst[k] = make_float4(o[4 * k] * inv, o[4 * k + 1] * inv, o[4 * k + 2] * inv,
                                  o[4 * k + 3] * inv);
           if (cg == 0 && hl == 0)
-            p.part_lse[row * p.n_split + split] = lsum > 0.f ? m_used + lg2(lsum) : kNegInf;
+            p.part_lse[row * p.n_split + split] = lsum == 0.f ? kNegInf : m_used + lg2(lsum);
         }
       }
     }

@@ -120,6 +120,9 @@ typedef struct {
  *   d_head       head dimension (128)
  *   scale        softmax scale (typically 1/sqrt(d_head))
  * Softmax and accumulation run in fp32; out is rounded to nearest-even.
+ * A NaN in a query or in a key that it sees, or a score of +inf, makes the row
+ * NaN (in every gqa_decode form); a score of -inf has weight 0, and a row with
+ * no other is zeros.
  */
 int gqa_decode(const void* q, const void* k_cache, const void* v_cache,
                const int32_t* block_table, const int32_t* seq_lens, void* out, int h_q, int h_kv,

@@ -7,13 +7,14 @@ import numpy as np
 import pytest
 import torch
 
+import gqa_mqa_mla_gb300 as da
 from oracle import step
 
-from test_step_ops_gpu import _attn_case, _close, _fp16_probs, _run_prefill
+from test_step_ops_gpu import DEV, HALF, _attn_case, _close, _fp16_probs, _run_prefill
 
 pytestmark = pytest.mark.gpu
 
-NAN = float("nan")
+NAN, INF = float("nan"), float("inf")
 
 
 def _values(x):
@@ -97,3 +98,63 @@ def test_prefill_passes_on_what_is_not_finite(case, what, fp8):
                                  num_splits=splits)
         assert flag == 0
         _agrees(out, ref, clean, dtype, f"{what}, {splits} splits")
+
+
+DECODE = [
+    # lens, h_q, h_kv, dtype, block, window, sinks
+    ([1000, 64, 500, 129], 16, 2, "bf16", 16, 900, 4),
+    ([700, 64], 8, 8, "fp16", 8, 600, 64),
+    ([900, 129], 32, 2, "fp16", 64, 800, 66),
+    ([1000, 900], 64, 1, "bf16", 16, 800, 130),
+    ([700, 300], 33, 1, "fp16", 256, 600, 3),
+]
+
+
+@pytest.mark.parametrize("what,fp8", WHAT)
+@pytest.mark.parametrize("case", range(len(DECODE)))
+def test_decode_passes_on_what_is_not_finite(case, what, fp8):
+    """With a window and sinks (one split, a cluster of them, a launch that joins
+    them), and without."""
+    lens, h_q, h_kv, dtype, bs, window, sinks = DECODE[case]
+    x = _attn_case([1] * len(lens), lens, h_q, h_kv, dtype, bs, 750 + case, fp8=fp8)
+    full = _defined(x, scale=0.09)
+    clean = _defined(x, scale=0.09, window=window, sinks=sinks)
+    _spoil(x, what)
+    if what == "k nan late":
+        assert int(x["lens"][0]) - 2 > int(x["lens"][0]) - window
+    fn = da.gqa_decode if not fp8 else da.gqa_decode_fp8kv
+    for w, n, c in ((window, sinks, clean), (0, 0, full)):
+        ref = _defined(x, scale=0.09, window=w, sinks=n)
+        if fp8:
+            ref, c = ((r[0], r[1] + 2.0**-25 * r[2] / HALF[dtype], r[2], r[3]) for r in (ref, c))
+        for splits in (1, 4, 10):
+            out = fn(x["q"], *x["caches"], *(x["scales"] or []), x["table"], x["lens"], scale=0.09,
+                     max_seq_len=x["max_len"], window=w or None, sinks=n, num_splits=splits)
+            _agrees(out, ref, c, dtype, f"{what}, window {w}, {splits} splits")
+
+
+def test_scores_of_minus_infinity_alone_see_nothing():
+    """A row all of whose scores are -inf has no weight to give: zeros, as a row
+    that sees nothing; a stretch of the cache without weight does not disturb the
+    rest (16-bit caches: e4m3 has no infinity)."""
+    for h_q, h_kv in ((8, 2), (8, 8), (64, 1)):
+        x = _attn_case([1, 1], [600, 600], h_q, h_kv, "bf16", 16, 795)
+        x["q"].abs_()
+        bs = 16
+        for b, (lo, hi) in enumerate([(0, 600), (64, 448)]):
+            t = torch.arange(lo, hi, device=DEV)
+            x["caches"][0][x["table"][b][t // bs].long(), t % bs, :, 9] = -INF
+        want = _defined(x, scale=0.09)
+        for splits in (1, 4, 10):
+            for fn in ("decode", "prefill", "sinks"):
+                if fn == "prefill":
+                    out, _ = _run_prefill(x, scale=0.09, num_splits=splits)
+                else:
+                    kw = dict(window=590, sinks=10) if fn == "sinks" else {}
+                    out = da.gqa_decode(x["q"], *x["caches"], x["table"], x["lens"], scale=0.09,
+                                        max_seq_len=600, num_splits=splits, **kw)
+                assert bool((out[0] == 0).all()), (fn, splits)
+                got, ref = out[1].double().cpu().numpy(), want[0][1]
+                # u |out| + (u + 2^-10) A, A = sum p |v| / sum p <= the spread
+                tol = 2.0**-8 * np.abs(ref) + (2.0**-8 + 2.0**-10) * want[1][1]
+                assert np.isfinite(got).all() and (np.abs(got - ref) <= tol).all(), (fn, splits)
