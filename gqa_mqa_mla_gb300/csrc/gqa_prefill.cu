@@ -357,7 +357,9 @@ __device__ __forceinline__ void split_q(const PrefillParams& p, const Item& w, i
       const uint32_t bits = __float_as_uint(m);
       const int ex = static_cast<int>((bits >> 23) & 0xffu) - 127;
       const int k2 = min(max(((bits & 0x7fffffu) <= 0x600000u ? 8 : 7) - ex, -126), 126);
-      const float alpha = __uint_as_float(static_cast<uint32_t>(k2 + 127) << 23);
+      // (An infinite value has no such terms: all of its row's become NaN.)
+      const float alpha =
+          __uint_as_float(bits == 0x7f800000u ? 0x7fc00000u : static_cast<uint32_t>(k2 + 127) << 23);
       if (c == 0) qexp[r] = static_cast<int8_t>(k2);
       uint32_t code[kTerms][2] = {};
 #pragma unroll

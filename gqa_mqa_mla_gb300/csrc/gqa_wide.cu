@@ -499,7 +499,11 @@ __global__ void __launch_bounds__(kThreads)
           const int ex = static_cast<int>((mb >> 23) & 0xffu) - 127;
           const int kexp = min(max(((mb & 0x7fffffu) <= 0x600000u ? 8 : 7) - ex, -126), 126);
           const float alpha = __uint_as_float(static_cast<uint32_t>(kexp + 127) << 23);
-          if (c16 == 0) qinv[row] = __uint_as_float(static_cast<uint32_t>(127 - kexp) << 23);
+          // (An infinite value has no such terms: its row's scores become NaN.)
+          if (c16 == 0)
+            qinv[row] = __uint_as_float(mb == 0x7f800000u
+                                            ? 0x7fc00000u
+                                            : static_cast<uint32_t>(127 - kexp) << 23);
           uint32_t code[kQTerms][2] = {};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {

@@ -158,3 +158,32 @@ def test_scores_of_minus_infinity_alone_see_nothing():
                 # u |out| + (u + 2^-10) A, A = sum p |v| / sum p <= the spread
                 tol = 2.0**-8 * np.abs(ref) + (2.0**-8 + 2.0**-10) * want[1][1]
                 assert np.isfinite(got).all() and (np.abs(got - ref) <= tol).all(), (fn, splits)
+
+
+@pytest.mark.parametrize("value", [INF, -INF])
+def test_infinite_queries_over_an_8_bit_cache(value):
+    """They have no e4m3 terms; their rows are NaN, the others what they are."""
+    for case, (q_lens, lens, h_q, h_kv, dtype, bs, window, sinks) in enumerate(CHUNKS):
+        x = _attn_case(q_lens, lens, h_q, h_kv, dtype, bs, 770 + case, fp8=True)
+        kw = dict(scale=0.09, window=window or None, sinks=sinks)
+        for splits in (1, 3):
+            good, _ = _run_prefill(x, num_splits=splits, **kw)
+            q = x["q"].clone()
+            q[q_lens[0] - 1, 1, 77], q[-1, 0, 0] = value, -value
+            out, flag = _run_prefill(dict(x, q=q), num_splits=splits, **kw)
+            bad = torch.zeros(q.shape[:2], dtype=torch.bool, device=DEV)
+            bad[q_lens[0] - 1, 1] = bad[-1, 0] = True
+            assert flag == 0 and bool(out[bad].isnan().all())
+            assert torch.equal(out[~bad], good[~bad])
+    for case, (lens, h_q, h_kv, dtype, bs, window, sinks) in enumerate(DECODE):
+        x = _attn_case([1] * len(lens), lens, h_q, h_kv, dtype, bs, 780 + case, fp8=True)
+        q = x["q"].clone()
+        q[0, 1, 77] = value
+        for kw in (dict(window=window, sinks=sinks), {}):
+            for splits in (1, 4):
+                good, out = (da.gqa_decode_fp8kv(y, *x["caches"], *x["scales"], x["table"], x["lens"],
+                                                 scale=0.09, max_seq_len=x["max_len"],
+                                                 num_splits=splits, **kw) for y in (x["q"], q))
+                assert bool(out[0, 1].isnan().all()) and torch.equal(out[1:], good[1:])
+                rest = [h for h in range(h_q) if h != 1]
+                assert torch.equal(out[0, rest], good[0, rest])
