@@ -1128,6 +1128,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         phase_o ^= 1u;
       }
       const Item w = items[k & 1];
+      // (The loop's scale is at least 1e-37 whatever K's: one that is not finite
+      // counts here, for every row that sees something.)
+      if (kF8 && l != 0.f) l += 0.f * p.k_scale[w.j];
       const int half = w.solo ? 0 : x;
       const int tok = half ? w.tok_b : w.tok_a;
       const int i0 = w.i0 + half * p.tokens_per_tile;

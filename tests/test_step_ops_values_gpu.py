@@ -187,3 +187,20 @@ def test_infinite_queries_over_an_8_bit_cache(value):
                 assert bool(out[0, 1].isnan().all()) and torch.equal(out[1:], good[1:])
                 rest = [h for h in range(h_q) if h != 1]
                 assert torch.equal(out[0, rest], good[0, rest])
+
+
+@pytest.mark.parametrize("splits", [1, 3])
+def test_scales_of_an_8_bit_cache_that_are_not_finite(splits):
+    """A head whose K or V scale is NaN gives NaN, in chunks and in decode; the
+    others what they are."""
+    for j in (0, 1):
+        x = _attn_case([40, 3], [400, 300], 6, 3, "bf16", 16, 790, fp8=True)
+        good, _ = _run_prefill(x, num_splits=splits)
+        x["scales"][j][1] = NAN
+        out, flag = _run_prefill(x, num_splits=splits)
+        assert flag == 0 and bool(out[:, 2:4].isnan().all())
+        assert torch.equal(out[:, :2], good[:, :2]) and torch.equal(out[:, 4:], good[:, 4:])
+        out = da.gqa_decode_fp8kv_sinks(x["q"][[39, 42]], *x["caches"], *x["scales"], x["table"],
+                                        x["lens"], scale=0.1, max_seq_len=400, window=300, sinks=4,
+                                        num_splits=splits)
+        assert bool(out[:, 2:4].isnan().all()) and bool(out[:, [0, 1, 4, 5]].isfinite().all())
