@@ -185,6 +185,11 @@ __device__ __forceinline__ int shorter_by(const PrefillParams& p, int n, int len
   return (n + s + tpi - 1) / tpi > (n + tpi - 1) / tpi ? 0 : s;
 }
 
+// Are sequence b's row offsets a, e = q_start[b], q_start[b + 1] those of a chunk?
+__device__ __forceinline__ bool rows_fit(const PrefillParams& p, int a, int e) {
+  return a >= 0 && e >= a && e <= p.tokens && e - a <= p.max_q_len;
+}
+
 // Walks the pieces, 32 sequences at a time (one per lane), from the last sequences
 // back.  Among the 32 the longest come first (a piece of two Q tiles counts
 // double), and within a chunk the last rows, which see most: what is left for the
@@ -203,9 +208,7 @@ __device__ __forceinline__ void load_cursor(const PrefillParams& p, Cursor& c, i
   if (b >= 0 && b < p.batch) {
     const int a = p.q_start[b], e = p.q_start[b + 1];
     c.len = p.seq_lens[b];
-    if (a < 0 || e < a || e > p.tokens || e - a > p.max_q_len) {
-      if (blockIdx.x == 0) flag_error(p.err_flag, kFlagBadSeqLen);
-    } else {
+    if (rows_fit(p, a, e)) {
       c.start = a;
       c.n = e - a;
       c.cnt = (e - a + tpi - 1) / tpi;
@@ -906,6 +909,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ---------------- softmax: thread = row r of tile x
+    // (The first CTA, which every grid starts, also looks at every sequence's row
+    // offsets while its first copies are on their way: a bad one has no piece, so no
+    // scheduler need come by it.)
+    if (blockIdx.x == 0)
+      for (int b = threadIdx.x; b < p.batch; b += 2 * kM)
+        if (!rows_fit(p, p.q_start[b], p.q_start[b + 1])) flag_error(p.err_flag, kFlagBadSeqLen);
     const int x = warp >> 2;
     const int r = 32 * (warp & 3) + lane;
     const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
@@ -1303,7 +1312,7 @@ __global__ void __launch_bounds__(256) gqa_prefill_combine_kernel(const PrefillP
     if (p.q_start[mid] <= tok) lo = mid; else hi = mid;
   }
   const int a = p.q_start[lo], e = p.q_start[lo + 1];
-  if (tok < a || tok >= e || a < 0 || e > p.tokens || e - a > p.max_q_len) return;
+  if (tok < a || tok >= e || !rows_fit(p, a, e)) return;
   const float* lse = p.part_lse + row * p.n_split;
   float mx = kNegInf;  // (the maximum of the numbers: NaN does not count)
   bool some = false;
