@@ -342,8 +342,8 @@ def gqa_decode(q, k_cache, v_cache, block_table, seq_lens, *, scale: float, max_
     """MHA/GQA/MQA decode through the C ABI; returns out [B, h_q, d].
 
     q [B, h_q, d]; k_cache/v_cache [num_blocks, block_size, h_kv, d];
-    block_table int32 [B, max_blocks]; seq_lens int32 [B]; max_seq_len a host
-    upper bound of seq_lens.  workspace: optional uint8 CUDA tensor (sized by
+    block_table int32 [B, max_blocks]; seq_lens int32 [B] (either may have more
+    entries: the first B count); max_seq_len a host upper bound of seq_lens.  workspace: optional uint8 CUDA tensor (sized by
     gqa_workspace_size); allocated here when needed and not given.  window:
     attend only to each sequence's last `window` tokens (gqa_decode_window),
     and with sinks > 0 to its first `sinks` tokens too (gqa_decode_sinks).

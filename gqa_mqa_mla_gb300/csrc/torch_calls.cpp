@@ -375,8 +375,9 @@ struct Attention {
   const float *sk = nullptr, *sv = nullptr;
   int dtype, h_q, h_kv, d, index;
   bool fp8;
-  Attention(PyObject* const* a)  // q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens
-      : fp8(!none(a[3])) {
+  // q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens.  `decode`: a row of
+  // q for each sequence, so that the table and the lengths must reach as far.
+  Attention(PyObject* const* a, bool decode) : fp8(!none(a[3])) {
     const Tensor& t = tensor(a[0], "q");
     q = &check(a[0], "q", t.scalar_type(), 3);
     dtype = dtype16(t, "q");
@@ -389,6 +390,10 @@ struct Attention {
     h_kv = size32(*kc, 2);
     if (kc->size(3) != d || vc->sizes() != kc->sizes())
       value_error(fp8 ? "k_codes / v_codes shape mismatch" : "k_cache / v_cache shape mismatch");
+    if (decode && (table->size(0) < t.size(0) || lens->size(0) < t.size(0)))
+      value_error("block_table and seq_lens need an entry for each of the " +
+                  std::to_string(t.size(0)) + " rows of q, got " + std::to_string(table->size(0)) +
+                  " and " + std::to_string(lens->size(0)));
     if (h_kv < 1 || h_q % h_kv != 0)
       value_error("h_q=" + std::to_string(h_q) + " is not a multiple of h_kv=" +
                   std::to_string(h_kv));
@@ -450,7 +455,7 @@ struct Attention {
 //   stream): out.
 PyObject* decode(PyObject* const* a, Py_ssize_t n) {
   count(n, 16);
-  const Attention x(a);
+  const Attention x(a, true);
   const float scale = static_cast<float>(as_double(a[7], "scale"));
   const int max_len = as_int(a[8], "max_seq_len"), sinks = as_int(a[10], "sinks");
   const bool windowed = !none(a[9]);
@@ -499,7 +504,7 @@ PyObject* decode(PyObject* const* a, Py_ssize_t n) {
 //   workspace, err_flag, stream): out.
 PyObject* prefill(PyObject* const* a, Py_ssize_t n) {
   count(n, 18);
-  const Attention x(a);
+  const Attention x(a, false);
   const Tensor& start = check(a[7], "q_start", ScalarType::Int, 1);
   const int B = size32(*x.lens, 0), T = size32(*x.q, 0);
   if (x.table->size(0) != B || start.size(0) != B + 1)

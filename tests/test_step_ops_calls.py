@@ -1,0 +1,26 @@
+"""How the GQA decode calls and the serving step's operators are called: what the
+binding refuses, without a GPU."""
+import pytest
+import torch
+
+import gqa_mqa_mla_gb300 as da
+
+I32 = dict(dtype=torch.int32)
+
+
+@pytest.mark.parametrize("rows,entries", [(2, 3), (3, 2), (0, 3), (3, 0)])
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("kw", [{}, dict(window=16), dict(window=16, sinks=4)])
+def test_decode_refuses_lists_that_are_too_short(rows, entries, fp8, kw):
+    """Three rows of q and a table or lengths of fewer: read past their end before."""
+    q = torch.zeros(3, 8, 128, dtype=torch.bfloat16)
+    cache = torch.zeros(4, 16, 2, 128, dtype=torch.uint8 if fp8 else torch.bfloat16)
+    scales = [torch.ones(2)] * 2 if fp8 else []
+    fn = da.gqa_decode_fp8kv if fp8 else da.gqa_decode
+    with pytest.raises(ValueError, match="an entry for each of the 3 rows"):
+        fn(q, cache, cache, *scales, torch.zeros(rows, 4, **I32), torch.zeros(entries, **I32),
+           scale=0.1, max_seq_len=64, **kw)
+    # as many or more: the next check, of the device
+    with pytest.raises(ValueError, match="CUDA"):
+        fn(q, cache, cache, *scales, torch.zeros(3, 4, **I32), torch.zeros(5, **I32), scale=0.1,
+           max_seq_len=64, **kw)
