@@ -671,6 +671,8 @@ def mla_decode(q_absorbed, q_rope, latent_cache, block_table, seq_lens, *, scale
     nb, bs, width = latent_cache.shape
     if width != MLA_D_C + MLA_D_R:
         raise ValueError("latent_cache must be [num_blocks, block_size, 576]")
+    if block_table.shape[0] < B or seq_lens.shape[0] < B:
+        raise ValueError(f"block_table and seq_lens need an entry for each of the {B} rows of q")
     if out is None:
         out = torch.empty_like(q_absorbed)
     ns = num_splits if num_splits else mla_plan_splits(B, max_seq_len)

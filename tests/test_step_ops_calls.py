@@ -24,3 +24,12 @@ def test_decode_refuses_lists_that_are_too_short(rows, entries, fp8, kw):
     with pytest.raises(ValueError, match="CUDA"):
         fn(q, cache, cache, *scales, torch.zeros(3, 4, **I32), torch.zeros(5, **I32), scale=0.1,
            max_seq_len=64, **kw)
+
+
+@pytest.mark.parametrize("rows,entries", [(2, 3), (3, 2)])
+def test_mla_decode_refuses_lists_that_are_too_short(rows, entries):
+    bf16 = dict(dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="an entry for each of the 3 rows"):
+        da.mla_decode(torch.zeros(3, 128, 512, **bf16), torch.zeros(3, 128, 64, **bf16),
+                      torch.zeros(4, 16, 576, **bf16), torch.zeros(rows, 4, **I32),
+                      torch.zeros(entries, **I32), scale=0.1, max_seq_len=64)
