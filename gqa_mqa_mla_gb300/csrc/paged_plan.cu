@@ -210,10 +210,15 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(const PlanParams p
 template <int kThreads>
 cudaError_t launch_t(const PlanParams& p, cudaStream_t stream) {
   auto kern = paged_plan_kernel<kThreads>;
-  const int smem = (5 * p.batch + 3) * static_cast<int>(sizeof(int));
+  auto bytes = [](int batch) { return (5 * batch + 3) * static_cast<int>(sizeof(int)); };
+  const int smem = bytes(p.batch);
   cudaError_t e = cudaSuccess;
-  if (smem > 48 * 1024)
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // The default limit of 48 KB is for static (under 1 KB) and dynamic shared memory
+  // together.  What is asked for is always the largest batch's, so that a call of one
+  // thread never lowers the limit that another has set for its launch.
+  if (smem > 47 * 1024)
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             bytes(kPlanMaxBatch));
   if (e != cudaSuccess) return e;
   // A token a thread, up to a CTA on every other SM (more only repeat the
   // scan); a cluster's CTAs where the step is updated in place.

@@ -1,10 +1,17 @@
 """How the serving step's operators are called, on the GPU."""
+import os
+import subprocess
+import sys
+import threading
+
+import numpy as np
 import pytest
 import torch
 
 import gqa_mqa_mla_gb300 as da
+from oracle import step
 
-from test_step_ops_gpu import _attn_case, _i32, _run_prefill
+from test_step_ops_gpu import _attn_case, _i32, _plan_case, _run_plan, _run_prefill, _same_plan
 
 pytestmark = pytest.mark.gpu
 
@@ -32,3 +39,51 @@ def test_prefill_flags_bad_offsets_of_any_sequence(batch, at, rows, fp8):
         bad[at + 1] = bad[at] - 1
         _, flag = _run_prefill(dict(x, start=_i32(bad)), num_splits=splits)
         assert flag == da.FLAG_BAD_SEQ_LEN
+
+
+# ------------------------------------------------------------------ the plan
+
+
+def _plan_once(B):
+    rng = np.random.default_rng(B)
+    case = _plan_case(rng, B, 16, 4, -20, 40, 4 * B)
+    want = step.paged_plan(*case, block_size=16, max_tokens=20 * B)
+    _same_plan(_run_plan(*case, 16, 20 * B), want)
+
+
+@pytest.mark.parametrize("B", [2416, 2417, 2418, 2440, 2457, 2458, 8192])
+def test_plan_batches_around_the_default_shared_memory(B):
+    _plan_once(B)
+
+
+@pytest.mark.parametrize("B", [2418, 2457, 8192])
+def test_plan_as_the_first_call_of_a_process(B):
+    here = os.path.dirname(os.path.abspath(__file__))
+    code = (f"import sys; sys.path[:0] = [{here!r}, {os.path.dirname(here)!r}]\n"
+            f"import test_step_ops_calls_gpu as t; t._plan_once({B})")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_plans_of_different_sizes_from_two_threads():
+    """The launches' shared memory does not depend on what another thread plans."""
+    failed = []
+
+    def work(B, n):
+        try:
+            rng = np.random.default_rng(B)
+            cached, new, table, free, count = _plan_case(rng, B, 16, 4, -20, 40, 4 * B)
+            t, f, c = _i32(table), _i32(free), _i32([count])
+            args = (_i32(cached), _i32(new))
+            for _ in range(n):
+                da.paged_plan(*args, t.clone(), f.clone(), c, block_size=16, max_tokens=16)
+            torch.cuda.synchronize()
+        except Exception as e:  # noqa: BLE001
+            failed.append((B, e))
+
+    threads = [threading.Thread(target=work, args=(B, 400)) for B in (2600, 8192, 3000, 100)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
