@@ -967,22 +967,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                                      w.solo ? 8 * x + 8 : 16, inv_g,
                                      smem + half * kTerms * kCodeBytes, qexp + half * kM);
             fence_proxy_async_smem();
+            // The row's exponent is read before this thread has arrived: behind it the
+            // other tile's warps may, with this piece done (a single K / V tile: its
+            // scores need no more of this warp), write the next piece's.
+            __syncwarp();
+            int ex = w.solo || r >= tok * G ? 0 : qexp[half * kM + r];
             mbar_arrive(bar(kBarQ));
-            // (Solo: some of a warp's row exponents come from another warp.)
+            // (Solo: some of a warp's row exponents come from another warp, which
+            // writes no others before the two have met at this piece's end.)
             if (w.solo) {
               ok = mbar_wait_or_abort(bar(kBarQ), q_made & 1, p.err_flag, abort_word);
               ok = __all_sync(0xffffffffu, ok);
               if (!ok) break;
+              if (r < tok * G) ex = qexp[r];
             }
-            __syncwarp();
             ++q_made;
             // K's scale multiplies every score of KV head j, and the row carries
             // 2^(its exponent).
             const float ks = p.k_scale[w.j];
             negate ^= ks < 0.f;
             scale *= fabsf(ks);
-            scale = fmaxf(
-                scale * __uint_as_float((127 - (r < tok * G ? qexp[half * kM + r] : 0)) << 23), 1e-37f);
+            scale = fmaxf(scale * __uint_as_float((127 - ex) << 23), 1e-37f);
           }
         }
         if (negate) plain_hi = plain_lo;  // (every tile changes its scores' sign)

@@ -11,7 +11,8 @@ import torch
 import gqa_mqa_mla_gb300 as da
 from oracle import step
 
-from test_step_ops_gpu import _attn_case, _i32, _plan_case, _run_plan, _run_prefill, _same_plan
+from test_step_ops_gpu import (DEV, _attn_case, _close, _fp16_probs, _gen, _i32, _plain_prefill,
+                               _plan_case, _run_plan, _run_prefill, _same_plan)
 
 pytestmark = pytest.mark.gpu
 
@@ -87,3 +88,32 @@ def test_plans_of_different_sizes_from_two_threads():
     for t in threads:
         t.join()
     assert not failed
+
+
+# ------------------------------------------------------------------ 8-bit cache
+
+
+def test_pieces_of_two_tiles_and_of_one_in_turn_over_an_8_bit_cache():
+    """CTAs that go from a piece with two Q tiles and a single K / V tile to one with
+    one Q tile and several: each row keeps the exponent of its own query (the rows'
+    sizes differ by up to 2^12)."""
+    rng = np.random.default_rng(30)
+    q_lens, lens = [], []
+    for _ in range(160):
+        q_lens += [32, int(rng.integers(1, 16))]
+        lens += [int(rng.integers(32, 128)), int(rng.integers(260, 500))]
+    for dtype in ("bf16", "fp16"):
+        x = _attn_case(q_lens, lens, 16, 2, dtype, 16, 830, fp8=True)
+        size = 2.0 ** torch.randint(-8, 5, (x["q"].shape[0], 16, 1), generator=_gen(3), device=DEV)
+        x["q"] = (x["q"].float() * size / 4).to(x["q"].dtype)
+        out, flag = _run_prefill(x, num_splits=1)
+        assert flag == 0
+        for _ in range(5):
+            again, _ = _run_prefill(x, num_splits=1)
+            assert torch.equal(again, out)
+        start = np.concatenate([[0], np.cumsum(q_lens)])
+        for b in range(0, 320, 41):
+            rows = slice(int(start[b]), int(start[b + 1]))
+            y = dict(x, q=x["q"][rows], table=x["table"][b: b + 1], start=_i32([0, q_lens[b]]),
+                     lens=x["lens"][b: b + 1])
+            _close(out[rows], _fp16_probs(_plain_prefill(y), dtype), dtype, b)
