@@ -171,6 +171,8 @@ def lib() -> ctypes.CDLL:
             L.decattn_status_string.restype = ctypes.c_char_p
             L.decattn_selftest_wait_timeout.argtypes = [P, P, I, P]
             L.decattn_selftest_wait_timeout.restype = I
+            L.decattn_selftest_warp_wait.argtypes = [P, P, I, P]
+            L.decattn_selftest_warp_wait.restype = I
             L.decattn_version.argtypes = []
             L.decattn_version.restype = I
             _lib = L
@@ -201,6 +203,18 @@ def calls():
 
 def _decode_name(name: str, window, sinks: int) -> str:
     return name if window is None else name + ("_sinks" if sinks else "_window")
+
+
+def selftest_warp_wait(limit_us: int = 1000, device="cuda"):
+    """Run the self test of a warp's waits; returns (err_flag, result list of 4 ints)."""
+    flag = torch.zeros(1, dtype=torch.int32, device=device)
+    res = torch.full((4,), -1, dtype=torch.int32, device=device)
+    st = lib().decattn_selftest_warp_wait(flag.data_ptr(), res.data_ptr(), int(limit_us),
+                                          _stream_handle(None))
+    if st != DECATTN_OK:
+        raise DecAttnError("decattn_selftest_warp_wait", st)
+    torch.cuda.synchronize()
+    return int(flag.item()), res.tolist()
 
 
 def selftest_wait_timeout(limit_us: int = 1000, device="cuda"):

@@ -831,7 +831,7 @@ DECATTN_DEV void gqa_partial(const CUtensorMap& tm_k, const CUtensorMap& tm_v,
   bool ok = true;
   for (int it = 0; it < n_tiles; ++it) {
     const int s = it % kStages;
-    if (!mbar_wait(full0 + 8 * s, (it / kStages) & 1, p.err_flag)) {
+    if (!mbar_wait_warp(full0 + 8 * s, (it / kStages) & 1, p.err_flag)) {
       ok = false;
       break;
     }
@@ -846,14 +846,14 @@ DECATTN_DEV void gqa_partial(const CUtensorMap& tm_k, const CUtensorMap& tm_v,
   // free once every warp has passed the last tile).
   __syncwarp();
   if (lane == 0) mbar_arrive(done_bar);
-  if (!ok || !mbar_wait(done_bar, 0, p.err_flag)) return;
+  if (!ok || !mbar_wait_warp(done_bar, 0, p.err_flag)) return;
   float* mo = reinterpret_cast<float*>(smem);
   float* mm = mo + kW * Consumer::kRowsPerWarp * kHeadDim;
   float* ml = mm + kW * Consumer::kRowsPerWarp;
   c.finish(mo, mm, ml, lane);
   __syncwarp();
   if (lane == 0) mbar_arrive(merge_bar);
-  if (!mbar_wait(merge_bar, 0, p.err_flag)) return;
+  if (!mbar_wait_warp(merge_bar, 0, p.err_flag)) return;
 
   const int tid = threadIdx.x - 32;
   for (int e = tid; e < G * kHeadDim; e += kW * 32) {

@@ -471,9 +471,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // The k-th piece, as every role sees it (all lanes of its warp); released
   // once the role is done with it.
   auto get_item = [&](int k, Item& w) -> bool {
-    const bool there =
-        mbar_wait_or_abort(bar(kBarItem + (k & 1)), (k >> 1) & 1, p.err_flag, abort_word);
-    if (!__all_sync(0xffffffffu, there)) return false;
+    if (!mbar_wait_or_abort_warp(bar(kBarItem + (k & 1)), (k >> 1) & 1, p.err_flag, abort_word))
+      return false;
     w = items[k & 1];
     return w.valid != 0;
   };
@@ -516,8 +515,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           clc_try_cancel(sbase + kOffAnswer, bar(kBarNext));
         }
         __syncwarp();
-        const bool there = mbar_wait_or_abort(bar(kBarNext), asks++ & 1, p.err_flag, abort_word);
-        if (!__all_sync(0xffffffffu, there)) return false;
+        if (!mbar_wait_or_abort_warp(bar(kBarNext), asks++ & 1, p.err_flag, abort_word))
+          return false;
         x = clc_answer(sbase + kOffAnswer);
         fence_proxy_async_smem();  // the answer is read before the next one is asked for
         return true;
@@ -958,8 +957,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (max(w.n_a, w.n_b) > 0) {
             // Q as e4m3 terms, once the last S of the piece before has read it.
             int8_t* qexp = reinterpret_cast<int8_t*>(smem + kOffQExp);
-            ok = mbar_wait_or_abort(bar(kBarQFree), (q_made & 1) ^ 1, p.err_flag, abort_word);
-            ok = __all_sync(0xffffffffu, ok);
+            ok = mbar_wait_or_abort_warp(bar(kBarQFree), (q_made & 1) ^ 1, p.err_flag, abort_word);
             if (!ok) break;
             // (Solo: tile A's rows, half of them each.)
             if (w.solo || x == 0 || w.tok_b > 0)
@@ -976,8 +974,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // (Solo: some of a warp's row exponents come from another warp, which
             // writes no others before the two have met at this piece's end.)
             if (w.solo) {
-              ok = mbar_wait_or_abort(bar(kBarQ), q_made & 1, p.err_flag, abort_word);
-              ok = __all_sync(0xffffffffu, ok);
+              ok = mbar_wait_or_abort_warp(bar(kBarQ), q_made & 1, p.err_flag, abort_word);
               if (!ok) break;
               if (r < tok * G) ex = qexp[r];
             }
@@ -999,7 +996,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (idle) {
         // No row of this warp is real: its P may be anything.
         for (; ok && o < end; o += o + step == gap0 ? step + gap1 - gap0 : step) {
-          ok = mbar_wait_or_abort(bar(kBarS + x), phase_s, p.err_flag, abort_word);
+          ok = mbar_wait_or_abort_warp(bar(kBarS + x), phase_s, p.err_flag, abort_word);
           phase_s ^= 1u;
           if (ok) {
             mbar_arrive(bar(kBarP + x));
@@ -1008,7 +1005,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       for (const int o0 = o; o < end; o += o + step == gap0 ? step + gap1 - gap0 : step) {
-        if (!mbar_wait_or_abort(bar(kBarS + x), phase_s, p.err_flag, abort_word)) {
+        if (!mbar_wait_or_abort_warp(bar(kBarS + x), phase_s, p.err_flag, abort_word)) {
           ok = false;
           break;
         }
@@ -1138,7 +1135,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // ---------------- epilogue
       if (ok && nt > 0) {
-        ok = mbar_wait_or_abort(bar(kBarO + x), phase_o, p.err_flag, abort_word);
+        ok = mbar_wait_or_abort_warp(bar(kBarO + x), phase_o, p.err_flag, abort_word);
         phase_o ^= 1u;
       }
       const Item w = items[k & 1];
@@ -1194,7 +1191,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t at = bar(kBarPair + (warp & 3));
           tc_fence_before();
           mbar_arrive(at);
-          ok = __all_sync(0xffffffffu, mbar_wait_or_abort(at, phase_pair, p.err_flag, abort_word));
+          ok = mbar_wait_or_abort_warp(at, phase_pair, p.err_flag, abort_word);
           phase_pair ^= 1u;
           tc_fence_after();
         };

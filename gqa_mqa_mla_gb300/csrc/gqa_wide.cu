@@ -543,7 +543,8 @@ __global__ void __launch_bounds__(kThreads)
       const GqaTile tl = span.tile(it);
       const int nval = tl.nval, nskip = tl.skip;
       const bool ragged = nval < kTile || nskip > 0;
-      if (!mbar_wait_or_abort(bar(kBarSFull + (it & 1)), (it >> 1) & 1, p.err_flag, abort_word)) {
+      if (!mbar_wait_or_abort_warp(bar(kBarSFull + (it & 1)), (it >> 1) & 1, p.err_flag,
+                                   abort_word)) {
         ok = false;
         break;
       }
@@ -584,8 +585,8 @@ __global__ void __launch_bounds__(kThreads)
         const float factor = need ? ex2(m_used - m_new) : 1.f;  // 0 from the lowest value
         if (it > 0) {
           // O += P(it - 1) V(it - 1) must have completed before O is rescaled.
-          if (!mbar_wait_or_abort(bar(kBarPvDone + ((it - 1) & 1)), ((it - 1) >> 1) & 1,
-                                  p.err_flag, abort_word)) {
+          if (!mbar_wait_or_abort_warp(bar(kBarPvDone + ((it - 1) & 1)), ((it - 1) >> 1) & 1,
+                                       p.err_flag, abort_word)) {
             ok = false;
             break;
           }
@@ -629,8 +630,8 @@ __global__ void __launch_bounds__(kThreads)
       // read by O += P(it - 2) V(it - 2).
       {
         const int last = it - L::kPBuffers;
-        if (last >= 0 && !mbar_wait_or_abort(bar(kBarPvDone + (last & 1)), (last >> 1) & 1,
-                                             p.err_flag, abort_word)) {
+        if (last >= 0 && !mbar_wait_or_abort_warp(bar(kBarPvDone + (last & 1)), (last >> 1) & 1,
+                                                  p.err_flag, abort_word)) {
           ok = false;
           break;
         }
@@ -639,7 +640,8 @@ __global__ void __launch_bounds__(kThreads)
         // V(it) into f16 slab it % 2 (its last reader, O += P(it - 2) V(it - 2),
         // has completed: the wait above), then its 8-bit stage is free again.
         const int s8 = it % kRing;
-        if (!mbar_wait_or_abort(bar(kBarFullV + s8), (it / kRing) & 1, p.err_flag, abort_word)) {
+        if (!mbar_wait_or_abort_warp(bar(kBarFullV + s8), (it / kRing) & 1, p.err_flag,
+                                     abort_word)) {
           ok = false;
           break;
         }
@@ -661,7 +663,8 @@ __global__ void __launch_bounds__(kThreads)
         // V rows outside [nskip, nval) may hold anything (even NaN): zero
         // them once the tile has landed, so that P = 0 there contributes
         // exactly nothing.  O += P(it) V(it) reads them after P(it) is published.
-        if (!mbar_wait_or_abort(bar(kBarFullV + s), (it / kStages) & 1, p.err_flag, abort_word)) {
+        if (!mbar_wait_or_abort_warp(bar(kBarFullV + s), (it / kStages) & 1, p.err_flag,
+                                     abort_word)) {
           ok = false;
           break;
         }
@@ -680,13 +683,13 @@ __global__ void __launch_bounds__(kThreads)
     }
 
     // ---------------- epilogue: O / l (one split) or the fp32 partial
-    if (ok) ok = mbar_wait_or_abort(bar(kBarPvDone + ((n - 1) & 1)), ((n - 1) >> 1) & 1, p.err_flag,
-                                    abort_word);
+    if (ok) ok = mbar_wait_or_abort_warp(bar(kBarPvDone + ((n - 1) & 1)), ((n - 1) >> 1) & 1,
+                                         p.err_flag, abort_word);
     if (ok) {
       l += __shfl_xor_sync(0xffffffffu, l, 16);  // both column halves of this group
       if (lane < 16) red[cg * kM + r] = l;
       mbar_arrive(bar(kBarSum));
-      ok = mbar_wait_or_abort(bar(kBarSum), 0, p.err_flag, abort_word);
+      ok = mbar_wait_or_abort_warp(bar(kBarSum), 0, p.err_flag, abort_word);
     }
     if (ok) {
       tc_fence_after();

@@ -218,6 +218,8 @@ cudaError_t launch_rope_append(const RopeParams& p, bool e4m3, bool bf16, cudaSt
 cudaError_t launch_mla_combine(const MlaCombineParams& p, bool bf16, cudaStream_t stream);
 
 // Bounded-wait self test (csrc/selftest.cu).
+cudaError_t launch_warp_wait_selftest(int* err_flag, int* result, uint64_t limit_ns,
+                                      cudaStream_t stream);
 cudaError_t launch_wait_selftest(int* err_flag, int* result, uint64_t limit_ns,
                                  cudaStream_t stream);
 

@@ -155,6 +155,23 @@ DECATTN_DEV bool mbar_wait_or_abort(uint32_t bar, uint32_t parity, int* err_flag
   return mbar_wait_or_abort_slow(bar, parity, err_flag, abort, cluster_scope, limit_ns);
 }
 
+// A warp's waits (all 32 lanes call them): each lane gets the same answer.  Lanes
+// that gave up on their own would leave the others waiting for them in the warp's
+// next collective (a shuffle, an aligned tcgen05 load).
+DECATTN_DEV bool mbar_wait_warp(uint32_t bar, uint32_t parity, int* err_flag,
+                                uint64_t limit_ns = kWaitTimeoutNs) {
+  const bool there = mbar_try_wait(bar, parity);
+  if (__all_sync(0xffffffffu, there)) return true;
+  return __all_sync(0xffffffffu, there || mbar_wait(bar, parity, err_flag, limit_ns));
+}
+DECATTN_DEV bool mbar_wait_or_abort_warp(uint32_t bar, uint32_t parity, int* err_flag,
+                                         volatile int* abort, uint64_t limit_ns = kWaitTimeoutNs) {
+  const bool there = mbar_try_wait(bar, parity);
+  if (__all_sync(0xffffffffu, there)) return true;
+  return __all_sync(0xffffffffu, there || mbar_wait_or_abort_slow(bar, parity, err_flag, abort,
+                                                                  false, limit_ns));
+}
+
 DECATTN_DEV bool mbar_wait_cluster(uint32_t bar, uint32_t parity, int* err_flag) {
   if (mbar_try_wait_cluster(bar, parity)) return true;
   const uint64_t t0 = global_timer_ns();

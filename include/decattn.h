@@ -529,6 +529,14 @@ const char* decattn_status_string(int status);
  * cudaStream_t or NULL. */
 int decattn_selftest_wait_timeout(int* err_flag, int* result, int limit_us, void* stream);
 
+/* decattn_selftest_warp_wait -- the same for a warp's waits, which must give all
+ * of its lanes one answer.  Half of a warp's lanes wait on a barrier that nothing
+ * completes, the others on a complete one.  result[0], result[1] = the lanes that
+ * were told that the wait succeeded (without and with an abort word: 0),
+ * result[2], result[3] = the same where all wait on the complete one (32);
+ * result holds 4 ints, the other arguments as above. */
+int decattn_selftest_warp_wait(int* err_flag, int* result, int limit_us, void* stream);
+
 /* Library version as major*10000 + minor*100 + patch. */
 int decattn_version(void);
 

@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import gqa_mqa_mla_gb300 as da
+from gqa_mqa_mla_gb300 import binding
 
 I32 = dict(dtype=torch.int32)
 
@@ -33,3 +34,9 @@ def test_mla_decode_refuses_lists_that_are_too_short(rows, entries):
         da.mla_decode(torch.zeros(3, 128, 512, **bf16), torch.zeros(3, 128, 64, **bf16),
                       torch.zeros(4, 16, 576, **bf16), torch.zeros(rows, 4, **I32),
                       torch.zeros(entries, **I32), scale=0.1, max_seq_len=64)
+
+
+@pytest.mark.parametrize("args", [(None, 16, 10), (16, None, 10), (18, 16, 10), (16, 17, 10),
+                                  (16, 16, 0), (16, 16, 100001)])
+def test_warp_wait_selftest_argument_checks(args):
+    assert binding.lib().decattn_selftest_warp_wait(*args, None) == binding.DECATTN_ERR_INVALID_ARG

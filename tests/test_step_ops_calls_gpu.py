@@ -9,6 +9,7 @@ import pytest
 import torch
 
 import gqa_mqa_mla_gb300 as da
+from gqa_mqa_mla_gb300 import binding
 from oracle import step
 
 from test_step_ops_gpu import (DEV, _attn_case, _close, _fp16_probs, _gen, _i32, _plain_prefill,
@@ -117,3 +118,13 @@ def test_pieces_of_two_tiles_and_of_one_in_turn_over_an_8_bit_cache():
             y = dict(x, q=x["q"][rows], table=x["table"][b: b + 1], start=_i32([0, q_lens[b]]),
                      lens=x["lens"][b: b + 1])
             _close(out[rows], _fp16_probs(_plain_prefill(y), dtype), dtype, b)
+
+
+# ------------------------------------------------------------------ waits
+
+
+@pytest.mark.parametrize("limit_us", [200, 2000])
+def test_a_wait_that_runs_out_for_some_lanes_does_for_the_warp(limit_us):
+    """Else the others would wait for them in the warp's next collective."""
+    flag, lanes = binding.selftest_warp_wait(limit_us)
+    assert flag == da.FLAG_TIMEOUT and lanes == [0, 0, 32, 32]
