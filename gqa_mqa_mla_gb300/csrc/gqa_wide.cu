@@ -52,7 +52,7 @@
 // stage, as it lands, is the B operand of S = Q K^T on kind::f8f6f4, whose A
 // operand is Q split into e4m3 terms (two for a bf16 query, three for fp16,
 // each row scaled by a power of two that the softmax undoes: exact except
-// for parts below 2^-18 of the row's largest element); the
+// for parts of at most 2^-10 / 224 of the row's largest element); the
 // softmax threads convert each landed V tile into one of two 16-bit slabs
 // (e4m3 -> f16 is exact) before they publish P(j), the slab being the B
 // operand of O += P V on f16; and the rings hold two 8 KB stages.  A
@@ -480,8 +480,9 @@ __global__ void __launch_bounds__(kThreads)
           // residual is a multiple of the query's own last bit no larger than
           // half of the previous term's, so two terms hold a bf16 query (8
           // significant bits) and three an fp16 one (11) exactly, except for
-          // parts below 2^-10 (e4m3's subnormal step) of the scaled row; the
-          // score row is scaled back by 1 / alpha_r.
+          // parts up to 2^-10 (half of e4m3's smallest step) of the scaled row,
+          // whose largest value is above 224; the score row is scaled back by
+          // 1 / alpha_r.
           float x[8];
           const uint32_t wv[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll

@@ -177,8 +177,8 @@ int gqa_decode_noalloc(const void* q, const void* k_cache, const void* v_cache,
  * convert exactly; q is rounded to fp16).  From 17 on, the scores take the
  * e4m3 codes as they are against q written as a sum of e4m3 terms (two for
  * bf16, three for fp16, each row scaled by a power of two; exact except for
- * parts below 2^-18 of the row's largest element), and P.V takes fp16
- * operands.
+ * parts of at most 2^-10 / 224, under 2^-17, of the row's largest element), and
+ * P.V takes fp16 operands.
  */
 int gqa_decode_fp8kv(const void* q, const void* k_cache, const void* v_cache,
                      const float* k_scale, const float* v_scale, const int32_t* block_table,
@@ -421,7 +421,8 @@ int gqa_rope_append_fp8kv(const void* q, const void* k_new, const void* v_new, i
  * in fp32, the probabilities rounded to the 16-bit type for the second
  * product (fp16 over an 8-bit cache).  An 8-bit cache's codes are multiplied as
  * they are: each query row is split into e4m3 terms, two for bf16 and three for
- * fp16, whose sum is the row but for parts below 2^-18 of its largest value.
+ * fp16, whose sum is the row but for parts of at most 2^-10 / 224, under 2^-17, of
+ * its largest value.
  * Values that only some rows of a chunk see must be finite: a
  * NaN or infinity in v at position t may reach the rows before t that share
  * its tile (slots past seq_lens and slots that no row of the tile's sequence

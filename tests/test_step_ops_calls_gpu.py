@@ -12,8 +12,8 @@ import gqa_mqa_mla_gb300 as da
 from gqa_mqa_mla_gb300 import binding
 from oracle import step
 
-from test_step_ops_gpu import (DEV, _attn_case, _close, _fp16_probs, _gen, _i32, _plain_prefill,
-                               _plan_case, _run_plan, _run_prefill, _same_plan)
+from test_step_ops_gpu import (DEV, HALF, TYPES, _attn_case, _close, _fp16_probs, _gen, _i32,
+                               _plain_prefill, _plan_case, _run_plan, _run_prefill, _same_plan)
 
 pytestmark = pytest.mark.gpu
 
@@ -118,6 +118,38 @@ def test_pieces_of_two_tiles_and_of_one_in_turn_over_an_8_bit_cache():
             y = dict(x, q=x["q"][rows], table=x["table"][b: b + 1], start=_i32([0, q_lens[b]]),
                      lens=x["lens"][b: b + 1])
             _close(out[rows], _fp16_probs(_plain_prefill(y), dtype), dtype, b)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("wide", [False, True])
+def test_what_the_terms_of_a_query_lose(wide, dtype):
+    """A row whose largest value is just above 1.75 * 2^k and whose others lie on half
+    of the terms' smallest step loses as much as a row can: each value is off by at
+    most 2^-10 / 224 (2^-17.8) of the largest.  Two tokens, V = 1 and 0: the output is
+    the first one's weight, 1 / (1 + e^-s), so its score s can be read off."""
+    big = 1.7578125  # a value of both types; scaled by 2^7 to 225, the other values to 2^-10
+    small = 2.0**-17
+    h_q = 33 if wide else 2
+    q = torch.full((1, h_q, 128), small, dtype=TYPES[dtype], device=DEV)
+    q[:, :, 0] = big
+    k = torch.zeros((1, 16, 1, 128), device=DEV)
+    k[0, 0, 0, 1:] = 448.0
+    v = torch.zeros((1, 16, 1, 128), device=DEV)
+    v[0, 0] = 1.0
+    codes = [c.to(torch.float8_e4m3fn).view(torch.uint8) for c in (k, v)]
+    one = torch.ones(1, device=DEV)
+    if wide:
+        out = da.gqa_decode_fp8kv(q, *codes, one, one, _i32([[0]]), _i32([2]), scale=1.0,
+                                  max_seq_len=2)
+    else:
+        out = da.gqa_prefill_fp8kv(q, *codes, one, one, _i32([[0]]), _i32([0, 1]), _i32([2]),
+                                   scale=1.0, max_q_len=1, max_seq_len=2)
+    got = out.double().cpu().numpy()
+    score = 127 * small * 448
+    bound = 2.0**-10 / 224 * big * 127 * 448
+    lo, hi = (1 / (1 + np.exp(-(score + e))) for e in (-bound, bound))
+    u = HALF[dtype]  # the output's rounding; the probabilities' (fp16), exp2 and the sums: 2^-10
+    assert (got >= lo * (1 - u - 2.0**-10)).all() and (got <= hi * (1 + u + 2.0**-10)).all()
 
 
 # ------------------------------------------------------------------ waits
