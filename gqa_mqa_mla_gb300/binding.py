@@ -6,6 +6,12 @@ stream.  The GQA decode calls and the serving step's operators are marshalled
 natively (csrc/torch_calls.cpp: checks, allocations, stream and call in one
 step, for the latency of small calls); the others through ctypes.  If a shared
 library is missing the calls raise; there is no fallback implementation.
+
+Every call runs on the current stream of the tensors' device, or on `stream`
+where it is given (a torch.cuda.Stream or a handle): inputs must then be ready on
+that stream.  What such a call allocates and returns (the GQA decode forms, the
+step operators) may be used on the current stream too, once that has waited for
+`stream`, and dropped at any time.
 """
 from __future__ import annotations
 

@@ -14,6 +14,7 @@
 #include <string>
 
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -160,16 +161,27 @@ void* stream_of(PyObject* o, int index) {
 }
 
 // A call on a given stream allocates on it, as one made under that stream would:
-// what it frees on its return (a workspace) is not handed to work on another.
+// what it frees on its return (a workspace) is not handed to work on another.  What
+// it returns is recorded as used on the caller's stream too, so that the caller may
+// use it there (having waited for the call's) and drop it.
 class OnStream {
   c10::cuda::CUDAGuard device_;
+  c10::cuda::CUDAStream caller_;
   std::optional<c10::cuda::CUDAStreamGuard> stream_;
 
  public:
-  OnStream(int index, bool given, void* stream) : device_(static_cast<c10::DeviceIndex>(index)) {
-    if (given)
+  OnStream(int index, bool given, void* stream)
+      : device_(static_cast<c10::DeviceIndex>(index)),
+        caller_(c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(index))) {
+    if (given && caller_.stream() != static_cast<cudaStream_t>(stream))
       stream_.emplace(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(stream),
                                                        static_cast<c10::DeviceIndex>(index)));
+  }
+  Tensor result(c10::IntArrayRef sizes, const c10::TensorOptions& options) const {
+    Tensor t = at::empty(sizes, options);
+    if (stream_)
+      c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), caller_);
+    return t;
   }
 };
 
@@ -260,7 +272,7 @@ PyObject* paged_plan(PyObject* const* a, Py_ssize_t n) {
     for (int k = 0; k < 5; ++k)
       if (!out[k].defined()) total += (sizes[k] + 63) / 64 * 64;
     if (total) {
-      const Tensor slab = at::empty({total}, cached.options());
+      const Tensor slab = guard.result({total}, cached.options());
       int64_t at = 0;
       for (int k = 0; k < 5; ++k) {
         if (out[k].defined()) continue;
@@ -360,7 +372,7 @@ PyObject* rope_append(PyObject* const* a, Py_ssize_t n) {
   const int st = [&] {
     const Unlocked unlocked;
     const OnStream guard(index, given, L.stream);
-    if (!out.defined()) out = at::empty({T, h_q, d}, q.options());
+    if (!out.defined()) out = guard.result({T, h_q, d}, q.options());
     return fp8 ? lib.gqa_rope_append_fp8kv(qp, kp, vp, qs, ks, vs, sk, sv, pp, rope, sp,
                                            out.data_ptr(), kcp, vcp, T, h_q, h_kv, d, &L)
                : lib.gqa_rope_append(qp, kp, vp, qs, ks, vs, pp, rope, sp, out.data_ptr(), kcp,
@@ -438,8 +450,9 @@ struct Attention {
     return t;
   }
   // What was not given is allocated: the output, `need` bytes of workspace.
-  void* allocate(Tensor& out, Tensor& ws, size_t need, decattn_launch& L) const {
-    if (!out.defined()) out = at::empty(q->sizes(), q->options());
+  void* allocate(const OnStream& guard, Tensor& out, Tensor& ws, size_t need,
+                 decattn_launch& L) const {
+    if (!out.defined()) out = guard.result(q->sizes(), q->options());
     if (!ws.defined() && need)
       ws = at::empty({static_cast<int64_t>(need)}, q->options().dtype(ScalarType::Byte));
     if (ws.defined()) {
@@ -480,7 +493,7 @@ PyObject* decode(PyObject* const* a, Py_ssize_t n) {
       L.num_splits = ns;
     }
     const int ns = L.num_splits;
-    void* o = x.allocate(out, ws,
+    void* o = x.allocate(guard, out, ws,
                          ns > 1 ? lib.gqa_decode_workspace_size(B, x.h_q, x.d, ns) : 0, L);
     if (!windowed)
       return x.fp8 ? lib.gqa_decode_fp8kv(q, kc, vc, x.sk, x.sv, bt, sl, o, x.h_q, x.h_kv, x.d,
@@ -531,7 +544,7 @@ PyObject* prefill(PyObject* const* a, Py_ssize_t n) {
     }
     const int ns = L.num_splits;
     void* o = x.allocate(
-        out, ws, T && ns > 1 ? lib.gqa_prefill_workspace_size(T, x.h_q, x.d, ns) : 0, L);
+        guard, out, ws, T && ns > 1 ? lib.gqa_prefill_workspace_size(T, x.h_q, x.d, ns) : 0, L);
     return x.fp8 ? lib.gqa_prefill_fp8kv(q, kc, vc, x.sk, x.sv, bt, qs, sl, o, T, max_q, x.h_q,
                                          x.h_kv, x.d, scale, window, sinks, &L)
                  : lib.gqa_prefill(q, kc, vc, bt, qs, sl, o, T, max_q, x.h_q, x.h_kv, x.d, scale,

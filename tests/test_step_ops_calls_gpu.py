@@ -91,6 +91,46 @@ def test_plans_of_different_sizes_from_two_threads():
     assert not failed
 
 
+# ------------------------------------------------------------------ streams
+
+
+def test_results_on_a_given_stream_may_be_used_on_the_current_one():
+    """A result that was allocated for a call on another stream, then read on the
+    current one and dropped, is not handed to that stream's next work while the
+    current one still reads it."""
+    x = _attn_case([1, 1, 1], [900, 90, 700], 16, 4, "bf16", 16, 820)
+    rope = da.rope_table([0.5] * 64)
+    slots = _i32([-1, -1, -1])
+    kv = torch.randn((3, 4, 128), generator=_gen(1), device=DEV).bfloat16()
+    pos = _i32([[3, 4, 5]])
+    table, new, free, top = x["table"].clone(), _i32([1, 1, 1]), _i32([0, 1, 2, 3]), _i32([4])
+    calls = {
+        "decode": lambda **kw: da.gqa_decode(x["q"], *x["caches"], x["table"], x["lens"], scale=0.1,
+                                             max_seq_len=900, **kw),
+        "prefill": lambda **kw: da.gqa_prefill(x["q"], *x["caches"], x["table"], x["start"],
+                                               x["lens"], scale=0.1, max_q_len=1, max_seq_len=900,
+                                               **kw),
+        "rope": lambda **kw: da.gqa_rope_append(x["q"], kv, kv, pos, rope, slots, *x["caches"], **kw),
+        "plan": lambda **kw: da.paged_plan(x["lens"], new, table, free, top, block_size=16,
+                                           max_tokens=4, **kw).positions,
+    }
+    s = torch.cuda.Stream()
+    for name, call in calls.items():
+        want = call()
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        got = call(stream=s)
+        torch.cuda.current_stream().wait_stream(s)
+        torch.cuda._sleep(20_000_000)  # what reads the result runs in some ms
+        seen = got.clone()
+        size = got.untyped_storage().nbytes()
+        del got
+        with torch.cuda.stream(s):
+            spoil = [torch.full((size,), 0x7F, dtype=torch.uint8, device=DEV) for _ in range(6)]
+        torch.cuda.synchronize()
+        assert torch.equal(seen, want) and len(spoil) == 6, name
+
+
 # ------------------------------------------------------------------ 8-bit cache
 
 
