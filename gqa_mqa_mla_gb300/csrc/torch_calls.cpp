@@ -445,7 +445,9 @@ struct Attention {
   Tensor workspace(PyObject* o) const {
     if (none(o)) return Tensor();
     const Tensor& t = tensor(o, "workspace");
-    if (!t.is_contiguous()) value_error("workspace must be contiguous");
+    // (Bytes alone count: any order of strides will do, but none of them may lie
+    // between the tensor's elements.)
+    if (!t.is_non_overlapping_and_dense()) value_error("workspace must be dense");
     same_device(index, t, "workspace");
     return t;
   }

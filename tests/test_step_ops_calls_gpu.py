@@ -131,6 +131,22 @@ def test_results_on_a_given_stream_may_be_used_on_the_current_one():
         assert torch.equal(seen, want) and len(spoil) == 6, name
 
 
+def test_a_workspace_may_be_any_dense_tensor():
+    """Strides in another order hold the same bytes."""
+    x = _attn_case([1, 1, 1], [900, 90, 700], 16, 4, "bf16", 16, 821)
+    ws = torch.empty(512, 512, dtype=torch.uint8, device=DEV).t()
+    assert not ws.is_contiguous()
+    kw = dict(scale=0.1, max_seq_len=900, num_splits=4)
+    args = (x["q"], *x["caches"], x["table"])
+    assert torch.equal(da.gqa_decode(*args, x["lens"], workspace=ws, **kw),
+                       da.gqa_decode(*args, x["lens"], **kw))
+    assert torch.equal(da.gqa_prefill(*args, x["start"], x["lens"], max_q_len=1, workspace=ws, **kw),
+                       da.gqa_prefill(*args, x["start"], x["lens"], max_q_len=1, **kw))
+    for bad in (ws[::2], torch.empty(1, dtype=torch.uint8, device=DEV).expand(2**18)):
+        with pytest.raises(ValueError):
+            da.gqa_decode(*args, x["lens"], workspace=bad, **kw)
+
+
 # ------------------------------------------------------------------ 8-bit cache
 
 
