@@ -4,8 +4,9 @@ Argument marshalling only: every step of the computation runs in the CUDA
 kernels behind the C ABI.  PyTorch supplies device memory and the current
 stream.  The GQA decode calls and the serving step's operators are marshalled
 natively (csrc/torch_calls.cpp: checks, allocations, stream and call in one
-step, for the latency of small calls); the others through ctypes.  If a shared
-library is missing the calls raise; there is no fallback implementation.
+step, for the latency of small calls); the others through ctypes, and the decode
+calls too where the native half is missing or was built for another PyTorch.  If
+libdecattn is missing the calls raise; there is no fallback implementation.
 
 Every call runs on the current stream of the tensors' device, or on `stream`
 where it is given (a torch.cuda.Stream or a handle): inputs must then be ready on
@@ -19,6 +20,7 @@ import ctypes
 import importlib.util
 import os
 import threading
+import warnings
 from typing import NamedTuple
 
 import torch
@@ -356,6 +358,88 @@ def make_launch(batch, num_blocks, block_size, max_blocks_per_seq, max_seq_len, 
                   dtype, workspace, workspace_bytes, err_flag, stream)
 
 
+class _CtypesCalls:
+    """The GQA decode calls without the native half: the same arguments, checks and
+    results, at some 10 us more a call."""
+
+    @staticmethod
+    def decode(q, kc, vc, k_scale, v_scale, table, lens, scale, max_seq_len, window, sinks,
+               num_splits, out, workspace, err_flag, stream):
+        fp8 = k_scale is not None
+        _check(q, "q", ndim=3)
+        if q.dtype not in _DT:
+            raise TypeError("q must be float16 or bfloat16")
+        for t, name in ((kc, "k_cache"), (vc, "v_cache")):
+            codes = isinstance(t, torch.Tensor) and t.dtype == torch.float8_e4m3fn
+            _check(t, name, q.dtype if not fp8 else t.dtype if codes else torch.uint8, 4)
+        _check(table, "block_table", torch.int32, 2)
+        _check(lens, "seq_lens", torch.int32, 1)
+        B, h_q, d = q.shape
+        nb, bs, h_kv, _ = kc.shape
+        if kc.shape[3] != d or vc.shape != kc.shape:
+            raise ValueError("k_cache / v_cache shape mismatch")
+        if table.shape[0] < B or lens.shape[0] < B:
+            raise ValueError(f"block_table and seq_lens need an entry for each of the {B} rows of q")
+        if h_kv < 1 or h_q % h_kv != 0:
+            raise ValueError(f"h_q={h_q} is not a multiple of h_kv={h_kv}")
+        scales = [k_scale, v_scale] if fp8 else []
+        for t in scales:
+            _check(t, "k_scale / v_scale", torch.float32, 1)
+            if t.shape[0] != h_kv:
+                raise ValueError("k_scale / v_scale must be [h_kv]")
+        if not q.is_cuda:
+            raise ValueError("the tensors must be on a CUDA device")
+        if out is not None:
+            _check(out, "out", q.dtype)
+            if out.numel() < q.numel():
+                raise ValueError(f"out: expected shape {tuple(q.shape)}, got {tuple(out.shape)}")
+        for t in (kc, vc, table, lens, *scales, out, workspace, err_flag):
+            if t is not None and not (t.device == q.device or (not t.is_cuda and t.is_pinned())):
+                raise ValueError(f"a tensor is on {t.device}, q on {q.device}")
+        caller = torch.cuda.current_stream(q.device)
+        own = caller if stream is None or stream == caller.cuda_stream else \
+            torch.cuda.ExternalStream(stream, device=q.device)
+        L_ = lib()
+        with torch.cuda.device(q.device), torch.cuda.stream(own):
+            ns = num_splits
+            if not ns:
+                ns = L_.gqa_decode_sinks_plan_splits(B, h_q, h_kv, d, max_seq_len, window, sinks, bs,
+                                                     1 if fp8 else 2, 0) if window is not None else \
+                    (L_.gqa_decode_fp8kv_plan_splits if fp8 else L_.gqa_decode_plan_splits)(
+                        B, h_q, h_kv, d, max_seq_len, 0)
+                if ns < 0:
+                    return ns
+            if out is None:
+                out = torch.empty_like(q)
+                out.record_stream(caller)
+            need = int(L_.gqa_decode_workspace_size(B, h_q, d, ns)) if ns > 1 else 0
+            if need and workspace is None:
+                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            size = 0 if workspace is None else workspace.numel() * workspace.element_size()
+            L = make_launch(B, nb, bs, table.shape[1], max_seq_len, ns, _DT[q.dtype],
+                            _ptr(workspace), size, _ptr(err_flag), own.cuda_stream)
+            args = [t.data_ptr() for t in (q, kc, vc, *scales, table, lens, out)]
+            args += [h_q, h_kv, d, float(scale)]
+            if window is not None:
+                args += [window] + ([sinks] if sinks else [])
+            name = _decode_name("gqa_decode_fp8kv" if fp8 else "gqa_decode", window, sinks)
+            st = getattr(L_, name)(*args, ctypes.byref(L))
+        return out if st == DECATTN_OK else st
+
+
+def _decode_calls():
+    """The native calls; without them (not built, or for another PyTorch) ctypes."""
+    if _calls is not None:
+        return _calls
+    lib()
+    try:
+        return calls()
+    except (RuntimeError, ImportError) as e:
+        warnings.warn(f"the GQA decode calls go through ctypes, some 10 us slower: {e}",
+                      RuntimeWarning, stacklevel=3)
+        return _CtypesCalls
+
+
 def gqa_decode(q, k_cache, v_cache, block_table, seq_lens, *, scale: float, max_seq_len: int,
                out=None, num_splits: int = 0, workspace=None, err_flag=None, stream=None,
                window: int | None = None, sinks: int = 0):
@@ -363,14 +447,16 @@ def gqa_decode(q, k_cache, v_cache, block_table, seq_lens, *, scale: float, max_
 
     q [B, h_q, d]; k_cache/v_cache [num_blocks, block_size, h_kv, d];
     block_table int32 [B, max_blocks]; seq_lens int32 [B] (either may have more
-    entries: the first B count); max_seq_len a host upper bound of seq_lens.  workspace: optional uint8 CUDA tensor (sized by
-    gqa_workspace_size); allocated here when needed and not given.  window:
-    attend only to each sequence's last `window` tokens (gqa_decode_window),
-    and with sinks > 0 to its first `sinks` tokens too (gqa_decode_sinks).
+    entries: the first B count); max_seq_len a host upper bound of seq_lens.
+    workspace: optional uint8 CUDA tensor (sized by gqa_workspace_size); allocated
+    here when needed and not given.  window: attend only to each sequence's last
+    `window` tokens (gqa_decode_window), and with sinks > 0 to its first `sinks`
+    tokens too (gqa_decode_sinks).
     """
     _check_sinks(window, sinks)
-    r = calls().decode(q, k_cache, v_cache, None, None, block_table, seq_lens, scale, max_seq_len,
-                       _window(window), sinks, num_splits, out, workspace, err_flag, _handle(stream))
+    r = _decode_calls().decode(q, k_cache, v_cache, None, None, block_table, seq_lens, scale,
+                               max_seq_len, _window(window), sinks, num_splits, out, workspace,
+                               err_flag, _handle(stream))
     if type(r) is int:
         raise DecAttnError(_decode_name("gqa_decode", window, sinks), r)
     return r
@@ -400,9 +486,9 @@ def gqa_decode_fp8kv(q, k_codes, v_codes, k_scale, v_scale, block_table, seq_len
     _check_sinks(window, sinks)
     if k_scale is None or v_scale is None:
         raise TypeError("k_scale and v_scale must be torch.Tensors")
-    r = calls().decode(q, k_codes, v_codes, k_scale, v_scale, block_table, seq_lens, scale,
-                       max_seq_len, _window(window), sinks, num_splits, out, workspace, err_flag,
-                       _handle(stream))
+    r = _decode_calls().decode(q, k_codes, v_codes, k_scale, v_scale, block_table, seq_lens, scale,
+                               max_seq_len, _window(window), sinks, num_splits, out, workspace,
+                               err_flag, _handle(stream))
     if type(r) is int:
         raise DecAttnError(_decode_name("gqa_decode_fp8kv", window, sinks), r)
     return r

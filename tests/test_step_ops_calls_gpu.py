@@ -147,6 +147,40 @@ def test_a_workspace_may_be_any_dense_tensor():
             da.gqa_decode(*args, x["lens"], workspace=bad, **kw)
 
 
+# ------------------------------------------------------------------ without the native half
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_decode_through_ctypes_gives_the_same(monkeypatch, fp8):
+    x = _attn_case([1, 1, 1], [900, 90, 700], 16, 4, "bf16", 16, 822, fp8=fp8)
+    fn = da.gqa_decode_fp8kv if fp8 else da.gqa_decode
+    args = (x["q"], *x["caches"], *(x["scales"] or []), x["table"], x["lens"])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    forms = [{}, dict(num_splits=3), dict(window=300), dict(window=300, sinks=4),
+             dict(num_splits=4, window=800, sinks=70), dict(stream=s), dict(stream=s.cuda_stream),
+             dict(out=torch.zeros(4, 16 * 128, dtype=torch.bfloat16, device=DEV)),
+             dict(num_splits=4, workspace=torch.empty(2**18, device=DEV))]
+    kw = dict(scale=0.09, max_seq_len=900)
+    want = [fn(*args, **kw, **f).clone() for f in forms if "stream" not in f]
+    torch.cuda.synchronize()
+    monkeypatch.setattr(binding, "_calls", None)
+    monkeypatch.setattr(binding._build, "calls_match", lambda: False)
+    with pytest.warns(RuntimeWarning, match="ctypes"):
+        got = [fn(*args, **kw, **f) for f in forms]
+        torch.cuda.synchronize()
+        bad = [dict(max_seq_len=10**6), dict(num_splits=-1), dict(num_splits=4, workspace=x["q"][0])]
+        for b in bad:
+            with pytest.raises(da.DecAttnError):
+                fn(*args, **{**kw, **b})
+        for b in (dict(out=x["q"].float()), dict(out=x["q"].cpu()), dict(out=x["q"][:1])):
+            with pytest.raises((TypeError, ValueError)):
+                fn(*args, **{**kw, **b})
+    same = [o for o, f in zip(got, forms) if "stream" not in f]
+    assert all(torch.equal(a, b) for a, b in zip(same, want))
+    assert all(torch.equal(o, want[0]) for o, f in zip(got, forms) if "stream" in f)
+
+
 # ------------------------------------------------------------------ 8-bit cache
 
 
