@@ -578,8 +578,9 @@ def paged_plan(cached_lens, new_lens, block_table, free_blocks, free_count, *, b
     cached_lens, new_lens int32 [B] (new < 0 gives tokens back); block_table
     int32 [B, max_blocks] and free_blocks int32 [num_blocks] (a stack of
     free_count[0] ids) are updated in place.  The outputs are allocated when
-    not given; free_count_out may be free_count and seq_lens may be
-    cached_lens (in place).  Rows past the step's last token get slot and
+    not given, as parts of one storage (a kept seq_lens keeps that step's slots
+    and positions in memory too); free_count_out may be free_count and seq_lens may
+    be cached_lens (in place).  Rows past the step's last token get slot and
     position -1.
     """
     r = calls().paged_plan(cached_lens, new_lens, block_table, free_blocks, free_count, block_size,

@@ -18,7 +18,8 @@
 // the CTAs need not wait for one another -- except where the lengths or the
 // free count are updated in place: then one CTA does a small step, and a
 // cluster of eight, behind a barrier, a larger one.  Measured (replayed): 64
-// requests with a token each 3.1 us, 1024 mixed ones with 64k rows 6.5 us.
+// requests with a token each 2.9 us, in place 3.4; 1024 mixed ones with 64k rows
+// 6.3 us, in place 18.9.
 #include <algorithm>
 
 #include "internal.h"

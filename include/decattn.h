@@ -224,8 +224,12 @@ int gqa_decode_fp8kv_window(const void* q, const void* k_cache, const void* v_ca
  * Every other argument, layout, status and the workspace rule as
  * gqa_decode_window (resp. gqa_decode_fp8kv_window).  Blocks that hold
  * neither a kept first token nor a token of the window are never read and
- * their block_table entries never checked.  The planner counts the window's
- * token range (as for gqa_decode_window) plus sinks rounded up to 64.
+ * their block_table entries never checked.  num_splits = 0 takes the windowed
+ * planner's count for the window's token range plus sinks rounded up to 64, and,
+ * up to 16 query heads per KV head and from six 64-token tiles on, at least as
+ * many splits as fill two thirds of the GPU, up to eight, of two tiles or more
+ * (two to eight splits merge within one launch): size the workspace by
+ * gqa_decode_sinks_plan_splits.
  */
 int gqa_decode_sinks(const void* q, const void* k_cache, const void* v_cache,
                      const int32_t* block_table, const int32_t* seq_lens, void* out, int h_q,
@@ -491,7 +495,8 @@ int mla_decode_plan_splits(int batch, int max_seq_len, int num_sms);
  * gqa_decode_fp8kv_window; block_size a power of two. */
 int gqa_decode_window_plan_splits(int batch, int h_q, int h_kv, int d_head, int max_seq_len,
                                   int window, int block_size, int kv_bytes, int num_sms);
-/* The same with `sinks` (>= 0) first tokens kept. */
+/* The same with `sinks` (>= 0) first tokens kept (gqa_decode_sinks says how it
+ * counts). */
 int gqa_decode_sinks_plan_splits(int batch, int h_q, int h_kv, int d_head, int max_seq_len,
                                  int window, int sinks, int block_size, int kv_bytes,
                                  int num_sms);
