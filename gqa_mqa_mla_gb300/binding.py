@@ -397,8 +397,12 @@ class _CtypesCalls:
             if t is not None and not (t.device == q.device or (not t.is_cuda and t.is_pinned())):
                 raise ValueError(f"a tensor is on {t.device}, q on {q.device}")
         caller = torch.cuda.current_stream(q.device)
-        own = caller if stream is None or stream == caller.cuda_stream else \
-            torch.cuda.ExternalStream(stream, device=q.device)
+        if stream is None or stream == caller.cuda_stream:
+            own = caller
+        elif stream == 0:  # (ExternalStream takes 0 for "a new one")
+            own = torch.cuda.default_stream(q.device)
+        else:
+            own = torch.cuda.ExternalStream(stream, device=q.device)
         L_ = lib()
         with torch.cuda.device(q.device), torch.cuda.stream(own):
             ns = num_splits

@@ -150,6 +150,31 @@ def test_a_workspace_may_be_any_dense_tensor():
 # ------------------------------------------------------------------ without the native half
 
 
+@pytest.mark.parametrize("native", [True, False])
+def test_a_call_on_the_default_stream_from_another(monkeypatch, native):
+    """Stream handle 0 is the default stream, not a new one: the call comes behind the
+    work that makes its input there."""
+    x = _attn_case([1, 1, 1], [900, 90, 700], 16, 4, "bf16", 16, 823)
+    if not native:
+        monkeypatch.setattr(binding, "_calls", None)
+        monkeypatch.setattr(binding._build, "calls_match", lambda: False)
+        monkeypatch.setattr(binding.warnings, "warn", lambda *a, **k: None)
+    q, spoilt = x["q"].clone(), torch.full_like(x["q"], 3.0)
+    call = lambda t, **kw: da.gqa_decode(t, *x["caches"], x["table"], x["lens"],  # noqa: E731
+                                         scale=0.1, max_seq_len=900, **kw)
+    want = call(q)
+    torch.cuda.synchronize()
+    for handle in (0, torch.cuda.default_stream()):
+        t = spoilt.clone()
+        torch.cuda.synchronize()
+        torch.cuda._sleep(20_000_000)
+        t.copy_(q)
+        with torch.cuda.stream(torch.cuda.Stream()):
+            out = call(t, stream=handle)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 def test_decode_through_ctypes_gives_the_same(monkeypatch, fp8):
     x = _attn_case([1, 1, 1], [900, 90, 700], 16, 4, "bf16", 16, 822, fp8=fp8)
