@@ -358,6 +358,16 @@ def make_launch(batch, num_blocks, block_size, max_blocks_per_seq, max_seq_len, 
                   dtype, workspace, workspace_bytes, err_flag, stream)
 
 
+def _dense(t: torch.Tensor) -> bool:
+    """No bytes between the tensor's elements, in whatever order its strides are."""
+    n = 1
+    for step, size in sorted((st, s) for s, st in zip(t.shape, t.stride()) if s != 1):
+        if step != n:
+            return False
+        n *= size
+    return True
+
+
 class _CtypesCalls:
     """The GQA decode calls without the native half: the same arguments, checks and
     results, at some 10 us more a call."""
@@ -393,6 +403,13 @@ class _CtypesCalls:
             _check(out, "out", q.dtype)
             if out.numel() < q.numel():
                 raise ValueError(f"out: expected shape {tuple(q.shape)}, got {tuple(out.shape)}")
+        for t, name in ((workspace, "workspace"), (err_flag, "err_flag")):
+            if t is not None and not isinstance(t, torch.Tensor):
+                raise TypeError(f"{name} must be a torch.Tensor")
+        if workspace is not None and not _dense(workspace):
+            raise ValueError("workspace must be dense")
+        if err_flag is not None and err_flag.numel() * err_flag.element_size() < 4:
+            raise ValueError("err_flag needs one int32 element")
         for t in (kc, vc, table, lens, *scales, out, workspace, err_flag):
             if t is not None and not (t.device == q.device or (not t.is_cuda and t.is_pinned())):
                 raise ValueError(f"a tensor is on {t.device}, q on {q.device}")

@@ -311,9 +311,10 @@ __device__ __forceinline__ uint4* staged(uint8_t* stage, int row, int c) {
 // e4m3(x - t1), ...  Each remainder is a multiple of the query's own last bit
 // no larger than half of the term's step, so two terms hold a bf16 query and
 // three an fp16 one exactly, but for parts up to 2^-10 (half of e4m3's smallest
-// step) of the scaled row, whose largest value is above 224.  Term t of the tile: [128 rows][128 codes], 128-byte swizzle;
-// k goes to qexp[r].  16 lanes take a row, 8 values each; of the 32 rows the pairs
-// [b0, b1) are this warp's, as far as they are real (the others may hold anything).
+// step) of the scaled row, whose largest value is above 224.  Term t of the tile:
+// [128 rows][128 codes], 128-byte swizzle; k goes to qexp[r].  16 lanes take a row,
+// 8 values each; of the 32 rows the pairs [b0, b1) are this warp's, as far as they
+// are real (the others may hold anything).
 template <bool kBF16, int kTerms>
 __device__ __forceinline__ void split_q(const PrefillParams& p, const Item& w, int x, int part,
                                         int b0, int b1, uint32_t inv_g, uint8_t* dst, int8_t* qexp) {

@@ -198,7 +198,12 @@ def test_decode_through_ctypes_gives_the_same(monkeypatch, fp8):
         for b in bad:
             with pytest.raises(da.DecAttnError):
                 fn(*args, **{**kw, **b})
-        for b in (dict(out=x["q"].float()), dict(out=x["q"].cpu()), dict(out=x["q"][:1])):
+        ws = torch.empty(512, 512, dtype=torch.uint8, device=DEV)
+        assert torch.equal(fn(*args, **kw, num_splits=3, workspace=ws.t()), want[1])
+        for b in (dict(out=x["q"].float()), dict(out=x["q"].cpu()), dict(out=x["q"][:1]),
+                  dict(workspace=ws[::2]), dict(workspace=ws[:1].expand(512, 512)),
+                  dict(workspace=3), dict(workspace=ws.cpu()), dict(err_flag=3),
+                  dict(err_flag=ws[0, :3])):
             with pytest.raises((TypeError, ValueError)):
                 fn(*args, **{**kw, **b})
     same = [o for o, f in zip(got, forms) if "stream" not in f]
