@@ -62,7 +62,7 @@ def draw(rng):
     h_q, h_kv = rng.choice([(64, 8), (32, 8), (32, 32), (32, 1), (28, 4), (12, 4), (8, 8), (64, 1), (5, 1)])
     case = {"op": op, "batch": _spread(rng, 1, 64), "h_q": h_q, "h_kv": h_kv, "dtype": rng.choice(["bf16", "fp16"]), "block": rng.choice([8, 16, 32, 64, 128, 256]),
             "fp8": rng.random() < 0.35, "shape": rng.randrange(1 << 20)}
-    hi = _spread(rng, 1, 131072 if op in ("select", "bounds") else 32768)
+    hi = _spread(rng, 64 * case["block"] if op == "select" else 1, 131072 if op in ("select", "bounds") else 32768)
     most = {"bounds": 200000, "select": 700000, "blocks": 300000, "weights": 350000, "evict": 200000}[op] * 8
     while case["batch"] * hi * h_kv > most:
         case["batch"], hi = (case["batch"] + 1) // 2, max(1, hi * 3 // 4)
@@ -72,8 +72,11 @@ def draw(rng):
     elif op in ("select", "blocks"):
         case["count"] = _spread(rng, 3, 4096 // case["block"])
         if op == "select":
-            case["first"] = rng.choice([0, 1, 1, 2])
-            case["last"] = rng.choice([0, 1, 1])
+            # some sequence has a choice to make
+            case["ctx_lo"] = rng.randint(1 if case["batch"] >= 8 else hi // 2, hi)
+            case["count"] = max(5, min(case["count"], max(_lens(case)) // case["block"] // 2))
+            case["first"] = rng.choice([0, 1, 1])
+            case["last"] = rng.choice([0, 1, 1, 2])
     elif op == "evict":
         case["keep"] = _spread(rng, 1, min(hi, 6000))
         case["recent"] = rng.randint(0, case["keep"])
