@@ -322,7 +322,7 @@ def run(state):
     if op == "bounds":
         return da.gqa_block_bounds(s["k"], s["table"], s["lens"], s["bounds"], first_lens=s["first"] if case["new"] else None, max_seq_len=most)
     if op == "select":
-        return da.gqa_select_blocks(s["q"], s["bounds"], s["table"], s["lens"], max_seq_len=most, count=case["count"], first=case["first"], last=case["last"])
+        return da.gqa_select_blocks(s["q"], s["bounds"], s["table"], s["lens"], block_size=case["block"], max_seq_len=most, count=case["count"], first=case["first"], last=case["last"])
     if op == "blocks":
         if case["fp8"]:
             return da.gqa_decode_fp8kv_blocks(s["q"], *s["caches"], *s["scales"], s["table"], s["lens"], s["selected"], scale=D ** -0.5, max_seq_len=most)
