@@ -89,6 +89,13 @@ class PagedPlan(NamedTuple):
     free_count: torch.Tensor  # int32 [1]
 
 
+class Evicted(NamedTuple):
+    """What gqa_kv_evict returns beside the caches and weights that it updates."""
+
+    new_lens: torch.Tensor  # int32 [B]: minus the tokens evicted (paged_plan's new_lens)
+    kept: torch.Tensor      # int32 [B, h_kv, keep]: old positions; -1: nothing evicted
+
+
 _lock = threading.Lock()
 _lib = None
 _calls = None
@@ -149,6 +156,26 @@ def lib() -> ctypes.CDLL:
             L.gqa_prefill_plan_splits.restype = I
             L.gqa_prefill_workspace_size.argtypes = [I, I, I, I]
             L.gqa_prefill_workspace_size.restype = S
+            L.gqa_decode_blocks.argtypes = [P, P, P, P, P, P, P, I, I, I, F, I, LP]
+            L.gqa_decode_blocks.restype = I
+            L.gqa_decode_fp8kv_blocks.argtypes = [P, P, P, P, P, P, P, P, P, I, I, I, F, I, LP]
+            L.gqa_decode_fp8kv_blocks.restype = I
+            L.gqa_decode_blocks_plan_splits.argtypes = [I, I, I, I, I, I, I, I, I]
+            L.gqa_decode_blocks_plan_splits.restype = I
+            L.gqa_decode_weights.argtypes = [P, P, P, P, P, P, P, P, I, I, I, F, F, LP]
+            L.gqa_decode_weights.restype = I
+            L.gqa_decode_fp8kv_weights.argtypes = [P, P, P, P, P, P, P, P, P, P, I, I, I, F, F, LP]
+            L.gqa_decode_fp8kv_weights.restype = I
+            L.gqa_decode_weights_workspace_size.argtypes = [I, I, I, I, I]
+            L.gqa_decode_weights_workspace_size.restype = S
+            L.gqa_block_bounds.argtypes = [P, P, P, P, P, I, I, I, LP]
+            L.gqa_block_bounds.restype = I
+            L.gqa_select_blocks.argtypes = [P, P, P, P, P, I, I, I, I, I, I, I, LP]
+            L.gqa_select_blocks.restype = I
+            L.gqa_select_workspace_size.argtypes = [I, I, I, I, I]
+            L.gqa_select_workspace_size.restype = S
+            L.gqa_kv_evict.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, I, LP]
+            L.gqa_kv_evict.restype = I
             L.gqa_kv_append.argtypes = [P, P, P, P, P, P, I, I, LP]
             L.gqa_kv_append.restype = I
             L.gqa_kv_append_fp8kv.argtypes = [P, P, P, P, P, P, P, P, I, I, LP]
@@ -293,6 +320,27 @@ def gqa_prefill_plan_splits(batch: int, tokens: int, max_q_len: int, h_q: int, h
     if r < 0:
         raise DecAttnError("gqa_prefill_plan_splits", r)
     return r
+
+
+def gqa_blocks_plan_splits(batch: int, h_q: int, h_kv: int, max_seq_len: int, count: int,
+                           block_size: int, kv_bytes: int = 2, d_head: int = 128,
+                           num_sms: int = 0) -> int:
+    r = lib().gqa_decode_blocks_plan_splits(batch, h_q, h_kv, d_head, max_seq_len, count,
+                                            block_size, kv_bytes, num_sms)
+    if r < 0:
+        raise DecAttnError("gqa_decode_blocks_plan_splits", r)
+    return r
+
+
+def gqa_weights_workspace_size(batch: int, h_q: int, max_seq_len: int, num_splits: int,
+                               d_head: int = 128) -> int:
+    return int(lib().gqa_decode_weights_workspace_size(batch, h_q, d_head, max_seq_len,
+                                                       num_splits))
+
+
+def gqa_select_workspace_size(batch: int, h_kv: int, max_seq_len: int, block_size: int,
+                              count: int) -> int:
+    return int(lib().gqa_select_workspace_size(batch, h_kv, max_seq_len, block_size, count))
 
 
 def gqa_prefill_workspace_size(tokens: int, h_q: int, num_splits: int, d_head: int = 128) -> int:
@@ -711,6 +759,126 @@ def gqa_prefill_fp8kv(q, k_codes, v_codes, k_scale, v_scale, block_table, q_star
     return _prefill("gqa_prefill_fp8kv", q, k_codes, v_codes, k_scale, v_scale, block_table, q_start,
                     seq_lens, scale, max_q_len, max_seq_len, window, sinks, out, num_splits,
                     workspace, err_flag, stream)
+
+
+def gqa_block_bounds(k_cache, block_table, seq_lens, bounds, *, max_seq_len: int, first_lens=None,
+                     err_flag=None, stream=None):
+    """Smallest and largest key of cache blocks, per KV head and dimension, for
+    gqa_select_blocks; updates bounds [num_blocks, 2, h_kv, d] in place and returns it.
+
+    k_cache [num_blocks, block_size, h_kv, d] fp16/bf16, or e4m3 codes (uint8 or
+    float8_e4m3fn); bounds of the same type; block_table int32 [B, max_blocks],
+    seq_lens int32 [B].  first_lens int32 [B]: the tokens whose blocks are up to
+    date (each sequence's length before the step); without it every block is taken.
+    """
+    r = calls().block_bounds(k_cache, block_table, seq_lens, bounds, first_lens, max_seq_len,
+                             err_flag, _handle(stream))
+    if type(r) is int:
+        raise DecAttnError("gqa_block_bounds", r)
+    return r
+
+
+def gqa_select_blocks(q, bounds, block_table, seq_lens, *, block_size: int, max_seq_len: int,
+                      count: int, first: int = 1, last: int = 1, out=None, workspace=None,
+                      err_flag=None, stream=None):
+    """The `count` blocks of each sequence that can matter most to its query, per KV
+    head; returns int32 [B, h_kv, count], block numbers within the sequence,
+    ascending, -1 behind the last.
+
+    q [B, h_q, d] fp16/bf16; bounds: gqa_block_bounds' (16-bit: q's type; or e4m3
+    codes).  The sequence's `first` first and `last` last blocks are always among
+    them, the others by the largest bound of q . k over their keys.  workspace:
+    optional uint8 CUDA tensor (gqa_select_workspace_size bytes).
+    """
+    r = calls().select_blocks(q, bounds, block_table, seq_lens, block_size, max_seq_len, count,
+                              first, last, out, workspace, err_flag, _handle(stream))
+    if type(r) is int:
+        raise DecAttnError("gqa_select_blocks", r)
+    return r
+
+
+def gqa_decode_blocks(q, k_cache, v_cache, block_table, seq_lens, selected, *, scale: float,
+                      max_seq_len: int, out=None, num_splits: int = 0, workspace=None,
+                      err_flag=None, stream=None):
+    """gqa_decode over the blocks that selected [B, h_kv, count] (int32, ascending
+    block numbers within the sequence, -1 behind the last: gqa_select_blocks') lists
+    for each sequence and KV head; returns out [B, h_q, d]."""
+    r = calls().decode_blocks(q, k_cache, v_cache, None, None, block_table, seq_lens, selected,
+                              scale, max_seq_len, num_splits, out, workspace, err_flag,
+                              _handle(stream))
+    if type(r) is int:
+        raise DecAttnError("gqa_decode_blocks", r)
+    return r
+
+
+def gqa_decode_fp8kv_blocks(q, k_codes, v_codes, k_scale, v_scale, block_table, seq_lens,
+                            selected, *, scale: float, max_seq_len: int, out=None,
+                            num_splits: int = 0, workspace=None, err_flag=None, stream=None):
+    """gqa_decode_blocks over an 8-bit e4m3 cache (uint8 or float8_e4m3fn) with one
+    scale per KV head."""
+    if k_scale is None or v_scale is None:
+        raise TypeError("k_scale and v_scale must be torch.Tensors")
+    r = calls().decode_blocks(q, k_codes, v_codes, k_scale, v_scale, block_table, seq_lens,
+                              selected, scale, max_seq_len, num_splits, out, workspace, err_flag,
+                              _handle(stream))
+    if type(r) is int:
+        raise DecAttnError("gqa_decode_fp8kv_blocks", r)
+    return r
+
+
+def gqa_decode_weights(q, k_cache, v_cache, weights, block_table, seq_lens, *, scale: float,
+                       max_seq_len: int, weighed_lens=None, decay: float = 1.0, out=None,
+                       num_splits: int = 0, workspace=None, err_flag=None, stream=None):
+    """gqa_decode that adds up each cached token's attention weight; returns out.
+
+    weights float32 [num_blocks, h_kv, block_size], updated in place: the slot of
+    each token t < seq_lens[b] gets (decay times its old value where t <
+    weighed_lens[b], else 0) plus the softmax weights that the KV head's query heads
+    give it.  weighed_lens int32 [B]: the tokens that have weights already; without
+    it all but the last.  workspace: gqa_weights_workspace_size bytes.
+    """
+    r = calls().decode_weights(q, k_cache, v_cache, None, None, block_table, seq_lens, weights,
+                               weighed_lens, scale, decay, max_seq_len, num_splits, out, workspace,
+                               err_flag, _handle(stream))
+    if type(r) is int:
+        raise DecAttnError("gqa_decode_weights", r)
+    return r
+
+
+def gqa_decode_fp8kv_weights(q, k_codes, v_codes, k_scale, v_scale, weights, block_table,
+                             seq_lens, *, scale: float, max_seq_len: int, weighed_lens=None,
+                             decay: float = 1.0, out=None, num_splits: int = 0, workspace=None,
+                             err_flag=None, stream=None):
+    """gqa_decode_weights over an 8-bit e4m3 cache (uint8 or float8_e4m3fn) with one
+    scale per KV head."""
+    if k_scale is None or v_scale is None:
+        raise TypeError("k_scale and v_scale must be torch.Tensors")
+    r = calls().decode_weights(q, k_codes, v_codes, k_scale, v_scale, block_table, seq_lens,
+                               weights, weighed_lens, scale, decay, max_seq_len, num_splits, out,
+                               workspace, err_flag, _handle(stream))
+    if type(r) is int:
+        raise DecAttnError("gqa_decode_fp8kv_weights", r)
+    return r
+
+
+def gqa_kv_evict(k_cache, v_cache, weights, block_table, seq_lens, *, max_seq_len: int, keep: int,
+                 recent: int, limit: int | None = None, new_lens=None, kept=None, err_flag=None,
+                 stream=None) -> Evicted:
+    """Sequences longer than `limit` (default: keep) go back to `keep` tokens: per KV
+    head the last `recent` and the heaviest others by weights (gqa_decode_weights'),
+    moved in order to the sequence's front.
+
+    k_cache, v_cache (fp16/bf16, or e4m3 codes as uint8 or float8_e4m3fn) and
+    weights are updated in place.  Returns new_lens [B] (minus the tokens evicted:
+    paged_plan's new_lens, which frees their blocks) and kept [B, h_kv, keep] (the
+    kept tokens' old positions, -1 where nothing is evicted).
+    """
+    r = calls().kv_evict(k_cache, v_cache, weights, block_table, seq_lens, max_seq_len, keep,
+                         recent, keep if limit is None else limit, new_lens, kept, err_flag,
+                         _handle(stream))
+    if type(r) is int:
+        raise DecAttnError("gqa_kv_evict", r)
+    return Evicted(*r)
 
 
 def mla_kv_append(latent_new, positions, block_table, latent_cache, *, err_flag=None,

@@ -380,6 +380,29 @@ int gqa_decode_sinks_plan_splits(int batch, int h_q, int h_kv, int d_head, int m
                        : plan_gqa_splits(batch, h_q, h_kv, span, num_sms);
 }
 
+int gqa_decode_blocks_plan_splits(int batch, int h_q, int h_kv, int d_head, int max_seq_len,
+                                  int count, int block_size, int kv_bytes, int num_sms) {
+  if (batch < 1 || h_q < 1 || h_kv < 1 || h_q % h_kv != 0 || d_head < 1 || max_seq_len < 0 ||
+      count < 1 || !is_pow2(block_size) || (kv_bytes != 1 && kv_bytes != 2))
+    return DECATTN_ERR_INVALID_ARG;
+  if (num_sms <= 0) num_sms = device_sm_count();
+  if (num_sms <= 0) return DECATTN_ERR_CUDA;
+  return plan_sinks_splits(batch, h_q, h_kv, static_cast<int>(std::min<int64_t>(
+                               max_seq_len, static_cast<int64_t>(count) * block_size)),
+                           num_sms, kv_bytes == 1);
+}
+
+size_t gqa_decode_weights_workspace_size(int batch, int h_q, int d_head, int max_seq_len,
+                                         int num_splits) {
+  if (batch < 1 || h_q < 1 || d_head < 1 || max_seq_len < 0 || num_splits < 1 ||
+      num_splits > DECATTN_MAX_SPLITS)
+    return 0;
+  const size_t rows = static_cast<size_t>(batch) * h_q;
+  const size_t stride = (std::max<size_t>(1, max_seq_len) + kTile - 1) / kTile * kTile;
+  return (num_splits > 1 ? align_up(rows * num_splits * d_head * sizeof(float)) : 0) +
+         align_up(rows * num_splits * sizeof(float)) + align_up(rows * stride * sizeof(float));
+}
+
 int mla_decode_plan_splits(int batch, int max_seq_len, int num_sms) {
   if (batch < 1 || max_seq_len < 0) return DECATTN_ERR_INVALID_ARG;
   if (num_sms <= 0) num_sms = device_sm_count();
@@ -434,25 +457,46 @@ int gqa_check_args(const void* q, const void* k_cache, const void* v_cache,
 
 extern "C" {
 
+// What the forms over listed blocks and with token weights have beside a decode's
+// arguments.
+struct DecodeMore {
+  const int32_t* selected = nullptr;
+  int count = 0;
+  float* weights = nullptr;
+  const int32_t* weighed_lens = nullptr;
+  float decay = 1.f;
+};
+
+static int64_t scores_stride(int max_seq_len) {
+  return (std::max<int64_t>(1, max_seq_len) + kTile - 1) / kTile * kTile;
+}
+
+// The longest token range that listed blocks make up.
+static int listed_span(int max_seq_len, int count, int block_size) {
+  return static_cast<int>(std::min<int64_t>(max_seq_len, static_cast<int64_t>(count) * block_size));
+}
+
 // gqa_decode and gqa_decode_fp8kv share everything but the cache element type
 // (and the 8-bit cache's per-KV-head scales).
 static int gqa_decode_impl(const void* q, const void* k_cache, const void* v_cache,
                            const float* k_scale, const float* v_scale, bool fp8,
                            const int32_t* block_table, const int32_t* seq_lens, void* out,
                            int h_q, int h_kv, int d_head, float scale, int window, int sinks,
-                           const decattn_launch* L) {
+                           const decattn_launch* L, const DecodeMore& more = {}) {
   const int st = gqa_check_args(q, k_cache, v_cache, k_scale, v_scale, fp8, block_table,
                                 seq_lens, out, h_q, h_kv, d_head, scale, window, L);
   if (st != DECATTN_OK) return st;
   if (sinks > 0) window = useful_window(window, L->max_seq_len);
-  const int span = sinks_span(L->max_seq_len, window, sinks, L->block_size);
+  const int span = more.selected ? listed_span(L->max_seq_len, more.count, L->block_size)
+                                 : sinks_span(L->max_seq_len, window, sinks, L->block_size);
+  const bool merges = more.selected || (sinks > 0 && window > 0);  // in one launch, where it can
   int n_split = L->num_splits;
   if (n_split == 0) {
     const int sms = device_sm_count();
     if (sms <= 0) return DECATTN_ERR_CUDA;
-    n_split = sinks > 0 && window > 0 ? plan_sinks_splits(L->batch, h_q, h_kv, span, sms, fp8)
-              : fp8                   ? plan_gqa_fp8_splits(L->batch, h_q, h_kv, span, sms)
-                                      : plan_gqa_splits(L->batch, h_q, h_kv, span, sms);
+    n_split = merges ? plan_sinks_splits(L->batch, h_q, h_kv, span, sms, fp8)
+              : fp8  ? plan_gqa_fp8_splits(L->batch, h_q, h_kv, span, sms)
+                     : plan_gqa_splits(L->batch, h_q, h_kv, span, sms);
   }
   int tps = 0;
   const int eff = resolve_splits(span, n_split, &tps);
@@ -478,16 +522,28 @@ static int gqa_decode_impl(const void* q, const void* k_cache, const void* v_cac
   p.window = window;
   p.sinks = window > 0 ? sinks : 0;
   // (A cluster has at most eight CTAs; wide groups have a kernel of their own.)
-  p.joint = p.sinks > 0 && eff > 1 && eff <= 8 && p.group <= kWideGroup;
+  p.joint = (p.sinks > 0 || more.selected) && eff > 1 && eff <= 8 && p.group <= kWideGroup;
   p.k_scale = k_scale;
   p.v_scale = v_scale;
-  if (eff > 1) {
-    const size_t need = gqa_decode_workspace_size(L->batch, h_q, d_head, eff);
+  p.selected = more.selected;
+  p.n_listed = more.count;
+  if (eff > 1 || more.weights) {
+    const size_t need =
+        more.weights
+            ? gqa_decode_weights_workspace_size(L->batch, h_q, d_head, L->max_seq_len, eff)
+            : gqa_decode_workspace_size(L->batch, h_q, d_head, eff);
     if (!L->workspace || L->workspace_bytes < need) return DECATTN_ERR_WORKSPACE;
     const size_t rows = static_cast<size_t>(L->batch) * h_q * eff;
-    p.part_o = static_cast<float*>(L->workspace);
-    p.part_lse = reinterpret_cast<float*>(static_cast<char*>(L->workspace) +
-                                          align_up(rows * d_head * sizeof(float)));
+    char* ws = static_cast<char*>(L->workspace);
+    if (eff > 1) {
+      p.part_o = reinterpret_cast<float*>(ws);
+      ws += align_up(rows * d_head * sizeof(float));
+    }
+    p.part_lse = reinterpret_cast<float*>(ws);
+    if (more.weights) {
+      p.scores = reinterpret_cast<float*>(ws + align_up(rows * sizeof(float)));
+      p.score_stride = scores_stride(L->max_seq_len);
+    }
   }
 
   const bool bf16 = L->dtype == DECATTN_BF16;
@@ -526,6 +582,29 @@ static int gqa_decode_impl(const void* q, const void* k_cache, const void* v_cac
   const cudaError_t e = fp8 ? launch_gqa_partial_fp8(p, tk, tv, bf16, stream)
                             : launch_gqa_partial(p, tk, tv, bf16, 0, stream);
   if (e != cudaSuccess) return DECATTN_ERR_CUDA;
+  if (more.weights) {
+    WeighParams w{};
+    w.part_o = p.part_o;
+    w.part_lse = p.part_lse;
+    w.scores = p.scores;
+    w.out = out;
+    w.weights = more.weights;
+    w.block_table = block_table;
+    w.seq_lens = seq_lens;
+    w.weighed_lens = more.weighed_lens;
+    w.score_stride = p.score_stride;
+    w.batch = L->batch;
+    w.h_q = h_q;
+    w.h_kv = h_kv;
+    w.group = p.group;
+    w.n_split = eff;
+    w.block_size = L->block_size;
+    w.log2_block_size = p.log2_block_size;
+    w.max_blocks_per_seq = L->max_blocks_per_seq;
+    w.max_seq_len = L->max_seq_len;
+    w.decay = more.decay;
+    return launch_weigh(w, bf16, stream) == cudaSuccess ? DECATTN_OK : DECATTN_ERR_CUDA;
+  }
   if (eff > 1 && !p.joint) {
     CombineParams c{p.part_o, p.part_lse, out, L->batch * h_q, eff};
     if (launch_combine(c, kHeadDim, bf16, stream) != cudaSuccess) return DECATTN_ERR_CUDA;
@@ -583,6 +662,218 @@ int gqa_decode_fp8kv_sinks(const void* q, const void* k_cache, const void* v_cac
   if (window < 1 || sinks < 0) return DECATTN_ERR_INVALID_ARG;
   return gqa_decode_impl(q, k_cache, v_cache, k_scale, v_scale, true, block_table, seq_lens, out,
                          h_q, h_kv, d_head, scale, window, sinks, L);
+}
+
+// Sizes that a 32-bit token position must reach beyond by a tile.
+static bool too_long(const decattn_launch* L) { return L && L->max_seq_len > 0x7fffffff - 256; }
+
+static int decode_blocks(const void* q, const void* k_cache, const void* v_cache,
+                         const float* k_scale, const float* v_scale, bool fp8,
+                         const int32_t* block_table, const int32_t* seq_lens,
+                         const int32_t* selected, void* out, int h_q, int h_kv, int d_head,
+                         float scale, int count, const decattn_launch* L) {
+  if (!selected || !aligned(selected, 4) || count < 1) return DECATTN_ERR_INVALID_ARG;
+  if (too_long(L)) return DECATTN_ERR_UNSUPPORTED;
+  DecodeMore more;
+  more.selected = selected;
+  more.count = count;
+  return gqa_decode_impl(q, k_cache, v_cache, k_scale, v_scale, fp8, block_table, seq_lens, out,
+                         h_q, h_kv, d_head, scale, 0, 0, L, more);
+}
+
+int gqa_decode_blocks(const void* q, const void* k_cache, const void* v_cache,
+                      const int32_t* block_table, const int32_t* seq_lens,
+                      const int32_t* selected, void* out, int h_q, int h_kv, int d_head,
+                      float scale, int count, const decattn_launch* L) {
+  return decode_blocks(q, k_cache, v_cache, nullptr, nullptr, false, block_table, seq_lens,
+                       selected, out, h_q, h_kv, d_head, scale, count, L);
+}
+
+int gqa_decode_fp8kv_blocks(const void* q, const void* k_cache, const void* v_cache,
+                            const float* k_scale, const float* v_scale,
+                            const int32_t* block_table, const int32_t* seq_lens,
+                            const int32_t* selected, void* out, int h_q, int h_kv, int d_head,
+                            float scale, int count, const decattn_launch* L) {
+  return decode_blocks(q, k_cache, v_cache, k_scale, v_scale, true, block_table, seq_lens,
+                       selected, out, h_q, h_kv, d_head, scale, count, L);
+}
+
+static int decode_weights(const void* q, const void* k_cache, const void* v_cache,
+                          const float* k_scale, const float* v_scale, bool fp8,
+                          const int32_t* block_table, const int32_t* seq_lens,
+                          const int32_t* weighed_lens, float* weights, void* out, int h_q,
+                          int h_kv, int d_head, float scale, float decay,
+                          const decattn_launch* L) {
+  if (!weights || !aligned(weights, 16) || !aligned(weighed_lens, 4) || !std::isfinite(decay))
+    return DECATTN_ERR_INVALID_ARG;
+  if (too_long(L)) return DECATTN_ERR_UNSUPPORTED;
+  DecodeMore more;
+  more.weights = weights;
+  more.weighed_lens = weighed_lens;
+  more.decay = decay;
+  return gqa_decode_impl(q, k_cache, v_cache, k_scale, v_scale, fp8, block_table, seq_lens, out,
+                         h_q, h_kv, d_head, scale, 0, 0, L, more);
+}
+
+int gqa_decode_weights(const void* q, const void* k_cache, const void* v_cache,
+                       const int32_t* block_table, const int32_t* seq_lens,
+                       const int32_t* weighed_lens, float* weights, void* out, int h_q, int h_kv,
+                       int d_head, float scale, float decay, const decattn_launch* L) {
+  return decode_weights(q, k_cache, v_cache, nullptr, nullptr, false, block_table, seq_lens,
+                        weighed_lens, weights, out, h_q, h_kv, d_head, scale, decay, L);
+}
+
+int gqa_decode_fp8kv_weights(const void* q, const void* k_cache, const void* v_cache,
+                             const float* k_scale, const float* v_scale,
+                             const int32_t* block_table, const int32_t* seq_lens,
+                             const int32_t* weighed_lens, float* weights, void* out, int h_q,
+                             int h_kv, int d_head, float scale, float decay,
+                             const decattn_launch* L) {
+  return decode_weights(q, k_cache, v_cache, k_scale, v_scale, true, block_table, seq_lens,
+                        weighed_lens, weights, out, h_q, h_kv, d_head, scale, decay, L);
+}
+
+int gqa_block_bounds(const void* k_cache, const int32_t* block_table, const int32_t* first_lens,
+                     const int32_t* seq_lens, void* bounds, int h_kv, int d_head, int kv_bytes,
+                     const decattn_launch* L) {
+  const int st = check_launch(L, false);
+  if (st != DECATTN_OK) return st;
+  if (!k_cache || !block_table || !seq_lens || !bounds || k_cache == bounds)
+    return DECATTN_ERR_INVALID_ARG;
+  if (!aligned(k_cache, 16) || !aligned(bounds, 16) || !aligned(block_table, 4) ||
+      !aligned(first_lens, 4) || !aligned(seq_lens, 4))
+    return DECATTN_ERR_INVALID_ARG;
+  if (h_kv < 1 || h_kv > 1024 || (kv_bytes != 1 && kv_bytes != 2)) return DECATTN_ERR_INVALID_ARG;
+  if (d_head != kHeadDim || too_long(L)) return DECATTN_ERR_UNSUPPORTED;
+  const int sms = device_sm_count();
+  if (sms <= 0) return DECATTN_ERR_CUDA;
+  BoundsParams p{};
+  p.k_cache = k_cache;
+  p.block_table = block_table;
+  p.first_lens = first_lens;
+  p.seq_lens = seq_lens;
+  p.bounds = bounds;
+  p.err_flag = L->err_flag;
+  p.batch = L->batch;
+  p.h_kv = h_kv;
+  p.block_size = L->block_size;
+  p.log2_block_size = ilog2(L->block_size);
+  p.num_blocks = L->num_blocks;
+  p.max_blocks_per_seq = L->max_blocks_per_seq;
+  p.max_seq_len = L->max_seq_len;
+  const cudaError_t e = launch_block_bounds(p, kv_bytes == 1, L->dtype == DECATTN_BF16, sms,
+                                            static_cast<cudaStream_t>(L->stream));
+  return e == cudaSuccess ? DECATTN_OK : DECATTN_ERR_CUDA;
+}
+
+static int64_t select_blocks_of(int max_seq_len, int block_size) {
+  return (static_cast<int64_t>(max_seq_len) + block_size - 1) / block_size;
+}
+
+size_t gqa_select_workspace_size(int batch, int h_kv, int max_seq_len, int block_size, int count) {
+  if (batch < 1 || h_kv < 1 || max_seq_len < 0 || !is_pow2(block_size) || count < 1) return 0;
+  const int64_t blocks = select_blocks_of(max_seq_len, block_size);
+  if (blocks <= count) return 0;
+  const size_t units = static_cast<size_t>(batch) * h_kv, stride = (blocks + 7) / 8 * 8;
+  return align_up(units * stride * sizeof(uint64_t)) + align_up(units * stride * sizeof(float)) +
+         align_up(units * ((stride + 31) / 32) * sizeof(float));
+}
+
+int gqa_select_blocks(const void* q, const void* bounds, const int32_t* block_table,
+                      const int32_t* seq_lens, int32_t* selected, int h_q, int h_kv, int d_head,
+                      int kv_bytes, int count, int first, int last, const decattn_launch* L) {
+  const int st = check_launch(L, false);
+  if (st != DECATTN_OK) return st;
+  if (!q || !bounds || !block_table || !seq_lens || !selected) return DECATTN_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(bounds, 16) || !aligned(block_table, 4) ||
+      !aligned(seq_lens, 4) || !aligned(selected, 4))
+    return DECATTN_ERR_INVALID_ARG;
+  if (h_q < 1 || h_kv < 1 || h_q % h_kv != 0 || (kv_bytes != 1 && kv_bytes != 2))
+    return DECATTN_ERR_INVALID_ARG;
+  if (count < 1 || first < 0 || last < 0 || static_cast<int64_t>(first) + last > count)
+    return DECATTN_ERR_INVALID_ARG;
+  if (d_head != kHeadDim || h_q / h_kv > 64 || L->batch > 65535 || h_kv > 65535 || too_long(L))
+    return DECATTN_ERR_UNSUPPORTED;
+  const int64_t blocks = select_blocks_of(L->max_seq_len, L->block_size);
+  SelectParams p{};
+  p.q = q;
+  p.bounds = bounds;
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.selected = selected;
+  p.err_flag = L->err_flag;
+  p.score_stride = (blocks + 7) / 8 * 8;
+  p.batch = L->batch;
+  p.h_kv = h_kv;
+  p.group = h_q / h_kv;
+  p.count = count;
+  p.first = first;
+  p.last = last;
+  p.block_size = L->block_size;
+  p.log2_block_size = ilog2(L->block_size);
+  p.num_blocks = L->num_blocks;
+  p.max_blocks_per_seq = L->max_blocks_per_seq;
+  p.max_seq_len = L->max_seq_len;
+  if (blocks > count) {
+    const size_t need =
+        gqa_select_workspace_size(L->batch, h_kv, L->max_seq_len, L->block_size, count);
+    if (!L->workspace || L->workspace_bytes < need) return DECATTN_ERR_WORKSPACE;
+    const int sms = device_sm_count();
+    if (sms <= 0) return DECATTN_ERR_CUDA;
+    p.score_ctas = select_score_ctas(L->batch, h_kv, static_cast<int>(blocks), count, sms);
+    p.cached_blocks = select_cached_blocks(static_cast<int>(blocks), count);
+    const size_t all = static_cast<size_t>(L->batch) * h_kv * p.score_stride;
+    char* ws = static_cast<char*>(L->workspace);
+    p.exact = reinterpret_cast<uint64_t*>(ws);
+    ws += align_up(all * sizeof(uint64_t));
+    p.scores = reinterpret_cast<float*>(ws);
+    ws += align_up(all * sizeof(float));
+    p.error = reinterpret_cast<float*>(ws);
+  }
+  const cudaError_t e = launch_select_blocks(p, kv_bytes == 1, L->dtype == DECATTN_BF16,
+                                             static_cast<cudaStream_t>(L->stream));
+  return e == cudaSuccess ? DECATTN_OK : DECATTN_ERR_CUDA;
+}
+
+int gqa_kv_evict(void* k_cache, void* v_cache, float* weights, const int32_t* block_table,
+                 const int32_t* seq_lens, int32_t* new_lens, int32_t* kept, int h_kv, int d_head,
+                 int kv_bytes, int keep, int recent, int limit, const decattn_launch* L) {
+  const int st = check_launch(L, false);
+  if (st != DECATTN_OK) return st;
+  if (!k_cache || !v_cache || !weights || !block_table || !seq_lens || !new_lens || !kept ||
+      k_cache == v_cache || new_lens == seq_lens)
+    return DECATTN_ERR_INVALID_ARG;
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(weights, 16) ||
+      !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(new_lens, 4) ||
+      !aligned(kept, 4))
+    return DECATTN_ERR_INVALID_ARG;
+  if (h_kv < 1 || h_kv > 1024 || (kv_bytes != 1 && kv_bytes != 2)) return DECATTN_ERR_INVALID_ARG;
+  if (keep < 1 || recent < 0 || recent > keep || limit < keep) return DECATTN_ERR_INVALID_ARG;
+  if (d_head != kHeadDim || L->batch > 65535 || too_long(L)) return DECATTN_ERR_UNSUPPORTED;
+  const int sms = device_sm_count();
+  if (sms <= 0) return DECATTN_ERR_CUDA;
+  EvictParams p{};
+  p.k_cache = static_cast<uint8_t*>(k_cache);
+  p.v_cache = static_cast<uint8_t*>(v_cache);
+  p.weights = weights;
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.new_lens = new_lens;
+  p.kept = kept;
+  p.err_flag = L->err_flag;
+  p.batch = L->batch;
+  p.h_kv = h_kv;
+  p.head_bytes = kHeadDim * kv_bytes;
+  p.keep = keep;
+  p.recent = recent;
+  p.limit = limit;
+  p.block_size = L->block_size;
+  p.log2_block_size = ilog2(L->block_size);
+  p.num_blocks = L->num_blocks;
+  p.max_blocks_per_seq = L->max_blocks_per_seq;
+  p.max_seq_len = L->max_seq_len;
+  const cudaError_t e = launch_kv_evict(p, sms, static_cast<cudaStream_t>(L->stream));
+  return e == cudaSuccess ? DECATTN_OK : DECATTN_ERR_CUDA;
 }
 
 int mla_decode(const void* q_absorbed, const void* q_rope, const void* latent_cache,

@@ -1,0 +1,163 @@
+// block_bounds.cu -- smallest and largest key of a cache block, per KV head and
+// dimension: what a query's scores over the block are bounded by.
+//
+// For the block of tokens T (those before the sequence's end) and KV head j
+//     lo_d = min_{t in T} k_td,   hi_d = max_{t in T} k_td,
+// NaN in both where one of the keys is NaN.  Whole blocks are taken anew, so
+// that a block whose tokens were given back or replaced needs no other care.
+//
+// Bound by the keys' bytes: one pass, a warp to a (block, head), whose lanes
+// read 16-byte pieces of two (16-bit) or four (8-bit) token rows at once, eight
+// loads in flight each; the warps of a CTA take neighbouring heads of a block,
+// whose rows are neighbours in memory.
+#include <algorithm>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace decattn {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kAhead = 8;  // loads in flight per lane
+
+// Packed 16-bit minimum and maximum; NaN if one is NaN.
+template <bool kBF16>
+DECATTN_DEV uint32_t min2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if constexpr (kBF16)
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else
+    asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+template <bool kBF16>
+DECATTN_DEV uint32_t max2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if constexpr (kBF16)
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// Two fp16 values that are e4m3 values (or NaN) to their codes, exactly.
+DECATTN_DEV uint32_t f16x2_to_e4m3x2(uint32_t x) {
+  uint16_t c;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c) : "r"(x));
+  return c;
+}
+
+// kF8: e4m3 codes, compared as the fp16 values they stand for.
+template <bool kF8, bool kBF16>
+__global__ void __launch_bounds__(kWarps * 32) block_bounds_kernel(const BoundsParams p) {
+  constexpr int kLanes = kF8 ? 8 : 16;         // lanes to a token row of 128 or 256 bytes
+  constexpr int kRows = 32 / kLanes;           // token rows a load
+  constexpr int kWords = kF8 ? 8 : 4;          // 16-bit pairs in 16 bytes
+  constexpr uint32_t kInf = kBF16 && !kF8 ? 0x7f807f80u : 0x7c007c00u;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int piece = lane & (kLanes - 1), row0 = lane / kLanes;
+  const int lg = p.log2_block_size;
+  const int64_t row_bytes = static_cast<int64_t>(p.h_kv) * kLanes * 16;
+  const uint8_t* keys = static_cast<const uint8_t*>(p.k_cache);
+  for (int b = blockIdx.y; b < p.batch; b += gridDim.y) {
+    const int n = p.seq_lens[b], first = p.first_lens ? p.first_lens[b] : 0;
+    if (n < 0 || n > p.max_seq_len || first < 0) {
+      if (blockIdx.x == 0 && threadIdx.x == 0) flag_error(p.err_flag, kFlagBadSeqLen);
+      continue;
+    }
+    if (n == 0) continue;
+    const int lb0 = min(first, n - 1) >> lg;
+    const int64_t units = static_cast<int64_t>(((n - 1) >> lg) + 1 - lb0) * p.h_kv;
+    const int32_t* bt = p.block_table + static_cast<int64_t>(b) * p.max_blocks_per_seq;
+    for (int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + warp; u < units;
+         u += static_cast<int64_t>(gridDim.x) * kWarps) {
+      const int lb = lb0 + static_cast<int>(u / p.h_kv), j = static_cast<int>(u % p.h_kv);
+      const int id = bt[lb];
+      if (id < 0 || id >= p.num_blocks) {
+        if (lane == 0) flag_error(p.err_flag, kFlagBadBlock);
+        continue;
+      }
+      const int rows = min(p.block_size, n - (lb << lg));
+      const uint8_t* src = keys + static_cast<int64_t>(id) * p.block_size * row_bytes +
+                           j * (kLanes * 16) + piece * 16;
+      uint32_t lo[kWords], hi[kWords];
+#pragma unroll
+      for (int k = 0; k < kWords; ++k) {
+        lo[k] = kInf;
+        hi[k] = kInf | 0x80008000u;
+      }
+      for (int r0 = row0; r0 < rows; r0 += kRows * kAhead) {
+        uint4 x[kAhead];
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) {
+          const int r = min(r0 + a * kRows, rows - 1);  // (the last row again, for none)
+          x[a] = *reinterpret_cast<const uint4*>(src + r * row_bytes);
+        }
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) {
+          const uint32_t w[4] = {x[a].x, x[a].y, x[a].z, x[a].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if constexpr (kF8) {
+              uint32_t h0, h1;
+              e4m3x4_to_f16x2(w[k], h0, h1);
+              lo[2 * k] = min2<false>(lo[2 * k], h0);
+              hi[2 * k] = max2<false>(hi[2 * k], h0);
+              lo[2 * k + 1] = min2<false>(lo[2 * k + 1], h1);
+              hi[2 * k + 1] = max2<false>(hi[2 * k + 1], h1);
+            } else {
+              lo[k] = min2<kBF16>(lo[k], w[k]);
+              hi[k] = max2<kBF16>(hi[k], w[k]);
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int o = kLanes; o < 32; o <<= 1) {
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) {
+          lo[k] = min2<kBF16 && !kF8>(lo[k], __shfl_xor_sync(0xffffffffu, lo[k], o));
+          hi[k] = max2<kBF16 && !kF8>(hi[k], __shfl_xor_sync(0xffffffffu, hi[k], o));
+        }
+      }
+      if (row0 < 2) {  // the first row's lanes write lo, the second's hi
+        uint32_t out[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if constexpr (kF8)
+            out[k] = row0 ? f16x2_to_e4m3x2(hi[2 * k]) | f16x2_to_e4m3x2(hi[2 * k + 1]) << 16
+                          : f16x2_to_e4m3x2(lo[2 * k]) | f16x2_to_e4m3x2(lo[2 * k + 1]) << 16;
+          else
+            out[k] = row0 ? hi[k] : lo[k];
+        }
+        uint8_t* dst = static_cast<uint8_t*>(p.bounds) +
+                       ((static_cast<int64_t>(id) * 2 + row0) * p.h_kv + j) * (kLanes * 16) + piece * 16;
+        *reinterpret_cast<uint4*>(dst) = make_uint4(out[0], out[1], out[2], out[3]);
+      }
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_block_bounds(const BoundsParams& p, bool e4m3, bool bf16, int num_sms,
+                                cudaStream_t stream) {
+  // A warp to each (block, head) that there can be, up to about one wave of CTAs.
+  const int64_t blocks = (static_cast<int64_t>(p.max_seq_len) + p.block_size - 1) / p.block_size;
+  const int64_t units = std::max<int64_t>(1, (blocks * p.h_kv + kWarps - 1) / kWarps);
+  const int y = std::min(p.batch, 65535);
+  const int64_t wave = std::max<int64_t>(1, static_cast<int64_t>(num_sms) * 8 / y);
+  const dim3 grid(static_cast<unsigned>(std::min(units, wave)), static_cast<unsigned>(y));
+  if (e4m3)
+    block_bounds_kernel<true, false><<<grid, kWarps * 32, 0, stream>>>(p);
+  else if (bf16)
+    block_bounds_kernel<false, true><<<grid, kWarps * 32, 0, stream>>>(p);
+  else
+    block_bounds_kernel<false, false><<<grid, kWarps * 32, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace decattn

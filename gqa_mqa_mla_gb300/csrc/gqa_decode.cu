@@ -116,8 +116,11 @@ struct CcConsumer {
 
   // Process this warp's 16 tokens (rows cw*16 .. cw*16+15) of one stage;
   // rows >= nval are past the sequence end and rows < nskip before a sliding
-  // window: neither is used.
-  __device__ __forceinline__ void tile(const uint8_t* stage, int nskip, int nval, float scale_log2) {
+  // window: neither is used.  kScores: the tile's scores go to `keep`, rows
+  // `ld` apart (those of rows that are not used may be anything).
+  template <bool kScores>
+  __device__ __forceinline__ void tile(const uint8_t* stage, int nskip, int nval, float scale_log2,
+                                       float* keep, int64_t ld) {
     const unsigned span = static_cast<unsigned>(nval - nskip);  // nskip < nval
     const uint8_t* ks = stage;
     const uint8_t* vs = stage + kKvTileBytes;
@@ -143,6 +146,16 @@ struct CcConsumer {
       const bool live = static_cast<unsigned>(r - nskip) < span;
 #pragma unroll
       for (int g = 0; g < G; ++g) s[i][g] = live ? part[g] * scale_log2 : kNegInf;
+    }
+    if constexpr (kScores) {
+      // Both half-warps hold their eight scores in every lane: lane i keeps the i-th.
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        float x = s[0][g];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) x = chunk == i ? s[i][g] : x;
+        if (chunk < 8) keep[g * ld + cw * 16 + 2 * chunk + half] = x;
+      }
     }
 #pragma unroll
     for (int g = 0; g < G; ++g) {
@@ -221,7 +234,7 @@ struct MmaConsumer {
   uint32_t qa[8][4];  // A fragments of the padded query group, 8 k-steps of 16
   float o[16][4];     // 16 n-tiles of 8 head dims, rows (lane/4, lane/4+8)
   float m[2], l[2];
-  int mt, tok0, cw, lane, lg_r;
+  int mt, tok0, cw, lane, lg_r, group;
 
   __device__ __forceinline__ void init(const GqaParams& p, int b, int j, int cw_, int lane_) {
     cw = cw_;
@@ -229,7 +242,7 @@ struct MmaConsumer {
     lg_r = min(p.log2_block_size, 6);
     mt = cw % MT;
     tok0 = (cw / MT) * kTokensPerWarp;
-    const int G = p.group;
+    const int G = group = p.group;
     const int r_lo = mt * 16 + (lane >> 2);
     const int r_hi = r_lo + 8;
     const int kc = (lane & 3) * 2;
@@ -249,7 +262,9 @@ struct MmaConsumer {
     l[0] = l[1] = 0.f;
   }
 
-  __device__ __forceinline__ void tile(uint8_t* stage, int nskip, int nval, float scale_log2) {
+  template <bool kScores>
+  __device__ __forceinline__ void tile(uint8_t* stage, int nskip, int nval, float scale_log2,
+                                       float* keep, int64_t ld) {
     const unsigned span = static_cast<unsigned>(nval - nskip);  // nskip < nval
     const uint32_t ks_base = smem_u32(stage);
     const uint32_t vs_base = ks_base + kKvTileBytes;
@@ -296,6 +311,17 @@ struct MmaConsumer {
       s1[1] = static_cast<unsigned>(tb + 1) < span ? s1[1] * scale_log2 : kNegInf;
       s1[2] = static_cast<unsigned>(tb) < span ? s1[2] * scale_log2 : kNegInf;
       s1[3] = static_cast<unsigned>(tb + 1) < span ? s1[3] * scale_log2 : kNegInf;
+      if constexpr (kScores) {
+        float* at = keep + (mt * 16 + (lane >> 2)) * ld + r0 + 2 * t4;
+        if (mt * 16 + (lane >> 2) < group) {
+          *reinterpret_cast<float2*>(at) = make_float2(s0[0], s0[1]);
+          *reinterpret_cast<float2*>(at + 8) = make_float2(s1[0], s1[1]);
+        }
+        if (mt * 16 + (lane >> 2) + 8 < group) {
+          *reinterpret_cast<float2*>(at + 8 * ld) = make_float2(s0[2], s0[3]);
+          *reinterpret_cast<float2*>(at + 8 * ld + 8) = make_float2(s1[2], s1[3]);
+        }
+      }
       float mx_lo = fmaxf(fmaxf(s0[0], s0[1]), fmaxf(s1[0], s1[1]));
       float mx_hi = fmaxf(fmaxf(s0[2], s0[3]), fmaxf(s1[2], s1[3]));
       mx_lo = fmaxf(mx_lo, __shfl_xor_sync(0xffffffffu, mx_lo, 1));
@@ -421,8 +447,11 @@ struct CcConsumerF8 {
 
   // Process this warp's 16 tokens (rows cw*16 .. cw*16+15) of one stage;
   // rows >= nval are past the sequence end and rows < nskip before a sliding
-  // window: neither is used.
-  __device__ __forceinline__ void tile(const uint8_t* stage, int nskip, int nval, float scale_log2) {
+  // window: neither is used.  kScores: the tile's scores go to `keep`, rows
+  // `ld` apart (those of rows that are not used may be anything).
+  template <bool kScores>
+  __device__ __forceinline__ void tile(const uint8_t* stage, int nskip, int nval, float scale_log2,
+                                       float* keep, int64_t ld) {
     const unsigned span = static_cast<unsigned>(nval - nskip);  // nskip < nval
     const uint8_t* ks = stage;
     const uint8_t* vs = stage + kF8TileBytes;
@@ -448,6 +477,16 @@ struct CcConsumerF8 {
       const bool live = static_cast<unsigned>(r - nskip) < span;
 #pragma unroll
       for (int g = 0; g < G; ++g) s[i][g] = live ? part[g] * scale_log2 : kNegInf;
+    }
+    if constexpr (kScores) {
+      // Both half-warps hold their eight scores in every lane: lane i keeps the i-th.
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        float x = s[0][g];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) x = chunk == i ? s[i][g] : x;
+        if (chunk < 8) keep[g * ld + cw * 16 + 2 * chunk + half] = x;
+      }
     }
 #pragma unroll
     for (int g = 0; g < G; ++g) {
@@ -535,14 +574,14 @@ struct MmaConsumerF8T {
   float o[8][NT][4];      // O^T, 16-dim block b: (2g, 2q) (2g, 2q+1) (2g+1, 2q) (2g+1, 2q+1)
   float m[NT][2], l[NT][2];
   float v_scale;
-  int tok0, cw, lane;
+  int tok0, cw, lane, group;
 
   __device__ __forceinline__ void init(const GqaParams& p, int b, int j, int cw_, int lane_) {
     cw = cw_;
     lane = lane_;
     tok0 = cw * 16;
     v_scale = p.v_scale[j];
-    const int G = p.group;
+    const int G = group = p.group;
     const int g = lane >> 2, q4 = lane & 3;
     const uint16_t* qp = static_cast<const uint16_t*>(p.q);
     const size_t base = (static_cast<size_t>(b) * p.h_q + static_cast<size_t>(j) * G) * kHeadDim;
@@ -564,7 +603,9 @@ struct MmaConsumerF8T {
     }
   }
 
-  __device__ __forceinline__ void tile(uint8_t* stage, int nskip, int nval, float scale_log2) {
+  template <bool kScores>
+  __device__ __forceinline__ void tile(uint8_t* stage, int nskip, int nval, float scale_log2,
+                                       float* keep, int64_t ld) {
     const unsigned span = static_cast<unsigned>(nval - nskip);  // nskip < nval
     const int r0 = tok0;
     if (r0 >= nval || r0 + 16 <= nskip) return;  // past the end, or before a sliding window
@@ -618,6 +659,16 @@ struct MmaConsumerF8T {
       s[nt][1] = la ? s[nt][1] * scale_log2 : kNegInf;
       s[nt][2] = lb ? s[nt][2] * scale_log2 : kNegInf;
       s[nt][3] = lb ? s[nt][3] * scale_log2 : kNegInf;
+      if constexpr (kScores) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int h = 8 * nt + 2 * (lane & 3) + e;
+          if (h < group) {
+            keep[h * ld + r0 + g] = s[nt][e];
+            keep[h * ld + r0 + g + 8] = s[nt][e + 2];
+          }
+        }
+      }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         float mx = fmaxf(s[nt][e], s[nt][e + 2]);
@@ -717,7 +768,7 @@ __host__ __device__ constexpr int smem_bytes() {
   return 1024 /*alignment slack*/ + kStages * stage_bytes<Consumer>() + 256 /*barriers*/;
 }
 
-template <class Consumer, bool kBF16, int kStages, bool kSinks>
+template <class Consumer, bool kBF16, int kStages, GqaForm kForm>
 DECATTN_DEV void gqa_partial(const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                              const GqaParams& p) {
   constexpr int kStage = stage_bytes<Consumer>();
@@ -736,7 +787,7 @@ DECATTN_DEV void gqa_partial(const CUtensorMap& tm_k, const CUtensorMap& tm_v,
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = p.group;
 
-  const GqaSpan<kSinks> span = gqa_span<kSinks>(p, split, j, b);
+  const GqaSpan<kForm> span = gqa_span<kForm>(p, split, j, b);
   int bad = span.bad;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -751,7 +802,7 @@ DECATTN_DEV void gqa_partial(const CUtensorMap& tm_k, const CUtensorMap& tm_v,
 
   const size_t row0 = static_cast<size_t>(b) * p.h_q + static_cast<size_t>(j) * G;
   if (bad || span.empty()) {
-    gqa_write_empty(p, row0, G, split, bad);
+    gqa_write_empty<kForm>(p, row0, G, split, bad);
     return;
   }
 
@@ -760,7 +811,54 @@ DECATTN_DEV void gqa_partial(const CUtensorMap& tm_k, const CUtensorMap& tm_v,
 
   if (warp == 0) {
     // ---------------- producer
-    if (lane == 0) {
+    if constexpr (kForm == kListed) {
+      // A block is found through two tables, so the lanes look 32 of them up at
+      // a time and lane k issues the copies of the tile's block k.
+      if (lane == 0) {
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
+      }
+      const uint64_t policy = policy_evict_first();
+      const int32_t* bt = p.block_table + static_cast<size_t>(b) * p.max_blocks_per_seq;
+      const int x0 = j * kHeadDim, lg = p.log2_block_size;
+      const int k_end = ((span.end() - 1) >> lg) + 1;  // one past the range's last block
+      int have = -(1 << 30), my_id = 0, issued = 0;
+      for (int it = 0; it < n_tiles; ++it) {
+        const GqaTile tl = span.tile(it);
+        const int k0 = tl.t0 >> lg, nblk = bs >= kTile ? 1 : (tl.nval + bs - 1) >> lg;
+        if (k0 + nblk > have + 32) {
+          have = k0;
+          my_id = k0 + lane < k_end ? bt[gqa_table_at<kForm>(p, j, b, k0 + lane)] : 0;
+        }
+        const int id = __shfl_sync(0xffffffffu, my_id, k0 - have + min(lane, nblk - 1));
+        const int s = it % kStages;
+        const uint32_t fb = full0 + 8 * s;
+        const int rows = bs >= kTile ? kTile : bs;
+        const uint32_t box = static_cast<uint32_t>(rows) * kHeadDim * Consumer::kCacheBytes;
+        int w = 1;
+        if (lane == 0) {
+          w = mbar_wait(empty0 + 8 * s, ((it / kStages) & 1) ^ 1, p.err_flag);
+          if (w) mbar_arrive_expect_tx(fb, 2 * box * nblk);
+        }
+        if (__shfl_sync(0xffffffffu, w, 0) == 0) break;
+        if (lane < nblk) {
+          const int row = id * bs + (bs >= kTile ? tl.t0 & (bs - 1) : 0);
+          const uint32_t kd = smem_u32(smem + s * kStage) + lane * box, vd = kd + kStage / 2;
+          if constexpr (Consumer::kCacheBytes == 1) {
+            tma_load_2d_hint(kd, &tm_k, x0, row, fb, policy);
+            tma_load_2d_hint(vd, &tm_v, x0, row, fb, policy);
+          } else {
+            tma_load_3d_hint(kd, &tm_k, 0, row, 2 * j, fb, policy);
+            tma_load_3d_hint(vd, &tm_v, 0, row, 2 * j, fb, policy);
+          }
+        }
+        ++issued;
+      }
+      if (lane == 0)  // (as below)
+        for (int it = max(0, issued - kStages); it < issued; ++it)
+          if (!mbar_wait(full0 + 8 * (it % kStages), (it / kStages) & 1, p.err_flag)) break;
+      __syncwarp();
+    } else if (lane == 0) {
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
       const uint64_t policy = policy_evict_first();
@@ -836,7 +934,11 @@ DECATTN_DEV void gqa_partial(const CUtensorMap& tm_k, const CUtensorMap& tm_v,
       break;
     }
     const GqaTile tl = span.tile(it);
-    c.tile(smem + s * kStage, tl.skip, tl.nval, scale_log2);
+    if constexpr (kForm == kWeighed)
+      c.template tile<true>(smem + s * kStage, tl.skip, tl.nval, scale_log2,
+                            p.scores + row0 * p.score_stride + tl.t0, p.score_stride);
+    else
+      c.template tile<false>(smem + s * kStage, tl.skip, tl.nval, scale_log2, nullptr, 0);
     fence_proxy_async_smem();  // order any generic smem writes before the next TMA fill
     __syncwarp();
     if (lane == 0) mbar_arrive(empty0 + 8 * s);
@@ -875,10 +977,11 @@ DECATTN_DEV void gqa_partial(const CUtensorMap& tm_k, const CUtensorMap& tm_v,
     const float res = L == 0.f ? 0.f : O / L;
     if (p.n_split == 1) {
       static_cast<uint16_t*>(p.out)[(row0 + r) * kHeadDim + d] = round1<kBF16>(res);
+      if (kForm != kWeighed) continue;
     } else {
       p.part_o[((row0 + r) * p.n_split + split) * kHeadDim + d] = res;
-      if (d == 0) p.part_lse[(row0 + r) * p.n_split + split] = L == 0.f ? kNegInf : M + lg2(L);
     }
+    if (d == 0) p.part_lse[(row0 + r) * p.n_split + split] = L == 0.f ? kNegInf : M + lg2(L);
   }
 }
 
@@ -929,11 +1032,11 @@ __device__ __noinline__ void merge_splits(const GqaParams& p) {
   }
 }
 
-template <class Consumer, bool kBF16, int kStages, bool kSinks, bool kJoint>
+template <class Consumer, bool kBF16, int kStages, GqaForm kForm, bool kJoint>
 __global__ void __launch_bounds__(32 * (1 + Consumer::kWarps), Consumer::kMinBlocks)
     gqa_partial_kernel(const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const GqaParams p) {
-  gqa_partial<Consumer, kBF16, kStages, kSinks>(tm_k, tm_v, p);
+  gqa_partial<Consumer, kBF16, kStages, kForm>(tm_k, tm_v, p);
   if constexpr (kJoint) {
     __syncwarp();
     cluster_sync();
@@ -941,10 +1044,10 @@ __global__ void __launch_bounds__(32 * (1 + Consumer::kWarps), Consumer::kMinBlo
   }
 }
 
-template <class Consumer, bool kBF16, int kStages, bool kSinks, bool kJoint>
+template <class Consumer, bool kBF16, int kStages, GqaForm kForm, bool kJoint>
 cudaError_t launch_with(const GqaParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
                         cudaStream_t stream, unsigned max_cluster) {
-  auto kern = gqa_partial_kernel<Consumer, kBF16, kStages, kSinks, kJoint>;
+  auto kern = gqa_partial_kernel<Consumer, kBF16, kStages, kForm, kJoint>;
   constexpr int smem = smem_bytes<Consumer, kStages>();
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -977,16 +1080,22 @@ cudaError_t launch_with(const GqaParams& p, const CUtensorMap& tk, const CUtenso
   return cudaGetLastError();
 }
 
-// A window with kept first tokens has its own instantiations, so that the
-// plain and windowed calls' code stays as it was.
+// Each form has its own instantiations, so that the plain and windowed calls'
+// code stays as it was.
 template <class Consumer, bool kBF16, int kStages>
 cudaError_t launch_one(const GqaParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
                        cudaStream_t stream, unsigned max_cluster) {
+  if (p.selected)
+    return p.joint
+               ? launch_with<Consumer, kBF16, kStages, kListed, true>(p, tk, tv, stream, max_cluster)
+               : launch_with<Consumer, kBF16, kStages, kListed, false>(p, tk, tv, stream, max_cluster);
+  if (p.scores)
+    return launch_with<Consumer, kBF16, kStages, kWeighed, false>(p, tk, tv, stream, max_cluster);
   if (p.sinks > 0)
     return p.joint
-               ? launch_with<Consumer, kBF16, kStages, true, true>(p, tk, tv, stream, max_cluster)
-               : launch_with<Consumer, kBF16, kStages, true, false>(p, tk, tv, stream, max_cluster);
-  return launch_with<Consumer, kBF16, kStages, false, false>(p, tk, tv, stream, max_cluster);
+               ? launch_with<Consumer, kBF16, kStages, kSinks, true>(p, tk, tv, stream, max_cluster)
+               : launch_with<Consumer, kBF16, kStages, kSinks, false>(p, tk, tv, stream, max_cluster);
+  return launch_with<Consumer, kBF16, kStages, kPlain, false>(p, tk, tv, stream, max_cluster);
 }
 
 template <bool kBF16>

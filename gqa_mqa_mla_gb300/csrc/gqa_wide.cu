@@ -208,7 +208,7 @@ __device__ __forceinline__ void convert_v8(const uint8_t* src, uint8_t* dst, int
 // score scale, V's into the output).  S = Q K^T then runs as kind::f8f6f4 on
 // the landed K codes, with Q split into e4m3 terms, and O += P V on f16
 // operands (V converted by the softmax threads).
-template <bool kBF16, bool kF8, bool kSinks>
+template <bool kBF16, bool kF8, GqaForm kForm>
 // (A minimum-blocks bound of 1 here made ptxas cap the registers at 168 and
 // spill; without it the kernel takes under 100.)
 __global__ void __launch_bounds__(kThreads)
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kThreads)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = p.group;
 
-  const GqaSpan<kSinks> span = gqa_span<kSinks>(p, split, j, b);
+  const GqaSpan<kForm> span = gqa_span<kForm>(p, split, j, b);
   if (threadIdx.x == 0) {
     mbar_init(bar(kBarQ), kSoftmaxThreads);
     for (int s = 0; s < kRing; ++s) {
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kThreads)
   const int bad = __syncthreads_or(span.bad);
   const size_t row0 = static_cast<size_t>(b) * p.h_q + static_cast<size_t>(j) * G;
   if (bad || span.empty()) {
-    gqa_write_empty(p, row0, G, split, bad);
+    gqa_write_empty<kForm>(p, row0, G, split, bad);
     return;
   }
 
@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(kThreads)
       const int nblk = bs >= kTile ? 1 : (nval + bs - 1) >> lg;
       if (kb0 + nblk > cache0 + 32) {
         cache0 = kb0;
-        my_id = kb0 + lane < kb_end ? bt[kb0 + lane] : 0;
+        my_id = kb0 + lane < kb_end ? bt[gqa_table_at<kForm>(p, j, b, kb0 + lane)] : 0;
       }
       const int id = __shfl_sync(0xffffffffu, my_id, kb0 - cache0 + min(lane, nblk - 1));
       const int rib = bs >= kTile ? (t0 & (bs - 1)) : 0;
@@ -566,6 +566,16 @@ __global__ void __launch_bounds__(kThreads)
           if (c_oth + kk >= nval || c_oth + kk < nskip) so[kk] = lowest;
         }
       }
+      if constexpr (kForm == kWeighed) {
+        // (Columns outside [nskip, nval) are never read.)
+        if (mine) {
+          float4* at = reinterpret_cast<float4*>(p.scores + (row0 + r) * p.score_stride + tl.t0 + c_own);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            at[k] = make_float4(sc[4 * k] * scale, sc[4 * k + 1] * scale, sc[4 * k + 2] * scale,
+                                sc[4 * k + 3] * scale);
+        }
+      }
 #pragma unroll
       for (int kk = 0; kk < 16; ++kk)
         so[kk] = scale >= 0.f ? fmaxf(so[kk], sc[kk]) : fminf(so[kk], sc[kk]);
@@ -724,9 +734,9 @@ __global__ void __launch_bounds__(kThreads)
           for (int k = 0; k < 8; ++k)
             dst[k] = make_float4(o[4 * k] * inv, o[4 * k + 1] * inv, o[4 * k + 2] * inv,
                                  o[4 * k + 3] * inv);
-          if (cg == 0 && hl == 0)
-            p.part_lse[row * p.n_split + split] = lsum == 0.f ? kNegInf : m_used + lg2(lsum);
         }
+        if ((kForm == kWeighed || p.n_split > 1) && cg == 0 && hl == 0)
+          p.part_lse[row * p.n_split + split] = lsum == 0.f ? kNegInf : m_used + lg2(lsum);
       }
     }
   }
@@ -742,7 +752,10 @@ __global__ void __launch_bounds__(kThreads)
 template <bool kBF16, bool kF8>
 cudaError_t launch_t(const GqaParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
                      cudaStream_t stream) {
-  auto kern = p.sinks > 0 ? gqa_wide_kernel<kBF16, kF8, true> : gqa_wide_kernel<kBF16, kF8, false>;
+  auto kern = p.selected    ? gqa_wide_kernel<kBF16, kF8, kListed>
+              : p.scores    ? gqa_wide_kernel<kBF16, kF8, kWeighed>
+              : p.sinks > 0 ? gqa_wide_kernel<kBF16, kF8, kSinks>
+                            : gqa_wide_kernel<kBF16, kF8, kPlain>;
   constexpr int smem = WLayout<kBF16, kF8>::kSmemBytes;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;

@@ -39,6 +39,10 @@ struct GqaParams {
   int joint;                      // sinks, n_split 2..8: the splits' CTAs merge their partials
   const float* k_scale;           // [h_kv], 8-bit caches only: K value = e4m3 * k_scale[j]
   const float* v_scale;           // [h_kv], 8-bit caches only
+  const int32_t* selected;        // [B, h_kv, n_listed]: attend to these blocks only, or null
+  int n_listed;
+  float* scores;                  // [B, h_q, score_stride]: keep the scores (log2 domain), or null
+  int64_t score_stride;           // max_seq_len rounded up to kTile
 };
 
 // MLA workspace (n_pairs > 1): a header of kHdrPref ints (slice width in
@@ -160,6 +164,69 @@ struct HeadGemmParams {
   int tmem_cols;    // power of two >= max(32, n_tile)
 };
 
+// Smallest and largest keys of cache blocks.
+struct BoundsParams {
+  const void* k_cache;        // [num_blocks, block_size, h_kv, 128]
+  const int32_t* block_table; // [B, max_blocks_per_seq]
+  const int32_t* first_lens;  // [B] tokens whose blocks are up to date, or null
+  const int32_t* seq_lens;    // [B]
+  void* bounds;               // [num_blocks, 2, h_kv, 128]
+  int* err_flag;
+  int batch, h_kv;
+  int block_size, log2_block_size, num_blocks, max_blocks_per_seq, max_seq_len;
+};
+
+// The blocks whose keys can score highest.
+struct SelectParams {
+  const void* q;              // [B, h_q, 128]
+  const void* bounds;         // [num_blocks, 2, h_kv, 128]
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  int32_t* selected;          // [B, h_kv, count]
+  float* scores;              // [B, h_kv, score_stride]    (score_ctas > 0)
+  float* error;               // [B, h_kv, score_ctas] how far a CTA's scores may be off
+  uint64_t* exact;            // [B, h_kv, score_stride] 64-bit scores in order, where needed
+  int* err_flag;
+  int64_t score_stride;       // blocks of max_seq_len, rounded up to 8
+  int batch, h_kv, group;
+  int count, first, last;     // first + last <= count
+  int score_ctas;             // CTAs a sequence and KV head; 0: no sequence has a choice to make
+  int cached_blocks;          // scores that the second kernel keeps in shared memory
+  int block_size, log2_block_size, num_blocks, max_blocks_per_seq, max_seq_len;
+};
+
+// Which tokens of a cache stay, and their move.
+struct EvictParams {
+  uint8_t* k_cache;           // [num_blocks, block_size, h_kv, 128]
+  uint8_t* v_cache;
+  float* weights;             // [num_blocks, h_kv, block_size]
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  int32_t* new_lens;          // [B]
+  int32_t* kept;              // [B, h_kv, keep]
+  int* err_flag;
+  int batch, h_kv, head_bytes;
+  int keep, recent, limit;
+  int cached_tokens;          // weights that the first kernel keeps in shared memory
+  int block_size, log2_block_size, num_blocks, max_blocks_per_seq, max_seq_len;
+};
+
+// The merge of a decode's partials, and its rows' attention weights added up.
+struct WeighParams {
+  const float* part_o;        // [B, h_q, n_split, 128]  (n_split > 1)
+  const float* part_lse;      // [B, h_q, n_split]
+  const float* scores;        // [B, h_q, score_stride]  log2 domain
+  void* out;                  // [B, h_q, 128]           (n_split > 1)
+  float* weights;             // [num_blocks, h_kv, block_size]
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* weighed_lens;  // [B], or null: all but the last token
+  int64_t score_stride;
+  int batch, h_q, h_kv, group, n_split;
+  int block_size, log2_block_size, max_blocks_per_seq, max_seq_len;
+  float decay;
+};
+
 struct CombineParams {
   const float* part_o;
   const float* part_lse;
@@ -215,6 +282,13 @@ cudaError_t launch_gqa_prefill(const PrefillParams& p, const CUtensorMap& tm_q,
                                bool fp8, cudaStream_t stream);
 cudaError_t launch_paged_plan(const PlanParams& p, cudaStream_t stream);
 cudaError_t launch_rope_append(const RopeParams& p, bool e4m3, bool bf16, cudaStream_t stream);
+cudaError_t launch_block_bounds(const BoundsParams& p, bool e4m3, bool bf16, int num_sms,
+                                cudaStream_t stream);
+int select_score_ctas(int batch, int h_kv, int blocks, int count, int num_sms);
+int select_cached_blocks(int blocks, int count);
+cudaError_t launch_select_blocks(const SelectParams& p, bool e4m3, bool bf16, cudaStream_t stream);
+cudaError_t launch_kv_evict(EvictParams p, int num_sms, cudaStream_t stream);
+cudaError_t launch_weigh(const WeighParams& p, bool bf16, cudaStream_t stream);
 cudaError_t launch_mla_combine(const MlaCombineParams& p, bool bf16, cudaStream_t stream);
 
 // Bounded-wait self test (csrc/selftest.cu).

@@ -1,0 +1,172 @@
+// kv_evict.cu -- a cache keeps its heaviest and its latest tokens: per sequence
+// and KV head, the choice by accumulated attention weight, and the move of what
+// stays to the front of the sequence, in order.
+//
+// A sequence of n > limit tokens keeps, of its first n - recent, the keep -
+// recent with the largest weights (ties: the earlier token; NaN is largest), and
+// its last `recent`.  Entry r of the list of kept positions is the token that
+// moves to position r.
+//
+// Two launches.  The first, a CTA to each sequence and KV head, brings the
+// weights into shared memory (they are needed up to four times: three passes of
+// the radix selection, one of the list), cuts and lists them, and moves the
+// weights themselves.  The second moves K and V: a kept position is never before
+// its place (the list ascends), so a CTA that loads a run of rows, meets, stores
+// it and goes on to the next run overwrites no row that is still to be read, and
+// CTAs that take different columns of the rows need not know of one another.
+// Bound by the moved rows' bytes, read and written once.
+#include <algorithm>
+
+#include "cut.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace decattn {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kCachedTokens = 53248;  // weights that shared memory holds (208 KB)
+
+__global__ void __launch_bounds__(kThreads) evict_rank_kernel(const EvictParams p) {
+  extern __shared__ float cached[];
+  __shared__ union {
+    CutScratch cut;
+    ListScratch<kThreads> list;
+  } sm;
+  const int j = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
+  const int lg = p.log2_block_size, in_block = p.block_size - 1;
+  int32_t* kept = p.kept + (static_cast<int64_t>(b) * p.h_kv + j) * p.keep;
+  const int n = p.seq_lens[b];
+  const int32_t* bt = p.block_table + static_cast<int64_t>(b) * p.max_blocks_per_seq;
+  bool stays = n <= p.limit;
+  if (n < 0 || n > p.max_seq_len) {
+    if (tid == 0 && j == 0) flag_error(p.err_flag, kFlagBadSeqLen);
+    stays = true;
+  }
+  float* weights = p.weights + static_cast<int64_t>(j) * p.block_size;
+  const int64_t block_stride = static_cast<int64_t>(p.h_kv) * p.block_size;
+  auto slot = [&](int t) { return weights + bt[t >> lg] * block_stride + (t & in_block); };
+  const bool cache = n <= p.cached_tokens;
+  if (!stays) {
+    int bad = 0;
+#pragma unroll 4
+    for (int t = tid; t < n; t += kThreads) {
+      const int id = bt[t >> lg];
+      const bool wrong = id < 0 || id >= p.num_blocks;
+      bad |= wrong;
+      if (cache && !wrong) cached[t] = weights[id * block_stride + (t & in_block)];
+    }
+    if (__syncthreads_or(bad)) {
+      if (tid == 0) flag_error(p.err_flag, kFlagBadBlock);
+      stays = true;
+    }
+  }
+  if (stays) {
+    for (int r = tid; r < p.keep; r += kThreads) kept[r] = -1;
+    if (tid == 0 && j == 0) p.new_lens[b] = 0;
+    return;
+  }
+  const int old = n - p.recent, heavy = p.keep - p.recent;
+  auto weight = [&](int t) { return cache ? cached[t] : *slot(t); };
+  if (heavy > 0) {
+    const Cut c = cut_largest<kThreads>(sm.cut, old, heavy, [&](int t, uint32_t& k) {
+      k = order_key(weight(t));
+      return true;
+    });
+    list_in_order<kThreads>(sm.list, old, c.ties, [&](int t) {
+      const uint32_t k = order_key(weight(t));
+      return k > c.key ? 1 : k == c.key ? 2 : 0;
+    }, [&](int t, int r) {
+      kept[r] = t;
+      if (cache) *slot(r) = cached[t];
+    });
+  }
+  for (int i = tid; i < p.recent; i += kThreads) {
+    kept[heavy + i] = old + i;
+    if (cache) *slot(heavy + i) = cached[old + i];
+  }
+  if (tid == 0 && j == 0) p.new_lens[b] = p.keep - n;
+  if (!cache) {  // in runs, as the rows are moved
+    __syncthreads();
+    for (int r0 = 0; r0 < p.keep; r0 += kThreads) {
+      const int r = r0 + tid;
+      const float w = r < p.keep ? *slot(kept[r]) : 0.f;
+      __syncthreads();
+      if (r < p.keep) *slot(r) = w;
+    }
+  }
+}
+
+constexpr int kMoveThreads = 256;
+constexpr int kAhead = 8;  // 16-byte pieces a thread holds
+
+// A CTA moves a run of columns (`pieces` 16-byte pieces of a head's row) of K or V.
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams p, int lg_pieces) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the list is there
+  const int j = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
+  const int32_t* kept = p.kept + (static_cast<int64_t>(b) * p.h_kv + j) * p.keep;
+  if (kept[0] < 0) return;  // nothing is evicted
+  const int parts = gridDim.x / 2;
+  const bool is_v = static_cast<int>(blockIdx.x) >= parts;
+  const int part = blockIdx.x - (is_v ? parts : 0);
+  const int lg = p.log2_block_size, in_block = p.block_size - 1;
+  const int64_t row_bytes = static_cast<int64_t>(p.h_kv) * p.head_bytes;
+  const int piece = tid & ((1 << lg_pieces) - 1), row = tid >> lg_pieces;
+  uint8_t* cache = (is_v ? p.v_cache : p.k_cache) + j * p.head_bytes + ((part << lg_pieces) + piece) * 16;
+  const int32_t* bt = p.block_table + static_cast<int64_t>(b) * p.max_blocks_per_seq;
+  auto place = [&](int t) {
+    return reinterpret_cast<uint4*>(cache + (static_cast<int64_t>(bt[t >> lg]) * p.block_size +
+                                             (t & in_block)) * row_bytes);
+  };
+  const int step = kMoveThreads >> lg_pieces;  // rows of one load
+  for (int r0 = 0; r0 < p.keep; r0 += step * kAhead) {
+    uint4 x[kAhead];
+    int from[kAhead];
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      const int r = r0 + a * step + row;
+      from[a] = r < p.keep ? kept[r] : r;
+      if (from[a] != r) x[a] = *place(from[a]);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      const int r = r0 + a * step + row;
+      if (from[a] != r) *place(r) = x[a];
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_kv_evict(EvictParams p, int num_sms, cudaStream_t stream) {
+  p.cached_tokens = std::min(p.max_seq_len, kCachedTokens);
+  const size_t smem = static_cast<size_t>(p.cached_tokens) * sizeof(float);
+  if (smem > 36 * 1024) {  // (beside static shared memory, of 48 KB)
+    const cudaError_t e =
+        cudaFuncSetAttribute(evict_rank_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kCachedTokens * static_cast<int>(sizeof(float)));
+    if (e != cudaSuccess) return e;
+  }
+  const dim3 units(static_cast<unsigned>(p.h_kv), static_cast<unsigned>(p.batch));
+  evict_rank_kernel<<<units, kThreads, smem, stream>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // 64 bytes of a row to a CTA, or 32 where that fills no wave.
+  const int64_t rows = static_cast<int64_t>(p.batch) * p.h_kv * 2;
+  const int lg_pieces = rows * (p.head_bytes / 64) < num_sms * 4 ? 1 : 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * (p.head_bytes >> (4 + lg_pieces))),
+                     static_cast<unsigned>(p.h_kv), static_cast<unsigned>(p.batch));
+  cfg.blockDim = dim3(kMoveThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, evict_move_kernel, p, lg_pieces);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace decattn

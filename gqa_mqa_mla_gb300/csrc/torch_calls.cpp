@@ -33,7 +33,11 @@ using at::Tensor;
   X(gqa_prefill_fp8kv) X(gqa_prefill_plan_splits) X(gqa_prefill_workspace_size)              \
   X(gqa_decode) X(gqa_decode_fp8kv) X(gqa_decode_window) X(gqa_decode_fp8kv_window)          \
   X(gqa_decode_sinks) X(gqa_decode_fp8kv_sinks) X(gqa_decode_plan_splits)                    \
-  X(gqa_decode_fp8kv_plan_splits) X(gqa_decode_sinks_plan_splits) X(gqa_decode_workspace_size)
+  X(gqa_decode_fp8kv_plan_splits) X(gqa_decode_sinks_plan_splits)                            \
+  X(gqa_decode_workspace_size) X(gqa_decode_blocks) X(gqa_decode_fp8kv_blocks)               \
+  X(gqa_decode_blocks_plan_splits) X(gqa_decode_weights) X(gqa_decode_fp8kv_weights)         \
+  X(gqa_decode_weights_workspace_size) X(gqa_block_bounds) X(gqa_select_blocks)              \
+  X(gqa_select_workspace_size) X(gqa_kv_evict)
 struct Library {
 #define DECATTN_FIELD(name) decltype(&::name) name = nullptr;
   DECATTN_CALLS(DECATTN_FIELD)
@@ -514,6 +518,307 @@ PyObject* decode(PyObject* const* a, Py_ssize_t n) {
   return st != DECATTN_OK ? status(st) : THPVariable_Wrap(out);
 }
 
+// decode_blocks(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
+//   selected, scale, max_seq_len, num_splits, out, workspace, err_flag, stream): out.
+PyObject* decode_blocks(PyObject* const* a, Py_ssize_t n) {
+  count(n, 15);
+  const Attention x(a, true);
+  const Tensor& selected = check(a[7], "selected", ScalarType::Int, 3);
+  const int B = size32(*x.q, 0), most = size32(selected, 2);
+  if (selected.size(0) < B || selected.size(1) != x.h_kv)
+    value_error("selected must be [" + std::to_string(B) + ", " + std::to_string(x.h_kv) +
+                ", count], got shape " + shape_of(selected));
+  same_device(x.index, selected, "selected");
+  const float scale = static_cast<float>(as_double(a[8], "scale"));
+  const int max_len = as_int(a[9], "max_seq_len");
+  decattn_launch L = x.launch(B, max_len, a[13], a[14]);
+  L.num_splits = as_int(a[10], "num_splits");
+  Tensor out = x.output(a[11], false), ws = x.workspace(a[12]);
+  const void *q = x.q->data_ptr(), *kc = x.kc->data_ptr(), *vc = x.vc->data_ptr();
+  const int *bt = x.table->data_ptr<int>(), *sl = x.lens->data_ptr<int>();
+  const int* some = selected.data_ptr<int>();
+  const bool given = !none(a[14]);
+  const int st = [&] {
+    const Unlocked unlocked;
+    const OnStream guard(x.index, given, L.stream);
+    if (L.num_splits == 0) {
+      const int ns = lib.gqa_decode_blocks_plan_splits(B, x.h_q, x.h_kv, x.d, max_len, most,
+                                                       L.block_size, x.fp8 ? 1 : 2, 0);
+      if (ns < 0) return ns;
+      L.num_splits = ns;
+    }
+    const int ns = L.num_splits;
+    void* o = x.allocate(guard, out, ws,
+                         ns > 1 ? lib.gqa_decode_workspace_size(B, x.h_q, x.d, ns) : 0, L);
+    return x.fp8 ? lib.gqa_decode_fp8kv_blocks(q, kc, vc, x.sk, x.sv, bt, sl, some, o, x.h_q,
+                                               x.h_kv, x.d, scale, most, &L)
+                 : lib.gqa_decode_blocks(q, kc, vc, bt, sl, some, o, x.h_q, x.h_kv, x.d, scale,
+                                         most, &L);
+  }();
+  return st != DECATTN_OK ? status(st) : THPVariable_Wrap(out);
+}
+
+// A cache's weights: float32 [num_blocks, h_kv, block_size].
+const Tensor& check_weights(PyObject* o, const Tensor& cache, int index) {
+  const Tensor& t = check(o, "weights", ScalarType::Float, 3);
+  if (t.size(0) != cache.size(0) || t.size(1) != cache.size(2) || t.size(2) != cache.size(1))
+    value_error("weights must be [num_blocks, h_kv, block_size], got shape " + shape_of(t));
+  same_device(index, t, "weights");
+  return t;
+}
+
+// decode_weights(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens,
+//   weights, weighed_lens or None, scale, decay, max_seq_len, num_splits, out,
+//   workspace, err_flag, stream): out.
+PyObject* decode_weights(PyObject* const* a, Py_ssize_t n) {
+  count(n, 17);
+  const Attention x(a, true);
+  const Tensor& weights = check_weights(a[7], *x.kc, x.index);
+  const int B = size32(*x.q, 0);
+  const int* weighed = nullptr;
+  if (!none(a[8])) {
+    const Tensor& t = check(a[8], "weighed_lens", ScalarType::Int, 1);
+    if (t.size(0) < B) value_error("weighed_lens needs an entry for each row of q");
+    same_device(x.index, t, "weighed_lens");
+    weighed = t.data_ptr<int>();
+  }
+  const float scale = static_cast<float>(as_double(a[9], "scale"));
+  const float decay = static_cast<float>(as_double(a[10], "decay"));
+  const int max_len = as_int(a[11], "max_seq_len");
+  decattn_launch L = x.launch(B, max_len, a[15], a[16]);
+  L.num_splits = as_int(a[12], "num_splits");
+  Tensor out = x.output(a[13], false), ws = x.workspace(a[14]);
+  const void *q = x.q->data_ptr(), *kc = x.kc->data_ptr(), *vc = x.vc->data_ptr();
+  const int *bt = x.table->data_ptr<int>(), *sl = x.lens->data_ptr<int>();
+  float* w = weights.data_ptr<float>();
+  const bool given = !none(a[16]);
+  const int st = [&] {
+    const Unlocked unlocked;
+    const OnStream guard(x.index, given, L.stream);
+    if (L.num_splits == 0) {
+      const int ns = x.fp8 ? lib.gqa_decode_fp8kv_plan_splits(B, x.h_q, x.h_kv, x.d, max_len, 0)
+                           : lib.gqa_decode_plan_splits(B, x.h_q, x.h_kv, x.d, max_len, 0);
+      if (ns < 0) return ns;
+      L.num_splits = ns;
+    }
+    void* o = x.allocate(
+        guard, out, ws,
+        lib.gqa_decode_weights_workspace_size(B, x.h_q, x.d, max_len, L.num_splits), L);
+    return x.fp8 ? lib.gqa_decode_fp8kv_weights(q, kc, vc, x.sk, x.sv, bt, sl, weighed, w, o,
+                                                x.h_q, x.h_kv, x.d, scale, decay, &L)
+                 : lib.gqa_decode_weights(q, kc, vc, bt, sl, weighed, w, o, x.h_q, x.h_kv, x.d,
+                                          scale, decay, &L);
+  }();
+  return st != DECATTN_OK ? status(st) : THPVariable_Wrap(out);
+}
+
+// A cache (or its bounds) of any of the library's types, and how it is numbered.
+struct Kind {
+  int bytes, dtype;
+};
+Kind kind_of(const Tensor& t, const char* name) {
+  switch (t.scalar_type()) {
+    case ScalarType::Half: return {2, DECATTN_FP16};
+    case ScalarType::BFloat16: return {2, DECATTN_BF16};
+    case ScalarType::Byte:
+    case ScalarType::Float8_e4m3fn: return {1, DECATTN_BF16};
+    default:
+      type_error(std::string(name) + " must be float16, bfloat16, float8_e4m3fn or uint8");
+  }
+}
+
+// block_table [B, max_blocks] and seq_lens [B] of a call without a query.
+void check_lists(const Tensor& table, const Tensor& lens, int index) {
+  if (table.size(0) != lens.size(0))
+    value_error("block_table must have a row for each of the " + std::to_string(lens.size(0)) +
+                " sequences, got " + std::to_string(table.size(0)));
+  same_device(index, table, "block_table");
+  same_device(index, lens, "seq_lens");
+}
+
+// block_bounds(k_cache, block_table, seq_lens, bounds, first_lens or None,
+//   max_seq_len, err_flag, stream): bounds.
+PyObject* block_bounds(PyObject* const* a, Py_ssize_t n) {
+  count(n, 8);
+  const Tensor& k = tensor(a[0], "k_cache");
+  const Kind kind = kind_of(k, "k_cache");
+  check(a[0], "k_cache", k.scalar_type(), 4);
+  const Tensor& table = check(a[1], "block_table", ScalarType::Int, 2);
+  const Tensor& lens = check(a[2], "seq_lens", ScalarType::Int, 1);
+  const Tensor& bounds = tensor(a[3], "bounds");
+  if (kind_of(bounds, "bounds").bytes != kind.bytes ||
+      (kind.bytes == 2 && bounds.scalar_type() != k.scalar_type()))
+    type_error("bounds must be of k_cache's type");
+  check(a[3], "bounds", bounds.scalar_type(), 4);
+  if (bounds.size(0) != k.size(0) || bounds.size(1) != 2 || bounds.size(2) != k.size(2) ||
+      bounds.size(3) != k.size(3))
+    value_error("bounds must be [num_blocks, 2, h_kv, d], got shape " + shape_of(bounds));
+  const int index = cuda_index(k);
+  check_lists(table, lens, index);
+  same_device(index, bounds, "bounds");
+  const int* first = nullptr;
+  if (!none(a[4])) {
+    const Tensor& t = check(a[4], "first_lens", ScalarType::Int, 1);
+    if (t.size(0) != lens.size(0)) value_error("first_lens must have seq_lens' shape");
+    same_device(index, t, "first_lens");
+    first = t.data_ptr<int>();
+  }
+  decattn_launch L = {};
+  L.batch = size32(lens, 0);
+  L.num_blocks = size32(k, 0);
+  L.block_size = size32(k, 1);
+  L.max_blocks_per_seq = size32(table, 1);
+  L.max_seq_len = as_int(a[5], "max_seq_len");
+  L.dtype = kind.dtype;
+  L.err_flag = flag_of(a[6], index);
+  L.stream = stream_of(a[7], index);
+  const bool given = !none(a[7]);
+  const int h_kv = size32(k, 2), d = size32(k, 3);
+  const void* kp = k.data_ptr();
+  void* bp = bounds.data_ptr();
+  const int *bt = table.data_ptr<int>(), *sl = lens.data_ptr<int>();
+  const int st = [&] {
+    const Unlocked unlocked;
+    const OnStream guard(index, given, L.stream);
+    return lib.gqa_block_bounds(kp, bt, first, sl, bp, h_kv, d, kind.bytes, &L);
+  }();
+  return st != DECATTN_OK ? status(st) : THPVariable_Wrap(bounds);
+}
+
+// select_blocks(q, bounds, block_table, seq_lens, block_size, max_seq_len,
+//   count, first, last, out, workspace, err_flag, stream): selected.
+PyObject* select_blocks(PyObject* const* a, Py_ssize_t n) {
+  count(n, 13);
+  const Tensor& q = tensor(a[0], "q");
+  const int dtype = dtype16(q, "q");
+  check(a[0], "q", q.scalar_type(), 3);
+  const Tensor& bounds = tensor(a[1], "bounds");
+  const Kind kind = kind_of(bounds, "bounds");
+  check(a[1], "bounds", kind.bytes == 2 ? q.scalar_type() : bounds.scalar_type(), 4);
+  const Tensor& table = check(a[2], "block_table", ScalarType::Int, 2);
+  const Tensor& lens = check(a[3], "seq_lens", ScalarType::Int, 1);
+  const int B = size32(q, 0), h_q = size32(q, 1), d = size32(q, 2), h_kv = size32(bounds, 2);
+  if (bounds.size(1) != 2 || bounds.size(3) != d)
+    value_error("bounds must be [num_blocks, 2, h_kv, d], got shape " + shape_of(bounds));
+  if (table.size(0) < B || lens.size(0) < B)
+    value_error("block_table and seq_lens need an entry for each of the " + std::to_string(B) +
+                " rows of q, got " + std::to_string(table.size(0)) + " and " +
+                std::to_string(lens.size(0)));
+  if (h_kv < 1 || h_q % h_kv != 0)
+    value_error("h_q=" + std::to_string(h_q) + " is not a multiple of h_kv=" + std::to_string(h_kv));
+  const int index = cuda_index(q);
+  same_device(index, bounds, "bounds");
+  same_device(index, table, "block_table");
+  same_device(index, lens, "seq_lens");
+  decattn_launch L = {};
+  L.batch = B;
+  L.num_blocks = size32(bounds, 0);
+  L.block_size = as_int(a[4], "block_size");
+  L.max_blocks_per_seq = size32(table, 1);
+  L.max_seq_len = as_int(a[5], "max_seq_len");
+  L.dtype = dtype;
+  L.err_flag = flag_of(a[11], index);
+  L.stream = stream_of(a[12], index);
+  const int most = as_int(a[6], "count"), first = as_int(a[7], "first"),
+            last = as_int(a[8], "last");
+  if (most < 1) value_error("count must be at least 1");
+  Tensor out, ws;
+  if (!none(a[9])) {
+    out = check(a[9], "out", ScalarType::Int, 3);
+    if (out.size(0) != B || out.size(1) != h_kv || out.size(2) != most)
+      value_error("out must be [" + std::to_string(B) + ", " + std::to_string(h_kv) + ", " +
+                  std::to_string(most) + "], got shape " + shape_of(out));
+    same_device(index, out, "out");
+  }
+  if (!none(a[10])) {
+    ws = tensor(a[10], "workspace");
+    if (!ws.is_non_overlapping_and_dense()) value_error("workspace must be dense");
+    same_device(index, ws, "workspace");
+  }
+  const bool given = !none(a[12]);
+  const void *qp = q.data_ptr(), *bp = bounds.data_ptr();
+  const int *bt = table.data_ptr<int>(), *sl = lens.data_ptr<int>();
+  const int st = [&] {
+    const Unlocked unlocked;
+    const OnStream guard(index, given, L.stream);
+    if (!out.defined())
+      out = guard.result({B, h_kv, most}, q.options().dtype(ScalarType::Int));
+    const size_t need =
+        lib.gqa_select_workspace_size(B, h_kv, L.max_seq_len, L.block_size, most);
+    if (!ws.defined() && need)
+      ws = at::empty({static_cast<int64_t>(need)}, q.options().dtype(ScalarType::Byte));
+    if (ws.defined()) {
+      L.workspace = ws.data_ptr();
+      L.workspace_bytes = ws.nbytes();
+    }
+    return lib.gqa_select_blocks(qp, bp, bt, sl, out.data_ptr<int>(), h_q, h_kv, d, kind.bytes,
+                                 most, first, last, &L);
+  }();
+  return st != DECATTN_OK ? status(st) : THPVariable_Wrap(out);
+}
+
+// kv_evict(k_cache, v_cache, weights, block_table, seq_lens, max_seq_len, keep,
+//   recent, limit, new_lens, kept, err_flag, stream): (new_lens, kept).
+PyObject* kv_evict(PyObject* const* a, Py_ssize_t n) {
+  count(n, 13);
+  const Tensor& k = tensor(a[0], "k_cache");
+  const Kind kind = kind_of(k, "k_cache");
+  check(a[0], "k_cache", k.scalar_type(), 4);
+  const Tensor& v = check(a[1], "v_cache", k.scalar_type(), 4);
+  if (v.sizes() != k.sizes()) value_error("k_cache / v_cache shape mismatch");
+  const int index = cuda_index(k);
+  same_device(index, v, "v_cache");
+  const Tensor& weights = check_weights(a[2], k, index);
+  const Tensor& table = check(a[3], "block_table", ScalarType::Int, 2);
+  const Tensor& lens = check(a[4], "seq_lens", ScalarType::Int, 1);
+  check_lists(table, lens, index);
+  decattn_launch L = {};
+  const int B = L.batch = size32(lens, 0);
+  L.num_blocks = size32(k, 0);
+  L.block_size = size32(k, 1);
+  L.max_blocks_per_seq = size32(table, 1);
+  L.max_seq_len = as_int(a[5], "max_seq_len");
+  L.dtype = kind.dtype;
+  L.err_flag = flag_of(a[11], index);
+  L.stream = stream_of(a[12], index);
+  const int keep = as_int(a[6], "keep"), recent = as_int(a[7], "recent"),
+            limit = as_int(a[8], "limit"), h_kv = size32(k, 2), d = size32(k, 3);
+  if (keep < 1) value_error("keep must be at least 1");
+  Tensor moved, kept;
+  if (!none(a[9])) {
+    moved = check(a[9], "new_lens", ScalarType::Int, 1);
+    if (moved.size(0) != B) value_error("new_lens must be [" + std::to_string(B) + "]");
+    same_device(index, moved, "new_lens");
+  }
+  if (!none(a[10])) {
+    kept = check(a[10], "kept", ScalarType::Int, 3);
+    if (kept.size(0) != B || kept.size(1) != h_kv || kept.size(2) != keep)
+      value_error("kept must be [" + std::to_string(B) + ", " + std::to_string(h_kv) + ", " +
+                  std::to_string(keep) + "], got shape " + shape_of(kept));
+    same_device(index, kept, "kept");
+  }
+  const bool given = !none(a[12]);
+  void *kp = k.data_ptr(), *vp = v.data_ptr();
+  float* w = weights.data_ptr<float>();
+  const int *bt = table.data_ptr<int>(), *sl = lens.data_ptr<int>();
+  const int st = [&] {
+    const Unlocked unlocked;
+    const OnStream guard(index, given, L.stream);
+    const at::TensorOptions i32 = weights.options().dtype(ScalarType::Int);
+    if (!moved.defined()) moved = guard.result({B}, i32);
+    if (!kept.defined()) kept = guard.result({B, h_kv, keep}, i32);
+    return lib.gqa_kv_evict(kp, vp, w, bt, sl, moved.data_ptr<int>(), kept.data_ptr<int>(), h_kv,
+                            d, kind.bytes, keep, recent, limit, &L);
+  }();
+  if (st != DECATTN_OK) return status(st);
+  PyObject* r = PyTuple_New(2);
+  if (r) {
+    PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(moved));
+    PyTuple_SET_ITEM(r, 1, THPVariable_Wrap(kept));
+  }
+  return r;
+}
+
 // prefill(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, q_start,
 //   scale, max_q_len, max_seq_len, window (0: none), sinks, num_splits, out,
 //   workspace, err_flag, stream): out.
@@ -577,7 +882,11 @@ PyMethodDef method(const char* name) {
 
 PyMethodDef methods[] = {method<open_library>("open"), method<paged_plan>("paged_plan"),
                          method<rope_append>("rope_append"), method<decode>("decode"),
-                         method<prefill>("prefill"), {nullptr, nullptr, 0, nullptr}};
+                         method<prefill>("prefill"), method<decode_blocks>("decode_blocks"),
+                         method<decode_weights>("decode_weights"),
+                         method<block_bounds>("block_bounds"),
+                         method<select_blocks>("select_blocks"),
+                         method<kv_evict>("kv_evict"), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods};
 
 }  // namespace

@@ -458,6 +458,142 @@ int gqa_prefill_plan_splits(int batch, int tokens, int max_q_len, int h_q, int h
 size_t gqa_prefill_workspace_size(int tokens, int h_q, int d_head, int num_splits);
 
 /*
+ * gqa_block_bounds -- per-block bounds of the cached keys, for gqa_select_blocks:
+ *   k_cache      as gqa_decode's (kv_bytes = 2) or gqa_decode_fp8kv's (1)
+ *   first_lens   [batch] int32, or NULL: each sequence's tokens whose blocks are
+ *                up to date (its length before the step); NULL: none
+ *   seq_lens     [batch] int32: tokens in the cache
+ *   bounds       [num_blocks, 2, h_kv, d_head] in the cache's type (8-bit: codes):
+ *                bounds[id][0] the smallest and [1] the largest key of block id's
+ *                tokens, for each KV head and dimension; NaN in both where one of
+ *                them is NaN.  Updated: the blocks that hold positions
+ *                first_lens[b] .. seq_lens[b] - 1, or, where there are none (tokens
+ *                were given back), the sequence's last block.  Such a block is
+ *                taken anew from all of its tokens; others are not touched.
+ * seq_lens[b] = 0 does nothing.  A length outside [0, max_seq_len] or a negative
+ * first_lens[b] sets DECATTN_FLAG_BAD_SEQ_LEN (that sequence is left out), a bad
+ * block id DECATTN_FLAG_BAD_BLOCK (that block is).  Sequences may share blocks
+ * whose tokens are the same.
+ */
+int gqa_block_bounds(const void* k_cache, const int32_t* block_table, const int32_t* first_lens,
+                     const int32_t* seq_lens, void* bounds, int h_kv, int d_head, int kv_bytes,
+                     const decattn_launch* launch);
+
+/*
+ * gqa_select_blocks -- the blocks of each sequence's cache that matter most to
+ * its query, per KV head, for gqa_decode_blocks.
+ *   q            [batch, h_q, d_head] fp16/bf16 (launch->dtype), h_q / h_kv <= 64
+ *   bounds       gqa_block_bounds' (kv_bytes 2: in launch->dtype; 1: e4m3 codes)
+ *   selected     [batch, h_kv, count] int32 (written): block numbers within the
+ *                sequence (0 is its first block), ascending, -1 behind the last
+ *   first, last  how many of the sequence's first and last blocks are always
+ *                among the count (first + last <= count)
+ * A sequence of at most count blocks gets all of them.  Otherwise the other
+ * count - first - last are those with the largest
+ *     max over the heads i of the group of sum_d max(q_id lo_d, q_id hi_d),
+ * an upper bound of q_i . k over the block's keys, in the order of these sums in 64
+ * bits (the earlier block where they are equal; NaN counts as +inf).  (An 8-bit
+ * cache's k_scale, positive, does not change the order.)
+ * A bad length (DECATTN_FLAG_BAD_SEQ_LEN) or block id (DECATTN_FLAG_BAD_BLOCK)
+ * gives a list of -1.  max_seq_len sizes the workspace
+ * (gqa_select_workspace_size; 0 bytes where no sequence can have more than count
+ * blocks); num_splits is not used.
+ */
+int gqa_select_blocks(const void* q, const void* bounds, const int32_t* block_table,
+                      const int32_t* seq_lens, int32_t* selected, int h_q, int h_kv, int d_head,
+                      int kv_bytes, int count, int first, int last, const decattn_launch* launch);
+size_t gqa_select_workspace_size(int batch, int h_kv, int max_seq_len, int block_size, int count);
+
+/*
+ * gqa_decode_blocks, gqa_decode_fp8kv_blocks -- gqa_decode (resp.
+ * gqa_decode_fp8kv) over some of the cache's blocks: KV head j's query heads of
+ * sequence b attend to the tokens (before seq_lens[b]) of the blocks that
+ * selected[b][j] lists, and to no others.
+ *   selected     [batch, h_kv, count] int32 (gqa_select_blocks', or any): block
+ *                numbers within the sequence, ascending, each once; the first
+ *                negative entry ends the list
+ * An empty list gives zero rows.  A list that does not ascend, goes on behind a
+ * negative entry or names a block past the sequence's last sets
+ * DECATTN_FLAG_BAD_BLOCK and gives that sequence and KV head zero rows.  Blocks
+ * that are not listed are never read and their block_table entries never
+ * checked.  Every other argument, layout, status and the workspace rule as
+ * gqa_decode; num_splits = 0 takes gqa_decode_blocks_plan_splits' count (the
+ * rule of gqa_decode_sinks for min(max_seq_len, count block_size) tokens).
+ */
+int gqa_decode_blocks(const void* q, const void* k_cache, const void* v_cache,
+                      const int32_t* block_table, const int32_t* seq_lens,
+                      const int32_t* selected, void* out, int h_q, int h_kv, int d_head,
+                      float scale, int count, const decattn_launch* launch);
+int gqa_decode_fp8kv_blocks(const void* q, const void* k_cache, const void* v_cache,
+                            const float* k_scale, const float* v_scale,
+                            const int32_t* block_table, const int32_t* seq_lens,
+                            const int32_t* selected, void* out, int h_q, int h_kv, int d_head,
+                            float scale, int count, const decattn_launch* launch);
+int gqa_decode_blocks_plan_splits(int batch, int h_q, int h_kv, int d_head, int max_seq_len,
+                                  int count, int block_size, int kv_bytes, int num_sms);
+
+/*
+ * gqa_decode_weights, gqa_decode_fp8kv_weights -- gqa_decode (resp.
+ * gqa_decode_fp8kv) that keeps account of how much attention each cached token
+ * gets, for gqa_kv_evict:
+ *   weights      [num_blocks, h_kv, block_size] fp32 (updated), 16-byte aligned:
+ *                for each token t < seq_lens[b] in its slot, with p the softmax
+ *                of query head i,
+ *                  w = (t < weighed_lens[b] ? decay * w : 0)
+ *                      + sum over the heads i of the KV head of p_it
+ *                in fp32, always in the same order; no other slot is written
+ *   weighed_lens [batch] int32, or NULL: the tokens whose slots hold weights
+ *                already (the others' begin at 0); NULL: all but the last token
+ *   decay        finite; 1 adds up, less forgets
+ * A row of zeros (no score but -inf) has no weights to add; a NaN row's are
+ * NaN.  A sequence with bad data (zero rows) keeps its weights.  Sequences must not
+ * share blocks (the weights of a shared one are unspecified).  Workspace:
+ * gqa_decode_weights_workspace_size, for any number of splits; the scores, 4
+ * bytes a query head and token, are most of it.
+ */
+int gqa_decode_weights(const void* q, const void* k_cache, const void* v_cache,
+                       const int32_t* block_table, const int32_t* seq_lens,
+                       const int32_t* weighed_lens, float* weights, void* out, int h_q, int h_kv,
+                       int d_head, float scale, float decay, const decattn_launch* launch);
+int gqa_decode_fp8kv_weights(const void* q, const void* k_cache, const void* v_cache,
+                             const float* k_scale, const float* v_scale,
+                             const int32_t* block_table, const int32_t* seq_lens,
+                             const int32_t* weighed_lens, float* weights, void* out, int h_q,
+                             int h_kv, int d_head, float scale, float decay,
+                             const decattn_launch* launch);
+size_t gqa_decode_weights_workspace_size(int batch, int h_q, int d_head, int max_seq_len,
+                                         int num_splits);
+
+/*
+ * gqa_kv_evict -- sequences that have grown past a limit keep their heaviest and
+ * latest tokens, moved to the front of their blocks.
+ *   k_cache, v_cache  as gqa_decode's (kv_bytes = 2) or gqa_decode_fp8kv's (1)
+ *                (updated)
+ *   weights      gqa_decode_weights' (updated: a token's weight moves with it)
+ *   seq_lens     [batch] int32: tokens in the cache
+ *   new_lens     [batch] int32 (written): keep - seq_lens[b] where the sequence is
+ *                longer than limit, else 0: what paged_plan takes as new_lens to
+ *                give the freed blocks back.  Must not be seq_lens
+ *   kept         [batch, h_kv, keep] int32 (written): entry r is the position that
+ *                KV head j's token now at position r had; -1 where nothing is
+ *                evicted
+ *   keep, recent, limit  1 <= keep <= limit, 0 <= recent <= keep
+ * Of a sequence of n > limit tokens each KV head keeps the last `recent` and, of
+ * the others, the keep - recent with the largest weights (the earlier token where
+ * they are equal; NaN is the largest), in their order.  KV heads choose for
+ * themselves, so that one position may then hold different tokens' rows; keys
+ * are moved as they are, with the rotation of the position that they had.  Slots
+ * from position keep on are left as they were.  The bounds of the blocks
+ * (gqa_block_bounds) have to be taken anew.
+ * A bad length (DECATTN_FLAG_BAD_SEQ_LEN) or block id (DECATTN_FLAG_BAD_BLOCK)
+ * leaves the sequence as it is (new_lens 0).  Sequences that are evicted from must
+ * not share blocks.  The caches, weights and outputs must not overlap.
+ */
+int gqa_kv_evict(void* k_cache, void* v_cache, float* weights, const int32_t* block_table,
+                 const int32_t* seq_lens, int32_t* new_lens, int32_t* kept, int h_kv, int d_head,
+                 int kv_bytes, int keep, int recent, int limit, const decattn_launch* launch);
+
+/*
  * mla_absorb_q, mla_unabsorb_out -- the two GEMMs either side of mla_decode
  * ("MQA, GQA, and MLA", section 5: q_i . k_i = x (W_q^(i) W_uk^(i)^T) c^T, so
  * the query is multiplied by W_uk^(i)^T once and the scores are taken
