@@ -151,10 +151,11 @@ struct CcConsumer {
       // Both half-warps hold their eight scores in every lane: lane i keeps the i-th.
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        float x = s[0][g];
-#pragma unroll
-        for (int i = 1; i < 8; ++i) x = chunk == i ? s[i][g] : x;
-        if (chunk < 8) keep[g * ld + cw * 16 + 2 * chunk + half] = x;
+        const bool b0 = chunk & 1, b1 = chunk & 2, b2 = chunk & 4;
+        const float x01 = b0 ? s[1][g] : s[0][g], x23 = b0 ? s[3][g] : s[2][g];
+        const float x45 = b0 ? s[5][g] : s[4][g], x67 = b0 ? s[7][g] : s[6][g];
+        const float x03 = b1 ? x23 : x01, x47 = b1 ? x67 : x45;
+        if (chunk < 8) keep[g * ld + cw * 16 + 2 * chunk + half] = b2 ? x47 : x03;
       }
     }
 #pragma unroll
@@ -482,10 +483,11 @@ struct CcConsumerF8 {
       // Both half-warps hold their eight scores in every lane: lane i keeps the i-th.
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        float x = s[0][g];
-#pragma unroll
-        for (int i = 1; i < 8; ++i) x = chunk == i ? s[i][g] : x;
-        if (chunk < 8) keep[g * ld + cw * 16 + 2 * chunk + half] = x;
+        const bool b0 = chunk & 1, b1 = chunk & 2, b2 = chunk & 4;
+        const float x01 = b0 ? s[1][g] : s[0][g], x23 = b0 ? s[3][g] : s[2][g];
+        const float x45 = b0 ? s[5][g] : s[4][g], x67 = b0 ? s[7][g] : s[6][g];
+        const float x03 = b1 ? x23 : x01, x47 = b1 ? x67 : x45;
+        if (chunk < 8) keep[g * ld + cw * 16 + 2 * chunk + half] = b2 ? x47 : x03;
       }
     }
 #pragma unroll
@@ -1032,8 +1034,18 @@ __device__ __noinline__ void merge_splits(const GqaParams& p) {
   }
 }
 
+// Two CTAs of the tensor-core consumer share an SM up to 168 registers (three of the
+// ten warps may meet in one quarter of the register file).  With the scores kept
+// it takes 183 unless held to that, by the bound for a warp more and two CTAs.
+template <class Consumer, GqaForm kForm>
+struct Bound {
+  static constexpr bool kHeld = kForm == kWeighed && Consumer::kCacheBytes == 2 && Consumer::kRowsPerWarp == 16;
+  static constexpr int kThreads = 32 * (1 + Consumer::kWarps + (kHeld ? 1 : 0));
+  static constexpr int kBlocks = kHeld ? 2 : Consumer::kMinBlocks;
+};
+
 template <class Consumer, bool kBF16, int kStages, GqaForm kForm, bool kJoint>
-__global__ void __launch_bounds__(32 * (1 + Consumer::kWarps), Consumer::kMinBlocks)
+__global__ void __launch_bounds__(Bound<Consumer, kForm>::kThreads, Bound<Consumer, kForm>::kBlocks)
     gqa_partial_kernel(const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const GqaParams p) {
   gqa_partial<Consumer, kBF16, kStages, kForm>(tm_k, tm_v, p);

@@ -24,11 +24,11 @@
 namespace decattn {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 1024;
 constexpr int kCachedTokens = 53248;  // weights that shared memory holds (208 KB)
 
 __global__ void __launch_bounds__(kThreads) evict_rank_kernel(const EvictParams p) {
-  extern __shared__ float cached[];
+  extern __shared__ __align__(16) float cached[];
   __shared__ union {
     CutScratch cut;
     ListScratch<kThreads> list;
@@ -49,12 +49,15 @@ __global__ void __launch_bounds__(kThreads) evict_rank_kernel(const EvictParams 
   const bool cache = n <= p.cached_tokens;
   if (!stays) {
     int bad = 0;
+    // Four tokens (of one block) at a time, all of a thread's loads in flight.
 #pragma unroll 4
-    for (int t = tid; t < n; t += kThreads) {
+    for (int t = tid * 4; t < n; t += kThreads * 4) {
       const int id = bt[t >> lg];
       const bool wrong = id < 0 || id >= p.num_blocks;
       bad |= wrong;
-      if (cache && !wrong) cached[t] = weights[id * block_stride + (t & in_block)];
+      if (cache && !wrong)
+        *reinterpret_cast<float4*>(cached + t) =
+            *reinterpret_cast<const float4*>(weights + id * block_stride + (t & in_block));
     }
     if (__syncthreads_or(bad)) {
       if (tid == 0) flag_error(p.err_flag, kFlagBadBlock);
@@ -76,18 +79,15 @@ __global__ void __launch_bounds__(kThreads) evict_rank_kernel(const EvictParams 
     list_in_order<kThreads>(sm.list, old, c.ties, [&](int t) {
       const uint32_t k = order_key(weight(t));
       return k > c.key ? 1 : k == c.key ? 2 : 0;
-    }, [&](int t, int r) {
-      kept[r] = t;
-      if (cache) *slot(r) = cached[t];
-    });
+    }, [&](int t, int r) { kept[r] = t; });
   }
-  for (int i = tid; i < p.recent; i += kThreads) {
-    kept[heavy + i] = old + i;
-    if (cache) *slot(heavy + i) = cached[old + i];
-  }
+  for (int i = tid; i < p.recent; i += kThreads) kept[heavy + i] = old + i;
   if (tid == 0 && j == 0) p.new_lens[b] = p.keep - n;
-  if (!cache) {  // in runs, as the rows are moved
-    __syncthreads();
+  __syncthreads();
+  if (cache) {
+#pragma unroll 4
+    for (int r = tid; r < p.keep; r += kThreads) *slot(r) = cached[kept[r]];
+  } else {  // in runs, as the rows are moved
     for (int r0 = 0; r0 < p.keep; r0 += kThreads) {
       const int r = r0 + tid;
       const float w = r < p.keep ? *slot(kept[r]) : 0.f;
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
 
 cudaError_t launch_kv_evict(EvictParams p, int num_sms, cudaStream_t stream) {
   p.cached_tokens = std::min(p.max_seq_len, kCachedTokens);
-  const size_t smem = static_cast<size_t>(p.cached_tokens) * sizeof(float);
+  const size_t smem = (static_cast<size_t>(p.cached_tokens) + 3) / 4 * 4 * sizeof(float);
   if (smem > 36 * 1024) {  // (beside static shared memory, of 48 KB)
     const cudaError_t e =
         cudaFuncSetAttribute(evict_rank_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,

@@ -18,7 +18,7 @@
 //     E = 2^-16 max_i sum_d |q_id| max_td |bound_td|:
 // four chains of four products of 16 terms, each term off by at most 2^-23 of the
 // chain's sum of magnitudes (4 x 17 x 2^-23), and their sum.  The second kernel, a
-// CTA to each sequence and KV head, finds the cut v by radix selection; blocks
+// CTA to each sequence and KV head, finds the cut v (cut.cuh); blocks
 // within 2 E of it, usually none but the cut itself, are scored again in 64 bits.
 // Doing all in 64 bits would take 40 times the floor here: 0.6 T products a second.
 #include <algorithm>
@@ -215,8 +215,38 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const Se
 constexpr int kFew = 32;  // blocks near the cut that one warp can order
 constexpr int kCachedBlocks = 40960;  // scores that are kept in shared memory
 
-// s_t in 64 bits, by a warp: lane l has dims 4 l .. 4 l + 3.  The same value in
-// every lane; NaN counts as +inf.
+// A block's score from its definition, in 64 bits throughout: what values that are
+// not finite take.  lo, hi: the lane's dims 4 l .. 4 l + 3.
+template <bool kBF16>
+__device__ __noinline__ double score_of_strange_values(const uint16_t* q, int group,
+                                                       const float4 lo4, const float4 hi4) {
+  const float lo[4] = {lo4.x, lo4.y, lo4.z, lo4.w}, hi[4] = {hi4.x, hi4.y, hi4.z, hi4.w};
+  const double inf = __longlong_as_double(0x7ff0000000000000ll);
+  double best = -inf;
+  for (int r = 0; r < group; ++r) {
+    const uint2 w = *reinterpret_cast<const uint2*>(q + r * kHeadDim);
+    const float2 a = unpack2<kBF16>(w.x), c = unpack2<kBF16>(w.y);
+    const float x[4] = {a.x, a.y, c.x, c.y};
+    double sum = 0.0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const double u = static_cast<double>(x[k]) * lo[k], v = static_cast<double>(x[k]) * hi[k];
+      sum += u != u ? u : v != v ? v : u > v ? u : v;
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (sum != sum) sum = inf;
+    best = sum > best ? sum : best;
+  }
+  return best;
+}
+
+// s_t in 64 bits, by a warp; the same value in every lane, NaN counts as +inf.  A
+// product in 64 bits takes a warp 16 cycles here, so only the heads that may hold
+// the maximum are taken so: those within the 32-bit sums' error (a lane's four
+// products and sums, five more, each 2^-24 of the sum of magnitudes) of the
+// largest.  (All heads, and the definition's comparisons in 64 bits, took 18 us
+// for three blocks of 8 heads.)
 template <bool kF8, bool kBF16>
 DECATTN_DEV double exact_score(const SelectParams& p, int64_t bj, int j, int id, int lane) {
   const int64_t row = (static_cast<int64_t>(id) * 2 * p.h_kv + j) * kHeadDim + lane * 4;
@@ -237,22 +267,61 @@ DECATTN_DEV double exact_score(const SelectParams& p, int64_t bj, int j, int id,
     to[0] = a.x; to[1] = a.y; to[2] = c.x; to[3] = c.y;
   }
   const uint16_t* q = static_cast<const uint16_t*>(p.q) + bj * p.group * kHeadDim + lane * 4;
-  const double inf = __longlong_as_double(0x7ff0000000000000ll);
-  double best = -inf;
+  float up[4], down[4], sum_all = 0.f;  // what a positive, a negative value of q meets
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    up[k] = fmaxf(lo[k], hi[k]);
+    down[k] = fminf(lo[k], hi[k]);
+    sum_all += fabsf(lo[k]) + fabsf(hi[k]);
+  }
+  // Head r's 32-bit sum and its error stay with lane r % 32.
+  float sums[2] = {-kInf, -kInf}, errors[2] = {0.f, 0.f}, floor_ = -kInf;
+  bool finite = sum_all < kInf;
   for (int r = 0; r < p.group; ++r) {
     const uint2 w = *reinterpret_cast<const uint2*>(q + r * kHeadDim);
     const float2 a = unpack2<kBF16>(w.x), c = unpack2<kBF16>(w.y);
     const float x[4] = {a.x, a.y, c.x, c.y};
-    double sum = 0.0;
+    float s = 0.f, mag = 0.f;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const double u = static_cast<double>(x[k]) * lo[k], v = static_cast<double>(x[k]) * hi[k];
-      sum += u != u ? u : v != v ? v : u > v ? u : v;
+      const float b = x[k] >= 0.f ? up[k] : down[k];
+      s = fmaf(x[k], b, s);
+      mag = fmaf(fabsf(x[k]), fabsf(b), mag);
     }
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (sum != sum) sum = inf;
-    best = sum > best ? sum : best;
+    for (int o = 16; o >= 1; o >>= 1) {
+      s += __shfl_xor_sync(0xffffffffu, s, o);
+      mag += __shfl_xor_sync(0xffffffffu, mag, o);
+    }
+    finite &= mag < 1e37f;
+    const float err = fmaf(mag, 0x1p-20f, 1e-36f);  // (products below 2^-126 round to its multiples)
+    floor_ = fmaxf(floor_, s - err);
+    if (lane == (r & 31)) {
+      sums[r >> 5] = s;
+      errors[r >> 5] = err;
+    }
+  }
+  if (!__all_sync(0xffffffffu, finite))
+    return score_of_strange_values<kBF16>(q, p.group, make_float4(lo[0], lo[1], lo[2], lo[3]),
+                                          make_float4(hi[0], hi[1], hi[2], hi[3]));
+  double best = -__longlong_as_double(0x7ff0000000000000ll);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    unsigned may = __ballot_sync(0xffffffffu, sums[h] + errors[h] >= floor_);
+    while (may) {
+      const int r = 32 * h + __ffs(may) - 1;
+      may &= may - 1;
+      const uint2 w = *reinterpret_cast<const uint2*>(q + r * kHeadDim);
+      const float2 a = unpack2<kBF16>(w.x), c = unpack2<kBF16>(w.y);
+      const float x[4] = {a.x, a.y, c.x, c.y};
+      double sum = 0.0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        sum = fma(static_cast<double>(x[k]), static_cast<double>(x[k] >= 0.f ? up[k] : down[k]), sum);
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      best = sum > best ? sum : best;
+    }
   }
   return best;
 }
@@ -421,8 +490,9 @@ cudaError_t launch_t(const SelectParams& p, cudaStream_t stream) {
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  constexpr int kThreads = 512;
-  auto kern = choose_blocks_kernel<kF8, kBF16, kThreads>;
+  // (A CTA of 1024 from 4096 blocks on.)
+  const bool many = p.cached_blocks > 4096 || (p.score_ctas > 0 && p.cached_blocks == 0);
+  auto kern = many ? choose_blocks_kernel<kF8, kBF16, 1024> : choose_blocks_kernel<kF8, kBF16, 512>;
   const size_t smem = static_cast<size_t>(p.cached_blocks) * sizeof(float);
   if (smem > 36 * 1024) {  // (beside static shared memory, of 48 KB)
     // (The largest that is ever asked for, so that no call lowers another's limit.)
@@ -432,7 +502,7 @@ cudaError_t launch_t(const SelectParams& p, cudaStream_t stream) {
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.h_kv), static_cast<unsigned>(p.batch));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(many ? 1024 : 512);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
