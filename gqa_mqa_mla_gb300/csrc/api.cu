@@ -814,14 +814,14 @@ int gqa_select_blocks(const void* q, const void* bounds, const int32_t* block_ta
   p.num_blocks = L->num_blocks;
   p.max_blocks_per_seq = L->max_blocks_per_seq;
   p.max_seq_len = L->max_seq_len;
+  const size_t need =
+      gqa_select_workspace_size(L->batch, h_kv, L->max_seq_len, L->block_size, count);
+  if (need > 0 && (!L->workspace || L->workspace_bytes < need)) return DECATTN_ERR_WORKSPACE;
+  const int sms = device_sm_count();
+  if (sms <= 0) return DECATTN_ERR_CUDA;
+  plan_choice(p, static_cast<int>(blocks), sms);
   if (blocks > count) {
-    const size_t need =
-        gqa_select_workspace_size(L->batch, h_kv, L->max_seq_len, L->block_size, count);
-    if (!L->workspace || L->workspace_bytes < need) return DECATTN_ERR_WORKSPACE;
-    const int sms = device_sm_count();
-    if (sms <= 0) return DECATTN_ERR_CUDA;
     p.score_ctas = select_score_ctas(L->batch, h_kv, static_cast<int>(blocks), count, sms);
-    p.cached_blocks = select_cached_blocks(static_cast<int>(blocks), count);
     const size_t all = static_cast<size_t>(L->batch) * h_kv * p.score_stride;
     char* ws = static_cast<char*>(L->workspace);
     p.exact = reinterpret_cast<uint64_t*>(ws);

@@ -1,5 +1,10 @@
-// cut.cuh -- the m largest of n keys by one CTA, and a list of some of n entries
-// in order: shared by the block selection and the eviction.
+// cut.cuh -- the m largest of n keys by a CTA, or by the CTAs of a cluster, and a list
+// of some of n entries in order: shared by the block selection and the eviction.
+//
+// With few sequences and KV heads a long row would leave most SMs idle: the CTAs of a
+// cluster then take a slice of its entries each, and read one another's counts
+// through distributed shared memory (one sequence of 131072 tokens, 8 KV heads, 8192
+// blocks: 23 us of the second kernel with a CTA each).
 #pragma once
 
 #include <cstdint>
@@ -11,15 +16,64 @@ namespace decattn {
 // A float's bits as an unsigned key of the same order: -0 is 0, every NaN the
 // largest key.
 DECATTN_DEV uint32_t order_key(float x) {
-  if (x != x) return 0xffffffffu;
   const uint32_t u = __float_as_uint(x + 0.f);  // (-0 + 0 = 0)
-  return u & 0x80000000u ? ~u : u | 0x80000000u;
+  const uint32_t k = u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+  return x != x ? 0xffffffffu : k;
 }
 DECATTN_DEV uint64_t order_key(double x) {
   if (x != x) return ~0ull;
   const uint64_t u = static_cast<uint64_t>(__double_as_longlong(x + 0.0));
   return u >> 63 ? ~u : u | 1ull << 63;
 }
+// The float of a key.
+DECATTN_DEV float key_value(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+}
+
+// The CTAs that share the entries: one, or a cluster (along x).
+template <bool kCluster>
+struct Team {
+  DECATTN_DEV static void sync() {
+    if constexpr (kCluster)
+      cluster_sync();
+    else
+      __syncthreads();
+  }
+  DECATTN_DEV static int size() { return kCluster ? static_cast<int>(gridDim.x) : 1; }
+  DECATTN_DEV static int rank() { return kCluster ? static_cast<int>(blockIdx.x) : 0; }
+  // Variable x of the team's CTA r (a word of shared memory).
+  template <class T>
+  DECATTN_DEV static T get(const T& x, int r) {
+    static_assert(sizeof(T) == 4, "a word");
+    if constexpr (kCluster) {
+      uint32_t v;
+      asm volatile("ld.shared::cluster.u32 %0, [%1];"
+                   : "=r"(v)
+                   : "r"(mapa_shared(smem_u32(&x), static_cast<uint32_t>(r)))
+                   : "memory");
+      return static_cast<T>(v);
+    } else {
+      return x;
+    }
+  }
+  // The first CTA's x[i] = v, with i counted up in its `n`; places from `most` on are
+  // counted but not written.
+  template <class T>
+  DECATTN_DEV static void push(T* x, int* n, int most, T v) {
+    if constexpr (kCluster) {
+      const uint32_t count = mapa_shared(smem_u32(n), 0), to = mapa_shared(smem_u32(x), 0);
+      uint32_t i;
+      asm volatile("atom.shared::cluster.add.u32 %0, [%1], 1;" : "=r"(i) : "r"(count) : "memory");
+      if (i < static_cast<uint32_t>(most))
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to + 4 * i),
+                     "r"(static_cast<uint32_t>(v))
+                     : "memory");
+    } else {
+      const int i = atomicAdd(n, 1);
+      if (i < most) x[i] = v;
+    }
+  }
+};
 
 // What separates the m largest keys from the others: the keys above `key` are
 // among them, and `ties` of those equal to it.
@@ -33,77 +87,79 @@ constexpr int kCutFew = 64;  // keys that are ranked against one another
 struct CutScratch {
   int bins[kCutBins];
   int sums[32];
-  uint32_t few[kCutFew];
-  uint32_t lo, hi;
-  int bin, left, count, gathered;
+  uint32_t few[kCutFew], own[kCutFew];
+  uint32_t lo, hi;  // between calls: an empty range
+  int gathered;
+  int bin, left, count;
 };
 
-// The keys' range is divided into 2048 bins of equal width (keys of floats: equal
-// ratios, or equal steps where they are alike), counted, and the bin of the m-th
-// largest found; the bin's keys are then ranked directly if they are few, else
-// their range is divided again (each time by 1024 at least, so at most four
-// times).  One counting and one collecting pass where the keys are spread: with
-// 32768 weights a third of the time of three radix passes, whose upper digits few
-// values share.  A value that many lanes of a warp hold is counted once for all.
-// key(i, k) gives entry i's key and whether it takes part; 1 <= m <= the entries
-// that do.  Called by all kThreads threads; ends behind a barrier.
-template <int kThreads, class Key>
-DECATTN_DEV Cut cut_largest(CutScratch& s, int n, int m, Key key) {
+// Before the first call (a barrier of the CTA has to follow).
+DECATTN_DEV void cut_prepare(CutScratch& s) {
+  if (threadIdx.x == 0) {
+    s.lo = 0xffffffffu;
+    s.hi = 0u;
+    s.gathered = 0;
+  }
+}
+
+// The keys' range is divided into up to 2048 bins of equal width, a power of two (keys
+// of floats: equal ratios, or equal steps where they are alike), counted, and the bin
+// of the m-th largest found; the bin's keys are then ranked directly if they are few,
+// else their range is divided again (each time by 1024 at least, so at most four
+// times).  One counting and one collecting pass where the keys are spread, against
+// three counting ones by digits, whose upper digits few values share.  A value that
+// many lanes of a warp hold is counted once for all.
+// key(i, k) gives entry i's key (of this CTA's n) and whether it takes part; lo, hi:
+// the range of the keys that this thread has looked at (all are by the team's
+// threads; empty: lo > hi); 1 <= m <= the team's entries that take part.  Called by all
+// kThreads threads of each CTA; ends behind a barrier.
+template <int kThreads, bool kCluster, class Key>
+DECATTN_DEV Cut cut_largest(CutScratch& s, uint32_t lo, uint32_t hi, int n, int m, Key key) {
+  using T = Team<kCluster>;
   constexpr int kOwn = kCutBins / kThreads;
   static_assert(kCutBins % kThreads == 0 && kThreads % 32 == 0 && kThreads >= kCutFew, "bins");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) {
-    s.lo = 0xffffffffu;
-    s.hi = 0u;
-  }
-  __syncthreads();
-  uint32_t lo = 0xffffffffu, hi = 0u;
-  for (int i = tid; i < n; i += kThreads) {
-    uint32_t k = 0;
-    if (key(i, k)) {
-      lo = min(lo, k);
-      hi = max(hi, k);
-    }
-  }
   lo = __reduce_min_sync(0xffffffffu, lo);
   hi = __reduce_max_sync(0xffffffffu, hi);
   if (lane == 0) {
     atomicMin(&s.lo, lo);
     atomicMax(&s.hi, hi);
   }
-  __syncthreads();
-  lo = s.lo;
-  hi = s.hi;
-  __syncthreads();  // (all have read before a next call writes)
-  while (lo < hi) {
-    const uint32_t range = hi - lo;
-    // Key k falls into bin floor((k - lo) scale / 2^32), or k - lo.
-    const bool direct = range < kCutBins;
-    const uint32_t scale =
-        direct ? 0u : static_cast<uint32_t>((static_cast<uint64_t>(kCutBins) << 32) / (range + 1ull));
 #pragma unroll
-    for (int k = 0; k < kOwn; ++k) s.bins[tid + k * kThreads] = 0;
-    if (tid == 0) s.gathered = 0;
-    __syncthreads();
+  for (int k = 0; k < kOwn; ++k) s.bins[tid + k * kThreads] = 0;
+  T::sync();
+  lo = lane < T::size() ? T::get(s.lo, lane) : 0xffffffffu;
+  hi = lane < T::size() ? T::get(s.hi, lane) : 0u;
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  while (lo < hi) {
+    // Key k falls into bin (k - lo) >> shift.
+    const int shift = max(0, 21 - __clz(hi - lo));
+#pragma unroll 2
     for (int i0 = 0; i0 < n; i0 += kThreads) {
       const int i = i0 + tid;
       uint32_t k = 0;
       const bool on = i < n && key(i, k) && k >= lo && k <= hi;
       const unsigned some = __ballot_sync(0xffffffffu, on);
       if (some == 0) continue;
-      const int bin = static_cast<int>(direct ? k - lo : __umulhi(k - lo, scale));
+      const int bin = static_cast<int>((k - lo) >> shift);
       const int lead = __ffs(some) - 1;
       const int common = __shfl_sync(0xffffffffu, bin, lead);
       const unsigned same = __ballot_sync(0xffffffffu, on && bin == common);
       if (lane == lead) atomicAdd(&s.bins[common], __popc(same));
       if (on && bin != common) atomicAdd(&s.bins[bin], 1);
     }
-    __syncthreads();
+    T::sync();
     // Thread t owns the bins from kCutBins - 1 - t kOwn down; sums from the top.
     const int top = kCutBins - 1 - tid * kOwn;
-    int mine = 0;
+    int each[kOwn], mine = 0;
 #pragma unroll
-    for (int k = 0; k < kOwn; ++k) mine += s.bins[top - k];
+    for (int k = 0; k < kOwn; ++k) {
+      each[k] = 0;
+#pragma unroll 4
+      for (int r = 0; r < T::size(); ++r) each[k] += T::get(s.bins[top - k], r);
+      mine += each[k];
+    }
     int upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -116,69 +172,70 @@ DECATTN_DEV Cut cut_largest(CutScratch& s, int n, int m, Key key) {
     if (above < m && m <= above + mine) {
 #pragma unroll
       for (int k = 0; k < kOwn; ++k) {
-        const int c = s.bins[top - k];
-        if (above < m && m <= above + c) {
+        if (above < m && m <= above + each[k]) {
           s.bin = top - k;
           s.left = m - above;
-          s.count = c;
+          s.count = each[k];
         }
-        above += c;
+        above += each[k];
       }
     }
     __syncthreads();
-    const uint32_t bin = static_cast<uint32_t>(s.bin);
     const int count = s.count;
     m = s.left;
-    if (direct) {
-      lo = hi = lo + bin;
-      break;
-    }
-    // The bin's keys: from the first that falls into it to the last.
-    auto from = [&](uint32_t b) {
-      return ((static_cast<uint64_t>(b) << 32) + scale - 1) / scale;
-    };
-    const uint64_t next = lo + from(bin + 1) - 1;
-    lo += static_cast<uint32_t>(from(bin));
-    hi = next < hi ? static_cast<uint32_t>(next) : hi;
+    lo += static_cast<uint32_t>(s.bin) << shift;
+    if (hi - lo >= 1u << shift) hi = lo + ((1u << shift) - 1);
+    if (lo == hi) break;
     if (count <= kCutFew) {
       for (int i = tid; i < n; i += kThreads) {
         uint32_t k = 0;
-        if (key(i, k) && k >= lo && k <= hi) s.few[atomicAdd(&s.gathered, 1)] = k;
+        if (key(i, k) && k >= lo && k <= hi) T::push(s.few, &s.gathered, kCutFew, k);
       }
+      T::sync();
+      if (tid < count) s.own[tid] = T::get(s.few[tid], 0);
       __syncthreads();
       if (tid < count) {
-        const uint32_t k = s.few[tid];
+        const uint32_t k = s.own[tid];
         int more = 0, equal = 0;
+#pragma unroll 8
         for (int c = 0; c < count; ++c) {
-          more += s.few[c] > k;
-          equal += s.few[c] == k;
+          more += s.own[c] > k;
+          equal += s.own[c] == k;
         }
         if (more < m && m <= more + equal) {  // (the same for all of these)
-          s.lo = k;
+          s.bin = static_cast<int>(k);
           s.left = m - more;
         }
       }
       __syncthreads();
-      const Cut c = {s.lo, s.left};
-      __syncthreads();
-      return c;
+      lo = static_cast<uint32_t>(s.bin);
+      m = s.left;
+      break;
     }
-    __syncthreads();  // (s.bin, s.left and s.count are read before they are written again)
+    T::sync();  // (the bins have been read everywhere)
+#pragma unroll
+    for (int k = 0; k < kOwn; ++k) s.bins[tid + k * kThreads] = 0;
+    __syncthreads();
   }
+  T::sync();  // (nothing of this call is read any more)
+  cut_prepare(s);
+  __syncthreads();
   return {lo, m};
 }
 
-// Go through n entries in order: kind(i) is 0 (not listed), 1 (listed) or 2 (the
-// first `ties` of these are listed); emit(i, rank) for each listed entry with its
-// place in the list.  A warp takes a run of entries: it counts them, and when all
-// have, gives out their places; lane s keeps what it saw in step s (of the first 32,
-// then kind is asked again).
-template <int kThreads>
+// Go through the team's entries in order, this CTA's n behind those of the CTAs before
+// it: kind(i) is 0 (not listed), 1 (listed) or 2 (the first `ties` of these are listed);
+// emit(i, rank) for each listed entry with its place in the list.  Returns the first
+// place of this CTA's entries and the one behind its last.  A warp takes a run of
+// entries: it counts them, and when all have, gives out their places; lane s keeps
+// what it saw in step s (of the first 32, then kind is asked again).
 struct ListScratch {
   int in[32], tied[32];
+  int all_in, all_tied;
 };
-template <int kThreads, class Kind, class Emit>
-DECATTN_DEV void list_in_order(ListScratch<kThreads>& s, int n, int ties, Kind kind, Emit emit) {
+template <int kThreads, bool kCluster, class Kind, class Emit>
+DECATTN_DEV int2 list_in_order(ListScratch& s, int n, int ties, Kind kind, Emit emit) {
+  using T = Team<kCluster>;
   constexpr int kWarps = kThreads / 32;
   static_assert(kWarps <= 32, "warps of a CTA");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -192,6 +249,7 @@ DECATTN_DEV void list_in_order(ListScratch<kThreads>& s, int n, int ties, Kind k
   };
   int in = 0, tied = 0;
   unsigned kept_in = 0, kept_tied = 0;
+#pragma unroll 2
   for (int st = 0; st < steps; ++st) {
     unsigned a, b;
     look(st, a, b);
@@ -207,8 +265,23 @@ DECATTN_DEV void list_in_order(ListScratch<kThreads>& s, int n, int ties, Kind k
     s.tied[warp] = tied;
   }
   __syncthreads();
-  in = __reduce_add_sync(0xffffffffu, lane < warp ? s.in[lane] : 0);
-  tied = __reduce_add_sync(0xffffffffu, lane < warp ? s.tied[lane] : 0);
+  int in_here = lane < kWarps ? s.in[lane] : 0, tied_here = lane < kWarps ? s.tied[lane] : 0;
+  in = __reduce_add_sync(0xffffffffu, lane < warp ? in_here : 0);
+  tied = __reduce_add_sync(0xffffffffu, lane < warp ? tied_here : 0);
+  in_here = __reduce_add_sync(0xffffffffu, in_here);
+  tied_here = __reduce_add_sync(0xffffffffu, tied_here);
+  int in_before = 0, tied_before = 0;  // in the CTAs before this one
+  if constexpr (kCluster) {
+    if (threadIdx.x == 0) {
+      s.all_in = in_here;
+      s.all_tied = tied_here;
+    }
+    T::sync();
+    in_before = __reduce_add_sync(0xffffffffu, lane < T::rank() ? T::get(s.all_in, lane) : 0);
+    tied_before = __reduce_add_sync(0xffffffffu, lane < T::rank() ? T::get(s.all_tied, lane) : 0);
+    in += in_before;
+    tied += tied_before;
+  }
   const unsigned me = 1u << lane, below = me - 1;
   for (int st = 0; st < steps; ++st) {
     unsigned a = __shfl_sync(0xffffffffu, kept_in, st & 31);
@@ -220,6 +293,9 @@ DECATTN_DEV void list_in_order(ListScratch<kThreads>& s, int n, int ties, Kind k
     in += __popc(a);
     tied += __popc(b);
   }
+  if constexpr (kCluster) T::sync();  // (a CTA that others read stays until they have)
+  return make_int2(in_before + min(tied_before, ties),
+                   in_before + in_here + min(tied_before + tied_here, ties));
 }
 
 }  // namespace decattn

@@ -7,13 +7,12 @@
 // its last `recent`.  Entry r of the list of kept positions is the token that
 // moves to position r.
 //
-// Two launches.  The first, a CTA to each sequence and KV head, brings the
-// weights into shared memory (they are needed up to four times: three passes of
-// the radix selection, one of the list), cuts and lists them, and moves the
-// weights themselves.  The second moves K and V: a kept position is never before
-// its place (the list ascends), so a CTA that loads a run of rows, meets, stores
-// it and goes on to the next run overwrites no row that is still to be read, and
-// CTAs that take different columns of the rows need not know of one another.
+// Two launches.  The first, a CTA or a cluster to each sequence and KV head, brings the
+// weights into shared memory (the cut and the list go over them several times), cuts,
+// lists, and moves the weights themselves.  The second moves K and V: a kept position
+// is never before its place (the list ascends), so a CTA that loads a run of rows,
+// meets, stores it and goes on to the next run overwrites no row that is still to be
+// read, and CTAs that take different columns of the rows need not know of one another.
 // Bound by the moved rows' bytes, read and written once.
 #include <algorithm>
 
@@ -27,37 +26,55 @@ namespace {
 constexpr int kThreads = 1024;
 constexpr int kCachedTokens = 53248;  // weights that shared memory holds (208 KB)
 
+template <bool kCluster>
 __global__ void __launch_bounds__(kThreads) evict_rank_kernel(const EvictParams p) {
+  using T = Team<kCluster>;
   extern __shared__ __align__(16) float cached[];
-  __shared__ union {
-    CutScratch cut;
-    ListScratch<kThreads> list;
-  } sm;
-  const int j = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
+  __shared__ CutScratch cut;
+  __shared__ ListScratch list;
+  const int j = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
   const int lg = p.log2_block_size, in_block = p.block_size - 1;
   int32_t* kept = p.kept + (static_cast<int64_t>(b) * p.h_kv + j) * p.keep;
   const int n = p.seq_lens[b];
   const int32_t* bt = p.block_table + static_cast<int64_t>(b) * p.max_blocks_per_seq;
   bool stays = n <= p.limit;
   if (n < 0 || n > p.max_seq_len) {
-    if (tid == 0 && j == 0) flag_error(p.err_flag, kFlagBadSeqLen);
+    if (tid == 0 && j == 0 && T::rank() == 0) flag_error(p.err_flag, kFlagBadSeqLen);
     stays = true;
   }
   float* weights = p.weights + static_cast<int64_t>(j) * p.block_size;
   const int64_t block_stride = static_cast<int64_t>(p.h_kv) * p.block_size;
   auto slot = [&](int t) { return weights + bt[t >> lg] * block_stride + (t & in_block); };
-  const bool cache = n <= p.cached_tokens;
+  // This CTA's tokens: [begin, begin + own), of which the first `old` may go.
+  const int slice = stays ? 0 : ((n + T::size() - 1) / T::size() + 3) & ~3;
+  const int begin = min(n, T::rank() * slice), own = min(slice, n - begin);
+  const int all_old = n - p.recent, old = max(0, min(own, all_old - begin)), heavy = p.keep - p.recent;
+  const bool cache = kCluster || own <= p.cached_tokens;
+  uint32_t lo = 0xffffffffu, hi = 0u;
   if (!stays) {
+    cut_prepare(cut);
     int bad = 0;
     // Four tokens (of one block) at a time, all of a thread's loads in flight.
 #pragma unroll 4
-    for (int t = tid * 4; t < n; t += kThreads * 4) {
-      const int id = bt[t >> lg];
+    for (int i = tid * 4; i < own; i += kThreads * 4) {
+      const int t = begin + i, id = bt[t >> lg];
       const bool wrong = id < 0 || id >= p.num_blocks;
       bad |= wrong;
-      if (cache && !wrong)
-        *reinterpret_cast<float4*>(cached + t) =
-            *reinterpret_cast<const float4*>(weights + id * block_stride + (t & in_block));
+      if (wrong) continue;
+      const float4 w = *reinterpret_cast<const float4*>(weights + id * block_stride + (t & in_block));
+      if (cache) *reinterpret_cast<float4*>(cached + i) = w;
+      const float x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (i + k < old) {
+          lo = min(lo, order_key(x[k]));
+          hi = max(hi, order_key(x[k]));
+        }
+      }
+    }
+    // (Every CTA of a team sees the whole table's verdict: they go on together.)
+    if constexpr (kCluster) {
+      for (int k = tid; k <= (n - 1) >> lg; k += kThreads) bad |= bt[k] < 0 || bt[k] >= p.num_blocks;
     }
     if (__syncthreads_or(bad)) {
       if (tid == 0) flag_error(p.err_flag, kFlagBadBlock);
@@ -65,29 +82,36 @@ __global__ void __launch_bounds__(kThreads) evict_rank_kernel(const EvictParams 
     }
   }
   if (stays) {
-    for (int r = tid; r < p.keep; r += kThreads) kept[r] = -1;
-    if (tid == 0 && j == 0) p.new_lens[b] = 0;
+    for (int r = T::rank() * kThreads + tid; r < p.keep; r += T::size() * kThreads) kept[r] = -1;
+    if (tid == 0 && j == 0 && T::rank() == 0) p.new_lens[b] = 0;
     return;
   }
-  const int old = n - p.recent, heavy = p.keep - p.recent;
-  auto weight = [&](int t) { return cache ? cached[t] : *slot(t); };
+  auto weight = [&](int i) { return cache ? cached[i] : *slot(begin + i); };
+  int2 places = make_int2(0, 0);  // of this CTA's heavy tokens in the list
   if (heavy > 0) {
-    const Cut c = cut_largest<kThreads>(sm.cut, old, heavy, [&](int t, uint32_t& k) {
-      k = order_key(weight(t));
+    const Cut c = cut_largest<kThreads, kCluster>(cut, lo, hi, old, heavy, [&](int i, uint32_t& k) {
+      k = order_key(weight(i));
       return true;
     });
-    list_in_order<kThreads>(sm.list, old, c.ties, [&](int t) {
-      const uint32_t k = order_key(weight(t));
+    places = list_in_order<kThreads, kCluster>(list, old, c.ties, [&](int i) {
+      const uint32_t k = order_key(weight(i));
       return k > c.key ? 1 : k == c.key ? 2 : 0;
-    }, [&](int t, int r) { kept[r] = t; });
+    }, [&](int i, int r) { kept[r] = begin + i; });
+  } else {
+    T::sync();  // (every weight has been read before the first is written)
   }
-  for (int i = tid; i < p.recent; i += kThreads) kept[heavy + i] = old + i;
-  if (tid == 0 && j == 0) p.new_lens[b] = p.keep - n;
+  if (tid == 0 && j == 0 && T::rank() == 0) p.new_lens[b] = p.keep - n;
+  const int latest = max(0, all_old - begin);  // the first of this CTA's that is among the last
+  for (int i = latest + tid; i < own; i += kThreads) {
+    const int r = heavy + begin + i - all_old;
+    kept[r] = begin + i;
+    if (cache) *slot(r) = cached[i];
+  }
   __syncthreads();
   if (cache) {
 #pragma unroll 4
-    for (int r = tid; r < p.keep; r += kThreads) *slot(r) = cached[kept[r]];
-  } else {  // in runs, as the rows are moved
+    for (int r = places.x + tid; r < places.y; r += kThreads) *slot(r) = cached[kept[r] - begin];
+  } else {  // (one CTA) in runs, as the rows are moved
     for (int r0 = 0; r0 < p.keep; r0 += kThreads) {
       const int r = r0 + tid;
       const float w = r < p.keep ? *slot(kept[r]) : 0.f;
@@ -139,18 +163,44 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
 
 }  // namespace
 
-cudaError_t launch_kv_evict(EvictParams p, int num_sms, cudaStream_t stream) {
-  p.cached_tokens = std::min(p.max_seq_len, kCachedTokens);
+template <bool kCluster>
+static cudaError_t launch_rank(const EvictParams& p, cudaStream_t stream) {
   const size_t smem = (static_cast<size_t>(p.cached_tokens) + 3) / 4 * 4 * sizeof(float);
   if (smem > 36 * 1024) {  // (beside static shared memory, of 48 KB)
-    const cudaError_t e =
-        cudaFuncSetAttribute(evict_rank_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kCachedTokens * static_cast<int>(sizeof(float)));
+    const cudaError_t e = cudaFuncSetAttribute(evict_rank_kernel<kCluster>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               kCachedTokens * static_cast<int>(sizeof(float)));
     if (e != cudaSuccess) return e;
   }
-  const dim3 units(static_cast<unsigned>(p.h_kv), static_cast<unsigned>(p.batch));
-  evict_rank_kernel<<<units, kThreads, smem, stream>>>(p);
-  cudaError_t e = cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.team), static_cast<unsigned>(p.h_kv),
+                     static_cast<unsigned>(p.batch));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(p.team);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, evict_rank_kernel<kCluster>, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t launch_kv_evict(EvictParams p, int num_sms, cudaStream_t stream) {
+  // A cluster of up to eight CTAs to a sequence and KV head, while there are SMs for
+  // them and 2048 tokens for each, or their shared memory is needed; past that one CTA
+  // reads the weights from global memory.
+  const int64_t units = static_cast<int64_t>(p.batch) * p.h_kv;
+  p.team = 1;
+  while (p.team < 8 && ((units * p.team * 2 <= num_sms && p.max_seq_len >= 2 * p.team * 2048) ||
+                        p.max_seq_len > p.team * kCachedTokens))
+    p.team *= 2;
+  if (p.max_seq_len > p.team * (kCachedTokens - 4)) p.team = 1;
+  p.cached_tokens = std::min((p.max_seq_len + p.team - 1) / p.team + 3, kCachedTokens);
+  cudaError_t e = p.team > 1 ? launch_rank<true>(p, stream) : launch_rank<false>(p, stream);
   if (e != cudaSuccess) return e;
   // 64 bytes of a row to a CTA, or 32 where that fills no wave.
   const int64_t rows = static_cast<int64_t>(p.batch) * p.h_kv * 2;

@@ -326,66 +326,85 @@ DECATTN_DEV double exact_score(const SelectParams& p, int64_t bj, int j, int id,
   return best;
 }
 
-template <bool kF8, bool kBF16, int kThreads>
+template <bool kF8, bool kBF16, int kThreads, bool kCluster>
 __global__ void __launch_bounds__(kThreads) choose_blocks_kernel(const SelectParams p) {
+  using T = Team<kCluster>;
   extern __shared__ float cached[];
-  __shared__ union {
-    CutScratch cut;
-    ListScratch<kThreads> list;
-  } sm;
-  __shared__ int few[kFew], count_few, count_sure;
+  __shared__ CutScratch cut;
+  __shared__ ListScratch list;
+  __shared__ int few[kFew], own_few[kFew], count_few, count_sure;
   __shared__ double few_score[kFew];
-  __shared__ unsigned few_taken;
-  __shared__ float wide[kThreads / 32];
-  const int j = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  __shared__ unsigned few_taken, widest;
+  const int j = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t bj = static_cast<int64_t>(b) * p.h_kv + j;
   int32_t* out = p.selected + bj * p.count;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the scores are there
   const int n = p.seq_lens[b];
   const bool bad_len = n < 0 || n > p.max_seq_len;
-  if (bad_len && tid == 0 && j == 0) flag_error(p.err_flag, kFlagBadSeqLen);
+  if (bad_len && tid == 0 && j == 0 && T::rank() == 0) flag_error(p.err_flag, kFlagBadSeqLen);
   const int blocks = n > 0 && !bad_len ? ((n - 1) >> p.log2_block_size) + 1 : 0;
   if (blocks <= p.count) {  // all of them
-    for (int k = tid; k < p.count; k += kThreads) out[k] = k < blocks ? k : -1;
+    if (T::rank() == 0)
+      for (int k = tid; k < p.count; k += kThreads) out[k] = k < blocks ? k : -1;
     return;
   }
+  // This CTA's blocks: [begin, begin + own).
+  const int slice = (blocks + T::size() - 1) / T::size();
+  const int begin = min(blocks, T::rank() * slice), own = min(slice, blocks - begin);
   const int32_t* bt = p.block_table + static_cast<int64_t>(b) * p.max_blocks_per_seq;
-  const float* scores = p.scores + bj * p.score_stride;
-  const bool cache = blocks <= p.cached_blocks;
+  const float* scores = p.scores + bj * p.score_stride + begin;
+  // [first, last) of them are chosen by score, `want` of the team's.
+  const int first = p.first - begin, last = blocks - p.last - begin;
+  const int want = p.count - p.first - p.last;
+  const bool cache = own <= p.cached_blocks;
+  cut_prepare(cut);
+  if (tid == 0) {
+    count_few = count_sure = 0;
+    widest = 0;
+  }
+  // The widest error of the scores (not negative: ordered as its bits), by a warp.
+  float e = 0.f;
+  for (int x = tid; x < p.score_ctas; x += kThreads) e = fmaxf(e, p.error[bj * p.score_ctas + x]);
   int bad = 0;
+  uint32_t lo = 0xffffffffu, hi = 0u;
 #pragma unroll 4
-  for (int t = tid; t < blocks; t += kThreads) {
-    const int id = bt[t];
+  for (int t = tid; t < own; t += kThreads) {
+    const int id = bt[begin + t];
+    const float x = scores[t];
     bad |= id < 0 || id >= p.num_blocks;
-    if (cache) cached[t] = scores[t];
+    if (cache) cached[t] = x;
+    if (t >= first && t < last) {
+      lo = min(lo, order_key(x));
+      hi = max(hi, order_key(x));
+    }
+  }
+  // (Every CTA of a team looks at the whole table's verdict: they go on together.)
+  if constexpr (kCluster) {
+    for (int t = tid; t < blocks; t += kThreads) {
+      const int id = bt[t];
+      bad |= id < 0 || id >= p.num_blocks;
+    }
   }
   if (cache) scores = cached;
   if (__syncthreads_or(bad)) {
     if (tid == 0) flag_error(p.err_flag, kFlagBadBlock);
-    for (int k = tid; k < p.count; k += kThreads) out[k] = -1;
+    if (T::rank() == 0)
+      for (int k = tid; k < p.count; k += kThreads) out[k] = -1;
     return;
   }
-
-  const int first = p.first, last = blocks - p.last;  // [first, last) are chosen by score
-  const int want = p.count - p.first - p.last;
-  float e = 0.f;
-  for (int x = tid; x < p.score_ctas; x += kThreads) e = fmaxf(e, p.error[bj * p.score_ctas + x]);
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) e = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, o));
-  if (lane == 0) wide[warp] = e;
-  if (tid == 0) count_few = count_sure = 0;
+  const unsigned wide = __reduce_max_sync(0xffffffffu, __float_as_uint(e));
+  if (lane == 0 && wide) atomicMax(&widest, wide);
   __syncthreads();
-  for (int w = 0; w < kThreads / 32; ++w) e = fmaxf(e, wide[w]);
+  e = __uint_as_float(widest);
 
   // Blocks surely in score above `above`, surely out below `below`.
   float above = kInf, below = -kInf;
   if (want > 0) {
-    const Cut c = cut_largest<kThreads>(sm.cut, blocks, want, [&](int t, uint32_t& k) {
+    const Cut c = cut_largest<kThreads, kCluster>(cut, lo, hi, own, want, [&](int t, uint32_t& k) {
       k = order_key(scores[t]);
       return t >= first && t < last;
     });
-    const uint32_t bits = c.key & 0x80000000u ? c.key & 0x7fffffffu : ~c.key;
-    const float v = __uint_as_float(bits);
+    const float v = key_value(c.key);
     // (Not finite anywhere: the scores order nothing.  Rounded outwards.)
     if (e < kInf && v < kInf) {
       above = __fadd_ru(v, 2.f * e);
@@ -401,34 +420,36 @@ __global__ void __launch_bounds__(kThreads) choose_blocks_kernel(const SelectPar
     return s > above ? 1 : s < below ? 0 : 2;
   };
   int sure = 0;
-  for (int t0 = 0; t0 < blocks; t0 += kThreads) {
+#pragma unroll 2
+  for (int t0 = 0; t0 < own; t0 += kThreads) {
     const int t = t0 + tid;
-    const int k = t < blocks ? near_cut(t) : 0;
+    const int k = t < own ? near_cut(t) : 0;
     sure += __popc(__ballot_sync(0xffffffffu, k == 1));
-    const unsigned close = __ballot_sync(0xffffffffu, k == 2);
-    if (close) {
-      int at = 0;
-      if (lane == 0) at = atomicAdd(&count_few, __popc(close));
-      at = __shfl_sync(0xffffffffu, at, 0) + __popc(close & ((1u << lane) - 1));
-      if (k == 2 && at < kFew) few[at] = t;
-    }
+    if (k == 2) T::push(few, &count_few, kFew, begin + t);
   }
-  if (lane == 0) atomicAdd(&count_sure, sure);
-  __syncthreads();
-  const int close = count_few, left = p.count - count_sure;  // `left` of the close ones are in
+  if (lane == 0 && sure) atomicAdd(&count_sure, sure);
+  T::sync();
+  const int close = T::get(count_few, 0);  // near the cut, and how many of these are in:
+  const int left =
+      p.count - __reduce_add_sync(0xffffffffu, lane < T::size() ? T::get(count_sure, lane) : 0);
 
-  auto emit = [&](int t, int rank) { out[rank] = t; };
+  auto emit = [&](int t, int rank) { out[rank] = begin + t; };
   if (left >= close || left <= 0) {
-    list_in_order<kThreads>(sm.list, blocks, 0, [&](int t) {
+    list_in_order<kThreads, kCluster>(list, own, 0, [&](int t) {
       const int k = near_cut(t);
       return k == 2 ? (left > 0 ? 1 : 0) : k;
     }, emit);
     return;
   }
   if (close <= kFew) {
+    // (Each CTA for itself.)
     for (int c = warp; c < close; c += kThreads / 32) {
-      const double s = exact_score<kF8, kBF16>(p, bj, j, bt[few[c]], lane);
-      if (lane == 0) few_score[c] = s;
+      const int t = T::get(few[c], 0);
+      const double s = exact_score<kF8, kBF16>(p, bj, j, bt[t], lane);
+      if (lane == 0) {
+        own_few[c] = t;
+        few_score[c] = s;
+      }
     }
     __syncthreads();
     if (warp == 0) {
@@ -436,17 +457,17 @@ __global__ void __launch_bounds__(kThreads) choose_blocks_kernel(const SelectPar
       if (lane < close)
         for (int c = 0; c < close; ++c)
           better += few_score[c] > few_score[lane] ||
-                    (few_score[c] == few_score[lane] && few[c] < few[lane]);
+                    (few_score[c] == few_score[lane] && own_few[c] < own_few[lane]);
       const unsigned taken = __ballot_sync(0xffffffffu, lane < close && better < left);
       if (lane == 0) few_taken = taken;
     }
     __syncthreads();
-    list_in_order<kThreads>(sm.list, blocks, 0, [&](int t) {
+    list_in_order<kThreads, kCluster>(list, own, 0, [&](int t) {
       int k = near_cut(t);
       if (k == 2) {
         k = 0;
         for (int c = 0; c < close; ++c)
-          if (few[c] == t) k = few_taken >> c & 1;
+          if (own_few[c] == begin + t) k = few_taken >> c & 1;
       }
       return k;
     }, emit);
@@ -454,28 +475,57 @@ __global__ void __launch_bounds__(kThreads) choose_blocks_kernel(const SelectPar
   }
   // Many blocks alike (equal keys, values that are not finite): all of them in 64
   // bits, cut by the upper word of their order, then by the lower.
-  uint64_t* exact = p.exact + bj * p.score_stride;
-  for (int t = warp; t < blocks; t += kThreads / 32) {
+  uint64_t* exact = p.exact + bj * p.score_stride + begin;
+  for (int t = warp; t < own; t += kThreads / 32) {
     if (near_cut(t) != 2) continue;
-    const double s = exact_score<kF8, kBF16>(p, bj, j, bt[t], lane);
+    const double s = exact_score<kF8, kBF16>(p, bj, j, bt[begin + t], lane);
     if (lane == 0) exact[t] = order_key(s);
   }
   __syncthreads();
-  const Cut up = cut_largest<kThreads>(sm.cut, blocks, left, [&](int t, uint32_t& k) {
+  const Cut up = cut_largest<kThreads, kCluster>(cut, 0u, 0xffffffffu, own, left, [&](int t, uint32_t& k) {
     if (near_cut(t) != 2) return false;
     k = static_cast<uint32_t>(exact[t] >> 32);
     return true;
   });
-  const Cut lowc = cut_largest<kThreads>(sm.cut, blocks, up.ties, [&](int t, uint32_t& k) {
+  const Cut lower = cut_largest<kThreads, kCluster>(cut, 0u, 0xffffffffu, own, up.ties, [&](int t, uint32_t& k) {
     if (near_cut(t) != 2 || exact[t] >> 32 != up.key) return false;
     k = static_cast<uint32_t>(exact[t]);
     return true;
   });
-  const uint64_t cut = static_cast<uint64_t>(up.key) << 32 | lowc.key;
-  list_in_order<kThreads>(sm.list, blocks, lowc.ties, [&](int t) {
+  const uint64_t at = static_cast<uint64_t>(up.key) << 32 | lower.key;
+  list_in_order<kThreads, kCluster>(list, own, lower.ties, [&](int t) {
     const int k = near_cut(t);
-    return k != 2 ? k : exact[t] > cut ? 1 : exact[t] == cut ? 2 : 0;
+    return k != 2 ? k : exact[t] > at ? 1 : exact[t] == at ? 2 : 0;
   }, emit);
+}
+
+template <bool kF8, bool kBF16, int kThreads, bool kCluster>
+cudaError_t launch_choice(const SelectParams& p, cudaStream_t stream) {
+  auto kern = choose_blocks_kernel<kF8, kBF16, kThreads, kCluster>;
+  const size_t smem = static_cast<size_t>(p.cached_blocks) * sizeof(float);
+  if (smem > 36 * 1024) {  // (beside static shared memory, of 48 KB)
+    // (The largest that is ever asked for, so that no call lowers another's limit.)
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               kCachedBlocks * static_cast<int>(sizeof(float)));
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.team), static_cast<unsigned>(p.h_kv),
+                     static_cast<unsigned>(p.batch));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(p.team);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.score_ctas > 0 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <bool kF8, bool kBF16>
@@ -490,28 +540,8 @@ cudaError_t launch_t(const SelectParams& p, cudaStream_t stream) {
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  // (A CTA of 1024 from 4096 blocks on.)
-  const bool many = p.cached_blocks > 4096 || (p.score_ctas > 0 && p.cached_blocks == 0);
-  auto kern = many ? choose_blocks_kernel<kF8, kBF16, 1024> : choose_blocks_kernel<kF8, kBF16, 512>;
-  const size_t smem = static_cast<size_t>(p.cached_blocks) * sizeof(float);
-  if (smem > 36 * 1024) {  // (beside static shared memory, of 48 KB)
-    // (The largest that is ever asked for, so that no call lowers another's limit.)
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               kCachedBlocks * static_cast<int>(sizeof(float)));
-    if (e != cudaSuccess) return e;
-  }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.h_kv), static_cast<unsigned>(p.batch));
-  cfg.blockDim = dim3(many ? 1024 : 512);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = p.score_ctas > 0 ? 1 : 0;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  return p.team > 1 ? launch_choice<kF8, kBF16, 512, true>(p, stream)
+                    : launch_choice<kF8, kBF16, 512, false>(p, stream);
 }
 
 }  // namespace
@@ -525,8 +555,18 @@ int select_score_ctas(int batch, int h_kv, int blocks, int count, int num_sms) {
   return static_cast<int>(std::min(most, share));
 }
 
-int select_cached_blocks(int blocks, int count) {
-  return blocks <= count ? 0 : blocks <= kCachedBlocks ? blocks : 0;
+// The second kernel's CTAs to a sequence and KV head: a cluster of up to eight, while
+// there are SMs for them and 1024 blocks for each.
+void plan_choice(SelectParams& p, int blocks, int num_sms) {
+  p.team = 1;
+  p.cached_blocks = 0;
+  if (blocks <= p.count) return;
+  while (p.team < 8 && static_cast<int64_t>(p.batch) * p.h_kv * p.team * 2 <= num_sms &&
+         blocks >= 2 * p.team * 1024)
+    p.team *= 2;
+  while (p.team < 8 && blocks > p.team * kCachedBlocks) p.team *= 2;
+  const int own = (blocks + p.team - 1) / p.team;
+  p.cached_blocks = own <= kCachedBlocks ? own : 0;
 }
 
 cudaError_t launch_select_blocks(const SelectParams& p, bool e4m3, bool bf16, cudaStream_t stream) {

@@ -263,6 +263,32 @@ def test_selection_of_equal_blocks_takes_the_earliest(alike, fp8):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("blocks", [500, 5000, 41000, 330000])
+def test_selection_among_repeated_blocks(blocks, fp8):
+    """Long tables (one CTA, a cluster, slices past a CTA's and a cluster's shared memory)
+    over few distinct blocks, so that every cut falls among equals."""
+    g, rng = _gen(blocks), np.random.default_rng(blocks)
+    q = torch.randn((2, 4, 128), generator=g, device=DEV).bfloat16()
+    lo, hi = -torch.rand((50, 1, 2, 128), generator=g, device=DEV), torch.rand((50, 1, 2, 128), generator=g, device=DEV)
+    bounds = (torch.cat([lo, hi], 1) * 4).to(torch.float8_e4m3fn if fp8 else torch.bfloat16)
+    table = rng.integers(0, 50, (2, blocks))
+    lens = [8 * blocks - 3, 8 * (blocks // 2)]
+    for count, first, last in ((7, 1, 1), (blocks // 3, 0, 2), (blocks // 2 + 5, 1, 0)):
+        got = da.gqa_select_blocks(q, bounds, _i32(table), _i32(lens), block_size=8, count=count,
+                                   max_seq_len=8 * blocks, first=first, last=last).cpu().numpy()
+        for b, n in enumerate((blocks, blocks // 2)):
+            for j in range(2):
+                if n <= count:
+                    want = np.concatenate([np.arange(n), np.full(count - n, -1)])
+                else:
+                    s = np.array([long_cache.block_score(_np(q)[b, 2 * j:2 * j + 2], *_np(bounds)[i, :, j])
+                                  for i in range(50)])[table[b, :n]]
+                    s[:first], s[n - last:] = np.inf, np.inf
+                    want = np.sort(np.argsort(-s, kind="stable")[:count])
+                assert np.array_equal(got[b, j], want)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 def test_selection_of_nearly_equal_blocks(fp8):
     """Scores that differ by less than 32 bits hold: one large product and a small
     one that only 64 bits tell apart."""
@@ -558,8 +584,8 @@ def _evict(x, **kw):
     return k, v, w, e, int(flag)
 
 
-def _same_eviction(x, keep, recent, limit):
-    k, v, w, e, flag = _evict(x, keep=keep, recent=recent, limit=limit)
+def _same_eviction(x, keep, recent, limit, **kw):
+    k, v, w, e, flag = _evict(x, keep=keep, recent=recent, limit=limit, **kw)
     raw = [c.view(torch.uint8 if x["fp8"] else torch.int16).cpu().numpy() for c in x["caches"]]
     bits = x["weights"].cpu().numpy()
     want = long_cache.evict(*raw, bits, x["table"].cpu().numpy(), x["n"], keep=keep, recent=recent,
@@ -604,11 +630,17 @@ def test_eviction_by_equal_and_strange_weights():
             _same_eviction(x, keep, recent, keep)
 
 
-def test_eviction_of_a_sequence_past_shared_memory():
-    """More tokens than the weights that a CTA's shared memory holds."""
-    x = _case([60000, 300], 1, 1, "bf16", 64, 131, fp8=True)
-    _same_eviction(x, 2500, 100, 2500)
-    _same_eviction(x, 55000, 100, 55000)
+@pytest.mark.parametrize("batch", [1, 40])
+def test_eviction_from_long_sequences(batch):
+    """More tokens than the weights that a CTA's shared memory holds: a cluster's, with
+    few and with many sequences; and, by the host's bound, one CTA without."""
+    x = _case([60000, 300, 5][:min(3, batch)] + [5] * (batch - 3), 2, 2, "bf16", 64, 131, fp8=True,
+              most=6720)
+    x["weights"].copy_((x["weights"] * 8).floor())
+    for most in (60000, 430000):
+        _same_eviction(x, 2500, 100, 2500, most=most)
+        _same_eviction(x, 55000, 0, 55000, most=most)
+        _same_eviction(x, 4000, 4000, 5000, most=most)
 
 
 def test_eviction_flags():
