@@ -54,6 +54,7 @@ from .binding import (  # noqa: F401
     gqa_select_blocks,
     gqa_select_workspace_size,
     gqa_sinks_plan_splits,
+    gqa_weights_plan_splits,
     gqa_weights_workspace_size,
     gqa_window_plan_splits,
     gqa_workspace_size,

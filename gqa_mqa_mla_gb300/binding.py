@@ -168,6 +168,8 @@ def lib() -> ctypes.CDLL:
             L.gqa_decode_fp8kv_weights.restype = I
             L.gqa_decode_weights_workspace_size.argtypes = [I, I, I, I, I]
             L.gqa_decode_weights_workspace_size.restype = S
+            L.gqa_decode_weights_plan_splits.argtypes = [I, I, I, I, I, I, I]
+            L.gqa_decode_weights_plan_splits.restype = I
             L.gqa_block_bounds.argtypes = [P, P, P, P, P, I, I, I, LP]
             L.gqa_block_bounds.restype = I
             L.gqa_select_blocks.argtypes = [P, P, P, P, P, I, I, I, I, I, I, I, LP]
@@ -329,6 +331,15 @@ def gqa_blocks_plan_splits(batch: int, h_q: int, h_kv: int, max_seq_len: int, co
                                             block_size, kv_bytes, num_sms)
     if r < 0:
         raise DecAttnError("gqa_decode_blocks_plan_splits", r)
+    return r
+
+
+def gqa_weights_plan_splits(batch: int, h_q: int, h_kv: int, max_seq_len: int, kv_bytes: int = 2,
+                            d_head: int = 128, num_sms: int = 0) -> int:
+    r = lib().gqa_decode_weights_plan_splits(batch, h_q, h_kv, d_head, max_seq_len, kv_bytes,
+                                             num_sms)
+    if r < 0:
+        raise DecAttnError("gqa_decode_weights_plan_splits", r)
     return r
 
 

@@ -14,6 +14,7 @@
 // so a row costs about two dependent global-load latencies.
 #include "internal.h"
 #include "ptx.cuh"
+#include "weigh.cuh"
 
 namespace decattn {
 namespace {
@@ -138,83 +139,77 @@ __global__ void __launch_bounds__(kRowsPerCta * 32) mla_combine_kernel(const Mla
                            threadIdx.x & 31);
 }
 
-// The weighing decode's second launch: the merge of its partials, and
-//     w_t = (t was weighed before ? decay w_t : 0) + sum_i 2^(s_it - lse_i)
-// over the query heads i of each KV head, from the scores that the partial kernel
-// kept.  A CTA takes 1024 tokens of a sequence and KV head, four to a thread,
-// each token's heads one after the other (always the same order of the sum), and
-// the rows i = blockIdx.x modulo the CTAs of the merge.  Bound by the scores'
-// bytes (4 G a token and KV head beside K's and V's 512, 16-bit), most of which a
-// step finds in L2.
-constexpr int kWeighThreads = 256;
-template <bool kBF16>
-__global__ void __launch_bounds__(kWeighThreads) weigh_kernel(const WeighParams p) {
+// The weighing decode's second launch (wide groups, and more splits than a cluster
+// has): the first CTAs of a sequence and KV head take a run of tokens each (weigh.cuh),
+// the others merge a row of its partials each, the splits dealt out to their warps.
+// One sequence of 32768 tokens, 32 heads on one KV head, 128 splits: 1024 tokens a CTA
+// and a warp to a row's merge beside them took 47 us.
+constexpr int kWeighWarps = 8;
+template <bool kBF16, int kVec>
+__global__ void __launch_bounds__(kWeighWarps * 32) weigh_kernel(const GqaParams p, int chunks) {
   __shared__ float lse[64];
+  __shared__ float4 part[kWeighWarps][32];
+  __shared__ float part_sum[kWeighWarps];
   wait_for_partials();
   const int j = blockIdx.y, b = blockIdx.z, G = p.group, ns = p.n_split;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const size_t row0 = static_cast<size_t>(b) * p.h_q + static_cast<size_t>(j) * G;
-  for (int r = warp; r < G; r += kWeighThreads / 32) {
-    const size_t at = (row0 + r) * ns;
-    float mx = kNegInf, sum = 0.f;
-    bool poison = false;
-    for (int s = lane; s < ns; s += 32) {
-      const float v = p.part_lse[at + s];
-      poison |= v == kPosInf;
-      mx = fmaxf(mx, v);
-    }
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
-    poison = __any_sync(kFull, poison);
-    for (int s = lane; s < ns; s += 32) {
-      const float v = p.part_lse[at + s];
-      sum += v == kNegInf ? 0.f : ex2(v - mx);  // (NaN where a split's is)
-    }
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-    // +inf: bad data, as a partial's; an empty row's scores have weight 0.
-    if (lane == 0)
-      lse[r] = poison ? kPosInf : ns == 1 ? p.part_lse[at] : sum == 0.f ? kNegInf : mx + lg2(sum);
-    if (ns > 1 && r % static_cast<int>(gridDim.x) == static_cast<int>(blockIdx.x))
-      merge_row<kHeadDim, kBF16>(p.part_lse, p.part_o, [at](int s) { return at + s; }, ns,
-                                 static_cast<uint16_t*>(p.out) + (row0 + r) * kHeadDim, lane);
+  if (static_cast<int>(blockIdx.x) < chunks) {
+    const int tokens = kWeighWarps * 32 * kVec, t0 = static_cast<int>(blockIdx.x) * tokens;
+    const int n = p.seq_lens[b];
+    if (t0 >= n) return;
+    weigh_lse<kWeighWarps>(p, row0, lse);
+    __syncthreads();
+    if (lse[0] == kPosInf) return;  // (bad data is met by every head of the group alike)
+    weigh_tokens<kVec>(p, j, b, n, t0, t0 + min(tokens, n - t0), threadIdx.x, kWeighWarps * 32, lse);
+    return;
   }
-  __syncthreads();
-  // (Bad data is met by every head of the group alike.)
-  if (lse[0] == kPosInf) return;
-  const int n = p.seq_lens[b];
-  const int weighed = p.weighed_lens ? p.weighed_lens[b] : n - 1;
-  const int32_t* bt = p.block_table + static_cast<size_t>(b) * p.max_blocks_per_seq;
-  for (int64_t t = (static_cast<int64_t>(blockIdx.x) * kWeighThreads + threadIdx.x) * 4; t < n;
-       t += static_cast<int64_t>(gridDim.x) * kWeighThreads * 4) {
-    const int id = bt[t >> p.log2_block_size];
-    float* at = p.weights + (static_cast<int64_t>(id) * p.h_kv + j) * p.block_size +
-                (t & (p.block_size - 1));
-    const float4 old = *reinterpret_cast<const float4*>(at);
-    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-    const float* s = p.scores + row0 * p.score_stride + t;
+  const size_t at = (row0 + blockIdx.x - chunks) * ns;
+  float mx = kNegInf;  // the maximum of the numbers: NaN does not count
+  bool poison = false, some = false;
+  for (int s = lane; s < ns; s += 32) {
+    const float v = p.part_lse[at + s];
+    poison |= v == kPosInf;
+    some |= v != kNegInf;
+    mx = fmaxf(mx, v);
+  }
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+  poison = __any_sync(kFull, poison);
+  some = __any_sync(kFull, some);
+  uint2* out = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) +
+                                        (row0 + blockIdx.x - chunks) * kHeadDim) + lane;
+  if (poison || !some) {  // (the same in every warp)
+    if (warp == 0) *out = make_uint2(0, 0);
+    return;
+  }
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float sum = 0.f;
+  const float4* po = reinterpret_cast<const float4*>(p.part_o + at * kHeadDim) + lane;
 #pragma unroll 8
-    for (int r = 0; r < G; ++r) {
-      const float4 x = *reinterpret_cast<const float4*>(s + r * p.score_stride);
-      const float l = lse[r];
-      const bool some = l != kNegInf;
-      sum.x += some ? ex2(x.x - l) : 0.f;
-      sum.y += some ? ex2(x.y - l) : 0.f;
-      sum.z += some ? ex2(x.z - l) : 0.f;
-      sum.w += some ? ex2(x.w - l) : 0.f;
-    }
-    if (t < weighed) sum.x = fmaf(p.decay, old.x, sum.x);
-    if (t + 1 < weighed) sum.y = fmaf(p.decay, old.y, sum.y);
-    if (t + 2 < weighed) sum.z = fmaf(p.decay, old.z, sum.z);
-    if (t + 3 < weighed) sum.w = fmaf(p.decay, old.w, sum.w);
-    if (t + 3 < n) {
-      *reinterpret_cast<float4*>(at) = sum;
-    } else {  // slots past the sequence stay as they are
-      at[0] = sum.x;
-      if (t + 1 < n) at[1] = sum.y;
-      if (t + 2 < n) at[2] = sum.z;
-    }
+  for (int s = warp; s < ns; s += kWeighWarps) {
+    const float w = ex2(p.part_lse[at + s] - mx);
+    const float4 x = po[static_cast<size_t>(s) * (kHeadDim / 4)];
+    sum += w;
+    acc.x = fmaf(w, x.x, acc.x);
+    acc.y = fmaf(w, x.y, acc.y);
+    acc.z = fmaf(w, x.z, acc.z);
+    acc.w = fmaf(w, x.w, acc.w);
   }
+  part[warp][lane] = acc;
+  if (lane == 0) part_sum[warp] = sum;
+  __syncthreads();
+  if (warp != 0) return;
+  for (int w = 1; w < kWeighWarps; ++w) {
+    const float4 x = part[w][lane];
+    acc.x += x.x;
+    acc.y += x.y;
+    acc.z += x.z;
+    acc.w += x.w;
+    sum += part_sum[w];
+  }
+  const float inv = 1.f / sum;
+  *out = make_uint2(pack2<kBF16>(acc.x * inv, acc.y * inv), pack2<kBF16>(acc.z * inv, acc.w * inv));
 }
 
 // Launch with programmatic stream serialization: the kernel may begin
@@ -251,20 +246,25 @@ cudaError_t launch_mla_combine(const MlaCombineParams& p, bool bf16, cudaStream_
               : launch_dependent(mla_combine_kernel<false>, ctas, p, stream);
 }
 
-cudaError_t launch_weigh(const WeighParams& p, bool bf16, cudaStream_t stream) {
-  constexpr int kTokens = kWeighThreads * 4;
-  const int chunks = p.max_seq_len > kTokens ? (p.max_seq_len - 1) / kTokens + 1 : 1;
+cudaError_t launch_weigh(const GqaParams& p, bool bf16, int num_sms, cudaStream_t stream) {
+  // Four tokens a thread, or one where that leaves SMs without a CTA.
+  const int64_t units = static_cast<int64_t>(p.batch) * p.h_kv;
+  const int threads = kWeighWarps * 32, most = p.max_seq_len > 0 ? p.max_seq_len : 1;
+  const bool few = units * ((most - 1) / (4 * threads) + 1) < num_sms;
+  const int chunks = (most - 1) / (few ? threads : 4 * threads) + 1;
+  auto kern = bf16 ? (few ? weigh_kernel<true, 1> : weigh_kernel<true, 4>)
+                   : (few ? weigh_kernel<false, 1> : weigh_kernel<false, 4>);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(chunks), static_cast<unsigned>(p.h_kv),
-                     static_cast<unsigned>(p.batch));
-  cfg.blockDim = dim3(kWeighThreads);
+  cfg.gridDim = dim3(static_cast<unsigned>(chunks + (p.n_split > 1 ? p.group : 0)),
+                     static_cast<unsigned>(p.h_kv), static_cast<unsigned>(p.batch));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, bf16 ? weigh_kernel<true> : weigh_kernel<false>, p);
+  return cudaLaunchKernelEx(&cfg, kern, p, chunks);
 }
 
 cudaError_t launch_combine(const CombineParams& p, int d, bool bf16, cudaStream_t stream) {

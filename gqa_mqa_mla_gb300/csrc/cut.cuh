@@ -56,6 +56,42 @@ struct Team {
       return x;
     }
   }
+  // The words x[0 .. kN) of all CTAs added up, this one's first (so that the CTAs do
+  // not all read the same one at a time), 16 or 8 bytes a load, all in flight.
+  template <int kN>
+  DECATTN_DEV static void add_up(const int* x, int (&sum)[kN]) {
+    static_assert(kN == 2 || kN == 4, "one load");
+    if constexpr (kCluster) {
+#pragma unroll
+      for (int k = 0; k < kN; ++k) sum[k] = 0;
+      const uint32_t at = smem_u32(x);
+      int v[8][kN];
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        if (r >= size()) break;
+        const uint32_t from = mapa_shared(at, static_cast<uint32_t>((rank() + r) % size()));
+        if constexpr (kN == 4)
+          asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(v[r][0]), "=r"(v[r][1]), "=r"(v[r][2]), "=r"(v[r][3])
+                       : "r"(from)
+                       : "memory");
+        else
+          asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];"
+                       : "=r"(v[r][0]), "=r"(v[r][1])
+                       : "r"(from)
+                       : "memory");
+      }
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        if (r >= size()) break;
+#pragma unroll
+        for (int k = 0; k < kN; ++k) sum[k] += v[r][k];
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < kN; ++k) sum[k] = x[k];
+    }
+  }
   // The first CTA's x[i] = v, with i counted up in its `n`; places from `most` on are
   // counted but not written.
   template <class T>
@@ -85,7 +121,7 @@ struct Cut {
 constexpr int kCutBins = 2048;
 constexpr int kCutFew = 64;  // keys that are ranked against one another
 struct CutScratch {
-  int bins[kCutBins];
+  __align__(16) int bins[kCutBins];
   int sums[32];
   uint32_t few[kCutFew], own[kCutFew];
   uint32_t lo, hi;  // between calls: an empty range
@@ -150,16 +186,12 @@ DECATTN_DEV Cut cut_largest(CutScratch& s, uint32_t lo, uint32_t hi, int n, int 
       if (on && bin != common) atomicAdd(&s.bins[bin], 1);
     }
     T::sync();
-    // Thread t owns the bins from kCutBins - 1 - t kOwn down; sums from the top.
-    const int top = kCutBins - 1 - tid * kOwn;
+    // Thread t owns the bins from kCutBins - kOwn - t kOwn up; sums from the top.
+    const int first = kCutBins - kOwn - tid * kOwn;
     int each[kOwn], mine = 0;
+    T::add_up(s.bins + first, each);
 #pragma unroll
-    for (int k = 0; k < kOwn; ++k) {
-      each[k] = 0;
-#pragma unroll 4
-      for (int r = 0; r < T::size(); ++r) each[k] += T::get(s.bins[top - k], r);
-      mine += each[k];
-    }
+    for (int k = 0; k < kOwn; ++k) mine += each[k];
     int upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -171,9 +203,9 @@ DECATTN_DEV Cut cut_largest(CutScratch& s, uint32_t lo, uint32_t hi, int n, int 
     int above = upto - mine + __reduce_add_sync(0xffffffffu, lane < warp ? s.sums[lane] : 0);
     if (above < m && m <= above + mine) {
 #pragma unroll
-      for (int k = 0; k < kOwn; ++k) {
+      for (int k = kOwn - 1; k >= 0; --k) {
         if (above < m && m <= above + each[k]) {
-          s.bin = top - k;
+          s.bin = first + k;
           s.left = m - above;
           s.count = each[k];
         }

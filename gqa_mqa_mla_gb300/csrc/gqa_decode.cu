@@ -1095,19 +1095,29 @@ cudaError_t launch_with(const GqaParams& p, const CUtensorMap& tk, const CUtenso
 // Each form has its own instantiations, so that the plain and windowed calls'
 // code stays as it was.
 template <class Consumer, bool kBF16, int kStages>
-cudaError_t launch_one(const GqaParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
-                       cudaStream_t stream, unsigned max_cluster) {
-  if (p.selected)
-    return p.joint
-               ? launch_with<Consumer, kBF16, kStages, kListed, true>(p, tk, tv, stream, max_cluster)
-               : launch_with<Consumer, kBF16, kStages, kListed, false>(p, tk, tv, stream, max_cluster);
-  if (p.scores)
-    return launch_with<Consumer, kBF16, kStages, kWeighed, false>(p, tk, tv, stream, max_cluster);
+cudaError_t launch_plain(const GqaParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
+                         cudaStream_t stream, unsigned max_cluster) {
   if (p.sinks > 0)
     return p.joint
                ? launch_with<Consumer, kBF16, kStages, kSinks, true>(p, tk, tv, stream, max_cluster)
                : launch_with<Consumer, kBF16, kStages, kSinks, false>(p, tk, tv, stream, max_cluster);
   return launch_with<Consumer, kBF16, kStages, kPlain, false>(p, tk, tv, stream, max_cluster);
+}
+template <class Consumer, bool kBF16, int kStages>
+cudaError_t launch_long(const GqaParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
+                        cudaStream_t stream, unsigned max_cluster) {
+  if (p.scores)
+    return launch_with<Consumer, kBF16, kStages, kWeighed, false>(p, tk, tv, stream, max_cluster);
+  return p.joint
+             ? launch_with<Consumer, kBF16, kStages, kListed, true>(p, tk, tv, stream, max_cluster)
+             : launch_with<Consumer, kBF16, kStages, kListed, false>(p, tk, tv, stream, max_cluster);
+}
+template <class Consumer, bool kBF16, int kStages>
+cudaError_t launch_one(const GqaParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
+                       cudaStream_t stream, unsigned max_cluster) {
+  return p.selected || p.scores
+             ? launch_long<Consumer, kBF16, kStages>(p, tk, tv, stream, max_cluster)
+             : launch_plain<Consumer, kBF16, kStages>(p, tk, tv, stream, max_cluster);
 }
 
 template <bool kBF16>
@@ -1129,7 +1139,13 @@ template <bool kBF16>
 cudaError_t dispatch_fp8(const GqaParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
                          cudaStream_t stream) {
   constexpr int S = 4;  // 16 KB stages: keep as many cache bytes in flight as the 16-bit ring
-  if (p.group == 1) return launch_one<CcConsumerF8<1, kBF16>, kBF16, S>(p, tk, tv, stream, 2);
+  // MHA: plain and windowed calls stay on CUDA cores.  The forms for long caches take
+  // the tensor cores, seven of whose eight columns are then idle: four CTAs an SM
+  // instead of three hide more of the chain (7 sequences of 1-5000 tokens, 32 heads,
+  // weighed: 42 us, 54; 8 of 4096: 65, 77; listed, 4 x 4096 of 1-8k: 39, 44; over 16
+  // bits, two CTAs either way, 101 and 100).
+  if (p.group == 1 && !p.selected && !p.scores)
+    return launch_plain<CcConsumerF8<1, kBF16>, kBF16, S>(p, tk, tv, stream, 2);
   // Four CTAs per SM of the transposed consumer: three 16 KB stages each.
   if (p.group <= 8)
     return launch_one<MmaConsumerF8T<1, kBF16>, kBF16, 3>(p, tk, tv, stream, 2);

@@ -43,6 +43,9 @@ struct GqaParams {
   int n_listed;
   float* scores;                  // [B, h_q, score_stride]: keep the scores (log2 domain), or null
   int64_t score_stride;           // max_seq_len rounded up to kTile
+  float* weights;                 // with scores: [num_blocks, h_kv, block_size]
+  const int32_t* weighed_lens;    // [B], or null: all but the last token
+  float decay;
 };
 
 // MLA workspace (n_pairs > 1): a header of kHdrPref ints (slice width in
@@ -213,22 +216,6 @@ struct EvictParams {
   int block_size, log2_block_size, num_blocks, max_blocks_per_seq, max_seq_len;
 };
 
-// The merge of a decode's partials, and its rows' attention weights added up.
-struct WeighParams {
-  const float* part_o;        // [B, h_q, n_split, 128]  (n_split > 1)
-  const float* part_lse;      // [B, h_q, n_split]
-  const float* scores;        // [B, h_q, score_stride]  log2 domain
-  void* out;                  // [B, h_q, 128]           (n_split > 1)
-  float* weights;             // [num_blocks, h_kv, block_size]
-  const int32_t* block_table;
-  const int32_t* seq_lens;
-  const int32_t* weighed_lens;  // [B], or null: all but the last token
-  int64_t score_stride;
-  int batch, h_q, h_kv, group, n_split;
-  int block_size, log2_block_size, max_blocks_per_seq, max_seq_len;
-  float decay;
-};
-
 struct CombineParams {
   const float* part_o;
   const float* part_lse;
@@ -290,7 +277,8 @@ int select_score_ctas(int batch, int h_kv, int blocks, int count, int num_sms);
 void plan_choice(SelectParams& p, int blocks, int num_sms);
 cudaError_t launch_select_blocks(const SelectParams& p, bool e4m3, bool bf16, cudaStream_t stream);
 cudaError_t launch_kv_evict(EvictParams p, int num_sms, cudaStream_t stream);
-cudaError_t launch_weigh(const WeighParams& p, bool bf16, cudaStream_t stream);
+// The weighing decode's second launch, where its splits are not one cluster each.
+cudaError_t launch_weigh(const GqaParams& p, bool bf16, int num_sms, cudaStream_t stream);
 cudaError_t launch_mla_combine(const MlaCombineParams& p, bool bf16, cudaStream_t stream);
 
 // Bounded-wait self test (csrc/selftest.cu).

@@ -274,31 +274,50 @@ DECATTN_DEV double exact_score(const SelectParams& p, int64_t bj, int j, int id,
     down[k] = fminf(lo[k], hi[k]);
     sum_all += fabsf(lo[k]) + fabsf(hi[k]);
   }
-  // Head r's 32-bit sum and its error stay with lane r % 32.
+  // Head r's 32-bit sum and its error stay with lane r % 32; eight heads at a time, so
+  // that their loads and exchanges overlap.
   float sums[2] = {-kInf, -kInf}, errors[2] = {0.f, 0.f}, floor_ = -kInf;
   bool finite = sum_all < kInf;
-  for (int r = 0; r < p.group; ++r) {
-    const uint2 w = *reinterpret_cast<const uint2*>(q + r * kHeadDim);
-    const float2 a = unpack2<kBF16>(w.x), c = unpack2<kBF16>(w.y);
-    const float x[4] = {a.x, a.y, c.x, c.y};
-    float s = 0.f, mag = 0.f;
+  for (int r0 = 0; r0 < p.group; r0 += 8) {
+    uint2 w[8];
+    float s[8], mag[8];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float b = x[k] >= 0.f ? up[k] : down[k];
-      s = fmaf(x[k], b, s);
-      mag = fmaf(fabsf(x[k]), fabsf(b), mag);
+    for (int r = 0; r < 8; ++r)
+      w[r] = *reinterpret_cast<const uint2*>(q + min(r0 + r, p.group - 1) * kHeadDim);
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      const float2 a = unpack2<kBF16>(w[r].x), c = unpack2<kBF16>(w[r].y);
+      const float x[4] = {a.x, a.y, c.x, c.y};
+      s[r] = mag[r] = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float b = x[k] >= 0.f ? up[k] : down[k];
+        s[r] = fmaf(x[k], b, s[r]);
+        mag[r] = fmaf(fabsf(x[k]), fabsf(b), mag[r]);
+      }
     }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) {
-      s += __shfl_xor_sync(0xffffffffu, s, o);
-      mag += __shfl_xor_sync(0xffffffffu, mag, o);
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        s[r] += __shfl_xor_sync(0xffffffffu, s[r], o);
+        mag[r] += __shfl_xor_sync(0xffffffffu, mag[r], o);
+      }
     }
-    finite &= mag < 1e37f;
-    const float err = fmaf(mag, 0x1p-20f, 1e-36f);  // (products below 2^-126 round to its multiples)
-    floor_ = fmaxf(floor_, s - err);
-    if (lane == (r & 31)) {
-      sums[r >> 5] = s;
-      errors[r >> 5] = err;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      finite &= mag[r] < 1e37f;
+      const float err = fmaf(mag[r], 0x1p-20f, 1e-36f);  // (products below 2^-126 lose their lower bits)
+      floor_ = fmaxf(floor_, s[r] - err);
+      if (lane == ((r0 + r) & 31) && r0 + r < p.group) {
+        if (r0 < 32) {
+          sums[0] = s[r];
+          errors[0] = err;
+        } else {
+          sums[1] = s[r];
+          errors[1] = err;
+        }
+      }
     }
   }
   if (!__all_sync(0xffffffffu, finite))
@@ -363,8 +382,7 @@ __global__ void __launch_bounds__(kThreads) choose_blocks_kernel(const SelectPar
     widest = 0;
   }
   // The widest error of the scores (not negative: ordered as its bits), by a warp.
-  float e = 0.f;
-  for (int x = tid; x < p.score_ctas; x += kThreads) e = fmaxf(e, p.error[bj * p.score_ctas + x]);
+  float e = tid < p.score_ctas ? p.error[bj * p.score_ctas + tid] : 0.f;
   int bad = 0;
   uint32_t lo = 0xffffffffu, hi = 0u;
 #pragma unroll 4
@@ -386,6 +404,8 @@ __global__ void __launch_bounds__(kThreads) choose_blocks_kernel(const SelectPar
     }
   }
   if (cache) scores = cached;
+  for (int x = tid + kThreads; x < p.score_ctas; x += kThreads)
+    e = fmaxf(e, p.error[bj * p.score_ctas + x]);
   if (__syncthreads_or(bad)) {
     if (tid == 0) flag_error(p.err_flag, kFlagBadBlock);
     if (T::rank() == 0)

@@ -36,7 +36,8 @@ using at::Tensor;
   X(gqa_decode_fp8kv_plan_splits) X(gqa_decode_sinks_plan_splits)                            \
   X(gqa_decode_workspace_size) X(gqa_decode_blocks) X(gqa_decode_fp8kv_blocks)               \
   X(gqa_decode_blocks_plan_splits) X(gqa_decode_weights) X(gqa_decode_fp8kv_weights)         \
-  X(gqa_decode_weights_workspace_size) X(gqa_block_bounds) X(gqa_select_blocks)              \
+  X(gqa_decode_weights_workspace_size) X(gqa_decode_weights_plan_splits)                     \
+  X(gqa_block_bounds) X(gqa_select_blocks)              \
   X(gqa_select_workspace_size) X(gqa_kv_evict)
 struct Library {
 #define DECATTN_FIELD(name) decltype(&::name) name = nullptr;
@@ -596,8 +597,8 @@ PyObject* decode_weights(PyObject* const* a, Py_ssize_t n) {
     const Unlocked unlocked;
     const OnStream guard(x.index, given, L.stream);
     if (L.num_splits == 0) {
-      const int ns = x.fp8 ? lib.gqa_decode_fp8kv_plan_splits(B, x.h_q, x.h_kv, x.d, max_len, 0)
-                           : lib.gqa_decode_plan_splits(B, x.h_q, x.h_kv, x.d, max_len, 0);
+      const int ns = lib.gqa_decode_weights_plan_splits(B, x.h_q, x.h_kv, x.d, max_len,
+                                                        x.fp8 ? 1 : 2, 0);
       if (ns < 0) return ns;
       L.num_splits = ns;
     }

@@ -517,8 +517,10 @@ size_t gqa_select_workspace_size(int batch, int h_kv, int max_seq_len, int block
  * DECATTN_FLAG_BAD_BLOCK and gives that sequence and KV head zero rows.  Blocks
  * that are not listed are never read and their block_table entries never
  * checked.  Every other argument, layout, status and the workspace rule as
- * gqa_decode; num_splits = 0 takes gqa_decode_blocks_plan_splits' count (the
- * rule of gqa_decode_sinks for min(max_seq_len, count block_size) tokens).
+ * gqa_decode; num_splits = 0 takes gqa_decode_blocks_plan_splits' count (for
+ * min(max_seq_len, count block_size) tokens; kv_bytes = 2, or 1 over an 8-bit cache).
+ * Over an 8-bit cache q is rounded to fp16 with one query head per KV head too (here
+ * and with weights).
  */
 int gqa_decode_blocks(const void* q, const void* k_cache, const void* v_cache,
                       const int32_t* block_table, const int32_t* seq_lens,
@@ -547,8 +549,9 @@ int gqa_decode_blocks_plan_splits(int batch, int h_q, int h_kv, int d_head, int 
  *   decay        finite; 1 adds up, less forgets
  * A row of zeros (no score but -inf) has no weights to add; a NaN row's are
  * NaN.  A sequence with bad data (zero rows) keeps its weights.  Sequences must not
- * share blocks (the weights of a shared one are unspecified).  Workspace:
- * gqa_decode_weights_workspace_size, for any number of splits; the scores, 4
+ * share blocks (the weights of a shared one are unspecified).  num_splits = 0 takes
+ * gqa_decode_weights_plan_splits' count (kv_bytes = 2, or 1 over an 8-bit cache).
+ * Workspace: gqa_decode_weights_workspace_size, for one split too; the scores, 4
  * bytes a query head and token, are most of it.
  */
 int gqa_decode_weights(const void* q, const void* k_cache, const void* v_cache,
@@ -563,6 +566,8 @@ int gqa_decode_fp8kv_weights(const void* q, const void* k_cache, const void* v_c
                              const decattn_launch* launch);
 size_t gqa_decode_weights_workspace_size(int batch, int h_q, int d_head, int max_seq_len,
                                          int num_splits);
+int gqa_decode_weights_plan_splits(int batch, int h_q, int h_kv, int d_head, int max_seq_len,
+                                   int kv_bytes, int num_sms);
 
 /*
  * gqa_kv_evict -- sequences that have grown past a limit keep their heaviest and

@@ -140,7 +140,7 @@ def test_sizes_and_splits(lib):
     assert da.gqa_select_workspace_size(2, 4, 1000, 16, 63) == 0
     assert da.gqa_select_workspace_size(2, 4, 1000, 16, 62) >= 8 * 63 * 12
     assert da.gqa_select_workspace_size(2, 4, 1000, 12, 5) == 0
-    assert da.gqa_select_workspace_size(1, 1, (1 << 31) - 300, 8, 5) > 12 << 28
+    assert da.gqa_select_workspace_size(1, 1, (1 << 31) - 70000, 8, 5) > 12 << 28
     for splits in (1, 7):
         rows = 3 * 12
         need = rows * splits * 4 + rows * 1024 * 4 + (rows * splits * 512 if splits > 1 else 0)
@@ -153,8 +153,16 @@ def test_sizes_and_splits(lib):
         got = da.gqa_blocks_plan_splits(B, h_q, h_kv, most, count, bs, kv, num_sms=152)
         span = min(most, count * bs)
         assert 1 <= got <= max(1, -(-span // 64))
+    for B, h_q, h_kv, most, kv in [(64, 64, 8, 8192, 2), (7, 32, 32, 5000, 1), (1, 32, 1, 32768, 1), (1, 8, 2, 0, 2)]:
+        got = da.gqa_weights_plan_splits(B, h_q, h_kv, most, kv, num_sms=152)
+        assert 1 <= got <= max(1, -(-most // 64))
+        if h_q != h_kv:
+            plain = da.gqa_plan_splits if kv == 2 else da.gqa_fp8_plan_splits
+            assert got == plain(B, h_q, h_kv, most, num_sms=152)
     with pytest.raises(da.DecAttnError):
         da.gqa_blocks_plan_splits(1, 8, 2, 100, 0, 16)
+    with pytest.raises(da.DecAttnError):
+        da.gqa_weights_plan_splits(1, 8, 2, 100, 3)
 
 
 # ------------------------------------------------------------------ the binding's refusals
