@@ -21,7 +21,7 @@
 namespace decattn {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 8, kThreads = kWarps * 32;
 constexpr int kAhead = 8;  // loads in flight per lane
 
 // Packed 16-bit minimum and maximum; NaN if one is NaN.
@@ -52,30 +52,58 @@ DECATTN_DEV uint32_t f16x2_to_e4m3x2(uint32_t x) {
 
 // kF8: e4m3 codes, compared as the fp16 values they stand for.
 template <bool kF8, bool kBF16>
-__global__ void __launch_bounds__(kWarps * 32) block_bounds_kernel(const BoundsParams p) {
+__global__ void __launch_bounds__(kThreads) block_bounds_kernel(const BoundsParams p) {
   constexpr int kLanes = kF8 ? 8 : 16;         // lanes to a token row of 128 or 256 bytes
   constexpr int kRows = 32 / kLanes;           // token rows a load
   constexpr int kWords = kF8 ? 8 : 4;          // 16-bit pairs in 16 bytes
   constexpr uint32_t kInf = kBF16 && !kF8 ? 0x7f807f80u : 0x7c007c00u;
+  __shared__ int64_t before[kThreads + 1];  // units of the sequences before each of a batch
+  __shared__ int lens[kThreads], firsts[kThreads];
+  __shared__ int64_t sums[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int piece = lane & (kLanes - 1), row0 = lane / kLanes;
   const int lg = p.log2_block_size;
   const int64_t row_bytes = static_cast<int64_t>(p.h_kv) * kLanes * 16;
   const uint8_t* keys = static_cast<const uint8_t*>(p.k_cache);
-  for (int b = blockIdx.y; b < p.batch; b += gridDim.y) {
-    const int n = p.seq_lens[b], first = p.first_lens ? p.first_lens[b] : 0;
-    if (n < 0 || n > p.max_seq_len || first < 0) {
-      if (blockIdx.x == 0 && threadIdx.x == 0) flag_error(p.err_flag, kFlagBadSeqLen);
-      continue;
+  // The (block, head) units of 256 sequences at a time, numbered through and dealt
+  // out to the grid's warps, so that sequences of any lengths load them alike.
+  for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
+    const int mine = b0 + threadIdx.x;
+    int64_t units = 0;
+    if (mine < p.batch) {
+      const int n = p.seq_lens[mine], first = p.first_lens ? p.first_lens[mine] : 0;
+      const int from = min(first, n - 1) >> lg;
+      if (n < 0 || n > p.max_seq_len || first < 0) {
+        if (blockIdx.x == 0) flag_error(p.err_flag, kFlagBadSeqLen);
+      } else if (n > 0) {
+        units = static_cast<int64_t>(((n - 1) >> lg) + 1 - from) * p.h_kv;
+      }
+      lens[threadIdx.x] = n;
+      firsts[threadIdx.x] = from;
     }
-    if (n == 0) continue;
-    const int lb0 = min(first, n - 1) >> lg;
-    const int64_t units = static_cast<int64_t>(((n - 1) >> lg) + 1 - lb0) * p.h_kv;
-    const int32_t* bt = p.block_table + static_cast<int64_t>(b) * p.max_blocks_per_seq;
-    for (int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + warp; u < units;
+    int64_t upto = units;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    if (lane == 31) sums[warp] = upto;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) upto += sums[w];
+    before[threadIdx.x + 1] = upto;
+    if (threadIdx.x == 0) before[0] = 0;
+    __syncthreads();
+    const int64_t all = before[kThreads];
+    for (int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + warp; u < all;
          u += static_cast<int64_t>(gridDim.x) * kWarps) {
-      const int lb = lb0 + static_cast<int>(u / p.h_kv), j = static_cast<int>(u % p.h_kv);
-      const int id = bt[lb];
+      int lo_b = 0, hi_b = kThreads;  // the last sequence with before <= u
+      while (hi_b - lo_b > 1) {
+        const int mid = (lo_b + hi_b) >> 1;
+        if (before[mid] <= u) lo_b = mid; else hi_b = mid;
+      }
+      const int n = lens[lo_b], k = static_cast<int>((u - before[lo_b]) / p.h_kv);
+      const int lb = firsts[lo_b] + k, j = static_cast<int>(u - before[lo_b] - static_cast<int64_t>(k) * p.h_kv);
+      const int id = p.block_table[static_cast<int64_t>(b0 + lo_b) * p.max_blocks_per_seq + lb];
       if (id < 0 || id >= p.num_blocks) {
         if (lane == 0) flag_error(p.err_flag, kFlagBadBlock);
         continue;
@@ -138,6 +166,7 @@ __global__ void __launch_bounds__(kWarps * 32) block_bounds_kernel(const BoundsP
         *reinterpret_cast<uint4*>(dst) = make_uint4(out[0], out[1], out[2], out[3]);
       }
     }
+    __syncthreads();  // (the next sequences' numbers)
   }
 }
 
@@ -145,18 +174,16 @@ __global__ void __launch_bounds__(kWarps * 32) block_bounds_kernel(const BoundsP
 
 cudaError_t launch_block_bounds(const BoundsParams& p, bool e4m3, bool bf16, int num_sms,
                                 cudaStream_t stream) {
-  // A warp to each (block, head) that there can be, up to about one wave of CTAs.
+  // A warp to each (block, head) that there can be, up to five CTAs an SM.
   const int64_t blocks = (static_cast<int64_t>(p.max_seq_len) + p.block_size - 1) / p.block_size;
-  const int64_t units = std::max<int64_t>(1, (blocks * p.h_kv + kWarps - 1) / kWarps);
-  const int y = std::min(p.batch, 65535);
-  const int64_t wave = std::max<int64_t>(1, static_cast<int64_t>(num_sms) * 8 / y);
-  const dim3 grid(static_cast<unsigned>(std::min(units, wave)), static_cast<unsigned>(y));
+  const int64_t units = std::max<int64_t>(1, (blocks * p.h_kv * p.batch + kWarps - 1) / kWarps);
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(units, static_cast<int64_t>(num_sms) * 5)));
   if (e4m3)
-    block_bounds_kernel<true, false><<<grid, kWarps * 32, 0, stream>>>(p);
+    block_bounds_kernel<true, false><<<grid, kThreads, 0, stream>>>(p);
   else if (bf16)
-    block_bounds_kernel<false, true><<<grid, kWarps * 32, 0, stream>>>(p);
+    block_bounds_kernel<false, true><<<grid, kThreads, 0, stream>>>(p);
   else
-    block_bounds_kernel<false, false><<<grid, kWarps * 32, 0, stream>>>(p);
+    block_bounds_kernel<false, false><<<grid, kThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 

@@ -155,13 +155,16 @@ __global__ void __launch_bounds__(kWeighWarps * 32) weigh_kernel(const GqaParams
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const size_t row0 = static_cast<size_t>(b) * p.h_q + static_cast<size_t>(j) * G;
   if (static_cast<int>(blockIdx.x) < chunks) {
-    const int tokens = kWeighWarps * 32 * kVec, t0 = static_cast<int>(blockIdx.x) * tokens;
-    const int n = p.seq_lens[b];
-    if (t0 >= n) return;
+    const int n = p.seq_lens[b], weighed = p.weighed_lens ? p.weighed_lens[b] : n - 1;
+    const int t0 = static_cast<int>(blockIdx.x) * kWeighWarps * 32 * kVec;
+    if (t0 >= n || n > p.max_seq_len) return;
+    const int t = t0 + threadIdx.x * kVec;
+    Weighed<kVec> tokens;
+    if (t < n) tokens.load(p, j, b, t);
     weigh_lse<kWeighWarps>(p, row0, lse);
     __syncthreads();
     if (lse[0] == kPosInf) return;  // (bad data is met by every head of the group alike)
-    weigh_tokens<kVec>(p, j, b, n, t0, t0 + min(tokens, n - t0), threadIdx.x, kWeighWarps * 32, lse);
+    if (t < n) tokens.store(p, t, n, weighed, lse);
     return;
   }
   const size_t at = (row0 + blockIdx.x - chunks) * ns;

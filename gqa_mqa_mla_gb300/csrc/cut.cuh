@@ -164,10 +164,24 @@ DECATTN_DEV Cut cut_largest(CutScratch& s, uint32_t lo, uint32_t hi, int n, int 
 #pragma unroll
   for (int k = 0; k < kOwn; ++k) s.bins[tid + k * kThreads] = 0;
   T::sync();
-  lo = lane < T::size() ? T::get(s.lo, lane) : 0xffffffffu;
-  hi = lane < T::size() ? T::get(s.hi, lane) : 0u;
-  lo = __reduce_min_sync(0xffffffffu, lo);
-  hi = __reduce_max_sync(0xffffffffu, hi);
+  if constexpr (kCluster) {
+    if (warp == 0) {
+      lo = lane < T::size() ? T::get(s.lo, lane) : 0xffffffffu;
+      hi = lane < T::size() ? T::get(s.hi, lane) : 0u;
+      lo = __reduce_min_sync(0xffffffffu, lo);
+      hi = __reduce_max_sync(0xffffffffu, hi);
+      if (lane == 0) {
+        s.own[0] = lo;
+        s.own[1] = hi;
+      }
+    }
+    __syncthreads();
+    lo = s.own[0];
+    hi = s.own[1];
+  } else {
+    lo = s.lo;
+    hi = s.hi;
+  }
   while (lo < hi) {
     // Key k falls into bin (k - lo) >> shift.
     const int shift = max(0, 21 - __clz(hi - lo));

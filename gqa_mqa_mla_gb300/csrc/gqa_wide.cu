@@ -231,6 +231,7 @@ __global__ void __launch_bounds__(kThreads)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = p.group;
 
+  if constexpr (kForm == kWeighed) launch_dependents();
   const GqaSpan<kForm> span = gqa_span<kForm>(p, split, j, b);
   if (threadIdx.x == 0) {
     mbar_init(bar(kBarQ), kSoftmaxThreads);

@@ -32,6 +32,7 @@ __global__ void __launch_bounds__(kThreads) evict_rank_kernel(const EvictParams 
   extern __shared__ __align__(16) float cached[];
   __shared__ CutScratch cut;
   __shared__ ListScratch list;
+  launch_dependents();
   const int j = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
   const int lg = p.log2_block_size, in_block = p.block_size - 1;
   int32_t* kept = p.kept + (static_cast<int64_t>(b) * p.h_kv + j) * p.keep;
@@ -124,9 +125,11 @@ __global__ void __launch_bounds__(kThreads) evict_rank_kernel(const EvictParams 
 constexpr int kMoveThreads = 256;
 constexpr int kAhead = 8;  // 16-byte pieces a thread holds
 
-// A CTA moves a run of columns (`pieces` 16-byte pieces of a head's row) of K or V.
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams p, int lg_pieces) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the list is there
+// A CTA moves some columns (2^lg_pieces 16-byte pieces of a head's row) of K or V, in runs
+// of as many rows as its threads hold; a run's places are looked up (through the list
+// and the table) while the rows of the run before are on their way.
+__global__ void __launch_bounds__(kMoveThreads, 3) evict_move_kernel(const EvictParams p, int lg_pieces) {
+  wait_for_dependence();  // the list is there
   const int j = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
   const int32_t* kept = p.kept + (static_cast<int64_t>(b) * p.h_kv + j) * p.keep;
   if (kept[0] < 0) return;  // nothing is evicted
@@ -138,26 +141,37 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
   const int piece = tid & ((1 << lg_pieces) - 1), row = tid >> lg_pieces;
   uint8_t* cache = (is_v ? p.v_cache : p.k_cache) + j * p.head_bytes + ((part << lg_pieces) + piece) * 16;
   const int32_t* bt = p.block_table + static_cast<int64_t>(b) * p.max_blocks_per_seq;
-  auto place = [&](int t) {
-    return reinterpret_cast<uint4*>(cache + (static_cast<int64_t>(bt[t >> lg]) * p.block_size +
-                                             (t & in_block)) * row_bytes);
-  };
+  auto place = [&](int t) { return (bt[t >> lg] << lg) + (t & in_block); };  // the row, < 2^31
   const int step = kMoveThreads >> lg_pieces;  // rows of one load
+  int from[kAhead], to[kAhead];  // (-1: the row stays where it is, or there is none)
+  auto look_up = [&](int r0) {
+    int t[kAhead];
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      const int r = r0 + a * step + row;
+      t[a] = r < p.keep ? kept[r] : r;
+    }
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) {
+      const int r = r0 + a * step + row;
+      from[a] = t[a] != r ? place(t[a]) : -1;
+      to[a] = t[a] != r ? place(r) : -1;
+    }
+  };
+  look_up(0);
   for (int r0 = 0; r0 < p.keep; r0 += step * kAhead) {
     uint4 x[kAhead];
-    int from[kAhead];
+    int at[kAhead];
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
-      const int r = r0 + a * step + row;
-      from[a] = r < p.keep ? kept[r] : r;
-      if (from[a] != r) x[a] = *place(from[a]);
+      at[a] = to[a];
+      if (at[a] >= 0) x[a] = *reinterpret_cast<const uint4*>(cache + from[a] * row_bytes);
     }
+    if (r0 + step * kAhead < p.keep) look_up(r0 + step * kAhead);
     __syncthreads();
 #pragma unroll
-    for (int a = 0; a < kAhead; ++a) {
-      const int r = r0 + a * step + row;
-      if (from[a] != r) *place(r) = x[a];
-    }
+    for (int a = 0; a < kAhead; ++a)
+      if (at[a] >= 0) *reinterpret_cast<uint4*>(cache + at[a] * row_bytes) = x[a];
   }
 }
 
@@ -204,7 +218,7 @@ cudaError_t launch_kv_evict(EvictParams p, int num_sms, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   // 64 bytes of a row to a CTA, or 32 where that fills no wave.
   const int64_t rows = static_cast<int64_t>(p.batch) * p.h_kv * 2;
-  const int lg_pieces = rows * (p.head_bytes / 64) < num_sms * 4 ? 1 : 2;
+  const int lg_pieces = rows * (p.head_bytes / 64) < num_sms * 4 ? 1 : 3;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * (p.head_bytes >> (4 + lg_pieces))),
                      static_cast<unsigned>(p.h_kv), static_cast<unsigned>(p.batch));

@@ -23,6 +23,11 @@ DECATTN_DEV uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
+// Programmatic dependents: let the next kernel's CTAs take what room is left, once
+// every CTA of this one has come here; and wait for the kernel before this one.
+DECATTN_DEV void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+DECATTN_DEV void wait_for_dependence() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 DECATTN_DEV uint64_t global_timer_ns() {
   uint64_t t;
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));

@@ -43,10 +43,11 @@ DECATTN_DEV void by_sign(uint32_t w, uint32_t& plus, uint32_t& minus) {
 }
 
 template <bool kF8, bool kBF16, int kTiles>
-__global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(kScoreWarps * 32, kTiles == 1 ? 8 : 1) block_scores_kernel(const SelectParams p) {
   constexpr bool kMmaBF16 = kBF16 && !kF8;
   __shared__ __align__(16) uint8_t qs[kTiles * 16 * kQStride];
   __shared__ float mag[kTiles * 16], part[kScoreWarps];
+  launch_dependents();
   const int j = blockIdx.y, b = blockIdx.z, G = p.group;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
   const int64_t bj = static_cast<int64_t>(b) * p.h_kv + j;
@@ -357,7 +358,7 @@ __global__ void __launch_bounds__(kThreads) choose_blocks_kernel(const SelectPar
   const int j = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t bj = static_cast<int64_t>(b) * p.h_kv + j;
   int32_t* out = p.selected + bj * p.count;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the scores are there
+  wait_for_dependence();  // the scores are there
   const int n = p.seq_lens[b];
   const bool bad_len = n < 0 || n > p.max_seq_len;
   if (bad_len && tid == 0 && j == 0 && T::rank() == 0) flag_error(p.err_flag, kFlagBadSeqLen);

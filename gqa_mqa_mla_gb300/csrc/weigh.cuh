@@ -67,55 +67,76 @@ DECATTN_DEV void weigh_lse(const GqaParams& p, size_t row0, float* lse) {
   }
 }
 
-// Tokens [t0, t1) of sequence b and KV head j (t0 a multiple of kTile), kVec to a thread
-// at a time (1 or 4; blocks hold a multiple of 8), thread `tid` of `threads`.  A token's
-// heads are added one after the other, always in the same order.
+// kVec tokens from t on of sequence b and KV head j (1 or 4; blocks hold a multiple of
+// 8): load() before the log-sum-exps are known, the slots' weights and the scores of
+// the first kAhead heads; store() adds up.  A token's heads are added one after the
+// other, always in the same order.
 template <int kVec>
-DECATTN_DEV void weigh_tokens(const GqaParams& p, int j, int b, int n, int t0, int t1, int tid,
-                              int threads, const float* lse) {
-  constexpr float kInf = __builtin_huge_valf();
-  const int G = p.group;
-  const int weighed = p.weighed_lens ? p.weighed_lens[b] : n - 1;
-  const int32_t* bt = p.block_table + static_cast<size_t>(b) * p.max_blocks_per_seq;
-  const float* scores =
-      p.scores + (static_cast<size_t>(b) * p.h_q + static_cast<size_t>(j) * G) * p.score_stride;
-  for (int t = t0 + tid * kVec; t < t1; t += threads * kVec) {
-    float sum[kVec], old[kVec];
-    float* at = p.weights + (static_cast<int64_t>(bt[t >> p.log2_block_size]) * p.h_kv + j) * p.block_size +
-                (t & (p.block_size - 1));
+struct Weighed {
+  static constexpr int kAhead = 8;
+  float old[kVec], x[kAhead][kVec];
+  float* at;
+  const float* scores;
+
+  DECATTN_DEV void head(int r, const GqaParams& p, float (&y)[kVec]) const {
     if constexpr (kVec == 4) {
-      const float4 w = *reinterpret_cast<const float4*>(at);
-      old[0] = w.x; old[1] = w.y; old[2] = w.z; old[3] = w.w;
+      const float4 s = __ldcg(reinterpret_cast<const float4*>(scores + r * p.score_stride));
+      y[0] = s.x; y[1] = s.y; y[2] = s.z; y[3] = s.w;
     } else {
-      old[0] = *at;
+      y[0] = __ldcg(scores + r * p.score_stride);
     }
+  }
+  DECATTN_DEV void load(const GqaParams& p, int j, int b, int t) {
+    const int id = p.block_table[static_cast<size_t>(b) * p.max_blocks_per_seq + (t >> p.log2_block_size)];
+    scores = p.scores + (static_cast<size_t>(b) * p.h_q + static_cast<size_t>(j) * p.group) * p.score_stride + t;
+#pragma unroll
+    for (int r = 0; r < kAhead; ++r)
+      if (r < p.group) head(r, p, x[r]);
+    // (A bad id, of a sequence whose log-sum-exps will say so, is not followed.)
+    at = id < 0 || id >= p.num_blocks
+             ? nullptr
+             : p.weights + (static_cast<int64_t>(id) * p.h_kv + j) * p.block_size + (t & (p.block_size - 1));
+    if (at) {
+      if constexpr (kVec == 4) {
+        const float4 w = *reinterpret_cast<const float4*>(at);
+        old[0] = w.x; old[1] = w.y; old[2] = w.z; old[3] = w.w;
+      } else {
+        old[0] = *at;
+      }
+    }
+  }
+  DECATTN_DEV void store(const GqaParams& p, int t, int n, int weighed, const float* lse) {
+    constexpr float kInf = __builtin_huge_valf();
+    float sum[kVec];
 #pragma unroll
     for (int k = 0; k < kVec; ++k) sum[k] = 0.f;
-#pragma unroll 8
-    for (int r = 0; r < G; ++r) {
-      float x[kVec];
-      if constexpr (kVec == 4) {
-        const float4 s = __ldcg(reinterpret_cast<const float4*>(scores + r * p.score_stride + t));
-        x[0] = s.x; x[1] = s.y; x[2] = s.z; x[3] = s.w;
-      } else {
-        x[0] = __ldcg(scores + r * p.score_stride + t);
-      }
+#pragma unroll
+    for (int r = 0; r < kAhead; ++r) {
+      if (r >= p.group) break;
       const float l = lse[r];
 #pragma unroll
-      for (int k = 0; k < kVec; ++k) sum[k] += l != -kInf ? ex2(x[k] - l) : 0.f;
+      for (int k = 0; k < kVec; ++k) sum[k] += l != -kInf ? ex2(x[r][k] - l) : 0.f;
+    }
+#pragma unroll 8
+    for (int r = kAhead; r < p.group; ++r) {
+      float y[kVec];
+      head(r, p, y);
+      const float l = lse[r];
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) sum[k] += l != -kInf ? ex2(y[k] - l) : 0.f;
     }
 #pragma unroll
     for (int k = 0; k < kVec; ++k)
       if (t + k < weighed) sum[k] = fmaf(p.decay, old[k], sum[k]);
-    if (kVec == 4 && t + 3 < t1) {
+    if (kVec == 4 && t + 3 < n) {
       *reinterpret_cast<float4*>(at) = make_float4(sum[0], sum[kVec > 1 ? 1 : 0], sum[kVec > 2 ? 2 : 0],
                                                    sum[kVec > 3 ? 3 : 0]);
     } else {  // (slots past the sequence stay as they are)
 #pragma unroll
       for (int k = 0; k < kVec; ++k)
-        if (t + k < t1) at[k] = sum[k];
+        if (t + k < n) at[k] = sum[k];
     }
   }
-}
+};
 
 }  // namespace decattn
