@@ -358,12 +358,13 @@ __global__ void __launch_bounds__(kThreads) choose_blocks_kernel(const SelectPar
   const int j = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t bj = static_cast<int64_t>(b) * p.h_kv + j;
   int32_t* out = p.selected + bj * p.count;
-  wait_for_dependence();  // the scores are there
+  // (What the first kernel does not write is read before it has ended.)
   const int n = p.seq_lens[b];
   const bool bad_len = n < 0 || n > p.max_seq_len;
   if (bad_len && tid == 0 && j == 0 && T::rank() == 0) flag_error(p.err_flag, kFlagBadSeqLen);
   const int blocks = n > 0 && !bad_len ? ((n - 1) >> p.log2_block_size) + 1 : 0;
   if (blocks <= p.count) {  // all of them
+    wait_for_dependence();
     if (T::rank() == 0)
       for (int k = tid; k < p.count; k += kThreads) out[k] = k < blocks ? k : -1;
     return;
@@ -382,26 +383,24 @@ __global__ void __launch_bounds__(kThreads) choose_blocks_kernel(const SelectPar
     count_few = count_sure = 0;
     widest = 0;
   }
+  // (Every CTA of a team checks the whole table: they go on together.)
+  int bad = 0;
+#pragma unroll 4
+  for (int t = tid; t < blocks; t += kThreads) {
+    const int id = bt[t];
+    bad |= id < 0 || id >= p.num_blocks;
+  }
+  wait_for_dependence();  // the scores are there
   // The widest error of the scores (not negative: ordered as its bits), by a warp.
   float e = tid < p.score_ctas ? p.error[bj * p.score_ctas + tid] : 0.f;
-  int bad = 0;
   uint32_t lo = 0xffffffffu, hi = 0u;
 #pragma unroll 4
   for (int t = tid; t < own; t += kThreads) {
-    const int id = bt[begin + t];
     const float x = scores[t];
-    bad |= id < 0 || id >= p.num_blocks;
     if (cache) cached[t] = x;
     if (t >= first && t < last) {
       lo = min(lo, order_key(x));
       hi = max(hi, order_key(x));
-    }
-  }
-  // (Every CTA of a team looks at the whole table's verdict: they go on together.)
-  if constexpr (kCluster) {
-    for (int t = tid; t < blocks; t += kThreads) {
-      const int id = bt[t];
-      bad |= id < 0 || id >= p.num_blocks;
     }
   }
   if (cache) scores = cached;
