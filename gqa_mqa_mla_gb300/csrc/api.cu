@@ -785,7 +785,7 @@ size_t gqa_select_workspace_size(int batch, int h_kv, int max_seq_len, int block
   if (batch < 1 || h_kv < 1 || max_seq_len < 0 || !is_pow2(block_size) || count < 1) return 0;
   const int64_t blocks = select_blocks_of(max_seq_len, block_size);
   if (blocks <= count) return 0;
-  const size_t units = static_cast<size_t>(batch) * h_kv, stride = (blocks + 7) / 8 * 8;
+  const size_t units = static_cast<size_t>(batch) * h_kv, stride = (blocks + 15) / 16 * 16;
   return align_up(units * stride * sizeof(uint64_t)) + align_up(units * stride * sizeof(float)) +
          align_up(units * ((stride + 31) / 32) * sizeof(float));
 }
@@ -813,7 +813,7 @@ int gqa_select_blocks(const void* q, const void* bounds, const int32_t* block_ta
   p.seq_lens = seq_lens;
   p.selected = selected;
   p.err_flag = L->err_flag;
-  p.score_stride = (blocks + 7) / 8 * 8;
+  p.score_stride = (blocks + 15) / 16 * 16;
   p.batch = L->batch;
   p.h_kv = h_kv;
   p.group = h_q / h_kv;

@@ -190,7 +190,7 @@ struct SelectParams {
   float* error;               // [B, h_kv, score_ctas] how far a CTA's scores may be off
   uint64_t* exact;            // [B, h_kv, score_stride] 64-bit scores in order, where needed
   int* err_flag;
-  int64_t score_stride;       // blocks of max_seq_len, rounded up to 8
+  int64_t score_stride;       // blocks of max_seq_len, rounded up to 16
   int batch, h_kv, group;
   int count, first, last;     // first + last <= count
   int score_ctas;             // CTAs a sequence and KV head; 0: no sequence has a choice to make

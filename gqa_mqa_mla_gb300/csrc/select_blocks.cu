@@ -11,10 +11,12 @@
 // how a kernel sums.
 //
 // Bound by the bounds' bytes (2 x 256 B a block and KV head, 16-bit), so the
-// scores run on mma.sync in 32 bits: a warp takes 8 blocks (n) against up to 16
-// query heads a tile (m); a lane's 16-byte pieces of a bounds row are the B
-// fragments as they are (the k index is permuted, the same for q).  Such a score
-// is off by at most
+// scores run on mma.sync in 32 bits: a warp takes 16 blocks (m) against 8 query heads
+// at a time (n); a lane's 16-byte pieces of the bounds' rows are the A fragments as
+// they are (the k index is permuted, the same for q), and up to 8 heads' q^+ and q^-
+// stay in registers as B fragments.  (With the heads as m, 8 blocks as n, the kernel
+// spent its issue slots on splitting q by sign for each tile: 37 us for 196 MB.)  Such
+// a score is off by at most
 //     E = 2^-16 max_i sum_d |q_id| max_td |bound_td|:
 // four chains of four products of 16 terms, each term off by at most 2^-23 of the
 // chain's sum of magnitudes (4 x 17 x 2^-23), and their sum.  The second kernel, a
@@ -31,22 +33,37 @@ namespace decattn {
 namespace {
 
 constexpr int kScoreWarps = 4;
-constexpr int kQStride = 320;  // bytes of a 128-value row in shared memory: rows two banks' groups apart
+constexpr int kScoreBlocks = 16;  // blocks of a warp's tile
+constexpr int kQStride = 320;     // bytes of a 128-value row in shared memory: rows two banks' groups apart
 constexpr float kInf = __builtin_huge_valf();
 constexpr float kError = 1.52587890625e-05f;  // 2^-16
 
 // q^+ and q^- of a pair: the halves whose sign bit is clear / set, else 0.
-DECATTN_DEV void by_sign(uint32_t w, uint32_t& plus, uint32_t& minus) {
-  const uint32_t negative = byte_perm(w, 0u, 0xbb99u);  // (each half's sign, 16 times)
-  plus = w & ~negative;
-  minus = w & negative;
+DECATTN_DEV uint4 by_sign(uint4 w, bool negative) {
+  auto part = [&](uint32_t x) {
+    const uint32_t sign = byte_perm(x, 0u, 0xbb99u);  // (each half's sign, 16 times)
+    return negative ? x & sign : x & ~sign;
+  };
+  return make_uint4(part(w.x), part(w.y), part(w.z), part(w.w));
 }
 
-template <bool kF8, bool kBF16, int kTiles>
-__global__ void __launch_bounds__(kScoreWarps * 32, kTiles == 1 ? 8 : 1) block_scores_kernel(const SelectParams p) {
+// Packed maximum and minimum; NaN where one is NaN.
+template <bool kBF16>
+DECATTN_DEV uint32_t max2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if constexpr (kBF16)
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// kHeads: 8 (their fragments in registers), 16 or 64 heads a KV head at most.
+template <bool kF8, bool kBF16, int kHeads>
+__global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const SelectParams p) {
   constexpr bool kMmaBF16 = kBF16 && !kF8;
-  __shared__ __align__(16) uint8_t qs[kTiles * 16 * kQStride];
-  __shared__ float mag[kTiles * 16], part[kScoreWarps];
+  __shared__ __align__(16) uint8_t qs[2][kHeads * kQStride];  // q^+, q^-
+  __shared__ float mag[kHeads], part[kScoreWarps];
   launch_dependents();
   const int j = blockIdx.y, b = blockIdx.z, G = p.group;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
@@ -59,145 +76,183 @@ __global__ void __launch_bounds__(kScoreWarps * 32, kTiles == 1 ? 8 : 1) block_s
   // q of the group (rows past it zero); over 8 bits as fp16, a bf16 query times the
   // power of two that brings the group's largest value to 2^14 .. 2^15 (the
   // scores of the pair (b, j) then all carry that factor; what falls below fp16's
-  // smallest step is 2^-38 of that value).
+  // smallest step is 2^-38 of that value).  16 lanes have a row, 8 values each.
   const uint16_t* q = static_cast<const uint16_t*>(p.q) + bj * G * kHeadDim;
-  for (int r = warp; r < kTiles * 16; r += kScoreWarps) {
-    uint2 w = make_uint2(0u, 0u);
-    if (r < G) w = *reinterpret_cast<const uint2*>(q + r * kHeadDim + lane * 4);
-    const float2 x = unpack2<kBF16>(w.x), y = unpack2<kBF16>(w.y);
-    float sum = fabsf(x.x) + fabsf(x.y) + fabsf(y.x) + fabsf(y.y);
-    float most = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(y.x), fabsf(y.y)));
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) {
-      sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-    }
-    *reinterpret_cast<uint2*>(qs + r * kQStride + lane * 8) = w;
-    if (lane == 0) mag[r] = kF8 && kBF16 ? most : sum;
-  }
-  __syncthreads();
-  float alpha = 1.f, q1 = 0.f;
+  float alpha = 1.f;
+  const int piece = lane & 15;
+  auto q_row = [&](int r) {
+    return r < G ? *reinterpret_cast<const uint4*>(q + r * kHeadDim + piece * 8) : make_uint4(0, 0, 0, 0);
+  };
   if constexpr (kF8 && kBF16) {
+    for (int r = 2 * warp + (lane >> 4); r < kHeads; r += 2 * kScoreWarps) {
+      const uint4 w = q_row(r);
+      const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+      float most = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = unpack2<true>(x[k]);
+        most = fmaxf(most, fmaxf(fabsf(f.x), fabsf(f.y)));
+      }
+#pragma unroll
+      for (int o = 8; o >= 1; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+      if (piece == 0) mag[r] = most;
+    }
+    __syncthreads();
     float most = 0.f;
     for (int r = 0; r < G; ++r) most = fmaxf(most, mag[r]);
     const int e = static_cast<int>(__float_as_uint(most) >> 23) - 127;  // 128: infinite
     const int k = e >= 128 ? 0 : min(14 - e, 126);
     alpha = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
     __syncthreads();
-    for (int r = warp; r < G; r += kScoreWarps) {
-      uint2* at = reinterpret_cast<uint2*>(qs + r * kQStride + lane * 8);
-      const float2 x = unpack2<true>(at->x), y = unpack2<true>(at->y);
-      *at = make_uint2(pack2<false>(x.x * alpha, x.y * alpha), pack2<false>(y.x * alpha, y.y * alpha));
-      float sum = alpha * (fabsf(x.x) + fabsf(x.y) + fabsf(y.x) + fabsf(y.y));
-#pragma unroll
-      for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      if (lane == 0) mag[r] = sum;
-    }
-    __syncthreads();
   }
+  for (int r = 2 * warp + (lane >> 4); r < kHeads; r += 2 * kScoreWarps) {
+    uint4 w = q_row(r);
+    uint32_t x[4] = {w.x, w.y, w.z, w.w};
+    float sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 f = unpack2<kBF16>(x[k]);
+      sum += alpha * (fabsf(f.x) + fabsf(f.y));
+      if constexpr (kF8 && kBF16) x[k] = pack2<false>(f.x * alpha, f.y * alpha);
+    }
+    w = make_uint4(x[0], x[1], x[2], x[3]);
+#pragma unroll
+    for (int o = 8; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (piece == 0) mag[r] = sum;
+    *reinterpret_cast<uint4*>(qs[0] + r * kQStride + piece * 16) = by_sign(w, false);
+    *reinterpret_cast<uint4*>(qs[1] + r * kQStride + piece * 16) = by_sign(w, true);
+  }
+  __syncthreads();
+  float q1 = 0.f;
   for (int r = 0; r < G; ++r) q1 = fmaxf(q1, mag[r]);
 
   const int32_t* bt = p.block_table + static_cast<int64_t>(b) * p.max_blocks_per_seq;
   constexpr int kRowBytes = kF8 ? kHeadDim : 2 * kHeadDim;
-  constexpr int kPieces = kRowBytes / 64;  // 16-byte pieces a lane has of a row
+  constexpr int kPieces = kRowBytes / 64;         // 16-byte pieces a lane has of a row
+  constexpr int kParts = kF8 ? 2 * kPieces : kPieces;  // of a row of q (16 bytes: two k-steps)
   const int64_t half = static_cast<int64_t>(p.h_kv) * kRowBytes;  // from a block's lo to its hi
   const uint8_t* bounds = static_cast<const uint8_t*>(p.bounds) + j * kRowBytes + t4 * 16;
-  const uint8_t* qrow = qs + g * kQStride;
+  // Head 8 nt + g's part i: dims 8 (t4 + 4 i) .. + 7, or (8-bit: the lane's piece i / 2 of
+  // a bounds row has dims 16 (t4 + 4 (i / 2)) .. + 15) the half i % 2 of them.
+  auto q_part = [&](int sign, int nt, int i) {
+    return *reinterpret_cast<const uint4*>(qs[sign] + (nt * 8 + g) * kQStride +
+                                           (kF8 ? (t4 + 4 * (i >> 1)) * 32 + (i & 1) * 16
+                                                : (t4 + 4 * i) * 16));
+  };
+  constexpr int kHeld = kHeads == 8 ? kParts : 1;
+  uint4 held[2][kHeld];
+  if constexpr (kHeads == 8) {
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) {
+      held[0][i] = q_part(0, 0, i);
+      held[1][i] = q_part(1, 0, i);
+    }
+  }
   float* scores = p.scores + bj * p.score_stride;
-  const int tiles = (blocks + 7) / 8, step = gridDim.x * kScoreWarps;
-  uint32_t widest = 0;  // the largest magnitude seen, packed
+  const int tiles = (blocks + kScoreBlocks - 1) / kScoreBlocks, step = gridDim.x * kScoreWarps;
+  // The largest bound and the largest of minus the bounds, packed (8-bit: the codes'
+  // magnitudes in the first).
+  uint32_t most_hi = kF8 ? 0u : (kBF16 ? 0xff80ff80u : 0xfc00fc00u), most_lo = most_hi;
   int tile = blockIdx.x * kScoreWarps + warp;
   // (-1 for blocks that are taken always: their bounds are not looked at.)
-  auto block_of = [&](int tl) {
-    const int t = tl * 8 + g;
-    return t >= p.first && t < blocks - p.last ? bt[t] : -1;
+  auto block_of = [&](int tl, int row) {
+    const int t = tl * kScoreBlocks + row;
+    return tl < tiles && t >= p.first && t < blocks - p.last ? bt[t] : -1;
   };
-  int id = tile < tiles ? block_of(tile) : -1;
+  int id[2] = {block_of(tile, g), block_of(tile, g + 8)};
   for (; tile < tiles; tile += step) {
-    uint4 lo[kPieces], hi[kPieces];
-    const bool there = id >= 0 && id < p.num_blocks;  // (a bad id: the second kernel reports it)
-    const uint8_t* at = bounds + static_cast<int64_t>(id) * 2 * half;
+    uint4 x[2][2][kPieces];  // blocks g and g + 8; lo and hi
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      lo[i] = hi[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (there) {
-        lo[i] = *reinterpret_cast<const uint4*>(at + i * 64);
-        hi[i] = *reinterpret_cast<const uint4*>(at + half + i * 64);
-      }
+    for (int r = 0; r < 2; ++r) {
+      const bool there = id[r] >= 0 && id[r] < p.num_blocks;  // (a bad id: the second kernel reports it)
+      const uint8_t* at = bounds + static_cast<int64_t>(id[r]) * 2 * half;
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+          x[r][e][i] = make_uint4(0u, 0u, 0u, 0u);
+          if (there) x[r][e][i] = *reinterpret_cast<const uint4*>(at + e * half + i * 64);
+        }
     }
-    id = tile + step < tiles ? block_of(tile + step) : -1;
-    float best[2] = {-kInf, -kInf};  // columns 2 t4 and 2 t4 + 1: blocks of the tile
+    id[0] = block_of(tile + step, g);
+    id[1] = block_of(tile + step, g + 8);
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      const uint32_t x[8] = {lo[i].x, lo[i].y, lo[i].z, lo[i].w, hi[i].x, hi[i].y, hi[i].z, hi[i].w};
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        widest = kF8 ? __vmaxu4(widest, x[k] & 0x7f7f7f7fu) : __vmaxu2(widest, x[k] & 0x7fff7fffu);
-    }
-#pragma unroll
-    for (int mt = 0; mt < kTiles; ++mt) {
-      if (mt * 16 >= G) break;
-      float acc[4][4] = {};  // chains: {plus, minus} x {first half, second half of the dims}
+    for (int r = 0; r < 2; ++r)
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) {
-        // The lane's piece i holds dims 8 (t4 + 4 i) .. + 7, or 16 (t4 + 4 i) .. + 15.
+        const uint4 l = x[r][0][i], h = x[r][1][i];
+        if constexpr (kF8) {
+          constexpr uint32_t kMag = 0x7f7f7f7fu;
+          most_hi = __vmaxu4(most_hi, __vmaxu4(__vmaxu4(l.x & kMag, l.y & kMag), __vmaxu4(l.z & kMag, l.w & kMag)));
+          most_hi = __vmaxu4(most_hi, __vmaxu4(__vmaxu4(h.x & kMag, h.y & kMag), __vmaxu4(h.z & kMag, h.w & kMag)));
+        } else {  // (lo <= hi: the largest magnitude is hi's largest or minus lo's smallest)
+          most_hi = max2<kBF16>(most_hi, max2<kBF16>(max2<kBF16>(h.x, h.y), max2<kBF16>(h.z, h.w)));
+          most_lo = max2<kBF16>(most_lo, max2<kBF16>(max2<kBF16>(l.x ^ 0x80008000u, l.y ^ 0x80008000u),
+                                                     max2<kBF16>(l.z ^ 0x80008000u, l.w ^ 0x80008000u)));
+        }
+      }
+    float best[2] = {-kInf, -kInf};  // of blocks g and g + 8
 #pragma unroll
-        for (int hf = 0; hf < (kF8 ? 2 : 1); ++hf) {
-          const uint8_t* a = qrow + mt * 16 * kQStride +
-                             (kF8 ? (t4 + 4 * i) * 32 + hf * 16 : (t4 + 4 * i) * 16);
-          const uint4 u = *reinterpret_cast<const uint4*>(a);
-          const uint4 v = *reinterpret_cast<const uint4*>(a + 8 * kQStride);
-          const uint32_t ua[4] = {u.x, u.y, u.z, u.w}, va[4] = {v.x, v.y, v.z, v.w};
+    for (int nt = 0; nt < kHeads / 8; ++nt) {
+      if (nt * 8 >= G) break;
+      float acc[4][4] = {};  // chains: {lo, hi} x {first half, second half of the dims}
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {  // two k-steps: words (0, 1) and (2, 3)
-            uint32_t plus[4], minus[4], l0, l1, h0, h1;
-            by_sign(ua[2 * k], plus[0], minus[0]);
-            by_sign(va[2 * k], plus[1], minus[1]);
-            by_sign(ua[2 * k + 1], plus[2], minus[2]);
-            by_sign(va[2 * k + 1], plus[3], minus[3]);
+      for (int i = 0; i < kPieces; ++i) {
+#pragma unroll
+        for (int hf = 0; hf < kParts / kPieces; ++hf) {
+          const int part_i = kF8 ? 2 * i + hf : i, c = kF8 ? 2 * i : 2 * (i >> 1);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {  // lo meets q^-, hi q^+
+            uint4 w;
+            if constexpr (kHeads == 8)
+              w = held[e ? 0 : 1][part_i];
+            else
+              w = q_part(e ? 0 : 1, nt, part_i);
+            const uint4 u = x[0][e][i], v = x[1][e][i];
             if constexpr (kF8) {
-              const uint32_t lw[4] = {lo[i].x, lo[i].y, lo[i].z, lo[i].w};
-              const uint32_t hw[4] = {hi[i].x, hi[i].y, hi[i].z, hi[i].w};
-              e4m3x4_to_f16x2(lw[2 * hf + k], l0, l1);
-              e4m3x4_to_f16x2(hw[2 * hf + k], h0, h1);
+              const uint32_t u2[2] = {hf ? u.z : u.x, hf ? u.w : u.y};
+              const uint32_t v2[2] = {hf ? v.z : v.x, hf ? v.w : v.y};
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                uint32_t a[4];
+                e4m3x4_to_f16x2(u2[k], a[0], a[2]);
+                e4m3x4_to_f16x2(v2[k], a[1], a[3]);
+                mma_16816<false>(acc[c + e], a, k ? w.z : w.x, k ? w.w : w.y);
+              }
             } else {
-              l0 = k ? lo[i].z : lo[i].x;
-              l1 = k ? lo[i].w : lo[i].y;
-              h0 = k ? hi[i].z : hi[i].x;
-              h1 = k ? hi[i].w : hi[i].y;
+              const uint32_t a0[4] = {u.x, v.x, u.y, v.y}, a1[4] = {u.z, v.z, u.w, v.w};
+              mma_16816<kMmaBF16>(acc[c + e], a0, w.x, w.y);
+              mma_16816<kMmaBF16>(acc[c + e], a1, w.z, w.w);
             }
-            const int c = kF8 ? 2 * i : 2 * (i >> 1);
-            mma_16816<kMmaBF16>(acc[c], plus, h0, h1);
-            mma_16816<kMmaBF16>(acc[c + 1], minus, l0, l1);
           }
         }
       }
+      // Element e of the lane: block g + 8 (e / 2), head 8 nt + 2 t4 + e % 2.
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         float s = (acc[0][e] + acc[1][e]) + (acc[2][e] + acc[3][e]);
         if (!(fabsf(s) < kInf)) s = kInf;  // not finite: to be scored in 64 bits
-        if (mt * 16 + g + (e >> 1) * 8 < G) best[e & 1] = fmaxf(best[e & 1], s);
+        if (nt * 8 + 2 * t4 + (e & 1) < G) best[e >> 1] = fmaxf(best[e >> 1], s);
       }
     }
 #pragma unroll
-    for (int o = 4; o < 32; o <<= 1) {
-      best[0] = fmaxf(best[0], __shfl_xor_sync(0xffffffffu, best[0], o));
-      best[1] = fmaxf(best[1], __shfl_xor_sync(0xffffffffu, best[1], o));
+    for (int r = 0; r < 2; ++r) {
+      best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 1));
+      best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 2));
+      if (t4 == 0) scores[tile * kScoreBlocks + g + 8 * r] = best[r];
     }
-    if (g == 0)
-      *reinterpret_cast<float2*>(scores + tile * 8 + 2 * t4) = make_float2(best[0], best[1]);
   }
   // This CTA's largest bound: E for its blocks (not finite if one of them is not).
-  float wide;
+  float wide = 0.f;
   if constexpr (kF8) {
     uint32_t h0, h1;
-    e4m3x4_to_f16x2(widest, h0, h1);
-    const float2 x = unpack2<false>(h0), y = unpack2<false>(h1);
-    wide = fmaxf(fmaxf(x.x, x.y), fmaxf(y.x, y.y));
-    if (x.x != x.x || x.y != x.y || y.x != y.x || y.y != y.y) wide = kInf;
+    e4m3x4_to_f16x2(most_hi, h0, h1);
+    const float2 u = unpack2<false>(h0), v = unpack2<false>(h1);
+    wide = fmaxf(fmaxf(u.x, u.y), fmaxf(v.x, v.y));
+    if (u.x != u.x || u.y != u.y || v.x != v.x || v.y != v.y) wide = kInf;
   } else {
-    const float2 x = unpack2<kBF16>(widest);
-    wide = x.x != x.x || x.y != x.y ? kInf : fmaxf(x.x, x.y);
+    const float2 u = unpack2<kBF16>(max2<kBF16>(most_hi, most_lo));
+    wide = u.x != u.x || u.y != u.y ? kInf : fmaxf(0.f, fmaxf(u.x, u.y));
   }
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) wide = fmaxf(wide, __shfl_xor_sync(0xffffffffu, wide, o));
@@ -553,10 +608,12 @@ cudaError_t launch_t(const SelectParams& p, cudaStream_t stream) {
   if (p.score_ctas > 0) {
     const dim3 grid(static_cast<unsigned>(p.score_ctas), static_cast<unsigned>(p.h_kv),
                     static_cast<unsigned>(p.batch));
-    if (p.group <= 16)
-      block_scores_kernel<kF8, kBF16, 1><<<grid, kScoreWarps * 32, 0, stream>>>(p);
+    if (p.group <= 8)
+      block_scores_kernel<kF8, kBF16, 8><<<grid, kScoreWarps * 32, 0, stream>>>(p);
+    else if (p.group <= 16)
+      block_scores_kernel<kF8, kBF16, 16><<<grid, kScoreWarps * 32, 0, stream>>>(p);
     else
-      block_scores_kernel<kF8, kBF16, 4><<<grid, kScoreWarps * 32, 0, stream>>>(p);
+      block_scores_kernel<kF8, kBF16, 64><<<grid, kScoreWarps * 32, 0, stream>>>(p);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
@@ -568,9 +625,10 @@ cudaError_t launch_t(const SelectParams& p, cudaStream_t stream) {
 
 int select_score_ctas(int batch, int h_kv, int blocks, int count, int num_sms) {
   if (blocks <= count) return 0;
-  // A warp's tile is 8 blocks; about two waves of eight CTAs an SM.
-  const int64_t most = (blocks + 8 * kScoreWarps - 1) / (8 * kScoreWarps);
-  const int64_t share = std::max<int64_t>(1, static_cast<int64_t>(num_sms) * 16 /
+  // About two waves of four CTAs an SM.
+  constexpr int kCta = kScoreBlocks * kScoreWarps;
+  const int64_t most = (blocks + kCta - 1) / kCta;
+  const int64_t share = std::max<int64_t>(1, static_cast<int64_t>(num_sms) * 8 /
                                                  (static_cast<int64_t>(batch) * h_kv));
   return static_cast<int>(std::min(most, share));
 }

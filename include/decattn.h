@@ -483,7 +483,8 @@ int gqa_block_bounds(const void* k_cache, const int32_t* block_table, const int3
  * gqa_select_blocks -- the blocks of each sequence's cache that matter most to
  * its query, per KV head, for gqa_decode_blocks.
  *   q            [batch, h_q, d_head] fp16/bf16 (launch->dtype), h_q / h_kv <= 64
- *   bounds       gqa_block_bounds' (kv_bytes 2: in launch->dtype; 1: e4m3 codes)
+ *   bounds       gqa_block_bounds' (kv_bytes 2: in launch->dtype; 1: e4m3 codes),
+ *                the first of each pair at most the second, or NaN
  *   selected     [batch, h_kv, count] int32 (written): block numbers within the
  *                sequence (0 is its first block), ascending, -1 behind the last
  *   first, last  how many of the sequence's first and last blocks are always
