@@ -12,6 +12,8 @@
 // columns l, l + 32, ...; the weights are computed one per lane and
 // broadcast, and the loads of all partials are independent of each other,
 // so a row costs about two dependent global-load latencies.
+#include <algorithm>
+
 #include "internal.h"
 #include "ptx.cuh"
 #include "weigh.cuh"
@@ -155,17 +157,23 @@ __global__ void __launch_bounds__(kWeighWarps * 32) weigh_kernel(const GqaParams
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const size_t row0 = static_cast<size_t>(b) * p.h_q + static_cast<size_t>(j) * G;
   if (static_cast<int>(blockIdx.x) < chunks) {
+    constexpr int kTokens = kWeighWarps * 32 * kVec;
     const int n = p.seq_lens[b], weighed = p.weighed_lens ? p.weighed_lens[b] : n - 1;
-    const int t0 = static_cast<int>(blockIdx.x) * kWeighWarps * 32 * kVec;
+    int t0 = static_cast<int>(blockIdx.x) * kTokens;
     if (t0 >= n || n > p.max_seq_len) return;
-    const int t = t0 + threadIdx.x * kVec;
     Weighed<kVec> tokens;
+    int t = t0 + threadIdx.x * kVec;
     if (t < n) tokens.load(p, j, b, t);
     weigh_lse<kWeighWarps>(p, row0, lse);
     __syncthreads();
     if (lse[0] == kPosInf) return;  // (bad data is met by every head of the group alike)
-    if (t < n) tokens.store(p, t, n, weighed, lse);
-    return;
+    for (;;) {
+      if (t < n) tokens.store(p, t, n, weighed, lse);
+      t0 += chunks * kTokens;
+      if (t0 >= n) return;
+      t = t0 + threadIdx.x * kVec;
+      if (t < n) tokens.load(p, j, b, t);
+    }
   }
   const size_t at = (row0 + blockIdx.x - chunks) * ns;
   float mx = kNegInf;  // the maximum of the numbers: NaN does not count
@@ -250,11 +258,15 @@ cudaError_t launch_mla_combine(const MlaCombineParams& p, bool bf16, cudaStream_
 }
 
 cudaError_t launch_weigh(const GqaParams& p, bool bf16, int num_sms, cudaStream_t stream) {
-  // Four tokens a thread, or one where that leaves SMs without a CTA.
+  // Four tokens a thread, or one where that leaves SMs without a CTA; CTAs for the
+  // longest sequence there can be, up to about five waves of them (with a bound far
+  // above the lengths most would find nothing to do).
   const int64_t units = static_cast<int64_t>(p.batch) * p.h_kv;
   const int threads = kWeighWarps * 32, most = p.max_seq_len > 0 ? p.max_seq_len : 1;
   const bool few = units * ((most - 1) / (4 * threads) + 1) < num_sms;
-  const int chunks = (most - 1) / (few ? threads : 4 * threads) + 1;
+  const int64_t cap = std::max<int64_t>(1, static_cast<int64_t>(num_sms) * 30 / units);
+  const int chunks = static_cast<int>(
+      std::min<int64_t>((most - 1) / (few ? threads : 4 * threads) + 1, cap));
   auto kern = bf16 ? (few ? weigh_kernel<true, 1> : weigh_kernel<true, 4>)
                    : (few ? weigh_kernel<false, 1> : weigh_kernel<false, 4>);
   cudaLaunchConfig_t cfg = {};

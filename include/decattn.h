@@ -588,9 +588,11 @@ int gqa_decode_weights_plan_splits(int batch, int h_q, int h_kv, int d_head, int
  * the others, the keep - recent with the largest weights (the earlier token where
  * they are equal; NaN is the largest), in their order.  KV heads choose for
  * themselves, so that one position may then hold different tokens' rows; keys
- * are moved as they are, with the rotation of the position that they had.  Slots
- * from position keep on are left as they were.  The bounds of the blocks
- * (gqa_block_bounds) have to be taken anew.
+ * are moved as they are, with the rotation of the position that they had (the
+ * positions that paged_plan gives later tokens count the tokens in the cache: the
+ * caller adds those evicted before it rotates).  Slots from position keep on are
+ * left as they were.  The bounds of the blocks (gqa_block_bounds) have to be taken
+ * anew.
  * A bad length (DECATTN_FLAG_BAD_SEQ_LEN) or block id (DECATTN_FLAG_BAD_BLOCK)
  * leaves the sequence as it is (new_lens 0).  Sequences that are evicted from must
  * not share blocks.  The caches, weights and outputs must not overlap.

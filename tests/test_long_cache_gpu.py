@@ -310,7 +310,7 @@ def test_selection_of_nearly_equal_blocks(fp8):
 @pytest.mark.parametrize("fp8", [False, True])
 def test_selection_by_values_that_are_not_finite(fp8):
     """NaN and infinities in bounds and queries; sums past 32 bits' range; NaN is +inf."""
-    for seed, what in enumerate(["nan", "inf", "-inf", "q nan", "q inf", "huge", "tiny"]):
+    for seed, what in enumerate(["nan", "inf", "-inf", "q nan", "q inf", "huge", "tiny", "smallest"]):
         x = _case([800, 640], 8, 2, "bf16", 16, 20 + seed, fp8=fp8)
         bounds, q = _bounds_of(x), x["q"].clone()
         t = x["table"].cpu().numpy()
@@ -329,6 +329,10 @@ def test_selection_by_values_that_are_not_finite(fp8):
             q *= 1e37
         elif what == "tiny":
             q *= 2.0**-120
+        elif what == "smallest":  # products below 32 bits' normal range
+            q *= 2.0**-124
+            if not fp8:
+                bounds *= 2.0**-14
         with np.errstate(over="ignore", invalid="ignore"):
             _same_choice(x, bounds, q=q, count=6)
 
@@ -667,6 +671,115 @@ def test_eviction_flags():
         for got, ref, had in zip((k, v, w), want, [*x["caches"], x["weights"]]):
             assert np.array_equal(_bytes(got[ids]), _bytes(had[ids]))
             assert np.array_equal(_bytes(got[other]), _bytes(ref[other]))
+
+
+# ------------------------------------------------------------------ streams, graphs, bounds
+
+
+def _calls_of(x, **kw):
+    """Each operator's call on x with fresh outputs, as a function of the stream, and the
+    tensors that it returns or updates."""
+    bounds, weights = _bounds_of(x), x["weights"]
+    lists = _i32(_lists(x, 9, 3, empty=False))
+    ws = torch.empty(da.gqa_weights_workspace_size(len(x["n"]), x["h_q"], x["max_len"], 4) + (1 << 20),
+                     dtype=torch.uint8, device=DEV)
+
+    def select(**k):
+        return [da.gqa_select_blocks(x["q"], bounds, x["table"], x["lens"], block_size=x["bs"],
+                                     max_seq_len=x["max_len"], count=6, workspace=ws, **kw, **k)]
+
+    def blocks(**k):
+        return [_decode(x, "blocks", x["table"], x["lens"], lists, scale=0.1, num_splits=3,
+                        workspace=ws, **kw, **k)]
+
+    def weighed(**k):
+        w = weights.clone()
+        return [_decode(x, "weights", w, x["table"], x["lens"], scale=0.1, num_splits=4, workspace=ws,
+                        **kw, **k), w]
+
+    def evict(**k):
+        c = [t.clone() for t in x["caches"]]
+        w = weights.clone()
+        e = da.gqa_kv_evict(*c, w, x["table"], x["lens"], max_seq_len=x["max_len"], keep=90, recent=9,
+                            limit=100, **kw, **k)
+        return [*(t.view(torch.uint8) for t in c), w, *e]
+
+    def bound(**k):
+        b = torch.zeros_like(bounds)
+        return [da.gqa_block_bounds(x["caches"][0], x["table"], x["lens"], b, max_seq_len=x["max_len"],
+                                    **kw, **k).view(torch.uint8)]
+
+    return select, blocks, weighed, evict, bound
+
+
+@pytest.mark.parametrize("heads", [(8, 2), (32, 1)])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_captured_calls_share_a_workspace(heads, fp8):
+    """Two graphs whose calls use the same workspace, replayed in turn over new queries."""
+    x = _case([700, 333, 100], *heads, "bf16", 16, 150, fp8=fp8)
+    y = _case([64, 900, 512], *heads, "bf16", 16, 151, fp8=fp8)
+    calls = [_calls_of(x), _calls_of(y)]
+    for fns in calls:
+        for fn in fns:
+            fn()
+    torch.cuda.synchronize()
+    graphs, outs, stream = [], [], torch.cuda.Stream()
+    for fns in calls:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=stream):
+            outs.append([t for fn in fns for t in fn()])
+    for seed in (1, 2):
+        for z, graph, out, fns in zip((x, y), graphs, outs, calls):
+            z["q"].copy_(torch.randn(z["q"].shape, generator=_gen(seed), device=DEV))
+            graph.replay()
+            torch.cuda.synchronize()
+            for got, want in zip(out, [t for fn in fns for t in fn()]):
+                assert torch.equal(got.view(torch.int32) if got.dtype == torch.float32 else got,
+                                   want.view(torch.int32) if want.dtype == torch.float32 else want)
+
+
+def test_calls_on_another_stream():
+    """On a given stream, and under one: the results of the default stream's calls; what is
+    returned may be dropped while it is in use."""
+    x = _case([700, 333, 100], 8, 2, "bf16", 16, 152)
+    want = [t for fn in _calls_of(x) for t in fn()]
+    torch.cuda.synchronize()
+    stream = torch.cuda.Stream()
+    for handle in (stream, stream.cuda_stream):
+        stream.wait_stream(torch.cuda.current_stream())
+        fns = _calls_of(x)
+        torch.cuda.synchronize()
+        got = []
+        for fn in fns:
+            r = fn(stream=handle) if fn.__name__ in ("select", "blocks") else None
+            if r is None:
+                with torch.cuda.stream(stream):
+                    r = fn()
+            got += r
+        torch.cuda.current_stream().wait_stream(stream)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("heads", [(8, 8), (8, 2), (32, 1)])
+def test_a_bound_far_above_the_lengths(heads):
+    """max_seq_len as a captured step has it (short sequences, a long bound) changes no
+    result."""
+    x = _case([700, 333, 1, 0], *heads, "bf16", 16, 153, most=4096)
+    bounds = _bounds_of(x)
+    x["max_len"] = 65536
+    assert torch.equal(bounds, _bounds_of(x))
+    _same_choice(x, bounds, count=6)
+    lists = _lists(x, 30, 4)
+    got = _decode(x, "blocks", x["table"], x["lens"], _i32(lists), scale=0.1)
+    ref, keys = _attend(x, 0.1, lists)
+    _close(x, got, ref, keys, 0.1)
+    before, w = x["weights"].clone(), x["weights"].clone()
+    got = _decode(x, "weights", w, x["table"], x["lens"], scale=0.1)
+    ref, keys = _attend(x, 0.1)
+    _close(x, got, ref, keys, 0.1)
+    _weights_close(x, w, before, ref, keys, 0.1)
+    if heads[0] != 32:
+        _same_eviction(x, 300, 20, 320)
 
 
 # ------------------------------------------------------------------ together
