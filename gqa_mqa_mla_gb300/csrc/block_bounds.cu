@@ -9,7 +9,8 @@
 // Bound by the keys' bytes: one pass, a warp to a (block, head), whose lanes
 // read 16-byte pieces of two (16-bit) or four (8-bit) token rows at once, eight
 // loads in flight each; the warps of a CTA take neighbouring heads of a block,
-// whose rows are neighbours in memory.
+// whose rows are neighbours in memory.  What the loads in flight can cover bounds
+// it: 5.5 TB/s, 0.83 of the measured copy, at 171k tokens of 8 heads.
 #include <algorithm>
 
 #include <cuda_bf16.h>
@@ -52,7 +53,7 @@ DECATTN_DEV uint32_t f16x2_to_e4m3x2(uint32_t x) {
 
 // kF8: e4m3 codes, compared as the fp16 values they stand for.
 template <bool kF8, bool kBF16>
-__global__ void __launch_bounds__(kThreads) block_bounds_kernel(const BoundsParams p) {
+__global__ void __launch_bounds__(kThreads, 5) block_bounds_kernel(const BoundsParams p) {
   constexpr int kLanes = kF8 ? 8 : 16;         // lanes to a token row of 128 or 256 bytes
   constexpr int kRows = 32 / kLanes;           // token rows a load
   constexpr int kWords = kF8 ? 8 : 4;          // 16-bit pairs in 16 bytes
@@ -93,22 +94,33 @@ __global__ void __launch_bounds__(kThreads) block_bounds_kernel(const BoundsPara
     before[threadIdx.x + 1] = upto;
     if (threadIdx.x == 0) before[0] = 0;
     __syncthreads();
-    const int64_t all = before[kThreads];
-    for (int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + warp; u < all;
-         u += static_cast<int64_t>(gridDim.x) * kWarps) {
+    const int64_t all = before[kThreads], stride = static_cast<int64_t>(gridDim.x) * kWarps;
+    // Unit u: its KV head, its block's id (-1: none, or a bad one) and that block's rows.
+    auto look_up = [&](int64_t u, int& j, int& id, int& rows) {
+      id = -1;
+      if (u >= all) return;
       int lo_b = 0, hi_b = kThreads;  // the last sequence with before <= u
       while (hi_b - lo_b > 1) {
         const int mid = (lo_b + hi_b) >> 1;
         if (before[mid] <= u) lo_b = mid; else hi_b = mid;
       }
-      const int n = lens[lo_b], k = static_cast<int>((u - before[lo_b]) / p.h_kv);
-      const int lb = firsts[lo_b] + k, j = static_cast<int>(u - before[lo_b] - static_cast<int64_t>(k) * p.h_kv);
-      const int id = p.block_table[static_cast<int64_t>(b0 + lo_b) * p.max_blocks_per_seq + lb];
+      const int k = static_cast<int>((u - before[lo_b]) / p.h_kv), lb = firsts[lo_b] + k;
+      j = static_cast<int>(u - before[lo_b] - static_cast<int64_t>(k) * p.h_kv);
+      rows = min(p.block_size, lens[lo_b] - (lb << lg));
+      id = p.block_table[static_cast<int64_t>(b0 + lo_b) * p.max_blocks_per_seq + lb];
+    };
+    int j, id, rows, next_j = 0, next_id = -1, next_rows = 0;
+    int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
+    look_up(u, next_j, next_id, next_rows);
+    for (; u < all; u += stride) {
+      j = next_j;
+      id = next_id;
+      rows = next_rows;
+      look_up(u + stride, next_j, next_id, next_rows);  // (behind this unit's loads)
       if (id < 0 || id >= p.num_blocks) {
         if (lane == 0) flag_error(p.err_flag, kFlagBadBlock);
         continue;
       }
-      const int rows = min(p.block_size, n - (lb << lg));
       const uint8_t* src = keys + static_cast<int64_t>(id) * p.block_size * row_bytes +
                            j * (kLanes * 16) + piece * 16;
       uint32_t lo[kWords], hi[kWords];
@@ -174,10 +186,11 @@ __global__ void __launch_bounds__(kThreads) block_bounds_kernel(const BoundsPara
 
 cudaError_t launch_block_bounds(const BoundsParams& p, bool e4m3, bool bf16, int num_sms,
                                 cudaStream_t stream) {
-  // A warp to each (block, head) that there can be, up to five CTAs an SM.
+  // A warp to each (block, head) that there can be, up to two waves of five CTAs an SM
+  // (4 prompts of 20-65k tokens: 45 us, one wave 46.5, with 8 CTAs of half the loads each 50).
   const int64_t blocks = (static_cast<int64_t>(p.max_seq_len) + p.block_size - 1) / p.block_size;
   const int64_t units = std::max<int64_t>(1, (blocks * p.h_kv * p.batch + kWarps - 1) / kWarps);
-  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(units, static_cast<int64_t>(num_sms) * 5)));
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(units, static_cast<int64_t>(num_sms) * 10)));
   if (e4m3)
     block_bounds_kernel<true, false><<<grid, kThreads, 0, stream>>>(p);
   else if (bf16)
