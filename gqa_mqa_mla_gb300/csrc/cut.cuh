@@ -34,10 +34,12 @@ DECATTN_DEV float key_value(uint32_t k) {
 template <bool kCluster>
 struct Team {
   DECATTN_DEV static void sync() {
-    if constexpr (kCluster)
+    if constexpr (kCluster) {
+      __syncwarp();  // (the cluster's barrier is for whole warps)
       cluster_sync();
-    else
+    } else {
       __syncthreads();
+    }
   }
   DECATTN_DEV static int size() { return kCluster ? static_cast<int>(gridDim.x) : 1; }
   DECATTN_DEV static int rank() { return kCluster ? static_cast<int>(blockIdx.x) : 0; }

@@ -260,10 +260,10 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const Se
   __syncthreads();
   if (threadIdx.x == 0) {
     for (int w = 0; w < kScoreWarps; ++w) wide = fmaxf(wide, part[w]);
-    // (Beyond 1e37 a sum could overflow; NaN is a product of 0 and an infinity; products
-    // below 2^-126 may count as 0: 128 of them.)
-    const float m = q1 * wide;
-    p.error[bj * gridDim.x + blockIdx.x] = m < 1e37f ? fmaf(kError, m, 0x1p-119f) : kInf;
+    // (Beyond 1e37 a sum could overflow, NaN is a product of 0 and an infinity; factors
+    // and products below 2^-126 may count as 0, 128 of them.)
+    const float m = q1 * wide, lost = 0x1p-118f * (1.f + wide + q1);
+    p.error[bj * gridDim.x + blockIdx.x] = m < 1e37f ? fmaf(kError, m, lost) : kInf;
   }
 }
 

@@ -307,15 +307,21 @@ def test_selection_of_nearly_equal_blocks(fp8):
         _same_choice(x, b, q=q, count=count)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("fp8", [False, True])
-def test_selection_by_values_that_are_not_finite(fp8):
-    """NaN and infinities in bounds and queries; sums past 32 bits' range; NaN is +inf."""
+def test_selection_by_values_that_are_not_finite(fp8, dtype):
+    """NaN and infinities in bounds and queries; sums past 32 bits' range or below its
+    normal one; NaN is +inf."""
     for seed, what in enumerate(["nan", "inf", "-inf", "q nan", "q inf", "huge", "tiny", "smallest"]):
-        x = _case([800, 640], 8, 2, "bf16", 16, 20 + seed, fp8=fp8)
+        x = _case([800, 640], 8, 2, dtype, 16, 20 + seed, fp8=fp8)
         bounds, q = _bounds_of(x), x["q"].clone()
         t = x["table"].cpu().numpy()
         view = bounds.view(torch.uint8) if fp8 else bounds
-        if what == "nan":
+        if what in ("huge", "tiny", "smallest") and dtype == "fp16":
+            q *= {"huge": 1e4, "tiny": 2.0**-14, "smallest": 2.0**-20}[what]
+            if what == "smallest" and not fp8:
+                bounds *= 2.0**-16
+        elif what == "nan":
             view[int(t[0, 7]), :, 0, 3] = 0x7F if fp8 else float("nan")
             view[int(t[1, 9]), 0, 1, 3] = 0xFF if fp8 else float("nan")
         elif what in ("inf", "-inf") and not fp8:
