@@ -787,7 +787,7 @@ size_t gqa_select_workspace_size(int batch, int h_kv, int max_seq_len, int block
   if (blocks <= count) return 0;
   const size_t units = static_cast<size_t>(batch) * h_kv, stride = (blocks + 15) / 16 * 16;
   return align_up(units * stride * sizeof(uint64_t)) + align_up(units * stride * sizeof(float)) +
-         align_up(units * ((stride + 31) / 32) * sizeof(float));
+         align_up(units * (stride / 16) * sizeof(float));
 }
 
 int gqa_select_blocks(const void* q, const void* bounds, const int32_t* block_table,
@@ -832,7 +832,7 @@ int gqa_select_blocks(const void* q, const void* bounds, const int32_t* block_ta
   if (sms <= 0) return DECATTN_ERR_CUDA;
   plan_choice(p, static_cast<int>(blocks), sms);
   if (blocks > count) {
-    p.score_ctas = select_score_ctas(L->batch, h_kv, static_cast<int>(blocks), count, sms);
+    plan_scores(p, static_cast<int>(blocks), sms);
     const size_t all = static_cast<size_t>(L->batch) * h_kv * p.score_stride;
     char* ws = static_cast<char*>(L->workspace);
     p.exact = reinterpret_cast<uint64_t*>(ws);

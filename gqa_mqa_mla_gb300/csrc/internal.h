@@ -194,6 +194,7 @@ struct SelectParams {
   int batch, h_kv, group;
   int count, first, last;     // first + last <= count
   int score_ctas;             // CTAs a sequence and KV head; 0: no sequence has a choice to make
+  int score_heads;            // KV heads to each of them
   int team;                   // CTAs of the second kernel to a sequence and KV head
   int cached_blocks;          // scores that each keeps in shared memory
   int block_size, log2_block_size, num_blocks, max_blocks_per_seq, max_seq_len;
@@ -273,7 +274,7 @@ cudaError_t launch_paged_plan(const PlanParams& p, cudaStream_t stream);
 cudaError_t launch_rope_append(const RopeParams& p, bool e4m3, bool bf16, cudaStream_t stream);
 cudaError_t launch_block_bounds(const BoundsParams& p, bool e4m3, bool bf16, int num_sms,
                                 cudaStream_t stream);
-int select_score_ctas(int batch, int h_kv, int blocks, int count, int num_sms);
+void plan_scores(SelectParams& p, int blocks, int num_sms);
 void plan_choice(SelectParams& p, int blocks, int num_sms);
 cudaError_t launch_select_blocks(const SelectParams& p, bool e4m3, bool bf16, cudaStream_t stream);
 cudaError_t launch_kv_evict(EvictParams p, int num_sms, cudaStream_t stream);

@@ -58,108 +58,157 @@ DECATTN_DEV uint32_t max2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// kHeads: 8 (their fragments in registers), 16 or 64 heads a KV head at most.
-template <bool kF8, bool kBF16, int kHeads>
+// What a warp knows of its KV head's queries: the largest sum of magnitudes of a row (of
+// what is multiplied), and for up to 8 of them their B fragments.
+template <bool kF8, bool kBF16>
+DECATTN_DEV float fp16_scale(float most) {
+  // Over 8 bits q is multiplied as fp16, a bf16 query times the power of two that brings
+  // the group's largest value to 2^14 .. 2^15 (the scores of the pair (b, j) then all
+  // carry that factor; what falls below fp16's smallest step is 2^-38 of that value).
+  if constexpr (!kF8 || !kBF16) return 1.f;
+  const int e = static_cast<int>(__float_as_uint(most) >> 23) - 127;  // 128: infinite
+  const int k = e >= 128 ? 0 : min(14 - e, 126);
+  return __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
+}
+template <bool kBF16>
+DECATTN_DEV float largest(uint4 w) {
+  const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+  float most = 0.f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 f = unpack2<kBF16>(x[k]);
+    most = fmaxf(most, fmaxf(fabsf(f.x), fabsf(f.y)));
+  }
+  return most;
+}
+// w times alpha, as it is multiplied, and the sum of its magnitudes added to `sum`.
+template <bool kF8, bool kBF16>
+DECATTN_DEV uint4 scaled(uint4 w, float alpha, float& sum) {
+  uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 f = unpack2<kBF16>(x[k]);
+    sum += alpha * (fabsf(f.x) + fabsf(f.y));
+    if constexpr (kF8 && kBF16) x[k] = pack2<false>(f.x * alpha, f.y * alpha);
+  }
+  return make_uint4(x[0], x[1], x[2], x[3]);
+}
+
+// kHeads: 8 (their fragments in registers), 16 or 64 heads a KV head at most.  kSpread
+// (8): a CTA's warps take p.score_heads neighbouring KV heads of the same blocks, whose
+// bounds are neighbours in memory, and load the queries themselves (32 sequences of
+// 16-32k tokens, 196 MB: 34.5 us, 36.5 with a KV head to a CTA); else a CTA's warps share
+// one KV head's, which lie in shared memory.
+template <bool kF8, bool kBF16, int kHeads, bool kSpread>
 __global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const SelectParams p) {
   constexpr bool kMmaBF16 = kBF16 && !kF8;
-  __shared__ __align__(16) uint8_t qs[2][kHeads * kQStride];  // q^+, q^-
-  __shared__ float mag[kHeads], part[kScoreWarps];
+  constexpr int kRows = kSpread ? 1 : kHeads;
+  static_assert(!kSpread || kHeads == 8, "fragments in registers");
+  __shared__ __align__(16) uint8_t qs[2][kRows * kQStride];  // q^+, q^-
+  __shared__ float mag[kRows], part[kScoreWarps];
   launch_dependents();
-  const int j = blockIdx.y, b = blockIdx.z, G = p.group;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+  const int heads = kSpread ? p.score_heads : 1;  // (a power of two that divides h_kv)
+  const int j = blockIdx.y * heads + (warp & (heads - 1)), b = blockIdx.z, G = p.group;
+  const int sub = kSpread ? warp / heads : warp, subs = kScoreWarps / heads;
   const int64_t bj = static_cast<int64_t>(b) * p.h_kv + j;
   const int n = p.seq_lens[b];
   const int blocks = n > 0 && n <= p.max_seq_len ? ((n - 1) >> p.log2_block_size) + 1 : 0;
   // Nothing to choose (or a bad length, which the second kernel reports).
   if (blocks <= p.count) return;
 
-  // q of the group (rows past it zero); over 8 bits as fp16, a bf16 query times the
-  // power of two that brings the group's largest value to 2^14 .. 2^15 (the
-  // scores of the pair (b, j) then all carry that factor; what falls below fp16's
-  // smallest step is 2^-38 of that value).  16 lanes have a row, 8 values each.
-  const uint16_t* q = static_cast<const uint16_t*>(p.q) + bj * G * kHeadDim;
-  float alpha = 1.f;
-  const int piece = lane & 15;
-  auto q_row = [&](int r) {
-    return r < G ? *reinterpret_cast<const uint4*>(q + r * kHeadDim + piece * 8) : make_uint4(0, 0, 0, 0);
-  };
-  if constexpr (kF8 && kBF16) {
-    for (int r = 2 * warp + (lane >> 4); r < kHeads; r += 2 * kScoreWarps) {
-      const uint4 w = q_row(r);
-      const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-      float most = 0.f;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 f = unpack2<true>(x[k]);
-        most = fmaxf(most, fmaxf(fabsf(f.x), fabsf(f.y)));
-      }
-#pragma unroll
-      for (int o = 8; o >= 1; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-      if (piece == 0) mag[r] = most;
-    }
-    __syncthreads();
-    float most = 0.f;
-    for (int r = 0; r < G; ++r) most = fmaxf(most, mag[r]);
-    const int e = static_cast<int>(__float_as_uint(most) >> 23) - 127;  // 128: infinite
-    const int k = e >= 128 ? 0 : min(14 - e, 126);
-    alpha = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
-    __syncthreads();
-  }
-  for (int r = 2 * warp + (lane >> 4); r < kHeads; r += 2 * kScoreWarps) {
-    uint4 w = q_row(r);
-    uint32_t x[4] = {w.x, w.y, w.z, w.w};
-    float sum = 0.f;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 f = unpack2<kBF16>(x[k]);
-      sum += alpha * (fabsf(f.x) + fabsf(f.y));
-      if constexpr (kF8 && kBF16) x[k] = pack2<false>(f.x * alpha, f.y * alpha);
-    }
-    w = make_uint4(x[0], x[1], x[2], x[3]);
-#pragma unroll
-    for (int o = 8; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (piece == 0) mag[r] = sum;
-    *reinterpret_cast<uint4*>(qs[0] + r * kQStride + piece * 16) = by_sign(w, false);
-    *reinterpret_cast<uint4*>(qs[1] + r * kQStride + piece * 16) = by_sign(w, true);
-  }
-  __syncthreads();
-  float q1 = 0.f;
-  for (int r = 0; r < G; ++r) q1 = fmaxf(q1, mag[r]);
-
   const int32_t* bt = p.block_table + static_cast<int64_t>(b) * p.max_blocks_per_seq;
-  constexpr int kRowBytes = kF8 ? kHeadDim : 2 * kHeadDim;
-  constexpr int kPieces = kRowBytes / 64;         // 16-byte pieces a lane has of a row
-  constexpr int kParts = kF8 ? 2 * kPieces : kPieces;  // of a row of q (16 bytes: two k-steps)
-  const int64_t half = static_cast<int64_t>(p.h_kv) * kRowBytes;  // from a block's lo to its hi
-  const uint8_t* bounds = static_cast<const uint8_t*>(p.bounds) + j * kRowBytes + t4 * 16;
-  // Head 8 nt + g's part i: dims 8 (t4 + 4 i) .. + 7, or (8-bit: the lane's piece i / 2 of
-  // a bounds row has dims 16 (t4 + 4 (i / 2)) .. + 15) the half i % 2 of them.
-  auto q_part = [&](int sign, int nt, int i) {
-    return *reinterpret_cast<const uint4*>(qs[sign] + (nt * 8 + g) * kQStride +
-                                           (kF8 ? (t4 + 4 * (i >> 1)) * 32 + (i & 1) * 16
-                                                : (t4 + 4 * i) * 16));
-  };
-  constexpr int kHeld = kHeads == 8 ? kParts : 1;
-  uint4 held[2][kHeld];
-  if constexpr (kHeads == 8) {
-#pragma unroll
-    for (int i = 0; i < kParts; ++i) {
-      held[0][i] = q_part(0, 0, i);
-      held[1][i] = q_part(1, 0, i);
-    }
-  }
-  float* scores = p.scores + bj * p.score_stride;
-  const int tiles = (blocks + kScoreBlocks - 1) / kScoreBlocks, step = gridDim.x * kScoreWarps;
-  // The largest bound and the largest of minus the bounds, packed (8-bit: the codes'
-  // magnitudes in the first).
-  uint32_t most_hi = kF8 ? 0u : (kBF16 ? 0xff80ff80u : 0xfc00fc00u), most_lo = most_hi;
-  int tile = blockIdx.x * kScoreWarps + warp;
+  const int tiles = (blocks + kScoreBlocks - 1) / kScoreBlocks, step = gridDim.x * subs;
+  int tile = blockIdx.x * subs + sub;
   // (-1 for blocks that are taken always: their bounds are not looked at.)
   auto block_of = [&](int tl, int row) {
     const int t = tl * kScoreBlocks + row;
     return tl < tiles && t >= p.first && t < blocks - p.last ? bt[t] : -1;
   };
   int id[2] = {block_of(tile, g), block_of(tile, g + 8)};
+  constexpr int kRowBytes = kF8 ? kHeadDim : 2 * kHeadDim;
+  constexpr int kPieces = kRowBytes / 64;         // 16-byte pieces a lane has of a row
+  constexpr int kParts = kF8 ? 2 * kPieces : kPieces;  // of a row of q (16 bytes: two k-steps)
+  const int64_t half = static_cast<int64_t>(p.h_kv) * kRowBytes;  // from a block's lo to its hi
+  const uint8_t* bounds = static_cast<const uint8_t*>(p.bounds) + j * kRowBytes + t4 * 16;
+  // A head's part i: dims 8 (t4 + 4 i) .. + 7, or (8-bit: the lane's piece i / 2 of a
+  // bounds row has dims 16 (t4 + 4 (i / 2)) .. + 15) the half i % 2 of them.  In bytes:
+  auto part_at = [&](int i) {
+    return kF8 ? (t4 + 4 * (i >> 1)) * 32 + (i & 1) * 16 : (t4 + 4 * i) * 16;
+  };
+  const uint8_t* q = static_cast<const uint8_t*>(p.q) + bj * G * (2 * kHeadDim);
+  float q1 = 0.f;
+  uint4 held[2][kHeads == 8 ? kParts : 1];
+  auto q_part = [&](int sign, int nt, int i) {
+    return *reinterpret_cast<const uint4*>(qs[sign] + (nt * 8 + g) * kQStride + part_at(i));
+  };
+  if constexpr (kSpread) {
+    uint4 w[kParts];
+    float most = 0.f, sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) {
+      w[i] = make_uint4(0, 0, 0, 0);
+      if (g < G) w[i] = *reinterpret_cast<const uint4*>(q + g * (2 * kHeadDim) + part_at(i));
+      most = fmaxf(most, largest<kBF16>(w[i]));
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    const float alpha = fp16_scale<kF8, kBF16>(most);
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) {
+      w[i] = scaled<kF8, kBF16>(w[i], alpha, sum);
+      held[0][i] = by_sign(w[i], false);
+      held[1][i] = by_sign(w[i], true);
+    }
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+    q1 = fmaxf(0.f, sum);
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) q1 = fmaxf(q1, __shfl_xor_sync(0xffffffffu, q1, o));
+  } else {
+    // 16 lanes have a row, 8 values each (rows past the group: zeros).
+    const int piece = lane & 15;
+    auto q_row = [&](int r) {
+      return r < G ? *reinterpret_cast<const uint4*>(q + r * (2 * kHeadDim) + piece * 16)
+                   : make_uint4(0, 0, 0, 0);
+    };
+    float alpha = 1.f;
+    if constexpr (kF8 && kBF16) {
+      for (int r = 2 * warp + (lane >> 4); r < kHeads; r += 2 * kScoreWarps) {
+        float most = largest<kBF16>(q_row(r));
+#pragma unroll
+        for (int o = 8; o >= 1; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+        if (piece == 0) mag[r] = most;
+      }
+      __syncthreads();
+      float most = 0.f;
+      for (int r = 0; r < G; ++r) most = fmaxf(most, mag[r]);
+      alpha = fp16_scale<kF8, kBF16>(most);
+      __syncthreads();
+    }
+    for (int r = 2 * warp + (lane >> 4); r < kHeads; r += 2 * kScoreWarps) {
+      float sum = 0.f;
+      const uint4 w = scaled<kF8, kBF16>(q_row(r), alpha, sum);
+#pragma unroll
+      for (int o = 8; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (piece == 0) mag[r] = sum;
+      *reinterpret_cast<uint4*>(qs[0] + r * kQStride + piece * 16) = by_sign(w, false);
+      *reinterpret_cast<uint4*>(qs[1] + r * kQStride + piece * 16) = by_sign(w, true);
+    }
+    __syncthreads();
+    for (int r = 0; r < G; ++r) q1 = fmaxf(q1, mag[r]);
+    if constexpr (kHeads == 8) {
+#pragma unroll
+      for (int i = 0; i < kParts; ++i) {
+        held[0][i] = q_part(0, 0, i);
+        held[1][i] = q_part(1, 0, i);
+      }
+    }
+  }
+  float* scores = p.scores + bj * p.score_stride;
+  // The largest bound and the largest of minus the bounds, packed (8-bit: the codes'
+  // magnitudes in the first).
+  uint32_t most_hi = kF8 ? 0u : (kBF16 ? 0xff80ff80u : 0xfc00fc00u), most_lo = most_hi;
   for (; tile < tiles; tile += step) {
     uint4 x[2][2][kPieces];  // blocks g and g + 8; lo and hi
 #pragma unroll
@@ -258,8 +307,8 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const Se
   for (int o = 16; o >= 1; o >>= 1) wide = fmaxf(wide, __shfl_xor_sync(0xffffffffu, wide, o));
   if (lane == 0) part[warp] = wide;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 0; w < kScoreWarps; ++w) wide = fmaxf(wide, part[w]);
+  if (lane == 0 && sub == 0) {
+    for (int w = 1; w < subs; ++w) wide = fmaxf(wide, part[warp + w * heads]);
     // (Beyond 1e37 a sum could overflow, NaN is a product of 0 and an infinity; factors
     // and products below 2^-126 may count as 0, 128 of them.)
     const float m = q1 * wide, lost = 0x1p-118f * (1.f + wide + q1);
@@ -607,14 +656,16 @@ cudaError_t launch_choice(const SelectParams& p, cudaStream_t stream) {
 template <bool kF8, bool kBF16>
 cudaError_t launch_t(const SelectParams& p, cudaStream_t stream) {
   if (p.score_ctas > 0) {
-    const dim3 grid(static_cast<unsigned>(p.score_ctas), static_cast<unsigned>(p.h_kv),
-                    static_cast<unsigned>(p.batch));
-    if (p.group <= 8)
-      block_scores_kernel<kF8, kBF16, 8><<<grid, kScoreWarps * 32, 0, stream>>>(p);
+    const dim3 grid(static_cast<unsigned>(p.score_ctas),
+                    static_cast<unsigned>(p.h_kv / p.score_heads), static_cast<unsigned>(p.batch));
+    if (p.score_heads > 1)
+      block_scores_kernel<kF8, kBF16, 8, true><<<grid, kScoreWarps * 32, 0, stream>>>(p);
+    else if (p.group <= 8)
+      block_scores_kernel<kF8, kBF16, 8, false><<<grid, kScoreWarps * 32, 0, stream>>>(p);
     else if (p.group <= 16)
-      block_scores_kernel<kF8, kBF16, 16><<<grid, kScoreWarps * 32, 0, stream>>>(p);
+      block_scores_kernel<kF8, kBF16, 16, false><<<grid, kScoreWarps * 32, 0, stream>>>(p);
     else
-      block_scores_kernel<kF8, kBF16, 64><<<grid, kScoreWarps * 32, 0, stream>>>(p);
+      block_scores_kernel<kF8, kBF16, 64, false><<<grid, kScoreWarps * 32, 0, stream>>>(p);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
@@ -624,14 +675,22 @@ cudaError_t launch_t(const SelectParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-int select_score_ctas(int batch, int h_kv, int blocks, int count, int num_sms) {
-  if (blocks <= count) return 0;
+// The first kernel's CTAs to a sequence and its KV heads (p.score_heads to a CTA).
+void plan_scores(SelectParams& p, int blocks, int num_sms) {
+  p.score_heads = 1;
+  p.score_ctas = 0;
+  if (blocks <= p.count) return;
+  // (Up to two tiles a warp of the GPU there is no stream to keep together: one sequence
+  // of 131072 tokens 23.1 us with a head to a CTA, 24.6 with four; 32 of 16-32k 49.2, 47.3.)
+  const int64_t tiles = static_cast<int64_t>(p.batch) * p.h_kv * ((blocks + kScoreBlocks - 1) / kScoreBlocks);
+  if (p.group <= 8 && tiles > static_cast<int64_t>(num_sms) * 16 * 2)
+    while (p.score_heads < kScoreWarps && p.h_kv % (2 * p.score_heads) == 0) p.score_heads *= 2;
   // About two waves of four CTAs an SM.
-  constexpr int kCta = kScoreBlocks * kScoreWarps;
-  const int64_t most = (blocks + kCta - 1) / kCta;
-  const int64_t share = std::max<int64_t>(1, static_cast<int64_t>(num_sms) * 8 /
-                                                 (static_cast<int64_t>(batch) * h_kv));
-  return static_cast<int>(std::min(most, share));
+  const int cta = kScoreBlocks * kScoreWarps / p.score_heads;
+  const int64_t most = (blocks + cta - 1) / cta;
+  const int64_t share = std::max<int64_t>(
+      1, static_cast<int64_t>(num_sms) * 8 / (static_cast<int64_t>(p.batch) * (p.h_kv / p.score_heads)));
+  p.score_ctas = static_cast<int>(std::min(most, share));
 }
 
 // The second kernel's CTAs to a sequence and KV head: a cluster of up to eight, while
