@@ -787,7 +787,7 @@ size_t gqa_select_workspace_size(int batch, int h_kv, int max_seq_len, int block
   if (blocks <= count) return 0;
   const size_t units = static_cast<size_t>(batch) * h_kv, stride = (blocks + 15) / 16 * 16;
   return align_up(units * stride * sizeof(uint64_t)) + align_up(units * stride * sizeof(float)) +
-         align_up(units * (stride / 16) * sizeof(float));
+         align_up(units * (stride / 16) * sizeof(uint4));
 }
 
 int gqa_select_blocks(const void* q, const void* bounds, const int32_t* block_table,
@@ -839,7 +839,7 @@ int gqa_select_blocks(const void* q, const void* bounds, const int32_t* block_ta
     ws += align_up(all * sizeof(uint64_t));
     p.scores = reinterpret_cast<float*>(ws);
     ws += align_up(all * sizeof(float));
-    p.error = reinterpret_cast<float*>(ws);
+    p.parts = reinterpret_cast<uint4*>(ws);
   }
   const cudaError_t e = launch_select_blocks(p, kv_bytes == 1, L->dtype == DECATTN_BF16,
                                              static_cast<cudaStream_t>(L->stream));

@@ -149,40 +149,45 @@ DECATTN_DEV void cut_prepare(CutScratch& s) {
 // many lanes of a warp hold is counted once for all.
 // key(i, k) gives entry i's key (of this CTA's n) and whether it takes part; lo, hi:
 // the range of the keys that this thread has looked at (all are by the team's
-// threads; empty: lo > hi); 1 <= m <= the team's entries that take part.  Called by all
-// kThreads threads of each CTA; ends behind a barrier.
-template <int kThreads, bool kCluster, class Key>
+// threads; empty: lo > hi), or kKnown: that of the team's keys; 1 <= m <= the team's
+// entries that take part.  Called by all kThreads threads of each CTA; ends behind a
+// barrier.
+template <int kThreads, bool kCluster, bool kKnown, class Key>
 DECATTN_DEV Cut cut_largest(CutScratch& s, uint32_t lo, uint32_t hi, int n, int m, Key key) {
   using T = Team<kCluster>;
   constexpr int kOwn = kCutBins / kThreads;
   static_assert(kCutBins % kThreads == 0 && kThreads % 32 == 0 && kThreads >= kCutFew, "bins");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  lo = __reduce_min_sync(0xffffffffu, lo);
-  hi = __reduce_max_sync(0xffffffffu, hi);
-  if (lane == 0) {
-    atomicMin(&s.lo, lo);
-    atomicMax(&s.hi, hi);
-  }
 #pragma unroll
   for (int k = 0; k < kOwn; ++k) s.bins[tid + k * kThreads] = 0;
-  T::sync();
-  if constexpr (kCluster) {
-    if (warp == 0) {
-      lo = lane < T::size() ? T::get(s.lo, lane) : 0xffffffffu;
-      hi = lane < T::size() ? T::get(s.hi, lane) : 0u;
-      lo = __reduce_min_sync(0xffffffffu, lo);
-      hi = __reduce_max_sync(0xffffffffu, hi);
-      if (lane == 0) {
-        s.own[0] = lo;
-        s.own[1] = hi;
-      }
-    }
+  if constexpr (kKnown) {
     __syncthreads();
-    lo = s.own[0];
-    hi = s.own[1];
   } else {
-    lo = s.lo;
-    hi = s.hi;
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    if (lane == 0) {
+      atomicMin(&s.lo, lo);
+      atomicMax(&s.hi, hi);
+    }
+    T::sync();
+    if constexpr (kCluster) {
+      if (warp == 0) {
+        lo = lane < T::size() ? T::get(s.lo, lane) : 0xffffffffu;
+        hi = lane < T::size() ? T::get(s.hi, lane) : 0u;
+        lo = __reduce_min_sync(0xffffffffu, lo);
+        hi = __reduce_max_sync(0xffffffffu, hi);
+        if (lane == 0) {
+          s.own[0] = lo;
+          s.own[1] = hi;
+        }
+      }
+      __syncthreads();
+      lo = s.own[0];
+      hi = s.own[1];
+    } else {
+      lo = s.lo;
+      hi = s.hi;
+    }
   }
   while (lo < hi) {
     // Key k falls into bin (k - lo) >> shift.
@@ -272,35 +277,31 @@ DECATTN_DEV Cut cut_largest(CutScratch& s, uint32_t lo, uint32_t hi, int n, int 
 }
 
 // Go through the team's entries in order, this CTA's n behind those of the CTAs before
-// it: kind(i) is 0 (not listed), 1 (listed) or 2 (the first `ties` of these are listed);
-// emit(i, rank) for each listed entry with its place in the list.  Returns the first
-// place of this CTA's entries and the one behind its last.  A warp takes a run of
-// entries: it counts them, and when all have, gives out their places; lane s keeps
-// what it saw in step s (of the first 32, then kind is asked again).
+// it: kind(i, again) is 0 (out), 1 (in) or 2 (tied); settle(in, tied) is told the team's totals
+// (by all threads, behind a barrier); emit(i, tied?, in before, tied before) sees each
+// entry that is not out, with the numbers of the team's entries before it.  Returns the
+// entries in and tied of the CTAs before this one, and this one's.  A warp takes a run
+// of entries: it counts them, and when all have, goes through them again; lane s
+// keeps what it saw in step s (of the first 32, then kind is asked again).
 struct ListScratch {
   int in[32], tied[32];
   int all_in, all_tied;
 };
-template <int kThreads, bool kCluster, class Kind, class Emit>
-DECATTN_DEV int2 list_in_order(ListScratch& s, int n, int ties, Kind kind, Emit emit) {
+template <int kThreads, bool kCluster, class Kind, class Settle, class Emit>
+DECATTN_DEV int4 list_in_order(ListScratch& s, int n, Kind kind, Settle settle, Emit emit) {
   using T = Team<kCluster>;
   constexpr int kWarps = kThreads / 32;
   static_assert(kWarps <= 32, "warps of a CTA");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int steps = (n + kThreads - 1) / kThreads;  // of a warp's run
   const int begin = warp * steps * 32;
-  auto look = [&](int st, unsigned& in, unsigned& tied) {
-    const int i = begin + st * 32 + lane;
-    const int k = i < n ? kind(i) : 0;
-    in = __ballot_sync(0xffffffffu, k == 1);
-    tied = __ballot_sync(0xffffffffu, k == 2);
-  };
-  int in = 0, tied = 0;
   unsigned kept_in = 0, kept_tied = 0;
+  int in = 0, tied = 0;
 #pragma unroll 2
   for (int st = 0; st < steps; ++st) {
-    unsigned a, b;
-    look(st, a, b);
+    const int i = begin + st * 32 + lane;
+    const int k = i < n ? kind(i, false) : 0;
+    const unsigned a = __ballot_sync(0xffffffffu, k == 1), b = __ballot_sync(0xffffffffu, k == 2);
     if (lane == st) {
       kept_in = a;
       kept_tied = b;
@@ -318,32 +319,51 @@ DECATTN_DEV int2 list_in_order(ListScratch& s, int n, int ties, Kind kind, Emit 
   tied = __reduce_add_sync(0xffffffffu, lane < warp ? tied_here : 0);
   in_here = __reduce_add_sync(0xffffffffu, in_here);
   tied_here = __reduce_add_sync(0xffffffffu, tied_here);
-  int in_before = 0, tied_before = 0;  // in the CTAs before this one
+  int in_before = 0, tied_before = 0, in_all = in_here, tied_all = tied_here;
   if constexpr (kCluster) {
     if (threadIdx.x == 0) {
       s.all_in = in_here;
       s.all_tied = tied_here;
     }
     T::sync();
-    in_before = __reduce_add_sync(0xffffffffu, lane < T::rank() ? T::get(s.all_in, lane) : 0);
-    tied_before = __reduce_add_sync(0xffffffffu, lane < T::rank() ? T::get(s.all_tied, lane) : 0);
+    const int a = lane < T::size() ? T::get(s.all_in, lane) : 0;
+    const int b = lane < T::size() ? T::get(s.all_tied, lane) : 0;
+    in_all = __reduce_add_sync(0xffffffffu, a);
+    tied_all = __reduce_add_sync(0xffffffffu, b);
+    in_before = __reduce_add_sync(0xffffffffu, lane < T::rank() ? a : 0);
+    tied_before = __reduce_add_sync(0xffffffffu, lane < T::rank() ? b : 0);
     in += in_before;
     tied += tied_before;
   }
+  settle(in_all, tied_all);
   const unsigned me = 1u << lane, below = me - 1;
   for (int st = 0; st < steps; ++st) {
     unsigned a = __shfl_sync(0xffffffffu, kept_in, st & 31);
     unsigned b = __shfl_sync(0xffffffffu, kept_tied, st & 31);
-    if (st >= 32) look(st, a, b);
-    const int my_in = in + __popc(a & below), my_tied = tied + __popc(b & below);
-    if ((a & me) || ((b & me) && my_tied < ties))
-      emit(begin + st * 32 + lane, my_in + min(my_tied, ties));
+    const int i = begin + st * 32 + lane;
+    if (st >= 32) {
+      const int k = i < n ? kind(i, true) : 0;
+      a = __ballot_sync(0xffffffffu, k == 1);
+      b = __ballot_sync(0xffffffffu, k == 2);
+    }
+    if ((a | b) & me) emit(i, (b & me) != 0, in + __popc(a & below), tied + __popc(b & below));
     in += __popc(a);
     tied += __popc(b);
   }
   if constexpr (kCluster) T::sync();  // (a CTA that others read stays until they have)
-  return make_int2(in_before + min(tied_before, ties),
-                   in_before + in_here + min(tied_before + tied_here, ties));
+  return make_int4(in_before, tied_before, in_here, tied_here);
+}
+
+// The list of the entries in and of the first `ties` of those tied: emit(i, its place).
+// Returns the first place of this CTA's entries and the one behind its last.
+template <int kThreads, bool kCluster, class Kind, class Emit>
+DECATTN_DEV int2 list_largest(ListScratch& s, int n, int ties, Kind kind, Emit emit) {
+  const int4 c = list_in_order<kThreads, kCluster>(
+      s, n, kind, [](int, int) {},
+      [&](int i, bool tied, int in_before, int tied_before) {
+        if (!tied || tied_before < ties) emit(i, in_before + min(tied_before, ties));
+      });
+  return make_int2(c.x + min(c.y, ties), c.x + c.z + min(c.y + c.w, ties));
 }
 
 }  // namespace decattn

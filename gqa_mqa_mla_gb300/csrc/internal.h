@@ -187,7 +187,8 @@ struct SelectParams {
   const int32_t* seq_lens;
   int32_t* selected;          // [B, h_kv, count]
   float* scores;              // [B, h_kv, score_stride]    (score_ctas > 0)
-  float* error;               // [B, h_kv, score_ctas] how far a CTA's scores may be off
+  uint4* parts;               // [B, h_kv, score_ctas] of a CTA's scores: how far they may be off
+                              // (float), the least and the largest (order_key)
   uint64_t* exact;            // [B, h_kv, score_stride] 64-bit scores in order, where needed
   int* err_flag;
   int64_t score_stride;       // blocks of max_seq_len, rounded up to 16

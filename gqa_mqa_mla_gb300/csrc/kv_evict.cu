@@ -90,11 +90,11 @@ __global__ void __launch_bounds__(kThreads) evict_rank_kernel(const EvictParams 
   auto weight = [&](int i) { return cache ? cached[i] : *slot(begin + i); };
   int2 places = make_int2(0, 0);  // of this CTA's heavy tokens in the list
   if (heavy > 0) {
-    const Cut c = cut_largest<kThreads, kCluster>(cut, lo, hi, old, heavy, [&](int i, uint32_t& k) {
+    const Cut c = cut_largest<kThreads, kCluster, false>(cut, lo, hi, old, heavy, [&](int i, uint32_t& k) {
       k = order_key(weight(i));
       return true;
     });
-    places = list_in_order<kThreads, kCluster>(list, old, c.ties, [&](int i) {
+    places = list_largest<kThreads, kCluster>(list, old, c.ties, [&](int i, bool) {
       const uint32_t k = order_key(weight(i));
       return k > c.key ? 1 : k == c.key ? 2 : 0;
     }, [&](int i, int r) { kept[r] = begin + i; });

@@ -100,12 +100,13 @@ DECATTN_DEV uint4 scaled(uint4 w, float alpha, float& sum) {
 // 16-32k tokens, 196 MB: 34.5 us, 36.5 with a KV head to a CTA); else a CTA's warps share
 // one KV head's, which lie in shared memory.
 template <bool kF8, bool kBF16, int kHeads, bool kSpread>
-__global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(kScoreWarps * 32, 4) block_scores_kernel(const SelectParams p) {
   constexpr bool kMmaBF16 = kBF16 && !kF8;
   constexpr int kRows = kSpread ? 1 : kHeads;
   static_assert(!kSpread || kHeads == 8, "fragments in registers");
   __shared__ __align__(16) uint8_t qs[2][kRows * kQStride];  // q^+, q^-
   __shared__ float mag[kRows], part[kScoreWarps];
+  __shared__ uint32_t part_lo[kScoreWarps], part_hi[kScoreWarps];
   launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
   const int heads = kSpread ? p.score_heads : 1;  // (a power of two that divides h_kv)
@@ -206,6 +207,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const Se
     }
   }
   float* scores = p.scores + bj * p.score_stride;
+  uint32_t key_lo = 0xffffffffu, key_hi = 0u;  // the range of the scores, as cut.cuh orders them
   // The largest bound and the largest of minus the bounds, packed (8-bit: the codes'
   // magnitudes in the first).
   uint32_t most_hi = kF8 ? 0u : (kBF16 ? 0xff80ff80u : 0xfc00fc00u), most_lo = most_hi;
@@ -288,10 +290,16 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const Se
     for (int r = 0; r < 2; ++r) {
       best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 1));
       best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 2));
-      if (t4 == 0) scores[tile * kScoreBlocks + g + 8 * r] = best[r];
+      const int t = tile * kScoreBlocks + g + 8 * r;
+      if (t4 == 0) scores[t] = best[r];
+      if (t >= p.first && t < blocks - p.last) {
+        key_lo = min(key_lo, order_key(best[r]));
+        key_hi = max(key_hi, order_key(best[r]));
+      }
     }
   }
-  // This CTA's largest bound: E for its blocks (not finite if one of them is not).
+  // This CTA's largest bound, E for its blocks (not finite if one of them is not), and
+  // the range of its scores.
   float wide = 0.f;
   if constexpr (kF8) {
     uint32_t h0, h1;
@@ -305,14 +313,25 @@ __global__ void __launch_bounds__(kScoreWarps * 32) block_scores_kernel(const Se
   }
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) wide = fmaxf(wide, __shfl_xor_sync(0xffffffffu, wide, o));
-  if (lane == 0) part[warp] = wide;
+  key_lo = __reduce_min_sync(0xffffffffu, key_lo);
+  key_hi = __reduce_max_sync(0xffffffffu, key_hi);
+  if (lane == 0) {
+    part[warp] = wide;
+    part_lo[warp] = key_lo;
+    part_hi[warp] = key_hi;
+  }
   __syncthreads();
   if (lane == 0 && sub == 0) {
-    for (int w = 1; w < subs; ++w) wide = fmaxf(wide, part[warp + w * heads]);
+    for (int w = 1; w < subs; ++w) {
+      wide = fmaxf(wide, part[warp + w * heads]);
+      key_lo = min(key_lo, part_lo[warp + w * heads]);
+      key_hi = max(key_hi, part_hi[warp + w * heads]);
+    }
     // (Beyond 1e37 a sum could overflow, NaN is a product of 0 and an infinity; factors
     // and products below 2^-126 may count as 0, 128 of them.)
     const float m = q1 * wide, lost = 0x1p-118f * (1.f + wide + q1);
-    p.error[bj * gridDim.x + blockIdx.x] = m < 1e37f ? fmaf(kError, m, lost) : kInf;
+    const float e = m < 1e37f ? fmaf(kError, m, lost) : kInf;
+    p.parts[bj * gridDim.x + blockIdx.x] = make_uint4(__float_as_uint(e), key_lo, key_hi, 0u);
   }
 }
 
@@ -451,15 +470,17 @@ DECATTN_DEV double exact_score(const SelectParams& p, int64_t bj, int j, int id,
   return best;
 }
 
+// (Without a cluster there are more CTAs than SMs, and two have to fit: at 72 registers
+// the choice took 21 us for 256 of them, 14 at 64.)
 template <bool kF8, bool kBF16, int kThreads, bool kCluster>
-__global__ void __launch_bounds__(kThreads) choose_blocks_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(kThreads, kCluster ? 1 : 1024 / kThreads) choose_blocks_kernel(const SelectParams p) {
   using T = Team<kCluster>;
   extern __shared__ float cached[];
   __shared__ CutScratch cut;
   __shared__ ListScratch list;
-  __shared__ int few[kFew], own_few[kFew], count_few, count_sure;
+  __shared__ int few[kFew], own_few[kFew], count_few;
   __shared__ double few_score[kFew];
-  __shared__ unsigned few_taken, widest;
+  __shared__ unsigned few_taken, widest, key_lo, key_hi;
   const int j = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t bj = static_cast<int64_t>(b) * p.h_kv + j;
   int32_t* out = p.selected + bj * p.count;
@@ -485,8 +506,9 @@ __global__ void __launch_bounds__(kThreads) choose_blocks_kernel(const SelectPar
   const bool cache = own <= p.cached_blocks;
   cut_prepare(cut);
   if (tid == 0) {
-    count_few = count_sure = 0;
-    widest = 0;
+    count_few = 0;
+    widest = key_hi = 0u;
+    key_lo = 0xffffffffu;
   }
   // (Every CTA of a team checks the whole table: they go on together.)
   int bad = 0;
@@ -496,36 +518,41 @@ __global__ void __launch_bounds__(kThreads) choose_blocks_kernel(const SelectPar
     bad |= id < 0 || id >= p.num_blocks;
   }
   wait_for_dependence();  // the scores are there
-  // The widest error of the scores (not negative: ordered as its bits), by a warp.
-  float e = tid < p.score_ctas ? p.error[bj * p.score_ctas + tid] : 0.f;
-  uint32_t lo = 0xffffffffu, hi = 0u;
+  // The widest error of the scores (not negative: ordered as its bits) and their range,
+  // from what the first kernel's CTAs left.
+  const uint4* parts = p.parts + bj * p.score_ctas;
+  uint4 mine = tid < p.score_ctas ? parts[tid] : make_uint4(0u, 0xffffffffu, 0u, 0u);
+  if (cache) {
 #pragma unroll 4
-  for (int t = tid; t < own; t += kThreads) {
-    const float x = scores[t];
-    if (cache) cached[t] = x;
-    if (t >= first && t < last) {
-      lo = min(lo, order_key(x));
-      hi = max(hi, order_key(x));
-    }
+    for (int t = tid; t < own; t += kThreads) cached[t] = scores[t];
+    scores = cached;
   }
-  if (cache) scores = cached;
-  for (int x = tid + kThreads; x < p.score_ctas; x += kThreads)
-    e = fmaxf(e, p.error[bj * p.score_ctas + x]);
+  for (int x = tid + kThreads; x < p.score_ctas; x += kThreads) {
+    const uint4 w = parts[x];
+    mine = make_uint4(max(mine.x, w.x), min(mine.y, w.y), max(mine.z, w.z), 0u);
+  }
   if (__syncthreads_or(bad)) {
     if (tid == 0) flag_error(p.err_flag, kFlagBadBlock);
     if (T::rank() == 0)
       for (int k = tid; k < p.count; k += kThreads) out[k] = -1;
     return;
   }
-  const unsigned wide = __reduce_max_sync(0xffffffffu, __float_as_uint(e));
-  if (lane == 0 && wide) atomicMax(&widest, wide);
+  if (warp * 32 < p.score_ctas) {
+    const unsigned e = __reduce_max_sync(0xffffffffu, mine.x);
+    const unsigned lo = __reduce_min_sync(0xffffffffu, mine.y), hi = __reduce_max_sync(0xffffffffu, mine.z);
+    if (lane == 0) {
+      atomicMax(&widest, e);
+      atomicMin(&key_lo, lo);
+      atomicMax(&key_hi, hi);
+    }
+  }
   __syncthreads();
-  e = __uint_as_float(widest);
+  const float e = __uint_as_float(widest);
 
   // Blocks surely in score above `above`, surely out below `below`.
   float above = kInf, below = -kInf;
   if (want > 0) {
-    const Cut c = cut_largest<kThreads, kCluster>(cut, lo, hi, own, want, [&](int t, uint32_t& k) {
+    const Cut c = cut_largest<kThreads, kCluster, true>(cut, key_lo, key_hi, own, want, [&](int t, uint32_t& k) {
       k = order_key(scores[t]);
       return t >= first && t < last;
     });
@@ -544,60 +571,58 @@ __global__ void __launch_bounds__(kThreads) choose_blocks_kernel(const SelectPar
     const float s = scores[t];
     return s > above ? 1 : s < below ? 0 : 2;
   };
-  int sure = 0;
-#pragma unroll 2
-  for (int t0 = 0; t0 < own; t0 += kThreads) {
-    const int t = t0 + tid;
-    const int k = t < own ? near_cut(t) : 0;
-    sure += __popc(__ballot_sync(0xffffffffu, k == 1));
-    if (k == 2) T::push(few, &count_few, kFew, begin + t);
-  }
-  if (lane == 0 && sure) atomicAdd(&count_sure, sure);
-  T::sync();
-  const int close = T::get(count_few, 0);  // near the cut, and how many of these are in:
-  const int left =
-      p.count - __reduce_add_sync(0xffffffffu, lane < T::size() ? T::get(count_sure, lane) : 0);
-
   auto emit = [&](int t, int rank) { out[rank] = begin + t; };
-  if (left >= close || left <= 0) {
-    list_in_order<kThreads, kCluster>(list, own, 0, [&](int t) {
-      const int k = near_cut(t);
-      return k == 2 ? (left > 0 ? 1 : 0) : k;
-    }, emit);
-    return;
-  }
-  if (close <= kFew) {
-    // (Each CTA for itself.)
-    for (int c = warp; c < close; c += kThreads / 32) {
-      const int t = T::get(few[c], 0);
-      const double s = exact_score<kF8, kBF16>(p, bj, j, bt[t], lane);
-      if (lane == 0) {
-        own_few[c] = t;
-        few_score[c] = s;
-      }
-    }
-    __syncthreads();
-    if (warp == 0) {
-      int better = 0;
-      if (lane < close)
-        for (int c = 0; c < close; ++c)
-          better += few_score[c] > few_score[lane] ||
-                    (few_score[c] == few_score[lane] && own_few[c] < own_few[lane]);
-      const unsigned taken = __ballot_sync(0xffffffffu, lane < close && better < left);
-      if (lane == 0) few_taken = taken;
-    }
-    __syncthreads();
-    list_in_order<kThreads, kCluster>(list, own, 0, [&](int t) {
-      int k = near_cut(t);
-      if (k == 2) {
-        k = 0;
-        for (int c = 0; c < close; ++c)
-          if (own_few[c] == begin + t) k = few_taken >> c & 1;
-      }
-      return k;
-    }, emit);
-    return;
-  }
+  // The list in one go: what is in and what is near the cut are counted, the close ones
+  // collected; then, `left` of these being in, it is settled which.
+  bool settled = true, all = false;
+  int close = 0, left = 0;
+  list_in_order<kThreads, kCluster>(
+      list, own,
+      [&](int t, bool again) {
+        const int k = near_cut(t);
+        if (k == 2 && !again) T::push(few, &count_few, kFew, begin + t);
+        return k;
+      },
+      [&](int in, int tied) {
+        close = tied;
+        left = p.count - in;
+        all = left >= close;
+        settled = all || left <= 0 || close <= kFew;
+        if (!settled || all || left <= 0) return;
+        // (Each CTA for itself; a warp to a block.)
+        for (int c = warp; c < close; c += kThreads / 32) {
+          const int t = T::get(few[c], 0);
+          const double s = exact_score<kF8, kBF16>(p, bj, j, bt[t], lane);
+          if (lane == 0) {
+            own_few[c] = t;
+            few_score[c] = s;
+          }
+        }
+        __syncthreads();
+        if (warp == 0) {
+          int better = 0;
+          if (lane < close)
+            for (int c = 0; c < close; ++c)
+              better += few_score[c] > few_score[lane] ||
+                        (few_score[c] == few_score[lane] && own_few[c] < own_few[lane]);
+          const unsigned taken = __ballot_sync(0xffffffffu, lane < close && better < left);
+          if (lane == 0) few_taken = taken;
+        }
+        __syncthreads();
+      },
+      [&](int t, bool tied, int in_before, int tied_before) {
+        if (!settled) return;
+        bool is_in = !tied || all;
+        int before = in_before + (all ? tied_before : 0);
+        if (!all && left > 0)
+          for (int c = 0; c < close; ++c) {
+            if (!(few_taken >> c & 1)) continue;
+            before += own_few[c] < begin + t;
+            is_in |= tied && own_few[c] == begin + t;
+          }
+        if (is_in) emit(t, before);
+      });
+  if (settled) return;
   // Many blocks alike (equal keys, values that are not finite): all of them in 64
   // bits, cut by the upper word of their order, then by the lower.
   uint64_t* exact = p.exact + bj * p.score_stride + begin;
@@ -607,18 +632,18 @@ __global__ void __launch_bounds__(kThreads) choose_blocks_kernel(const SelectPar
     if (lane == 0) exact[t] = order_key(s);
   }
   __syncthreads();
-  const Cut up = cut_largest<kThreads, kCluster>(cut, 0u, 0xffffffffu, own, left, [&](int t, uint32_t& k) {
+  const Cut up = cut_largest<kThreads, kCluster, true>(cut, 0u, 0xffffffffu, own, left, [&](int t, uint32_t& k) {
     if (near_cut(t) != 2) return false;
     k = static_cast<uint32_t>(exact[t] >> 32);
     return true;
   });
-  const Cut lower = cut_largest<kThreads, kCluster>(cut, 0u, 0xffffffffu, own, up.ties, [&](int t, uint32_t& k) {
+  const Cut lower = cut_largest<kThreads, kCluster, true>(cut, 0u, 0xffffffffu, own, up.ties, [&](int t, uint32_t& k) {
     if (near_cut(t) != 2 || exact[t] >> 32 != up.key) return false;
     k = static_cast<uint32_t>(exact[t]);
     return true;
   });
   const uint64_t at = static_cast<uint64_t>(up.key) << 32 | lower.key;
-  list_in_order<kThreads, kCluster>(list, own, lower.ties, [&](int t) {
+  list_largest<kThreads, kCluster>(list, own, lower.ties, [&](int t, bool) {
     const int k = near_cut(t);
     return k != 2 ? k : exact[t] > at ? 1 : exact[t] == at ? 2 : 0;
   }, emit);
