@@ -17,6 +17,8 @@ logarithm of the sum, 2^-22, and twice the rounding of lse (one more where split
 are merged), 2^-24 (|s| + log2 n + 1) each, and that of s - lse, all times ln 2; two
 steps of exp2 (2^-22); together 2 D + 2^-20 + 3 2^-24 (reach log2 e + log2 n + 1).
 The sum of G heads and the old weight adds (G + 1) 2^-24 of the total."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -786,6 +788,82 @@ def test_a_bound_far_above_the_lengths(heads):
     _weights_close(x, w, before, ref, keys, 0.1)
     if heads[0] != 32:
         _same_eviction(x, 300, 20, 320)
+
+
+def test_calls_of_different_sizes_from_threads():
+    """Choices and evictions that need little and much shared memory, at the same time, each
+    on a stream of its own: every result as alone."""
+    jobs, failed = [], []
+    for i, (n, bs) in enumerate([(500, 16), (60000, 8), (9000, 8), (33000, 16)]):
+        x = _case([n, n // 3], 2, 1, "bf16", bs, 160 + i, fp8=True)
+        bounds = _bounds_of(x)
+
+        def both(x=x, bounds=bounds):
+            some = da.gqa_select_blocks(x["q"], bounds, x["table"], x["lens"], block_size=x["bs"],
+                                        max_seq_len=x["max_len"], count=9)
+            c, w = [t.clone() for t in x["caches"]], x["weights"].clone()
+            e = da.gqa_kv_evict(*c, w, x["table"], x["lens"], max_seq_len=x["max_len"], keep=300,
+                                recent=20)
+            return [some, *(t.view(torch.uint8) for t in c), w.view(torch.int32), *e]
+
+        jobs.append((both, [t.clone() for t in both()]))
+    torch.cuda.synchronize()
+
+    def work(both, want):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                for _ in range(30):
+                    got = both()
+                stream.synchronize()
+                assert all(torch.equal(a, b) for a, b in zip(got, want))
+                stream.synchronize()
+        except BaseException as e:  # noqa: BLE001
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=j) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+
+
+@pytest.mark.parametrize("heads", [(16, 8), (64, 1)])
+def test_blocks_far_into_a_large_cache(heads):
+    """Sequences whose blocks lie past 2^31 elements of the cache: the same results as those
+    of the same sequences in a small one."""
+    h_q, h_kv = heads
+    x = _case([300, 77], h_q, h_kv, "bf16", 256, 170, spare=0)
+    nb = (1 << 31) // (256 * h_kv * 128) + 9
+    far = torch.tensor([nb - 1, nb - 4, nb - 2], dtype=torch.int32, device=DEV)
+    y = dict(x)
+    y["table"] = torch.where(x["table"] >= 0, far[x["table"].clamp(min=0).long()], -1)
+    y["caches"] = [torch.empty((nb, *c.shape[1:]), dtype=c.dtype, device=DEV) for c in x["caches"]]
+    y["weights"] = torch.empty((nb, *x["weights"].shape[1:]), device=DEV)
+    for a, b in zip([*x["caches"], x["weights"]], [*y["caches"], y["weights"]]):
+        b[far.long()] = a
+    bounds = [torch.zeros((z["caches"][0].shape[0], 2, h_kv, 128), dtype=torch.bfloat16, device=DEV)
+              for z in (x, y)]
+    lists = _i32(_lists(x, 2, 5, empty=False))
+    results = []
+    for z, b in zip((x, y), bounds):
+        flag = _flag()
+        rows = torch.arange(3, device=DEV) if z is x else far.long()
+        da.gqa_block_bounds(z["caches"][0], z["table"], z["lens"], b, max_seq_len=300, err_flag=flag)
+        r = [b[rows].view(torch.int16),
+             da.gqa_select_blocks(z["q"], b, z["table"], z["lens"], block_size=256, max_seq_len=300,
+                                  count=1, first=0, last=0, err_flag=flag),
+             _decode(z, "blocks", z["table"], z["lens"], lists, scale=0.1, err_flag=flag),
+             _decode(z, "weights", z["weights"], z["table"], z["lens"], scale=0.1, err_flag=flag)]
+        r.append(z["weights"][rows].clone())
+        e = da.gqa_kv_evict(*z["caches"], z["weights"], z["table"], z["lens"], max_seq_len=300, keep=70,
+                            recent=9, err_flag=flag)
+        r += [e.kept, e.new_lens, z["weights"][rows]] + [c[rows].view(torch.int16) for c in z["caches"]]
+        assert int(flag) == 0
+        results.append(r)
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
 
 
 # ------------------------------------------------------------------ together
