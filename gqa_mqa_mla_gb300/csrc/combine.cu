@@ -146,9 +146,13 @@ __global__ void __launch_bounds__(kRowsPerCta * 32) mla_combine_kernel(const Mla
 // the others merge a row of its partials each, the splits dealt out to their warps.
 // One sequence of 32768 tokens, 32 heads on one KV head, 128 splits: 1024 tokens a CTA
 // and a warp to a row's merge beside them took 47 us.
-constexpr int kWeighWarps = 8;
+// Four tokens a thread go with CTAs of four warps (64 x 4-8k tokens, 64 heads on 8: 303 us
+// for both launches, 306 with eight); where one token a thread is taken, eight warps share
+// a CTA's log-sum-exps and merges (23 us, 26 with four).
+constexpr int weigh_warps(int vec) { return vec == 4 ? 4 : 8; }
 template <bool kBF16, int kVec>
-__global__ void __launch_bounds__(kWeighWarps * 32) weigh_kernel(const GqaParams p, int chunks) {
+__global__ void __launch_bounds__(weigh_warps(kVec) * 32) weigh_kernel(const GqaParams p, int chunks) {
+  constexpr int kWeighWarps = weigh_warps(kVec);
   __shared__ float lse[64];
   __shared__ float4 part[kWeighWarps][32];
   __shared__ float part_sum[kWeighWarps];
@@ -259,14 +263,15 @@ cudaError_t launch_mla_combine(const MlaCombineParams& p, bool bf16, cudaStream_
 
 cudaError_t launch_weigh(const GqaParams& p, bool bf16, int num_sms, cudaStream_t stream) {
   // Four tokens a thread, or one where that leaves SMs without a CTA; CTAs for the
-  // longest sequence there can be, up to about five waves of them (with a bound far
+  // longest sequence there can be, up to five to ten waves of them (with a bound far
   // above the lengths most would find nothing to do).
   const int64_t units = static_cast<int64_t>(p.batch) * p.h_kv;
-  const int threads = kWeighWarps * 32, most = p.max_seq_len > 0 ? p.max_seq_len : 1;
-  const bool few = units * ((most - 1) / (4 * threads) + 1) < num_sms;
-  const int64_t cap = std::max<int64_t>(1, static_cast<int64_t>(num_sms) * 30 / units);
-  const int chunks = static_cast<int>(
-      std::min<int64_t>((most - 1) / (few ? threads : 4 * threads) + 1, cap));
+  const int most = p.max_seq_len > 0 ? p.max_seq_len : 1;
+  const bool few = units * ((most - 1) / (4 * weigh_warps(4) * 32) + 1) < num_sms;
+  const int vec = few ? 1 : 4, threads = weigh_warps(vec) * 32;
+  const int64_t cap = std::max<int64_t>(1, static_cast<int64_t>(num_sms) * (few ? 30 : 60) / units);
+  const int chunks =
+      static_cast<int>(std::min<int64_t>((most - 1) / (vec * threads) + 1, cap));
   auto kern = bf16 ? (few ? weigh_kernel<true, 1> : weigh_kernel<true, 4>)
                    : (few ? weigh_kernel<false, 1> : weigh_kernel<false, 4>);
   cudaLaunchConfig_t cfg = {};

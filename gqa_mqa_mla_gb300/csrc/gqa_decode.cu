@@ -921,6 +921,7 @@ DECATTN_DEV void gqa_partial(const CUtensorMap& tm_k, const CUtensorMap& tm_v,
         }
         ++issued;
       }
+      if constexpr (kForm == kWeighed) launch_dependents();
       // Never leave the CTA with copies in flight: wait (bounded) for the
       // last phase of every stage that was filled.
       for (int it = max(0, issued - kStages); it < issued; ++it)
@@ -953,6 +954,11 @@ DECATTN_DEV void gqa_partial(const CUtensorMap& tm_k, const CUtensorMap& tm_v,
     __syncwarp();
     if (lane == 0) mbar_arrive(empty0 + 8 * s);
   }
+
+  // The weighing launch's CTAs may come once the tiles of all CTAs are read (7 sequences of
+  // up to 8k e4m3 tokens, 32 heads: 37.4 us for both launches, 38.0 without). They wait for
+  // this grid's end before they read anything.
+  if constexpr (kForm == kWeighed) launch_dependents();
 
   // Merge the consumer warps' (m, l, o) through shared memory (the ring is
   // free once every warp has passed the last tile).
