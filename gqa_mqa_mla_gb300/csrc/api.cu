@@ -675,8 +675,9 @@ int gqa_decode_fp8kv_sinks(const void* q, const void* k_cache, const void* v_cac
                          h_q, h_kv, d_head, scale, window, sinks, L);
 }
 
-// Lengths beyond which a 32-bit token position has no room for a CTA's step.
-static bool too_long(const decattn_launch* L) { return L && L->max_seq_len > 0x7fffffff - 65536; }
+// Lengths (of sequences, of lists) beyond which a 32-bit position has no room for a CTA's step.
+static bool too_many(int n) { return n > 0x7fffffff - 65536; }
+static bool too_long(const decattn_launch* L) { return L && too_many(L->max_seq_len); }
 
 static int decode_blocks(const void* q, const void* k_cache, const void* v_cache,
                          const float* k_scale, const float* v_scale, bool fp8,
@@ -684,7 +685,7 @@ static int decode_blocks(const void* q, const void* k_cache, const void* v_cache
                          const int32_t* selected, void* out, int h_q, int h_kv, int d_head,
                          float scale, int count, const decattn_launch* L) {
   if (!selected || !aligned(selected, 4) || count < 1) return DECATTN_ERR_INVALID_ARG;
-  if (too_long(L)) return DECATTN_ERR_UNSUPPORTED;
+  if (too_long(L) || too_many(count)) return DECATTN_ERR_UNSUPPORTED;
   DecodeMore more;
   more.selected = selected;
   more.count = count;
@@ -803,7 +804,8 @@ int gqa_select_blocks(const void* q, const void* bounds, const int32_t* block_ta
     return DECATTN_ERR_INVALID_ARG;
   if (count < 1 || first < 0 || last < 0 || static_cast<int64_t>(first) + last > count)
     return DECATTN_ERR_INVALID_ARG;
-  if (d_head != kHeadDim || h_q / h_kv > 64 || L->batch > 65535 || h_kv > 65535 || too_long(L))
+  if (d_head != kHeadDim || h_q / h_kv > 64 || L->batch > 65535 || h_kv > 65535 || too_long(L) ||
+      too_many(count))
     return DECATTN_ERR_UNSUPPORTED;
   const int64_t blocks = select_blocks_of(L->max_seq_len, L->block_size);
   SelectParams p{};
@@ -860,7 +862,8 @@ int gqa_kv_evict(void* k_cache, void* v_cache, float* weights, const int32_t* bl
     return DECATTN_ERR_INVALID_ARG;
   if (h_kv < 1 || h_kv > 1024 || (kv_bytes != 1 && kv_bytes != 2)) return DECATTN_ERR_INVALID_ARG;
   if (keep < 1 || recent < 0 || recent > keep || limit < keep) return DECATTN_ERR_INVALID_ARG;
-  if (d_head != kHeadDim || L->batch > 65535 || too_long(L)) return DECATTN_ERR_UNSUPPORTED;
+  if (d_head != kHeadDim || L->batch > 65535 || too_long(L) || too_many(keep))
+    return DECATTN_ERR_UNSUPPORTED;
   const int sms = device_sm_count();
   if (sms <= 0) return DECATTN_ERR_CUDA;
   EvictParams p{};

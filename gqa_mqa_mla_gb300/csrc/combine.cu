@@ -171,10 +171,11 @@ __global__ void __launch_bounds__(weigh_warps(kVec) * 32) weigh_kernel(const Gqa
     weigh_lse<kWeighWarps>(p, row0, lse);
     __syncthreads();
     if (lse[0] == kPosInf) return;  // (bad data is met by every head of the group alike)
+    const int step = chunks * kTokens;
     for (;;) {
       if (t < n) tokens.store(p, t, n, weighed, lse);
-      t0 += chunks * kTokens;
-      if (t0 >= n) return;
+      if (n - t0 <= step) return;
+      t0 += step;
       t = t0 + threadIdx.x * kVec;
       if (t < n) tokens.load(p, j, b, t);
     }

@@ -136,6 +136,19 @@ def test_eviction_host_checks(lib, case, expect):
                             _launch(a["L"])) == expect
 
 
+@pytest.mark.parametrize("many", [0x7fffffff, 0x7fffffff - 65535])
+def test_lists_past_32_bit_steps_are_refused(lib, many):
+    L = _launch({})
+    assert lib.gqa_select_blocks(FAKE, FAKE, FAKE, FAKE, FAKE, 8, 2, 128, 2, many, 1, 1,
+                                 L) == UNSUPPORTED
+    assert lib.gqa_decode_blocks(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 8, 2, 128, 0.1, many,
+                                 L) == UNSUPPORTED
+    assert lib.gqa_decode_fp8kv_blocks(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 8, 2,
+                                       128, 0.1, many, L) == UNSUPPORTED
+    assert lib.gqa_kv_evict(FAKE, 2 * FAKE, FAKE, FAKE, FAKE, 2 * FAKE, FAKE, 2, 128, 2, many, 0,
+                            many, L) == UNSUPPORTED
+
+
 def test_sizes_and_splits(lib):
     assert da.gqa_select_workspace_size(2, 4, 1000, 16, 63) == 0
     assert da.gqa_select_workspace_size(2, 4, 1000, 16, 62) >= 8 * 63 * 12
