@@ -21,7 +21,8 @@
 // four chains of four products of 16 terms, each term off by at most 2^-23 of the
 // chain's sum of magnitudes (4 x 17 x 2^-23), and their sum.  The second kernel, a
 // CTA to each sequence and KV head, finds the cut v (cut.cuh); blocks
-// within 2 E of it, usually none but the cut itself, are scored again in 64 bits.
+// within 2 E of it, usually none but the cut itself, are scored again, in 32 bits with
+// tighter bounds on the error and, where these leave something open, in 64.
 // Doing all in 64 bits would take 40 times the floor here: 0.6 T products a second.
 #include <algorithm>
 
@@ -366,16 +367,10 @@ __device__ __noinline__ double score_of_strange_values(const uint16_t* q, int gr
   return best;
 }
 
-// s_t in 64 bits, by a warp; the same value in every lane, NaN counts as +inf.  A
-// product in 64 bits takes a warp 16 cycles here, so only the heads that may hold
-// the maximum are taken so: those within the 32-bit sums' error (a lane's four
-// products and sums, five more, each 2^-24 of the sum of magnitudes) of the
-// largest.  (All heads, and the definition's comparisons in 64 bits, took 18 us
-// for three blocks of 8 heads.)
+// A block's lo and hi for the lane's dims 4 l .. 4 l + 3.
 template <bool kF8, bool kBF16>
-DECATTN_DEV double exact_score(const SelectParams& p, int64_t bj, int j, int id, int lane) {
+DECATTN_DEV void load_bounds(const SelectParams& p, int j, int id, int lane, float (&lo)[4], float (&hi)[4]) {
   const int64_t row = (static_cast<int64_t>(id) * 2 * p.h_kv + j) * kHeadDim + lane * 4;
-  float lo[4], hi[4];
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const int64_t at = row + k * static_cast<int64_t>(p.h_kv) * kHeadDim;
@@ -391,67 +386,101 @@ DECATTN_DEV double exact_score(const SelectParams& p, int64_t bj, int j, int id,
     float* to = k ? hi : lo;
     to[0] = a.x; to[1] = a.y; to[2] = c.x; to[3] = c.y;
   }
-  const uint16_t* q = static_cast<const uint16_t*>(p.q) + bj * p.group * kHeadDim + lane * 4;
-  float up[4], down[4], sum_all = 0.f;  // what a positive, a negative value of q meets
+}
+
+// s_t in 32 bits, by a warp, with bounds on its error: a lane's four products and sums,
+// five more, and the bound itself, each off by 2^-24 of the sum of magnitudes at most: 11 of these.  (Tighter than E,
+// which takes one magnitude for all dims, and adds as the tensor cores do.)
+struct Rough {
+  float lo, hi;               // the maximum over the heads lies within
+  float sums[2], errors[2];   // heads lane and lane + 32
+  bool finite;                // else nothing is known
+};
+template <bool kBF16>
+DECATTN_DEV Rough rough_score(const uint16_t* q, int group, int lane, const float (&lo)[4],
+                              const float (&hi)[4], const float (&up)[4], const float (&down)[4]) {
+  Rough r = {-kInf, -kInf, {-kInf, -kInf}, {0.f, 0.f}, true};
+  float sum_all = 0.f;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    up[k] = fmaxf(lo[k], hi[k]);
-    down[k] = fminf(lo[k], hi[k]);
-    sum_all += fabsf(lo[k]) + fabsf(hi[k]);
-  }
-  // Head r's 32-bit sum and its error stay with lane r % 32; eight heads at a time, so
-  // that their loads and exchanges overlap.
-  float sums[2] = {-kInf, -kInf}, errors[2] = {0.f, 0.f}, floor_ = -kInf;
-  bool finite = sum_all < kInf;
-  for (int r0 = 0; r0 < p.group; r0 += 8) {
+  for (int k = 0; k < 4; ++k) sum_all += fabsf(lo[k]) + fabsf(hi[k]);
+  r.finite = sum_all < kInf;
+  // Eight heads at a time, so that their loads and exchanges overlap.
+  for (int h0 = 0; h0 < group; h0 += 8) {
     uint2 w[8];
     float s[8], mag[8];
 #pragma unroll
-    for (int r = 0; r < 8; ++r)
-      w[r] = *reinterpret_cast<const uint2*>(q + min(r0 + r, p.group - 1) * kHeadDim);
+    for (int h = 0; h < 8; ++h)
+      w[h] = *reinterpret_cast<const uint2*>(q + min(h0 + h, group - 1) * kHeadDim);
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      const float2 a = unpack2<kBF16>(w[r].x), c = unpack2<kBF16>(w[r].y);
+    for (int h = 0; h < 8; ++h) {
+      const float2 a = unpack2<kBF16>(w[h].x), c = unpack2<kBF16>(w[h].y);
       const float x[4] = {a.x, a.y, c.x, c.y};
-      s[r] = mag[r] = 0.f;
+      s[h] = mag[h] = 0.f;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const float b = x[k] >= 0.f ? up[k] : down[k];
-        s[r] = fmaf(x[k], b, s[r]);
-        mag[r] = fmaf(fabsf(x[k]), fabsf(b), mag[r]);
+        s[h] = fmaf(x[k], b, s[h]);
+        mag[h] = fmaf(fabsf(x[k]), fabsf(b), mag[h]);
       }
     }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) {
 #pragma unroll
-      for (int r = 0; r < 8; ++r) {
-        s[r] += __shfl_xor_sync(0xffffffffu, s[r], o);
-        mag[r] += __shfl_xor_sync(0xffffffffu, mag[r], o);
+      for (int h = 0; h < 8; ++h) {
+        s[h] += __shfl_xor_sync(0xffffffffu, s[h], o);
+        mag[h] += __shfl_xor_sync(0xffffffffu, mag[h], o);
       }
     }
 #pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      finite &= mag[r] < 1e37f;
-      const float err = fmaf(mag[r], 0x1p-20f, 1e-36f);  // (products below 2^-126 lose their lower bits)
-      floor_ = fmaxf(floor_, s[r] - err);
-      if (lane == ((r0 + r) & 31) && r0 + r < p.group) {
-        if (r0 < 32) {
-          sums[0] = s[r];
-          errors[0] = err;
+    for (int h = 0; h < 8; ++h) {
+      r.finite &= mag[h] < 1e37f;
+      const float err = fmaf(mag[h], 0x1.6p-21f, 1e-36f);  // (products below 2^-126 lose their lower bits)
+      r.lo = fmaxf(r.lo, s[h] - err);
+      r.hi = fmaxf(r.hi, s[h] + err);
+      if (lane == ((h0 + h) & 31) && h0 + h < group) {
+        if (h0 < 32) {
+          r.sums[0] = s[h];
+          r.errors[0] = err;
         } else {
-          sums[1] = s[r];
-          errors[1] = err;
+          r.sums[1] = s[h];
+          r.errors[1] = err;
         }
       }
     }
   }
-  if (!__all_sync(0xffffffffu, finite))
+  r.finite = __all_sync(0xffffffffu, r.finite);
+  return r;
+}
+
+template <bool kF8, bool kBF16>
+DECATTN_DEV Rough look_score(const SelectParams& p, int64_t bj, int j, int id, int lane,
+                             float (&lo)[4], float (&hi)[4], float (&up)[4], float (&down)[4]) {
+  load_bounds<kF8, kBF16>(p, j, id, lane, lo, hi);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {  // what a positive, a negative value of q meets
+    up[k] = fmaxf(lo[k], hi[k]);
+    down[k] = fminf(lo[k], hi[k]);
+  }
+  const uint16_t* q = static_cast<const uint16_t*>(p.q) + bj * p.group * kHeadDim + lane * 4;
+  return rough_score<kBF16>(q, p.group, lane, lo, hi, up, down);
+}
+
+// s_t in 64 bits, by a warp; the same value in every lane, NaN counts as +inf.  A
+// product in 64 bits takes a warp 16 cycles here, so only the heads that may hold
+// the maximum are taken so.  (All heads, and the definition's comparisons in 64 bits,
+// took 18 us for three blocks of 8 heads.)
+template <bool kF8, bool kBF16>
+__device__ __noinline__ double exact_score(const SelectParams& p, int64_t bj, int j, int id, int lane) {
+  float lo[4], hi[4], up[4], down[4];
+  const Rough rough = look_score<kF8, kBF16>(p, bj, j, id, lane, lo, hi, up, down);
+  const uint16_t* q = static_cast<const uint16_t*>(p.q) + bj * p.group * kHeadDim + lane * 4;
+  if (!rough.finite)
     return score_of_strange_values<kBF16>(q, p.group, make_float4(lo[0], lo[1], lo[2], lo[3]),
                                           make_float4(hi[0], hi[1], hi[2], hi[3]));
   double best = -__longlong_as_double(0x7ff0000000000000ll);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    unsigned may = __ballot_sync(0xffffffffu, sums[h] + errors[h] >= floor_);
+    unsigned may = __ballot_sync(0xffffffffu, rough.sums[h] + rough.errors[h] >= rough.lo);
     while (may) {
       const int r = 32 * h + __ffs(may) - 1;
       may &= may - 1;
@@ -480,7 +509,8 @@ __global__ void __launch_bounds__(kThreads, kCluster ? 1 : 1024 / kThreads) choo
   __shared__ ListScratch list;
   __shared__ int few[kFew], own_few[kFew], count_few;
   __shared__ double few_score[kFew];
-  __shared__ unsigned few_taken, widest, key_lo, key_hi;
+  __shared__ float few_lo[kFew], few_hi[kFew];
+  __shared__ unsigned few_taken, few_open, widest, key_lo, key_hi;
   const int j = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t bj = static_cast<int64_t>(b) * p.h_kv + j;
   int32_t* out = p.selected + bj * p.count;
@@ -589,14 +619,39 @@ __global__ void __launch_bounds__(kThreads, kCluster ? 1 : 1024 / kThreads) choo
         all = left >= close;
         settled = all || left <= 0 || close <= kFew;
         if (!settled || all || left <= 0) return;
-        // (Each CTA for itself; a warp to a block.)
+        // (Each CTA for itself; a warp to a block.)  First with the 32-bit sums' own
+        // errors, which mostly tell the blocks apart (one sequence of 131072 tokens 20.5
+        // us, 22.4 with 64 bits at once).
         for (int c = warp; c < close; c += kThreads / 32) {
           const int t = T::get(few[c], 0);
-          const double s = exact_score<kF8, kBF16>(p, bj, j, bt[t], lane);
+          float lo[4], hi[4], up[4], down[4];
+          const Rough r = look_score<kF8, kBF16>(p, bj, j, bt[t], lane, lo, hi, up, down);
           if (lane == 0) {
             own_few[c] = t;
-            few_score[c] = s;
+            few_lo[c] = r.finite ? r.lo : -kInf;
+            few_hi[c] = r.finite ? r.hi : kInf;
           }
+        }
+        __syncthreads();
+        if (warp == 0) {
+          int surely = 0, perhaps = 0;  // better than the lane's block
+          if (lane < close)
+            for (int c = 0; c < close; ++c) {
+              surely += c != lane && few_lo[c] > few_hi[lane];
+              perhaps += c != lane && few_hi[c] >= few_lo[lane];
+            }
+          const unsigned taken = __ballot_sync(0xffffffffu, lane < close && perhaps < left);
+          const unsigned open = __ballot_sync(0xffffffffu, lane < close && perhaps >= left && surely < left);
+          if (lane == 0) {
+            few_taken = taken;
+            few_open = open;
+          }
+        }
+        __syncthreads();
+        if (few_open == 0) return;
+        for (int c = warp; c < close; c += kThreads / 32) {
+          const double s = exact_score<kF8, kBF16>(p, bj, j, bt[own_few[c]], lane);
+          if (lane == 0) few_score[c] = s;
         }
         __syncthreads();
         if (warp == 0) {

@@ -309,6 +309,35 @@ def test_selection_of_nearly_equal_blocks(fp8):
         _same_choice(x, b, q=q, count=count)
 
 
+@pytest.mark.parametrize("lens", [[1600], [40000]])  # (one CTA, a cluster)
+@pytest.mark.parametrize("step", [2.0**-5, 2.0**-12, 0.0])
+@pytest.mark.parametrize("alike", [2, 9, 32])
+def test_selection_where_a_few_are_nearly_equal(alike, step, lens):
+    """`alike` blocks around the cut, the others surely in or out.  Their scores are 2^16
+    plus whole steps, in pairs: within the products' common error (2^-16 of 256 x 512);
+    steps of 2^-5 are told apart by a 32-bit sum with its own error (11 x 2^-24 of 2^16)
+    from the third on, those of 2^-12 in 64 bits only; equals go by their places."""
+    x = _case(lens, 2, 1, "bf16", 8, 9)
+    n = lens[0] // 8
+    rng = np.random.default_rng(alike)
+    order = rng.permutation(n)
+    above, close = order[: n // 3], np.sort(order[n // 3 : n // 3 + alike])
+    small = np.zeros(n)
+    large = np.full(n, 128.0)
+    large[above] = 512.0
+    large[close] = 256.0
+    small[close] = rng.permutation(alike) // 2 * 1.0  # (pairs of equals)
+    bounds = torch.zeros((x["caches"][0].shape[0], 2, 1, 128), device=DEV)
+    t = x["table"][0].long()
+    bounds[t, :, 0, 0] = torch.tensor(large, dtype=torch.float32, device=DEV)[:, None]
+    bounds[t, :, 0, 1] = torch.tensor(small, dtype=torch.float32, device=DEV)[:, None]
+    q = torch.zeros_like(x["q"])
+    q[:, 0, 0], q[:, 0, 1] = 256.0, step
+    q[:, 1, 0], q[:, 1, 2] = 128.0, 1.0
+    for k in sorted({1, alike // 2, alike - 1}):
+        _same_choice(x, bounds.bfloat16(), q=q, count=n // 3 + k, first=0, last=0)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("fp8", [False, True])
 def test_selection_by_values_that_are_not_finite(fp8, dtype):
