@@ -88,6 +88,7 @@ struct CcConsumer {
   static constexpr int kMinBlocks = 1;
   static constexpr int kWarps = 4;
   static constexpr int kRowsPerWarp = G;
+  static constexpr bool kScalesHeads = false;
 
   float q[G][8];
   float o[G][8];
@@ -237,6 +238,7 @@ struct MmaConsumer {
   // register file then holds one CTA per SM either way).
   static constexpr int kWarps = MT == 1 ? 4 : 8;
   static constexpr int kRowsPerWarp = 16;
+  static constexpr bool kScalesHeads = false;
   static constexpr int kWarpsPerMtile = kWarps / MT;
   static constexpr int kTokensPerWarp = kTile / kWarpsPerMtile;
 
@@ -413,6 +415,7 @@ struct CcConsumerF8 {
   static constexpr int kMinBlocks = 1;
   static constexpr int kWarps = 4;
   static constexpr int kRowsPerWarp = G;
+  static constexpr bool kScalesHeads = false;
 
   float q[G][8];
   float o[G][8];
@@ -579,12 +582,20 @@ struct MmaConsumerF8T {
   static constexpr int kMinBlocks = NT == 1 ? 4 : 2;
   static constexpr int kWarps = 4;
   static constexpr int kRowsPerWarp = 8 * NT;
+  static constexpr bool kScalesHeads = kBF16;
 
   uint32_t qb[8][NT][2];  // Q^T B fragments: k-step, n-tile, dims (4q, 4q+1 | 4q+2, 4q+3)
   float o[8][NT][4];      // O^T, 16-dim block b: (2g, 2q) (2g, 2q+1) (2g+1, 2q) (2g+1, 2q+1)
   float m[NT][2], l[NT][2];
   float v_scale;
   int tok0, cw, lane, group;
+
+  // What each head's scores are multiplied by, where that is not the same for all (see
+  // scale_heads).  Every warp writes the same.
+  DECATTN_DEV static float* head_scale() {
+    __shared__ __align__(8) float s[8 * NT];
+    return s;
+  }
 
   __device__ __forceinline__ void init(const GqaParams& p, int b, int j, int cw_, int lane_) {
     cw = cw_;
@@ -611,6 +622,56 @@ struct MmaConsumerF8T {
 #pragma unroll
       for (int bb = 0; bb < 8; ++bb) o[bb][nt][0] = o[bb][nt][1] = o[bb][nt][2] = o[bb][nt][3] = 0.f;
     }
+  }
+
+  // A bf16 query may lie outside fp16's range, or so near its smallest step (2^-24) that
+  // more than 2^-19 of its largest value is lost.  Each head's is then multiplied as itself
+  // times a power of two, which its scores lose again through head_scale; returned is what
+  // tile() takes as scale, NaN for such a group.  (For every query, in registers, this took
+  // the weighing form from 230 to 252 us at 64 sequences of 8192 tokens, 64 heads on 8.)
+  __device__ __forceinline__ float scale_heads(const GqaParams& p, int b, int j, float scale) {
+    if constexpr (!kBF16) return scale;
+    const int g = lane >> 2, q4 = lane & 3;
+    bool far = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      uint32_t most2 = 0u;
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks)
+        most2 = __vmaxu2(most2, __vmaxu2(qb[ks][nt][0] & 0x7fff7fffu, qb[ks][nt][1] & 0x7fff7fffu));
+      uint32_t most = max(most2 & 0xffffu, most2 >> 16);
+      most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
+      most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
+      far |= 8 * nt + g < group && (most >= 0x7c00u || most < 0x2400u);  // infinite; below 2^-6
+    }
+    if (!__any_sync(0xffffffffu, far) && scale == scale) return scale;
+    const uint16_t* q = static_cast<const uint16_t*>(p.q) +
+                        (static_cast<size_t>(b) * p.h_q + static_cast<size_t>(j) * group) * kHeadDim + 4 * q4;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int h = 8 * nt + g;
+      float x[8][4], most = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks) {
+        uint2 w = make_uint2(0u, 0u);
+        if (h < group) w = *reinterpret_cast<const uint2*>(q + h * kHeadDim + ks * 16);
+        const float2 f0 = unpack2<true>(w.x), f1 = unpack2<true>(w.y);
+        x[ks][0] = f0.x; x[ks][1] = f0.y; x[ks][2] = f1.x; x[ks][3] = f1.y;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) most = fmaxf(most, fabsf(x[ks][k]));
+      }
+      most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+      most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+      const float alpha = fp16_scale(most);
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks) {
+        qb[ks][nt][0] = pack2<false>(x[ks][0] * alpha, x[ks][1] * alpha);
+        qb[ks][nt][1] = pack2<false>(x[ks][2] * alpha, x[ks][3] * alpha);
+      }
+      if (q4 == 0) head_scale()[h] = scale * __uint_as_float(0x7f000000u - __float_as_uint(alpha));  // / alpha
+    }
+    __syncwarp();
+    return __uint_as_float(0x7fffffffu);
   }
 
   template <bool kScores>
@@ -665,10 +726,16 @@ struct MmaConsumerF8T {
     float cr[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      s[nt][0] = la ? s[nt][0] * scale_log2 : kNegInf;
-      s[nt][1] = la ? s[nt][1] * scale_log2 : kNegInf;
-      s[nt][2] = lb ? s[nt][2] * scale_log2 : kNegInf;
-      s[nt][3] = lb ? s[nt][3] * scale_log2 : kNegInf;
+      float scale0 = scale_log2, scale1 = scale_log2;
+      if (kBF16 && scale_log2 != scale_log2) {
+        const float2 f = *reinterpret_cast<const float2*>(head_scale() + 8 * nt + 2 * (lane & 3));
+        scale0 = f.x;
+        scale1 = f.y;
+      }
+      s[nt][0] = la ? s[nt][0] * scale0 : kNegInf;
+      s[nt][1] = la ? s[nt][1] * scale1 : kNegInf;
+      s[nt][2] = lb ? s[nt][2] * scale0 : kNegInf;
+      s[nt][3] = lb ? s[nt][3] * scale1 : kNegInf;
       if constexpr (kScores) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -935,8 +1002,8 @@ DECATTN_DEV void gqa_partial(const CUtensorMap& tm_k, const CUtensorMap& tm_v,
   Consumer c;
   c.init(p, b, j, cw, lane);
   // An 8-bit cache's K scale multiplies every score of KV head j.
-  const float scale_log2 =
-      Consumer::kCacheBytes == 1 ? p.scale_log2 * p.k_scale[j] : p.scale_log2;
+  float scale_log2 = Consumer::kCacheBytes == 1 ? p.scale_log2 * p.k_scale[j] : p.scale_log2;
+  if constexpr (Consumer::kScalesHeads) scale_log2 = c.scale_heads(p, b, j, scale_log2);
   bool ok = true;
   for (int it = 0; it < n_tiles; ++it) {
     const int s = it % kStages;

@@ -401,6 +401,15 @@ DECATTN_DEV uint32_t pack2(float x, float y) {
   return w;
 }
 
+// The power of two that brings values of magnitude `most` to 2^14 .. 2^15, where fp16 holds
+// a bf16 value exactly and what falls below its smallest step is under 2^-38 of `most`
+// (1 for an infinite `most`).
+DECATTN_DEV float fp16_scale(float most) {
+  const int e = static_cast<int>(__float_as_uint(most) >> 23) - 127;  // 128: infinite
+  const int k = e >= 128 ? 0 : min(14 - e, 126);
+  return __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
+}
+
 DECATTN_DEV uint32_t byte_perm(uint32_t a, uint32_t b, uint32_t sel) {
   uint32_t r;
   asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));

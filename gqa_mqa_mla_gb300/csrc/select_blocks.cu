@@ -59,17 +59,11 @@ DECATTN_DEV uint32_t max2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// What a warp knows of its KV head's queries: the largest sum of magnitudes of a row (of
-// what is multiplied), and for up to 8 of them their B fragments.
+// Over 8 bits q is multiplied as fp16, a bf16 query times a power of two for its group
+// (the scores of the pair (b, j) then all carry that factor).
 template <bool kF8, bool kBF16>
-DECATTN_DEV float fp16_scale(float most) {
-  // Over 8 bits q is multiplied as fp16, a bf16 query times the power of two that brings
-  // the group's largest value to 2^14 .. 2^15 (the scores of the pair (b, j) then all
-  // carry that factor; what falls below fp16's smallest step is 2^-38 of that value).
-  if constexpr (!kF8 || !kBF16) return 1.f;
-  const int e = static_cast<int>(__float_as_uint(most) >> 23) - 127;  // 128: infinite
-  const int k = e >= 128 ? 0 : min(14 - e, 126);
-  return __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
+DECATTN_DEV float query_scale(float most) {
+  return kF8 && kBF16 ? fp16_scale(most) : 1.f;
 }
 template <bool kBF16>
 DECATTN_DEV float largest(uint4 w) {
@@ -155,7 +149,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 4) block_scores_kernel(const
     }
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-    const float alpha = fp16_scale<kF8, kBF16>(most);
+    const float alpha = query_scale<kF8, kBF16>(most);
 #pragma unroll
     for (int i = 0; i < kParts; ++i) {
       w[i] = scaled<kF8, kBF16>(w[i], alpha, sum);
@@ -185,7 +179,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 4) block_scores_kernel(const
       __syncthreads();
       float most = 0.f;
       for (int r = 0; r < G; ++r) most = fmaxf(most, mag[r]);
-      alpha = fp16_scale<kF8, kBF16>(most);
+      alpha = query_scale<kF8, kBF16>(most);
       __syncthreads();
     }
     for (int r = 2 * warp + (lane >> 4); r < kHeads; r += 2 * kScoreWarps) {

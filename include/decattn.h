@@ -173,8 +173,11 @@ int gqa_decode_noalloc(const void* q, const void* k_cache, const void* v_cache,
  * Every other argument, status and layout rule as gqa_decode (workspace
  * sized by gqa_decode_workspace_size).  Scores and P.V run on tensor cores
  * with fp32 accumulation; K's scale multiplies the scores, V's the output.
- * Up to 16 query heads per KV head both take fp16 operands (the codes
- * convert exactly; q is rounded to fp16).  From 17 on, the scores take the
+ * One query head per KV head is computed in fp32 throughout.  From 2 to 16
+ * both take fp16 operands: the codes convert exactly; a bf16 query of any
+ * magnitude keeps its values to within 2^-19 of the head's largest (a head
+ * outside fp16's range is scaled by a power of two); the probabilities are
+ * rounded to fp16.  From 17 on, the scores take the
  * e4m3 codes as they are against q written as a sum of e4m3 terms (two for
  * bf16, three for fp16, each row scaled by a power of two; exact except for
  * parts of at most 2^-10 / 224, under 2^-17, of the row's largest element), and
@@ -520,8 +523,9 @@ size_t gqa_select_workspace_size(int batch, int h_kv, int max_seq_len, int block
  * checked.  Every other argument, layout, status and the workspace rule as
  * gqa_decode; num_splits = 0 takes gqa_decode_blocks_plan_splits' count (for
  * min(max_seq_len, count block_size) tokens; kv_bytes = 2, or 1 over an 8-bit cache).
- * Over an 8-bit cache q is rounded to fp16 with one query head per KV head too (here
- * and with weights).
+ * Over an 8-bit cache one query head per KV head takes fp16 operands too, as groups of
+ * 2 to 16 do (here and with weights): the probabilities are rounded to fp16, which
+ * gqa_decode_fp8kv keeps in fp32 there.
  */
 int gqa_decode_blocks(const void* q, const void* k_cache, const void* v_cache,
                       const int32_t* block_table, const int32_t* seq_lens,
