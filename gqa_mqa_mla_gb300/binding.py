@@ -210,6 +210,8 @@ def lib() -> ctypes.CDLL:
             L.decattn_selftest_wait_timeout.restype = I
             L.decattn_selftest_warp_wait.argtypes = [P, P, I, P]
             L.decattn_selftest_warp_wait.restype = I
+            L.decattn_selftest_gave_up.argtypes = [P, P, I, P]
+            L.decattn_selftest_gave_up.restype = I
             L.decattn_version.argtypes = []
             L.decattn_version.restype = I
             _lib = L
@@ -252,6 +254,19 @@ def selftest_warp_wait(limit_us: int = 1000, device="cuda"):
         raise DecAttnError("decattn_selftest_warp_wait", st)
     torch.cuda.synchronize()
     return int(flag.item()), res.tolist()
+
+
+def selftest_gave_up(limit_us: int = 1000, device="cuda"):
+    """Run the self test of a weighing decode's split that gives up; returns (err_flag,
+    float tensor [40, 3]: a row's sums by split)."""
+    flag = torch.zeros(1, dtype=torch.int32, device=device)
+    res = torch.full((40, 3), -1.0, device=device)
+    st = lib().decattn_selftest_gave_up(flag.data_ptr(), res.data_ptr(), int(limit_us),
+                                        _stream_handle(None))
+    if st != DECATTN_OK:
+        raise DecAttnError("decattn_selftest_gave_up", st)
+    torch.cuda.synchronize()
+    return int(flag.item()), res.cpu()
 
 
 def selftest_wait_timeout(limit_us: int = 1000, device="cuda"):

@@ -1031,41 +1031,46 @@ DECATTN_DEV void gqa_partial(const CUtensorMap& tm_k, const CUtensorMap& tm_v,
   // free once every warp has passed the last tile).
   __syncwarp();
   if (lane == 0) mbar_arrive(done_bar);
-  if (!ok || !mbar_wait_warp(done_bar, 0, p.err_flag)) return;
-  float* mo = reinterpret_cast<float*>(smem);
-  float* mm = mo + kW * Consumer::kRowsPerWarp * kHeadDim;
-  float* ml = mm + kW * Consumer::kRowsPerWarp;
-  c.finish(mo, mm, ml, lane);
-  __syncwarp();
-  if (lane == 0) mbar_arrive(merge_bar);
-  if (!mbar_wait_warp(merge_bar, 0, p.err_flag)) return;
+  auto merge = [&] {
+    if (!ok || !mbar_wait_warp(done_bar, 0, p.err_flag)) return false;
+    float* mo = reinterpret_cast<float*>(smem);
+    float* mm = mo + kW * Consumer::kRowsPerWarp * kHeadDim;
+    float* ml = mm + kW * Consumer::kRowsPerWarp;
+    c.finish(mo, mm, ml, lane);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(merge_bar);
+    if (!mbar_wait_warp(merge_bar, 0, p.err_flag)) return false;
 
-  const int tid = threadIdx.x - 32;
-  for (int e = tid; e < G * kHeadDim; e += kW * 32) {
-    const int r = e / kHeadDim, d = e % kHeadDim;
-    float M = kLowest;
+    const int tid = threadIdx.x - 32;
+    for (int e = tid; e < G * kHeadDim; e += kW * 32) {
+      const int r = e / kHeadDim, d = e % kHeadDim;
+      float M = kLowest;
 #pragma unroll
-    for (int w = 0; w < kW; ++w)
-      if (Consumer::covers(w, r)) M = fmaxf(M, mm[Consumer::slot(w, r)]);
-    float L = 0.f, O = 0.f;
+      for (int w = 0; w < kW; ++w)
+        if (Consumer::covers(w, r)) M = fmaxf(M, mm[Consumer::slot(w, r)]);
+      float L = 0.f, O = 0.f;
 #pragma unroll
-    for (int w = 0; w < kW; ++w) {
-      if (!Consumer::covers(w, r)) continue;
-      const int sl = Consumer::slot(w, r);
-      const float f = ex2(mm[sl] - M);
-      L = fmaf(ml[sl], f, L);
-      O = fmaf(mo[sl * kHeadDim + d], f, O);
+      for (int w = 0; w < kW; ++w) {
+        if (!Consumer::covers(w, r)) continue;
+        const int sl = Consumer::slot(w, r);
+        const float f = ex2(mm[sl] - M);
+        L = fmaf(ml[sl], f, L);
+        O = fmaf(mo[sl * kHeadDim + d], f, O);
+      }
+      // L is 0, exactly, where no score but -inf was seen; NaN scores make it NaN.
+      const float res = L == 0.f ? 0.f : O / L;
+      if (p.n_split == 1) {
+        static_cast<uint16_t*>(p.out)[(row0 + r) * kHeadDim + d] = round1<kBF16>(res);
+        if (kForm != kWeighed) continue;
+      } else {
+        p.part_o[((row0 + r) * p.n_split + split) * kHeadDim + d] = res;
+      }
+      if (d == 0) p.part_lse[(row0 + r) * p.n_split + split] = L == 0.f ? kNegInf : M + lg2(L);
     }
-    // L is 0, exactly, where no score but -inf was seen; NaN scores make it NaN.
-    const float res = L == 0.f ? 0.f : O / L;
-    if (p.n_split == 1) {
-      static_cast<uint16_t*>(p.out)[(row0 + r) * kHeadDim + d] = round1<kBF16>(res);
-      if (kForm != kWeighed) continue;
-    } else {
-      p.part_o[((row0 + r) * p.n_split + split) * kHeadDim + d] = res;
-    }
-    if (d == 0) p.part_lse[(row0 + r) * p.n_split + split] = L == 0.f ? kNegInf : M + lg2(L);
-  }
+    return true;
+  };
+  const bool merged = merge();
+  if constexpr (kForm == kWeighed) gqa_mark_unless(merged, kW * 32, cw == 0, p);
 }
 
 // Few sequences in a window: the splits of a sequence and KV head are one cluster,

@@ -744,6 +744,7 @@ __global__ void __launch_bounds__(kThreads)
 
   tc_fence_before();
   __syncthreads();
+  if (kForm == kWeighed && warp == 0 && *abort_word) gqa_mark_rows(p);
   if (warp == kWarpMma) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);

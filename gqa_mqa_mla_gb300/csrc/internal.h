@@ -284,6 +284,8 @@ cudaError_t launch_weigh(const GqaParams& p, bool bf16, int num_sms, cudaStream_
 cudaError_t launch_mla_combine(const MlaCombineParams& p, bool bf16, cudaStream_t stream);
 
 // Bounded-wait self test (csrc/selftest.cu).
+cudaError_t launch_gave_up_selftest(int* err_flag, float* result, uint64_t limit_ns,
+                                    cudaStream_t stream);
 cudaError_t launch_warp_wait_selftest(int* err_flag, int* result, uint64_t limit_ns,
                                       cudaStream_t stream);
 cudaError_t launch_wait_selftest(int* err_flag, int* result, uint64_t limit_ns,

@@ -2,6 +2,7 @@
 // on the GPU, without a fault: one CTA waits on barriers that nothing ever
 // completes, so the waits must give up, set the error flag and let the CTA
 // leave.
+#include "gqa_common.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -68,7 +69,41 @@ __global__ void __launch_bounds__(32) warp_wait_kernel(int* err_flag, int* resul
   }
 }
 
+// The end of a weighing decode's split (gqa_mark_unless), three of them: warp 3 of the second
+// waits on a barrier that nothing completes, all others on one that is complete; those
+// of the four writing warps that got through write their rows, then the barrier.
+__global__ void __launch_bounds__(160) gave_up_kernel(const GqaParams p, uint64_t limit_ns) {
+  __shared__ __align__(8) uint64_t bars[2];
+  if (threadIdx.x == 0) {
+    mbar_init(smem_u32(&bars[0]), 1);
+    mbar_init(smem_u32(&bars[1]), 1);
+    fence_barrier_init();
+    mbar_arrive(smem_u32(&bars[0]));
+  }
+  __syncthreads();
+  const int cw = static_cast<int>(threadIdx.x >> 5) - 1, lane = threadIdx.x & 31;
+  if (cw < 0) return;  // (as a producer does)
+  const bool done =
+      mbar_wait_warp(smem_u32(&bars[blockIdx.x == 1 && cw == 3]), 0, p.err_flag, limit_ns);
+  if (done)
+    for (int r = cw; r < p.group; r += 4)
+      if (lane == 0) p.part_lse[r * p.n_split + blockIdx.x] = static_cast<float>(r);
+  gqa_mark_unless(done, 128, cw == 0, p);
+}
+
 }  // namespace
+
+cudaError_t launch_gave_up_selftest(int* err_flag, float* result, uint64_t limit_ns,
+                                    cudaStream_t stream) {
+  GqaParams p{};
+  p.part_lse = result;
+  p.err_flag = err_flag;
+  p.batch = p.h_kv = 1;
+  p.h_q = p.group = 40;
+  p.n_split = 3;
+  gave_up_kernel<<<3, 160, 0, stream>>>(p, limit_ns);
+  return cudaGetLastError();
+}
 
 cudaError_t launch_warp_wait_selftest(int* err_flag, int* result, uint64_t limit_ns,
                                       cudaStream_t stream) {

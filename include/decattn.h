@@ -553,7 +553,8 @@ int gqa_decode_blocks_plan_splits(int batch, int h_q, int h_kv, int d_head, int 
  *                already (the others' begin at 0); NULL: all but the last token
  *   decay        finite; 1 adds up, less forgets
  * A row of zeros (no score but -inf) has no weights to add; a NaN row's are
- * NaN.  A sequence with bad data (zero rows) keeps its weights.  Sequences must not
+ * NaN.  A sequence with bad data (zero rows) keeps its weights, and so does a KV head
+ * of it where a pipeline wait gave up (DECATTN_FLAG_TIMEOUT).  Sequences must not
  * share blocks (the weights of a shared one are unspecified).  num_splits = 0 takes
  * gqa_decode_weights_plan_splits' count (kv_bytes = 2, or 1 over an 8-bit cache).
  * Workspace: gqa_decode_weights_workspace_size, for one split too; the scores, 4
@@ -690,6 +691,12 @@ int decattn_selftest_wait_timeout(int* err_flag, int* result, int limit_us, void
  * result[2], result[3] = the same where all wait on the complete one (32);
  * result holds 4 ints, the other arguments as above. */
 int decattn_selftest_warp_wait(int* err_flag, int* result, int limit_us, void* stream);
+
+/* decattn_selftest_gave_up -- the end of a weighing decode's splits, one of which has a
+ * warp whose wait gives up: its rows are marked, whatever its other warps wrote, so
+ * that the second launch adds nothing for them.  40 rows of 3 splits: result[3 r + s]
+ * (float, 120 of them) = r, or +inf for s = 1; the other arguments as above. */
+int decattn_selftest_gave_up(int* err_flag, float* result, int limit_us, void* stream);
 
 /* Library version as major*10000 + minor*100 + patch. */
 int decattn_version(void);

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import gqa_mqa_mla_gb300 as da
+from gqa_mqa_mla_gb300 import binding
 
 from test_long_cache_gpu import _attend, _case, _close, _decode, _flag, _i32, _lists, _weights_close
 
@@ -46,3 +47,16 @@ def test_bf16_queries_of_any_size_over_8_bits(heads, size, kind):
     _close(x, got, ref, keys, scale)
     if kind == "weights":
         _weights_close(x, w, x["weights"], ref, keys, scale)
+
+
+# ------------------------------------------------------------------ a call that gave up
+
+
+@pytest.mark.parametrize("limit_us", [200, 2000])
+def test_a_split_that_gave_up_is_marked_in_every_row(limit_us):
+    """(What the second launch does with such a split is tested with bad block ids, whose
+    mark is the same.)"""
+    flag, rows = binding.selftest_gave_up(limit_us)
+    want = torch.arange(40.0)[:, None].repeat(1, 3)
+    want[:, 1] = float("inf")
+    assert flag == da.FLAG_TIMEOUT and torch.equal(rows, want)
