@@ -860,8 +860,9 @@ def gqa_decode_weights(q, k_cache, v_cache, weights, block_table, seq_lens, *, s
     weights float32 [num_blocks, h_kv, block_size], updated in place: the slot of
     each token t < seq_lens[b] gets (decay times its old value where t <
     weighed_lens[b], else 0) plus the softmax weights that the KV head's query heads
-    give it.  weighed_lens int32 [B]: the tokens that have weights already; without
-    it all but the last.  workspace: gqa_weights_workspace_size bytes.
+    give it.  weighed_lens int32 [B]: the tokens that have weights already (after a
+    prompt, 0: its slots hold what their blocks' last user left); without it all but
+    the last.  workspace: gqa_weights_workspace_size bytes.
     """
     r = calls().decode_weights(q, k_cache, v_cache, None, None, block_table, seq_lens, weights,
                                weighed_lens, scale, decay, max_seq_len, num_splits, out, workspace,
@@ -898,6 +899,11 @@ def gqa_kv_evict(k_cache, v_cache, weights, block_table, seq_lens, *, max_seq_le
     weights are updated in place.  Returns new_lens [B] (minus the tokens evicted:
     paged_plan's new_lens, which frees their blocks) and kept [B, h_kv, keep] (the
     kept tokens' old positions, -1 where nothing is evicted).
+
+    Afterwards the caller takes the sequences' bounds anew (gqa_block_bounds without
+    first_lens), and adds the tokens evicted so far to paged_plan's positions, which
+    count the tokens in the cache: kept keys carry the rotation of the positions that
+    they had.
     """
     r = calls().kv_evict(k_cache, v_cache, weights, block_table, seq_lens, max_seq_len, keep,
                          recent, keep if limit is None else limit, new_lens, kept, err_flag,

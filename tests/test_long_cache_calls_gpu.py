@@ -1,14 +1,17 @@
 """Calls of the operators for long caches that their documentation allows, beside those of
 test_long_cache_gpu.py, against the same plain forms in 64 bits with the same tolerances."""
+import os
 
 import numpy as np
 import pytest
 import torch
 
 import gqa_mqa_mla_gb300 as da
-from gqa_mqa_mla_gb300 import binding
+from gqa_mqa_mla_gb300 import binding, build
+from oracle import long_cache
 
-from test_long_cache_gpu import _attend, _case, _close, _decode, _flag, _i32, _lists, _weights_close
+from test_long_cache_gpu import (DEV, _attend, _case, _close, _decode, _flag,
+                                 _gen, _i32, _lists, _np, _weights_close)
 
 pytestmark = pytest.mark.gpu
 
@@ -60,3 +63,74 @@ def test_a_split_that_gave_up_is_marked_in_every_row(limit_us):
     want = torch.arange(40.0)[:, None].repeat(1, 3)
     want[:, 1] = float("inf")
     assert flag == da.FLAG_TIMEOUT and torch.equal(rows, want)
+
+
+# ------------------------------------------------------------------ the README's step
+
+
+def _readme():
+    """The code of the README's step over long caches, and of the weights and the eviction."""
+    with open(os.path.join(build.ROOT, "README.md")) as f:
+        text = f.read()
+    text = text[text.index("A step over long caches"):text.index("From C:")]
+    lines = [line[4:] for line in text.split("\n") if line.startswith("    ") or not line]
+    code = "\n".join(lines).strip("\n").split("\n\n")
+    return [c for c in code if c.strip()]
+
+
+def test_the_readme_step_over_long_caches():
+    """Run as it stands, over caches, bounds and weights that other sequences have used: after
+    an eviction the bounds are those of the rows that are there, new tokens' positions count
+    the evicted ones, and weights begin at 0."""
+    step, evict = _readme()
+    h_q, h_kv, bs, nb, longest, B = 4, 2, 16, 1200, 8400, 2
+    g = _gen(380)
+    freq = [1e4 ** (-i / 64) for i in range(64)]
+    kv = [torch.randn((nb, bs, h_kv, 128), generator=g, device=DEV).bfloat16() for _ in "kv"]
+    s = dict(da=da, torch=torch, k_cache=kv[0], v_cache=kv[1], longest=longest,
+             rope=da.rope_table(freq), lens=_i32([0] * B), gone=_i32([0] * B), weighed=_i32([0] * B),
+             table=_i32(np.full((B, longest // bs), -1)), free=_i32(np.random.default_rng(3).permutation(nb)),
+             free_count=_i32([nb]), bounds=torch.randn((nb, 2, h_kv, 128), generator=g, device=DEV).bfloat16() * 9,
+             weights=torch.rand((nb, h_kv, bs), generator=g, device=DEV) * 1e3)
+    seen, scale = [0] * B, 128 ** -0.5
+    for new in ([8300, 900], [1, 1], [3, 7000], [1, 450], [1, 1]):
+        T = sum(new) + 5
+        raw = [torch.randn((T, h, 128), generator=g, device=DEV).bfloat16() for h in (h_q, h_kv, h_kv)]
+        before = s["weights"].clone()
+        had = s["lens"].tolist()
+        s.update(new=_i32(new), T=T, q=raw[0], k=raw[1], v=raw[2])
+        exec(step, s)
+        torch.cuda.synchronize()
+        seen = [a + b for a, b in zip(seen, new)]
+        assert s["lens"].tolist() == [a + b for a, b in zip(had, new)]
+        # The newest tokens' queries, turned by all the tokens that their sequences have had.
+        at = np.cumsum(new) - 1
+        rows = _np(raw[0])[at]
+        angle = np.outer([n - 1 for n in seen], freq)[:, None]
+        a, b = rows[..., :64], rows[..., 64:]
+        want = np.concatenate([a * np.cos(angle) - b * np.sin(angle), a * np.sin(angle) + b * np.cos(angle)], -1)
+        # (each result rounded to bf16 once; its products and the sum in fp32)
+        far = np.concatenate([np.abs(a) + np.abs(b)] * 2, -1)
+        assert (np.abs(_np(s["newest"]) - want) <= 2.0**-8 * np.abs(want) + 2.0**-21 * far).all()
+        # The bounds of every block of the sequences.
+        x = dict(q=s["newest"], caches=kv, scales=[], table=s["table"], lens=s["lens"], n=s["lens"].tolist(),
+                 bs=bs, h_q=h_q, h_kv=h_kv, dtype="bf16", fp8=False, max_len=longest, weights=before)
+        table, now = s["table"].cpu().numpy(), _np(s["bounds"])
+        assert np.array_equal(now, long_cache.block_bounds(_np(kv[0]), table, None, x["n"], now))
+        want = long_cache.select_blocks(_np(s["newest"]), now, table, x["n"], block_size=bs, count=128,
+                                        first=1, last=2)
+        assert np.array_equal(s["some"].cpu().numpy(), want)
+        ref, keys = _attend(x, scale, want)
+        _close(x, s["out"], ref, keys, scale)
+        # Weights: those that the sequences' tokens had, 0 for the new ones.
+        _decode(x, "weights", before, s["table"], s["lens"], scale=scale, weighed_lens=_i32(had))
+        raw = [c.view(torch.int16).cpu().numpy() for c in kv]
+        plain = long_cache.evict(*raw, before.cpu().numpy(), table, x["n"], keep=6144, recent=1024, limit=8192)
+        exec(evict, s)
+        torch.cuda.synchronize()
+        ref, keys = _attend(dict(x, caches=[torch.tensor(r, device=DEV).view(torch.bfloat16) for r in raw]), scale)
+        _close(x, s["out"], ref, keys, scale)
+        assert s["lens"].tolist() == [min(n, 6144) if n > 8192 else n for n in x["n"]]
+        for got, ref in zip([*(c.view(torch.int16) for c in kv), s["weights"]], plain):
+            assert np.array_equal(got.cpu().numpy(), ref)
+    assert s["gone"].tolist()[0] > 0 and s["gone"].tolist()[1] > 0
