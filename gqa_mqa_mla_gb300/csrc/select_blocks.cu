@@ -513,16 +513,25 @@ __global__ void __launch_bounds__(kThreads, kCluster ? 1 : 1024 / kThreads) choo
   const bool bad_len = n < 0 || n > p.max_seq_len;
   if (bad_len && tid == 0 && j == 0 && T::rank() == 0) flag_error(p.err_flag, kFlagBadSeqLen);
   const int blocks = n > 0 && !bad_len ? ((n - 1) >> p.log2_block_size) + 1 : 0;
+  const int32_t* bt = p.block_table + static_cast<int64_t>(b) * p.max_blocks_per_seq;
+  // (Every CTA of a team checks the whole table: they go on together.)
+  int bad = 0;
+#pragma unroll 4
+  for (int t = tid; t < blocks; t += kThreads) {
+    const int id = bt[t];
+    bad |= id < 0 || id >= p.num_blocks;
+  }
   if (blocks <= p.count) {  // all of them
     wait_for_dependence();
+    const bool wrong = __syncthreads_or(bad);
+    if (wrong && tid == 0) flag_error(p.err_flag, kFlagBadBlock);
     if (T::rank() == 0)
-      for (int k = tid; k < p.count; k += kThreads) out[k] = k < blocks ? k : -1;
+      for (int k = tid; k < p.count; k += kThreads) out[k] = k < blocks && !wrong ? k : -1;
     return;
   }
   // This CTA's blocks: [begin, begin + own).
   const int slice = (blocks + T::size() - 1) / T::size();
   const int begin = min(blocks, T::rank() * slice), own = min(slice, blocks - begin);
-  const int32_t* bt = p.block_table + static_cast<int64_t>(b) * p.max_blocks_per_seq;
   const float* scores = p.scores + bj * p.score_stride + begin;
   // [first, last) of them are chosen by score, `want` of the team's.
   const int first = p.first - begin, last = blocks - p.last - begin;
@@ -533,13 +542,6 @@ __global__ void __launch_bounds__(kThreads, kCluster ? 1 : 1024 / kThreads) choo
     count_few = 0;
     widest = key_hi = 0u;
     key_lo = 0xffffffffu;
-  }
-  // (Every CTA of a team checks the whole table: they go on together.)
-  int bad = 0;
-#pragma unroll 4
-  for (int t = tid; t < blocks; t += kThreads) {
-    const int id = bt[t];
-    bad |= id < 0 || id >= p.num_blocks;
   }
   wait_for_dependence();  // the scores are there
   // The widest error of the scores (not negative: ordered as its bits) and their range,

@@ -10,7 +10,7 @@ import gqa_mqa_mla_gb300 as da
 from gqa_mqa_mla_gb300 import binding, build
 from oracle import long_cache
 
-from test_long_cache_gpu import (DEV, _attend, _case, _close, _decode, _flag,
+from test_long_cache_gpu import (DEV, _attend, _bounds_of, _case, _close, _decode, _flag,
                                  _gen, _i32, _lists, _np, _weights_close)
 
 pytestmark = pytest.mark.gpu
@@ -63,6 +63,27 @@ def test_a_split_that_gave_up_is_marked_in_every_row(limit_us):
     want = torch.arange(40.0)[:, None].repeat(1, 3)
     want[:, 1] = float("inf")
     assert flag == da.FLAG_TIMEOUT and torch.equal(rows, want)
+
+
+# ------------------------------------------------------------------ selection: tables
+
+
+def test_selection_from_a_bad_table_with_nothing_to_choose():
+    """A sequence of no more blocks than are listed: its table is checked as a longer
+    one's is."""
+    x = _case([400, 60, 80], 8, 2, "bf16", 16, 330)
+    bounds = _bounds_of(x)
+    for count in (5, 30):
+        want = long_cache.select_blocks(_np(x["q"]), _np(bounds), x["table"].cpu().numpy(), x["n"],
+                                        block_size=16, count=count, first=1, last=1)
+        for at in (-1, bounds.shape[0]):
+            table, flag = x["table"].clone(), _flag()
+            table[1, 3] = at
+            table[2, 6:] = -9  # (past the sequence: not looked at)
+            got = da.gqa_select_blocks(x["q"], bounds, table, x["lens"], block_size=16, max_seq_len=400,
+                                       count=count, err_flag=flag).cpu().numpy()
+            assert int(flag) == da.FLAG_BAD_BLOCK and (got[1] == -1).all()
+            assert np.array_equal(got[[0, 2]], want[[0, 2]])
 
 
 # ------------------------------------------------------------------ the README's step
