@@ -755,7 +755,7 @@ cudaError_t launch_t(const SelectParams& p, cudaStream_t stream) {
 void plan_scores(SelectParams& p, int blocks, int num_sms) {
   p.score_heads = 1;
   p.score_ctas = 0;
-  if (blocks <= p.count) return;
+  if (blocks <= p.count || p.first + p.last == p.count) return;  // no choice to make
   // (Up to two tiles a warp of the GPU there is no stream to keep together: one sequence
   // of 131072 tokens 23.1 us with a head to a CTA, 24.6 with four; 32 of 16-32k 49.2, 47.3.)
   const int64_t tiles = static_cast<int64_t>(p.batch) * p.h_kv * ((blocks + kScoreBlocks - 1) / kScoreBlocks);
@@ -774,7 +774,7 @@ void plan_scores(SelectParams& p, int blocks, int num_sms) {
 void plan_choice(SelectParams& p, int blocks, int num_sms) {
   p.team = 1;
   p.cached_blocks = 0;
-  if (blocks <= p.count) return;
+  if (blocks <= p.count || p.first + p.last == p.count) return;
   while (p.team < 8 && static_cast<int64_t>(p.batch) * p.h_kv * p.team * 2 <= num_sms &&
          blocks >= 2 * p.team * 1024)
     p.team *= 2;

@@ -501,7 +501,8 @@ int gqa_block_bounds(const void* k_cache, const int32_t* block_table, const int3
  * A bad length (DECATTN_FLAG_BAD_SEQ_LEN) or block id (DECATTN_FLAG_BAD_BLOCK)
  * gives a list of -1.  max_seq_len sizes the workspace
  * (gqa_select_workspace_size; 0 bytes where no sequence can have more than count
- * blocks); num_splits is not used.
+ * blocks; asked for, but left as it is, where first + last = count: no block is chosen
+ * by its score, and the bounds are not read); num_splits is not used.
  */
 int gqa_select_blocks(const void* q, const void* bounds, const int32_t* block_table,
                       const int32_t* seq_lens, int32_t* selected, int h_q, int h_kv, int d_head,

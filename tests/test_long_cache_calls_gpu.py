@@ -11,7 +11,7 @@ from gqa_mqa_mla_gb300 import binding, build
 from oracle import long_cache
 
 from test_long_cache_gpu import (DEV, _attend, _bounds_of, _case, _close, _decode, _flag,
-                                 _gen, _i32, _lists, _np, _weights_close)
+                                 _gen, _i32, _lists, _np, _same_choice, _weights_close)
 
 pytestmark = pytest.mark.gpu
 
@@ -66,6 +66,18 @@ def test_a_split_that_gave_up_is_marked_in_every_row(limit_us):
 
 
 # ------------------------------------------------------------------ selection: tables
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("first,last", [(2, 4), (0, 6), (6, 0)])
+@pytest.mark.parametrize("lens", [[1000, 0, 90, 97, 2000], [70000, 30]])
+def test_blocks_that_are_all_taken_always_need_no_scores(lens, first, last, fp8):
+    x = _case(lens, 8, 2, "bf16", 16, 320, fp8=fp8)
+    bounds = _bounds_of(x)
+    need = da.gqa_select_workspace_size(len(lens), 2, x["max_len"], 16, 6)
+    ws = torch.full((need,), 77, dtype=torch.uint8, device=DEV)
+    _same_choice(x, bounds, count=6, first=first, last=last, workspace=ws)
+    assert bool((ws == 77).all())
 
 
 def test_selection_from_a_bad_table_with_nothing_to_choose():
