@@ -167,3 +167,88 @@ def test_the_readme_step_over_long_caches():
         for got, ref in zip([*(c.view(torch.int16) for c in kv), s["weights"]], plain):
             assert np.array_equal(got.cpu().numpy(), ref)
     assert s["gone"].tolist()[0] > 0 and s["gone"].tolist()[1] > 0
+
+
+# ------------------------------------------------------------------ launch shapes
+
+
+def _far_bound(x, blocks):
+    """The case under a bound of `blocks` blocks a sequence."""
+    table = torch.full((len(x["n"]), blocks), -1, dtype=torch.int32, device=DEV)
+    table[:, : x["table"].shape[1]] = x["table"]
+    x.update(table=table, max_len=blocks * x["bs"])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("heads", [(64, 8), (32, 8), (28, 4), (8, 8), (18, 6), (7, 7)])
+def test_selection_by_ctas_of_several_heads(heads, dtype, fp8):
+    """Bounds of far more tiles than the GPU has warps: CTAs take four (of 8 and 4 KV heads),
+    two (of 6) or one (of 7) heads' scores."""
+    x = _case([3000, 777, 0, 24, 1111], *heads, dtype, 8, 340, fp8=fp8)
+    bounds = _bounds_of(x)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    _far_bound(x, 16 * (sms * 32 // (5 * heads[1]) + 2))
+    for count, first, last in ((9, 1, 2), (90, 0, 0)):
+        _same_choice(x, bounds, count=count, first=first, last=last)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_selection_by_many_ctas_for_one_row(dtype, fp8):
+    """One sequence and KV head of 36000 blocks: more CTAs of scores than the choice has
+    threads."""
+    g = _gen(350)
+    n = 36000
+    mid = torch.randn((n, 1, 1, 128), generator=g, device=DEV)
+    half = torch.rand((n, 1, 1, 128), generator=g, device=DEV) * 2
+    bounds = torch.cat([mid - half, mid + half], 1)
+    bounds = (bounds * 64).to(torch.float8_e4m3fn) if fp8 else bounds.to(getattr(torch, {"bf16": "bfloat16", "fp16": "float16"}[dtype]))
+    table = torch.randperm(n, generator=g, device=DEV).int()[None].contiguous()
+    q = torch.randn((1, 3, 128), generator=g, device=DEV).to(getattr(torch, {"bf16": "bfloat16", "fp16": "float16"}[dtype]))
+    x = dict(q=q, table=table, lens=_i32([8 * n - 5]), n=[8 * n - 5], bs=8, max_len=8 * n)
+    low, high = (_np(bounds[:, k, 0])[table[0].cpu().numpy()] for k in (0, 1))
+    score = np.max([np.maximum(row * low, row * high).sum(-1) for row in _np(q)[0]], 0)
+    for count in (130, 20000):
+        got = da.gqa_select_blocks(q, bounds, table, x["lens"], block_size=8, max_seq_len=8 * n, count=count)
+        s = score.copy()
+        s[[0, -1]] = np.inf
+        assert np.array_equal(got[0, 0].cpu().numpy(), np.sort(np.argsort(-s, kind="stable")[:count]))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("batch", [257, 700])
+def test_bounds_of_many_sequences(batch, fp8):
+    rng = np.random.default_rng(batch)
+    lens = rng.integers(0, 60, batch).tolist()
+    lens[3], lens[255], lens[256] = 200, 0, 33
+    x = _case(lens, 2, 2, "bf16", 16, 360, fp8=fp8)
+    first = [int(rng.integers(0, n + 2)) for n in lens]
+    k = x["caches"][0]
+    for f in (None, first):
+        bounds, flag = torch.full((k.shape[0], 2, 2, 128), 3.0, device=DEV).to(k.dtype), _flag()
+        before = _np(bounds)
+        da.gqa_block_bounds(k, x["table"], x["lens"], bounds, max_seq_len=200, err_flag=flag,
+                            first_lens=None if f is None else _i32(f))
+        torch.cuda.synchronize()
+        assert int(flag) == 0
+        want = long_cache.block_bounds(_np(k), x["table"].cpu().numpy(), f, lens, before)
+        assert np.array_equal(_np(bounds), want)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("heads", [(2, 2), (8, 2), (34, 2)])
+def test_weights_of_one_long_sequence_among_many(heads, fp8):
+    """More sequences than the second launch has waves for: its CTAs take several runs of
+    the long one's tokens."""
+    rng = np.random.default_rng(7)
+    lens = rng.integers(0, 4, 400).tolist()
+    lens[123] = 9001
+    x = _case(lens, *heads, "bf16", 32, 370, fp8=fp8)
+    w, flag = x["weights"].clone(), _flag()
+    got = _decode(x, "weights", w, x["table"], x["lens"], scale=0.09, err_flag=flag)
+    torch.cuda.synchronize()
+    assert int(flag) == 0
+    ref, keys = _attend(x, 0.09)
+    _close(x, got, ref, keys, 0.09)
+    _weights_close(x, w, x["weights"], ref, keys, 0.09)
