@@ -11,7 +11,8 @@ from gqa_mqa_mla_gb300 import binding, build
 from oracle import long_cache
 
 from test_long_cache_gpu import (DEV, _attend, _bounds_of, _case, _close, _decode, _flag,
-                                 _gen, _i32, _lists, _np, _same_choice, _weights_close)
+                                 _gen, _i32, _lists, _np, _same_choice, _values,
+                                 _weights_close)
 
 pytestmark = pytest.mark.gpu
 
@@ -50,6 +51,38 @@ def test_bf16_queries_of_any_size_over_8_bits(heads, size, kind):
     _close(x, got, ref, keys, scale)
     if kind == "weights":
         _weights_close(x, w, x["weights"], ref, keys, scale)
+
+
+@pytest.mark.parametrize("heads", [(8, 8), (8, 2), (32, 2)])
+@pytest.mark.parametrize("kind", ["blocks", "weights"])
+def test_strange_queries_over_8_bits_leave_the_other_heads_alone(heads, kind):
+    """Zero queries attend to all tokens alike; infinite ones and NaN make their own rows
+    NaN (where a score is not -inf); the other heads give the same bytes as without them."""
+    x = _case([700, 65, 1], *heads, "bf16", 16, 305, fp8=True)
+    lists = _lists(x, 30, 8, empty=False)
+
+    def call():
+        if kind == "blocks":
+            return _decode(x, "blocks", x["table"], x["lens"], _i32(lists), scale=0.09)
+        return _decode(x, "weights", x["weights"].clone(), x["table"], x["lens"], scale=0.09)
+
+    plain = call()
+    x["q"][:, 0] = 0
+    zero = call()
+    x["q"][:, 1, 7], x["q"][:, 2, 9] = float("inf"), float("nan")
+    got = call()
+    assert torch.equal(got[:, 3:], plain[:, 3:]) and torch.equal(zero[:, 1:], plain[:, 1:])
+    assert bool(got[:, 2].isnan().all()) and torch.equal(got[:, 0], zero[:, 0])
+    j = 1 // (heads[0] // heads[1])  # (the infinite query's KV head)
+    for b, n in enumerate(x["n"]):
+        t = [t for t in range(n) if kind != "blocks" or t // 16 in lists[b, j]]
+        keys = _values(x)[0][x["table"][b].cpu().numpy()[np.array(t) // 16], np.array(t) % 16, j, 7]
+        # (Where every score is -inf the row may be zeros: nothing has weight.)
+        assert bool(got[b, 1].isnan().all()) or ((keys < 0).all() and bool((got[b, 1] == 0).all()))
+    x["q"][:, 1:3] = 0
+    ref, keys = _attend(x, 0.09, lists if kind == "blocks" else None)
+    zero[:, 1:3] = torch.tensor(ref[0][:, 1:3], device=DEV).to(zero.dtype)
+    _close(x, zero, ref, keys, 0.09)
 
 
 # ------------------------------------------------------------------ a call that gave up
