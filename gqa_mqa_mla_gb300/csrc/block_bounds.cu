@@ -25,25 +25,6 @@ namespace {
 constexpr int kWarps = 8, kThreads = kWarps * 32;
 constexpr int kAhead = 8;  // loads in flight per lane
 
-// Packed 16-bit minimum and maximum; NaN if one is NaN.
-template <bool kBF16>
-DECATTN_DEV uint32_t min2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  if constexpr (kBF16)
-    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  else
-    asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-template <bool kBF16>
-DECATTN_DEV uint32_t max2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  if constexpr (kBF16)
-    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  else
-    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
 // Two fp16 values that are e4m3 values (or NaN) to their codes, exactly.
 DECATTN_DEV uint32_t f16x2_to_e4m3x2(uint32_t x) {
   uint16_t c;

@@ -141,9 +141,9 @@ __global__ void __launch_bounds__(kRowsPerCta * 32) mla_combine_kernel(const Mla
                            threadIdx.x & 31);
 }
 
-// The weighing decode's second launch (wide groups, and more splits than a cluster
-// has): the first CTAs of a sequence and KV head take a run of tokens each (weigh.cuh),
-// the others merge a row of its partials each, the splits dealt out to their warps.
+// The weighing decode's second launch: the first CTAs of a sequence and KV head take a
+// run of tokens each (weigh.cuh); with more than one split the others merge a row of its
+// partials each, the splits dealt out to their warps.
 // One sequence of 32768 tokens, 32 heads on one KV head, 128 splits: 1024 tokens a CTA
 // and a warp to a row's merge beside them took 47 us.
 // Four tokens a thread go with CTAs of four warps (64 x 4-8k tokens, 64 heads on 8: 303 us

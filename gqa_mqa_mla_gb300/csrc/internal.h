@@ -36,7 +36,8 @@ struct GqaParams {
   float scale_log2;               // scale * log2(e)
   int window;                     // > 0: attend only to the last `window` tokens
   int sinks;                      // > 0 (with a window): and to the first `sinks` tokens
-  int joint;                      // sinks, n_split 2..8: the splits' CTAs merge their partials
+  int joint;                      // sinks or listed blocks, n_split 2..8: the splits' CTAs merge
+                                  // their partials
   const float* k_scale;           // [h_kv], 8-bit caches only: K value = e4m3 * k_scale[j]
   const float* v_scale;           // [h_kv], 8-bit caches only
   const int32_t* selected;        // [B, h_kv, n_listed]: attend to these blocks only, or null
@@ -279,7 +280,7 @@ void plan_scores(SelectParams& p, int blocks, int num_sms);
 void plan_choice(SelectParams& p, int blocks, int num_sms);
 cudaError_t launch_select_blocks(const SelectParams& p, bool e4m3, bool bf16, cudaStream_t stream);
 cudaError_t launch_kv_evict(EvictParams p, int num_sms, cudaStream_t stream);
-// The weighing decode's second launch, where its splits are not one cluster each.
+// The weighing decode's second launch: the tokens' weights, and the merge of the splits.
 cudaError_t launch_weigh(const GqaParams& p, bool bf16, int num_sms, cudaStream_t stream);
 cudaError_t launch_mla_combine(const MlaCombineParams& p, bool bf16, cudaStream_t stream);
 

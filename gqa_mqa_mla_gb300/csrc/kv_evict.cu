@@ -205,7 +205,7 @@ static cudaError_t launch_rank(const EvictParams& p, cudaStream_t stream) {
 
 cudaError_t launch_kv_evict(EvictParams p, int num_sms, cudaStream_t stream) {
   // A cluster of up to eight CTAs to a sequence and KV head, while there are SMs for
-  // them and 4096 tokens for each (2 x 30-32k tokens, 8 KV heads: 34 us, 42 with 2048),
+  // them and 4096 tokens for each (2 x 30-32k tokens, 8 KV heads: 28 us, 39 with 2048),
   // or their shared memory is needed; past that one CTA reads the weights from global
   // memory.
   const int64_t units = static_cast<int64_t>(p.batch) * p.h_kv;
@@ -217,8 +217,8 @@ cudaError_t launch_kv_evict(EvictParams p, int num_sms, cudaStream_t stream) {
   p.cached_tokens = std::min((p.max_seq_len + p.team - 1) / p.team + 3, kCachedTokens);
   cudaError_t e = p.team > 1 ? launch_rank<true>(p, stream) : launch_rank<false>(p, stream);
   if (e != cudaSuccess) return e;
-  // 128 bytes of a row to a CTA (64 sequences, a quarter of them cut to 4096 tokens of 8
-  // heads: 99 us with a flushed L2, 106 with 64 bytes), or 32 where that fills no wave.
+  // 128 bytes of a row to a CTA (64 sequences, a fifth of them cut to 4096 tokens of 8
+  // heads: 93 us, 101 with 64 bytes), or 32 where that fills no wave.
   const int64_t rows = static_cast<int64_t>(p.batch) * p.h_kv * 2;
   const int lg_pieces = rows * (p.head_bytes / 64) < num_sms * 4 ? 1 : 3;
   cudaLaunchConfig_t cfg = {};

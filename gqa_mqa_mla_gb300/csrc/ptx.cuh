@@ -412,6 +412,26 @@ DECATTN_DEV uint32_t pack2(float x, float y) {
   return w;
 }
 
+// Packed minimum and maximum; NaN where one is NaN.
+template <bool kBF16>
+DECATTN_DEV uint32_t min2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if constexpr (kBF16)
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else
+    asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+template <bool kBF16>
+DECATTN_DEV uint32_t max2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if constexpr (kBF16)
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 // The power of two that brings values of magnitude `most` to 2^14 .. 2^15, where fp16 holds
 // a bf16 value exactly and what falls below its smallest step is under 2^-38 of `most`
 // (1 for an infinite `most`).

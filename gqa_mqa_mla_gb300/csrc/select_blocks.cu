@@ -48,17 +48,6 @@ DECATTN_DEV uint4 by_sign(uint4 w, bool negative) {
   return make_uint4(part(w.x), part(w.y), part(w.z), part(w.w));
 }
 
-// Packed maximum and minimum; NaN where one is NaN.
-template <bool kBF16>
-DECATTN_DEV uint32_t max2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  if constexpr (kBF16)
-    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  else
-    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
 // Over 8 bits q is multiplied as fp16, a bf16 query times a power of two for its group
 // (the scores of the pair (b, j) then all carry that factor).
 template <bool kF8, bool kBF16>
@@ -616,8 +605,8 @@ __global__ void __launch_bounds__(kThreads, kCluster ? 1 : 1024 / kThreads) choo
         settled = all || left <= 0 || close <= kFew;
         if (!settled || all || left <= 0) return;
         // (Each CTA for itself; a warp to a block.)  First with the 32-bit sums' own
-        // errors, which mostly tell the blocks apart (one sequence of 131072 tokens 20.5
-        // us, 22.4 with 64 bits at once).
+        // errors, which mostly tell the blocks apart (one sequence of 131072 tokens 22.9
+        // us, 24.1 with 64 bits at once).
         for (int c = warp; c < close; c += kThreads / 32) {
           const int t = T::get(few[c], 0);
           float lo[4], hi[4], up[4], down[4];
